@@ -34,25 +34,16 @@
 // the other roles stop, waits (bounded) for its own copies and MMAs, frees its
 // TMEM and returns.
 #include <cuda.h>
-#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
 #include <cstdlib>
-#include <mutex>
-#include <utility>
 
 #include "tc_fused.h"
+#include "tc_ptx.cuh"
 
 namespace ttc {
-
-__device__ DeviceStatus g_status;
-// Limit of every bounded device wait (ns on the global timer), and the test
-// hook that makes one arrival go missing (tt_set_wait_limit_ns,
-// tt_debug_skip_arrival).
-__device__ unsigned long long g_wait_limit_ns = 2000000000ull;
-__device__ int g_debug_skip = 0;
 
 cudaError_t read_and_clear_device_status(DeviceStatus* out) {
   cudaError_t e = cudaMemcpyFromSymbol(out, g_status, sizeof(DeviceStatus));
@@ -82,44 +73,6 @@ constexpr uint32_t F_Z = 0, F_Y = 128;                       // forward
 constexpr uint32_t B_Z = 0, B_DZP = 64, B_W = 128, B_X = 256;  // backward
 constexpr uint32_t TMEM_COLS = 512;
 
-// --------------------------------------------------------------------------
-// PTX helpers
-
-__device__ __forceinline__ uint32_t su32(const void* p) {
-  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-
-__device__ __forceinline__ uint64_t gtimer() {
-  uint64_t t;
-  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-  return t;
-}
-
-__device__ __forceinline__ void mbar_init(uint64_t* b, uint32_t count) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(su32(b)), "r"(count));
-}
-
-__device__ __forceinline__ void mbar_expect_tx(uint64_t* b, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(su32(b)),
-               "r"(bytes)
-               : "memory");
-}
-
-__device__ __forceinline__ void mbar_arrive(uint64_t* b) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(su32(b)) : "memory");
-}
-
-__device__ __forceinline__ bool mbar_try_wait(uint64_t* b, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-      " selp.u32 %0, 1, 0, p;\n}"
-      : "=r"(ok)
-      : "r"(su32(b)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
 // Optional per-CTA timeline (global-timer stamps), compiled in only with
 // -DTTC_TIMELINE for performance investigation; the default build has none.
 #ifdef TTC_TIMELINE
@@ -137,233 +90,6 @@ __device__ unsigned long long g_tlk[16][48];
 #define TL_STAMP(k, slot) ((void)0)
 #define TLK(slot) ((void)0)
 #endif
-
-__device__ void record_error(unsigned code, unsigned where) {
-  if (atomicCAS(&g_status.code, 0u, code) == 0u) atomicExch(&g_status.detail, where);
-}
-
-// True (once) when the test hook asks this launch to skip one arrival.
-__device__ __forceinline__ bool debug_take(int site) {
-  return *(volatile int*)&g_debug_skip == site && atomicCAS(&g_debug_skip, site, 0) == site;
-}
-
-// Wait for the phase of the given parity; false if aborted or timed out.
-__device__ __forceinline__ bool wait_bar(uint64_t* b, uint32_t parity, volatile int* abort_flag,
-                                         unsigned where) {
-  if (mbar_try_wait(b, parity)) return true;
-  const uint64_t t0 = gtimer();
-  const uint64_t limit = *(volatile unsigned long long*)&g_wait_limit_ns;
-  while (!mbar_try_wait(b, parity)) {
-    if (*abort_flag) return false;
-    if (gtimer() - t0 > limit) {
-      *abort_flag = 1;
-      record_error(TT_ERR_TIMEOUT, where);
-      return false;
-    }
-  }
-  return true;
-}
-
-// Warp-uniform wait: lane 0 polls, the result is broadcast, so that the
-// warp stays converged for the .sync.aligned TMEM loads that follow.
-__device__ __forceinline__ bool warp_wait(uint64_t* b, uint32_t parity, volatile int* abort_flag,
-                                          unsigned where) {
-  int ok = 0;
-  if ((threadIdx.x & 31) == 0) ok = wait_bar(b, parity, abort_flag, where) ? 1 : 0;
-  return __shfl_sync(0xffffffffu, ok, 0) != 0;
-}
-
-// Drain wait used on the way out: bounded, ignores the abort flag.
-__device__ __forceinline__ void drain_bar(uint64_t* b, uint32_t parity) {
-  const uint64_t t0 = gtimer();
-  const uint64_t limit = *(volatile unsigned long long*)&g_wait_limit_ns / 4;
-  while (!mbar_try_wait(b, parity)) {
-    if (gtimer() - t0 > limit) return;
-  }
-}
-
-__device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, uint64_t* bar, int c0,
-                                         int c1) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4}], [%2];" ::"r"(su32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(su32(bar)), "r"(c0), "r"(c1)
-      : "memory");
-}
-
-// Programmatic dependent launch: wait for the grids this one depends on
-// (their memory is visible afterwards), and let the next grid in the stream
-// be scheduled early.  Both are no-ops for a grid launched without the
-// programmatic-serialization attribute.
-__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void pdl_trigger() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-
-__device__ __forceinline__ void tc_fence_before() {
-  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tc_fence_after() {
-  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void fence_async_smem() {
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-
-// smem matrix descriptor, 128-byte swizzle, sm_100 family (version 1)
-__device__ __forceinline__ uint64_t sdesc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-  return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
-         ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
-}
-__device__ __forceinline__ uint64_t kdesc(uint32_t saddr) { return sdesc(saddr, 16, 1024); }
-__device__ __forceinline__ uint64_t mndesc(uint32_t saddr, uint32_t lbo) {
-  return sdesc(saddr, lbo, 1024);
-}
-
-// instruction descriptor: bf16 x bf16 -> f32, dense
-__host__ __device__ constexpr uint32_t idesc(int M, int N, int a_mn, int b_mn) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) |
-         ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
-}
-
-__device__ __forceinline__ void mma(uint32_t dtmem, uint64_t a, uint64_t b, uint32_t id,
-                                    uint32_t acc) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(dtmem),
-      "l"(a), "l"(b), "r"(id), "r"(acc));
-}
-
-__device__ __forceinline__ void mma_commit(uint64_t* bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-          su32(bar))
-      : "memory");
-}
-
-#define TT_LD32_REGS                                                                         \
-  "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, " \
-  "%19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}"
-
-// 32 consecutive f32 columns of this thread's TMEM lane
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
-  uint32_t r[32];
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 " TT_LD32_REGS ", [%32];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
-                 "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
-                 "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
-                 "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-                 "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
-                 "=r"(r[30]), "=r"(r[31])
-               : "r"(taddr));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-}
-
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-  __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<uint32_t*>(&h);
-}
-
-// Write 32 values (columns [32h, 32h+32) of row `row`) as bf16 into a
-// [128][64] tile in the 128-byte swizzled layout used by TMA and the MMAs.
-__device__ __forceinline__ void st_tile_half(uint8_t* tile, int row, int h, const float (&v)[32]) {
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    uint4 u;
-    u.x = pack_bf16(v[8 * q + 0], v[8 * q + 1]);
-    u.y = pack_bf16(v[8 * q + 2], v[8 * q + 3]);
-    u.z = pack_bf16(v[8 * q + 4], v[8 * q + 5]);
-    u.w = pack_bf16(v[8 * q + 6], v[8 * q + 7]);
-    const int chunk = (4 * h + q) ^ (row & 7);
-    *reinterpret_cast<uint4*>(tile + row * 128 + chunk * 16) = u;
-  }
-}
-
-// Inverse of st_tile_half: columns [32h, 32h+32) of row `row` as f32.
-__device__ __forceinline__ void ld_tile_half(const uint8_t* tile, int row, int h, float (&v)[32]) {
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const int chunk = (4 * h + q) ^ (row & 7);
-    const uint4 u = *reinterpret_cast<const uint4*>(tile + row * 128 + chunk * 16);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]));
-      v[8 * q + 2 * i] = f.x;
-      v[8 * q + 2 * i + 1] = f.y;
-    }
-  }
-}
-
-__device__ __forceinline__ void tma_store(const CUtensorMap* map, const void* src, int c0, int c1) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
-          reinterpret_cast<uint64_t>(map)),
-      "r"(su32(src)), "r"(c0), "r"(c1)
-      : "memory");
-}
-
-// Element-wise atomic add of a shared-memory box into global memory.
-__device__ __forceinline__ void tma_reduce_add(const CUtensorMap* map, const void* src, int c0,
-                                               int c1) {
-  asm volatile(
-      "cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group"
-      " [%0, {%2, %3}], [%1];" ::"l"(reinterpret_cast<uint64_t>(map)),
-      "r"(su32(src)), "r"(c0), "r"(c1)
-      : "memory");
-}
-
-__device__ __forceinline__ void bulk_commit() {
-  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-}
-// Wait until at most N committed bulk groups of this thread still read smem.
-template <int N>
-__device__ __forceinline__ void bulk_wait_read() {
-  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ void bulk_wait_all() {
-  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-}
-
-// Staging boxes are [32 rows][128 bytes] with the 128-byte swizzle the
-// tensor maps use: 16-byte chunk q of row r lives at r*128 + (q ^ (r & 7))*16.
-__device__ __forceinline__ void stage_bf16_32(uint8_t* box, int r, int piece,
-                                              const float (&v)[32]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint4 u;
-    u.x = pack_bf16(v[8 * i + 0], v[8 * i + 1]);
-    u.y = pack_bf16(v[8 * i + 2], v[8 * i + 3]);
-    u.z = pack_bf16(v[8 * i + 4], v[8 * i + 5]);
-    u.w = pack_bf16(v[8 * i + 6], v[8 * i + 7]);
-    const int q = 4 * piece + i;
-    *reinterpret_cast<uint4*>(box + r * 128 + ((q ^ (r & 7)) << 4)) = u;
-  }
-}
-__device__ __forceinline__ void stage_f32_32(uint8_t* box, int r, const float (&v)[32]) {
-#pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    const float4 f = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-    *reinterpret_cast<float4*>(box + r * 128 + ((q ^ (r & 7)) << 4)) = f;
-  }
-}
-
-// After the butterfly, lane l holds sum over the warp's 32 lanes of v[l].
-__device__ __forceinline__ float warp_transpose_sum(float (&v)[32], int lane) {
-#pragma unroll
-  for (int w = 16; w >= 1; w >>= 1) {
-    const bool upper = (lane & w) != 0;
-#pragma unroll
-    for (int i = 0; i < w; ++i) {
-      const float send = upper ? v[i] : v[i + w];
-      const float keep = upper ? v[i + w] : v[i];
-      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, w);
-    }
-  }
-  return v[0];
-}
 
 // Two E4M3 codes (low byte first) -> two bf16 values (low half first).
 // Every E4M3 value is exact in f16, f32 and bf16, so no rounding happens.
@@ -495,10 +221,6 @@ __device__ void zero_tail_rows(uint8_t* stages, int nstage, uint8_t* zp_tile, in
     *reinterpret_cast<uint4*>(bp + tt * 128 + o * 16) = make_uint4(0u, 0u, 0u, 0u);
   }
   fence_async_smem();  // the MMAs read these rows through the async proxy
-}
-
-__device__ __forceinline__ uint8_t* align1k(uint8_t* p) {
-  return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
 }
 
 __device__ void tmem_alloc(uint32_t* slot) {
@@ -1401,43 +1123,6 @@ TcLayout tc_layout(const LayerPlan& L) {
   return t;
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-  });
-  return fn;
-}
-
-enum MapType { kMapBF16, kMapF32, kMapU8 };
-
-// 2-D tensor (outer x inner, row-major) of bf16, f32 or bytes (E4M3 codes),
-// box (box_outer x box_inner), 128-byte swizzle, zero fill outside the tensor.
-bool make_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint32_t box_inner,
-              uint32_t box_outer, MapType type = kMapBF16) {
-  auto fn = encode_fn();
-  if (!fn) return false;
-  const uint64_t esz = type == kMapF32 ? 4 : type == kMapU8 ? 1 : 2;
-  const CUtensorMapDataType dt = type == kMapF32  ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
-                                 : type == kMapU8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
-                                                  : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  cuuint64_t dims[2] = {inner, outer};
-  cuuint64_t strides[1] = {inner * esz};
-  cuuint32_t box[2] = {box_inner, box_outer};
-  cuuint32_t estr[2] = {1, 1};
-  CUresult r = fn(m, dt, 2,
-                  const_cast<void*>(base), dims, strides, box, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
-}
-
 constexpr size_t kSmemFwd = NSTAGE_F * STAGE + BOX + NEPI * 2 * STG + sizeof(SmemCommon) + 1024;
 constexpr size_t kSmemBwd = NSTAGE_B * STAGE + BOX + NEPI * 2 * STG + sizeof(SmemCommon) + 1024;
 static_assert(kSmemFwd <= 227 * 1024, "forward smem");
@@ -1481,44 +1166,6 @@ int tokens_per_tile(int64_t T) {
   int64_t tt = (T + waves * sms - 1) / (waves * sms);
   tt = (tt + 15) / 16 * 16;
   return (int)(tt < 16 ? 16 : tt > TILE ? TILE : tt);
-}
-
-// Programmatic dependent launch is on unless TTC_NO_PDL is set (to 1).
-bool pdl_enabled() {
-  static int on = -1;
-  if (on < 0) {
-    const char* e = getenv("TTC_NO_PDL");
-    on = (e && e[0] && e[0] != '0') ? 0 : 1;
-  }
-  return on == 1;
-}
-
-// Launch with the programmatic-serialization attribute (and optionally as a
-// cooperative grid).  The kernels call pdl_wait() before reading anything a
-// predecessor may write.
-template <typename... KArgs, typename... Args>
-cudaError_t launch_ex(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
-                      bool cooperative, Args&&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attrs[2];
-  int n = 0;
-  if (pdl_enabled()) {
-    attrs[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attrs[n].val.programmaticStreamSerializationAllowed = 1;
-    ++n;
-  }
-  if (cooperative) {
-    attrs[n].id = cudaLaunchAttributeCooperative;
-    attrs[n].val.cooperative = 1;
-    ++n;
-  }
-  cfg.attrs = attrs;
-  cfg.numAttrs = n;
-  return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
 }
 
 template <typename T>
