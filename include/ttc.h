@@ -42,7 +42,7 @@
  *    that ran out, a failed consistency check) are recorded in a status word
  *    that the library keeps in device memory, one per GPU (a module-scope
  *    variable, zero at load), and read back by tt_get_device_status.
- *  - Activations: x is (T, N), y is (T, M), dy is (T, M), dx is (T, N), all
+ *  - Activations of the TT layers: x is (T, N), y is (T, M), dy is (T, M), dx is (T, N), all
  *    row-major, dense, in the plan's activation type (f32 or bf16), 16-byte
  *    aligned.  Cores, diagonals and their gradients are f32.
  *  - Packed parameters: one f32 buffer holding G_1..G_2d, each
@@ -322,6 +322,128 @@ tt_status tt_ttm_lookup_backward(const tt_plan_t* plan, int64_t B, const int32_t
  * distinct rows and of distinct (i_1, i_2) prefixes of that batch. */
 tt_status tt_ttm_stats(const tt_plan_t* plan, const void* ws, int64_t* unique_rows,
                        int64_t* unique_pairs, void* stream);
+
+/* ---- layer normalisation ------------------------------------------------------
+ * The normalisation between an encoder block's TT layers, with the residual
+ * sum in front of it.  The CoMERA pages leave it uncompressed and do not
+ * describe it; the definition is Ba, Kiros and Hinton's.  For a row t of N
+ * values
+ *   s = x + res  (s = x without res),   mean = sum_j s_j / N,
+ *   rstd = 1 / sqrt(sum_j (s_j - mean)^2 / N + eps),
+ *   y_j = (s_j - mean) rstd gamma_j + beta_j.
+ * Row statistics and sums are fp32; y and s are rounded once, s after y was
+ * computed from its unrounded value. */
+typedef struct tt_norm_desc {
+  int64_t N;      /* width of a row, 1 .. 2^20 */
+  float eps;      /* > 0, finite */
+  int act;        /* tt_dtype of x, res, s, y and their gradients: F32 or BF16 */
+  unsigned flags; /* TT_ACCUMULATE: the backward adds into dgamma and dbeta */
+} tt_norm_desc;
+/* Host only.  TT_ERR_INVALID_ARG for a bad field, TT_ERR_UNSUPPORTED for E4M3
+ * or N above 2^20. */
+tt_status tt_norm_plan(const tt_norm_desc* desc, tt_plan_t** out);
+/* T rows.  x, res, sum and y are (T, N), dense, 16-byte aligned; res may be
+ * NULL (no residual), sum may be NULL (s not wanted); sum or y may be x or res
+ * itself.  gamma and beta: N fp32 each, either may be NULL (1 and 0).
+ * stats: T x 2 fp32 (mean, rstd of each row), for the backward; may be NULL.
+ * Needs no workspace.  T == 0 is a no-op. */
+tt_status tt_norm_forward(const tt_plan_t* plan, int64_t T, const void* x, const void* res,
+                          const float* gamma, const float* beta, void* sum, void* y,
+                          float* stats, void* stream);
+/* Gradients of L = <dy, y> + <dsum, s>.  s: what was normalised (x, or the
+ * forward's sum); stats: the forward's.  With g = dy gamma, h = (s - mean) rstd:
+ *   dx = rstd (g - sum_j g_j / N - h sum_j g_j h_j / N) + dsum   (the gradient
+ * of x, and of res: they are equal), dgamma = sum_t dy h, dbeta = sum_t dy.
+ * dsum (the gradient that reaches s along the residual path) may be NULL;
+ * dgamma and dbeta (fp32, overwritten, or added to under TT_ACCUMULATE) may
+ * each be NULL.  dx may be dy or dsum itself.  Sums over tokens are taken in a fixed order: the
+ * same inputs give the same bits on a given GPU model.  Workspace:
+ * tt_workspace_size(plan, T).  T == 0 writes zero dgamma and dbeta (or leaves
+ * them under TT_ACCUMULATE). */
+tt_status tt_norm_backward(const tt_plan_t* plan, int64_t T, const void* s, const void* dy,
+                           const void* dsum, const float* gamma, const float* stats, void* dx,
+                           float* dgamma, float* dbeta, void* ws, size_t ws_bytes,
+                           void* stream);
+
+/* ---- attention with a sliding window and first tokens that stay visible ------
+ * The attention between the Q, K, V projections and O.  The CoMERA pages
+ * leave it uncompressed; the definition is scaled dot-product attention
+ * (Vaswani et al.) under the mask below.
+ * Sequence b has queries q rows q_begin[b] .. q_end[b] and keys k rows
+ * k_begin[b] .. k_end[b] (lq and lk of them).  Its query row t (0-based)
+ * stands at position i = t + lk - lq: with lq == lk that is self-attention,
+ * with lq < lk the queries are the last ones of a longer cache.  Key j
+ * (0-based) is visible to it when
+ *   (right < 0 or j <= i + right)  and  (left < 0 or j >= i - left or j < sinks)
+ * so right = 0 is causal, left = W - 1 a window of W tokens, and the first
+ * `sinks` tokens never leave it.  Query head h reads key head h / (heads /
+ * kv_heads).  Over the visible j:
+ *   z_j = scale q_i . k_j,  lse = log sum_j exp(z_j),  p_j = exp(z_j - lse),
+ *   o_i = sum_j p_j v_j.
+ * A row that sees no key gets o = 0 and lse = -infinity, and zero gradients.
+ * Keys that no query of their sequence sees are not used: what they hold (a
+ * cache's unwritten rows, NaN) reaches no output.
+ * Scores, softmax statistics and all sums are fp32.  With bf16 activations
+ * the weights p (and in the backward z's gradient) are rounded to bf16 for
+ * the tensor-core products. */
+typedef struct tt_attn_desc {
+  int heads;     /* query heads, 1 .. 1024 */
+  int kv_heads;  /* key / value heads, a divisor of heads */
+  int dim;       /* width of a head, 1 .. 256 */
+  int left;      /* tokens to the left that stay visible; < 0: all */
+  int right;     /* tokens to the right; < 0: all */
+  int sinks;     /* first tokens that the left bound does not hide, >= 0 */
+  float scale;   /* 0: 1 / sqrt(dim) */
+  int act;       /* tt_dtype of q, k, v, o and their gradients: F32 or BF16 */
+  unsigned flags; /* 0 */
+} tt_attn_desc;
+/* Host only.  TT_ERR_INVALID_ARG for a bad field, TT_ERR_UNSUPPORTED for E4M3
+ * or dim above 256. */
+tt_status tt_attn_plan(const tt_attn_desc* desc, tt_plan_t** out);
+
+/* The rows of a batch's sequences.  The four arrays are device memory, B
+ * int32 each; packed self-attention passes one array of B + 1 offsets as
+ * begin and the same array + 1 as end, for queries and keys alike.  Query
+ * ranges must not overlap; key ranges must not overlap in a backward.
+ * max_q and max_k bound lq and lk (they size the launch).  A sequence with a
+ * negative length, a row outside [0, Tq) / [0, Tk), or longer than max_q /
+ * max_k is skipped (its rows left unwritten) and recorded in the device
+ * status word (TT_ERR_DEVICE).  Rows of no sequence are left unwritten. */
+typedef struct tt_attn_seqs {
+  int B;                 /* sequences, 0 .. 2^20 */
+  int max_q, max_k;      /* 0 .. 2^29 */
+  int64_t Tq, Tk;        /* rows of the q and k buffers, < 2^31 */
+  const int32_t* q_begin;
+  const int32_t* q_end;
+  const int32_t* k_begin;
+  const int32_t* k_end;
+} tt_attn_seqs;
+/* A tensor of heads: element (t, h, c) is at p[t * row + h * head + c] (row
+ * and head in elements, >= 0).  p is aligned to its type; the tensor-core kernels
+ * additionally take p 16-byte aligned and, in bf16, row, head and dim
+ * multiples of 8 with dim <= 128; anything else runs on the general kernels. */
+typedef struct tt_heads {
+  void* p;
+  int64_t row, head;
+} tt_heads;
+
+/* Bytes of workspace (256-byte aligned) for a forward or a backward of seqs
+ * (its device arrays are not read). */
+tt_status tt_attn_workspace_size(const tt_plan_t* plan, const tt_attn_seqs* seqs, int backward,
+                                 size_t* bytes);
+/* q and o: (Tq, heads, dim), k and v: (Tk, kv_heads, dim); lse: (heads, Tq)
+ * fp32, may be NULL. */
+tt_status tt_attn_forward(const tt_plan_t* plan, const tt_attn_seqs* seqs, const tt_heads* q,
+                          const tt_heads* k, const tt_heads* v, const tt_heads* o, float* lse,
+                          void* ws, size_t ws_bytes, void* stream);
+/* Gradients of L = <dout, o>: dq, dk and dv (overwritten; the gradient of a
+ * shared key head is the sum over its query heads), with o and lse as the
+ * forward left them.  Every sum is taken in a fixed order. */
+tt_status tt_attn_backward(const tt_plan_t* plan, const tt_attn_seqs* seqs, const tt_heads* q,
+                           const tt_heads* k, const tt_heads* v, const tt_heads* o,
+                           const float* lse, const tt_heads* dout, const tt_heads* dq,
+                           const tt_heads* dk, const tt_heads* dv, void* ws, size_t ws_bytes,
+                           void* stream);
 
 /* ---- the device-side error path ---------------------------------------------
  * Every wait inside the library's kernels (on a TMA transfer, on another warp

@@ -1,0 +1,680 @@
+// Layer normalisation with a residual sum in front of it: forward, and
+// backward with the reduction of the weight gradients.
+//
+// Both passes are bound by HBM: a row is read once, kept in registers (up to
+// 16384 values across 1 to 32 warps), and written once.  The variance is
+// taken from the centred values in a second pass over the registers, so a
+// large mean costs no accuracy.  The backward's sums over tokens (dgamma,
+// dbeta) accumulate in registers over the rows a group of warps owns, each
+// block leaves one partial row in the workspace, and a second kernel adds the
+// partials in block order: no atomics, the same bits every time.
+#include <cuda_bf16.h>
+
+#include <cmath>
+#include <new>
+
+#include "tc_ptx.cuh"
+#include "ttc.h"
+#include "ttc_internal.h"
+
+namespace ttc {
+namespace {
+
+// ---- vector loads and stores -------------------------------------------------
+// VEC consecutive elements of type T as they lie in memory.
+template <typename T, int VEC>
+struct Raw;
+template <>
+struct Raw<float, 4> {
+  float4 v;
+  __device__ void get(float* f) const { f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w; }
+  __device__ void set(const float* f) { v = make_float4(f[0], f[1], f[2], f[3]); }
+};
+template <>
+struct Raw<float, 1> {
+  float v;
+  __device__ void get(float* f) const { f[0] = v; }
+  __device__ void set(const float* f) { v = f[0]; }
+};
+template <>
+struct Raw<__nv_bfloat16, 8> {
+  uint4 v;
+  __device__ void get(float* f) const {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {  // a bf16 is the upper half of its f32
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  }
+  __device__ void set(const float* f) {
+    v = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
+                   pack_bf16(f[6], f[7]));
+  }
+};
+template <>
+struct Raw<__nv_bfloat16, 1> {
+  __nv_bfloat16 v;
+  __device__ void get(float* f) const { f[0] = __bfloat162float(v); }
+  __device__ void set(const float* f) { v = __float2bfloat16_rn(f[0]); }
+};
+
+// Sum over the G = 32 W threads of a group, in a fixed order; every thread
+// gets it.  `slot` alternates between two shared rows so that one barrier a
+// reduction is enough.
+template <int W>
+__device__ __forceinline__ float group_sum(float v, float (*red)[32], int slot) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if (W == 1) return v;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (lane == 0) red[slot][warp] = v;
+  __syncthreads();
+  float t = lane < W ? red[slot][lane] : 0.f;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+  return t;
+}
+
+struct NormFwdArgs {
+  int64_t T;
+  int N;
+  float eps, n;  // n: N as a float; sums are divided, so that equal values have their own mean
+  const void* x;
+  const void* res;
+  const float* gamma;
+  const float* beta;
+  void* sum;
+  void* y;
+  float2* stats;
+};
+
+struct NormBwdArgs {
+  int64_t T;
+  int N;
+  float n;
+  const void* s;
+  const void* dy;
+  const void* dsum;
+  const float* gamma;
+  const float2* stats;
+  void* dx;
+  float* parts;   // [gridDim.x][2 N]: this block's share of dgamma, then of dbeta
+  float* dgamma;  // written directly when the grid is one block (parts unused)
+  float* dbeta;
+  int accumulate;
+};
+
+constexpr int kRowWarps = 8;  // rows side by side in a block when a warp holds a row
+
+// A group of W warps holds a row of up to 32 W VEC CH values; groups stride
+// over the rows, loading the next row while the current one is worked on.
+template <typename T, int VEC, int CH, int W, bool RES>
+__global__ void __launch_bounds__(W == 1 ? 32 * kRowWarps : 32 * W)
+    norm_fwd_kernel(NormFwdArgs p) {
+  using R = Raw<T, VEC>;
+  constexpr int G = 32 * W;
+  __shared__ float red[2][32];
+  const int tid = W == 1 ? threadIdx.x & 31 : threadIdx.x;
+  const int per_block = W == 1 ? kRowWarps : 1;
+  const int64_t step = (int64_t)gridDim.x * per_block;
+  int64_t row = (int64_t)blockIdx.x * per_block + (W == 1 ? threadIdx.x >> 5 : 0);
+  const int N = p.N;
+  R rx[CH], rr[CH];
+  pdl_wait();
+  pdl_trigger();
+  auto fetch = [&](int64_t r) {
+    const T* x = static_cast<const T*>(p.x) + r * N;
+    const T* s = static_cast<const T*>(p.res) + r * N;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int j = (c * G + tid) * VEC;
+      if (j < N) {
+        rx[c] = *reinterpret_cast<const R*>(x + j);
+        if (RES) rr[c] = *reinterpret_cast<const R*>(s + j);
+      }
+    }
+  };
+  if (row < p.T) fetch(row);
+  for (; row < p.T; row += step) {
+    float v[CH * VEC];
+    float part = 0.f;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int j = (c * G + tid) * VEC;
+      if (j < N) {
+        rx[c].get(v + c * VEC);
+        if (RES) {
+          float a[VEC];
+          rr[c].get(a);
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) v[c * VEC + i] += a[i];
+        }
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) part += v[c * VEC + i];
+      }
+    }
+    if (row + step < p.T) fetch(row + step);
+    const float mean = group_sum<W>(part, red, 0) / p.n;
+    part = 0.f;
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+      if ((c * G + tid) * VEC < N) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          const float d = v[c * VEC + i] - mean;
+          part = fmaf(d, d, part);
+        }
+      }
+    const float var = group_sum<W>(part, red, 1) / p.n;
+    const float rstd = 1.f / sqrtf(var + p.eps);
+    if (tid == 0 && p.stats) p.stats[row] = make_float2(mean, rstd);
+    T* y = static_cast<T*>(p.y) + row * N;
+    T* so = static_cast<T*>(p.sum) + row * N;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int j = (c * G + tid) * VEC;
+      if (j < N) {
+        R o;
+        if (p.sum) {
+          o.set(v + c * VEC);
+          *reinterpret_cast<R*>(so + j) = o;
+        }
+        float f[VEC];
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          // gamma and beta come from the L1 for every row but the first
+          const float g = p.gamma ? __ldg(p.gamma + j + i) : 1.f;
+          const float b = p.beta ? __ldg(p.beta + j + i) : 0.f;
+          f[i] = fmaf((v[c * VEC + i] - mean) * rstd, g, b);
+        }
+        o.set(f);
+        *reinterpret_cast<R*>(y + j) = o;
+      }
+    }
+  }
+}
+
+// dgamma[j] or dbeta[j] from its sum
+__device__ __forceinline__ void put_sum(float* out, int j, float v, int accumulate) {
+  if (out) out[j] = accumulate ? out[j] + v : v;
+}
+
+template <typename T, int VEC, int CH, int W>
+__global__ void __launch_bounds__(W == 1 ? 32 * kRowWarps : 32 * W)
+    norm_bwd_kernel(NormBwdArgs p) {
+  using R = Raw<T, VEC>;
+  constexpr int G = 32 * W, E = CH * VEC;
+  __shared__ float red[4][32];
+  __shared__ float cross[W == 1 ? kRowWarps * 32 * E * 2 : 1];
+  const int tid = W == 1 ? threadIdx.x & 31 : threadIdx.x;
+  const int per_block = W == 1 ? kRowWarps : 1;
+  const int64_t step = (int64_t)gridDim.x * per_block;
+  int64_t row = (int64_t)blockIdx.x * per_block + (W == 1 ? threadIdx.x >> 5 : 0);
+  const int N = p.N;
+  R rs[CH], rd[CH], ru[CH];
+  float2 st = make_float2(0.f, 0.f);
+  float dg[E], db[E];
+#pragma unroll
+  for (int i = 0; i < E; ++i) dg[i] = db[i] = 0.f;
+  pdl_wait();
+  pdl_trigger();
+  auto fetch = [&](int64_t r) {
+    const T* s = static_cast<const T*>(p.s) + r * N;
+    const T* d = static_cast<const T*>(p.dy) + r * N;
+    const T* u = static_cast<const T*>(p.dsum) + r * N;
+    st = p.stats[r];
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int j = (c * G + tid) * VEC;
+      if (j < N) {
+        rs[c] = *reinterpret_cast<const R*>(s + j);
+        rd[c] = *reinterpret_cast<const R*>(d + j);
+        if (p.dsum) ru[c] = *reinterpret_cast<const R*>(u + j);
+      }
+    }
+  };
+  int flip = 0;
+  if (row < p.T) fetch(row);
+  for (; row < p.T; row += step, flip ^= 2) {
+    float h[E], g[E];  // normalised values; dy gamma
+    R us[CH];
+    float sg = 0.f, sgh = 0.f;
+    const float2 ms = st;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int j = (c * G + tid) * VEC;
+      us[c] = ru[c];
+      if (j < N) {
+        rs[c].get(h + c * VEC);
+        rd[c].get(g + c * VEC);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          const int e = c * VEC + i;
+          h[e] = (h[e] - ms.x) * ms.y;
+          dg[e] = fmaf(g[e], h[e], dg[e]);
+          db[e] += g[e];
+          if (p.gamma) g[e] *= __ldg(p.gamma + j + i);
+          sg += g[e];
+          sgh = fmaf(g[e], h[e], sgh);
+        }
+      }
+    }
+    if (row + step < p.T) fetch(row + step);
+    // both sums behind one barrier
+    if (W == 1) {
+      sg = group_sum<1>(sg, red, 0);
+      sgh = group_sum<1>(sgh, red, 0);
+    } else {
+#pragma unroll
+      for (int o = 16; o; o >>= 1) {
+        sg += __shfl_xor_sync(0xffffffffu, sg, o);
+        sgh += __shfl_xor_sync(0xffffffffu, sgh, o);
+      }
+      const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+      if (lane == 0) red[flip][warp] = sg, red[flip + 1][warp] = sgh;
+      __syncthreads();
+      sg = lane < W ? red[flip][lane] : 0.f;
+      sgh = lane < W ? red[flip + 1][lane] : 0.f;
+#pragma unroll
+      for (int o = 16; o; o >>= 1) {
+        sg += __shfl_xor_sync(0xffffffffu, sg, o);
+        sgh += __shfl_xor_sync(0xffffffffu, sgh, o);
+      }
+    }
+    const float a = sg / p.n, b = sgh / p.n;
+    T* dx = static_cast<T*>(p.dx) + row * N;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int j = (c * G + tid) * VEC;
+      if (j < N) {
+        float f[VEC], u[VEC];
+        if (p.dsum) us[c].get(u);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          const int e = c * VEC + i;
+          f[i] = ms.y * (g[e] - a - h[e] * b) + (p.dsum ? u[i] : 0.f);
+        }
+        R o;
+        o.set(f);
+        *reinterpret_cast<R*>(dx + j) = o;
+      }
+    }
+  }
+  // this block's share of the token sums
+  const bool last = gridDim.x == 1;
+  float* pg = p.parts + (size_t)blockIdx.x * 2 * N;
+  if (W == 1) {
+    const int warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      cross[((warp * 2) * E + i) * 32 + tid] = dg[i];
+      cross[((warp * 2 + 1) * E + i) * 32 + tid] = db[i];
+    }
+    __syncthreads();
+    for (int k = threadIdx.x; k < 2 * E * 32; k += blockDim.x) {
+      const int t = k & 31, i = (k >> 5) % E, which = k / (32 * E);
+      const int j = ((i / VEC) * 32 + t) * VEC + i % VEC;
+      if (j >= N) continue;
+      float v = 0.f;
+#pragma unroll
+      for (int w = 0; w < kRowWarps; ++w) v += cross[((w * 2 + which) * E + i) * 32 + t];
+      if (last)
+        put_sum(which ? p.dbeta : p.dgamma, j, v, p.accumulate);
+      else
+        pg[which * N + j] = v;
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int j = (c * G + tid) * VEC;
+      if (j < N) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          if (last) {
+            put_sum(p.dgamma, j + i, dg[c * VEC + i], p.accumulate);
+            put_sum(p.dbeta, j + i, db[c * VEC + i], p.accumulate);
+          } else {
+            pg[j + i] = dg[c * VEC + i];
+            pg[N + j + i] = db[c * VEC + i];
+          }
+        }
+      }
+    }
+  }
+}
+
+// Sums of the partial rows in row order: 32 columns a block, 32 row slices
+// side by side, then the slices in order.
+__global__ void __launch_bounds__(1024)
+    norm_reduce_kernel(const float* parts, int nparts, int N, float* dgamma, float* dbeta,
+                       int accumulate) {
+  __shared__ float acc[32][33];
+  const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
+  const int col = blockIdx.x * 32 + lane;
+  pdl_wait();
+  pdl_trigger();
+  float v = 0.f;
+  if (col < 2 * N)
+    for (int r = slice; r < nparts; r += 32) v += parts[(size_t)r * 2 * N + col];
+  acc[slice][lane] = v;
+  __syncthreads();
+  if (slice == 0 && col < 2 * N) {
+    float t = 0.f;
+#pragma unroll
+    for (int k = 0; k < 32; ++k) t += acc[k][lane];
+    if (col < N)
+      put_sum(dgamma, col, t, accumulate);
+    else
+      put_sum(dbeta, col - N, t, accumulate);
+  }
+}
+
+// ---- rows wider than the registers of a block ----------------------------------
+constexpr int kWideThreads = 1024;
+
+template <typename T>
+__device__ __forceinline__ float wide_at(const void* p, int64_t i) {
+  float f;
+  reinterpret_cast<const Raw<T, 1>*>(p)[i].get(&f);
+  return f;
+}
+template <typename T>
+__device__ __forceinline__ void wide_put(void* p, int64_t i, float f) {
+  reinterpret_cast<Raw<T, 1>*>(p)[i].set(&f);
+}
+
+// One block a row, the row read three times (from L2 after the first).
+template <typename T>
+__global__ void __launch_bounds__(kWideThreads) norm_fwd_wide_kernel(NormFwdArgs p) {
+  __shared__ float red[2][32];
+  pdl_wait();
+  pdl_trigger();
+  for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x) {
+    const int64_t o = row * p.N;
+    auto value = [&](int j) {
+      return wide_at<T>(p.x, o + j) + (p.res ? wide_at<T>(p.res, o + j) : 0.f);
+    };
+    float part = 0.f;
+    for (int j = threadIdx.x; j < p.N; j += kWideThreads) part += value(j);
+    const float mean = group_sum<32>(part, red, 0) / p.n;
+    part = 0.f;
+    for (int j = threadIdx.x; j < p.N; j += kWideThreads) {
+      const float d = value(j) - mean;
+      part = fmaf(d, d, part);
+    }
+    const float rstd = 1.f / sqrtf(group_sum<32>(part, red, 1) / p.n + p.eps);
+    if (threadIdx.x == 0 && p.stats) p.stats[row] = make_float2(mean, rstd);
+    for (int j = threadIdx.x; j < p.N; j += kWideThreads) {
+      const float v = value(j);
+      if (p.sum) wide_put<T>(p.sum, o + j, v);
+      wide_put<T>(p.y, o + j, fmaf((v - mean) * rstd, p.gamma ? __ldg(p.gamma + j) : 1.f,
+                                   p.beta ? __ldg(p.beta + j) : 0.f));
+    }
+  }
+}
+
+// dgamma and dbeta of wide rows: a thread a column, rows split over gridDim.y
+// (before the dx kernel, which may overwrite dy).
+template <typename T>
+__global__ void __launch_bounds__(256) norm_cols_wide_kernel(NormBwdArgs p) {
+  pdl_wait();
+  pdl_trigger();
+  const int j = blockIdx.x * 256 + threadIdx.x;
+  if (j >= p.N) return;
+  float g = 0.f, b = 0.f;
+  for (int64_t r = blockIdx.y; r < p.T; r += gridDim.y) {
+    const float2 st = p.stats[r];
+    const float d = wide_at<T>(p.dy, r * p.N + j);
+    g = fmaf(d, (wide_at<T>(p.s, r * p.N + j) - st.x) * st.y, g);
+    b += d;
+  }
+  p.parts[(size_t)blockIdx.y * 2 * p.N + j] = g;
+  p.parts[(size_t)blockIdx.y * 2 * p.N + p.N + j] = b;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kWideThreads) norm_dx_wide_kernel(NormBwdArgs p) {
+  __shared__ float red[2][32];
+  pdl_wait();
+  pdl_trigger();
+  for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x) {
+    const int64_t o = row * p.N;
+    const float2 st = p.stats[row];
+    auto h = [&](int j) { return (wide_at<T>(p.s, o + j) - st.x) * st.y; };
+    auto g = [&](int j) {
+      return wide_at<T>(p.dy, o + j) * (p.gamma ? __ldg(p.gamma + j) : 1.f);
+    };
+    float sg = 0.f, sgh = 0.f;
+    for (int j = threadIdx.x; j < p.N; j += kWideThreads) {
+      const float v = g(j);
+      sg += v;
+      sgh = fmaf(v, h(j), sgh);
+    }
+    const float a = group_sum<32>(sg, red, 0) / p.n;
+    const float b = group_sum<32>(sgh, red, 1) / p.n;
+    for (int j = threadIdx.x; j < p.N; j += kWideThreads) {
+      const float u = p.dsum ? wide_at<T>(p.dsum, o + j) : 0.f;
+      wide_put<T>(p.dx, o + j, st.y * (g(j) - a - h(j) * b) + u);
+    }
+  }
+}
+
+// ---- dispatch --------------------------------------------------------------------
+constexpr int kMaxRegRow = 16384;  // widest row held in the registers of a block
+
+// Warps of a row, by its width.  Forward: 1024 values a warp.  Backward: its
+// accumulators double the registers, so 768 in one warp, then 512 a warp.
+int fwd_warps(int64_t N) { return N <= 1024 ? 1 : N <= 4096 ? 4 : 16; }
+int bwd_warps(int64_t N) {
+  if (N <= 768) return 1;
+  int w = 2;
+  while (N > 512 * w) w *= 2;
+  return w;
+}
+
+// Blocks of the backward: enough to keep an SM's registers in use, no more
+// than there are rows, and one block when a second launch for the partial
+// sums would cost more than its few rows.
+int64_t bwd_blocks(int64_t N, int64_t T) {
+  if (N > kMaxRegRow) return T < 64 ? (T < 1 ? 1 : T) : 64;  // row slices of the column sums
+  const int w = bwd_warps(N);
+  const int rows = w == 1 ? kRowWarps : 1;
+  const int per_sm = w == 1 ? 2 : w <= 4 ? 8 / w * 2 : w == 8 ? 2 : 1;
+  int64_t b = (T + rows - 1) / rows;
+  if (T <= 4 * rows) return 1;
+  const int64_t most = (int64_t)device_sms() * per_sm;
+  return b < most ? b : most;
+}
+
+bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
+
+template <typename T, int VEC, int CH, int W>
+cudaError_t fwd_go(const NormFwdArgs& a, cudaStream_t st) {
+  constexpr int rows = W == 1 ? kRowWarps : 1;
+  const int64_t need = (a.T + rows - 1) / rows;
+  const int64_t most = (int64_t)device_sms() * (W == 1 ? 4 : W == 4 ? 8 : 2);
+  const dim3 grid((unsigned)(need < most ? need : most));
+  const dim3 block(W == 1 ? 32 * kRowWarps : 32 * W);
+  return a.res ? launch_ex(norm_fwd_kernel<T, VEC, CH, W, true>, grid, block, 0, st, false, a)
+               : launch_ex(norm_fwd_kernel<T, VEC, CH, W, false>, grid, block, 0, st, false, a);
+}
+
+template <typename T, int V>
+cudaError_t fwd_pick(const NormFwdArgs& a, cudaStream_t st) {
+  const int N = a.N;
+  if (N > kMaxRegRow) {
+    const int64_t most = 2 * (int64_t)device_sms();
+    return launch_ex(norm_fwd_wide_kernel<T>, dim3((unsigned)(a.T < most ? a.T : most)),
+                     dim3(kWideThreads), 0, st, false, a);
+  }
+  const int w = fwd_warps(N);
+  const int e = (N + 32 * w - 1) / (32 * w);  // values a thread
+  if (w == 1) {
+    if (e <= 8) return fwd_go<T, V, 8 / V, 1>(a, st);
+    if (e <= 16) return fwd_go<T, V, 16 / V, 1>(a, st);
+    if (e <= 24) return fwd_go<T, V, 24 / V, 1>(a, st);
+    return fwd_go<T, V, 32 / V, 1>(a, st);
+  }
+  if (w == 4) return e <= 16 ? fwd_go<T, V, 16 / V, 4>(a, st) : fwd_go<T, V, 32 / V, 4>(a, st);
+  return e <= 16 ? fwd_go<T, V, 16 / V, 16>(a, st) : fwd_go<T, V, 32 / V, 16>(a, st);
+}
+
+template <typename T, int VEC, int CH, int W>
+cudaError_t bwd_go(const NormBwdArgs& a, int64_t blocks, cudaStream_t st) {
+  return launch_ex(norm_bwd_kernel<T, VEC, CH, W>, dim3((unsigned)blocks),
+                   dim3(W == 1 ? 32 * kRowWarps : 32 * W), 0, st, false, a);
+}
+
+template <typename T, int V>
+cudaError_t bwd_pick(const NormBwdArgs& a, int64_t blocks, cudaStream_t st) {
+  const int N = a.N;
+  switch (bwd_warps(N)) {
+    case 1:
+      if (N <= 256) return bwd_go<T, V, 8 / V, 1>(a, blocks, st);
+      if (N <= 512) return bwd_go<T, V, 16 / V, 1>(a, blocks, st);
+      return bwd_go<T, V, 24 / V, 1>(a, blocks, st);
+    case 2: return bwd_go<T, V, 16 / V, 2>(a, blocks, st);
+    case 4: return bwd_go<T, V, 16 / V, 4>(a, blocks, st);
+    case 8: return bwd_go<T, V, 16 / V, 8>(a, blocks, st);
+    case 16: return bwd_go<T, V, 16 / V, 16>(a, blocks, st);
+    default: return bwd_go<T, V, 16 / V, 32>(a, blocks, st);
+  }
+}
+
+template <typename T>
+cudaError_t bwd_wide(const NormBwdArgs& a, int64_t slices, cudaStream_t st) {
+  cudaError_t e = launch_ex(norm_cols_wide_kernel<T>,
+                            dim3((unsigned)((a.N + 255) / 256), (unsigned)slices), dim3(256), 0,
+                            st, false, a);
+  if (e != cudaSuccess) return e;
+  const int64_t most = 2 * (int64_t)device_sms();
+  return launch_ex(norm_dx_wide_kernel<T>, dim3((unsigned)(a.T < most ? a.T : most)),
+                   dim3(kWideThreads), 0, st, false, a);
+}
+
+}  // namespace
+
+size_t norm_workspace_bytes(const NormPlan& P, int64_t T) {
+  return (size_t)bwd_blocks(P.N, T) * 2 * (size_t)P.N * sizeof(float);
+}
+
+}  // namespace ttc
+
+using namespace ttc;
+
+extern "C" {
+
+tt_status tt_norm_plan(const tt_norm_desc* desc, tt_plan_t** out) {
+  if (!out) return TT_ERR_INVALID_ARG;
+  *out = nullptr;
+  if (!desc || desc->N < 1 || !std::isfinite(desc->eps) || !(desc->eps > 0.f) ||
+      (desc->flags & ~TT_ACCUMULATE))
+    return TT_ERR_INVALID_ARG;
+  if (desc->act != TT_DT_F32 && desc->act != TT_DT_BF16 && desc->act != TT_DT_E4M3)
+    return TT_ERR_INVALID_ARG;
+  if (desc->act == TT_DT_E4M3 || desc->N > (1 << 20)) return TT_ERR_UNSUPPORTED;
+  tt_plan_s* p = new (std::nothrow) tt_plan_s();
+  if (!p) return TT_ERR_INVALID_ARG;
+  p->kind = 4;
+  p->norm.N = desc->N;
+  p->norm.eps = desc->eps;
+  p->norm.act = desc->act;
+  p->norm.flags = desc->flags;
+  *out = p;
+  return TT_OK;
+}
+
+tt_status tt_norm_forward(const tt_plan_t* plan, int64_t T, const void* x, const void* res,
+                          const float* gamma, const float* beta, void* sum, void* y,
+                          float* stats, void* stream) {
+  if (!plan || plan->kind != 4 || T < 0) return TT_ERR_INVALID_ARG;
+  if (T == 0) return TT_OK;
+  if (!x || !y || !aligned_to(x, 16) || !aligned_to(y, 16) || !aligned_to(res, 16) ||
+      !aligned_to(sum, 16) || !aligned_to(gamma, 4) || !aligned_to(beta, 4) ||
+      !aligned_to(stats, 8))
+    return TT_ERR_INVALID_ARG;
+  const NormPlan& P = plan->norm;
+  NormFwdArgs a;
+  a.T = T;
+  a.N = (int)P.N;
+  a.eps = P.eps;
+  a.n = (float)P.N;
+  a.x = x;
+  a.res = res;
+  a.gamma = gamma;
+  a.beta = beta;
+  a.sum = sum;
+  a.y = y;
+  a.stats = reinterpret_cast<float2*>(stats);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  // rows start 16-byte aligned only when the width fills 16-byte units
+  prof_begin(kPhElem, st);
+  const cudaError_t e =
+      P.act == TT_DT_BF16
+          ? (P.N % 8 == 0 ? fwd_pick<__nv_bfloat16, 8>(a, st) : fwd_pick<__nv_bfloat16, 1>(a, st))
+          : (P.N % 4 == 0 ? fwd_pick<float, 4>(a, st) : fwd_pick<float, 1>(a, st));
+  prof_end(kPhElem, st);
+  count_launches(1);
+  return e == cudaSuccess ? TT_OK : TT_ERR_CUDA;
+}
+
+tt_status tt_norm_backward(const tt_plan_t* plan, int64_t T, const void* s, const void* dy,
+                           const void* dsum, const float* gamma, const float* stats, void* dx,
+                           float* dgamma, float* dbeta, void* ws, size_t ws_bytes,
+                           void* stream) {
+  if (!plan || plan->kind != 4 || T < 0) return TT_ERR_INVALID_ARG;
+  const NormPlan& P = plan->norm;
+  const int acc = (P.flags & TT_ACCUMULATE) != 0;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (!aligned_to(dgamma, 4) || !aligned_to(dbeta, 4)) return TT_ERR_INVALID_ARG;
+  if (T == 0) {
+    if (acc) return TT_OK;
+    const size_t n = (size_t)P.N * sizeof(float);
+    if (dgamma && cudaMemsetAsync(dgamma, 0, n, st) != cudaSuccess) return TT_ERR_CUDA;
+    if (dbeta && cudaMemsetAsync(dbeta, 0, n, st) != cudaSuccess) return TT_ERR_CUDA;
+    return TT_OK;
+  }
+  if (!s || !dy || !stats || !dx || !aligned_to(s, 16) || !aligned_to(dy, 16) ||
+      !aligned_to(dsum, 16) || !aligned_to(dx, 16) || !aligned_to(gamma, 4) ||
+      !aligned_to(stats, 8))
+    return TT_ERR_INVALID_ARG;
+  if (!ws || !aligned_to(ws, 256) || ws_bytes < norm_workspace_bytes(P, T))
+    return TT_ERR_WORKSPACE;
+  const int64_t blocks = bwd_blocks(P.N, T);
+  const bool wide = P.N > kMaxRegRow;
+  NormBwdArgs a;
+  a.T = T;
+  a.N = (int)P.N;
+  a.n = (float)P.N;
+  a.s = s;
+  a.dy = dy;
+  a.dsum = dsum;
+  a.gamma = gamma;
+  a.stats = reinterpret_cast<const float2*>(stats);
+  a.dx = dx;
+  a.parts = static_cast<float*>(ws);
+  a.dgamma = dgamma;
+  a.dbeta = dbeta;
+  a.accumulate = acc;
+  prof_begin(kPhElem, st);
+  cudaError_t e;
+  if (P.act == TT_DT_BF16)
+    e = wide           ? bwd_wide<__nv_bfloat16>(a, blocks, st)
+        : P.N % 8 == 0 ? bwd_pick<__nv_bfloat16, 8>(a, blocks, st)
+                       : bwd_pick<__nv_bfloat16, 1>(a, blocks, st);
+  else
+    e = wide           ? bwd_wide<float>(a, blocks, st)
+        : P.N % 4 == 0 ? bwd_pick<float, 4>(a, blocks, st)
+                       : bwd_pick<float, 1>(a, blocks, st);
+  count_launches(wide ? 2 : 1);
+  if (e == cudaSuccess && (wide || blocks > 1) && (dgamma || dbeta)) {
+    e = launch_ex(norm_reduce_kernel, dim3((unsigned)((2 * P.N + 31) / 32)), dim3(1024), 0, st,
+                  false, (const float*)a.parts, (int)blocks, a.N, dgamma, dbeta, acc);
+    count_launches(1);
+  }
+  prof_end(kPhElem, st);
+  return e == cudaSuccess ? TT_OK : TT_ERR_CUDA;
+}
+
+}  // extern "C"

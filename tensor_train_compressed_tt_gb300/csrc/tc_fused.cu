@@ -1327,8 +1327,10 @@ tt_status tc_backward(const LayerPlan& L, int64_t T, const void* x, const void* 
 extern "C" tt_status tt_set_wait_limit_ns(uint64_t ns) {
   if (ns < 1000) return TT_ERR_INVALID_ARG;
   const unsigned long long v = ns;
-  return cudaMemcpyToSymbol(ttc::g_wait_limit_ns, &v, sizeof(v)) == cudaSuccess ? TT_OK
-                                                                              : TT_ERR_CUDA;
+  return cudaMemcpyToSymbol(ttc::g_wait_limit_ns, &v, sizeof(v)) == cudaSuccess &&
+                 ttc::attn_set_wait_limit(v) == cudaSuccess
+             ? TT_OK
+             : TT_ERR_CUDA;
 }
 
 extern "C" tt_status tt_debug_skip_arrival(int site) {

@@ -46,13 +46,33 @@ struct TtmPlan {
   unsigned flags = 0;
 };
 size_t ttm_workspace_bytes(const TtmPlan& P, int64_t B);
+// Layer normalisation (norm.cu).
+struct NormPlan {
+  int64_t N = 0;
+  float eps = 0.f;
+  int act = TT_DT_F32;
+  unsigned flags = 0;
+};
+size_t norm_workspace_bytes(const NormPlan& P, int64_t T);
+
+// Windowed attention (attn.cu).
+struct AttnPlan {
+  int heads = 0, kv = 0, dim = 0;
+  int left = -1, right = -1, sinks = 0;
+  float scale = 0.f;
+  int act = TT_DT_F32;
+};
 }  // namespace ttc
 
 struct tt_plan_s {
-  int kind = 0;  // 0 = single layer, 1 = FFN pair, 2 = TT-matrix embedding, 3 = layers on one x
+  // 0 = single layer, 1 = FFN pair, 2 = TT-matrix embedding, 3 = layers on one x,
+  // 4 = layer normalisation, 5 = attention
+  int kind = 0;
   int G = 1;     // layers of a kind-3 plan
   ttc::LayerPlan L[3];
   ttc::TtmPlan ttm;
+  ttc::NormPlan norm;
+  ttc::AttnPlan attn;
 };
 
 namespace ttc {
@@ -96,6 +116,9 @@ struct DeviceStatus {
 cudaError_t read_and_clear_device_status(DeviceStatus* out);
 // The same for the embedding kernels' own word (ttm.cu).
 cudaError_t read_and_clear_ttm_status(DeviceStatus* out);
+// The same for the attention kernels' own word, and their wait limit (attn.cu).
+cudaError_t read_and_clear_attn_status(DeviceStatus* out);
+cudaError_t attn_set_wait_limit(unsigned long long ns);
 
 // ---- rank-adaptive step (rank_update.cu) ------------------------------------
 // One elementwise launch of the step over a layer's packed params / dparams.

@@ -254,3 +254,159 @@ class TTMEmbedding:
     def stats(self, ws: torch.Tensor, stream=None):
         """(distinct rows, distinct (i_1, i_2) prefixes) of the last call on ws."""
         return ttc.tt_ttm_stats(self.plan, _ptr(ws), _stream(stream))
+
+
+def _dense(t: Optional[torch.Tensor], shape, dtype: torch.dtype, name: str) -> int:
+    """Pointer of a dense CUDA tensor of the given shape and type (0 for None)."""
+    if t is None:
+        return 0
+    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError(f"{name}: expected a contiguous CUDA tensor of shape {shape} and "
+                         f"{dtype}, got {tuple(t.shape)} {t.dtype} on {t.device}")
+    return t.data_ptr()
+
+
+class TTNorm:
+    """Layer normalisation of (T, N) rows with an optional residual sum in
+    front of it: s = x + res, y = (s - mean(s)) / sqrt(var(s) + eps) gamma + beta."""
+
+    def __init__(self, N: int, dtype: torch.dtype = torch.bfloat16, eps: float = 1e-5,
+                 accumulate: bool = False):
+        self.N = int(N)
+        self.dtype = dtype
+        self.plan = ttc.tt_norm_plan(N, eps, _DT[dtype], ttc.TT_ACCUMULATE if accumulate else 0)
+
+    def workspace(self, T: int, device="cuda") -> torch.Tensor:
+        return torch.empty(ttc.tt_workspace_size(self.plan, T), dtype=torch.uint8, device=device)
+
+    def forward(self, x, gamma=None, beta=None, res=None, y=None, sum=None, stats=None,
+                stream=None):
+        """(y, s, stats): s is None without a residual (it would be x), stats
+        holds each row's mean and 1 / sqrt(var + eps) for the backward."""
+        T, N = x.shape[0], self.N
+        if y is None:
+            y = torch.empty((T, N), dtype=self.dtype, device=x.device)
+        if res is not None and sum is None:
+            sum = torch.empty((T, N), dtype=self.dtype, device=x.device)
+        if stats is None:
+            stats = torch.empty((T, 2), dtype=torch.float32, device=x.device)
+        f32, sh = torch.float32, (T, N)
+        ttc.check(ttc.tt_norm_forward(
+            self.plan, T, _dense(x, sh, self.dtype, "x"), _dense(res, sh, self.dtype, "res"),
+            _dense(gamma, (N,), f32, "gamma"), _dense(beta, (N,), f32, "beta"),
+            _dense(sum, sh, self.dtype, "sum"), _dense(y, sh, self.dtype, "y"),
+            _dense(stats, (T, 2), f32, "stats"), _stream(stream)), "tt_norm_forward")
+        return y, sum, stats
+
+    def backward(self, s, dy, gamma, stats, dsum=None, dx=None, dgamma=None, dbeta=None, ws=None,
+                 stream=None):
+        """(dx, dgamma, dbeta); dx is the gradient of x and of res.  dsum is
+        the gradient that reaches s along the residual path."""
+        T, N = s.shape[0], self.N
+        if dx is None:
+            dx = torch.empty((T, N), dtype=self.dtype, device=s.device)
+        if dgamma is None:
+            dgamma = torch.zeros(N, dtype=torch.float32, device=s.device)
+        if dbeta is None:
+            dbeta = torch.zeros(N, dtype=torch.float32, device=s.device)
+        if ws is None:
+            ws = self.workspace(T, s.device)
+        f32, sh = torch.float32, (T, N)
+        ttc.check(ttc.tt_norm_backward(
+            self.plan, T, _dense(s, sh, self.dtype, "s"), _dense(dy, sh, self.dtype, "dy"),
+            _dense(dsum, sh, self.dtype, "dsum"), _dense(gamma, (N,), f32, "gamma"),
+            _dense(stats, (T, 2), f32, "stats"), _dense(dx, sh, self.dtype, "dx"),
+            _dense(dgamma, (N,), f32, "dgamma"), _dense(dbeta, (N,), f32, "dbeta"), _ptr(ws),
+            ws.numel(), _stream(stream)), "tt_norm_backward")
+        return dx, dgamma, dbeta
+
+
+class TTSeqs:
+    """The sequences of a batch: int32 device arrays of first and past-the-end
+    rows of each one's queries and keys, the buffers' row counts and bounds on
+    a sequence's lengths.  Keeps the arrays alive."""
+
+    def __init__(self, q_begin, q_end, k_begin, k_end, Tq: int, Tk: int, max_q: int, max_k: int):
+        B = q_begin.shape[0]
+        self.arrays = (q_begin, q_end, k_begin, k_end)
+        for t in self.arrays:
+            _dense(t, (B,), torch.int32, "sequence rows")
+        self.Tq, self.Tk = int(Tq), int(Tk)
+        self.c = ttc.tt_attn_seqs(B, int(max_q), int(max_k), self.Tq, self.Tk,
+                                  *(t.data_ptr() for t in self.arrays))
+
+    @classmethod
+    def packed(cls, offsets: torch.Tensor, T: int, max_len: int) -> "TTSeqs":
+        """Self-attention over sequences packed one after another: sequence b
+        is rows offsets[b] .. offsets[b + 1] of T."""
+        return cls(offsets[:-1], offsets[1:], offsets[:-1], offsets[1:], T, T, max_len, max_len)
+
+
+class TTAttention:
+    """Attention between the Q, K, V projections and O: query i sees key j
+    when j <= i + right (right >= 0) and j >= i - left (left >= 0) or j < sinks;
+    kv_heads key heads are shared by heads / kv_heads query heads each."""
+
+    def __init__(self, heads: int, dim: int, kv_heads: Optional[int] = None,
+                 dtype: torch.dtype = torch.bfloat16, left: int = -1, right: int = -1,
+                 sinks: int = 0, scale: float = 0.0):
+        self.heads, self.dim = int(heads), int(dim)
+        self.kv_heads = self.heads if kv_heads is None else int(kv_heads)
+        self.dtype = dtype
+        self.plan = ttc.tt_attn_plan(heads, self.kv_heads, dim, left, right, sinks, scale,
+                                     _DT[dtype])
+
+    def workspace(self, seqs: TTSeqs, backward: bool = True, device="cuda") -> torch.Tensor:
+        return torch.empty(ttc.tt_attn_workspace_size(self.plan, seqs.c, backward),
+                           dtype=torch.uint8, device=device)
+
+    def _heads(self, t: torch.Tensor, rows: int, heads: int, name: str) -> ttc.tt_heads:
+        """(rows, heads, dim) of any row and head stride, or (rows, heads * dim)."""
+        shape, st = t.shape, t.stride()
+        if t.dtype == self.dtype and t.is_cuda and shape[0] == rows:
+            if len(shape) == 3 and shape[1] == heads and shape[2] == self.dim and \
+                    (st[2] == 1 or self.dim == 1):
+                return ttc.tt_heads(t.data_ptr(), st[0], st[1])
+            if len(shape) == 2 and shape[1] == heads * self.dim and \
+                    (st[1] == 1 or shape[1] == 1):
+                return ttc.tt_heads(t.data_ptr(), st[0], self.dim)
+        raise ValueError(f"{name}: expected a CUDA tensor of ({rows}, {heads}, {self.dim}) "
+                         f"{self.dtype} with its last axis dense, got {tuple(shape)} {t.dtype} "
+                         f"on {t.device}, strides {tuple(st)}")
+
+    def forward(self, q, k, v, seqs: TTSeqs, o=None, lse=None, ws=None, stream=None):
+        """(o, lse); o like q but dense, lse (heads, Tq) fp32."""
+        if o is None:
+            o = torch.empty(q.shape, dtype=self.dtype, device=q.device)
+        if lse is None:
+            lse = torch.empty((self.heads, seqs.Tq), dtype=torch.float32, device=q.device)
+        if ws is None:
+            ws = self.workspace(seqs, False, q.device)
+        H, G = self.heads, self.kv_heads
+        ttc.check(ttc.tt_attn_forward(
+            self.plan, seqs.c, self._heads(q, seqs.Tq, H, "q"), self._heads(k, seqs.Tk, G, "k"),
+            self._heads(v, seqs.Tk, G, "v"), self._heads(o, seqs.Tq, H, "o"),
+            _dense(lse, (H, seqs.Tq), torch.float32, "lse"), _ptr(ws), ws.numel(),
+            _stream(stream)), "tt_attn_forward")
+        return o, lse
+
+    def backward(self, q, k, v, o, lse, do, seqs: TTSeqs, dq=None, dk=None, dv=None, ws=None,
+                 stream=None):
+        """(dq, dk, dv) for the gradient do of o."""
+        if dq is None:
+            dq = torch.empty(q.shape, dtype=self.dtype, device=q.device)
+        if dk is None:
+            dk = torch.empty(k.shape, dtype=self.dtype, device=q.device)
+        if dv is None:
+            dv = torch.empty(v.shape, dtype=self.dtype, device=q.device)
+        if ws is None:
+            ws = self.workspace(seqs, True, q.device)
+        H, G = self.heads, self.kv_heads
+        ttc.check(ttc.tt_attn_backward(
+            self.plan, seqs.c, self._heads(q, seqs.Tq, H, "q"), self._heads(k, seqs.Tk, G, "k"),
+            self._heads(v, seqs.Tk, G, "v"), self._heads(o, seqs.Tq, H, "o"),
+            _dense(lse, (H, seqs.Tq), torch.float32, "lse"),
+            self._heads(do, seqs.Tq, H, "do"), self._heads(dq, seqs.Tq, H, "dq"),
+            self._heads(dk, seqs.Tk, G, "dk"), self._heads(dv, seqs.Tk, G, "dv"), _ptr(ws),
+            ws.numel(), _stream(stream)), "tt_attn_backward")
+        return dq, dk, dv

@@ -73,6 +73,51 @@ class tt_rank_opts(ctypes.Structure):
     ]
 
 
+class tt_norm_desc(ctypes.Structure):
+    _fields_ = [
+        ("N", ctypes.c_int64),
+        ("eps", ctypes.c_float),
+        ("act", ctypes.c_int),
+        ("flags", ctypes.c_uint),
+    ]
+
+
+class tt_attn_desc(ctypes.Structure):
+    _fields_ = [
+        ("heads", ctypes.c_int),
+        ("kv_heads", ctypes.c_int),
+        ("dim", ctypes.c_int),
+        ("left", ctypes.c_int),
+        ("right", ctypes.c_int),
+        ("sinks", ctypes.c_int),
+        ("scale", ctypes.c_float),
+        ("act", ctypes.c_int),
+        ("flags", ctypes.c_uint),
+    ]
+
+
+class tt_attn_seqs(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int),
+        ("max_q", ctypes.c_int),
+        ("max_k", ctypes.c_int),
+        ("Tq", ctypes.c_int64),
+        ("Tk", ctypes.c_int64),
+        ("q_begin", ctypes.c_void_p),
+        ("q_end", ctypes.c_void_p),
+        ("k_begin", ctypes.c_void_p),
+        ("k_end", ctypes.c_void_p),
+    ]
+
+
+class tt_heads(ctypes.Structure):
+    _fields_ = [
+        ("p", ctypes.c_void_p),
+        ("row", ctypes.c_int64),
+        ("head", ctypes.c_int64),
+    ]
+
+
 _lib = None
 _P = ctypes.c_void_p
 _SZ = ctypes.c_size_t
@@ -111,6 +156,13 @@ def lib() -> ctypes.CDLL:
             "tt_ttm_lookup": [_P, _I64, _P, _P, _P, _P, _SZ, _P],
             "tt_ttm_lookup_backward": [_P, _I64, _P, _P, _P, _P, _P, _SZ, _P],
             "tt_ttm_stats": [_P, _P, _P, _P, _P],
+            "tt_norm_plan": [_P, _P],
+            "tt_norm_forward": [_P, _I64, _P, _P, _P, _P, _P, _P, _P, _P],
+            "tt_norm_backward": [_P, _I64, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P],
+            "tt_attn_plan": [_P, _P],
+            "tt_attn_workspace_size": [_P, _P, ctypes.c_int, _P],
+            "tt_attn_forward": [_P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P],
+            "tt_attn_backward": [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P],
             "tt_get_device_status": [_P],
             "tt_set_wait_limit_ns": [ctypes.c_uint64],
             "tt_debug_skip_arrival": [ctypes.c_int],
@@ -338,6 +390,56 @@ def tt_ttm_stats(plan: Plan, ws: int, stream: int = 0):
     _check(lib().tt_ttm_stats(ctypes.c_void_p(plan.handle), ws, ctypes.byref(u),
                               ctypes.byref(p), stream), "tt_ttm_stats")
     return u.value, p.value
+
+
+def tt_norm_plan(N: int, eps: float, act: int, flags: int = 0) -> Plan:
+    desc = tt_norm_desc(int(N), float(eps), int(act), int(flags))
+    h = ctypes.c_void_p()
+    _check(lib().tt_norm_plan(ctypes.byref(desc), ctypes.byref(h)), "tt_norm_plan")
+    return Plan(h.value, "norm", ())
+
+
+def tt_norm_forward(plan: Plan, T: int, x: int, res: int, gamma: int, beta: int, sum: int,
+                    y: int, stats: int, stream: int = 0) -> int:
+    return lib().tt_norm_forward(plan.handle, T, x, res, gamma, beta, sum, y, stats, stream)
+
+
+def tt_norm_backward(plan: Plan, T: int, s: int, dy: int, dsum: int, gamma: int, stats: int,
+                     dx: int, dgamma: int, dbeta: int, ws: int, ws_bytes: int,
+                     stream: int = 0) -> int:
+    return lib().tt_norm_backward(plan.handle, T, s, dy, dsum, gamma, stats, dx, dgamma, dbeta,
+                                  ws, ws_bytes, stream)
+
+
+def tt_attn_plan(heads: int, kv_heads: int, dim: int, left: int, right: int, sinks: int,
+                 scale: float, act: int, flags: int = 0) -> Plan:
+    desc = tt_attn_desc(int(heads), int(kv_heads), int(dim), int(left), int(right), int(sinks),
+                        float(scale), int(act), int(flags))
+    h = ctypes.c_void_p()
+    _check(lib().tt_attn_plan(ctypes.byref(desc), ctypes.byref(h)), "tt_attn_plan")
+    return Plan(h.value, "attn", ())
+
+
+def tt_attn_workspace_size(plan: Plan, seqs: tt_attn_seqs, backward: bool) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().tt_attn_workspace_size(plan.handle, ctypes.byref(seqs), int(backward),
+                                        ctypes.byref(n)), "tt_attn_workspace_size")
+    return n.value
+
+
+def tt_attn_forward(plan: Plan, seqs: tt_attn_seqs, q: tt_heads, k: tt_heads, v: tt_heads,
+                    o: tt_heads, lse: int, ws: int, ws_bytes: int, stream: int = 0) -> int:
+    ref = ctypes.byref
+    return lib().tt_attn_forward(plan.handle, ref(seqs), ref(q), ref(k), ref(v), ref(o), lse, ws,
+                                 ws_bytes, stream)
+
+
+def tt_attn_backward(plan: Plan, seqs: tt_attn_seqs, q: tt_heads, k: tt_heads, v: tt_heads,
+                     o: tt_heads, lse: int, dout: tt_heads, dq: tt_heads, dk: tt_heads,
+                     dv: tt_heads, ws: int, ws_bytes: int, stream: int = 0) -> int:
+    ref = ctypes.byref
+    return lib().tt_attn_backward(plan.handle, ref(seqs), ref(q), ref(k), ref(v), ref(o), lse,
+                                  ref(dout), ref(dq), ref(dk), ref(dv), ws, ws_bytes, stream)
 
 
 def tt_get_device_status(stream: int = 0) -> int:

@@ -1,0 +1,370 @@
+"""Windowed attention on the GPU against the fp64 oracle."""
+
+import numpy as np
+import pytest
+
+from block_util import TOL, assert_near
+from oracle import block_oracle as B
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA GPU")
+    from tensor_train_compressed_tt_gb300 import _build
+    _build.build()
+
+
+def _np(t):
+    return t.double().cpu().numpy()
+
+
+def _rows(spans):
+    return [torch.tensor([s[i] for s in spans], dtype=torch.int32, device="cuda") for i in range(4)]
+
+
+def packed(lens):
+    """Self-attention: (q0, q1, k0, k1) of sequences one after another."""
+    end = np.cumsum(lens)
+    return [(int(e - n), int(e), int(e - n), int(e)) for n, e in zip(lens, end)]
+
+
+def cached(lq, lk, gap=3):
+    """Queries one after another, keys in cache slots with `gap` unused rows after each."""
+    out, q, k = [], 0, 0
+    for a, b in zip(lq, lk):
+        out.append((q, q + a, k, k + b))
+        q, k = q + a, k + b + gap
+    return out
+
+
+def _check(spans, heads, kv, dim, left, right, sinks, act, scale=0.0, make=None, backward=True,
+           seed=0, qscale=1.5, slack=0):
+    """Forward and backward against the oracle; outputs start as NaN, so that a
+    row left out shows, and rows of no sequence have to stay NaN."""
+    from tensor_train_compressed_tt_gb300 import ttc
+    from tensor_train_compressed_tt_gb300.layer import TTAttention, TTSeqs
+    r = np.random.default_rng(seed)
+    Tq = max([s[1] for s in spans], default=0) + slack
+    Tk = max([s[3] for s in spans], default=0) + slack
+    make = make or (lambda x: x)
+
+    def rand(T, H, sc=1.0):
+        x = torch.from_numpy((sc * r.standard_normal((T, H, dim))).astype(np.float32))
+        return make(x.to(DT[act]).cuda())
+
+    q, k, v, do = rand(Tq, heads, qscale), rand(Tk, kv), rand(Tk, kv), rand(Tq, heads)
+    op = TTAttention(heads, dim, kv_heads=kv, dtype=DT[act], left=left, right=right, sinks=sinks,
+                     scale=scale)
+    seqs = TTSeqs(*_rows(spans), Tq=Tq, Tk=Tk,
+                  max_q=max([s[1] - s[0] for s in spans], default=0),
+                  max_k=max([s[3] - s[2] for s in spans], default=0))
+    nan = lambda x: make(torch.full((x.shape[0], x.shape[1], dim), float("nan"), dtype=DT[act],  # noqa: E731
+                                    device="cuda"))
+    lse = torch.full((heads, Tq), float("nan"), device="cuda")
+    o, lse = op.forward(q, k, v, seqs, o=nan(q), lse=lse)
+    kw = dict(left=left, right=right, sinks=sinks, scale=scale or None)
+    ro, rl = B.attn_forward(_np(q), _np(k), _np(v), spans, **kw)
+    assert_near(_np(o), ro, TOL[act], "o")
+    # scores are fp32 sums of products of the stored inputs in either type
+    assert_near(_np(lse), rl, 1e-5, "lse")
+    if backward:
+        dq, dk, dv = op.backward(q, k, v, o, lse, do, seqs, dq=nan(q), dk=nan(k), dv=nan(v))
+        rq, rk, rv = B.attn_backward(_np(q), _np(k), _np(v), _np(do), spans, **kw)
+        assert_near(_np(dv), rv, TOL[act], "dv")
+        assert_near(_np(dq), rq, TOL[act], "dq")
+        assert_near(_np(dk), rk, TOL[act], "dk")
+    assert ttc.tt_get_device_status(torch.cuda.current_stream().cuda_stream) == 0
+    return op, q, k, v, o, lse, do, seqs
+
+
+MASKS = [(-1, -1, 0), (-1, 0, 0), (64, 64, 1), (5, 0, 2), (0, 0, 0), (40, 20, 17), (0, 3, 200),
+         (129, 0, 140), (20, -1, 1)]
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("left,right,sinks", MASKS)
+@pytest.mark.parametrize("lens", [[1], [2, 1, 3], [128], [127, 129, 1, 64], [0, 5, 0, 300, 0]],
+                         ids=str)
+def test_masks(lens, left, right, sinks, act):
+    _check(packed(lens), 2, 2, 64, left, right, sinks, act)
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("dim", [1, 3, 8, 16, 24, 32, 40, 64, 72, 80, 96, 104, 128, 129, 136, 256])
+def test_head_widths(dim, act):
+    _check(packed([70, 150]), 2, 1, dim, 50, 30, 2, act)
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("heads,kv", [(1, 1), (4, 1), (6, 2), (8, 8), (16, 2), (5, 5)])
+def test_shared_key_heads(heads, kv, act):
+    _check(packed([65, 200]), heads, kv, 64, 70, 0, 3, act)
+    _check(packed([40, 33]), heads, kv, 128, -1, -1, 0, act)
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("dim,heads,kv", [(64, 4, 4), (128, 8, 2), (40, 12, 1), (128, 16, 1)])
+@pytest.mark.parametrize("left,right,sinks", [(-1, 0, 0), (100, 0, 4), (15, 0, 1), (0, 0, 0)])
+def test_one_token_against_a_cache(dim, heads, kv, left, right, sinks, act):
+    lk = [1, 2, 17, 128, 129, 700, 1500]
+    _check(cached([1] * len(lk), lk), heads, kv, dim, left, right, sinks, act)
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("lq,lk", [([2, 3], [300, 64]), ([5, 16], [5, 1000]), ([70, 1], [200, 900]),
+                                   ([4, 9], [2, 0]), ([130, 7], [3, 7])], ids=str)
+def test_several_tokens_against_a_cache(lq, lk, act):
+    """More queries than keys leave rows that see nothing (o = 0, lse = -inf)."""
+    for left, right, sinks in ((-1, 0, 0), (33, 0, 2), (10, 4, 0)):
+        _check(cached(lq, lk), 4, 2, 64, left, right, sinks, act)
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+def test_layouts(act):
+    """Head-major tensors, slices of one fused projection, rows that start off
+    the 16-byte grid: the values come out the same."""
+    spans = packed([100, 61])
+
+    def head_major(x):
+        return x.transpose(0, 1).contiguous().transpose(0, 1)
+
+    def sliced(x):
+        T, H, D = x.shape
+        big = torch.full((T, 3 * H + 1, D), 7.0, dtype=x.dtype, device="cuda")
+        big[:, H:2 * H] = x
+        return big[:, H:2 * H]
+
+    def shifted(x):
+        T, H, D = x.shape
+        flat = torch.full((T * H * D + 1,), 7.0, dtype=x.dtype, device="cuda")
+        flat[1:] = x.reshape(-1)
+        return flat[1:].view(T, H, D)
+
+    def odd_rows(x):
+        T, H, D = x.shape
+        big = torch.full((T, H * D + 1), 7.0, dtype=x.dtype, device="cuda")
+        big[:, :H * D] = x.reshape(T, H * D)
+        return big[:, :H * D].unflatten(1, (H, D))
+
+    for make in (head_major, sliced, shifted, odd_rows):
+        for dim in (64, 128):
+            _check(spans, 4, 2, dim, 30, 10, 1, act, make=make)
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+def test_flat_heads(act):
+    """(T, heads * dim) tensors, as the projections write them."""
+    from tensor_train_compressed_tt_gb300.layer import TTAttention, TTSeqs
+    r = np.random.default_rng(1)
+    q, k, v = (torch.from_numpy(r.standard_normal((200, 4 * 64)).astype(np.float32))
+               .to(DT[act]).cuda() for _ in range(3))
+    off = torch.tensor([0, 77, 200], dtype=torch.int32, device="cuda")
+    seqs = TTSeqs.packed(off, 200, 123)
+    op = TTAttention(4, 64, dtype=DT[act], left=20, right=20)
+    o, lse = op.forward(q, k, v, seqs)
+    o3, lse3 = op.forward(*(t.view(200, 4, 64) for t in (q, k, v)), seqs)
+    assert o.shape == (200, 256) and torch.equal(o.view(200, 4, 64), o3) and torch.equal(lse, lse3)
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("scale", [0.02, 1.0])
+def test_scales(act, scale):
+    """scale 1 at width 64: scores of tens, weights from 1 down to exp(-60)."""
+    _check(packed([90, 140]), 2, 2, 64, 60, 60, 1, act, scale=scale, qscale=0.7)
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -3.0e38])
+def test_unseen_rows_reach_nothing(act, bad):
+    """Cache rows past a sequence's end, evicted by the window, or of no
+    sequence hold anything; so may the rows of a neighbouring sequence."""
+    from tensor_train_compressed_tt_gb300.layer import TTAttention, TTSeqs
+    r = np.random.default_rng(2)
+    spans = [(0, 1, 5, 405), (1, 3, 410, 547), (3, 60, 600, 700)]
+    left, sinks = 50, 3
+    Tq, Tk = 64, 720
+    q = torch.from_numpy(r.standard_normal((Tq, 4, 64)).astype(np.float32)).to(DT[act]).cuda()
+    k, v = (torch.from_numpy(r.standard_normal((Tk, 2, 64)).astype(np.float32)).to(DT[act]).cuda()
+            for _ in range(2))
+    do = torch.randn(q.shape, device="cuda").to(q.dtype)
+    seen = np.zeros(Tk, bool)
+    for q0, q1, k0, k1 in spans:
+        seen[k0:k1] |= B.attn_mask(q1 - q0, k1 - k0, left, 0, sinks).any(0)
+    ro, rl = B.attn_forward(_np(q), _np(k), _np(v), spans, left, 0, sinks)
+    rg = B.attn_backward(_np(q), _np(k), _np(v), _np(do), spans, left, 0, sinks)
+    hide = torch.from_numpy(~seen).cuda()
+    k[hide], v[hide] = bad, bad
+    q[60:], do[60:] = bad, bad
+    op = TTAttention(4, 64, kv_heads=2, dtype=DT[act], left=left, right=0, sinks=sinks)
+    for only in (spans, spans[:2], spans[2:]):
+        seqs = TTSeqs(*_rows(only), Tq=Tq, Tk=Tk, max_q=60, max_k=400)
+        o, lse = op.forward(q, k, v, seqs)
+        dq, dk, dv = op.backward(q, k, v, o, lse, do, seqs)
+        for q0, q1, k0, k1 in only:
+            assert_near(_np(o[q0:q1]), ro[q0:q1], TOL[act], "o")
+            assert_near(_np(lse[:, q0:q1]), rl[:, q0:q1], 1e-5, "lse")
+            assert_near(_np(dq[q0:q1]), rg[0][q0:q1], TOL[act], "dq")
+            assert_near(_np(dk[k0:k1]), rg[1][k0:k1], TOL[act], "dk")
+            assert_near(_np(dv[k0:k1]), rg[2][k0:k1], TOL[act], "dv")
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+def test_neighbours_do_not_leak(act):
+    """A packed sequence of NaN leaves the sequences on its sides as they are."""
+    from tensor_train_compressed_tt_gb300.layer import TTAttention, TTSeqs
+    r = np.random.default_rng(3)
+    lens = [37, 50, 41]
+    q, k, v, do = (torch.from_numpy(r.standard_normal((128, 2, 64)).astype(np.float32))
+                   .to(DT[act]).cuda() for _ in range(4))
+    off = torch.tensor(np.cumsum([0] + lens), dtype=torch.int32, device="cuda")
+    seqs = TTSeqs.packed(off, 128, 50)
+    op = TTAttention(2, 64, dtype=DT[act], left=20, right=20, sinks=1)
+
+    def run():
+        o, lse = op.forward(q, k, v, seqs)
+        return [o, lse.t()] + list(op.backward(q, k, v, o, lse, do, seqs))
+
+    first = run()
+    for t in (q, k, v, do):
+        t[37:87] = float("nan")
+    for a, b in zip(first, run()):
+        assert torch.equal(a[:37], b[:37]) and torch.equal(a[87:], b[87:])
+
+
+def test_gradients_are_bit_reproducible():
+    for act in ("f32", "bf16"):
+        op, q, k, v, o, lse, do, seqs = _check(packed([300, 129, 7]), 4, 2, 64, 60, 0, 4, act)
+        first = op.backward(q, k, v, o, lse, do, seqs)
+        for _ in range(3):
+            for a, b in zip(first, op.backward(q, k, v, o, lse, do, seqs)):
+                assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+def test_rows_of_no_sequence_stay(act):
+    _check([(2, 40, 1, 39), (50, 90, 45, 120)], 2, 2, 64, 16, 16, 1, act, slack=9)
+
+
+def test_bad_sequences_are_reported():
+    """Rows outside the buffers or longer than promised: skipped, and reported."""
+    from tensor_train_compressed_tt_gb300 import ttc
+    from tensor_train_compressed_tt_gb300.layer import TTAttention, TTSeqs
+    st = torch.cuda.current_stream().cuda_stream
+    q = torch.randn(64, 2, 64, device="cuda").bfloat16()
+    for act in ("f32", "bf16"):
+        x = q.to(DT[act])
+        op = TTAttention(2, 64, dtype=DT[act])
+        good = (0, 10, 0, 10)
+        want, _ = op.forward(x, x, x, TTSeqs(*_rows([good]), Tq=64, Tk=64, max_q=20, max_k=20))
+        for bad in ((20, 65, 20, 40), (20, 30, 60, 70), (-1, 9, 20, 30), (30, 20, 20, 30),
+                    (20, 41, 20, 30), (20, 30, 20, 41), (20, 30, -5, 5)):
+            seqs = TTSeqs(*_rows([good, bad]), Tq=64, Tk=64, max_q=20, max_k=20)
+            o, lse = op.forward(x, x, x, seqs, o=torch.full_like(x, 7.0))
+            assert ttc.tt_get_device_status(st) == 6, bad
+            assert torch.equal(o[:10], want[:10]) and bool((o[10:] == 7).all())
+            dq, dk, dv = op.backward(x, x, x, o, lse, x, seqs, dq=torch.full_like(x, 7.0))
+            assert ttc.tt_get_device_status(st) == 6, bad
+            assert bool((dq[10:] == 7).all())
+        assert ttc.tt_get_device_status(st) == 0
+
+
+@pytest.mark.parametrize("act,kv,dim", [("bf16", 8, 128), ("f32", 4, 128)])
+def test_offsets_past_32_bits(act, kv, dim):
+    """A cache of more than 2^31 elements: its last sequence against a copy of its own."""
+    from tensor_train_compressed_tt_gb300.layer import TTAttention, TTSeqs
+    n, rows = 200, (1 << 31) // (kv * dim) + 500
+    k = torch.zeros((rows, kv, dim), dtype=DT[act], device="cuda")
+    v = torch.zeros((rows, kv, dim), dtype=DT[act], device="cuda")
+    k[-n:].normal_()
+    v[-n:].normal_()
+    for lq in (1, n):
+        q = torch.randn(lq, 2 * kv, dim, device="cuda").to(DT[act])
+        op = TTAttention(2 * kv, dim, kv_heads=kv, dtype=DT[act], left=99, right=0, sinks=2)
+        far = TTSeqs(*_rows([(0, lq, rows - n, rows)]), Tq=lq, Tk=rows, max_q=lq, max_k=n)
+        near = TTSeqs(*_rows([(0, lq, 0, n)]), Tq=lq, Tk=n, max_q=lq, max_k=n)
+        kn, vn = k[-n:].clone(), v[-n:].clone()
+        o, lse = op.forward(q, k, v, far)
+        o2, lse2 = op.forward(q, kn, vn, near)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+        g = op.backward(q, kn, vn, o2, lse2, q, near)
+        dk, dv = torch.empty_like(k), torch.empty_like(v)
+        dq, dk, dv = op.backward(q, k, v, o, lse, q, far, dk=dk, dv=dv)
+        assert torch.equal(dq, g[0]) and torch.equal(dk[-n:], g[1]) and torch.equal(dv[-n:], g[2])
+        del dk, dv
+
+
+def test_another_stream_and_graph():
+    from tensor_train_compressed_tt_gb300.layer import TTAttention
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        op, q, k, v, o, lse, do, seqs = _check(packed([200, 31]), 4, 2, 64, 40, 0, 2, "bf16")
+    torch.cuda.current_stream().wait_stream(side)
+    want = [o, lse] + list(op.backward(q, k, v, o, lse, do, seqs))
+    got = [torch.zeros_like(t) for t in want]
+    ws = op.workspace(seqs)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        op.forward(q, k, v, seqs, o=got[0], lse=got[1], ws=ws)
+        op.backward(q, k, v, got[0], got[1], do, seqs, dq=got[2], dk=got[3], dv=got[4], ws=ws)
+    for _ in range(2):
+        g.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
+    assert isinstance(op, TTAttention)
+
+
+def test_wrapper_refuses():
+    from tensor_train_compressed_tt_gb300.layer import TTAttention, TTSeqs
+    op = TTAttention(4, 64, kv_heads=2)
+    off = torch.tensor([0, 8], dtype=torch.int32, device="cuda")
+    seqs = TTSeqs.packed(off, 8, 8)
+    q = torch.zeros(8, 4, 64, dtype=torch.bfloat16, device="cuda")
+    k = q[:, :2]
+    op.forward(q, k, k, seqs)
+    for bad in (q.float(), q.cpu(), q[:4], q[:, :3], q[..., :32], q[:, :, ::2]):
+        with pytest.raises(ValueError):
+            op.forward(bad, k, k, seqs)
+    with pytest.raises(ValueError):
+        op.forward(q, q, q, seqs)
+    with pytest.raises(ValueError):
+        TTSeqs.packed(off.long(), 8, 8)
+    with pytest.raises(ValueError):
+        TTSeqs(off, off[:1], off, off, Tq=8, Tk=8, max_q=8, max_k=8)
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+def test_gradient_against_differences(act):
+    """The loss's change along the gradient, from two more forward passes."""
+    from tensor_train_compressed_tt_gb300.layer import TTAttention, TTSeqs
+    r = np.random.default_rng(7)
+    lens = [50, 90]
+    q, k, v, do = (torch.from_numpy(r.standard_normal((140, 2, 32)).astype(np.float32))
+                   .to(DT[act]).cuda() for _ in range(4))
+    off = torch.tensor(np.cumsum([0] + lens), dtype=torch.int32, device="cuda")
+    seqs = TTSeqs.packed(off, 140, 90)
+    op = TTAttention(2, 32, dtype=DT[act], left=30, right=30, sinks=1)
+    o, lse = op.forward(q, k, v, seqs)
+    grads = op.backward(q, k, v, o, lse, do, seqs)
+    f32 = TTAttention(2, 32, dtype=torch.float32, left=30, right=30, sinks=1)
+    x = [t.float() for t in (q, k, v)]
+    for i in range(3):
+        g = grads[i].double()
+        step = 1e-2 * x[i].double().norm() / g.norm()
+        val = []
+        for s in (1.0, -1.0):
+            y = list(x)
+            y[i] = (x[i].double() + s * step * g).float()
+            val.append(float((f32.forward(*y, seqs)[0].double() * do.double()).sum()))
+        slope, want = (val[0] - val[1]) / (2 * float(step)), float((g * g).sum())
+        # the third-order term at a step of a hundredth of the input, and the gradient's own error
+        assert abs(slope / want - 1) < 5e-3 + 2 * TOL[act], (i, slope, want)
