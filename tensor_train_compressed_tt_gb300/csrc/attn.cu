@@ -6,6 +6,7 @@
 #include "attn.h"
 #include "attn_general.cuh"
 #include "attn_seq.cuh"
+#include "attn_tc_fwd.cuh"
 #include "ttc.h"
 
 namespace ttc {
@@ -135,8 +136,9 @@ tt_status tt_attn_forward(const tt_plan_t* plan, const tt_attn_seqs* seqs, const
   if (a.B == 0 || a.max_q == 0) return TT_OK;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   prof_begin(kPhFwd, st);
-  const cudaError_t e = P.act == TT_DT_BF16 ? general_pass<__nv_bfloat16>(a, 0, st)
-                                            : general_pass<float>(a, 0, st);
+  const cudaError_t e = P.act == TT_DT_F32 ? general_pass<float>(a, 0, st)
+                        : tc_fwd_takes(a)  ? tc_fwd(a, st)
+                                           : general_pass<__nv_bfloat16>(a, 0, st);
   prof_end(kPhFwd, st);
   return from_cuda(e);
 }

@@ -1,0 +1,164 @@
+// What the tensor-core attention kernels share: tiles of 128 rows in
+// 128-byte-swizzled shared memory boxes of 64 channels, products with one
+// operand in tensor memory, masks as bit words.
+#pragma once
+
+#include "attn_seq.cuh"
+
+namespace ttc {
+namespace {
+
+constexpr int AT = 128;                  // rows of a query or key tile
+constexpr int ABOX = AT * 128;           // bytes of [128 rows][64 bf16]
+constexpr int ALOAD = 64;                // rows a TMA box brings
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ void tma_load3(void* dst, const CUtensorMap* map, uint64_t* bar, int c0,
+                                          int c1, int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(su32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(su32(bar)), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+
+// n rows (1 .. 128) of head h from `row` on into NB boxes of 64 channels, in
+// 64-row pieces.  Rows past n up to the piece's end, and channels past the
+// head's width (zeros), come along.
+template <int NB>
+__device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* map, uint64_t* bar,
+                                          int h, int row, int n) {
+  const int pieces = (n + ALOAD - 1) / ALOAD;
+  mbar_expect_tx(bar, (uint32_t)(pieces * NB * ALOAD * 128));
+  for (int r = 0; r < pieces; ++r)
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+      tma_load3(dst + b * ABOX + r * ALOAD * 128, map, bar, 64 * b, h, row + ALOAD * r);
+}
+
+// D (tensor memory) += A (tensor memory, two bf16 of consecutive K a column) . B (shared)
+__device__ __forceinline__ void mma_ts(uint32_t dtmem, uint32_t atmem, uint64_t b, uint32_t id,
+                                       uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(dtmem),
+      "r"(atmem), "l"(b), "r"(id), "r"(acc));
+}
+
+// 32 columns of this thread's lane, not yet readable: tmem_landed orders the
+// uses after the wait.
+__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, float (&v)[32]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 " TT_LD32_REGS ", [%32];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]),
+                 "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]),
+                 "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]),
+                 "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]),
+                 "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]),
+                 "=f"(v[30]), "=f"(v[31])
+               : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait_ld() {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_landed(float (&v)[32]) {
+  asm volatile(""
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]),
+                 "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]),
+                 "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]), "+f"(v[17]),
+                 "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]),
+                 "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]));
+  asm volatile("" : "+f"(v[30]), "+f"(v[31]));
+}
+
+// 16 packed columns (32 bf16) of this thread's lane
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15]));
+}
+// 32 f32 columns of this thread's lane
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, "
+      "%20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]),
+      "f"(v[8]), "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]),
+      "f"(v[15]), "f"(v[16]), "f"(v[17]), "f"(v[18]), "f"(v[19]), "f"(v[20]), "f"(v[21]),
+      "f"(v[22]), "f"(v[23]), "f"(v[24]), "f"(v[25]), "f"(v[26]), "f"(v[27]), "f"(v[28]),
+      "f"(v[29]), "f"(v[30]), "f"(v[31]));
+}
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void tmem_take(uint32_t* slot, uint32_t cols) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                   su32(slot)),
+               "r"(cols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_give(uint32_t base, uint32_t cols) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(cols)
+               : "memory");
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Rows n .. (n rounded up to 16) - 1 of a tile's boxes set to zero by one
+// warp: the products read keys in steps of 16, and what lies past a
+// sequence's end may hold anything (0 * NaN is NaN).
+template <int NB>
+__device__ __forceinline__ void zero_tail(uint8_t* tile, int n, int lane) {
+  const int rows = (16 - (n & 15)) & 15;
+  if (!rows) return;
+  for (int i = lane; i < rows * 8 * NB; i += 32) {
+    const int b = i / (rows * 8), o = i - b * rows * 8;
+    *reinterpret_cast<uint4*>(tile + b * ABOX + n * 128 + o * 16) = make_uint4(0u, 0u, 0u, 0u);
+  }
+  fence_async_smem();
+  __syncwarp();
+}
+
+// Bits [lo, hi] of a word (none when lo > hi), lo and hi any integers.
+__device__ __forceinline__ uint32_t bit_span(int lo, int hi) {
+  const uint32_t a = lo <= 0 ? 0xFFFFFFFFu : lo > 31 ? 0u : 0xFFFFFFFFu << lo;
+  const uint32_t b = hi >= 31 ? 0xFFFFFFFFu : hi < 0 ? 0u : 0xFFFFFFFFu >> (31 - hi);
+  return a & b;
+}
+
+// (T, heads, dim) tensor as TMA sees it: boxes of 64 channels x 1 head x 64
+// rows, 128-byte swizzle, zeros outside.
+bool make_heads_map(CUtensorMap* m, const Heads& x, int64_t T, int heads, int dim) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)dim, (cuuint64_t)heads, (cuuint64_t)T};
+  // the stride of an axis of one is not used; any legal value does
+  const int64_t row = T > 1 ? x.row : 64, head = heads > 1 ? x.head : 64;
+  cuuint64_t strides[2] = {(cuuint64_t)head * 2, (cuuint64_t)row * 2};
+  cuuint32_t box[3] = {64, 1, ALOAD};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, x.p, dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The layouts that the tensor-core kernels take: 16-byte aligned rows of
+// whole 16-byte units, strides within the tensor map's 40 bits.
+bool tc_heads(const Heads& x, int64_t T, int heads) {
+  auto stride_ok = [](int64_t s) { return s > 0 && s % 8 == 0 && s < (int64_t(1) << 38); };
+  return reinterpret_cast<uintptr_t>(x.p) % 16 == 0 && T > 0 && (T == 1 || stride_ok(x.row)) &&
+         (heads == 1 || stride_ok(x.head));
+}
+
+}  // namespace
+}  // namespace ttc
