@@ -8,9 +8,9 @@
 namespace ttc {
 namespace {
 
-constexpr int AT = 128;                  // rows of a query or key tile
+constexpr int AT = 128;                  // rows of an accumulator tile
 constexpr int ABOX = AT * 128;           // bytes of [128 rows][64 bf16]
-constexpr int ALOAD = 64;                // rows a TMA box brings
+constexpr int ALOAD = 32;                // rows a TMA box brings
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -23,18 +23,18 @@ __device__ __forceinline__ void tma_load3(void* dst, const CUtensorMap* map, uin
       : "memory");
 }
 
-// n rows (1 .. 128) of head h from `row` on into NB boxes of 64 channels, in
-// 64-row pieces.  Rows past n up to the piece's end, and channels past the
-// head's width (zeros), come along.
+// n rows of head h from `row` on into NB boxes of 64 channels, `box` bytes
+// apart, in 32-row pieces.  Rows past n up to the piece's end, and channels
+// past the head's width (zeros), come along.
 template <int NB>
-__device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* map, uint64_t* bar,
-                                          int h, int row, int n) {
+__device__ __forceinline__ void load_tile(uint8_t* dst, int box, const CUtensorMap* map,
+                                          uint64_t* bar, int h, int row, int n) {
   const int pieces = (n + ALOAD - 1) / ALOAD;
   mbar_expect_tx(bar, (uint32_t)(pieces * NB * ALOAD * 128));
   for (int r = 0; r < pieces; ++r)
 #pragma unroll
     for (int b = 0; b < NB; ++b)
-      tma_load3(dst + b * ABOX + r * ALOAD * 128, map, bar, 64 * b, h, row + ALOAD * r);
+      tma_load3(dst + b * box + r * ALOAD * 128, map, bar, 64 * b, h, row + ALOAD * r);
 }
 
 // D (tensor memory) += A (tensor memory, two bf16 of consecutive K a column) . B (shared)
@@ -80,6 +80,21 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
       "r"(r[15]));
 }
+__device__ __forceinline__ void tmem_ld16_async(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_landed(uint32_t (&r)[16]) {
+  asm volatile(""
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
+}
 // 32 f32 columns of this thread's lane
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32]) {
   asm volatile(
@@ -114,16 +129,51 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// Two f32 in one 64-bit register: x * m + a, and a + b.
+__device__ __forceinline__ float2 fma2(float2 x, float2 m, float2 a) {
+  return __ffma2_rn(x, m, a);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
+
+// 32 values as bf16 to global memory, `n` (a multiple of 8) of them.  wide: the
+// address is 32-byte aligned and whole sectors can be written at once.
+__device__ __forceinline__ void st_row32(__nv_bfloat16* dst, const float (&v)[32], int n,
+                                         bool wide) {
+  uint32_t w[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) w[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    if (wide && 16 * q + 16 <= n) {
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + 16 * q),
+                   "r"(w[8 * q]), "r"(w[8 * q + 1]), "r"(w[8 * q + 2]), "r"(w[8 * q + 3]),
+                   "r"(w[8 * q + 4]), "r"(w[8 * q + 5]), "r"(w[8 * q + 6]), "r"(w[8 * q + 7])
+                   : "memory");
+    } else {
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        if (16 * q + 8 * u < n)
+          *reinterpret_cast<uint4*>(dst + 16 * q + 8 * u) =
+              make_uint4(w[8 * q + 4 * u], w[8 * q + 4 * u + 1], w[8 * q + 4 * u + 2],
+                         w[8 * q + 4 * u + 3]);
+    }
+  }
+}
+__device__ __forceinline__ bool wide_rows(const Heads& x) {
+  return ((reinterpret_cast<uintptr_t>(x.p) | (uintptr_t)(x.row * 2) | (uintptr_t)(x.head * 2)) &
+          31) == 0;
+}
+
 // Rows n .. (n rounded up to 16) - 1 of a tile's boxes set to zero by one
 // warp: the products read keys in steps of 16, and what lies past a
 // sequence's end may hold anything (0 * NaN is NaN).
 template <int NB>
-__device__ __forceinline__ void zero_tail(uint8_t* tile, int n, int lane) {
+__device__ __forceinline__ void zero_tail(uint8_t* tile, int box, int n, int lane) {
   const int rows = (16 - (n & 15)) & 15;
   if (!rows) return;
   for (int i = lane; i < rows * 8 * NB; i += 32) {
     const int b = i / (rows * 8), o = i - b * rows * 8;
-    *reinterpret_cast<uint4*>(tile + b * ABOX + n * 128 + o * 16) = make_uint4(0u, 0u, 0u, 0u);
+    *reinterpret_cast<uint4*>(tile + b * box + n * 128 + o * 16) = make_uint4(0u, 0u, 0u, 0u);
   }
   fence_async_smem();
   __syncwarp();
