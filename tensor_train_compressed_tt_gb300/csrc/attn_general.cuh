@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(kGenThreads) attn_fwd_general(AttnArgs p) {
   pdl_trigger();
   const GenWork w = gen_work(p.heads, (p.max_q + S::BT - 1) / S::BT);
   Seq s;
-  if (!load_seq(p, w.b, &s)) return;
+  if (!load_seq(p, w.b, &s, threadIdx.x == 0)) return;
   const int t0 = w.tile * S::BT;
   if (t0 >= s.lq) return;
   const int hk = w.h / p.group;
@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(kGenThreads) attn_dq_general(AttnArgs p) {
   pdl_trigger();
   const GenWork w = gen_work(p.heads, (p.max_q + S::BT - 1) / S::BT);
   Seq s;
-  if (!load_seq(p, w.b, &s)) return;
+  if (!load_seq(p, w.b, &s, threadIdx.x == 0)) return;
   const int t0 = w.tile * S::BT;
   if (t0 >= s.lq) return;
   const int hk = w.h / p.group;
@@ -348,7 +348,7 @@ __global__ void __launch_bounds__(kGenThreads) attn_dkv_general(AttnArgs p) {
   pdl_trigger();
   const GenWork w = gen_work(p.kv, (p.max_k + S::BT - 1) / S::BT);
   Seq s;
-  if (!load_seq(p, w.b, &s)) return;
+  if (!load_seq(p, w.b, &s, threadIdx.x == 0)) return;
   const int j0 = w.tile * S::BT;
   if (j0 >= s.lk) return;
   const int j1 = min(j0 + S::BT, s.lk) - 1;

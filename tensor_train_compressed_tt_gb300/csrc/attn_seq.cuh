@@ -14,13 +14,13 @@ struct Seq {
   __device__ int off() const { return lk - lq; }  // position of query row 0
 };
 
-// False, and recorded in the status word, for a sequence outside the buffers
-// or the caller's bounds.
-__device__ __forceinline__ bool load_seq(const AttnArgs& p, int b, Seq* s) {
+// False, and recorded in the status word (by the threads that tell), for a
+// sequence outside the buffers or the caller's bounds.
+__device__ __forceinline__ bool load_seq(const AttnArgs& p, int b, Seq* s, bool tell) {
   const int64_t q0 = p.q_begin[b], q1 = p.q_end[b], k0 = p.k_begin[b], k1 = p.k_end[b];
   if (q0 < 0 || q1 < q0 || q1 > p.Tq || k0 < 0 || k1 < k0 || k1 > p.Tk || q1 - q0 > p.max_q ||
       k1 - k0 > p.max_k) {
-    if (threadIdx.x == 0) record_error(TT_ERR_DEVICE, 64);
+    if (tell) record_error(TT_ERR_DEVICE, 64);
     return false;
   }
   s->q0 = q0;

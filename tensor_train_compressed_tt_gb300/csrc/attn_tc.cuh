@@ -27,14 +27,45 @@ __device__ __forceinline__ void tma_load3(void* dst, const CUtensorMap* map, uin
 // apart, in 32-row pieces.  Rows past n up to the piece's end, and channels
 // past the head's width (zeros), come along.
 template <int NB>
-__device__ __forceinline__ void load_tile(uint8_t* dst, int box, const CUtensorMap* map,
-                                          uint64_t* bar, int h, int row, int n) {
+__device__ __noinline__ void load_tile(uint8_t* dst, int box, const CUtensorMap* map,
+                                       uint64_t* bar, int h, int row, int n) {
   const int pieces = (n + ALOAD - 1) / ALOAD;
   mbar_expect_tx(bar, (uint32_t)(pieces * NB * ALOAD * 128));
+#pragma unroll 1
   for (int r = 0; r < pieces; ++r)
 #pragma unroll
     for (int b = 0; b < NB; ++b)
       tma_load3(dst + b * box + r * ALOAD * 128, map, bar, 64 * b, h, row + ALOAD * r);
+}
+// The wait for a load of one's own on the way out.
+__device__ __noinline__ void drain_one(uint64_t* b, uint32_t parity) { drain_bar(b, parity); }
+
+// Waits of these kernels: one try in line, everything else out of line.  The
+// roles of all CTAs of an SM share its instruction cache, and a hand-over
+// between two roles is short, so the out-of-line part polls for a while
+// before it looks at the timer, whose limit is a load from global memory.
+__device__ __noinline__ bool wait_long(uint64_t* b, uint32_t parity, volatile int* abort_flag,
+                                       unsigned where) {
+#pragma unroll 1
+  for (int i = 0; i < 256; ++i)
+    if (mbar_try_wait(b, parity)) return true;
+  return wait_bar(b, parity, abort_flag, where);
+}
+__device__ __forceinline__ bool wait_one(uint64_t* b, uint32_t parity, volatile int* abort_flag,
+                                         unsigned where) {
+  return mbar_try_wait(b, parity) || wait_long(b, parity, abort_flag, where);
+}
+// Every lane of a converged warp waits; the warp is converged after it.
+__device__ __forceinline__ bool wait_all(uint64_t* b, uint32_t parity, volatile int* abort_flag,
+                                         unsigned where) {
+  return __all_sync(0xffffffffu, wait_one(b, parity, abort_flag, where));
+}
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_lane() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}"
+               : "=r"(p));
+  return p != 0;
 }
 
 // D (tensor memory) += A (tensor memory, two bf16 of consecutive K a column) . B (shared)
@@ -169,14 +200,44 @@ __device__ __forceinline__ bool wide_rows(const Heads& x) {
 // sequence's end may hold anything (0 * NaN is NaN).
 template <int NB>
 __device__ __forceinline__ void zero_tail(uint8_t* tile, int box, int n, int lane) {
-  const int rows = (16 - (n & 15)) & 15;
-  if (!rows) return;
-  for (int i = lane; i < rows * 8 * NB; i += 32) {
-    const int b = i / (rows * 8), o = i - b * rows * 8;
-    *reinterpret_cast<uint4*>(tile + b * box + n * 128 + o * 16) = make_uint4(0u, 0u, 0u, 0u);
-  }
+  const int units = ((16 - (n & 15)) & 15) * 8;  // 16-byte units of a box
+  if (!units) return;
+#pragma unroll 1
+  for (int i = lane; i < units; i += 32)
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+      *reinterpret_cast<uint4*>(tile + b * box + n * 128 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
   fence_async_smem();
   __syncwarp();
+}
+
+// The next piece of work of a grid that has one CTA a piece: a running CTA
+// takes over a CTA that has not started (cluster launch control), so pieces of
+// unlike cost even out and each CTA sets itself up once.  clc_ask requests
+// one; the answer (16 bytes) lands on `bar`, and clc_take reads it: the CTA's
+// number, or -1 when none is left.
+__device__ __forceinline__ void clc_ask(uint4* answer, uint64_t* bar) {
+  mbar_expect_tx(bar, 16);
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128"
+      " [%0], [%1];" ::"r"(su32(answer)),
+      "r"(su32(bar))
+      : "memory");
+}
+__device__ __forceinline__ int clc_take(const uint4* answer) {
+  uint32_t got, x;
+  asm volatile(
+      "{\n .reg .b128 r;\n .reg .pred p;\n"
+      " ld.shared.b128 r, [%2];\n"
+      " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n"
+      " selp.u32 %0, 1, 0, p;\n"
+      " mov.u32 %1, 0;\n"
+      " @p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n}"
+      : "=r"(got), "=r"(x)
+      : "r"(su32(answer))
+      : "memory");
+  fence_async_smem();  // the next answer is written through the async proxy
+  return got ? (int)x : -1;
 }
 
 // Bits [lo, hi] of a word (none when lo > hi), lo and hi any integers.

@@ -368,3 +368,34 @@ def test_gradient_against_differences(act):
         slope, want = (val[0] - val[1]) / (2 * float(step)), float((g * g).sum())
         # the third-order term at a step of a hundredth of the input, and the gradient's own error
         assert abs(slope / want - 1) < 5e-3 + 2 * TOL[act], (i, slope, want)
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_scores_that_rise_far(act, dim):
+    """Scores that grow along the keys by hundreds of nats: the weights of a
+    row's first keys vanish against those of its last.  An fp32 score of size s
+    is off by some s 2^-24, which its weight takes over as a relative error:
+    with scores of up to 1200 that is 1.5e-4 on top of the usual bound."""
+    from tensor_train_compressed_tt_gb300.layer import TTAttention, TTSeqs
+    r = np.random.default_rng(11)
+    n = 300
+    q = r.standard_normal((n, 2, dim)).astype(np.float32)
+    k = r.standard_normal((n, 2, dim)).astype(np.float32)
+    q[:, :, 0] = np.where(np.arange(n)[:, None] % 3 == 0, 8.0, 0.5)
+    k[:, :, 0] = np.arange(n)[:, None] * 0.5
+    q, k, v, do = (torch.from_numpy(a).to(DT[act]).cuda() for a in
+                   (q, k, r.standard_normal((n, 2, dim)).astype(np.float32),
+                    r.standard_normal((n, 2, dim)).astype(np.float32)))
+    off = torch.tensor([0, 120, n], dtype=torch.int32, device="cuda")
+    spans = [(0, 120, 0, 120), (120, n, 120, n)]
+    seqs = TTSeqs.packed(off, n, 180)
+    for left, right, sinks in ((-1, -1, 0), (-1, 0, 0), (100, 0, 2)):
+        op = TTAttention(2, dim, dtype=DT[act], left=left, right=right, sinks=sinks, scale=1.0)
+        o, lse = op.forward(q, k, v, seqs)
+        kw = dict(left=left, right=right, sinks=sinks, scale=1.0)
+        ro, rl = B.attn_forward(_np(q), _np(k), _np(v), spans, **kw)
+        assert_near(_np(o), ro, TOL[act] + 1200 * 2.0 ** -23, "o")
+        assert_near(_np(lse), rl, 1e-5, "lse")
+        got = op.backward(q, k, v, o, lse, do, seqs)
+        assert all(bool(torch.isfinite(t.float()).all()) for t in got)
