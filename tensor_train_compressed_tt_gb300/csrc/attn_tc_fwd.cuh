@@ -51,12 +51,13 @@ struct TcFwd {
   // Two buffers of S and one O share 256 columns of tensor memory (two CTAs
   // an SM): 96 + 96 + 64, or 64 + 64 + 128.
   static constexpr int KT = NB == 1 ? 96 : 64;  // keys of a tile
+  static constexpr int QS = NB == 1 ? 2 : 1;    // query tiles in flight
   static constexpr int KP = NB == 1 ? 3 : 2;    // pairs of a key and a value tile in flight
   static constexpr int CTAS = 2;                // CTAs an SM
   static constexpr int KBOX = KT * 128, UNIT = NB * KBOX;
   static constexpr uint32_t O_COL = 2 * KT, COLS = 256;
   struct Shared {
-    uint64_t q_full, q_empty, kv_full[2 * KP], kv_empty[2 * KP];
+    uint64_t q_full[QS], q_empty[QS], kv_full[2 * KP], kv_empty[2 * KP];
     uint64_t s_full[2], p_full[2], pv_done[2], o_free, fin;  // [tile & 1]
     uint64_t item_full[2], item_empty[2], clc;
     FwdItem item[2];
@@ -64,7 +65,7 @@ struct TcFwd {
     uint32_t tmem;
     int abort_flag, never;
   };
-  static constexpr size_t kSmem = NB * ABOX + 2 * KP * UNIT + sizeof(Shared) + 1024;
+  static constexpr size_t kSmem = QS * NB * ABOX + 2 * KP * UNIT + sizeof(Shared) + 1024;
 };
 
 constexpr int kTcThreads = 192;
@@ -140,15 +141,14 @@ __global__ void __launch_bounds__(kTcThreads, TcFwd<NB>::CTAS)
     attn_fwd_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                 const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ AttnArgs p) {
   using C = TcFwd<NB>;
-  constexpr int KT = C::KT, KP = C::KP;
+  constexpr int KT = C::KT, KP = C::KP, QS = C::QS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* qbuf = align1k(smem_raw);
-  uint8_t* kvbuf = qbuf + NB * ABOX;  // K and V of pair s: units 2 s and 2 s + 1
+  uint8_t* kvbuf = qbuf + QS * NB * ABOX;  // K and V of pair s: units 2 s and 2 s + 1
   auto& S = *reinterpret_cast<typename C::Shared*>(kvbuf + 2 * KP * C::UNIT);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    mbar_init(&S.q_full, 1);
-    mbar_init(&S.q_empty, 1);
+    for (int i = 0; i < QS; ++i) mbar_init(&S.q_full[i], 1), mbar_init(&S.q_empty[i], 1);
 #pragma unroll 1
     for (int i = 0; i < 2 * KP; ++i) mbar_init(&S.kv_full[i], 1), mbar_init(&S.kv_empty[i], 1);
 #pragma unroll 1
@@ -182,47 +182,69 @@ __global__ void __launch_bounds__(kTcThreads, TcFwd<NB>::CTAS)
       uint32_t ph = 1;  // parity of the ring's empty barriers, as of a round before the first
       bool ok = true;
       int cta = (int)blockIdx.x;
+      FwdItem cur, w;
+      cur.nt = 0;
+      bool more = true;
 #pragma unroll 1
-      while (cta >= 0) {
-        clc_ask(&S.answer, &S.clc);  // the one after this
-        ++asked;
-        FwdItem w;
-        if (ok && fwd_item<KT>(p, (uint32_t)cta, ntiles, &w)) {
-          ok = wait_one(&S.item_empty[n & 1], ((n >> 1) & 1) ^ 1, abort_flag, 99);
-          if (ok) {
+      while (more && ok) {
+        int u = 0;  // K, V of tile 0, K, V of tile 1, ...
+#pragma unroll 1
+        for (int pass = 0; pass < 2; ++pass) {
+          // With two query buffers the next piece of work is looked for, and its
+          // queries sent for, once the ring of keys is full.
+          const int end = pass == 0 && QS == 2 ? min(2 * KP, 2 * cur.nt) : 2 * cur.nt;
+#pragma unroll 1
+          for (; ok && u < end; ++u) {
+            int j0, nk;
+            cur.tile<KT>(u >> 1, &j0, &nk);
+            ok = wait_one(&S.kv_empty[s], ph, abort_flag, 101);
+            if (!ok) break;
+            load_tile<NB>(kvbuf + s * C::UNIT, C::KBOX, u & 1 ? &tm_v : &tm_k, &S.kv_full[s],
+                          cur.h / p.group, (int)cur.k0 + j0, nk);
+            ++loads;
+            if (++s == 2 * KP) s = 0, ph ^= 1;
+          }
+          more = pass == 0 ? false : more;
+#pragma unroll 1
+          while (pass == 0 && ok && !more) {
+            if (asked > 0)
+              cta = wait_one(&S.clc, (asked - 1) & 1, &S.never, 96) ? clc_take(&S.answer) : -1;
+            if (cta < 0) break;
+            clc_ask(&S.answer, &S.clc);  // the one after it
+            ++asked;
+            more = fwd_item<KT>(p, (uint32_t)cta, ntiles, &w);
+            if (!more) continue;
+            ok = wait_one(&S.item_empty[n & 1], ((n >> 1) & 1) ^ 1, abort_flag, 99);
+            if (!ok) break;
             S.item[n & 1] = w;
             mbar_arrive(&S.item_full[n & 1]);
             ++n;
-          }
-          if (ok && w.nt > 0) {
-            const int hk = w.h / p.group;
-            ok = wait_one(&S.q_empty, (nload & 1) ^ 1, abort_flag, 100);
-            if (ok) {
-              load_tile<NB>(qbuf, ABOX, &tm_q, &S.q_full, w.h, (int)w.q0 + w.t0, w.nq);
-              ++nload;
-            }
-#pragma unroll 1
-            for (int u = 0; ok && u < 2 * w.nt; ++u) {  // K, V of tile 0, K, V of tile 1, ...
-              int j0, nk;
-              w.tile<KT>(u >> 1, &j0, &nk);
-              ok = wait_one(&S.kv_empty[s], ph, abort_flag, 101);
+            if (w.nt > 0) {
+              const int qs = nload % QS;
+              ok = wait_one(&S.q_empty[qs], ((nload / QS) & 1) ^ 1, abort_flag, 100);
               if (!ok) break;
-              load_tile<NB>(kvbuf + s * C::UNIT, C::KBOX, u & 1 ? &tm_v : &tm_k, &S.kv_full[s],
-                            hk, (int)w.k0 + j0, nk);
-              ++loads;
-              if (++s == 2 * KP) s = 0, ph ^= 1;
+              load_tile<NB>(qbuf + qs * NB * ABOX, ABOX, &tm_q, &S.q_full[qs], w.h,
+                            (int)w.q0 + w.t0, w.nq);
+              ++nload;
             }
           }
         }
-        // After an abort the remaining CTAs are still taken over, and do nothing.
-        cta = wait_one(&S.clc, (asked - 1) & 1, &S.never, 96) ? clc_take(&S.answer) : -1;
+        cur = w;
       }
-      if (ok && wait_one(&S.item_empty[n & 1], ((n >> 1) & 1) ^ 1, abort_flag, 98)) {
+      // After an abort the CTAs that have not started are still taken over, and do nothing.
+#pragma unroll 1
+      while (!ok && cta >= 0) {
+        cta = wait_one(&S.clc, (asked - 1) & 1, &S.never, 98) ? clc_take(&S.answer) : -1;
+        if (cta >= 0) clc_ask(&S.answer, &S.clc), ++asked;
+      }
+      if (ok && wait_one(&S.item_empty[n & 1], ((n >> 1) & 1) ^ 1, abort_flag, 94)) {
         S.item[n & 1].nt = -1;
         mbar_arrive(&S.item_full[n & 1]);
       }
       // nothing is in flight into shared memory when the CTA leaves
-      if (nload > 0) drain_one(&S.q_full, (uint32_t)((nload - 1) & 1));
+#pragma unroll 1
+      for (int i = 1; i <= QS && i <= nload; ++i)
+        drain_one(&S.q_full[(nload - i) % QS], (uint32_t)(((nload - i) / QS) & 1));
 #pragma unroll 1
       for (int i = 0; i < 2 * KP && i < loads; ++i) {
         if (--s < 0) s = 2 * KP - 1, ph ^= 1;
@@ -249,7 +271,7 @@ __global__ void __launch_bounds__(kTcThreads, TcFwd<NB>::CTAS)
           int j0;
           S.item[n & 1].template tile<KT>(t, &j0, &nk);
           // S of tile g goes where P of tile g - 2 was
-          if ((t == 0 && !wait_all(&S.q_full, nload & 1, abort_flag, 105)) ||
+          if ((t == 0 && !wait_all(&S.q_full[nload % QS], (nload / QS) & 1, abort_flag, 105)) ||
               !wait_all(&S.kv_full[2 * ss], ps, abort_flag, 107) ||
               (g > 1 && !wait_all(&S.pv_done[g & 1], ((g >> 1) - 1) & 1, abort_flag, 106))) {
             ok = false;
@@ -257,7 +279,7 @@ __global__ void __launch_bounds__(kTcThreads, TcFwd<NB>::CTAS)
           }
           tc_fence_after();
           if (elect_lane()) {
-            const uint64_t q = kdesc(su32(qbuf));
+            const uint64_t q = kdesc(su32(qbuf + (nload % QS) * NB * ABOX));
             const uint64_t k = kdesc(su32(kvbuf + 2 * ss * C::UNIT));
             const uint32_t id = idesc(128, (nk + 15) & ~15, 0, 0);
             const uint32_t sc = tmem + (g & 1) * KT;
@@ -267,7 +289,7 @@ __global__ void __launch_bounds__(kTcThreads, TcFwd<NB>::CTAS)
                   k + (c >> 2) * (C::KBOX >> 4) + 2 * (c & 3), id, c != 0);
             mma_commit(&S.s_full[g & 1]);
             mma_commit(&S.kv_empty[2 * ss]);
-            if (t == nt - 1) mma_commit(&S.q_empty);
+            if (t == nt - 1) mma_commit(&S.q_empty[nload % QS]);
           }
           __syncwarp();
           if (++ss == KP) ss = 0, ps ^= 1;
