@@ -6,6 +6,7 @@
 #include "attn.h"
 #include "attn_general.cuh"
 #include "attn_seq.cuh"
+#include "attn_tc_bwd.cuh"
 #include "attn_tc_fwd.cuh"
 #include "ttc.h"
 
@@ -37,6 +38,10 @@ bool seqs_ok(const tt_attn_seqs* s) {
     if (s->B > 0 && (!a[i] || !aligned_to(a[i], 4))) return false;
   return true;
 }
+
+// Fewest query rows of a sequence for the tensor-core backward: of fewer, most of
+// a 128-row tile is empty.
+constexpr int kTcBwdRows = 32;
 
 // A tensor that the call reads or writes when it has rows.
 bool heads_ok(const tt_heads* h, int64_t rows, int act, Heads* out) {
@@ -70,9 +75,12 @@ AttnArgs make_args(const AttnPlan& P, const tt_attn_seqs* s) {
   return a;
 }
 
-// Workspace of a pass: delta in a backward.
+// Workspace of a pass.  Backward: delta, then the partial sums of key tiles in pieces.
+size_t delta_bytes(const AttnPlan& P, const tt_attn_seqs* s) {
+  return al256((size_t)P.heads * (size_t)s->Tq * sizeof(float));
+}
 size_t attn_ws(const AttnPlan& P, const tt_attn_seqs* s, bool backward) {
-  return backward ? al256((size_t)P.heads * (size_t)s->Tq * sizeof(float)) : 0;
+  return backward ? delta_bytes(P, s) + al256(bwd_parts_bytes(P, s)) : 0;
 }
 
 tt_status from_cuda(cudaError_t e) {
@@ -165,7 +173,11 @@ tt_status tt_attn_backward(const tt_plan_t* plan, const tt_attn_seqs* seqs, cons
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   prof_begin(kPhBwd, st);
   cudaError_t e = cudaSuccess;
-  for (int pass = 1; pass <= 2 && e == cudaSuccess; ++pass)
+  const bool tc = P.act == TT_DT_BF16 && tc_bwd_takes(a) && a.max_q >= kTcBwdRows;
+  if (tc)
+    e = tc_bwd(P, seqs, a, reinterpret_cast<float*>(static_cast<char*>(ws) + delta_bytes(P, seqs)),
+               st);
+  for (int pass = 1; pass <= 2 && !tc && e == cudaSuccess; ++pass)
     e = P.act == TT_DT_BF16 ? general_pass<__nv_bfloat16>(a, pass, st)
                             : general_pass<float>(a, pass, st);
   prof_end(kPhBwd, st);

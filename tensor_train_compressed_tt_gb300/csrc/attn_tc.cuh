@@ -28,9 +28,10 @@ __device__ __forceinline__ void tma_load3(void* dst, const CUtensorMap* map, uin
 // past the head's width (zeros), come along.
 template <int NB>
 __device__ __noinline__ void load_tile(uint8_t* dst, int box, const CUtensorMap* map,
-                                       uint64_t* bar, int h, int row, int n) {
+                                       uint64_t* bar, int h, int row, int n, int tiles = 1) {
+  // (bytes of all the tiles that come on this phase of the barrier; 0: told before)
   const int pieces = (n + ALOAD - 1) / ALOAD;
-  mbar_expect_tx(bar, (uint32_t)(pieces * NB * ALOAD * 128));
+  if (tiles) mbar_expect_tx(bar, (uint32_t)(tiles * pieces * NB * ALOAD * 128));
 #pragma unroll 1
   for (int r = 0; r < pieces; ++r)
 #pragma unroll

@@ -1,0 +1,734 @@
+// Tensor-core backward of windowed attention (bf16, heads of up to 128
+// channels in multiples of 8), as two passes of one kernel.
+//
+// With s = c q.k - lse (in powers of two), p = exp2(s), dp = do.v and
+// ds = p (dp - delta), delta = sum_j p dp = o.do:
+//   dq = scale ds k   needs a tile of queries and every key it sees,
+//   dk = scale ds^T q, dv = p^T do   a tile of keys and every query that sees it.
+// One kernel for both would add one of the two into memory from many CTAs: an
+// fp32 buffer of dq's size read and written again and again, in an order that
+// changes.  Two passes compute s and dp twice (7 products instead of 5, twice
+// the exponentials), keep every sum in tensor memory in a fixed order, and
+// write each gradient once.
+//
+// Both passes have the same shape.  X1, X2 are the 128 rows that a CTA works
+// on (Q and dO, or K and V), Y1, Y2 tiles of YT of the others' rows (K and V,
+// or Q and dO):  S = X1 Y1^T and dP = X2 Y2^T into tensor memory, the softmax
+// warps (thread = row) put p and ds over them as bf16, and the accumulators
+// take  acc0 += dS Y1  (dq, or dk) and, in the pass over keys, acc1 += P Y2 (dv).
+//
+// delta comes from the stored o, whose rounding shows in rows of few keys:
+// sum_j ds_j, which should vanish, is then delta's error (the p_j add up to 1).
+// The first pass adds that sum to the delta that it leaves for the second.
+//
+// Roles as in the forward.  Heads of up to 64 channels run two CTAs an SM with
+// one buffer of S and dP each; wider ones fill the tensor memory with two
+// buffers in one CTA, each with its own four softmax warps.
+//
+// The pass over keys: the first tokens are seen by every later query, so their
+// tile is cut into pieces of its list of query tiles, each the work of one
+// item; so is every tile when there are fewer tiles than SMs.  The pieces'
+// sums go to the workspace in fp32 and are added in order by one more kernel.
+#pragma once
+
+#include "attn_tc.cuh"
+#include "attn_tc_fwd.cuh"
+
+namespace ttc {
+namespace {
+
+struct BwdCut {
+  int tiles;           // key tiles of the longest sequence
+  int lead;            // of them, those that hold first tokens outside the window's bound
+  int lead_pieces, pieces;
+  int64_t lead_slots;  // partial slots of all lead tiles (the others' follow)
+  float* parts;        // [slot][2][128][dim]
+};
+
+struct BwdItem {
+  int64_t x0, y0;      // first rows of the sequence in X and in Y
+  int hx, r0, nx;      // head of X, first row and rows of the tile
+  int off, sinks;      // position of query row 0; first tokens
+  int nt;              // tiles of Y; < 0: no more work
+  // over keys: the two spans, tiles of the first
+  KeySpan ks;
+  int n1;
+  // over queries: rows [t0, t1), tiles of one head, first entry of the list
+  int t0, t1, per, u0;
+  int slot;            // partial sums go here (-1: the gradients themselves)
+};
+
+template <bool KV, int NB>
+struct TcBwd {
+  static constexpr int BUF = NB;                          // buffers of S and dP
+  static constexpr int YT = !KV && NB == 1 ? 96 : 64;     // rows of a Y tile
+  static constexpr int KP = NB == 1 ? (KV ? 4 : 3) : 4;   // pairs of Y tiles in flight
+  static constexpr int CTAS = NB == 1 ? 2 : 1;            // CTAs an SM
+  static constexpr int YBOX = YT * 128, UNIT = NB * YBOX;
+  static constexpr uint32_t ACC = BUF * 2 * YT, COLS = NB == 1 ? 256 : 512;
+  static constexpr int WARPS = 4 * BUF;                   // softmax warps
+  static constexpr int THREADS = 32 * (WARPS + 2);
+  struct Shared {
+    uint64_t x_full, x_empty, y_full[2 * KP], y_empty[2 * KP];
+    uint64_t s_full[2], p_full[2], done[2], acc_full, acc_free, fin;  // [tile & 1]
+    uint64_t item_full[2], item_empty[2], clc;
+    uint64_t col_full[2];  // [buffer]
+    BwdItem item[2];
+    uint4 answer;
+    float col[KV ? BUF : 1][2][2][KV ? YT : 4];  // lse and delta of a tile's queries
+    float half[KV ? 1 : AT];  // the second buffer's sums of ds
+    uint32_t tmem;
+    int abort_flag, never;
+  };
+  static constexpr size_t kSmem = 2 * NB * ABOX + 2 * KP * UNIT + sizeof(Shared) + 1024;
+  static_assert(ACC + (KV ? 2 : 1) * 64 * NB <= COLS, "tensor memory");
+};
+
+// Tile u of an item's list: head, first row, rows.
+template <bool KV, int YT>
+__device__ __forceinline__ void bwd_tile(const BwdItem& w, const AttnArgs& p, int u, int* h,
+                                         int* r, int* n) {
+  if (KV) {
+    const int v = w.u0 + u, g = v / w.per;
+    *h = w.hx * p.group + g;
+    *r = w.t0 + YT * (v - g * w.per);
+    *n = min(YT, w.t1 - *r);
+  } else {
+    *h = w.hx / p.group;
+    if (u < w.n1) {
+      *r = YT * u;
+      *n = min(YT, w.ks.a1 - *r);
+    } else {
+      *r = w.ks.b0 + YT * (u - w.n1);
+      *n = min(YT, w.ks.b1 - *r);
+    }
+  }
+}
+
+// CTA number -> item.  False: nothing to do.
+template <bool KV, int YT>
+__device__ __forceinline__ bool bwd_item(const AttnArgs& p, const BwdCut& cut, uint32_t cta,
+                                         BwdItem* w) {
+  Seq s;
+  w->sinks = p.sinks;
+  w->slot = -1;
+  if (KV) {
+    const uint32_t lead = cut.lead * cut.lead_pieces;
+    const uint32_t per = lead + (cut.tiles - cut.lead) * cut.pieces;
+    const uint32_t r = cta / per, e = cta - r * per;
+    const uint32_t b = r / (uint32_t)p.kv;
+    w->hx = (int)(r - b * p.kv);
+    int tile, piece, pieces;
+    if (e < lead) {
+      pieces = cut.lead_pieces;
+      tile = e / pieces;
+      piece = e - tile * pieces;
+      if (pieces > 1) w->slot = (int)(r * lead + e);
+    } else {
+      pieces = cut.pieces;
+      tile = (e - lead) / pieces;
+      piece = e - lead - tile * pieces;
+      if (pieces > 1)
+        w->slot = (int)(cut.lead_slots + r * (per - lead) + (e - lead));
+      tile += cut.lead;
+    }
+    if (!load_seq(p, (int)b, &s, true)) return false;
+    w->r0 = tile * AT;
+    if (w->r0 >= s.lk) return false;
+    w->x0 = s.k0;
+    w->y0 = s.q0;
+    w->nx = min(AT, s.lk - w->r0);
+    const RowSpan rs = row_span(p, s, w->r0, w->r0 + w->nx - 1);
+    w->t0 = rs.t0;
+    w->t1 = rs.t1;
+    w->per = (rs.t1 - rs.t0 + YT - 1) / YT;
+    const int list = w->per * p.group;
+    w->u0 = (int)((int64_t)list * piece / pieces);
+    w->nt = (int)((int64_t)list * (piece + 1) / pieces) - w->u0;
+    if (w->per == 0) w->per = 1;
+  } else {
+    const uint32_t ntiles = (p.max_q + AT - 1) / AT;
+    const uint32_t r = cta / ntiles;
+    const int tile = (int)(ntiles - 1 - (cta - r * ntiles));
+    const uint32_t b = r / (uint32_t)p.heads;
+    w->hx = (int)(r - b * p.heads);
+    if (!load_seq(p, (int)b, &s, true)) return false;
+    w->r0 = tile * AT;
+    if (w->r0 >= s.lq) return false;
+    w->x0 = s.q0;
+    w->y0 = s.k0;
+    w->nx = min(AT, s.lq - w->r0);
+    const int i0 = w->r0 + s.off();
+    w->ks = key_span(p, s.lk, i0, i0 + w->nx - 1);
+    w->n1 = (w->ks.a1 + YT - 1) / YT;
+    w->nt = w->n1 + (w->ks.b1 - w->ks.b0 + YT - 1) / YT;
+  }
+  w->off = s.off();
+  return true;
+}
+
+// sum over the channels of o do, of one row
+__device__ __noinline__ float row_delta(const AttnArgs& p, int64_t r, int h) {
+  const uint4* o = reinterpret_cast<const uint4*>(p.o.at<const __nv_bfloat16>(r, h));
+  const uint4* d = reinterpret_cast<const uint4*>(p.dout.at<const __nv_bfloat16>(r, h));
+  float s = 0.f;
+#pragma unroll 2
+  for (int e = 0; e < p.dim / 8; ++e) {
+    const uint4 a = o[e], b = d[e];
+    const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      s = fmaf(__uint_as_float(x[i] << 16), __uint_as_float(y[i] << 16), s);
+      s = fmaf(__uint_as_float(x[i] & 0xFFFF0000u), __uint_as_float(y[i] & 0xFFFF0000u), s);
+    }
+  }
+  return s;
+}
+
+template <bool KV, int NB>
+__global__ void __launch_bounds__(TcBwd<KV, NB>::THREADS, TcBwd<KV, NB>::CTAS)
+    attn_bwd_tc(const __grid_constant__ CUtensorMap tm_x1, const __grid_constant__ CUtensorMap tm_x2,
+                const __grid_constant__ CUtensorMap tm_y1, const __grid_constant__ CUtensorMap tm_y2,
+                const __grid_constant__ AttnArgs p, const __grid_constant__ BwdCut cut) {
+  using C = TcBwd<KV, NB>;
+  constexpr int YT = C::YT, KP = C::KP, BUF = C::BUF, WARPS = C::WARPS;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* xbuf = align1k(smem_raw);      // X1, then X2
+  uint8_t* ybuf = xbuf + 2 * NB * ABOX;   // Y1 and Y2 of pair s: units 2 s and 2 s + 1
+  auto& S = *reinterpret_cast<typename C::Shared*>(ybuf + 2 * KP * C::UNIT);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    mbar_init(&S.x_full, 1);
+    mbar_init(&S.x_empty, 1);
+#pragma unroll 1
+    for (int i = 0; i < 2 * KP; ++i) mbar_init(&S.y_full[i], 1), mbar_init(&S.y_empty[i], 1);
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&S.s_full[i], 1);
+      mbar_init(&S.p_full[i], 4);
+      mbar_init(&S.done[i], 1);
+      mbar_init(&S.col_full[i], 4);
+      mbar_init(&S.item_full[i], 1);
+      mbar_init(&S.item_empty[i], WARPS + 1);
+    }
+    mbar_init(&S.acc_full, 1);
+    mbar_init(&S.acc_free, WARPS);
+    mbar_init(&S.clc, 1);
+    mbar_init(&S.fin, 1);
+    S.abort_flag = S.never = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == WARPS + 1) tmem_take(&S.tmem, C::COLS);
+  pdl_wait();
+  pdl_trigger();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = S.tmem;
+  volatile int* abort_flag = &S.abort_flag;
+
+  if (warp == WARPS) {
+    // ---------------- work and loads
+    if (lane == 0) {
+      int n = 0, nload = 0, s = 0, loads = 0;
+      uint32_t ph = 1, clc = 0;  // parity of the ring's empty barriers; of the next answer
+      bool ok = true;
+      int cta = (int)blockIdx.x;
+#pragma unroll 1
+      while (cta >= 0) {
+        clc_ask(&S.answer, &S.clc);  // the one after this
+        BwdItem w;
+        if (ok && bwd_item<KV, YT>(p, cut, (uint32_t)cta, &w)) {
+          ok = wait_one(&S.item_empty[n & 1], ((n >> 1) & 1) ^ 1, abort_flag, 120);
+          if (ok) {
+            S.item[n & 1] = w;
+            mbar_arrive(&S.item_full[n & 1]);
+            ++n;
+          }
+          if (ok && w.nt > 0) {
+            ok = wait_one(&S.x_empty, (nload & 1) ^ 1, abort_flag, 121);
+            if (ok) {
+              load_tile<NB>(xbuf, ABOX, &tm_x1, &S.x_full, w.hx, (int)w.x0 + w.r0, w.nx, 2);
+              load_tile<NB>(xbuf + NB * ABOX, ABOX, &tm_x2, &S.x_full, w.hx, (int)w.x0 + w.r0,
+                            w.nx, 0);
+              ++nload;
+            }
+#pragma unroll 1
+            for (int u = 0; ok && u < 2 * w.nt; ++u) {  // Y1, Y2 of tile 0, of tile 1, ...
+              int h, r, ny;
+              bwd_tile<KV, YT>(w, p, u >> 1, &h, &r, &ny);
+              ok = wait_one(&S.y_empty[s], ph, abort_flag, 122);
+              if (!ok) break;
+              load_tile<NB>(ybuf + s * C::UNIT, C::YBOX, u & 1 ? &tm_y2 : &tm_y1, &S.y_full[s], h,
+                            (int)w.y0 + r, ny);
+              ++loads;
+              if (++s == 2 * KP) s = 0, ph ^= 1;
+            }
+          }
+        }
+        // After an abort the CTAs that have not started are still taken over, and do nothing.
+        cta = wait_one(&S.clc, clc, &S.never, 123) ? clc_take(&S.answer) : -1;
+        clc ^= 1;
+      }
+      if (ok && wait_one(&S.item_empty[n & 1], ((n >> 1) & 1) ^ 1, abort_flag, 124)) {
+        S.item[n & 1].nt = -1;
+        mbar_arrive(&S.item_full[n & 1]);
+      }
+      // nothing is in flight into shared memory when the CTA leaves
+      if (nload > 0) drain_one(&S.x_full, (uint32_t)((nload - 1) & 1));
+#pragma unroll 1
+      for (int i = 0; i < 2 * KP && i < loads; ++i) {
+        if (--s < 0) s = 2 * KP - 1, ph ^= 1;
+        drain_one(&S.y_full[s], ph ^ 1);  // the last load into unit s
+      }
+    }
+  } else if (warp == WARPS + 1) {
+    // ---------------- products: S and dP of tile t, then the sums of tile t - (BUF - 1)
+    const int ksteps = (p.dim + 15) >> 4;
+    const uint32_t id_acc = idesc(128, ksteps * 16, 0, 1);
+    int g = 0, nload = 0, ss = 0, sv = 0;  // tiles so far; pair of the next S, of the next sums
+    uint32_t ps = 0;                       // parity of the former
+    bool ok = true;
+#pragma unroll 1
+    for (int n = 0; ok; ++n) {
+      if (!wait_all(&S.item_full[n & 1], (n >> 1) & 1, abort_flag, 125)) break;
+      const int nt = S.item[n & 1].nt;
+      if (nt < 0) break;
+      int prev_ny = 0;
+#pragma unroll 1
+      for (int t = 0; ok && nt > 0 && t < nt + BUF - 1; ++t) {
+        int ny = 0;
+        if (t < nt) {
+          int h, r;
+          bwd_tile<KV, YT>(S.item[n & 1], p, t, &h, &r, &ny);
+          // S and dP of tile g go where the weights of tile g - BUF were
+          if ((t == 0 && !wait_all(&S.x_full, nload & 1, abort_flag, 126)) ||
+              (g >= BUF && !wait_all(&S.done[(g - BUF) & 1], ((g - BUF) >> 1) & 1, abort_flag,
+                                     127))) {
+            ok = false;
+            break;
+          }
+#pragma unroll 1
+          for (int which = 0; ok && which < 2; ++which) {
+            ok = wait_all(&S.y_full[2 * ss + which], ps, abort_flag, 128);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_lane()) {
+              const uint64_t x = kdesc(su32(xbuf + which * NB * ABOX));
+              const uint64_t y = kdesc(su32(ybuf + (2 * ss + which) * C::UNIT));
+              const uint32_t id = idesc(128, (ny + 15) & ~15, 0, 0);
+              const uint32_t to = tmem + ((g % BUF) * 2 + which) * YT;
+#pragma unroll 1
+              for (int c = 0; c < ksteps; ++c)
+                mma(to, x + (c >> 2) * (ABOX >> 4) + 2 * (c & 3),
+                    y + (c >> 2) * (C::YBOX >> 4) + 2 * (c & 3), id, c != 0);
+              if (which) {
+                mma_commit(&S.s_full[g & 1]);
+                if (!KV) mma_commit(&S.y_empty[2 * ss + 1]);  // V is done with
+                if (t == nt - 1) mma_commit(&S.x_empty);
+              }
+            }
+            __syncwarp();
+          }
+          if (!ok) break;
+          if (++ss == KP) ss = 0, ps ^= 1;
+          ++g;
+        }
+        const int tp = t - (BUF - 1);
+        if (tp >= 0) {
+          const int gp = BUF == 1 || t >= nt ? g - 1 : g - 2;
+          const int py = BUF == 1 ? ny : prev_ny;
+          uint8_t* y = ybuf + 2 * sv * C::UNIT;
+          zero_tail<NB>(y, C::YBOX, py, lane);
+          if (KV) zero_tail<NB>(y + C::UNIT, C::YBOX, py, lane);
+          // the first sums of an item: the item before has read its accumulators
+          if ((tp == 0 && !wait_all(&S.acc_free, (nload & 1) ^ 1, abort_flag, 129)) ||
+              !wait_all(&S.p_full[gp & 1], (gp >> 1) & 1, abort_flag, 130)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          if (elect_lane()) {
+            const uint32_t w = tmem + (gp % BUF) * 2 * YT;
+            const int steps = (py + 15) >> 4;
+#pragma unroll 1
+            for (int which = KV ? 0 : 1; which < 2; ++which) {  // P Y2 (dv), then dS Y1
+              const uint64_t b = mndesc(su32(y + (1 - which) * C::UNIT), C::YBOX);
+              const uint32_t to = tmem + C::ACC + (KV ? (1 - which) * 64 * NB : 0);
+#pragma unroll 1
+              for (int k = 0; k < steps; ++k)
+                mma_ts(to, w + which * YT + 8 * k, b + 128 * k, id_acc, k != 0 || tp > 0);
+            }
+            mma_commit(&S.done[gp & 1]);
+            mma_commit(&S.y_empty[2 * sv]);
+            if (KV) mma_commit(&S.y_empty[2 * sv + 1]);
+            if (tp == nt - 1) mma_commit(&S.acc_full);
+          }
+          __syncwarp();
+          if (++sv == KP) sv = 0;
+        }
+        prev_ny = ny;
+      }
+      if (nt > 0) ++nload;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.item_empty[n & 1]);
+    }
+    if (elect_lane()) {
+      mma_commit(&S.fin);
+      drain_one(&S.fin, 0);
+    }
+    __syncwarp();
+  } else {
+    // ---------------- p, ds and the gradients: thread = row of X
+    const int buf = warp >> 2;                // tiles g with g % BUF == buf
+    const int quad = warp & 3, tid = threadIdx.x & 127;
+    const uint32_t lane_off = (uint32_t)(32 * quad) << 16;
+    const int row = 32 * quad + lane;
+    const float c = p.scale * kLog2e;
+    const float2 c2 = make_float2(c, c);
+    int g = 0, nload = 0, flip = 0;
+    bool ok = true;
+#pragma unroll 1
+    for (int n = 0; ok; ++n) {
+      if (!wait_all(&S.item_full[n & 1], (n >> 1) & 1, abort_flag, 131)) break;
+      const BwdItem w = S.item[n & 1];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.item_empty[n & 1]);
+      if (w.nt < 0) break;
+      const bool in = row < w.nx;
+      const int64_t xr = w.x0 + w.r0 + row;   // the thread's row
+      const int xw = w.r0 + 32 * quad + (KV ? 0 : w.off);  // position of the warp's first row
+      float2 rl = make_float2(0.f, 0.f);      // - lse (in powers of two) and - delta of the row
+      float2 ds2 = make_float2(0.f, 0.f);     // sum of the row's ds
+      if (!KV && in) {
+        const float ls = p.lse_in[(int64_t)w.hx * p.Tq + xr];
+        rl.x = ls == -INFINITY ? 0.f : -ls * kLog2e;  // (sees no key)
+        if (w.nt > 0) rl.y = -row_delta(p, xr, w.hx);
+      }
+#pragma unroll 1
+      for (int t = 0; t < w.nt; ++t, ++g) {
+        if (BUF == 2 && (g & 1) != buf) continue;
+        int h, r, ny;
+        bwd_tile<KV, YT>(w, p, t, &h, &r, &ny);
+        const uint32_t sp = tmem + lane_off + (g % BUF) * 2 * YT;  // S, then dP
+        // In columns of the tile: the last that the warp's first row sees, the first
+        // that its last row sees, and (over keys) the end of the first tokens.
+        int wh, wl, sk = 0, up, low;  // up: no row sees a column past it; low: none before it
+        float cv = 0.f;
+        if (KV) {
+          const int ip = r + w.off;  // position of the tile's first query
+          const bool sunk = xw < w.sinks;
+          wl = p.right < 0 ? -kAttnMaxLen : xw + 31 - p.right - ip;
+          wh = p.left < 0 ? kAttnMaxLen : xw + p.left - ip;
+          low = wl - 31;
+          up = p.left < 0 || sunk ? kAttnMaxLen : wh + 31;
+          // this thread's share of the tile's lse and delta
+          const int e = tid < YT ? tid : tid - YT;
+          if (e < ny) {
+            const int64_t at = (int64_t)h * p.Tq + w.y0 + r + e;
+            if (tid < YT) {
+              cv = p.lse_in[at];
+              cv = cv == -INFINITY ? 0.f : -cv * kLog2e;
+            } else {
+              cv = -p.delta[at];
+            }
+          }
+        } else {
+          wh = p.right < 0 ? kAttnMaxLen : xw + p.right - r;
+          wl = p.left < 0 ? -kAttnMaxLen : xw + 31 - p.left - r;
+          sk = w.sinks - r;
+          up = wh + 31;
+          low = wl - 31;
+        }
+        const int end = 32 * quad < w.nx ? min(ny, up + 1) : 0;
+        if (!wait_all(&S.s_full[g & 1], (g >> 1) & 1, abort_flag, 132)) { ok = false; break; }
+        tc_fence_after();
+        const float* col = nullptr;
+        if (KV) {
+          // (two buffers in turn: a warp that is still at the last tile reads the other)
+          float* dst = &S.col[KV ? buf : 0][flip][0][0];
+          dst[tid] = cv;
+          col = dst;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&S.col_full[buf]);
+          if (!wait_all(&S.col_full[buf], flip, abort_flag, 134)) { ok = false; break; }
+          flip ^= 1;
+        }
+        // A row whose keys all lie in one tile corrects delta before it is used.
+#pragma unroll 1
+        for (bool last = KV || w.nt > 1;; last = true) {
+#pragma unroll 1
+          for (int q = 0; q < ny; q += 32) {
+            uint32_t p16[16], d16[16];
+            if (q >= end || (q + 31 < low && (KV || q >= sk))) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) p16[e] = d16[e] = 0u;
+            } else {
+              float v[32], d[32];
+              tmem_ld32_async(sp + q, v);
+              tmem_ld32_async(sp + YT + q, d);
+              tmem_wait_ld();
+              tmem_landed(v);
+              tmem_landed(d);
+              if (q + 32 > min(ny, wh + 1) || (q < wl && (KV || q + 32 > sk))) {
+                uint32_t see;
+                if (KV) {
+                  const bool sink = w.r0 + row < w.sinks;
+                  see = bit_span(wl - 31 + lane - q, sink ? ny - 1 - q : min(ny - 1, wh + lane) - q);
+                } else {
+                  see = bit_span(0, min(ny - 1, wh + lane) - q) &
+                        (bit_span(wl - 31 + lane - q, 31) | bit_span(0, sk - 1 - q));
+                }
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                  const bool vis = see & (1u << e);
+                  v[e] = vis ? v[e] : -INFINITY;
+                  d[e] = vis ? d[e] : 0.f;
+                }
+              }
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) {
+                float2 ml, md;
+                if (KV) {
+                  ml = *reinterpret_cast<const float2*>(col + q + e);
+                  md = *reinterpret_cast<const float2*>(col + YT + q + e);
+                } else {
+                  ml = make_float2(rl.x, rl.x);
+                  md = make_float2(rl.y, rl.y);
+                }
+                const float2 z = fma2(make_float2(v[e], v[e + 1]), c2, ml);
+                const float2 y = make_float2(ex2(z.x), ex2(z.y));
+                const float2 dd = add2(make_float2(d[e], d[e + 1]), md);
+                const float2 x = fma2(y, dd, make_float2(0.f, 0.f));
+                if (!KV) ds2 = add2(ds2, x);
+                if (KV) p16[e >> 1] = pack_bf16(y.x, y.y);
+                d16[e >> 1] = pack_bf16(x.x, x.y);
+              }
+            }
+            if (last) {  // over the pieces of S and dP that have been read
+              if (KV) tmem_st16(sp + (q >> 1), p16);
+              tmem_st16(sp + YT + (q >> 1), d16);
+            }
+          }
+          if (last) break;
+          rl.y -= ds2.x + ds2.y;
+          ds2 = make_float2(0.f, 0.f);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.p_full[g & 1]);
+      }
+      if (!ok) break;
+      // The gradients of the row.  One buffer: all of them; two: half of dq's
+      // channels each, or dk and dv.
+      constexpr int NACC = KV ? 2 : 1;
+      if (w.nt > 0) {
+        if (!wait_all(&S.acc_full, nload & 1, abort_flag, 133)) break;
+        tc_fence_after();
+        ++nload;
+      }
+      if (!KV) {
+        float delta = ds2.x + ds2.y - (buf == 0 ? rl.y : 0.f);
+        if (BUF == 2 && w.nt > 1) {  // the other buffer's tiles
+          // (written again only after the next sums, which wait for acc_free)
+          if (buf == 1) {
+            S.half[row] = delta;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&S.col_full[0]);
+          } else {
+            if (!wait_all(&S.col_full[0], flip, abort_flag, 135)) break;
+            flip ^= 1;
+            delta += S.half[row];
+          }
+        }
+        // of a single tile, the warps that had it know the sum
+        if (w.nt == 1 && BUF == 2 && buf == 1) delta -= rl.y;
+        if (in && buf == (w.nt == 1 ? (g - 1) % BUF : 0))
+          p.delta[(int64_t)w.hx * p.Tq + xr] = delta;
+      }
+      const int a0 = KV && BUF == 2 ? buf : 0, a1 = KV && BUF == 2 ? buf + 1 : NACC;
+      const int d0 = !KV && BUF == 2 ? 64 * buf : 0;
+      const int d1 = !KV && BUF == 2 ? min(p.dim, 64 * buf + 64) : p.dim;
+#pragma unroll 1
+      for (int a = a0; a < a1; ++a) {
+        const Heads& out = KV ? (a ? p.dv : p.dk) : p.dq;
+        const float mul = a ? 1.f : p.scale;
+        const bool wide = wide_rows(out);
+        __nv_bfloat16* dst = out.at<__nv_bfloat16>(xr, w.hx);
+        float* part = cut.parts + (((int64_t)w.slot * 2 + a) * AT + row) * p.dim;
+#pragma unroll 1
+        for (int d = d0; d < d1; d += 32) {
+          float o[32];
+          if (w.nt > 0) {
+            tmem_ld32_async(tmem + lane_off + C::ACC + a * 64 * NB + d, o);
+            tmem_wait_ld();
+            tmem_landed(o);
+          }
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = w.nt > 0 ? o[e] * mul : 0.f;
+          if (!in) continue;
+          if (KV && w.slot >= 0) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              if (d + e < p.dim)
+                *reinterpret_cast<float4*>(part + d + e) =
+                    make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          } else {
+            st_row32(dst + d, o, p.dim - d, wide);
+          }
+        }
+      }
+      if (w.nt > 0) {  // the accumulators have been read
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.acc_free);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == WARPS + 1) tmem_give(tmem, C::COLS);
+}
+
+// dk and dv of the key tiles that were worked on in pieces: the pieces' sums
+// in order.  A block takes 8 rows of a tile.
+__global__ void __launch_bounds__(256) attn_pieces_kernel(AttnArgs p, BwdCut cut) {
+  pdl_wait();
+  pdl_trigger();
+  const bool lead_only = cut.pieces <= 1;
+  const uint32_t first = cut.lead_pieces > 1 ? 0 : cut.lead;  // the first tile in pieces
+  const uint32_t tiles = (lead_only ? cut.lead : cut.tiles) - first;
+  const uint32_t block = blockIdx.x >> 4, rows8 = blockIdx.x & 15;
+  const uint32_t r = block / tiles;
+  const int tile = (int)(first + block - r * tiles);
+  const int b = (int)(r / p.kv), h = (int)(r - (uint32_t)b * p.kv);
+  Seq s;
+  if (!load_seq(p, b, &s, false)) return;
+  const int n = min(AT, s.lk - tile * AT);
+  const bool lead = tile < cut.lead;
+  const int pieces = lead ? cut.lead_pieces : cut.pieces;
+  const int64_t slot = lead ? ((int64_t)r * cut.lead + tile) * pieces
+                            : cut.lead_slots +
+                                  ((int64_t)r * (cut.tiles - cut.lead) + tile - cut.lead) * pieces;
+  const int quads = p.dim / 4;
+  for (int e = threadIdx.x; e < 2 * 8 * quads; e += 256) {
+    const int a = e / (8 * quads), f = e - a * 8 * quads;
+    const int row = rows8 * 8 + f / quads, d = 4 * (f % quads);
+    if (row >= n) continue;
+    const float* src = cut.parts + ((slot * 2 + a) * AT + row) * p.dim + d;
+    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = 0; i < pieces; ++i) {
+      const float4 x = *reinterpret_cast<const float4*>(src + (int64_t)i * 2 * AT * p.dim);
+      t.x += x.x, t.y += x.y, t.z += x.z, t.w += x.w;
+    }
+    __nv_bfloat16* dst = (a ? p.dv : p.dk).at<__nv_bfloat16>(s.k0 + tile * AT + row, h) + d;
+    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(t.x, t.y), pack_bf16(t.z, t.w));
+  }
+}
+
+// ---- launch ---------------------------------------------------------------------
+// (without the tensors' layouts: the workspace holds the partial sums in either case)
+bool tc_bwd_shape(const AttnPlan& P) {
+  return P.act == TT_DT_BF16 && P.dim % 8 == 0 && P.dim <= 128 && P.scale > 0.f;
+}
+bool tc_bwd_takes(const AttnArgs& p) {
+  return p.dim % 8 == 0 && p.dim <= 128 && p.scale > 0.f && tc_heads(p.q, p.Tq, p.heads) &&
+         tc_heads(p.k, p.Tk, p.kv) && tc_heads(p.v, p.Tk, p.kv) && tc_heads(p.o, p.Tq, p.heads) &&
+         tc_heads(p.dout, p.Tq, p.heads) && tc_heads(p.dq, p.Tq, p.heads) &&
+         tc_heads(p.dk, p.Tk, p.kv) && tc_heads(p.dv, p.Tk, p.kv);
+}
+
+// How the pass over keys is cut (see the top of the file); *slots: partial slots.
+BwdCut bwd_cut(const AttnPlan& P, const tt_attn_seqs* s, int64_t* slots) {
+  constexpr int YT = 64;
+  BwdCut c = {};
+  const int group = P.heads / P.kv;
+  c.tiles = (s->max_k + AT - 1) / AT;
+  if (P.left >= 0 && P.sinks > 0) {
+    c.lead = (P.sinks + AT - 1) / AT;
+    if (c.lead > c.tiles) c.lead = c.tiles;
+  }
+  const int64_t all = (int64_t)group * ((s->max_q + YT - 1) / YT);  // a lead tile's list at most
+  int64_t list = all;                                               // another tile's
+  if (P.left >= 0 && P.right >= 0) {
+    const int64_t span = (int64_t)AT + P.left + P.right;
+    const int64_t l = group * ((span + YT - 1) / YT + 1);
+    if (l < list) list = l;
+  }
+  // a lead tile: pieces of about another tile's length; every tile: enough
+  // pieces to reach the SMs' CTAs once
+  const int64_t ctas = (int64_t)device_sms() * (P.dim <= 64 ? 2 : 1);
+  const int64_t items = (int64_t)c.tiles * P.kv * s->B;
+  int64_t cut = items > 0 && items < ctas ? ctas / items : 1;
+  if (cut > list / 4) cut = list / 4;  // no piece under four tiles
+  if (cut < 1) cut = 1;
+  c.pieces = (int)cut;
+  const int64_t len = (list + cut - 1) / cut;
+  int64_t lead = len > 0 ? (all + len - 1) / len : 1;
+  if (2 * all < 3 * len) lead = 1;
+  c.lead_pieces = (int)(lead < 1 ? 1 : lead);
+  c.lead_slots = c.lead_pieces > 1 ? (int64_t)s->B * P.kv * c.lead * c.lead_pieces : 0;
+  *slots = c.lead_slots +
+           (c.pieces > 1 ? (int64_t)s->B * P.kv * (c.tiles - c.lead) * c.pieces : 0);
+  return c;
+}
+size_t bwd_parts_bytes(const AttnPlan& P, const tt_attn_seqs* s) {
+  if (!tc_bwd_shape(P)) return 0;
+  int64_t slots = 0;
+  bwd_cut(P, s, &slots);
+  return (size_t)slots * 2 * AT * P.dim * sizeof(float);
+}
+
+template <bool KV, int NB>
+cudaError_t tc_bwd_go(const AttnArgs& p, const BwdCut& cut, cudaStream_t st) {
+  using C = TcBwd<KV, NB>;
+  static_assert(C::CTAS * (C::kSmem + 1024) <= 228 * 1024, "CTAs an SM");
+  static PerDevice once;
+  cudaError_t e = once.get([] {
+    return cudaFuncSetAttribute(attn_bwd_tc<KV, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)C::kSmem);
+  });
+  if (e != cudaSuccess) return e;
+  CUtensorMap mq, mk, mv, md;
+  if (!make_heads_map(&mq, p.q, p.Tq, p.heads, p.dim) ||
+      !make_heads_map(&mk, p.k, p.Tk, p.kv, p.dim) ||
+      !make_heads_map(&mv, p.v, p.Tk, p.kv, p.dim) ||
+      !make_heads_map(&md, p.dout, p.Tq, p.heads, p.dim))
+    return cudaErrorInvalidValue;
+  const int64_t items =
+      KV ? (int64_t)p.B * p.kv *
+               ((int64_t)cut.lead * cut.lead_pieces + (int64_t)(cut.tiles - cut.lead) * cut.pieces)
+         : (int64_t)((p.max_q + AT - 1) / AT) * p.heads * p.B;
+  if (items == 0) return cudaSuccess;
+  if (items > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+  count_launches(1);
+  return launch_ex(attn_bwd_tc<KV, NB>, dim3((unsigned)items), dim3(C::THREADS), C::kSmem, st,
+                   false, KV ? mk : mq, KV ? mv : md, KV ? mq : mk, KV ? md : mv, p, cut);
+}
+
+cudaError_t tc_bwd(const AttnPlan& P, const tt_attn_seqs* s, const AttnArgs& p, float* parts,
+                   cudaStream_t st) {
+  int64_t slots = 0;
+  BwdCut cut = bwd_cut(P, s, &slots);
+  cut.parts = parts;
+  cudaError_t e = p.dim <= 64 ? tc_bwd_go<false, 1>(p, cut, st) : tc_bwd_go<false, 2>(p, cut, st);
+  if (e == cudaSuccess)
+    e = p.dim <= 64 ? tc_bwd_go<true, 1>(p, cut, st) : tc_bwd_go<true, 2>(p, cut, st);
+  if (e == cudaSuccess && slots > 0) {
+    const int first = cut.lead_pieces > 1 ? 0 : cut.lead;
+    const int tiles = (cut.pieces > 1 ? cut.tiles : cut.lead) - first;
+    const int64_t blocks = (int64_t)p.B * p.kv * tiles * 16;
+    if (blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+    if (blocks > 0) {
+      count_launches(1);
+      e = launch_ex(attn_pieces_kernel, dim3((unsigned)blocks), dim3(256), 0, st, false, p, cut);
+    }
+  }
+  return e;
+}
+
+}  // namespace
+}  // namespace ttc
