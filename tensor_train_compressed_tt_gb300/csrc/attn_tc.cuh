@@ -10,7 +10,6 @@ namespace {
 
 constexpr int AT = 128;                  // rows of an accumulator tile
 constexpr int ABOX = AT * 128;           // bytes of [128 rows][64 bf16]
-constexpr int ALOAD = 32;                // rows a TMA box brings
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -23,21 +22,56 @@ __device__ __forceinline__ void tma_load3(void* dst, const CUtensorMap* map, uin
       : "memory");
 }
 
-// n rows of head h from `row` on into NB boxes of 64 channels, `box` bytes
-// apart, in 32-row pieces.  Rows past n up to the piece's end, and channels
-// past the head's width (zeros), come along.
+// The rows of one box of the map from `row` on, head h, into NB boxes of 64
+// channels, `box` bytes apart.  Rows past the sequence, and channels past the
+// head's width (zeros), come along.
 template <int NB>
-__device__ __noinline__ void load_tile(uint8_t* dst, int box, const CUtensorMap* map,
-                                       uint64_t* bar, int h, int row, int n, int tiles = 1) {
-  // (bytes of all the tiles that come on this phase of the barrier; 0: told before)
-  const int pieces = (n + ALOAD - 1) / ALOAD;
-  if (tiles) mbar_expect_tx(bar, (uint32_t)(tiles * pieces * NB * ALOAD * 128));
+__device__ __forceinline__ void load_tile(uint8_t* dst, int box, const CUtensorMap* map,
+                                          uint64_t* bar, int h, int row) {
+#pragma unroll
+  for (int b = 0; b < NB; ++b) tma_load3(dst + b * box, map, bar, 64 * b, h, row);
+}
+// n rows on their way from memory to L2 (`box` rows at a time): what the next
+// piece of work reads first.
+template <int NB>
+__device__ __noinline__ void prefetch_rows(const CUtensorMap* map, int box, int h, int row,
+                                           int n) {
 #pragma unroll 1
-  for (int r = 0; r < pieces; ++r)
+  for (int r = 0; r < n; r += box)
 #pragma unroll
     for (int b = 0; b < NB; ++b)
-      tma_load3(dst + b * box + r * ALOAD * 128, map, bar, 64 * b, h, row + ALOAD * r);
+      asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
+                       reinterpret_cast<uint64_t>(map)),
+                   "r"(64 * b), "r"(h), "r"(row + r)
+                   : "memory");
 }
+
+// The list of tiles that a piece of work passes over: rows [r, lim) of head h
+// in steps of a tile, then [r2, lim2) of head h + dh, and so on.
+struct TileList {
+  int h, r, lim, r2, lim2, dh;
+  __device__ __forceinline__ int rows(int step) const { return min(step, lim - r); }
+  __device__ __forceinline__ void next(int step) {
+    r += step;
+    if (r >= lim) {
+      r = r2;
+      lim = lim2;
+      h += dh;
+    }
+  }
+};
+// The keys that a tile of queries sees: the first tokens, then the window.
+__device__ __forceinline__ TileList key_list(const KeySpan& ks, int h) {
+  TileList l;
+  l.h = h;
+  l.r = ks.a1 > 0 ? 0 : ks.b0;
+  l.lim = ks.a1 > 0 ? ks.a1 : ks.b1;
+  l.r2 = ks.b0;
+  l.lim2 = ks.b1;
+  l.dh = 0;
+  return l;
+}
+
 // The wait for a load of one's own on the way out.
 __device__ __noinline__ void drain_one(uint64_t* b, uint32_t parity) { drain_bar(b, parity); }
 
@@ -78,6 +112,32 @@ __device__ __forceinline__ void mma_ts(uint32_t dtmem, uint32_t atmem, uint64_t 
       "r"(atmem), "l"(b), "r"(id), "r"(acc));
 }
 
+// The products of one tile, by one thread.  dot: over the channels, both
+// operands K-major tiles of 64-channel boxes (abox, bbox bytes apart).  sum_ts:
+// over rows of b (MN-major), the weights in tensor memory.  In fours where they
+// come in fours: with known offsets the products follow one another closer.
+__device__ __forceinline__ void dot_tile(uint32_t to, uint64_t a, int abox, uint64_t b, int bbox,
+                                         uint32_t id, int ksteps) {
+#pragma unroll 1
+  for (int c = 0; c < ksteps; c += 4) {
+    const uint64_t x = a + (c >> 2) * (abox >> 4), y = b + (c >> 2) * (bbox >> 4);
+    if (c + 4 <= ksteps) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) mma(to, x + 2 * e, y + 2 * e, id, c + e != 0);
+    } else {
+#pragma unroll 1
+      for (int e = 0; c + e < ksteps; ++e) mma(to, x + 2 * e, y + 2 * e, id, c + e != 0);
+    }
+  }
+}
+__device__ __forceinline__ void sum_ts(uint32_t to, uint32_t w, uint64_t b, uint32_t id, int steps,
+                                       bool add) {
+#pragma unroll 1
+  for (int k = 0; k < steps; k += 2) {
+    mma_ts(to, w + 8 * k, b + 128 * k, id, k != 0 || add);
+    if (k + 1 < steps) mma_ts(to, w + 8 * k + 8, b + 128 * k + 128, id, 1);
+  }
+}
 // 32 columns of this thread's lane, not yet readable: tmem_landed orders the
 // uses after the wait.
 __device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, float (&v)[32]) {
@@ -166,6 +226,7 @@ __device__ __forceinline__ float2 fma2(float2 x, float2 m, float2 a) {
   return __ffma2_rn(x, m, a);
 }
 __device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
 
 // 32 values as bf16 to global memory, `n` (a multiple of 8) of them.  wide: the
 // address is 32-byte aligned and whole sectors can be written at once.
@@ -248,16 +309,16 @@ __device__ __forceinline__ uint32_t bit_span(int lo, int hi) {
   return a & b;
 }
 
-// (T, heads, dim) tensor as TMA sees it: boxes of 64 channels x 1 head x 64
+// (T, heads, dim) tensor as TMA sees it: boxes of 64 channels x 1 head x `rows`
 // rows, 128-byte swizzle, zeros outside.
-bool make_heads_map(CUtensorMap* m, const Heads& x, int64_t T, int heads, int dim) {
+bool make_heads_map(CUtensorMap* m, const Heads& x, int64_t T, int heads, int dim, int rows) {
   auto fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[3] = {(cuuint64_t)dim, (cuuint64_t)heads, (cuuint64_t)T};
   // the stride of an axis of one is not used; any legal value does
   const int64_t row = T > 1 ? x.row : 64, head = heads > 1 ? x.head : 64;
   cuuint64_t strides[2] = {(cuuint64_t)head * 2, (cuuint64_t)row * 2};
-  cuuint32_t box[3] = {64, 1, ALOAD};
+  cuuint32_t box[3] = {64, 1, (cuuint32_t)rows};
   cuuint32_t estr[3] = {1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, x.p, dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,

@@ -14,14 +14,20 @@
 // Both passes have the same shape.  X1, X2 are the 128 rows that a CTA works
 // on (Q and dO, or K and V), Y1, Y2 tiles of YT of the others' rows (K and V,
 // or Q and dO):  S = X1 Y1^T and dP = X2 Y2^T into tensor memory, the softmax
-// warps (thread = row) put p and ds over them as bf16, and the accumulators
+// warps (thread = row) turn them into p and ds as bf16, and the accumulators
 // take  acc0 += dS Y1  (dq, or dk) and, in the pass over keys, acc1 += P Y2 (dv).
+// Over queries ds has columns of its own, so S and dP of the next tile are
+// computed as soon as this tile's have been read; over keys the accumulators
+// take those columns, and p and ds lie over S and dP.  (p and ds in shared
+// memory instead were no faster: the warps that write them are what bounds the
+// pass, and shared memory, with lse and delta read for every column, is what
+// they wait for.)
 //
 // delta comes from the stored o, whose rounding shows in rows of few keys:
 // sum_j ds_j, which should vanish, is then delta's error (the p_j add up to 1).
 // The first pass adds that sum to the delta that it leaves for the second.
 //
-// Roles as in the forward.  Heads of up to 64 channels run two CTAs an SM with
+// Roles as in the forward (one warp issues S and dP, another the sums).  Heads of up to 64 channels run two CTAs an SM with
 // one buffer of S and dP each; wider ones fill the tensor memory with two
 // buffers in one CTA, each with its own four softmax warps.
 //
@@ -49,61 +55,41 @@ struct BwdItem {
   int64_t x0, y0;      // first rows of the sequence in X and in Y
   int hx, r0, nx;      // head of X, first row and rows of the tile
   int off, sinks;      // position of query row 0; first tokens
-  int nt;              // tiles of Y; < 0: no more work
-  // over keys: the two spans, tiles of the first
-  KeySpan ks;
-  int n1;
-  // over queries: rows [t0, t1), tiles of one head, first entry of the list
-  int t0, t1, per, u0;
+  TileList list;       // tiles of Y
+  int nt;              // their number; < 0: no more work
   int slot;            // partial sums go here (-1: the gradients themselves)
 };
 
 template <bool KV, int NB>
 struct TcBwd {
   static constexpr int BUF = NB;                          // buffers of S and dP
-  static constexpr int YT = !KV && NB == 1 ? 96 : 64;     // rows of a Y tile
-  static constexpr int KP = NB == 1 ? (KV ? 4 : 3) : 4;   // pairs of Y tiles in flight
+  static constexpr int YT = 64;                           // rows of a Y tile
+  static constexpr int NX = KV ? 2 : 3;                   // X tiles: over queries o, too
+  static constexpr int KP = KV ? 4 : 3;                   // pairs of Y tiles in flight
+  static constexpr int ITEMS = 4;                         // items told to the roles
   static constexpr int CTAS = NB == 1 ? 2 : 1;            // CTAs an SM
   static constexpr int YBOX = YT * 128, UNIT = NB * YBOX;
-  static constexpr uint32_t ACC = BUF * 2 * YT, COLS = NB == 1 ? 256 : 512;
+  static constexpr uint32_t DS = BUF * 2 * YT, ACC = DS + (KV ? 0 : BUF * YT / 2),
+                            COLS = NB == 1 ? 256 : 512;
   static constexpr int WARPS = 4 * BUF;                   // softmax warps
-  static constexpr int THREADS = 32 * (WARPS + 2);
+  static constexpr int THREADS = 32 * (WARPS + 3);
   struct Shared {
-    uint64_t x_full, x_empty, y_full[2 * KP], y_empty[2 * KP];
-    uint64_t s_full[2], p_full[2], done[2], acc_full, acc_free, fin;  // [tile & 1]
-    uint64_t item_full[2], item_empty[2], clc;
+    uint64_t x_full, x_empty, y_full[KP], y_empty[KP];
+    uint64_t s_full[2], s_free[2], p_full[2], done[2], acc_full, acc_free, fin, fin2;  // [tile & 1]
+    uint64_t item_full[ITEMS], item_empty[ITEMS], clc;
+    uint64_t o_full, o_empty;
     uint64_t col_full[2];  // [buffer]
-    BwdItem item[2];
+    BwdItem item[ITEMS];
     uint4 answer;
+    int rows[KP];  // rows of the pair's tile
     float col[KV ? BUF : 1][2][2][KV ? YT : 4];  // lse and delta of a tile's queries
     float half[KV ? 1 : AT];  // the second buffer's sums of ds
     uint32_t tmem;
     int abort_flag, never;
   };
-  static constexpr size_t kSmem = 2 * NB * ABOX + 2 * KP * UNIT + sizeof(Shared) + 1024;
+  static constexpr size_t kSmem = NX * NB * ABOX + 2 * KP * UNIT + sizeof(Shared) + 1024;
   static_assert(ACC + (KV ? 2 : 1) * 64 * NB <= COLS, "tensor memory");
 };
-
-// Tile u of an item's list: head, first row, rows.
-template <bool KV, int YT>
-__device__ __forceinline__ void bwd_tile(const BwdItem& w, const AttnArgs& p, int u, int* h,
-                                         int* r, int* n) {
-  if (KV) {
-    const int v = w.u0 + u, g = v / w.per;
-    *h = w.hx * p.group + g;
-    *r = w.t0 + YT * (v - g * w.per);
-    *n = min(YT, w.t1 - *r);
-  } else {
-    *h = w.hx / p.group;
-    if (u < w.n1) {
-      *r = YT * u;
-      *n = min(YT, w.ks.a1 - *r);
-    } else {
-      *r = w.ks.b0 + YT * (u - w.n1);
-      *n = min(YT, w.ks.b1 - *r);
-    }
-  }
-}
 
 // CTA number -> item.  False: nothing to do.
 template <bool KV, int YT>
@@ -139,13 +125,16 @@ __device__ __forceinline__ bool bwd_item(const AttnArgs& p, const BwdCut& cut, u
     w->y0 = s.q0;
     w->nx = min(AT, s.lk - w->r0);
     const RowSpan rs = row_span(p, s, w->r0, w->r0 + w->nx - 1);
-    w->t0 = rs.t0;
-    w->t1 = rs.t1;
-    w->per = (rs.t1 - rs.t0 + YT - 1) / YT;
-    const int list = w->per * p.group;
-    w->u0 = (int)((int64_t)list * piece / pieces);
-    w->nt = (int)((int64_t)list * (piece + 1) / pieces) - w->u0;
-    if (w->per == 0) w->per = 1;
+    // the tiles of every head that shares the keys, one head after another
+    const int ntq = (rs.t1 - rs.t0 + YT - 1) / YT, all = ntq * p.group;
+    const int u0 = (int)((int64_t)all * piece / pieces);
+    w->nt = (int)((int64_t)all * (piece + 1) / pieces) - u0;
+    const int g0 = ntq ? u0 / ntq : 0;
+    w->list.h = w->hx * p.group + g0;
+    w->list.r = rs.t0 + YT * (u0 - g0 * ntq);
+    w->list.lim = w->list.lim2 = rs.t1;
+    w->list.r2 = rs.t0;
+    w->list.dh = 1;
   } else {
     const uint32_t ntiles = (p.max_q + AT - 1) / AT;
     const uint32_t r = cta / ntiles;
@@ -159,62 +148,69 @@ __device__ __forceinline__ bool bwd_item(const AttnArgs& p, const BwdCut& cut, u
     w->y0 = s.k0;
     w->nx = min(AT, s.lq - w->r0);
     const int i0 = w->r0 + s.off();
-    w->ks = key_span(p, s.lk, i0, i0 + w->nx - 1);
-    w->n1 = (w->ks.a1 + YT - 1) / YT;
-    w->nt = w->n1 + (w->ks.b1 - w->ks.b0 + YT - 1) / YT;
+    const KeySpan ks = key_span(p, s.lk, i0, i0 + w->nx - 1);
+    w->list = key_list(ks, w->hx / p.group);
+    w->nt = (ks.a1 + YT - 1) / YT + (ks.b1 - ks.b0 + YT - 1) / YT;
   }
   w->off = s.off();
   return true;
 }
 
-// sum over the channels of o do, of one row
-__device__ __noinline__ float row_delta(const AttnArgs& p, int64_t r, int h) {
-  const uint4* o = reinterpret_cast<const uint4*>(p.o.at<const __nv_bfloat16>(r, h));
-  const uint4* d = reinterpret_cast<const uint4*>(p.dout.at<const __nv_bfloat16>(r, h));
-  float s = 0.f;
-#pragma unroll 2
-  for (int e = 0; e < p.dim / 8; ++e) {
-    const uint4 a = o[e], b = d[e];
+// sum over the channels of o do, of a row of two swizzled tiles
+template <int NB>
+__device__ __forceinline__ float row_delta(const uint8_t* o, const uint8_t* d, int row, int dim) {
+  float s[2] = {0.f, 0.f};
+#pragma unroll 1
+  for (int e = 0; 8 * e < dim; ++e) {
+    const int at = (e >> 3) * ABOX + row * 128 + (((e & 7) ^ (row & 7)) << 4);
+    const uint4 a = *reinterpret_cast<const uint4*>(o + at);
+    const uint4 b = *reinterpret_cast<const uint4*>(d + at);
     const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      s = fmaf(__uint_as_float(x[i] << 16), __uint_as_float(y[i] << 16), s);
-      s = fmaf(__uint_as_float(x[i] & 0xFFFF0000u), __uint_as_float(y[i] & 0xFFFF0000u), s);
+      s[0] = fmaf(__uint_as_float(x[i] << 16), __uint_as_float(y[i] << 16), s[0]);
+      s[1] = fmaf(__uint_as_float(x[i] & 0xFFFF0000u), __uint_as_float(y[i] & 0xFFFF0000u), s[1]);
     }
   }
-  return s;
+  return s[0] + s[1];
 }
 
 template <bool KV, int NB>
 __global__ void __launch_bounds__(TcBwd<KV, NB>::THREADS, TcBwd<KV, NB>::CTAS)
     attn_bwd_tc(const __grid_constant__ CUtensorMap tm_x1, const __grid_constant__ CUtensorMap tm_x2,
                 const __grid_constant__ CUtensorMap tm_y1, const __grid_constant__ CUtensorMap tm_y2,
+                const __grid_constant__ CUtensorMap tm_o,
                 const __grid_constant__ AttnArgs p, const __grid_constant__ BwdCut cut) {
   using C = TcBwd<KV, NB>;
   constexpr int YT = C::YT, KP = C::KP, BUF = C::BUF, WARPS = C::WARPS;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* xbuf = align1k(smem_raw);      // X1, then X2
-  uint8_t* ybuf = xbuf + 2 * NB * ABOX;   // Y1 and Y2 of pair s: units 2 s and 2 s + 1
+  uint8_t* xbuf = align1k(smem_raw);      // X1, X2 and, over queries, o
+  uint8_t* ybuf = xbuf + C::NX * NB * ABOX;  // Y1 and Y2 of pair s: units 2 s and 2 s + 1
   auto& S = *reinterpret_cast<typename C::Shared*>(ybuf + 2 * KP * C::UNIT);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     mbar_init(&S.x_full, 1);
     mbar_init(&S.x_empty, 1);
 #pragma unroll 1
-    for (int i = 0; i < 2 * KP; ++i) mbar_init(&S.y_full[i], 1), mbar_init(&S.y_empty[i], 1);
+    for (int i = 0; i < KP; ++i) mbar_init(&S.y_full[i], 1), mbar_init(&S.y_empty[i], 1);
 #pragma unroll 1
     for (int i = 0; i < 2; ++i) {
       mbar_init(&S.s_full[i], 1);
+      mbar_init(&S.s_free[i], 4);
       mbar_init(&S.p_full[i], 4);
       mbar_init(&S.done[i], 1);
       mbar_init(&S.col_full[i], 4);
-      mbar_init(&S.item_full[i], 1);
-      mbar_init(&S.item_empty[i], WARPS + 1);
     }
+#pragma unroll 1
+    for (int i = 0; i < C::ITEMS; ++i)
+      mbar_init(&S.item_full[i], 1), mbar_init(&S.item_empty[i], WARPS + 2);
+    mbar_init(&S.o_full, 1);
+    mbar_init(&S.o_empty, WARPS);
     mbar_init(&S.acc_full, 1);
     mbar_init(&S.acc_free, WARPS);
     mbar_init(&S.clc, 1);
     mbar_init(&S.fin, 1);
+    mbar_init(&S.fin2, 1);
     S.abort_flag = S.never = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -232,150 +228,187 @@ __global__ void __launch_bounds__(TcBwd<KV, NB>::THREADS, TcBwd<KV, NB>::CTAS)
     if (lane == 0) {
       int n = 0, nload = 0, s = 0, loads = 0;
       uint32_t ph = 1, clc = 0;  // parity of the ring's empty barriers; of the next answer
-      bool ok = true;
+      bool ok = true, first = true;
       int cta = (int)blockIdx.x;
+      BwdItem cur, w;
+      cur.nt = -1;
 #pragma unroll 1
-      while (cta >= 0) {
-        clc_ask(&S.answer, &S.clc);  // the one after this
-        BwdItem w;
-        if (ok && bwd_item<KV, YT>(p, cut, (uint32_t)cta, &w)) {
-          ok = wait_one(&S.item_empty[n & 1], ((n >> 1) & 1) ^ 1, abort_flag, 120);
-          if (ok) {
-            S.item[n & 1] = w;
-            mbar_arrive(&S.item_full[n & 1]);
-            ++n;
+      while (true) {
+        // The next item: told to the roles, its first rows sent for from memory, before
+        // the loads of the current one, so that its own loads find them in L2.
+        w.nt = -1;
+#pragma unroll 1
+        while (cta >= 0) {
+          if (!first) {
+            // After an abort the CTAs that have not started are still taken over, and do
+            // nothing.
+            cta = wait_one(&S.clc, clc, &S.never, 123) ? clc_take(&S.answer) : -1;
+            clc ^= 1;
+            if (cta < 0) break;
           }
-          if (ok && w.nt > 0) {
-            ok = wait_one(&S.x_empty, (nload & 1) ^ 1, abort_flag, 121);
-            if (ok) {
-              load_tile<NB>(xbuf, ABOX, &tm_x1, &S.x_full, w.hx, (int)w.x0 + w.r0, w.nx, 2);
-              load_tile<NB>(xbuf + NB * ABOX, ABOX, &tm_x2, &S.x_full, w.hx, (int)w.x0 + w.r0,
-                            w.nx, 0);
-              ++nload;
+          first = false;
+          clc_ask(&S.answer, &S.clc);
+          if (!ok || !bwd_item<KV, YT>(p, cut, (uint32_t)cta, &w)) {
+            w.nt = -1;
+            continue;
+          }
+          const int slot = n % C::ITEMS;
+          ok = wait_one(&S.item_empty[slot], ((n / C::ITEMS) & 1) ^ 1, abort_flag, 120);
+          if (!ok) {
+            w.nt = -1;
+            continue;
+          }
+          S.item[slot] = w;
+          mbar_arrive(&S.item_full[slot]);
+          ++n;
+          if (w.nt > 0) {
+            prefetch_rows<NB>(&tm_x1, AT, w.hx, (int)w.x0 + w.r0, w.nx);
+            prefetch_rows<NB>(&tm_x2, AT, w.hx, (int)w.x0 + w.r0, w.nx);
+            if (!KV) prefetch_rows<NB>(&tm_o, AT, w.hx, (int)w.x0 + w.r0, w.nx);
+            // (over queries the window: the first tokens are in L2)
+            const int r = KV ? w.list.r : w.list.r2, rows = min(w.list.lim2 - r, 4 * YT);
+            prefetch_rows<NB>(&tm_y1, YT, w.list.h, (int)w.y0 + r, rows);
+            prefetch_rows<NB>(&tm_y2, YT, w.list.h, (int)w.y0 + r, rows);
+          }
+          break;
+        }
+        if (ok && cur.nt > 0) {
+          ok = wait_one(&S.x_empty, (nload & 1) ^ 1, abort_flag, 121) &&
+               (KV || wait_one(&S.o_empty, (nload & 1) ^ 1, abort_flag, 119));
+          if (ok) {
+            const int row = (int)cur.x0 + cur.r0;
+            mbar_expect_tx(&S.x_full, 2 * NB * ABOX);
+            load_tile<NB>(xbuf, ABOX, &tm_x1, &S.x_full, cur.hx, row);
+            load_tile<NB>(xbuf + NB * ABOX, ABOX, &tm_x2, &S.x_full, cur.hx, row);
+            if (!KV) {
+              mbar_expect_tx(&S.o_full, NB * ABOX);
+              load_tile<NB>(xbuf + 2 * NB * ABOX, ABOX, &tm_o, &S.o_full, cur.hx, row);
             }
+            ++nload;
+          }
+          TileList l = cur.list;
 #pragma unroll 1
-            for (int u = 0; ok && u < 2 * w.nt; ++u) {  // Y1, Y2 of tile 0, of tile 1, ...
-              int h, r, ny;
-              bwd_tile<KV, YT>(w, p, u >> 1, &h, &r, &ny);
-              ok = wait_one(&S.y_empty[s], ph, abort_flag, 122);
-              if (!ok) break;
-              load_tile<NB>(ybuf + s * C::UNIT, C::YBOX, u & 1 ? &tm_y2 : &tm_y1, &S.y_full[s], h,
-                            (int)w.y0 + r, ny);
-              ++loads;
-              if (++s == 2 * KP) s = 0, ph ^= 1;
-            }
+          for (int t = 0; ok && t < cur.nt; ++t) {
+            ok = wait_one(&S.y_empty[s], ph, abort_flag, 122);
+            if (!ok) break;
+            S.rows[s] = l.rows(YT);
+            mbar_expect_tx(&S.y_full[s], 2 * C::UNIT);
+            uint8_t* dst = ybuf + 2 * s * C::UNIT;
+            load_tile<NB>(dst, C::YBOX, &tm_y1, &S.y_full[s], l.h, (int)cur.y0 + l.r);
+            load_tile<NB>(dst + C::UNIT, C::YBOX, &tm_y2, &S.y_full[s], l.h, (int)cur.y0 + l.r);
+            l.next(YT);
+            ++loads;
+            if (++s == KP) s = 0, ph ^= 1;
           }
         }
-        // After an abort the CTAs that have not started are still taken over, and do nothing.
-        cta = wait_one(&S.clc, clc, &S.never, 123) ? clc_take(&S.answer) : -1;
-        clc ^= 1;
+        if (w.nt < 0) break;
+        cur = w;
       }
-      if (ok && wait_one(&S.item_empty[n & 1], ((n >> 1) & 1) ^ 1, abort_flag, 124)) {
-        S.item[n & 1].nt = -1;
-        mbar_arrive(&S.item_full[n & 1]);
+      if (ok && wait_one(&S.item_empty[n % C::ITEMS], ((n / C::ITEMS) & 1) ^ 1, abort_flag, 124)) {
+        S.item[n % C::ITEMS].nt = -1;
+        mbar_arrive(&S.item_full[n % C::ITEMS]);
       }
       // nothing is in flight into shared memory when the CTA leaves
       if (nload > 0) drain_one(&S.x_full, (uint32_t)((nload - 1) & 1));
+      if (!KV && nload > 0) drain_one(&S.o_full, (uint32_t)((nload - 1) & 1));
 #pragma unroll 1
-      for (int i = 0; i < 2 * KP && i < loads; ++i) {
-        if (--s < 0) s = 2 * KP - 1, ph ^= 1;
-        drain_one(&S.y_full[s], ph ^ 1);  // the last load into unit s
+      for (int i = 0; i < KP && i < loads; ++i) {
+        if (--s < 0) s = KP - 1, ph ^= 1;
+        drain_one(&S.y_full[s], ph ^ 1);  // the last load into pair s
       }
     }
   } else if (warp == WARPS + 1) {
-    // ---------------- products: S and dP of tile t, then the sums of tile t - (BUF - 1)
+    // ---------------- S and dP of every tile
     const int ksteps = (p.dim + 15) >> 4;
-    const uint32_t id_acc = idesc(128, ksteps * 16, 0, 1);
-    int g = 0, nload = 0, ss = 0, sv = 0;  // tiles so far; pair of the next S, of the next sums
-    uint32_t ps = 0;                       // parity of the former
+    const uint64_t x = kdesc(su32(xbuf));
+    int g = 0, nload = 0, s = 0;
+    uint32_t ph = 0;
     bool ok = true;
 #pragma unroll 1
     for (int n = 0; ok; ++n) {
-      if (!wait_all(&S.item_full[n & 1], (n >> 1) & 1, abort_flag, 125)) break;
-      const int nt = S.item[n & 1].nt;
-      if (nt < 0) break;
-      int prev_ny = 0;
-#pragma unroll 1
-      for (int t = 0; ok && nt > 0 && t < nt + BUF - 1; ++t) {
-        int ny = 0;
-        if (t < nt) {
-          int h, r;
-          bwd_tile<KV, YT>(S.item[n & 1], p, t, &h, &r, &ny);
-          // S and dP of tile g go where the weights of tile g - BUF were
-          if ((t == 0 && !wait_all(&S.x_full, nload & 1, abort_flag, 126)) ||
-              (g >= BUF && !wait_all(&S.done[(g - BUF) & 1], ((g - BUF) >> 1) & 1, abort_flag,
-                                     127))) {
-            ok = false;
-            break;
-          }
-#pragma unroll 1
-          for (int which = 0; ok && which < 2; ++which) {
-            ok = wait_all(&S.y_full[2 * ss + which], ps, abort_flag, 128);
-            if (!ok) break;
-            tc_fence_after();
-            if (elect_lane()) {
-              const uint64_t x = kdesc(su32(xbuf + which * NB * ABOX));
-              const uint64_t y = kdesc(su32(ybuf + (2 * ss + which) * C::UNIT));
-              const uint32_t id = idesc(128, (ny + 15) & ~15, 0, 0);
-              const uint32_t to = tmem + ((g % BUF) * 2 + which) * YT;
-#pragma unroll 1
-              for (int c = 0; c < ksteps; ++c)
-                mma(to, x + (c >> 2) * (ABOX >> 4) + 2 * (c & 3),
-                    y + (c >> 2) * (C::YBOX >> 4) + 2 * (c & 3), id, c != 0);
-              if (which) {
-                mma_commit(&S.s_full[g & 1]);
-                if (!KV) mma_commit(&S.y_empty[2 * ss + 1]);  // V is done with
-                if (t == nt - 1) mma_commit(&S.x_empty);
-              }
-            }
-            __syncwarp();
-          }
-          if (!ok) break;
-          if (++ss == KP) ss = 0, ps ^= 1;
-          ++g;
-        }
-        const int tp = t - (BUF - 1);
-        if (tp >= 0) {
-          const int gp = BUF == 1 || t >= nt ? g - 1 : g - 2;
-          const int py = BUF == 1 ? ny : prev_ny;
-          uint8_t* y = ybuf + 2 * sv * C::UNIT;
-          zero_tail<NB>(y, C::YBOX, py, lane);
-          if (KV) zero_tail<NB>(y + C::UNIT, C::YBOX, py, lane);
-          // the first sums of an item: the item before has read its accumulators
-          if ((tp == 0 && !wait_all(&S.acc_free, (nload & 1) ^ 1, abort_flag, 129)) ||
-              !wait_all(&S.p_full[gp & 1], (gp >> 1) & 1, abort_flag, 130)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          if (elect_lane()) {
-            const uint32_t w = tmem + (gp % BUF) * 2 * YT;
-            const int steps = (py + 15) >> 4;
-#pragma unroll 1
-            for (int which = KV ? 0 : 1; which < 2; ++which) {  // P Y2 (dv), then dS Y1
-              const uint64_t b = mndesc(su32(y + (1 - which) * C::UNIT), C::YBOX);
-              const uint32_t to = tmem + C::ACC + (KV ? (1 - which) * 64 * NB : 0);
-#pragma unroll 1
-              for (int k = 0; k < steps; ++k)
-                mma_ts(to, w + which * YT + 8 * k, b + 128 * k, id_acc, k != 0 || tp > 0);
-            }
-            mma_commit(&S.done[gp & 1]);
-            mma_commit(&S.y_empty[2 * sv]);
-            if (KV) mma_commit(&S.y_empty[2 * sv + 1]);
-            if (tp == nt - 1) mma_commit(&S.acc_full);
-          }
-          __syncwarp();
-          if (++sv == KP) sv = 0;
-        }
-        prev_ny = ny;
-      }
-      if (nt > 0) ++nload;
+      if (!wait_all(&S.item_full[n % C::ITEMS], (n / C::ITEMS) & 1, abort_flag, 125)) break;
+      const int nt = S.item[n % C::ITEMS].nt;
       __syncwarp();
-      if (lane == 0) mbar_arrive(&S.item_empty[n & 1]);
+      if (lane == 0) mbar_arrive(&S.item_empty[n % C::ITEMS]);
+      if (nt < 0) break;
+      if (nt == 0) continue;
+      ok = wait_all(&S.x_full, nload & 1, abort_flag, 126);
+#pragma unroll 1
+      for (int t = 0; ok && t < nt; ++t, ++g) {
+        // S and dP of the tile BUF before have been read, and p and ds over them
+        ok = wait_all(&S.y_full[s], ph, abort_flag, 128) &&
+             (g < BUF || wait_all(KV ? &S.done[(g - BUF) & 1] : &S.s_free[(g - BUF) & 1],
+                                  ((g - BUF) >> 1) & 1, abort_flag, 127));
+        if (!ok) break;
+        tc_fence_after();
+        const int ny = S.rows[s];
+        if (elect_lane()) {
+          const uint64_t y = kdesc(su32(ybuf + 2 * s * C::UNIT));
+          const uint32_t id = idesc(128, (ny + 15) & ~15, 0, 0), to = tmem + (g % BUF) * 2 * YT;
+          dot_tile(to, x, ABOX, y, C::YBOX, id, ksteps);
+          dot_tile(to + YT, x + NB * (ABOX >> 4), ABOX, y + (C::UNIT >> 4), C::YBOX, id, ksteps);
+          mma_commit(&S.s_full[g & 1]);
+          if (t == nt - 1) mma_commit(&S.x_empty);
+        }
+        __syncwarp();
+        if (++s == KP) s = 0, ph ^= 1;
+      }
+      ++nload;
     }
     if (elect_lane()) {
       mma_commit(&S.fin);
       drain_one(&S.fin, 0);
+    }
+    __syncwarp();
+  } else if (warp == WARPS + 2) {
+    // ---------------- the sums
+    const uint32_t id = idesc(128, ((p.dim + 15) >> 4) * 16, 0, 1);
+    int g = 0, nload = 0, s = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+#pragma unroll 1
+    for (int n = 0; ok; ++n) {
+      if (!wait_all(&S.item_full[n % C::ITEMS], (n / C::ITEMS) & 1, abort_flag, 139)) break;
+      const int nt = S.item[n % C::ITEMS].nt;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.item_empty[n % C::ITEMS]);
+      if (nt < 0) break;
+      if (nt == 0) continue;
+#pragma unroll 1
+      for (int t = 0; ok && t < nt; ++t, ++g) {
+        ok = wait_all(&S.y_full[s], ph, abort_flag, 140);
+        if (!ok) break;
+        const int ny = S.rows[s];
+        uint8_t* y = ybuf + 2 * s * C::UNIT;
+        zero_tail<NB>(y, C::YBOX, ny, lane);
+        if (KV) zero_tail<NB>(y + C::UNIT, C::YBOX, ny, lane);
+        // (the first: the item before has read its accumulators)
+        ok = (t > 0 || wait_all(&S.acc_free, (nload & 1) ^ 1, abort_flag, 129)) &&
+             wait_all(&S.p_full[g & 1], (g >> 1) & 1, abort_flag, 130);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_lane()) {
+          const int steps = (ny + 15) >> 4;
+          const uint64_t y1 = mndesc(su32(y), C::YBOX);
+          if (KV) {
+            const uint32_t w = tmem + (g % BUF) * 2 * YT;
+            sum_ts(tmem + C::ACC + 64 * NB, w, y1 + (C::UNIT >> 4), id, steps, t > 0);
+            sum_ts(tmem + C::ACC, w + YT, y1, id, steps, t > 0);
+          } else {
+            sum_ts(tmem + C::ACC, tmem + C::DS + (g % BUF) * (YT / 2), y1, id, steps, t > 0);
+          }
+          mma_commit(&S.done[g & 1]);
+          mma_commit(&S.y_empty[s]);
+          if (t == nt - 1) mma_commit(&S.acc_full);
+        }
+        __syncwarp();
+        if (++s == KP) s = 0, ph ^= 1;
+      }
+      ++nload;
+    }
+    if (elect_lane()) {
+      mma_commit(&S.fin2);
+      drain_one(&S.fin2, 0);
     }
     __syncwarp();
   } else {
@@ -390,10 +423,10 @@ __global__ void __launch_bounds__(TcBwd<KV, NB>::THREADS, TcBwd<KV, NB>::CTAS)
     bool ok = true;
 #pragma unroll 1
     for (int n = 0; ok; ++n) {
-      if (!wait_all(&S.item_full[n & 1], (n >> 1) & 1, abort_flag, 131)) break;
-      const BwdItem w = S.item[n & 1];
+      if (!wait_all(&S.item_full[n % C::ITEMS], (n / C::ITEMS) & 1, abort_flag, 131)) break;
+      const BwdItem w = S.item[n % C::ITEMS];
       __syncwarp();
-      if (lane == 0) mbar_arrive(&S.item_empty[n & 1]);
+      if (lane == 0) mbar_arrive(&S.item_empty[n % C::ITEMS]);
       if (w.nt < 0) break;
       const bool in = row < w.nx;
       const int64_t xr = w.x0 + w.r0 + row;   // the thread's row
@@ -403,13 +436,20 @@ __global__ void __launch_bounds__(TcBwd<KV, NB>::THREADS, TcBwd<KV, NB>::CTAS)
       if (!KV && in) {
         const float ls = p.lse_in[(int64_t)w.hx * p.Tq + xr];
         rl.x = ls == -INFINITY ? 0.f : -ls * kLog2e;  // (sees no key)
-        if (w.nt > 0) rl.y = -row_delta(p, xr, w.hx);
       }
+      if (!KV && w.nt > 0) {
+        if (!wait_all(&S.o_full, nload & 1, abort_flag, 137) ||
+            !wait_all(&S.x_full, nload & 1, abort_flag, 138))
+          break;
+        if (in) rl.y = -row_delta<NB>(xbuf + 2 * NB * ABOX, xbuf + NB * ABOX, row, p.dim);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.o_empty);
+      }
+      TileList list = w.list;
 #pragma unroll 1
-      for (int t = 0; t < w.nt; ++t, ++g) {
+      for (int t = 0; t < w.nt; ++t, ++g, list.next(YT)) {
         if (BUF == 2 && (g & 1) != buf) continue;
-        int h, r, ny;
-        bwd_tile<KV, YT>(w, p, t, &h, &r, &ny);
+        const int h = list.h, r = list.r, ny = list.rows(YT);
         const uint32_t sp = tmem + lane_off + (g % BUF) * 2 * YT;  // S, then dP
         // In columns of the tile: the last that the warp's first row sees, the first
         // that its last row sees, and (over keys) the end of the first tokens.
@@ -460,16 +500,24 @@ __global__ void __launch_bounds__(TcBwd<KV, NB>::THREADS, TcBwd<KV, NB>::CTAS)
 #pragma unroll 1
           for (int q = 0; q < ny; q += 32) {
             uint32_t p16[16], d16[16];
-            if (q >= end || (q + 31 < low && (KV || q >= sk))) {
-#pragma unroll
-              for (int e = 0; e < 16; ++e) p16[e] = d16[e] = 0u;
-            } else {
-              float v[32], d[32];
+            const bool skip = q >= end || (q + 31 < low && (KV || q >= sk));
+            float v[32], d[32];
+            if (!skip) {
               tmem_ld32_async(sp + q, v);
               tmem_ld32_async(sp + YT + q, d);
               tmem_wait_ld();
               tmem_landed(v);
               tmem_landed(d);
+            }
+            if (!KV && q + 32 >= ny && last) {  // S and dP have been read
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&S.s_free[g & 1]);
+            }
+            if (skip) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) p16[e] = d16[e] = 0u;
+            } else {
               if (q + 32 > min(ny, wh + 1) || (q < wl && (KV || q + 32 > sk))) {
                 uint32_t see;
                 if (KV) {
@@ -487,33 +535,46 @@ __global__ void __launch_bounds__(TcBwd<KV, NB>::THREADS, TcBwd<KV, NB>::CTAS)
                 }
               }
 #pragma unroll
-              for (int e = 0; e < 32; e += 2) {
-                float2 ml, md;
+              for (int e = 0; e < 32; e += 4) {
+                float4 ml = make_float4(rl.x, rl.x, rl.x, rl.x);
+                float4 md = make_float4(rl.y, rl.y, rl.y, rl.y);
                 if (KV) {
-                  ml = *reinterpret_cast<const float2*>(col + q + e);
-                  md = *reinterpret_cast<const float2*>(col + YT + q + e);
-                } else {
-                  ml = make_float2(rl.x, rl.x);
-                  md = make_float2(rl.y, rl.y);
+                  ml = *reinterpret_cast<const float4*>(col + q + e);
+                  md = *reinterpret_cast<const float4*>(col + YT + q + e);
                 }
-                const float2 z = fma2(make_float2(v[e], v[e + 1]), c2, ml);
-                const float2 y = make_float2(ex2(z.x), ex2(z.y));
-                const float2 dd = add2(make_float2(d[e], d[e + 1]), md);
-                const float2 x = fma2(y, dd, make_float2(0.f, 0.f));
-                if (!KV) ds2 = add2(ds2, x);
-                if (KV) p16[e >> 1] = pack_bf16(y.x, y.y);
-                d16[e >> 1] = pack_bf16(x.x, x.y);
+#pragma unroll
+                for (int f = 0; f < 4; f += 2) {
+                  const float2 z = fma2(make_float2(v[e + f], v[e + f + 1]), c2,
+                                        f ? make_float2(ml.z, ml.w) : make_float2(ml.x, ml.y));
+                  const float2 y = make_float2(ex2(z.x), ex2(z.y));
+                  const float2 dd = add2(make_float2(d[e + f], d[e + f + 1]),
+                                         f ? make_float2(md.z, md.w) : make_float2(md.x, md.y));
+                  const float2 x = mul2(y, dd);
+                  if (!KV) ds2 = add2(ds2, x);
+                  if (KV) p16[(e + f) >> 1] = pack_bf16(y.x, y.y);
+                  d16[(e + f) >> 1] = pack_bf16(x.x, x.y);
+                }
               }
             }
-            if (last) {  // over the pieces of S and dP that have been read
-              if (KV) tmem_st16(sp + (q >> 1), p16);
+            if (!last) continue;
+            if (KV) {  // over the pieces of S and dP that have been read
+              tmem_st16(sp + (q >> 1), p16);
               tmem_st16(sp + YT + (q >> 1), d16);
+            } else {
+              // the sums of the tile before have read its ds
+              if (q == 0 && g >= BUF &&
+                  !wait_all(&S.done[(g - BUF) & 1], ((g - BUF) >> 1) & 1, abort_flag, 136)) {
+                ok = false;
+                break;
+              }
+              tmem_st16(tmem + lane_off + C::DS + buf * (YT / 2) + (q >> 1), d16);
             }
           }
           if (last) break;
           rl.y -= ds2.x + ds2.y;
           ds2 = make_float2(0.f, 0.f);
         }
+        if (!ok) break;
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -692,11 +753,13 @@ cudaError_t tc_bwd_go(const AttnArgs& p, const BwdCut& cut, cudaStream_t st) {
                                 (int)C::kSmem);
   });
   if (e != cudaSuccess) return e;
-  CUtensorMap mq, mk, mv, md;
-  if (!make_heads_map(&mq, p.q, p.Tq, p.heads, p.dim) ||
-      !make_heads_map(&mk, p.k, p.Tk, p.kv, p.dim) ||
-      !make_heads_map(&mv, p.v, p.Tk, p.kv, p.dim) ||
-      !make_heads_map(&md, p.dout, p.Tq, p.heads, p.dim))
+  CUtensorMap mq, mk, mv, md, mo;
+  constexpr int xq = KV ? C::YT : AT, xk = KV ? AT : C::YT;  // rows of a box
+  if (!make_heads_map(&mq, p.q, p.Tq, p.heads, p.dim, xq) ||
+      !make_heads_map(&mk, p.k, p.Tk, p.kv, p.dim, xk) ||
+      !make_heads_map(&mv, p.v, p.Tk, p.kv, p.dim, xk) ||
+      !make_heads_map(&md, p.dout, p.Tq, p.heads, p.dim, xq) ||
+      !make_heads_map(&mo, p.o, p.Tq, p.heads, p.dim, AT))
     return cudaErrorInvalidValue;
   const int64_t items =
       KV ? (int64_t)p.B * p.kv *
@@ -706,7 +769,7 @@ cudaError_t tc_bwd_go(const AttnArgs& p, const BwdCut& cut, cudaStream_t st) {
   if (items > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
   count_launches(1);
   return launch_ex(attn_bwd_tc<KV, NB>, dim3((unsigned)items), dim3(C::THREADS), C::kSmem, st,
-                   false, KV ? mk : mq, KV ? mv : md, KV ? mq : mk, KV ? md : mv, p, cut);
+                   false, KV ? mk : mq, KV ? mv : md, KV ? mq : mk, KV ? md : mv, mo, p, cut);
 }
 
 cudaError_t tc_bwd(const AttnPlan& P, const tt_attn_seqs* s, const AttnArgs& p, float* parts,

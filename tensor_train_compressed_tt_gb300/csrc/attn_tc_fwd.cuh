@@ -15,11 +15,16 @@
 // and is computed again by itself with a running maximum (exact_row).
 //
 // Roles: warps 0-3 softmax and output, warp 4 finds the work and loads it,
-// warp 5 issues the products.  S has two buffers, so that the next S is
+// warp 5 issues S, warp 6 O += P V.  S has two buffers, so that the next S is
 // computed during a softmax, and two CTAs on an SM fill each other's waits.
-// The loops are not unrolled more than the softmax needs: with the code at
-// twice its size the kernel waited for instructions (the cache that several
-// SMs share answered at 90 % of its rate) and took 1.6 times as long.
+//
+// What held the kernel back was not a pipe.  The loops are not unrolled more
+// than the softmax needs: with the code at twice its size the kernel waited
+// for instructions (the cache that several SMs share answered at 90 % of its
+// rate) and took 1.6 times as long.  And each role's own code between two
+// hand-overs is kept short (tile lists that step, one barrier for a key and a
+// value tile, two warps for the two products): one thread that does the
+// bookkeeping of a whole tile takes as long as the tile.
 #pragma once
 
 #include "attn_tc.cuh"
@@ -32,18 +37,8 @@ struct FwdItem {
   int64_t q0, k0;      // the sequence's first rows
   int h, t0, nq, i0;   // head, first row, rows, position of the first row
   int lk;              // keys of the sequence
-  KeySpan ks;
-  int n1, nt;          // key tiles of the first span, of both; nt < 0: no more work
-  template <int KT>
-  __device__ void tile(int t, int* j0, int* n) const {
-    if (t < n1) {
-      *j0 = KT * t;
-      *n = min(KT, ks.a1 - *j0);
-    } else {
-      *j0 = ks.b0 + KT * (t - n1);
-      *n = min(KT, ks.b1 - *j0);
-    }
-  }
+  TileList keys;
+  int nt;              // key tiles; < 0: no more work
 };
 
 template <int NB>
@@ -53,22 +48,25 @@ struct TcFwd {
   static constexpr int KT = NB == 1 ? 96 : 64;  // keys of a tile
   static constexpr int QS = NB == 1 ? 2 : 1;    // query tiles in flight
   static constexpr int KP = NB == 1 ? 3 : 2;    // pairs of a key and a value tile in flight
+  static constexpr int ITEMS = 4;               // pieces of work told to the roles
   static constexpr int CTAS = 2;                // CTAs an SM
   static constexpr int KBOX = KT * 128, UNIT = NB * KBOX;
   static constexpr uint32_t O_COL = 2 * KT, COLS = 256;
   struct Shared {
-    uint64_t q_full[QS], q_empty[QS], kv_full[2 * KP], kv_empty[2 * KP];
-    uint64_t s_full[2], p_full[2], pv_done[2], o_free, fin;  // [tile & 1]
-    uint64_t item_full[2], item_empty[2], clc;
-    FwdItem item[2];
+    uint64_t q_full[QS], q_empty[QS], k_full[KP], k_empty[KP], v_full[KP], v_empty[KP];
+    uint64_t s_full[2], p_full[2], pv_done[2], o_free, fin, fin2;  // [tile & 1]
+    uint64_t item_full[ITEMS], item_empty[ITEMS], clc;
+    FwdItem item[ITEMS];
     uint4 answer;
+    int rows[2 * KP];  // keys of a tile, by its number (a key tile's place is free before
+                       // the product of its values has read this)
     uint32_t tmem;
     int abort_flag, never;
   };
   static constexpr size_t kSmem = QS * NB * ABOX + 2 * KP * UNIT + sizeof(Shared) + 1024;
 };
 
-constexpr int kTcThreads = 192;
+constexpr int kTcThreads = 224;
 
 // CTA number -> tile.  The tiles of one sequence and head come one after
 // another, so that they share its keys in L2; the last ones, which see the
@@ -89,9 +87,9 @@ __device__ __forceinline__ bool fwd_item(const AttnArgs& p, uint32_t item, uint3
   if (w->t0 >= s.lq) return false;
   w->nq = min(AT, s.lq - w->t0);
   w->i0 = w->t0 + s.off();
-  w->ks = key_span(p, s.lk, w->i0, w->i0 + w->nq - 1);
-  w->n1 = (w->ks.a1 + KT - 1) / KT;
-  w->nt = w->n1 + (w->ks.b1 - w->ks.b0 + KT - 1) / KT;
+  const KeySpan ks = key_span(p, s.lk, w->i0, w->i0 + w->nq - 1);
+  w->keys = key_list(ks, w->h / p.group);
+  w->nt = (ks.a1 + KT - 1) / KT + (ks.b1 - ks.b0 + KT - 1) / KT;
   return true;
 }
 
@@ -150,18 +148,25 @@ __global__ void __launch_bounds__(kTcThreads, TcFwd<NB>::CTAS)
   if (threadIdx.x == 0) {
     for (int i = 0; i < QS; ++i) mbar_init(&S.q_full[i], 1), mbar_init(&S.q_empty[i], 1);
 #pragma unroll 1
-    for (int i = 0; i < 2 * KP; ++i) mbar_init(&S.kv_full[i], 1), mbar_init(&S.kv_empty[i], 1);
+    for (int i = 0; i < KP; ++i) {
+      mbar_init(&S.k_full[i], 1);
+      mbar_init(&S.k_empty[i], 1);
+      mbar_init(&S.v_full[i], 1);
+      mbar_init(&S.v_empty[i], 1);
+    }
 #pragma unroll 1
     for (int i = 0; i < 2; ++i) {
       mbar_init(&S.s_full[i], 1);
       mbar_init(&S.p_full[i], 4);
       mbar_init(&S.pv_done[i], 1);
-      mbar_init(&S.item_full[i], 1);
-      mbar_init(&S.item_empty[i], 5);
     }
+#pragma unroll 1
+    for (int i = 0; i < C::ITEMS; ++i)
+      mbar_init(&S.item_full[i], 1), mbar_init(&S.item_empty[i], 6);
     mbar_init(&S.o_free, 4);
     mbar_init(&S.clc, 1);
     mbar_init(&S.fin, 1);
+    mbar_init(&S.fin2, 1);
     S.abort_flag = S.never = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -178,157 +183,179 @@ __global__ void __launch_bounds__(kTcThreads, TcFwd<NB>::CTAS)
     // ---------------- work and loads
     if (lane == 0) {
       const uint32_t ntiles = (p.max_q + AT - 1) / AT;
-      int n = 0, nload = 0, asked = 0, s = 0, loads = 0;
-      uint32_t ph = 1;  // parity of the ring's empty barriers, as of a round before the first
-      bool ok = true;
+      int n = 0, nload = 0, s = 0, loads = 0;
+      uint32_t ph = 1, clc = 0;  // parity of the ring's empty barriers; of the next answer
+      bool ok = true, first = true;
       int cta = (int)blockIdx.x;
       FwdItem cur, w;
-      cur.nt = 0;
-      bool more = true;
+      cur.nt = -1;
 #pragma unroll 1
-      while (more && ok) {
-        int u = 0;  // K, V of tile 0, K, V of tile 1, ...
+      while (true) {
+        // The next piece of work: told to the roles, its rows sent for from memory, before
+        // the loads of the current one, so that its own loads find them in L2.
+        w.nt = -1;
 #pragma unroll 1
-        for (int pass = 0; pass < 2; ++pass) {
-          // With two query buffers the next piece of work is looked for, and its
-          // queries sent for, once the ring of keys is full.
-          const int end = pass == 0 && QS == 2 ? min(2 * KP, 2 * cur.nt) : 2 * cur.nt;
-#pragma unroll 1
-          for (; ok && u < end; ++u) {
-            int j0, nk;
-            cur.tile<KT>(u >> 1, &j0, &nk);
-            ok = wait_one(&S.kv_empty[s], ph, abort_flag, 101);
-            if (!ok) break;
-            load_tile<NB>(kvbuf + s * C::UNIT, C::KBOX, u & 1 ? &tm_v : &tm_k, &S.kv_full[s],
-                          cur.h / p.group, (int)cur.k0 + j0, nk);
-            ++loads;
-            if (++s == 2 * KP) s = 0, ph ^= 1;
-          }
-          more = pass == 0 ? false : more;
-#pragma unroll 1
-          while (pass == 0 && ok && !more) {
-            if (asked > 0)
-              cta = wait_one(&S.clc, (asked - 1) & 1, &S.never, 96) ? clc_take(&S.answer) : -1;
+        while (cta >= 0) {
+          if (!first) {
+            // After an abort the CTAs that have not started are still taken over, and do
+            // nothing.
+            cta = wait_one(&S.clc, clc, &S.never, 95) ? clc_take(&S.answer) : -1;
+            clc ^= 1;
             if (cta < 0) break;
-            clc_ask(&S.answer, &S.clc);  // the one after it
-            ++asked;
-            more = fwd_item<KT>(p, (uint32_t)cta, ntiles, &w);
-            if (!more) continue;
-            ok = wait_one(&S.item_empty[n & 1], ((n >> 1) & 1) ^ 1, abort_flag, 99);
+          }
+          first = false;
+          clc_ask(&S.answer, &S.clc);
+          if (!ok || !fwd_item<KT>(p, (uint32_t)cta, ntiles, &w)) {
+            w.nt = -1;
+            continue;
+          }
+          const int slot = n % C::ITEMS;
+          ok = wait_one(&S.item_empty[slot], ((n / C::ITEMS) & 1) ^ 1, abort_flag, 96);
+          if (!ok) {
+            w.nt = -1;
+            continue;
+          }
+          S.item[slot] = w;
+          mbar_arrive(&S.item_full[slot]);
+          ++n;
+          if (w.nt > 0) {
+            const int span = min(w.keys.lim2 - w.keys.r2, 4 * KT);
+            prefetch_rows<NB>(&tm_q, AT, w.h, (int)w.q0 + w.t0, w.nq);
+            prefetch_rows<NB>(&tm_k, KT, w.keys.h, (int)w.k0 + w.keys.r2, span);
+            prefetch_rows<NB>(&tm_v, KT, w.keys.h, (int)w.k0 + w.keys.r2, span);
+          }
+          break;
+        }
+        if (ok && cur.nt > 0) {
+          const int qs = nload % QS;
+          ok = wait_one(&S.q_empty[qs], ((nload / QS) & 1) ^ 1, abort_flag, 97);
+          if (ok) {
+            mbar_expect_tx(&S.q_full[qs], NB * ABOX);
+            load_tile<NB>(qbuf + qs * NB * ABOX, ABOX, &tm_q, &S.q_full[qs], cur.h,
+                          (int)cur.q0 + cur.t0);
+            ++nload;
+          }
+          TileList l = cur.keys;
+#pragma unroll 1
+          for (int t = 0; ok && t < cur.nt; ++t) {
+            ok = wait_one(&S.k_empty[s], ph, abort_flag, 98);
             if (!ok) break;
-            S.item[n & 1] = w;
-            mbar_arrive(&S.item_full[n & 1]);
-            ++n;
-            if (w.nt > 0) {
-              const int qs = nload % QS;
-              ok = wait_one(&S.q_empty[qs], ((nload / QS) & 1) ^ 1, abort_flag, 100);
-              if (!ok) break;
-              load_tile<NB>(qbuf + qs * NB * ABOX, ABOX, &tm_q, &S.q_full[qs], w.h,
-                            (int)w.q0 + w.t0, w.nq);
-              ++nload;
+            S.rows[loads % (2 * KP)] = l.rows(KT);
+            uint8_t* dst = kvbuf + 2 * s * C::UNIT;
+            mbar_expect_tx(&S.k_full[s], C::UNIT);
+            load_tile<NB>(dst, C::KBOX, &tm_k, &S.k_full[s], l.h, (int)cur.k0 + l.r);
+            ok = wait_one(&S.v_empty[s], ph, abort_flag, 94);
+            if (!ok) {
+              drain_one(&S.k_full[s], ph ^ 1);
+              break;
             }
+            mbar_expect_tx(&S.v_full[s], C::UNIT);
+            load_tile<NB>(dst + C::UNIT, C::KBOX, &tm_v, &S.v_full[s], l.h, (int)cur.k0 + l.r);
+            l.next(KT);
+            ++loads;
+            if (++s == KP) s = 0, ph ^= 1;
           }
         }
+        if (w.nt < 0) break;
         cur = w;
       }
-      // After an abort the CTAs that have not started are still taken over, and do nothing.
-#pragma unroll 1
-      while (!ok && cta >= 0) {
-        cta = wait_one(&S.clc, (asked - 1) & 1, &S.never, 98) ? clc_take(&S.answer) : -1;
-        if (cta >= 0) clc_ask(&S.answer, &S.clc), ++asked;
-      }
-      if (ok && wait_one(&S.item_empty[n & 1], ((n >> 1) & 1) ^ 1, abort_flag, 94)) {
-        S.item[n & 1].nt = -1;
-        mbar_arrive(&S.item_full[n & 1]);
+      if (ok && wait_one(&S.item_empty[n % C::ITEMS], ((n / C::ITEMS) & 1) ^ 1, abort_flag, 99)) {
+        S.item[n % C::ITEMS].nt = -1;
+        mbar_arrive(&S.item_full[n % C::ITEMS]);
       }
       // nothing is in flight into shared memory when the CTA leaves
 #pragma unroll 1
       for (int i = 1; i <= QS && i <= nload; ++i)
         drain_one(&S.q_full[(nload - i) % QS], (uint32_t)(((nload - i) / QS) & 1));
 #pragma unroll 1
-      for (int i = 0; i < 2 * KP && i < loads; ++i) {
-        if (--s < 0) s = 2 * KP - 1, ph ^= 1;
-        drain_one(&S.kv_full[s], ph ^ 1);  // the last load into unit s
+      for (int i = 0; i < KP && i < loads; ++i) {
+        if (--s < 0) s = KP - 1, ph ^= 1;
+        drain_one(&S.k_full[s], ph ^ 1);  // the last loads into pair s
+        drain_one(&S.v_full[s], ph ^ 1);
       }
     }
   } else if (warp == 5) {
-    // ---------------- products: S of tile t, then O (+)= P V of tile t - 1
+    // ---------------- S of every tile
     const int ksteps = (p.dim + 15) >> 4;
-    const uint32_t id_o = idesc(128, ksteps * 16, 0, 1);
-    int g = 0, nload = 0, ss = 0, sv = 0;  // tiles so far; pair of the next S, of the next P V
-    uint32_t ps = 0, pp = 0;               // their parities
+    int g = 0, nload = 0, s = 0;
+    uint32_t ph = 0;
     bool ok = true;
 #pragma unroll 1
     for (int n = 0; ok; ++n) {
-      if (!wait_all(&S.item_full[n & 1], (n >> 1) & 1, abort_flag, 97)) break;
-      const int nt = S.item[n & 1].nt;
-      if (nt < 0) break;
-      int prev_nk = 0;
-#pragma unroll 1
-      for (int t = 0; ok && t <= nt && nt > 0; ++t) {
-        int nk = 0;
-        if (t < nt) {
-          int j0;
-          S.item[n & 1].template tile<KT>(t, &j0, &nk);
-          // S of tile g goes where P of tile g - 2 was
-          if ((t == 0 && !wait_all(&S.q_full[nload % QS], (nload / QS) & 1, abort_flag, 105)) ||
-              !wait_all(&S.kv_full[2 * ss], ps, abort_flag, 107) ||
-              (g > 1 && !wait_all(&S.pv_done[g & 1], ((g >> 1) - 1) & 1, abort_flag, 106))) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          if (elect_lane()) {
-            const uint64_t q = kdesc(su32(qbuf + (nload % QS) * NB * ABOX));
-            const uint64_t k = kdesc(su32(kvbuf + 2 * ss * C::UNIT));
-            const uint32_t id = idesc(128, (nk + 15) & ~15, 0, 0);
-            const uint32_t sc = tmem + (g & 1) * KT;
-#pragma unroll 1
-            for (int c = 0; c < ksteps; ++c)
-              mma(sc, q + (c >> 2) * (ABOX >> 4) + 2 * (c & 3),
-                  k + (c >> 2) * (C::KBOX >> 4) + 2 * (c & 3), id, c != 0);
-            mma_commit(&S.s_full[g & 1]);
-            mma_commit(&S.kv_empty[2 * ss]);
-            if (t == nt - 1) mma_commit(&S.q_empty[nload % QS]);
-          }
-          __syncwarp();
-          if (++ss == KP) ss = 0, ps ^= 1;
-          ++g;
-        }
-        if (t > 0) {
-          const int gp = t < nt ? g - 2 : g - 1;
-          uint8_t* vt = kvbuf + (2 * sv + 1) * C::UNIT;
-          if (!wait_all(&S.kv_full[2 * sv + 1], pp, abort_flag, 102)) { ok = false; break; }
-          zero_tail<NB>(vt, C::KBOX, prev_nk, lane);
-          // the first product of an item: the item before has read its O
-          if ((t == 1 && !wait_all(&S.o_free, (nload & 1) ^ 1, abort_flag, 103)) ||
-              !wait_all(&S.p_full[gp & 1], (gp >> 1) & 1, abort_flag, 104)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          if (elect_lane()) {
-            const uint64_t v = mndesc(su32(vt), C::KBOX);
-            const uint32_t pc = tmem + (gp & 1) * KT;
-            const int steps = (prev_nk + 15) >> 4;
-#pragma unroll 1
-            for (int k = 0; k < steps; ++k)
-              mma_ts(tmem + C::O_COL, pc + 8 * k, v + 128 * k, id_o, k != 0 || t > 1);
-            mma_commit(&S.pv_done[gp & 1]);
-            mma_commit(&S.kv_empty[2 * sv + 1]);
-          }
-          __syncwarp();
-          if (++sv == KP) sv = 0, pp ^= 1;
-        }
-        prev_nk = nk;
-      }
-      if (nt > 0) ++nload;
+      if (!wait_all(&S.item_full[n % C::ITEMS], (n / C::ITEMS) & 1, abort_flag, 100)) break;
+      const int nt = S.item[n % C::ITEMS].nt;
       __syncwarp();
-      if (lane == 0) mbar_arrive(&S.item_empty[n & 1]);
+      if (lane == 0) mbar_arrive(&S.item_empty[n % C::ITEMS]);
+      if (nt < 0) break;
+      if (nt == 0) continue;
+      const int qs = nload % QS;
+      ok = wait_all(&S.q_full[qs], (nload / QS) & 1, abort_flag, 101);
+      const uint64_t q = kdesc(su32(qbuf + qs * NB * ABOX));
+#pragma unroll 1
+      for (int t = 0; ok && t < nt; ++t, ++g) {
+        // S of tile g goes where P of tile g - 2 was
+        ok = wait_all(&S.k_full[s], ph, abort_flag, 102) &&
+             (g < 2 || wait_all(&S.pv_done[g & 1], ((g >> 1) - 1) & 1, abort_flag, 103));
+        if (!ok) break;
+        tc_fence_after();
+        const int nk = S.rows[g % (2 * KP)];
+        if (elect_lane()) {
+          dot_tile(tmem + (g & 1) * KT, q, ABOX, kdesc(su32(kvbuf + 2 * s * C::UNIT)), C::KBOX,
+                   idesc(128, (nk + 15) & ~15, 0, 0), ksteps);
+          mma_commit(&S.s_full[g & 1]);
+          mma_commit(&S.k_empty[s]);
+          if (t == nt - 1) mma_commit(&S.q_empty[qs]);
+        }
+        __syncwarp();
+        if (++s == KP) s = 0, ph ^= 1;
+      }
+      ++nload;
     }
     if (elect_lane()) {
       mma_commit(&S.fin);
       drain_one(&S.fin, 0);
+    }
+    __syncwarp();
+  } else if (warp == 6) {
+    // ---------------- O (+)= P V of every tile
+    const uint32_t id = idesc(128, ((p.dim + 15) >> 4) * 16, 0, 1);
+    int g = 0, nload = 0, s = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+#pragma unroll 1
+    for (int n = 0; ok; ++n) {
+      if (!wait_all(&S.item_full[n % C::ITEMS], (n / C::ITEMS) & 1, abort_flag, 104)) break;
+      const int nt = S.item[n % C::ITEMS].nt;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.item_empty[n % C::ITEMS]);
+      if (nt < 0) break;
+      if (nt == 0) continue;
+#pragma unroll 1
+      for (int t = 0; ok && t < nt; ++t, ++g) {
+        ok = wait_all(&S.v_full[s], ph, abort_flag, 105);
+        if (!ok) break;
+        const int nk = S.rows[g % (2 * KP)];
+        uint8_t* vt = kvbuf + (2 * s + 1) * C::UNIT;
+        zero_tail<NB>(vt, C::KBOX, nk, lane);
+        // (the first: the item before has read its O)
+        ok = (t > 0 || wait_all(&S.o_free, (nload & 1) ^ 1, abort_flag, 106)) &&
+             wait_all(&S.p_full[g & 1], (g >> 1) & 1, abort_flag, 107);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_lane()) {
+          sum_ts(tmem + C::O_COL, tmem + (g & 1) * KT, mndesc(su32(vt), C::KBOX), id,
+                 (nk + 15) >> 4, t > 0);
+          mma_commit(&S.pv_done[g & 1]);
+          mma_commit(&S.v_empty[s]);
+        }
+        __syncwarp();
+        if (++s == KP) s = 0, ph ^= 1;
+      }
+      ++nload;
+    }
+    if (elect_lane()) {
+      mma_commit(&S.fin2);
+      drain_one(&S.fin2, 0);
     }
     __syncwarp();
   } else {
@@ -341,18 +368,18 @@ __global__ void __launch_bounds__(kTcThreads, TcFwd<NB>::CTAS)
     bool ok = true;
 #pragma unroll 1
     for (int n = 0; ok; ++n) {
-      if (!wait_all(&S.item_full[n & 1], (n >> 1) & 1, abort_flag, 108)) break;
-      const FwdItem w = S.item[n & 1];
+      if (!wait_all(&S.item_full[n % C::ITEMS], (n / C::ITEMS) & 1, abort_flag, 108)) break;
+      const FwdItem w = S.item[n % C::ITEMS];
       __syncwarp();
-      if (lane == 0) mbar_arrive(&S.item_empty[n & 1]);
+      if (lane == 0) mbar_arrive(&S.item_empty[n % C::ITEMS]);
       if (w.nt < 0) break;
       const int iw = w.i0 + 32 * warp;  // position of the warp's first row
       float m = -INFINITY, l = 0.f;
       bool fresh = true;  // some row of the warp has seen no key
+      TileList keys = w.keys;
 #pragma unroll 1
-      for (int t = 0; t < w.nt; ++t, ++g) {
-        int j0, nk;
-        w.tile<KT>(t, &j0, &nk);
+      for (int t = 0; t < w.nt; ++t, ++g, keys.next(KT)) {
+        const int j0 = keys.r, nk = keys.rows(KT);
         const uint32_t sp = tmem + lane_off + (g & 1) * KT;  // S, and P over it
         // In keys from j0 on: the last one that the warp's first row sees, the first
         // one that its last row sees, the end of the first tokens.  A later row sees
@@ -472,8 +499,9 @@ cudaError_t tc_fwd_go(const AttnArgs& p, cudaStream_t st) {
   });
   if (e != cudaSuccess) return e;
   CUtensorMap mq, mk, mv;
-  if (!make_heads_map(&mq, p.q, p.Tq, p.heads, p.dim) ||
-      !make_heads_map(&mk, p.k, p.Tk, p.kv, p.dim) || !make_heads_map(&mv, p.v, p.Tk, p.kv, p.dim))
+  if (!make_heads_map(&mq, p.q, p.Tq, p.heads, p.dim, AT) ||
+      !make_heads_map(&mk, p.k, p.Tk, p.kv, p.dim, C::KT) ||
+      !make_heads_map(&mv, p.v, p.Tk, p.kv, p.dim, C::KT))
     return cudaErrorInvalidValue;
   const int64_t items = (int64_t)((p.max_q + AT - 1) / AT) * p.heads * p.B;
   if (items > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
