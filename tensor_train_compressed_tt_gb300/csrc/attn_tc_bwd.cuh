@@ -14,22 +14,21 @@
 // Both passes have the same shape.  X1, X2 are the 128 rows that a CTA works
 // on (Q and dO, or K and V), Y1, Y2 tiles of YT of the others' rows (K and V,
 // or Q and dO):  S = X1 Y1^T and dP = X2 Y2^T into tensor memory, the softmax
-// warps (thread = row) turn them into p and ds as bf16, and the accumulators
-// take  acc0 += dS Y1  (dq, or dk) and, in the pass over keys, acc1 += P Y2 (dv).
-// Over queries ds has columns of its own, so S and dP of the next tile are
-// computed as soon as this tile's have been read; over keys the accumulators
-// take those columns, and p and ds lie over S and dP.  (p and ds in shared
-// memory instead were no faster: the warps that write them are what bounds the
-// pass, and shared memory, with lse and delta read for every column, is what
-// they wait for.)
+// warps (thread = row) put p and ds over them as bf16, and the accumulators
+// take  acc0 += dS Y1  and  acc1 += P Y  (over keys dk and dv; over queries dq
+// and P K, see below).
 //
 // delta comes from the stored o, whose rounding shows in rows of few keys:
-// sum_j ds_j, which should vanish, is then delta's error (the p_j add up to 1).
-// The first pass adds that sum to the delta that it leaves for the second.
+// with e = sum_j ds_j, which should vanish, delta + e is right (the p_j add up
+// to 1).  Over queries e is known at the end, and dq = scale (acc0 - e P K);
+// the pass over keys gets the corrected delta.
 //
-// Roles as in the forward (one warp issues S and dP, another the sums).  Heads of up to 64 channels run two CTAs an SM with
-// one buffer of S and dP each; wider ones fill the tensor memory with two
-// buffers in one CTA, each with its own four softmax warps.
+// Roles as in the forward (one warp issues S and dP, another the sums).  What
+// bounds the passes is the chain of hand-overs of a tile, S and dP (0.35 us),
+// softmax (1 us), sums (0.3 us), 2.2 us with the waits between, so the one CTA of
+// an SM keeps as many tiles in turn as the tensor memory holds: three buffers
+// of S and dP for heads of up to 64 channels, two for wider ones, each with its
+// own four softmax warps.
 //
 // The pass over keys: the first tokens are seen by every later query, so their
 // tile is cut into pieces of its list of query tiles, each the work of one
@@ -62,33 +61,31 @@ struct BwdItem {
 
 template <bool KV, int NB>
 struct TcBwd {
-  static constexpr int BUF = NB;                          // buffers of S and dP
-  static constexpr int YT = 64;                           // rows of a Y tile
-  static constexpr int NX = KV ? 2 : 3;                   // X tiles: over queries o, too
-  static constexpr int KP = KV ? 4 : 3;                   // pairs of Y tiles in flight
-  static constexpr int ITEMS = 4;                         // items told to the roles
-  static constexpr int CTAS = NB == 1 ? 2 : 1;            // CTAs an SM
-  static constexpr int YBOX = YT * 128, UNIT = NB * YBOX;
-  static constexpr uint32_t DS = BUF * 2 * YT, ACC = DS + (KV ? 0 : BUF * YT / 2),
-                            COLS = NB == 1 ? 256 : 512;
-  static constexpr int WARPS = 4 * BUF;                   // softmax warps
+  static constexpr int BUF = NB == 1 ? 3 : 2;     // buffers of S and dP
+  static constexpr int YT = 64;                   // rows of a Y tile
+  static constexpr int NX = KV ? 2 : 3;           // X tiles: over queries o, too
+  static constexpr int XS = NB == 1 ? 2 : 1;      // sets of X tiles in flight
+  static constexpr int KP = NB == 1 ? 6 : KV ? 4 : 3;  // pairs of Y tiles in flight
+  static constexpr int ITEMS = 4;                 // items told to the roles
+  static constexpr int YBOX = YT * 128, UNIT = NB * YBOX, XSET = NX * NB * ABOX;
+  static constexpr uint32_t ACC = BUF * 2 * YT, COLS = 512;
+  static constexpr int WARPS = 4 * BUF;           // softmax warps
   static constexpr int THREADS = 32 * (WARPS + 3);
   struct Shared {
-    uint64_t x_full, x_empty, y_full[KP], y_empty[KP];
-    uint64_t s_full[2], s_free[2], p_full[2], done[2], acc_full, acc_free, fin, fin2;  // [tile & 1]
+    uint64_t x_full[XS], x_empty[XS], y_full[KP], y_empty[KP];
+    uint64_t s_full[BUF], p_full[BUF], done[BUF], acc_full, acc_free, fin, fin2;
     uint64_t item_full[ITEMS], item_empty[ITEMS], clc;
-    uint64_t o_full, o_empty;
-    uint64_t col_full[2];  // [buffer]
+    uint64_t col_full[BUF], half_full;
     BwdItem item[ITEMS];
     uint4 answer;
     int rows[KP];  // rows of the pair's tile
-    float col[KV ? BUF : 1][2][2][KV ? YT : 4];  // lse and delta of a tile's queries
-    float half[KV ? 1 : AT];  // the second buffer's sums of ds
+    alignas(16) float col[KV ? BUF : 1][2][2][KV ? YT : 4];  // lse and delta of a tile's queries
+    float half[KV ? 1 : BUF][KV ? 1 : AT];  // each buffer's sums of ds
     uint32_t tmem;
     int abort_flag, never;
   };
-  static constexpr size_t kSmem = NX * NB * ABOX + 2 * KP * UNIT + sizeof(Shared) + 1024;
-  static_assert(ACC + (KV ? 2 : 1) * 64 * NB <= COLS, "tensor memory");
+  static constexpr size_t kSmem = XS * XSET + 2 * KP * UNIT + sizeof(Shared) + 1024;
+  static_assert(ACC + 2 * 64 * NB <= COLS, "tensor memory");
 };
 
 // CTA number -> item.  False: nothing to do.
@@ -176,27 +173,27 @@ __device__ __forceinline__ float row_delta(const uint8_t* o, const uint8_t* d, i
 }
 
 template <bool KV, int NB>
-__global__ void __launch_bounds__(TcBwd<KV, NB>::THREADS, TcBwd<KV, NB>::CTAS)
+__global__ void __launch_bounds__(TcBwd<KV, NB>::THREADS, 1)
     attn_bwd_tc(const __grid_constant__ CUtensorMap tm_x1, const __grid_constant__ CUtensorMap tm_x2,
                 const __grid_constant__ CUtensorMap tm_y1, const __grid_constant__ CUtensorMap tm_y2,
                 const __grid_constant__ CUtensorMap tm_o,
                 const __grid_constant__ AttnArgs p, const __grid_constant__ BwdCut cut) {
   using C = TcBwd<KV, NB>;
-  constexpr int YT = C::YT, KP = C::KP, BUF = C::BUF, WARPS = C::WARPS;
+  constexpr int YT = C::YT, KP = C::KP, BUF = C::BUF, WARPS = C::WARPS, XS = C::XS;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* xbuf = align1k(smem_raw);      // X1, X2 and, over queries, o
-  uint8_t* ybuf = xbuf + C::NX * NB * ABOX;  // Y1 and Y2 of pair s: units 2 s and 2 s + 1
+  uint8_t* xbuf = align1k(smem_raw);      // sets of X1, X2 and, over queries, o
+  uint8_t* ybuf = xbuf + XS * C::XSET;    // Y1 and Y2 of pair s: units 2 s and 2 s + 1
   auto& S = *reinterpret_cast<typename C::Shared*>(ybuf + 2 * KP * C::UNIT);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    mbar_init(&S.x_full, 1);
-    mbar_init(&S.x_empty, 1);
+#pragma unroll 1
+    for (int i = 0; i < XS; ++i)
+      mbar_init(&S.x_full[i], 1), mbar_init(&S.x_empty[i], KV ? 1 : 1 + WARPS);
 #pragma unroll 1
     for (int i = 0; i < KP; ++i) mbar_init(&S.y_full[i], 1), mbar_init(&S.y_empty[i], 1);
 #pragma unroll 1
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < BUF; ++i) {
       mbar_init(&S.s_full[i], 1);
-      mbar_init(&S.s_free[i], 4);
       mbar_init(&S.p_full[i], 4);
       mbar_init(&S.done[i], 1);
       mbar_init(&S.col_full[i], 4);
@@ -204,8 +201,7 @@ __global__ void __launch_bounds__(TcBwd<KV, NB>::THREADS, TcBwd<KV, NB>::CTAS)
 #pragma unroll 1
     for (int i = 0; i < C::ITEMS; ++i)
       mbar_init(&S.item_full[i], 1), mbar_init(&S.item_empty[i], WARPS + 2);
-    mbar_init(&S.o_full, 1);
-    mbar_init(&S.o_empty, WARPS);
+    mbar_init(&S.half_full, WARPS);
     mbar_init(&S.acc_full, 1);
     mbar_init(&S.acc_free, WARPS);
     mbar_init(&S.clc, 1);
@@ -273,17 +269,15 @@ __global__ void __launch_bounds__(TcBwd<KV, NB>::THREADS, TcBwd<KV, NB>::CTAS)
           break;
         }
         if (ok && cur.nt > 0) {
-          ok = wait_one(&S.x_empty, (nload & 1) ^ 1, abort_flag, 121) &&
-               (KV || wait_one(&S.o_empty, (nload & 1) ^ 1, abort_flag, 119));
+          const int xs = nload % XS;
+          ok = wait_one(&S.x_empty[xs], ((nload / XS) & 1) ^ 1, abort_flag, 121);
           if (ok) {
             const int row = (int)cur.x0 + cur.r0;
-            mbar_expect_tx(&S.x_full, 2 * NB * ABOX);
-            load_tile<NB>(xbuf, ABOX, &tm_x1, &S.x_full, cur.hx, row);
-            load_tile<NB>(xbuf + NB * ABOX, ABOX, &tm_x2, &S.x_full, cur.hx, row);
-            if (!KV) {
-              mbar_expect_tx(&S.o_full, NB * ABOX);
-              load_tile<NB>(xbuf + 2 * NB * ABOX, ABOX, &tm_o, &S.o_full, cur.hx, row);
-            }
+            uint8_t* dst = xbuf + xs * C::XSET;
+            mbar_expect_tx(&S.x_full[xs], C::XSET);
+            load_tile<NB>(dst, ABOX, &tm_x1, &S.x_full[xs], cur.hx, row);
+            load_tile<NB>(dst + NB * ABOX, ABOX, &tm_x2, &S.x_full[xs], cur.hx, row);
+            if (!KV) load_tile<NB>(dst + 2 * NB * ABOX, ABOX, &tm_o, &S.x_full[xs], cur.hx, row);
             ++nload;
           }
           TileList l = cur.list;
@@ -309,8 +303,9 @@ __global__ void __launch_bounds__(TcBwd<KV, NB>::THREADS, TcBwd<KV, NB>::CTAS)
         mbar_arrive(&S.item_full[n % C::ITEMS]);
       }
       // nothing is in flight into shared memory when the CTA leaves
-      if (nload > 0) drain_one(&S.x_full, (uint32_t)((nload - 1) & 1));
-      if (!KV && nload > 0) drain_one(&S.o_full, (uint32_t)((nload - 1) & 1));
+#pragma unroll 1
+      for (int i = 1; i <= XS && i <= nload; ++i)
+        drain_one(&S.x_full[(nload - i) % XS], (uint32_t)(((nload - i) / XS) & 1));
 #pragma unroll 1
       for (int i = 0; i < KP && i < loads; ++i) {
         if (--s < 0) s = KP - 1, ph ^= 1;
@@ -320,9 +315,8 @@ __global__ void __launch_bounds__(TcBwd<KV, NB>::THREADS, TcBwd<KV, NB>::CTAS)
   } else if (warp == WARPS + 1) {
     // ---------------- S and dP of every tile
     const int ksteps = (p.dim + 15) >> 4;
-    const uint64_t x = kdesc(su32(xbuf));
-    int g = 0, nload = 0, s = 0;
-    uint32_t ph = 0;
+    int nload = 0, s = 0, b = 0;
+    uint32_t ph = 0, pb = 1;  // parity of the pair; of the buffer's last sums
     bool ok = true;
 #pragma unroll 1
     for (int n = 0; ok; ++n) {
@@ -332,26 +326,28 @@ __global__ void __launch_bounds__(TcBwd<KV, NB>::THREADS, TcBwd<KV, NB>::CTAS)
       if (lane == 0) mbar_arrive(&S.item_empty[n % C::ITEMS]);
       if (nt < 0) break;
       if (nt == 0) continue;
-      ok = wait_all(&S.x_full, nload & 1, abort_flag, 126);
+      const int xs = nload % XS;
+      ok = wait_all(&S.x_full[xs], (nload / XS) & 1, abort_flag, 126);
+      const uint64_t x = kdesc(su32(xbuf + xs * C::XSET));
 #pragma unroll 1
-      for (int t = 0; ok && t < nt; ++t, ++g) {
-        // S and dP of the tile BUF before have been read, and p and ds over them
+      for (int t = 0; ok && t < nt; ++t) {
+        // the p and ds that lie over the buffer have been summed
         ok = wait_all(&S.y_full[s], ph, abort_flag, 128) &&
-             (g < BUF || wait_all(KV ? &S.done[(g - BUF) & 1] : &S.s_free[(g - BUF) & 1],
-                                  ((g - BUF) >> 1) & 1, abort_flag, 127));
+             wait_all(&S.done[b], pb, abort_flag, 127);
         if (!ok) break;
         tc_fence_after();
         const int ny = S.rows[s];
         if (elect_lane()) {
           const uint64_t y = kdesc(su32(ybuf + 2 * s * C::UNIT));
-          const uint32_t id = idesc(128, (ny + 15) & ~15, 0, 0), to = tmem + (g % BUF) * 2 * YT;
+          const uint32_t id = idesc(128, (ny + 15) & ~15, 0, 0), to = tmem + b * 2 * YT;
           dot_tile(to, x, ABOX, y, C::YBOX, id, ksteps);
           dot_tile(to + YT, x + NB * (ABOX >> 4), ABOX, y + (C::UNIT >> 4), C::YBOX, id, ksteps);
-          mma_commit(&S.s_full[g & 1]);
-          if (t == nt - 1) mma_commit(&S.x_empty);
+          mma_commit(&S.s_full[b]);
+          if (t == nt - 1) mma_commit(&S.x_empty[xs]);
         }
         __syncwarp();
         if (++s == KP) s = 0, ph ^= 1;
+        if (++b == BUF) b = 0, pb ^= 1;
       }
       ++nload;
     }
@@ -363,8 +359,8 @@ __global__ void __launch_bounds__(TcBwd<KV, NB>::THREADS, TcBwd<KV, NB>::CTAS)
   } else if (warp == WARPS + 2) {
     // ---------------- the sums
     const uint32_t id = idesc(128, ((p.dim + 15) >> 4) * 16, 0, 1);
-    int g = 0, nload = 0, s = 0;
-    uint32_t ph = 0;
+    int nload = 0, s = 0, b = 0;
+    uint32_t ph = 0, pb = 0;
     bool ok = true;
 #pragma unroll 1
     for (int n = 0; ok; ++n) {
@@ -375,7 +371,7 @@ __global__ void __launch_bounds__(TcBwd<KV, NB>::THREADS, TcBwd<KV, NB>::CTAS)
       if (nt < 0) break;
       if (nt == 0) continue;
 #pragma unroll 1
-      for (int t = 0; ok && t < nt; ++t, ++g) {
+      for (int t = 0; ok && t < nt; ++t) {
         ok = wait_all(&S.y_full[s], ph, abort_flag, 140);
         if (!ok) break;
         const int ny = S.rows[s];
@@ -384,25 +380,22 @@ __global__ void __launch_bounds__(TcBwd<KV, NB>::THREADS, TcBwd<KV, NB>::CTAS)
         if (KV) zero_tail<NB>(y + C::UNIT, C::YBOX, ny, lane);
         // (the first: the item before has read its accumulators)
         ok = (t > 0 || wait_all(&S.acc_free, (nload & 1) ^ 1, abort_flag, 129)) &&
-             wait_all(&S.p_full[g & 1], (g >> 1) & 1, abort_flag, 130);
+             wait_all(&S.p_full[b], pb, abort_flag, 130);
         if (!ok) break;
         tc_fence_after();
         if (elect_lane()) {
           const int steps = (ny + 15) >> 4;
           const uint64_t y1 = mndesc(su32(y), C::YBOX);
-          if (KV) {
-            const uint32_t w = tmem + (g % BUF) * 2 * YT;
-            sum_ts(tmem + C::ACC + 64 * NB, w, y1 + (C::UNIT >> 4), id, steps, t > 0);
-            sum_ts(tmem + C::ACC, w + YT, y1, id, steps, t > 0);
-          } else {
-            sum_ts(tmem + C::ACC, tmem + C::DS + (g % BUF) * (YT / 2), y1, id, steps, t > 0);
-          }
-          mma_commit(&S.done[g & 1]);
+          const uint32_t w = tmem + b * 2 * YT;
+          sum_ts(tmem + C::ACC + 64 * NB, w, y1 + (KV ? C::UNIT >> 4 : 0), id, steps, t > 0);
+          sum_ts(tmem + C::ACC, w + YT, y1, id, steps, t > 0);
+          mma_commit(&S.done[b]);
           mma_commit(&S.y_empty[s]);
           if (t == nt - 1) mma_commit(&S.acc_full);
         }
         __syncwarp();
         if (++s == KP) s = 0, ph ^= 1;
+        if (++b == BUF) b = 0, pb ^= 1;
       }
       ++nload;
     }
@@ -413,13 +406,14 @@ __global__ void __launch_bounds__(TcBwd<KV, NB>::THREADS, TcBwd<KV, NB>::CTAS)
     __syncwarp();
   } else {
     // ---------------- p, ds and the gradients: thread = row of X
-    const int buf = warp >> 2;                // tiles g with g % BUF == buf
+    const int buf = warp >> 2;                // every BUF-th tile, from the buf-th on
     const int quad = warp & 3, tid = threadIdx.x & 127;
     const uint32_t lane_off = (uint32_t)(32 * quad) << 16;
     const int row = 32 * quad + lane;
     const float c = p.scale * kLog2e;
     const float2 c2 = make_float2(c, c);
-    int g = 0, nload = 0, flip = 0;
+    int turn = 0, nload = 0;  // buffer of the next tile
+    uint32_t ps = 0, flip = 0, pcol = 0;
     bool ok = true;
 #pragma unroll 1
     for (int n = 0; ok; ++n) {
@@ -438,19 +432,21 @@ __global__ void __launch_bounds__(TcBwd<KV, NB>::THREADS, TcBwd<KV, NB>::CTAS)
         rl.x = ls == -INFINITY ? 0.f : -ls * kLog2e;  // (sees no key)
       }
       if (!KV && w.nt > 0) {
-        if (!wait_all(&S.o_full, nload & 1, abort_flag, 137) ||
-            !wait_all(&S.x_full, nload & 1, abort_flag, 138))
-          break;
-        if (in) rl.y = -row_delta<NB>(xbuf + 2 * NB * ABOX, xbuf + NB * ABOX, row, p.dim);
+        const int xs = nload % XS;
+        if (!wait_all(&S.x_full[xs], (nload / XS) & 1, abort_flag, 138)) break;
+        const uint8_t* x = xbuf + xs * C::XSET;
+        if (in) rl.y = -row_delta<NB>(x + 2 * NB * ABOX, x + NB * ABOX, row, p.dim);
         __syncwarp();
-        if (lane == 0) mbar_arrive(&S.o_empty);
+        if (lane == 0) mbar_arrive(&S.x_empty[xs]);
       }
       TileList list = w.list;
 #pragma unroll 1
-      for (int t = 0; t < w.nt; ++t, ++g, list.next(YT)) {
-        if (BUF == 2 && (g & 1) != buf) continue;
+      for (int t = 0; t < w.nt; ++t, list.next(YT)) {
+        const bool mine = turn == buf;
+        if (++turn == BUF) turn = 0;
+        if (!mine) continue;
         const int h = list.h, r = list.r, ny = list.rows(YT);
-        const uint32_t sp = tmem + lane_off + (g % BUF) * 2 * YT;  // S, then dP
+        const uint32_t sp = tmem + lane_off + buf * 2 * YT;  // S, then dP
         // In columns of the tile: the last that the warp's first row sees, the first
         // that its last row sees, and (over keys) the end of the first tokens.
         int wh, wl, sk = 0, up, low;  // up: no row sees a column past it; low: none before it
@@ -481,7 +477,8 @@ __global__ void __launch_bounds__(TcBwd<KV, NB>::THREADS, TcBwd<KV, NB>::CTAS)
           low = wl - 31;
         }
         const int end = 32 * quad < w.nx ? min(ny, up + 1) : 0;
-        if (!wait_all(&S.s_full[g & 1], (g >> 1) & 1, abort_flag, 132)) { ok = false; break; }
+        if (!wait_all(&S.s_full[buf], ps, abort_flag, 132)) { ok = false; break; }
+        ps ^= 1;
         tc_fence_after();
         const float* col = nullptr;
         if (KV) {
@@ -494,140 +491,117 @@ __global__ void __launch_bounds__(TcBwd<KV, NB>::THREADS, TcBwd<KV, NB>::CTAS)
           if (!wait_all(&S.col_full[buf], flip, abort_flag, 134)) { ok = false; break; }
           flip ^= 1;
         }
-        // A row whose keys all lie in one tile corrects delta before it is used.
 #pragma unroll 1
-        for (bool last = KV || w.nt > 1;; last = true) {
-#pragma unroll 1
-          for (int q = 0; q < ny; q += 32) {
-            uint32_t p16[16], d16[16];
-            const bool skip = q >= end || (q + 31 < low && (KV || q >= sk));
+        for (int q = 0; q < ny; q += 32) {
+          uint32_t p16[16], d16[16];
+          if (q >= end || (q + 31 < low && (KV || q >= sk))) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) p16[e] = d16[e] = 0u;
+          } else {
             float v[32], d[32];
-            if (!skip) {
-              tmem_ld32_async(sp + q, v);
-              tmem_ld32_async(sp + YT + q, d);
-              tmem_wait_ld();
-              tmem_landed(v);
-              tmem_landed(d);
-            }
-            if (!KV && q + 32 >= ny && last) {  // S and dP have been read
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&S.s_free[g & 1]);
-            }
-            if (skip) {
-#pragma unroll
-              for (int e = 0; e < 16; ++e) p16[e] = d16[e] = 0u;
-            } else {
-              if (q + 32 > min(ny, wh + 1) || (q < wl && (KV || q + 32 > sk))) {
-                uint32_t see;
-                if (KV) {
-                  const bool sink = w.r0 + row < w.sinks;
-                  see = bit_span(wl - 31 + lane - q, sink ? ny - 1 - q : min(ny - 1, wh + lane) - q);
-                } else {
-                  see = bit_span(0, min(ny - 1, wh + lane) - q) &
-                        (bit_span(wl - 31 + lane - q, 31) | bit_span(0, sk - 1 - q));
-                }
-#pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                  const bool vis = see & (1u << e);
-                  v[e] = vis ? v[e] : -INFINITY;
-                  d[e] = vis ? d[e] : 0.f;
-                }
+            tmem_ld32_async(sp + q, v);
+            tmem_ld32_async(sp + YT + q, d);
+            tmem_wait_ld();
+            tmem_landed(v);
+            tmem_landed(d);
+            if (q + 32 > min(ny, wh + 1) || (q < wl && (KV || q + 32 > sk))) {
+              uint32_t see;
+              if (KV) {
+                const bool sink = w.r0 + row < w.sinks;
+                see = bit_span(wl - 31 + lane - q, sink ? ny - 1 - q : min(ny - 1, wh + lane) - q);
+              } else {
+                see = bit_span(0, min(ny - 1, wh + lane) - q) &
+                      (bit_span(wl - 31 + lane - q, 31) | bit_span(0, sk - 1 - q));
               }
 #pragma unroll
-              for (int e = 0; e < 32; e += 4) {
-                float4 ml = make_float4(rl.x, rl.x, rl.x, rl.x);
-                float4 md = make_float4(rl.y, rl.y, rl.y, rl.y);
-                if (KV) {
-                  ml = *reinterpret_cast<const float4*>(col + q + e);
-                  md = *reinterpret_cast<const float4*>(col + YT + q + e);
-                }
-#pragma unroll
-                for (int f = 0; f < 4; f += 2) {
-                  const float2 z = fma2(make_float2(v[e + f], v[e + f + 1]), c2,
-                                        f ? make_float2(ml.z, ml.w) : make_float2(ml.x, ml.y));
-                  const float2 y = make_float2(ex2(z.x), ex2(z.y));
-                  const float2 dd = add2(make_float2(d[e + f], d[e + f + 1]),
-                                         f ? make_float2(md.z, md.w) : make_float2(md.x, md.y));
-                  const float2 x = mul2(y, dd);
-                  if (!KV) ds2 = add2(ds2, x);
-                  if (KV) p16[(e + f) >> 1] = pack_bf16(y.x, y.y);
-                  d16[(e + f) >> 1] = pack_bf16(x.x, x.y);
-                }
+              for (int e = 0; e < 32; ++e) {
+                const bool vis = see & (1u << e);
+                v[e] = vis ? v[e] : -INFINITY;
+                d[e] = vis ? d[e] : 0.f;
               }
             }
-            if (!last) continue;
-            if (KV) {  // over the pieces of S and dP that have been read
-              tmem_st16(sp + (q >> 1), p16);
-              tmem_st16(sp + YT + (q >> 1), d16);
-            } else {
-              // the sums of the tile before have read its ds
-              if (q == 0 && g >= BUF &&
-                  !wait_all(&S.done[(g - BUF) & 1], ((g - BUF) >> 1) & 1, abort_flag, 136)) {
-                ok = false;
-                break;
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              float4 ml = make_float4(rl.x, rl.x, rl.x, rl.x);
+              float4 md = make_float4(rl.y, rl.y, rl.y, rl.y);
+              if (KV) {
+                ml = *reinterpret_cast<const float4*>(col + q + e);
+                md = *reinterpret_cast<const float4*>(col + YT + q + e);
               }
-              tmem_st16(tmem + lane_off + C::DS + buf * (YT / 2) + (q >> 1), d16);
+#pragma unroll
+              for (int f = 0; f < 4; f += 2) {
+                const float2 z = fma2(make_float2(v[e + f], v[e + f + 1]), c2,
+                                      f ? make_float2(ml.z, ml.w) : make_float2(ml.x, ml.y));
+                const float2 y = make_float2(ex2(z.x), ex2(z.y));
+                const float2 dd = add2(make_float2(d[e + f], d[e + f + 1]),
+                                       f ? make_float2(md.z, md.w) : make_float2(md.x, md.y));
+                const float2 x = mul2(y, dd);
+                if (!KV) ds2 = add2(ds2, x);
+                p16[(e + f) >> 1] = pack_bf16(y.x, y.y);
+                d16[(e + f) >> 1] = pack_bf16(x.x, x.y);
+              }
             }
           }
-          if (last) break;
-          rl.y -= ds2.x + ds2.y;
-          ds2 = make_float2(0.f, 0.f);
+          // over the pieces of S and dP that have been read
+          tmem_st16(sp + (q >> 1), p16);
+          tmem_st16(sp + YT + (q >> 1), d16);
         }
-        if (!ok) break;
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&S.p_full[g & 1]);
+        if (lane == 0) mbar_arrive(&S.p_full[buf]);
       }
       if (!ok) break;
-      // The gradients of the row.  One buffer: all of them; two: half of dq's
-      // channels each, or dk and dv.
-      constexpr int NACC = KV ? 2 : 1;
+      // The gradients of the row: dk by the first buffer's warps and dv by the
+      // second's, or half of dq's channels by each of the two.
       if (w.nt > 0) {
         if (!wait_all(&S.acc_full, nload & 1, abort_flag, 133)) break;
         tc_fence_after();
         ++nload;
       }
-      if (!KV) {
-        float delta = ds2.x + ds2.y - (buf == 0 ? rl.y : 0.f);
-        if (BUF == 2 && w.nt > 1) {  // the other buffer's tiles
-          // (written again only after the next sums, which wait for acc_free)
-          if (buf == 1) {
-            S.half[row] = delta;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&S.col_full[0]);
-          } else {
-            if (!wait_all(&S.col_full[0], flip, abort_flag, 135)) break;
-            flip ^= 1;
-            delta += S.half[row];
-          }
-        }
-        // of a single tile, the warps that had it know the sum
-        if (w.nt == 1 && BUF == 2 && buf == 1) delta -= rl.y;
-        if (in && buf == (w.nt == 1 ? (g - 1) % BUF : 0))
-          p.delta[(int64_t)w.hx * p.Tq + xr] = delta;
+      float err = 0.f;  // sum of the row's ds
+      if (!KV && w.nt > 0) {
+        // (written again only after the next sums, which wait for acc_free)
+        S.half[buf][row] = ds2.x + ds2.y;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.half_full);
+        if (!wait_all(&S.half_full, pcol, abort_flag, 135)) break;
+        pcol ^= 1;
+#pragma unroll
+        for (int i = 0; i < BUF; ++i) err += S.half[i][row];
       }
-      const int a0 = KV && BUF == 2 ? buf : 0, a1 = KV && BUF == 2 ? buf + 1 : NACC;
-      const int d0 = !KV && BUF == 2 ? 64 * buf : 0;
-      const int d1 = !KV && BUF == 2 ? min(p.dim, 64 * buf + 64) : p.dim;
-#pragma unroll 1
-      for (int a = a0; a < a1; ++a) {
-        const Heads& out = KV ? (a ? p.dv : p.dk) : p.dq;
-        const float mul = a ? 1.f : p.scale;
+      if (!KV && in && buf == 0) p.delta[(int64_t)w.hx * p.Tq + xr] = err - rl.y;
+      if (buf < 2) {
+        const Heads& out = KV ? (buf ? p.dv : p.dk) : p.dq;
+        const float mul = KV && buf ? 1.f : p.scale;
+        const float back = -mul * err;
         const bool wide = wide_rows(out);
+        const uint32_t acc = tmem + lane_off + C::ACC + (KV ? buf * 64 * NB : 0);
         __nv_bfloat16* dst = out.at<__nv_bfloat16>(xr, w.hx);
-        float* part = cut.parts + (((int64_t)w.slot * 2 + a) * AT + row) * p.dim;
+        float* part = cut.parts + (((int64_t)w.slot * 2 + buf) * AT + row) * p.dim;
+        const int d0 = KV ? 0 : buf * 32 * NB, d1 = KV ? p.dim : min(p.dim, d0 + 32 * NB);
 #pragma unroll 1
         for (int d = d0; d < d1; d += 32) {
           float o[32];
           if (w.nt > 0) {
-            tmem_ld32_async(tmem + lane_off + C::ACC + a * 64 * NB + d, o);
-            tmem_wait_ld();
-            tmem_landed(o);
-          }
+            tmem_ld32_async(acc + d, o);
+            if (KV) {
+              tmem_wait_ld();
+              tmem_landed(o);
+            } else {  // - scale e P K
+              float m[32];
+              tmem_ld32_async(acc + 64 * NB + d, m);
+              tmem_wait_ld();
+              tmem_landed(o);
+              tmem_landed(m);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = w.nt > 0 ? o[e] * mul : 0.f;
+              for (int e = 0; e < 32; ++e) o[e] = fmaf(m[e], back, o[e] * mul);
+            }
+          }
+          if (KV || w.nt == 0) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = w.nt > 0 ? o[e] * mul : 0.f;
+          }
           if (!in) continue;
           if (KV && w.slot >= 0) {
 #pragma unroll
@@ -720,8 +694,8 @@ BwdCut bwd_cut(const AttnPlan& P, const tt_attn_seqs* s, int64_t* slots) {
     if (l < list) list = l;
   }
   // a lead tile: pieces of about another tile's length; every tile: enough
-  // pieces to reach the SMs' CTAs once
-  const int64_t ctas = (int64_t)device_sms() * (P.dim <= 64 ? 2 : 1);
+  // pieces to reach the SMs once
+  const int64_t ctas = device_sms();
   const int64_t items = (int64_t)c.tiles * P.kv * s->B;
   int64_t cut = items > 0 && items < ctas ? ctas / items : 1;
   if (cut > list / 4) cut = list / 4;  // no piece under four tiles
@@ -746,7 +720,7 @@ size_t bwd_parts_bytes(const AttnPlan& P, const tt_attn_seqs* s) {
 template <bool KV, int NB>
 cudaError_t tc_bwd_go(const AttnArgs& p, const BwdCut& cut, cudaStream_t st) {
   using C = TcBwd<KV, NB>;
-  static_assert(C::CTAS * (C::kSmem + 1024) <= 228 * 1024, "CTAs an SM");
+  static_assert(C::kSmem <= 227 * 1024, "shared memory of the attention backward");
   static PerDevice once;
   cudaError_t e = once.get([] {
     return cudaFuncSetAttribute(attn_bwd_tc<KV, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
