@@ -28,7 +28,8 @@
 // softmax (1 us), sums (0.3 us), 2.2 us with the waits between, so the one CTA of
 // an SM keeps as many tiles in turn as the tensor memory holds: three buffers
 // of S and dP for heads of up to 64 channels, two for wider ones, each with its
-// own four softmax warps.
+// own four softmax warps.  Four more warps write the gradients, so that the
+// softmax goes on with the next item meanwhile.
 //
 // The pass over keys: the first tokens are seen by every later query, so their
 // tile is cut into pieces of its list of query tiles, each the work of one
@@ -70,17 +71,17 @@ struct TcBwd {
   static constexpr int YBOX = YT * 128, UNIT = NB * YBOX, XSET = NX * NB * ABOX;
   static constexpr uint32_t ACC = BUF * 2 * YT, COLS = 512;
   static constexpr int WARPS = 4 * BUF;           // softmax warps
-  static constexpr int THREADS = 32 * (WARPS + 3);
+  static constexpr int THREADS = 32 * (WARPS + 7);        // and four that write, three that issue
   struct Shared {
     uint64_t x_full[XS], x_empty[XS], y_full[KP], y_empty[KP];
     uint64_t s_full[BUF], p_full[BUF], done[BUF], acc_full, acc_free, fin, fin2;
     uint64_t item_full[ITEMS], item_empty[ITEMS], clc;
-    uint64_t col_full[BUF], half_full;
+    uint64_t col_full[BUF], half_full[2], half_free[2];  // [item & 1]
     BwdItem item[ITEMS];
     uint4 answer;
     int rows[KP];  // rows of the pair's tile
     alignas(16) float col[KV ? BUF : 1][2][2][KV ? YT : 4];  // lse and delta of a tile's queries
-    float half[KV ? 1 : BUF][KV ? 1 : AT];  // each buffer's sums of ds
+    float half[2][KV ? 1 : BUF + 1][KV ? 1 : AT];  // each buffer's sums of ds, then delta
     uint32_t tmem;
     int abort_flag, never;
   };
@@ -200,17 +201,19 @@ __global__ void __launch_bounds__(TcBwd<KV, NB>::THREADS, 1)
     }
 #pragma unroll 1
     for (int i = 0; i < C::ITEMS; ++i)
-      mbar_init(&S.item_full[i], 1), mbar_init(&S.item_empty[i], WARPS + 2);
-    mbar_init(&S.half_full, WARPS);
+      mbar_init(&S.item_full[i], 1), mbar_init(&S.item_empty[i], WARPS + 6);
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i)
+      mbar_init(&S.half_full[i], WARPS), mbar_init(&S.half_free[i], 4);
     mbar_init(&S.acc_full, 1);
-    mbar_init(&S.acc_free, WARPS);
+    mbar_init(&S.acc_free, 4);
     mbar_init(&S.clc, 1);
     mbar_init(&S.fin, 1);
     mbar_init(&S.fin2, 1);
     S.abort_flag = S.never = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == WARPS + 1) tmem_take(&S.tmem, C::COLS);
+  if (warp == WARPS + 5) tmem_take(&S.tmem, C::COLS);
   pdl_wait();
   pdl_trigger();
   tc_fence_before();
@@ -219,7 +222,7 @@ __global__ void __launch_bounds__(TcBwd<KV, NB>::THREADS, 1)
   const uint32_t tmem = S.tmem;
   volatile int* abort_flag = &S.abort_flag;
 
-  if (warp == WARPS) {
+  if (warp == WARPS + 4) {
     // ---------------- work and loads
     if (lane == 0) {
       int n = 0, nload = 0, s = 0, loads = 0;
@@ -312,7 +315,7 @@ __global__ void __launch_bounds__(TcBwd<KV, NB>::THREADS, 1)
         drain_one(&S.y_full[s], ph ^ 1);  // the last load into pair s
       }
     }
-  } else if (warp == WARPS + 1) {
+  } else if (warp == WARPS + 5) {
     // ---------------- S and dP of every tile
     const int ksteps = (p.dim + 15) >> 4;
     int nload = 0, s = 0, b = 0;
@@ -356,7 +359,7 @@ __global__ void __launch_bounds__(TcBwd<KV, NB>::THREADS, 1)
       drain_one(&S.fin, 0);
     }
     __syncwarp();
-  } else if (warp == WARPS + 2) {
+  } else if (warp == WARPS + 6) {
     // ---------------- the sums
     const uint32_t id = idesc(128, ((p.dim + 15) >> 4) * 16, 0, 1);
     int nload = 0, s = 0, b = 0;
@@ -404,8 +407,8 @@ __global__ void __launch_bounds__(TcBwd<KV, NB>::THREADS, 1)
       drain_one(&S.fin2, 0);
     }
     __syncwarp();
-  } else {
-    // ---------------- p, ds and the gradients: thread = row of X
+  } else if (warp < WARPS) {
+    // ---------------- p and ds: thread = row of X
     const int buf = warp >> 2;                // every BUF-th tile, from the buf-th on
     const int quad = warp & 3, tid = threadIdx.x & 127;
     const uint32_t lane_off = (uint32_t)(32 * quad) << 16;
@@ -413,7 +416,7 @@ __global__ void __launch_bounds__(TcBwd<KV, NB>::THREADS, 1)
     const float c = p.scale * kLog2e;
     const float2 c2 = make_float2(c, c);
     int turn = 0, nload = 0;  // buffer of the next tile
-    uint32_t ps = 0, flip = 0, pcol = 0;
+    uint32_t ps = 0, flip = 0;
     bool ok = true;
 #pragma unroll 1
     for (int n = 0; ok; ++n) {
@@ -423,12 +426,11 @@ __global__ void __launch_bounds__(TcBwd<KV, NB>::THREADS, 1)
       if (lane == 0) mbar_arrive(&S.item_empty[n % C::ITEMS]);
       if (w.nt < 0) break;
       const bool in = row < w.nx;
-      const int64_t xr = w.x0 + w.r0 + row;   // the thread's row
       const int xw = w.r0 + 32 * quad + (KV ? 0 : w.off);  // position of the warp's first row
       float2 rl = make_float2(0.f, 0.f);      // - lse (in powers of two) and - delta of the row
       float2 ds2 = make_float2(0.f, 0.f);     // sum of the row's ds
       if (!KV && in) {
-        const float ls = p.lse_in[(int64_t)w.hx * p.Tq + xr];
+        const float ls = p.lse_in[(int64_t)w.hx * p.Tq + w.x0 + w.r0 + row];
         rl.x = ls == -INFINITY ? 0.f : -ls * kLog2e;  // (sees no key)
       }
       if (!KV && w.nt > 0) {
@@ -491,20 +493,21 @@ __global__ void __launch_bounds__(TcBwd<KV, NB>::THREADS, 1)
           if (!wait_all(&S.col_full[buf], flip, abort_flag, 134)) { ok = false; break; }
           flip ^= 1;
         }
+        // 16 columns at a time: more would not fit the registers of as many warps
 #pragma unroll 1
-        for (int q = 0; q < ny; q += 32) {
-          uint32_t p16[16], d16[16];
-          if (q >= end || (q + 31 < low && (KV || q >= sk))) {
+        for (int q = 0; q < ny; q += 16) {
+          uint32_t p8[8], d8[8];
+          if (q >= end || (q + 15 < low && (KV || q >= sk))) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) p16[e] = d16[e] = 0u;
+            for (int e = 0; e < 8; ++e) p8[e] = d8[e] = 0u;
           } else {
-            float v[32], d[32];
-            tmem_ld32_async(sp + q, v);
-            tmem_ld32_async(sp + YT + q, d);
+            float v[16], d[16];
+            tmem_ld16_async(sp + q, v);
+            tmem_ld16_async(sp + YT + q, d);
             tmem_wait_ld();
             tmem_landed(v);
             tmem_landed(d);
-            if (q + 32 > min(ny, wh + 1) || (q < wl && (KV || q + 32 > sk))) {
+            if (q + 16 > min(ny, wh + 1) || (q < wl && (KV || q + 16 > sk))) {
               uint32_t see;
               if (KV) {
                 const bool sink = w.r0 + row < w.sinks;
@@ -514,14 +517,14 @@ __global__ void __launch_bounds__(TcBwd<KV, NB>::THREADS, 1)
                       (bit_span(wl - 31 + lane - q, 31) | bit_span(0, sk - 1 - q));
               }
 #pragma unroll
-              for (int e = 0; e < 32; ++e) {
+              for (int e = 0; e < 16; ++e) {
                 const bool vis = see & (1u << e);
                 v[e] = vis ? v[e] : -INFINITY;
                 d[e] = vis ? d[e] : 0.f;
               }
             }
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) {
+            for (int e = 0; e < 16; e += 4) {
               float4 ml = make_float4(rl.x, rl.x, rl.x, rl.x);
               float4 md = make_float4(rl.y, rl.y, rl.y, rl.y);
               if (KV) {
@@ -537,14 +540,14 @@ __global__ void __launch_bounds__(TcBwd<KV, NB>::THREADS, 1)
                                        f ? make_float2(md.z, md.w) : make_float2(md.x, md.y));
                 const float2 x = mul2(y, dd);
                 if (!KV) ds2 = add2(ds2, x);
-                p16[(e + f) >> 1] = pack_bf16(y.x, y.y);
-                d16[(e + f) >> 1] = pack_bf16(x.x, x.y);
+                p8[(e + f) >> 1] = pack_bf16(y.x, y.y);
+                d8[(e + f) >> 1] = pack_bf16(x.x, x.y);
               }
             }
           }
           // over the pieces of S and dP that have been read
-          tmem_st16(sp + (q >> 1), p16);
-          tmem_st16(sp + YT + (q >> 1), d16);
+          tmem_st8(sp + (q >> 1), p8);
+          tmem_st8(sp + YT + (q >> 1), d8);
         }
         tmem_wait_st();
         tc_fence_before();
@@ -552,55 +555,80 @@ __global__ void __launch_bounds__(TcBwd<KV, NB>::THREADS, 1)
         if (lane == 0) mbar_arrive(&S.p_full[buf]);
       }
       if (!ok) break;
-      // The gradients of the row: dk by the first buffer's warps and dv by the
-      // second's, or half of dq's channels by each of the two.
       if (w.nt > 0) {
+        if (!KV) {  // for the warps that write
+          const int half = nload & 1;
+          if (!wait_all(&S.half_free[half], ((nload >> 1) & 1) ^ 1, abort_flag, 134)) break;
+          S.half[half][buf][row] = ds2.x + ds2.y;
+          if (buf == 0) S.half[half][KV ? 0 : BUF][row] = -rl.y;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&S.half_full[half]);
+        }
+        ++nload;
+      }
+    }
+  } else {
+    // ---------------- the gradients
+    const int quad = warp & 3, row = 32 * quad + lane;
+    const uint32_t acc = tmem + ((uint32_t)(32 * quad) << 16) + C::ACC;
+    int nload = 0;
+#pragma unroll 1
+    for (int n = 0;; ++n) {
+      if (!wait_all(&S.item_full[n % C::ITEMS], (n / C::ITEMS) & 1, abort_flag, 141)) break;
+      const BwdItem w = S.item[n % C::ITEMS];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.item_empty[n % C::ITEMS]);
+      if (w.nt < 0) break;
+      const bool in = row < w.nx, some = w.nt > 0;
+      const int64_t xr = w.x0 + w.r0 + row;
+      float err = 0.f, delta = 0.f;  // sum of the row's ds
+      if (!KV && some) {
+        const int half = nload & 1;
+        if (!wait_all(&S.half_full[half], (nload >> 1) & 1, abort_flag, 135)) break;
+#pragma unroll
+        for (int i = 0; i < BUF; ++i) err += S.half[half][KV ? 0 : i][row];
+        delta = S.half[half][KV ? 0 : BUF][row] + err;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.half_free[half]);
+      }
+      if (!KV && in) p.delta[(int64_t)w.hx * p.Tq + xr] = delta;
+      if (some) {
         if (!wait_all(&S.acc_full, nload & 1, abort_flag, 133)) break;
         tc_fence_after();
         ++nload;
       }
-      float err = 0.f;  // sum of the row's ds
-      if (!KV && w.nt > 0) {
-        // (written again only after the next sums, which wait for acc_free)
-        S.half[buf][row] = ds2.x + ds2.y;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&S.half_full);
-        if (!wait_all(&S.half_full, pcol, abort_flag, 135)) break;
-        pcol ^= 1;
-#pragma unroll
-        for (int i = 0; i < BUF; ++i) err += S.half[i][row];
-      }
-      if (!KV && in && buf == 0) p.delta[(int64_t)w.hx * p.Tq + xr] = err - rl.y;
-      if (buf < 2) {
-        const Heads& out = KV ? (buf ? p.dv : p.dk) : p.dq;
-        const float mul = KV && buf ? 1.f : p.scale;
-        const float back = -mul * err;
-        const bool wide = wide_rows(out);
-        const uint32_t acc = tmem + lane_off + C::ACC + (KV ? buf * 64 * NB : 0);
-        __nv_bfloat16* dst = out.at<__nv_bfloat16>(xr, w.hx);
-        float* part = cut.parts + (((int64_t)w.slot * 2 + buf) * AT + row) * p.dim;
-        const int d0 = KV ? 0 : buf * 32 * NB, d1 = KV ? p.dim : min(p.dim, d0 + 32 * NB);
+      // dk = scale acc0 and dv = acc1, or dq = scale (acc0 - err acc1)
 #pragma unroll 1
-        for (int d = d0; d < d1; d += 32) {
+      for (int a = 0; a < (KV ? 2 : 1); ++a) {
+        const Heads& out = KV ? (a ? p.dv : p.dk) : p.dq;
+        const float mul = a ? 1.f : p.scale, back = -mul * err;
+        const bool wide = wide_rows(out);
+        __nv_bfloat16* dst = out.at<__nv_bfloat16>(xr, w.hx);
+        float* part = cut.parts + (((int64_t)w.slot * 2 + a) * AT + row) * p.dim;
+#pragma unroll 1
+        for (int d = 0; d < p.dim; d += 32) {
           float o[32];
-          if (w.nt > 0) {
-            tmem_ld32_async(acc + d, o);
-            if (KV) {
-              tmem_wait_ld();
-              tmem_landed(o);
-            } else {  // - scale e P K
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0.f;
+          if (some) {
+            tmem_ld32_async(acc + a * 64 * NB + d, o);
+            tmem_wait_ld();
+            tmem_landed(o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] *= mul;
+            if (!KV) {
               float m[32];
               tmem_ld32_async(acc + 64 * NB + d, m);
               tmem_wait_ld();
-              tmem_landed(o);
               tmem_landed(m);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = fmaf(m[e], back, o[e] * mul);
+              for (int e = 0; e < 32; ++e) o[e] = fmaf(m[e], back, o[e]);
             }
-          }
-          if (KV || w.nt == 0) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = w.nt > 0 ? o[e] * mul : 0.f;
+            if (d + 32 >= p.dim && (!KV || a)) {  // the accumulators have been read
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&S.acc_free);
+            }
           }
           if (!in) continue;
           if (KV && w.slot >= 0) {
@@ -614,17 +642,12 @@ __global__ void __launch_bounds__(TcBwd<KV, NB>::THREADS, 1)
           }
         }
       }
-      if (w.nt > 0) {  // the accumulators have been read
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&S.acc_free);
-      }
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == WARPS + 1) tmem_give(tmem, C::COLS);
+  if (warp == WARPS + 5) tmem_give(tmem, C::COLS);
 }
 
 // dk and dv of the key tiles that were worked on in pieces: the pieces' sums
