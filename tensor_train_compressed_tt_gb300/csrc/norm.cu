@@ -37,19 +37,18 @@ struct Raw<float, 1> {
   __device__ void set(const float* f) { v = f[0]; }
 };
 template <>
-struct Raw<__nv_bfloat16, 8> {
-  uint4 v;
+struct Raw<__nv_bfloat16, 4> {
+  uint2 v;
   __device__ void get(float* f) const {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    const uint32_t w[2] = {v.x, v.y};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {  // a bf16 is the upper half of its f32
+    for (int i = 0; i < 2; ++i) {  // a bf16 is the upper half of its f32
       f[2 * i] = __uint_as_float(w[i] << 16);
       f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
     }
   }
   __device__ void set(const float* f) {
-    v = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
-                   pack_bf16(f[6], f[7]));
+    v = make_uint2(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]));
   }
 };
 template <>
@@ -59,21 +58,62 @@ struct Raw<__nv_bfloat16, 1> {
   __device__ void set(const float* f) { v = __float2bfloat16_rn(f[0]); }
 };
 
-// Sum over the G = 32 W threads of a group, in a fixed order; every thread
-// gets it.  `slot` alternates between two shared rows so that one barrier a
-// reduction is enough.
-template <int W>
-__device__ __forceinline__ float group_sum(float v, float (*red)[32], int slot) {
+// VEC values of gamma or beta (`other` where there is none).  Four in one load
+// when the array is 16-byte aligned: a warp's loads then cover whole lines of
+// the L1, which holds the array for every row but the first.
+template <int VEC>
+__device__ __forceinline__ void weights_at(const float* w, int j, float other, bool aligned,
+                                           float* f) {
+  if (!w) {
 #pragma unroll
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if (W == 1) return v;
+    for (int i = 0; i < VEC; ++i) f[i] = other;
+  } else if (VEC == 4 && aligned) {
+    const float4 v = __ldg(reinterpret_cast<const float4*>(w + j));
+    f[0] = v.x;
+    f[VEC > 1 ? 1 : 0] = v.y;
+    f[VEC > 2 ? 2 : 0] = v.z;
+    f[VEC > 3 ? 3 : 0] = v.w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) f[i] = __ldg(w + j + i);
+  }
+}
+
+// The barrier of one group of W warps among the block's groups.
+template <int W, int GROUPS>
+__device__ __forceinline__ void group_sync(int group) {
+  if (GROUPS == 1)
+    __syncthreads();
+  else
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(32 * W) : "memory");
+}
+
+// Sums of two values over the G = 32 W threads of a group, in a fixed order;
+// every thread gets them.  `slot` alternates between shared rows so that one
+// barrier a call is enough.
+template <int W, int GROUPS>
+__device__ __forceinline__ float2 group_sum2(float a, float b, float2 (*red)[32], int slot,
+                                             int group) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    a += __shfl_xor_sync(0xffffffffu, a, o);
+    b += __shfl_xor_sync(0xffffffffu, b, o);
+  }
+  if (W == 1) return make_float2(a, b);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (lane == 0) red[slot][warp] = v;
-  __syncthreads();
-  float t = lane < W ? red[slot][lane] : 0.f;
+  if (lane == 0) red[slot][warp] = make_float2(a, b);
+  group_sync<W, GROUPS>(group);
+  float2 t = lane < W ? red[slot][group * W + lane] : make_float2(0.f, 0.f);
 #pragma unroll
-  for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+  for (int o = 16; o; o >>= 1) {
+    t.x += __shfl_xor_sync(0xffffffffu, t.x, o);
+    t.y += __shfl_xor_sync(0xffffffffu, t.y, o);
+  }
   return t;
+}
+template <int W>
+__device__ __forceinline__ float group_sum(float v, float2 (*red)[32], int slot) {
+  return group_sum2<W, 1>(v, 0.f, red, slot, 0).x;
 }
 
 struct NormFwdArgs {
@@ -87,6 +127,7 @@ struct NormFwdArgs {
   void* sum;
   void* y;
   float2* stats;
+  int gamma16, beta16;  // 16-byte aligned
 };
 
 struct NormBwdArgs {
@@ -103,6 +144,7 @@ struct NormBwdArgs {
   float* dgamma;  // written directly when the grid is one block (parts unused)
   float* dbeta;
   int accumulate;
+  int gamma16;  // 16-byte aligned
 };
 
 constexpr int kRowWarps = 8;  // rows side by side in a block when a warp holds a row
@@ -114,7 +156,7 @@ __global__ void __launch_bounds__(W == 1 ? 32 * kRowWarps : 32 * W)
     norm_fwd_kernel(NormFwdArgs p) {
   using R = Raw<T, VEC>;
   constexpr int G = 32 * W;
-  __shared__ float red[2][32];
+  __shared__ float2 red[2][32];
   const int tid = W == 1 ? threadIdx.x & 31 : threadIdx.x;
   const int per_block = W == 1 ? kRowWarps : 1;
   const int64_t step = (int64_t)gridDim.x * per_block;
@@ -180,14 +222,11 @@ __global__ void __launch_bounds__(W == 1 ? 32 * kRowWarps : 32 * W)
           o.set(v + c * VEC);
           *reinterpret_cast<R*>(so + j) = o;
         }
-        float f[VEC];
+        float f[VEC], g[VEC], b[VEC];
+        weights_at<VEC>(p.gamma, j, 1.f, p.gamma16, g);
+        weights_at<VEC>(p.beta, j, 0.f, p.beta16, b);
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          // gamma and beta come from the L1 for every row but the first
-          const float g = p.gamma ? __ldg(p.gamma + j + i) : 1.f;
-          const float b = p.beta ? __ldg(p.beta + j + i) : 0.f;
-          f[i] = fmaf((v[c * VEC + i] - mean) * rstd, g, b);
-        }
+        for (int i = 0; i < VEC; ++i) f[i] = fmaf((v[c * VEC + i] - mean) * rstd, g[i], b[i]);
         o.set(f);
         *reinterpret_cast<R*>(y + j) = o;
       }
@@ -200,17 +239,19 @@ __device__ __forceinline__ void put_sum(float* out, int j, float v, int accumula
   if (out) out[j] = accumulate ? out[j] + v : v;
 }
 
+// Groups of W warps side by side in a block of the backward.
+__host__ __device__ constexpr int bwd_groups(int W) { return W < kRowWarps ? kRowWarps / W : 1; }
+
 template <typename T, int VEC, int CH, int W>
-__global__ void __launch_bounds__(W == 1 ? 32 * kRowWarps : 32 * W)
+__global__ void __launch_bounds__(32 * W * bwd_groups(W), W <= 8 ? 2 : 1)
     norm_bwd_kernel(NormBwdArgs p) {
   using R = Raw<T, VEC>;
-  constexpr int G = 32 * W, E = CH * VEC;
-  __shared__ float red[4][32];
-  __shared__ float cross[W == 1 ? kRowWarps * 32 * E * 2 : 1];
-  const int tid = W == 1 ? threadIdx.x & 31 : threadIdx.x;
-  const int per_block = W == 1 ? kRowWarps : 1;
-  const int64_t step = (int64_t)gridDim.x * per_block;
-  int64_t row = (int64_t)blockIdx.x * per_block + (W == 1 ? threadIdx.x >> 5 : 0);
+  constexpr int G = 32 * W, E = CH * VEC, GROUPS = bwd_groups(W);
+  __shared__ float2 red[2][32];
+  __shared__ float cross[GROUPS > 1 ? 2 * G * E : 1];
+  const int group = threadIdx.x / G, tid = threadIdx.x % G;
+  const int64_t step = (int64_t)gridDim.x * GROUPS;
+  int64_t row = (int64_t)blockIdx.x * GROUPS + group;
   const int N = p.N;
   R rs[CH], rd[CH], ru[CH];
   float2 st = make_float2(0.f, 0.f);
@@ -236,7 +277,7 @@ __global__ void __launch_bounds__(W == 1 ? 32 * kRowWarps : 32 * W)
   };
   int flip = 0;
   if (row < p.T) fetch(row);
-  for (; row < p.T; row += step, flip ^= 2) {
+  for (; row < p.T; row += step, flip ^= 1) {
     float h[E], g[E];  // normalised values; dy gamma
     R us[CH];
     float sg = 0.f, sgh = 0.f;
@@ -246,6 +287,8 @@ __global__ void __launch_bounds__(W == 1 ? 32 * kRowWarps : 32 * W)
       const int j = (c * G + tid) * VEC;
       us[c] = ru[c];
       if (j < N) {
+        float w[VEC];
+        weights_at<VEC>(p.gamma, j, 1.f, p.gamma16, w);
         rs[c].get(h + c * VEC);
         rd[c].get(g + c * VEC);
 #pragma unroll
@@ -254,35 +297,15 @@ __global__ void __launch_bounds__(W == 1 ? 32 * kRowWarps : 32 * W)
           h[e] = (h[e] - ms.x) * ms.y;
           dg[e] = fmaf(g[e], h[e], dg[e]);
           db[e] += g[e];
-          if (p.gamma) g[e] *= __ldg(p.gamma + j + i);
+          g[e] *= w[i];
           sg += g[e];
           sgh = fmaf(g[e], h[e], sgh);
         }
       }
     }
     if (row + step < p.T) fetch(row + step);
-    // both sums behind one barrier
-    if (W == 1) {
-      sg = group_sum<1>(sg, red, 0);
-      sgh = group_sum<1>(sgh, red, 0);
-    } else {
-#pragma unroll
-      for (int o = 16; o; o >>= 1) {
-        sg += __shfl_xor_sync(0xffffffffu, sg, o);
-        sgh += __shfl_xor_sync(0xffffffffu, sgh, o);
-      }
-      const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-      if (lane == 0) red[flip][warp] = sg, red[flip + 1][warp] = sgh;
-      __syncthreads();
-      sg = lane < W ? red[flip][lane] : 0.f;
-      sgh = lane < W ? red[flip + 1][lane] : 0.f;
-#pragma unroll
-      for (int o = 16; o; o >>= 1) {
-        sg += __shfl_xor_sync(0xffffffffu, sg, o);
-        sgh += __shfl_xor_sync(0xffffffffu, sgh, o);
-      }
-    }
-    const float a = sg / p.n, b = sgh / p.n;
+    const float2 t = group_sum2<W, GROUPS>(sg, sgh, red, flip, group);
+    const float a = t.x / p.n, b = t.y / p.n;
     T* dx = static_cast<T*>(p.dx) + row * N;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
@@ -301,43 +324,35 @@ __global__ void __launch_bounds__(W == 1 ? 32 * kRowWarps : 32 * W)
       }
     }
   }
-  // this block's share of the token sums
+  // this block's share of the token sums: the groups' in order
+  if (GROUPS > 1) {
+    for (int k = 0; k < GROUPS; ++k) {
+      if (group == k) {
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+          if (k > 0) dg[i] += cross[i * G + tid], db[i] += cross[(E + i) * G + tid];
+          cross[i * G + tid] = dg[i];
+          cross[(E + i) * G + tid] = db[i];
+        }
+      }
+      __syncthreads();
+    }
+    if (group != GROUPS - 1) return;
+  }
   const bool last = gridDim.x == 1;
   float* pg = p.parts + (size_t)blockIdx.x * 2 * N;
-  if (W == 1) {
-    const int warp = threadIdx.x >> 5;
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-      cross[((warp * 2) * E + i) * 32 + tid] = dg[i];
-      cross[((warp * 2 + 1) * E + i) * 32 + tid] = db[i];
-    }
-    __syncthreads();
-    for (int k = threadIdx.x; k < 2 * E * 32; k += blockDim.x) {
-      const int t = k & 31, i = (k >> 5) % E, which = k / (32 * E);
-      const int j = ((i / VEC) * 32 + t) * VEC + i % VEC;
-      if (j >= N) continue;
-      float v = 0.f;
+  for (int c = 0; c < CH; ++c) {
+    const int j = (c * G + tid) * VEC;
+    if (j < N) {
 #pragma unroll
-      for (int w = 0; w < kRowWarps; ++w) v += cross[((w * 2 + which) * E + i) * 32 + t];
-      if (last)
-        put_sum(which ? p.dbeta : p.dgamma, j, v, p.accumulate);
-      else
-        pg[which * N + j] = v;
-    }
-  } else {
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const int j = (c * G + tid) * VEC;
-      if (j < N) {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          if (last) {
-            put_sum(p.dgamma, j + i, dg[c * VEC + i], p.accumulate);
-            put_sum(p.dbeta, j + i, db[c * VEC + i], p.accumulate);
-          } else {
-            pg[j + i] = dg[c * VEC + i];
-            pg[N + j + i] = db[c * VEC + i];
-          }
+      for (int i = 0; i < VEC; ++i) {
+        if (last) {
+          put_sum(p.dgamma, j + i, dg[c * VEC + i], p.accumulate);
+          put_sum(p.dbeta, j + i, db[c * VEC + i], p.accumulate);
+        } else {
+          pg[j + i] = dg[c * VEC + i];
+          pg[N + j + i] = db[c * VEC + i];
         }
       }
     }
@@ -387,7 +402,7 @@ __device__ __forceinline__ void wide_put(void* p, int64_t i, float f) {
 // One block a row, the row read three times (from L2 after the first).
 template <typename T>
 __global__ void __launch_bounds__(kWideThreads) norm_fwd_wide_kernel(NormFwdArgs p) {
-  __shared__ float red[2][32];
+  __shared__ float2 red[2][32];
   pdl_wait();
   pdl_trigger();
   for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x) {
@@ -435,7 +450,7 @@ __global__ void __launch_bounds__(256) norm_cols_wide_kernel(NormBwdArgs p) {
 
 template <typename T>
 __global__ void __launch_bounds__(kWideThreads) norm_dx_wide_kernel(NormBwdArgs p) {
-  __shared__ float red[2][32];
+  __shared__ float2 red[2][32];
   pdl_wait();
   pdl_trigger();
   for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x) {
@@ -463,13 +478,19 @@ __global__ void __launch_bounds__(kWideThreads) norm_dx_wide_kernel(NormBwdArgs 
 // ---- dispatch --------------------------------------------------------------------
 constexpr int kMaxRegRow = 16384;  // widest row held in the registers of a block
 
-// Warps of a row, by its width.  Forward: 1024 values a warp.  Backward: its
-// accumulators double the registers, so 768 in one warp, then 512 a warp.
-int fwd_warps(int64_t N) { return N <= 1024 ? 1 : N <= 4096 ? 4 : 16; }
-int bwd_warps(int64_t N) {
-  if (N <= 768) return 1;
-  int w = 2;
+// Warps of a row, by its width.  Forward: 1024 values in one warp, else 512 a
+// warp.  Backward: 512, since its accumulators take as many registers again,
+// and 256 where the values come one by one (an address and a predicate each).
+int fwd_warps(int64_t N) {
+  if (N <= 1024) return 1;
+  int w = 4;
   while (N > 512 * w) w *= 2;
+  return w;
+}
+int bwd_warps(int64_t N) {
+  const int64_t per = N % 4 == 0 || N > 8192 ? 512 : 256;
+  int w = 1;
+  while (N > per * w) w *= 2;
   return w;
 }
 
@@ -478,26 +499,39 @@ int bwd_warps(int64_t N) {
 // sums would cost more than its few rows.
 int64_t bwd_blocks(int64_t N, int64_t T) {
   if (N > kMaxRegRow) return T < 64 ? (T < 1 ? 1 : T) : 64;  // row slices of the column sums
-  const int w = bwd_warps(N);
-  const int rows = w == 1 ? kRowWarps : 1;
-  const int per_sm = w == 1 ? 2 : w <= 4 ? 8 / w * 2 : w == 8 ? 2 : 1;
-  int64_t b = (T + rows - 1) / rows;
+  const int rows = bwd_groups(bwd_warps(N));
+  const int64_t b = (T + rows - 1) / rows;
   if (T <= 4 * rows) return 1;
-  const int64_t most = (int64_t)device_sms() * per_sm;
+  const int64_t most = (int64_t)device_sms() * (bwd_warps(N) <= 8 ? 2 : 1);
   return b < most ? b : most;
 }
 
 bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
 
+template <typename T, int VEC, int CH, int W, bool RES>
+cudaError_t fwd_launch(const NormFwdArgs& a, cudaStream_t st) {
+  constexpr int rows = W == 1 ? kRowWarps : 1, threads = W == 1 ? 32 * kRowWarps : 32 * W;
+  auto kernel = norm_fwd_kernel<T, VEC, CH, W, RES>;
+  // as many blocks as stay on the SMs, each taking rows in turn
+  static PerDevice once;
+  static int fit[kMaxDevices] = {};
+  int dev = 0;
+  const cudaError_t e = once.get([&] {
+    int d = 0, n = 0;
+    cudaError_t r = cudaGetDevice(&d);
+    if (r == cudaSuccess)
+      r = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, 0);
+    fit[d] = n > 0 ? n : 1;
+    return r;
+  });
+  if (e != cudaSuccess || cudaGetDevice(&dev) != cudaSuccess) return cudaErrorUnknown;
+  const int64_t need = (a.T + rows - 1) / rows, most = (int64_t)device_sms() * fit[dev];
+  return launch_ex(kernel, dim3((unsigned)(need < most ? need : most)), dim3(threads), 0, st,
+                   false, a);
+}
 template <typename T, int VEC, int CH, int W>
 cudaError_t fwd_go(const NormFwdArgs& a, cudaStream_t st) {
-  constexpr int rows = W == 1 ? kRowWarps : 1;
-  const int64_t need = (a.T + rows - 1) / rows;
-  const int64_t most = (int64_t)device_sms() * (W == 1 ? 4 : W == 4 ? 8 : 2);
-  const dim3 grid((unsigned)(need < most ? need : most));
-  const dim3 block(W == 1 ? 32 * kRowWarps : 32 * W);
-  return a.res ? launch_ex(norm_fwd_kernel<T, VEC, CH, W, true>, grid, block, 0, st, false, a)
-               : launch_ex(norm_fwd_kernel<T, VEC, CH, W, false>, grid, block, 0, st, false, a);
+  return a.res ? fwd_launch<T, VEC, CH, W, true>(a, st) : fwd_launch<T, VEC, CH, W, false>(a, st);
 }
 
 template <typename T, int V>
@@ -516,28 +550,31 @@ cudaError_t fwd_pick(const NormFwdArgs& a, cudaStream_t st) {
     if (e <= 24) return fwd_go<T, V, 24 / V, 1>(a, st);
     return fwd_go<T, V, 32 / V, 1>(a, st);
   }
-  if (w == 4) return e <= 16 ? fwd_go<T, V, 16 / V, 4>(a, st) : fwd_go<T, V, 32 / V, 4>(a, st);
-  return e <= 16 ? fwd_go<T, V, 16 / V, 16>(a, st) : fwd_go<T, V, 32 / V, 16>(a, st);
+  if (w == 4) return fwd_go<T, V, 16 / V, 4>(a, st);
+  if (w == 8) return fwd_go<T, V, 16 / V, 8>(a, st);
+  return w == 16 ? fwd_go<T, V, 16 / V, 16>(a, st) : fwd_go<T, V, 16 / V, 32>(a, st);
 }
 
 template <typename T, int VEC, int CH, int W>
 cudaError_t bwd_go(const NormBwdArgs& a, int64_t blocks, cudaStream_t st) {
   return launch_ex(norm_bwd_kernel<T, VEC, CH, W>, dim3((unsigned)blocks),
-                   dim3(W == 1 ? 32 * kRowWarps : 32 * W), 0, st, false, a);
+                   dim3(32 * W * bwd_groups(W)), 0, st, false, a);
 }
 
 template <typename T, int V>
 cudaError_t bwd_pick(const NormBwdArgs& a, int64_t blocks, cudaStream_t st) {
   const int N = a.N;
+  constexpr int E = V == 1 ? 8 : 16;  // values a thread
   switch (bwd_warps(N)) {
     case 1:
-      if (N <= 256) return bwd_go<T, V, 8 / V, 1>(a, blocks, st);
-      if (N <= 512) return bwd_go<T, V, 16 / V, 1>(a, blocks, st);
-      return bwd_go<T, V, 24 / V, 1>(a, blocks, st);
-    case 2: return bwd_go<T, V, 16 / V, 2>(a, blocks, st);
-    case 4: return bwd_go<T, V, 16 / V, 4>(a, blocks, st);
-    case 8: return bwd_go<T, V, 16 / V, 8>(a, blocks, st);
-    case 16: return bwd_go<T, V, 16 / V, 16>(a, blocks, st);
+      if (V > 1 && N <= 256) return bwd_go<T, V, 8 / V, 1>(a, blocks, st);
+      return bwd_go<T, V, E / V, 1>(a, blocks, st);
+    case 2:
+      if (V > 1 && N <= 768) return bwd_go<T, V, 12 / V, 2>(a, blocks, st);
+      return bwd_go<T, V, E / V, 2>(a, blocks, st);
+    case 4: return bwd_go<T, V, E / V, 4>(a, blocks, st);
+    case 8: return bwd_go<T, V, E / V, 8>(a, blocks, st);
+    case 16: return bwd_go<T, V, E / V, 16>(a, blocks, st);
     default: return bwd_go<T, V, 16 / V, 32>(a, blocks, st);
   }
 }
@@ -607,12 +644,14 @@ tt_status tt_norm_forward(const tt_plan_t* plan, int64_t T, const void* x, const
   a.sum = sum;
   a.y = y;
   a.stats = reinterpret_cast<float2*>(stats);
+  a.gamma16 = aligned_to(gamma, 16);
+  a.beta16 = aligned_to(beta, 16);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  // rows start 16-byte aligned only when the width fills 16-byte units
+  // rows start aligned to four values only when four divide the width
   prof_begin(kPhElem, st);
   const cudaError_t e =
       P.act == TT_DT_BF16
-          ? (P.N % 8 == 0 ? fwd_pick<__nv_bfloat16, 8>(a, st) : fwd_pick<__nv_bfloat16, 1>(a, st))
+          ? (P.N % 4 == 0 ? fwd_pick<__nv_bfloat16, 4>(a, st) : fwd_pick<__nv_bfloat16, 1>(a, st))
           : (P.N % 4 == 0 ? fwd_pick<float, 4>(a, st) : fwd_pick<float, 1>(a, st));
   prof_end(kPhElem, st);
   count_launches(1);
@@ -657,11 +696,12 @@ tt_status tt_norm_backward(const tt_plan_t* plan, int64_t T, const void* s, cons
   a.dgamma = dgamma;
   a.dbeta = dbeta;
   a.accumulate = acc;
+  a.gamma16 = aligned_to(gamma, 16);
   prof_begin(kPhElem, st);
   cudaError_t e;
   if (P.act == TT_DT_BF16)
     e = wide           ? bwd_wide<__nv_bfloat16>(a, blocks, st)
-        : P.N % 8 == 0 ? bwd_pick<__nv_bfloat16, 8>(a, blocks, st)
+        : P.N % 4 == 0 ? bwd_pick<__nv_bfloat16, 4>(a, blocks, st)
                        : bwd_pick<__nv_bfloat16, 1>(a, blocks, st);
   else
     e = wide           ? bwd_wide<float>(a, blocks, st)
