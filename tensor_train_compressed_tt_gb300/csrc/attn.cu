@@ -4,6 +4,7 @@
 #include <new>
 
 #include "attn.h"
+#include "attn_decode.cuh"
 #include "attn_general.cuh"
 #include "attn_seq.cuh"
 #include "attn_tc_bwd.cuh"
@@ -75,12 +76,12 @@ AttnArgs make_args(const AttnPlan& P, const tt_attn_seqs* s) {
   return a;
 }
 
-// Workspace of a pass.  Backward: delta, then the partial sums of key tiles in pieces.
+// Workspace of a pass.  Forward: partial results of keys split over CTAs.  Backward: delta, then the partial sums of key tiles in pieces.
 size_t delta_bytes(const AttnPlan& P, const tt_attn_seqs* s) {
   return al256((size_t)P.heads * (size_t)s->Tq * sizeof(float));
 }
 size_t attn_ws(const AttnPlan& P, const tt_attn_seqs* s, bool backward) {
-  return backward ? delta_bytes(P, s) + al256(bwd_parts_bytes(P, s)) : 0;
+  return backward ? delta_bytes(P, s) + al256(bwd_parts_bytes(P, s)) : al256(decode_bytes(P, s));
 }
 
 tt_status from_cuda(cudaError_t e) {
@@ -144,9 +145,11 @@ tt_status tt_attn_forward(const tt_plan_t* plan, const tt_attn_seqs* seqs, const
   if (a.B == 0 || a.max_q == 0) return TT_OK;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   prof_begin(kPhFwd, st);
-  const cudaError_t e = P.act == TT_DT_F32 ? general_pass<float>(a, 0, st)
-                        : tc_fwd_takes(a)  ? tc_fwd(a, st)
-                                           : general_pass<__nv_bfloat16>(a, 0, st);
+  const bool few = decode_shape(P, seqs) && decode_takes(a, P.act);
+  const cudaError_t e = few                   ? decode(P, seqs, a, ws, st)
+                        : P.act == TT_DT_F32 ? general_pass<float>(a, 0, st)
+                        : tc_fwd_takes(a)    ? tc_fwd(a, st)
+                                             : general_pass<__nv_bfloat16>(a, 0, st);
   prof_end(kPhFwd, st);
   return from_cuda(e);
 }
