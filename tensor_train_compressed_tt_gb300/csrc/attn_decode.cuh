@@ -19,6 +19,7 @@ namespace {
 constexpr int kDecWarps = 4;
 constexpr int kDecRows = 16;   // most rows (query heads of a group x queries), bf16
 constexpr int kDecRowsF32 = 8;
+constexpr int kDecStages = 2;
 constexpr int kDecUnroll = 4;  // keys on their way in a lane
 
 struct DecodeCut {
@@ -45,11 +46,11 @@ __device__ __forceinline__ float2 join(float ma, float mb, float* m) {
   return make_float2(exp2f(ma - ref), exp2f(mb - ref));
 }
 
-// The warps' shares of a CTA's rows (so: [warp][R][C + 2], o then maximum and
-// sum) joined and written: the result, or this split's part of it.
+// The warps' shares of a CTA's rows (so: `stride` floats a warp, rows of C + 4,
+// o, then maximum and sum) joined and written: the result, or this split's part of it.
 template <typename T, int C>
 __device__ __forceinline__ void decode_out(const AttnArgs& p, const DecodeCut& cut, const Seq& s,
-                                           int hk, int split, int rows, const float* so, int R) {
+                                           int hk, int split, int rows, const float* so, int stride) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   __syncthreads();
   for (int r = warp; r < rows; r += kDecWarps) {
@@ -57,7 +58,7 @@ __device__ __forceinline__ void decode_out(const AttnArgs& p, const DecodeCut& c
     const float* at_w[kDecWarps];
 #pragma unroll
     for (int w = 0; w < kDecWarps; ++w) {
-      at_w[w] = so + (w * R + r) * (C + 2);
+      at_w[w] = so + w * stride + r * (C + 4);
       mm = fmaxf(mm, at_w[w][C]);
     }
     const float ref = mm == -INFINITY ? 0.f : mm;
@@ -98,19 +99,49 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Lane = (g, t), g = lane / 4, t = lane % 4.  A product's fragments hold, for
-// rows or columns g, the pairs 2t, 2t + 1 and 2t + 8, 2t + 9 along the summed
-// axis.  That axis may be taken in any order that both operands share, so for
-// Q K^T lane t holds 8 channels in a row of every 32 (one 16-byte load), two
-// products' worth.  For P V the summed axis is the keys, a column a channel:
-// lane g holds 8 channels in a row of the keys 2t, 2t + 1, 2t + 8, 2t + 9, and
-// column g of product i stands for its channel i.
+// Products are taken with the keys (or the channels) as the 16 rows of the left
+// operand and the call's rows as the 8 columns of the right one, N times 8.
+// Lane = (g, t), g = lane / 4, t = lane % 4: a result holds rows g, g + 8 and
+// columns 2t, 2t + 1, so a lane keeps the softmax of its columns and the keys'
+// maximum is taken over g.  The weights go from a result (keys g) to a right
+// operand (keys 2t, 2t + 1) by one 8 x 8 transposition a half.  A warp copies its
+// 16 keys and values asynchronously into shared memory of its own, kDecStages - 1
+// steps ahead (16-byte pieces of a row turned by row % 8: eight rows' pieces at one
+// place lie in eight different bank groups), so only warps meet, not the CTA.
 // DB: blocks of 32 channels.
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 template <int DB>
-__global__ void __launch_bounds__(32 * kDecWarps, 3)
+constexpr int kDecRing = kDecStages * 32 * (64 * DB);  // bytes a warp: 16 keys, 16 values a stage
+template <int DB, int N>
+__global__ void __launch_bounds__(32 * kDecWarps, N == 1 ? 3 : 2)
     attn_decode_mma_kernel(AttnArgs p, DecodeCut cut) {
-  constexpr int C = 32 * DB, VB = DB / 2;
-  extern __shared__ float dec_smem[];  // [warp][kDecRows][C + 2]
+  constexpr int C = 32 * DB, kRow = 2 * C, kRing = kDecRing<DB>, kHalf = 16 * kRow;
+  static_assert(kRing >= 32 * N * (C + 4));
+  extern __shared__ __align__(128) uint8_t dec_smem[];  // a warp's ring, its share afterwards
   pdl_wait();
   pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -120,152 +151,166 @@ __global__ void __launch_bounds__(32 * kDecWarps, 3)
   if (!load_seq(p, b, &s, threadIdx.x == 0)) return;
   const int rows = p.group * s.lq;
   if (rows == 0) return;
-  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-  // queries: rows g and g + 8 (row r: query head hk group + r / lq, query r % lq)
-  uint4 q[2][DB];
-  int pos[2];
+  // Steps of 16 keys: those of the first tokens, then those of the window.
+  const KeySpan ks = key_span(p, s.lk, s.off(), s.lk - 1);
+  const int lead = (ks.a1 + 15) >> 4, steps = lead + ((ks.b1 - ks.b0 + 15) >> 4);
+  const int j1 = (int)((int64_t)steps * (split + 1) / cut.splits);
+  int j = (int)((int64_t)steps * split / cut.splits) + warp;
+  const uint32_t ring = su32(dec_smem) + warp * kRing;
+  const __nv_bfloat16* kbase = p.k.at<const __nv_bfloat16>(s.k0, hk);
+  const __nv_bfloat16* vbase = p.v.at<const __nv_bfloat16>(s.k0, hk);
+  const int krow = (int)p.k.row, vrow = (int)p.v.row;
+  constexpr int kPer = 4 * DB, kPass = 32 / kPer;  // lanes a row, rows a pass
+  const int r0 = lane / kPer, c0 = lane % kPer;
+  const bool in = 8 * c0 < p.dim;
+  if (p.dim < C)  // no copy writes the channels above dim: zeros
+    for (int i = lane; i < kRing / 16; i += 32)
+      *reinterpret_cast<uint4*>(dec_smem + warp * kRing + 16 * i) = make_uint4(0u, 0u, 0u, 0u);
+  __syncwarp();
+  // a step's first key and count; its rows past the count repeat the last one
+  auto span = [&](int at, int* key0) {
+    const bool first = at < lead;
+    *key0 = first ? 16 * at : ks.b0 + 16 * (at - lead);
+    return min(16, (first ? ks.a1 : ks.b1) - *key0);
+  };
+  auto fetch = [&](int at, int stage) {
+    int key0;
+    const int last = span(at, &key0) - 1;
+    const __nv_bfloat16* kp = kbase + key0 * p.k.row + 8 * c0;
+    const __nv_bfloat16* vp = vbase + key0 * p.v.row + 8 * c0;
+    const uint32_t dst = ring + stage * (2 * kHalf) + r0 * kRow;
+    if (in) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int r = g + 8 * i, gr = r / s.lq, tq = r - gr * s.lq;
-    pos[i] = s.off() + tq;
-#pragma unroll
-    for (int d = 0; d < DB; ++d) {
-      const int c = 32 * d + 8 * t;
-      q[i][d] = r < rows && c < p.dim
-                    ? *reinterpret_cast<const uint4*>(
-                          p.q.at<const __nv_bfloat16>(s.q0 + tq, hk * p.group + gr) + c)
-                    : zero;
+      for (int i = 0; i < 16 / kPass; ++i) {
+        const int r = r0 + i * kPass, from = min(r, last);
+        const uint32_t to = dst + i * kPass * kRow + 16 * (c0 ^ (r & 7));
+        copy16(to, kp + (int64_t)from * krow);
+        copy16(to + kHalf, vp + (int64_t)from * vrow);
+      }
     }
+  };
+  int stage = 0;
+#pragma unroll
+  for (int i = 0; i < kDecStages - 1; ++i) {
+    if (j + i * kDecWarps < j1) fetch(j + i * kDecWarps, i);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  // queries: column c is query c % lq of query head hk group + c / lq
+  uint32_t q[N][2 * DB][2];
+  int pos[N][2];
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    const int c = 8 * n + g, gr = c / s.lq;
+    const __nv_bfloat16* src =
+        p.q.at<const __nv_bfloat16>(s.q0 + c - gr * s.lq, hk * p.group + gr) + 2 * t;
+#pragma unroll
+    for (int i = 0; i < 2 * DB; ++i)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        q[n][i][e] = c < rows && 16 * i + 8 * e < p.dim
+                         ? *reinterpret_cast<const uint32_t*>(src + 16 * i + 8 * e)
+                         : 0u;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) pos[n][e] = s.off() + (8 * n + 2 * t + e) % s.lq;
   }
   const float scale = p.scale * 1.4426950408889634f;
-  const KeySpan ks = key_span(p, s.lk, s.off(), s.lk - 1);
-  const int n = ks.a1 + ks.b1 - ks.b0;  // keys that some row sees, the first tokens first
-  const int x0 = (int)((int64_t)n * split / cut.splits);
-  const int x1 = (int)((int64_t)n * (split + 1) / cut.splits);
-  auto key = [&](int x) { return x < ks.a1 ? x : ks.b0 + x - ks.a1; };
-  float o[VB][8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  float o[N][2 * DB][4], m[N][2], l[N][2];
 #pragma unroll
-  for (int w = 0; w < VB; ++w)
+  for (int n = 0; n < N; ++n) {
+    m[n][0] = m[n][1] = -INFINITY;
+    l[n][0] = l[n][1] = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[w][i][e] = 0.f;
-  uint4 kk[2][DB], vv[4][VB];
-  auto load_k = [&](int x) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int y = x + 8 * i + g;
-      const __nv_bfloat16* row = p.k.at<const __nv_bfloat16>(s.k0 + key(y), hk);
-#pragma unroll
-      for (int d = 0; d < DB; ++d) {
-        const int c = 32 * d + 8 * t;
-        kk[i][d] = y < x1 && c < p.dim ? *reinterpret_cast<const uint4*>(row + c) : zero;
-      }
-    }
-  };
-  auto load_v = [&](int x) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int y = x + 2 * t + (i & 1) + 8 * (i >> 1);
-      const __nv_bfloat16* row = p.v.at<const __nv_bfloat16>(s.k0 + key(y), hk);
-#pragma unroll
-      for (int w = 0; w < VB; ++w) {
-        const int c = 64 * w + 8 * g;
-        vv[i][w] = y < x1 && c < p.dim ? *reinterpret_cast<const uint4*>(row + c) : zero;
-      }
-    }
-  };
-  int x = x0 + 16 * warp;
-  if (x < x1) {
-    load_k(x);
-    load_v(x);
+    for (int i = 0; i < 2 * DB; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
   }
+  // A 16 x 16 block of keys x channels: matrices (keys 0-7, channels 0-7), (8-15,
+  // 0-7), (0-7, 8-15), (8-15, 8-15).  Of values, transposed, with the middle two
+  // exchanged (rows are the channels there).
+  const int kr = lane & 15, kc = lane >> 4;
+  const int vr = (lane & 7) + 8 * (lane >> 4), vc = (lane >> 3) & 1;
 #pragma unroll 1
-  for (; x < x1; x += 16 * kDecWarps) {
-    float sc[2][4];
+  for (; j < j1; j += kDecWarps) {
+    const int ahead = j + (kDecStages - 1) * kDecWarps;
+    if (ahead < j1) fetch(ahead, stage == 0 ? kDecStages - 1 : stage - 1);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    asm volatile("cp.async.wait_group %0;" ::"n"(kDecStages - 1) : "memory");
+    __syncwarp();
+    const uint32_t at = ring + stage * (2 * kHalf);
+    stage = stage == kDecStages - 1 ? 0 : stage + 1;
+    float sc[N][4];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
+    for (int n = 0; n < N; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.f;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) sc[j][e] = 0.f;
+    for (int i = 0; i < 2 * DB; ++i) {
+      uint32_t a[4];
+      ldsm4(a, at + kr * kRow + 16 * ((2 * i + kc) ^ (kr & 7)));
 #pragma unroll
-      for (int d = 0; d < DB; ++d) {
-        const uint32_t a0[4] = {q[0][d].x, q[1][d].x, q[0][d].y, q[1][d].y};
-        const uint32_t a1[4] = {q[0][d].z, q[1][d].z, q[0][d].w, q[1][d].w};
-        mma16816(sc[j], a0, kk[j][d].x, kk[j][d].y);
-        mma16816(sc[j], a1, kk[j][d].z, kk[j][d].w);
-      }
+      for (int n = 0; n < N; ++n) mma16816(sc[n], a, q[n][i][0], q[n][i][1]);
     }
-    const int next = x + 16 * kDecWarps;
-    if (next < x1) load_k(next);
-    float top[2] = {-INFINITY, -INFINITY};
+    int key0;
+    const int count = span(j, &key0);
+    uint32_t w[N][2];
+    bool turn = false;
+    float f[N][2];
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int n = 0; n < N; ++n) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int y = x + 8 * j + 2 * t + (e & 1), i = e >> 1;
-        const bool see = y < x1 && (s.lq == 1 || visible(p, pos[i], key(y)));
-        sc[j][e] = see ? sc[j][e] * scale : -INFINITY;
-        top[i] = fmaxf(top[i], sc[j][e]);
-      }
-    float f[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
-      top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 2));
-      const float mn = fmaxf(m[i], top[i]);
-      f[i] = mn == m[i] ? 1.f : exp2f(m[i] - mn);
-      m[i] = mn;
-      l[i] *= f[i];
-    }
-    if (__any_sync(0xffffffffu, f[0] != 1.f || f[1] != 1.f)) {
-#pragma unroll
-      for (int w = 0; w < VB; ++w)
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[w][i][e] *= f[e >> 1];
-    }
-    uint32_t a[4];
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float ref = m[i] == -INFINITY ? 0.f : m[i];
-        const float u = exp2f(sc[j][2 * i] - ref), v = exp2f(sc[j][2 * i + 1] - ref);
-        l[i] += u + v;
-        a[2 * j + i] = pack_bf16(u, v);
+        const int k = g + 8 * (e >> 1);
+        const bool see = k < count && (s.lq == 1 || visible(p, pos[n][e & 1], key0 + k));
+        sc[n][e] = see ? sc[n][e] * scale : -INFINITY;
       }
 #pragma unroll
-    for (int w = 0; w < VB; ++w) {
-      const uint32_t v0[4] = {vv[0][w].x, vv[0][w].y, vv[0][w].z, vv[0][w].w};
-      const uint32_t v1[4] = {vv[1][w].x, vv[1][w].y, vv[1][w].z, vv[1][w].w};
-      const uint32_t v2[4] = {vv[2][w].x, vv[2][w].y, vv[2][w].z, vv[2][w].w};
-      const uint32_t v3[4] = {vv[3][w].x, vv[3][w].y, vv[3][w].z, vv[3][w].w};
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t pick = i & 1 ? 0x7632u : 0x5410u;
-        mma16816(o[w][i], a, __byte_perm(v0[i >> 1], v1[i >> 1], pick),
-                 __byte_perm(v2[i >> 1], v3[i >> 1], pick));
+      for (int e = 0; e < 2; ++e) {
+        float top = fmaxf(sc[n][e], sc[n][e + 2]);
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+        const float mn = fmaxf(m[n][e], top);
+        const float ref = mn == -INFINITY ? 0.f : mn;
+        f[n][e] = exp2_fast(m[n][e] - ref);
+        turn |= mn != m[n][e];
+        m[n][e] = mn;
+        sc[n][e] = exp2_fast(sc[n][e] - ref);
+        sc[n][e + 2] = exp2_fast(sc[n][e + 2] - ref);
+        l[n][e] = fmaf(l[n][e], f[n][e], sc[n][e] + sc[n][e + 2]);
       }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) w[n][h] = transpose8(pack_bf16(sc[n][2 * h], sc[n][2 * h + 1]));
     }
-    if (next < x1) load_v(next);
+    if (__any_sync(0xffffffffu, turn)) {
+#pragma unroll
+      for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int i = 0; i < 2 * DB; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[n][i][e] *= f[n][e & 1];
+    }
+#pragma unroll
+    for (int i = 0; i < 2 * DB; ++i) {
+      uint32_t a[4];
+      ldsm4t(a, at + kHalf + vr * kRow + 16 * ((2 * i + vc) ^ (vr & 7)));
+#pragma unroll
+      for (int n = 0; n < N; ++n) mma16816(o[n][i], a, w[n][0], w[n][1]);
+    }
+    __syncwarp();  // every lane has read the stage that the next step fills
   }
-  float* so = dec_smem + warp * kDecRows * (C + 2);
+  float* so = reinterpret_cast<float*>(dec_smem + warp * kRing);
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-    l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-    float* row = so + (g + 8 * i) * (C + 2);
-    if (t == 0) row[C] = m[i], row[C + 1] = l[i];
+  for (int n = 0; n < N; ++n)
 #pragma unroll
-    for (int w = 0; w < VB; ++w)
+    for (int e = 0; e < 2; ++e) {
+      float* row = so + (8 * n + 2 * t + e) * (C + 4);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        row[64 * w + 8 * (2 * t) + k] = o[w][k][2 * i];
-        row[64 * w + 8 * (2 * t + 1) + k] = o[w][k][2 * i + 1];
+      for (int x = 4; x < 32; x *= 2) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], x);
+      if (g == 0) row[C] = m[n][e], row[C + 1] = l[n][e];
+#pragma unroll
+      for (int i = 0; i < 2 * DB; ++i) {
+        row[16 * i + g] = o[n][i][e];
+        row[16 * i + 8 + g] = o[n][i][e + 2];
       }
-  }
-  decode_out<__nv_bfloat16, C>(p, cut, s, hk, split, rows, dec_smem, kDecRows);
+    }
+  decode_out<__nv_bfloat16, C>(p, cut, s, hk, split, rows,
+                               reinterpret_cast<const float*>(dec_smem), kRing / 4);
 }
 
 // R: rows in registers (at least the call's); L lanes a key.
@@ -273,7 +318,7 @@ template <typename T, int R, int L>
 __global__ void __launch_bounds__(32 * kDecWarps) attn_decode_kernel(AttnArgs p, DecodeCut cut) {
   using P = Pack16<T>;
   constexpr int N = P::N, KEYS = 32 / L, U = kDecUnroll;
-  __shared__ float so[kDecWarps][R][L * N + 2];
+  __shared__ float so[kDecWarps][R][L * N + 4];
   pdl_wait();
   pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, u = lane % L, sub = lane / L;
@@ -393,7 +438,7 @@ __global__ void __launch_bounds__(32 * kDecWarps) attn_decode_kernel(AttnArgs p,
       if (u == 0) so[warp][r][L * N] = m[r], so[warp][r][L * N + 1] = l[r];
     }
   }
-  decode_out<T, L * N>(p, cut, s, hk, split, rows, &so[0][0][0], R);
+  decode_out<T, L * N>(p, cut, s, hk, split, rows, &so[0][0][0], R * (L * N + 4));
 }
 
 // The splits of a row joined, in their order: a warp a row.
@@ -453,7 +498,8 @@ bool decode_shape(const AttnPlan& P, const tt_attn_seqs* s) {
 bool decode_takes(const AttnArgs& p, int act) {
   const int n = elems16(act);
   auto ok = [&](const Heads& x) {
-    return reinterpret_cast<uintptr_t>(x.p) % 16 == 0 && x.row % n == 0 && x.head % n == 0;
+    return reinterpret_cast<uintptr_t>(x.p) % 16 == 0 && x.row % n == 0 && x.head % n == 0 &&
+           x.row < (1 << 30) && x.row > -(1 << 30);  // 32 bits in the kernel
   };
   return ok(p.q) && ok(p.k) && ok(p.v);
 }
@@ -487,10 +533,18 @@ cudaError_t decode_f32(const AttnArgs& p, const DecodeCut& cut, dim3 grid, cudaS
 }
 cudaError_t decode_bf16(const AttnArgs& p, const DecodeCut& cut, dim3 grid, cudaStream_t st) {
   const dim3 block(32 * kDecWarps);
-  auto smem = [](int db) { return sizeof(float) * kDecWarps * kDecRows * (32 * db + 2); };
+  auto go = [&](auto kernel, int ring) {
+    const size_t smem = (size_t)ring * kDecWarps;
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    return e != cudaSuccess ? e : launch_ex(kernel, grid, block, smem, st, false, p, cut);
+  };
+  const bool one = p.group * p.max_q <= 8;
   if (p.dim <= 64)
-    return launch_ex(attn_decode_mma_kernel<2>, grid, block, smem(2), st, false, p, cut);
-  return launch_ex(attn_decode_mma_kernel<4>, grid, block, smem(4), st, false, p, cut);
+    return one ? go(attn_decode_mma_kernel<2, 1>, kDecRing<2>)
+               : go(attn_decode_mma_kernel<2, 2>, kDecRing<2>);
+  return one ? go(attn_decode_mma_kernel<4, 1>, kDecRing<4>)
+             : go(attn_decode_mma_kernel<4, 2>, kDecRing<4>);
 }
 cudaError_t decode(const AttnPlan& P, const tt_attn_seqs* s, const AttnArgs& p, void* ws,
                    cudaStream_t st) {
