@@ -1,14 +1,19 @@
 // Attention of a few query rows against long caches: the form for single
-// tokens.  There is nothing to tile over the queries, the pass is one read of
-// the visible keys and values, so what counts is bytes in flight: the keys of
-// a sequence and key head are split over CTAs and warps, and every row of the
-// group's query heads uses what a warp read.  The shares of warps and CTAs are
-// joined by their maxima, the CTAs' by a second kernel.
+// tokens.  There is nothing to tile over the queries; the pass is one read of the
+// visible keys and values, so what counts is bytes in flight and instructions a
+// key.  The keys of a sequence and key head are split over the CTAs of a cluster
+// and their warps, every row of the group's query heads uses what a warp read,
+// and the shares are joined by their maxima through shared memory (across
+// clusters, where a sequence has more CTAs than eight, by a second kernel).
 //
-// bf16: 16 rows x 16 keys a step on warp-level matrix instructions, operands
-// straight from global memory in 16-byte pieces (an fp32 dot product by shuffles
-// took five times the instructions and 44 us where this takes XX, 32 sequences,
-// 16 heads on 4, 1028 keys of 128).  f32: dot products over lanes, exact.
+// bf16: 16 keys a step on warp-level matrix instructions.  The 128-row tiles of
+// the tensor-memory kernels would be filled by 4 rows of a group here, and one CTA
+// a key head leaves SMs idle.  32 sequences, 1028 visible keys of 128, 16 heads on
+// 4 (67 MB): 16.1 us, 4.2 TB/s; by the tiled kernel 39 us; by dot products over
+// lanes and a second kernel for every join 50 us; 256 such sequences 87 us, 6.2
+// TB/s, tiled 237 us.  One sequence of 8192 keys 24 us, tiled 85 us.
+// f32: dot products over lanes, every product in 32 bits: 51 us against 763 us of
+// the kernel for any layout (the same shape), bound by its instructions.
 #pragma once
 
 #include "attn_general.cuh"
@@ -23,9 +28,11 @@ constexpr int kDecStages = 2;
 constexpr int kDecUnroll = 4;  // keys on their way in a lane
 
 struct DecodeCut {
-  int splits;
-  float* o;    // [split][head][Tq][dim], not yet divided by the sum
-  float2* ml;  // [split][head][Tq]: maximum (in powers of two) and sum
+  int splits;   // CTAs of a sequence and key head: `cluster` times `parts`
+  int cluster;  // CTAs that join through shared memory
+  int parts;    // joins left for the second kernel
+  float* o;     // [part][query head][query][dim]
+  float2* ml;   // [part][query head][query]: maximum, sum
 };
 
 // 16 bytes as floats
@@ -46,48 +53,94 @@ __device__ __forceinline__ float2 join(float ma, float mb, float* m) {
   return make_float2(exp2f(ma - ref), exp2f(mb - ref));
 }
 
+__device__ __forceinline__ float remote(uint32_t at, int rank) {
+  uint32_t there;
+  float x;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(at), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(there) : "memory");
+  return x;
+}
+__device__ __forceinline__ void cluster_meet() {
+  asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+
 // The warps' shares of a CTA's rows (so: `stride` floats a warp, rows of C + 4,
-// o, then maximum and sum) joined and written: the result, or this split's part of it.
+// o, then maximum and sum) joined, then those of the cluster's CTAs, a warp a
+// row; the result, or this part of it, is written.
 template <typename T, int C>
 __device__ __forceinline__ void decode_out(const AttnArgs& p, const DecodeCut& cut, const Seq& s,
-                                           int hk, int split, int rows, const float* so, int stride) {
+                                           int hk, int split, int rows, float* so, int stride) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int part = split / cut.cluster, rank = split - part * cut.cluster;
   __syncthreads();
   for (int r = warp; r < rows; r += kDecWarps) {
+    float* at = so + r * (C + 4);
     float mm = -INFINITY, ll = 0.f;
-    const float* at_w[kDecWarps];
 #pragma unroll
-    for (int w = 0; w < kDecWarps; ++w) {
-      at_w[w] = so + w * stride + r * (C + 4);
-      mm = fmaxf(mm, at_w[w][C]);
-    }
+    for (int w = 0; w < kDecWarps; ++w) mm = fmaxf(mm, at[w * stride + C]);
     const float ref = mm == -INFINITY ? 0.f : mm;
     float f[kDecWarps];
 #pragma unroll
     for (int w = 0; w < kDecWarps; ++w) {
-      f[w] = exp2f(at_w[w][C] - ref);
-      ll += at_w[w][C + 1] * f[w];
+      f[w] = exp2f(at[w * stride + C] - ref);
+      ll += at[w * stride + C + 1] * f[w];
     }
-    const int g = r / s.lq, h = hk * p.group + g;
-    const int64_t t = s.q0 + r - g * s.lq;
-    const float inv = cut.splits > 1 ? 1.f : ll > 0.f || ll != ll ? 1.f / ll : 0.f;
-    const int64_t at = ((int64_t)split * p.heads + h) * p.Tq + t;
-    for (int d = lane; d < p.dim; d += 32) {
+    __syncwarp();
+    if (lane == 0) at[C] = mm, at[C + 1] = ll;
+#pragma unroll
+    for (int d = lane; d < C; d += 32) {
       float sum = 0.f;
 #pragma unroll
-      for (int w = 0; w < kDecWarps; ++w) sum = fmaf(at_w[w][d], f[w], sum);
-      if (cut.splits > 1)
-        cut.o[at * p.dim + d] = sum;
-      else
-        p.o.at<T>(t, h)[d] = from_f32<T>(sum * inv);
-    }
-    if (lane == 0) {
-      if (cut.splits > 1)
-        cut.ml[at] = make_float2(mm, ll);
-      else if (p.lse)
-        p.lse[at] = ll > 0.f || ll != ll ? (mm + log2f(ll)) * 0.6931471805599453f : -INFINITY;
+      for (int w = 0; w < kDecWarps; ++w) sum = fmaf(at[w * stride + d], f[w], sum);
+      at[d] = sum;
     }
   }
+  __syncwarp();
+  cluster_meet();
+  const uint32_t base = su32(so);
+  for (int r = rank * kDecWarps + warp; r < rows; r += cut.cluster * kDecWarps) {
+    const uint32_t at = base + 4 * r * (C + 4);
+    // lane k: maximum and sum of CTA k
+    const float m = lane < cut.cluster ? remote(at + 4 * C, lane) : -INFINITY;
+    const float l = lane < cut.cluster ? remote(at + 4 * C + 4, lane) : 0.f;
+    float mm = m;
+#pragma unroll
+    for (int w = 4; w; w >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, w));
+    const float f = exp2f(m - (mm == -INFINITY ? 0.f : mm));
+    float ll = 0.f, o[C / 32];
+#pragma unroll
+    for (int c = 0; c < C / 32; ++c) o[c] = 0.f;
+#pragma unroll 2
+    for (int k = 0; k < cut.cluster; ++k) {
+      const float fk = __shfl_sync(0xffffffffu, f, k);
+      ll = fmaf(__shfl_sync(0xffffffffu, l, k), fk, ll);
+#pragma unroll
+      for (int c = 0; c < C / 32; ++c)
+        o[c] = fmaf(remote(at + 4 * (32 * c + lane), k), fk, o[c]);
+    }
+    mm = __shfl_sync(0xffffffffu, mm, 0);
+    const int g = r / s.lq, h = hk * p.group + g;
+    const int64_t t = s.q0 + r - g * s.lq;
+    const float inv = cut.parts > 1 ? 1.f : ll > 0.f || ll != ll ? 1.f / ll : 0.f;
+    const int64_t to = ((int64_t)part * p.heads + h) * p.Tq + t;
+#pragma unroll
+    for (int c = 0; c < C / 32; ++c) {
+      const int d = 32 * c + lane;
+      if (d >= p.dim) break;
+      if (cut.parts > 1)
+        cut.o[to * p.dim + d] = o[c];
+      else
+        p.o.at<T>(t, h)[d] = from_f32<T>(o[c] * inv);
+    }
+    if (lane == 0) {
+      if (cut.parts > 1)
+        cut.ml[to] = make_float2(mm, ll);
+      else if (p.lse)
+        p.lse[to] = ll > 0.f || ll != ll ? (mm + log2f(ll)) * 0.6931471805599453f : -INFINITY;
+    }
+  }
+  __syncwarp();
+  cluster_meet();  // no CTA leaves while another reads its shares
 }
 
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
@@ -310,7 +363,7 @@ __global__ void __launch_bounds__(32 * kDecWarps, N == 1 ? 3 : 2)
       }
     }
   decode_out<__nv_bfloat16, C>(p, cut, s, hk, split, rows,
-                               reinterpret_cast<const float*>(dec_smem), kRing / 4);
+                               reinterpret_cast<float*>(dec_smem), kRing / 4);
 }
 
 // R: rows in registers (at least the call's); L lanes a key.
@@ -441,7 +494,7 @@ __global__ void __launch_bounds__(32 * kDecWarps) attn_decode_kernel(AttnArgs p,
   decode_out<T, L * N>(p, cut, s, hk, split, rows, &so[0][0][0], R * (L * N + 4));
 }
 
-// The splits of a row joined, in their order: a warp a row.
+// The parts of a row (at most 32) joined, in their order: a warp a row.
 template <typename T>
 __global__ void __launch_bounds__(128) attn_join_kernel(AttnArgs p, DecodeCut cut) {
   pdl_wait();
@@ -455,32 +508,28 @@ __global__ void __launch_bounds__(128) attn_join_kernel(AttnArgs p, DecodeCut cu
   Seq s;
   if (!load_seq(p, b, &s, false) || t >= s.lq) return;
   const int64_t row = (int64_t)h * p.Tq + s.q0 + t, step = (int64_t)p.heads * p.Tq;
-  float m = -INFINITY;
-  for (int k = lane; k < cut.splits; k += 32) m = fmaxf(m, cut.ml[k * step + row].x);
+  // lane k: maximum and sum of part k
+  const float2 ml =
+      lane < cut.parts ? cut.ml[lane * step + row] : make_float2(-INFINITY, 0.f);
+  float m = ml.x;
 #pragma unroll
   for (int w = 16; w; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
-  const float ref = m == -INFINITY ? 0.f : m;
-  float l = 0.f, o[8];
+  const float f = exp2f(ml.x - (m == -INFINITY ? 0.f : m));
+  float l = 0.f, o[4];
 #pragma unroll
-  for (int c = 0; c < 8; ++c) o[c] = 0.f;
-  for (int k0 = 0; k0 < cut.splits; k0 += 32) {  // lane k: the weight of split k0 + k
-    const float2 ml = k0 + lane < cut.splits ? cut.ml[(k0 + lane) * step + row]
-                                             : make_float2(-INFINITY, 0.f);
-    const float f = exp2f(ml.x - ref);
-    const int n = min(32, cut.splits - k0);
-#pragma unroll 4
-    for (int k = 0; k < n; ++k) {
-      const float fk = __shfl_sync(0xffffffffu, f, k), lk = __shfl_sync(0xffffffffu, ml.y, k);
-      l = fmaf(lk, fk, l);
-      const float* src = cut.o + ((k0 + k) * step + row) * p.dim;
+  for (int c = 0; c < 4; ++c) o[c] = 0.f;
+#pragma unroll 8
+  for (int k = 0; k < cut.parts; ++k) {
+    const float fk = __shfl_sync(0xffffffffu, f, k);
+    l = fmaf(__shfl_sync(0xffffffffu, ml.y, k), fk, l);
+    const float* src = cut.o + (k * step + row) * p.dim;
 #pragma unroll
-      for (int c = 0; c < 8; ++c)
-        if (32 * c + lane < p.dim) o[c] = fmaf(src[32 * c + lane], fk, o[c]);
-    }
+    for (int c = 0; c < 4; ++c)
+      if (32 * c + lane < p.dim) o[c] = fmaf(src[32 * c + lane], fk, o[c]);
   }
   const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
 #pragma unroll
-  for (int c = 0; c < 8; ++c)
+  for (int c = 0; c < 4; ++c)
     if (32 * c + lane < p.dim) p.o.at<T>(s.q0 + t, h)[32 * c + lane] = from_f32<T>(o[c] * inv);
   if (lane == 0 && p.lse)
     p.lse[row] = l > 0.f || l != l ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
@@ -504,22 +553,33 @@ bool decode_takes(const AttnArgs& p, int act) {
   return ok(p.q) && ok(p.k) && ok(p.v);
 }
 
-// Splits: as many CTAs as the SMs hold at once (three each), but no fewer than
-// 64 keys a CTA (16 a warp).
-int decode_splits(const AttnPlan& P, const tt_attn_seqs* s) {
+// Splits: as many CTAs as the SMs hold at once, three each, of many rows (whose
+// sums take more registers) two, but no fewer than 64 keys a CTA (16 a warp);
+// clusters of up to eight, the portable size.  1028 keys, 16 heads on 4: one query
+// a sequence 16 us at two and three an SM, 26 us at six (a second wave); 16 rows
+// 21 us at two, 28 us at three.  f32 4 rows 51 us at three, 58 us at two; 8 rows
+// 74 us at three, 65 us at two.
+DecodeCut decode_cut(const AttnPlan& P, const tt_attn_seqs* s) {
   int64_t keys = s->max_k;
   if (P.left >= 0) {
     const int64_t most = (int64_t)P.left + s->max_q + P.sinks + (P.right > 0 ? P.right : 0);
     if (P.right >= 0 && most < keys) keys = most;
   }
   const int64_t pairs = (int64_t)s->B * P.kv;
-  int64_t n = pairs > 0 ? 3 * (int64_t)device_sms() / pairs : 1;
+  const int64_t rows = (int64_t)(P.heads / P.kv) * s->max_q;
+  const int an_sm = rows <= (P.act == TT_DT_F32 ? 4 : 8) ? 3 : 2;
+  int64_t n = pairs > 0 ? an_sm * (int64_t)device_sms() / pairs : 1;
   if (n > keys / 64) n = keys / 64;
-  return (int)(n < 1 ? 1 : n > 256 ? 256 : n);
+  n = n < 1 ? 1 : n > 256 ? 256 : n;
+  DecodeCut cut = {};
+  cut.parts = (int)(n + 7) / 8;
+  cut.cluster = (int)n / cut.parts;
+  cut.splits = cut.parts * cut.cluster;
+  return cut;
 }
 size_t decode_bytes(const AttnPlan& P, const tt_attn_seqs* s) {
   if (!decode_shape(P, s)) return 0;
-  const int n = decode_splits(P, s);
+  const int n = decode_cut(P, s).parts;
   if (n == 1) return 0;
   return (size_t)n * P.heads * (size_t)s->Tq * ((size_t)P.dim * sizeof(float) + sizeof(float2));
 }
@@ -527,9 +587,12 @@ size_t decode_bytes(const AttnPlan& P, const tt_attn_seqs* s) {
 template <int R>
 cudaError_t decode_f32(const AttnArgs& p, const DecodeCut& cut, dim3 grid, cudaStream_t st) {
   const dim3 block(32 * kDecWarps);
-  if (p.dim <= 32) return launch_ex(attn_decode_kernel<float, R, 8>, grid, block, 0, st, false, p, cut);
-  if (p.dim <= 64) return launch_ex(attn_decode_kernel<float, R, 16>, grid, block, 0, st, false, p, cut);
-  return launch_ex(attn_decode_kernel<float, R, 32>, grid, block, 0, st, false, p, cut);
+  auto go = [&](auto kernel) {
+    return launch_cluster(kernel, grid, block, 0, st, cut.cluster, p, cut);
+  };
+  if (p.dim <= 32) return go(attn_decode_kernel<float, R, 8>);
+  if (p.dim <= 64) return go(attn_decode_kernel<float, R, 16>);
+  return go(attn_decode_kernel<float, R, 32>);
 }
 cudaError_t decode_bf16(const AttnArgs& p, const DecodeCut& cut, dim3 grid, cudaStream_t st) {
   const dim3 block(32 * kDecWarps);
@@ -537,7 +600,7 @@ cudaError_t decode_bf16(const AttnArgs& p, const DecodeCut& cut, dim3 grid, cuda
     const size_t smem = (size_t)ring * kDecWarps;
     const cudaError_t e =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    return e != cudaSuccess ? e : launch_ex(kernel, grid, block, smem, st, false, p, cut);
+    return e != cudaSuccess ? e : launch_cluster(kernel, grid, block, smem, st, cut.cluster, p, cut);
   };
   const bool one = p.group * p.max_q <= 8;
   if (p.dim <= 64)
@@ -548,10 +611,9 @@ cudaError_t decode_bf16(const AttnArgs& p, const DecodeCut& cut, dim3 grid, cuda
 }
 cudaError_t decode(const AttnPlan& P, const tt_attn_seqs* s, const AttnArgs& p, void* ws,
                    cudaStream_t st) {
-  DecodeCut cut;
-  cut.splits = decode_splits(P, s);
+  DecodeCut cut = decode_cut(P, s);
   cut.ml = static_cast<float2*>(ws);
-  cut.o = reinterpret_cast<float*>(cut.ml + (size_t)cut.splits * p.heads * (size_t)p.Tq);
+  cut.o = reinterpret_cast<float*>(cut.ml + (size_t)cut.parts * p.heads * (size_t)p.Tq);
   const int64_t blocks = (int64_t)p.B * p.kv * cut.splits;
   if (blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
   const dim3 grid((unsigned)blocks);
@@ -563,7 +625,7 @@ cudaError_t decode(const AttnPlan& P, const tt_attn_seqs* s, const AttnArgs& p, 
                   : rows <= 2 ? decode_f32<2>(p, cut, grid, st)
                   : rows <= 4 ? decode_f32<4>(p, cut, grid, st)
                               : decode_f32<8>(p, cut, grid, st);
-  if (e == cudaSuccess && cut.splits > 1) {
+  if (e == cudaSuccess && cut.parts > 1) {
     const dim3 join((unsigned)(((int64_t)p.B * p.heads * p.max_q + 3) / 4));
     count_launches(1);
     e = f32 ? launch_ex(attn_join_kernel<float>, join, dim3(128), 0, st, false, p, cut)
