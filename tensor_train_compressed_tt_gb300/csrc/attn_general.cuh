@@ -35,18 +35,50 @@ struct GenShape {
   static constexpr int LP = BT + 4;
   static constexpr int TILE = BT * LD;
   static constexpr int DC = (DP + 63) / 64;  // float4 column groups a thread owns
+  // heads of 32: the 16 lanes of a row are two sets of 8, with half the sum each
+  static constexpr int SETS = DP < 64 ? 64 / DP : 1, LANES = 16 / SETS;
 };
 
+// Four elements of a row as floats.
+template <typename T>
+__device__ __forceinline__ float4 gen_four(const T* x);
+template <>
+__device__ __forceinline__ float4 gen_four<float>(const float* x) {
+  return *reinterpret_cast<const float4*>(x);
+}
+template <>
+__device__ __forceinline__ float4 gen_four<__nv_bfloat16>(const __nv_bfloat16* x) {
+  const uint2 v = *reinterpret_cast<const uint2*>(x);
+  return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u),
+                     __uint_as_float(v.y << 16), __uint_as_float(v.y & 0xFFFF0000u));
+}
+
 // Rows r0 .. r0 + BT - 1 of head h (zero past `n` rows and past the head's
-// width) into a tile.
+// width) into a tile, four elements a load where the tensor's alignment lets it.
 template <typename T, int DP, int MT>
-__device__ void gen_load(float* tile, const Heads& x, int64_t base, int h, int r0, int n,
-                         int dim) {
+__device__ __forceinline__ void gen_load(float* tile, const Heads& x, int64_t base, int h, int r0,
+                                         int n, int dim) {
   using S = GenShape<DP, MT>;
-  for (int e = threadIdx.x; e < S::BT * DP; e += kGenThreads) {
-    const int r = e / DP, c = e % DP;
-    tile[r * S::LD + c] =
-        (r0 + r < n && c < dim) ? as_f32<T>(x.at<const T>(base + r0 + r, h)[c]) : 0.f;
+  const bool wide = ((reinterpret_cast<uintptr_t>(x.p) / sizeof(T)) | (uintptr_t)x.row |
+                     (uintptr_t)x.head | (uintptr_t)dim) % 4 == 0;
+  constexpr int Q = DP / 4;
+#pragma unroll
+  for (int i = 0; i < S::BT * Q; i += kGenThreads) {
+    const int e = i + threadIdx.x, r = e / Q, c = e % Q * 4;
+    if (S::BT * Q % kGenThreads && e >= S::BT * Q) break;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r0 + r < n && c < dim) {
+      const T* at = x.at<const T>(base + r0 + r, h) + c;
+      if (wide) {
+        v = gen_four<T>(at);
+      } else {
+        v.x = as_f32<T>(at[0]);
+        if (c + 1 < dim) v.y = as_f32<T>(at[1]);
+        if (c + 2 < dim) v.z = as_f32<T>(at[2]);
+        if (c + 3 < dim) v.w = as_f32<T>(at[3]);
+      }
+    }
+    *reinterpret_cast<float4*>(tile + r * S::LD + c) = v;
   }
 }
 
@@ -80,26 +112,33 @@ __device__ __forceinline__ void gen_dot(const float* A, const float* B, int ty, 
   }
 }
 
-// acc[a][4 g + i] += sum_j W[ty MT + a][j] V[j][(16 g + tx) 4 + i], j < n
+// acc[a][4 g + i] += sum_j W[ty MT + a][j] V[j][(16 g + lane) 4 + i], j < n rounded up
+// to fours (rows of V past n and their weights are zero); a lane set's share of it.
 template <int DP, int MT>
 __device__ __forceinline__ void gen_acc(const float* W, const float* V, int n, int ty, int tx,
                                         float (&acc)[MT][4 * GenShape<DP, MT>::DC]) {
   using S = GenShape<DP, MT>;
-  for (int j = 0; j < n; ++j) {
-    float w[MT];
+  const int lane = tx % S::LANES, set = tx / S::LANES;
+#pragma unroll 1
+  for (int j = 4 * set; j < n; j += 4 * S::SETS) {
+    float4 w[MT];
 #pragma unroll
-    for (int a = 0; a < MT; ++a) w[a] = W[(ty * MT + a) * S::LP + j];
+    for (int a = 0; a < MT; ++a)
+      w[a] = *reinterpret_cast<const float4*>(W + (ty * MT + a) * S::LP + j);
 #pragma unroll
     for (int g = 0; g < S::DC; ++g) {
-      const int c = (16 * g + tx) * 4;
-      if (DP % 64 && c >= DP) continue;
-      const float4 v = *reinterpret_cast<const float4*>(V + j * S::LD + c);
+      const float* col = V + j * S::LD + (16 * g + lane) * 4;
 #pragma unroll
-      for (int a = 0; a < MT; ++a) {
-        acc[a][4 * g + 0] = fmaf(w[a], v.x, acc[a][4 * g + 0]);
-        acc[a][4 * g + 1] = fmaf(w[a], v.y, acc[a][4 * g + 1]);
-        acc[a][4 * g + 2] = fmaf(w[a], v.z, acc[a][4 * g + 2]);
-        acc[a][4 * g + 3] = fmaf(w[a], v.w, acc[a][4 * g + 3]);
+      for (int u = 0; u < 4; ++u) {
+        const float4 v = *reinterpret_cast<const float4*>(col + u * S::LD);
+#pragma unroll
+        for (int a = 0; a < MT; ++a) {
+          const float x = u == 0 ? w[a].x : u == 1 ? w[a].y : u == 2 ? w[a].z : w[a].w;
+          acc[a][4 * g + 0] = fmaf(x, v.x, acc[a][4 * g + 0]);
+          acc[a][4 * g + 1] = fmaf(x, v.y, acc[a][4 * g + 1]);
+          acc[a][4 * g + 2] = fmaf(x, v.z, acc[a][4 * g + 2]);
+          acc[a][4 * g + 3] = fmaf(x, v.w, acc[a][4 * g + 3]);
+        }
       }
     }
   }
@@ -107,20 +146,24 @@ __device__ __forceinline__ void gen_acc(const float* W, const float* V, int n, i
 
 // Rows ty MT + a of a tile's accumulators, times mul[a], to the tensor.
 template <typename T, int DP, int MT>
-__device__ void gen_store(const Heads& x, int64_t base, int h, int r0, int n, int dim, int ty,
-                          int tx, const float (&acc)[MT][4 * GenShape<DP, MT>::DC],
-                          const float (&mul)[MT]) {
+__device__ __forceinline__ void gen_store(const Heads& x, int64_t base, int h, int r0, int n,
+                                          int dim, int ty, int tx,
+                                          const float (&acc)[MT][4 * GenShape<DP, MT>::DC],
+                                          const float (&mul)[MT]) {
+  using S = GenShape<DP, MT>;
 #pragma unroll
   for (int a = 0; a < MT; ++a) {
     const int r = r0 + ty * MT + a;
-    if (r >= n) continue;
-    T* row = x.at<T>(base + r, h);
+    T* row = x.at<T>(base + min(r, n - 1), h);
 #pragma unroll
-    for (int g = 0; g < GenShape<DP, MT>::DC; ++g)
+    for (int g = 0; g < S::DC; ++g)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
+        float v = acc[a][4 * g + i];
+#pragma unroll
+        for (int w = S::LANES; w < 16; w *= 2) v += __shfl_xor_sync(0xffffffffu, v, w);
         const int c = (16 * g + tx) * 4 + i;
-        if (c < dim) row[c] = from_f32<T>(acc[a][4 * g + i] * mul[a]);
+        if (tx < S::LANES && r < n && c < dim) row[c] = from_f32<T>(v * mul[a]);
       }
   }
 }
