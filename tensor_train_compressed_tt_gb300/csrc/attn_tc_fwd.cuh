@@ -55,9 +55,11 @@ struct TcFwd {
   struct Shared {
     uint64_t q_full[QS], q_empty[QS], k_full[KP], k_empty[KP], v_full[KP], v_empty[KP];
     uint64_t s_full[2], p_full[2], pv_done[2], o_free, fin, fin2;  // [tile & 1]
+    uint64_t stat_full, stat_free;
     uint64_t item_full[ITEMS], item_empty[ITEMS], clc;
     FwdItem item[ITEMS];
     uint4 answer;
+    float m[AT], l[AT];  // of an item's rows, for the writing warps
     int rows[2 * KP];  // keys of a tile, by its number (a key tile's place is free before
                        // the product of its values has read this)
     uint32_t tmem;
@@ -66,7 +68,7 @@ struct TcFwd {
   static constexpr size_t kSmem = QS * NB * ABOX + 2 * KP * UNIT + sizeof(Shared) + 1024;
 };
 
-constexpr int kTcThreads = 224;
+constexpr int kTcThreads = 352;
 
 // CTA number -> tile.  The tiles of one sequence and head come one after
 // another, so that they share its keys in L2; the last ones, which see the
@@ -162,8 +164,10 @@ __global__ void __launch_bounds__(kTcThreads, TcFwd<NB>::CTAS)
     }
 #pragma unroll 1
     for (int i = 0; i < C::ITEMS; ++i)
-      mbar_init(&S.item_full[i], 1), mbar_init(&S.item_empty[i], 6);
+      mbar_init(&S.item_full[i], 1), mbar_init(&S.item_empty[i], 10);
     mbar_init(&S.o_free, 4);
+    mbar_init(&S.stat_full, 4);
+    mbar_init(&S.stat_free, 4);
     mbar_init(&S.clc, 1);
     mbar_init(&S.fin, 1);
     mbar_init(&S.fin2, 1);
@@ -358,8 +362,8 @@ __global__ void __launch_bounds__(kTcThreads, TcFwd<NB>::CTAS)
       drain_one(&S.fin2, 0);
     }
     __syncwarp();
-  } else {
-    // ---------------- softmax and output: thread = row
+  } else if (warp < 4) {
+    // ---------------- softmax: thread = row
     const uint32_t lane_off = (uint32_t)(32 * warp) << 16;
     const int row = 32 * warp + lane;
     const float c = p.scale * kLog2e;
@@ -436,7 +440,30 @@ __global__ void __launch_bounds__(kTcThreads, TcFwd<NB>::CTAS)
         __syncwarp();
         if (lane == 0) mbar_arrive(&S.p_full[g & 1]);
       }
-      if (!ok) break;
+      ok = ok && wait_all(&S.stat_free, (n & 1) ^ 1, abort_flag, 110);
+      S.m[row] = m;
+      S.l[row] = l;
+      __syncwarp();
+      if (ok && lane == 0) mbar_arrive(&S.stat_full);
+    }
+  } else {
+    // ---------------- output: thread = row of the warp's quarter of tensor memory
+    const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
+    const int row = 32 * (warp & 3) + lane;
+    const bool wide = wide_rows(p.o);
+    int g = 0;
+#pragma unroll 1
+    for (int n = 0;; ++n) {
+      if (!wait_all(&S.item_full[n % C::ITEMS], (n / C::ITEMS) & 1, abort_flag, 112)) break;
+      const FwdItem w = S.item[n % C::ITEMS];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.item_empty[n % C::ITEMS]);
+      if (w.nt < 0) break;
+      g += w.nt;
+      if (!wait_all(&S.stat_full, n & 1, abort_flag, 113)) break;
+      const float m = S.m[row], l = S.l[row];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.stat_free);
       const bool in = row < w.nq;
       if (p.lse && in)
         p.lse[(int64_t)w.h * p.Tq + w.q0 + w.t0 + row] =
@@ -449,11 +476,11 @@ __global__ void __launch_bounds__(kTcThreads, TcFwd<NB>::CTAS)
         continue;
       }
       // One barrier for even and one for odd tiles: the product of tile g - 3 was
-      // done before S of tile g - 1 came, so the parity is not taken for another's.
+      // done before S of tile g - 1 came, and that before the statistics, so the
+      // parity is not taken for another's.
       if (!wait_all(&S.pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, abort_flag, 111)) break;
       tc_fence_after();
       const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-      const bool wide = wide_rows(p.o);
 #pragma unroll 1
       for (int d = 0; d < p.dim; d += 32) {
         float o[32];
@@ -473,7 +500,7 @@ __global__ void __launch_bounds__(kTcThreads, TcFwd<NB>::CTAS)
       uint32_t again = __ballot_sync(0xffffffffu, in && l >= 1.15e18f);
 #pragma unroll 1
       for (; again; again &= again - 1)
-        exact_row(p, w, 32 * warp + __ffs(again) - 1, w.lk);
+        exact_row(p, w, row - lane + __ffs(again) - 1, w.lk);
     }
   }
   tc_fence_before();
