@@ -103,17 +103,27 @@ __device__ __forceinline__ float2 group_sum2(float a, float b, float2 (*red)[32]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (lane == 0) red[slot][warp] = make_float2(a, b);
   group_sync<W, GROUPS>(group);
-  float2 t = lane < W ? red[slot][group * W + lane] : make_float2(0.f, 0.f);
+  float2 t = red[slot][group * W + (lane & (W - 1))];  // every W lanes hold the W shares
 #pragma unroll
-  for (int o = 16; o; o >>= 1) {
+  for (int o = W / 2; o; o >>= 1) {
     t.x += __shfl_xor_sync(0xffffffffu, t.x, o);
     t.y += __shfl_xor_sync(0xffffffffu, t.y, o);
   }
   return t;
 }
+// Of one value, by a block that is one group.
 template <int W>
 __device__ __forceinline__ float group_sum(float v, float2 (*red)[32], int slot) {
-  return group_sum2<W, 1>(v, 0.f, red, slot, 0).x;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if (W == 1) return v;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (lane == 0) red[slot][warp].x = v;
+  __syncthreads();
+  v = red[slot][lane & (W - 1)].x;
+#pragma unroll
+  for (int o = W / 2; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
 }
 
 struct NormFwdArgs {
