@@ -79,6 +79,55 @@ __device__ __forceinline__ void weights_at(const float* w, int j, float other, b
   }
 }
 
+// VEC values at once, two an instruction where they come in pairs.
+template <int VEC>
+__device__ __forceinline__ void add_up(float2& sum, const float* v) {  // sum += v
+  if (VEC == 1) sum.x += v[0];
+#pragma unroll
+  for (int i = 0; i + 1 < VEC; i += 2) sum = __fadd2_rn(sum, make_float2(v[i], v[i + 1]));
+}
+template <int VEC>
+__device__ __forceinline__ void mul_up(float2& sum, const float* a, const float* b) {  // += a b
+  if (VEC == 1) sum.x = fmaf(a[0], b[0], sum.x);
+#pragma unroll
+  for (int i = 0; i + 1 < VEC; i += 2)
+    sum = __ffma2_rn(make_float2(a[i], a[i + 1]), make_float2(b[i], b[i + 1]), sum);
+}
+template <int VEC>
+__device__ __forceinline__ void add(const float* a, const float* b, float* o) {  // o = a + b
+  if (VEC == 1) o[0] = a[0] + b[0];
+#pragma unroll
+  for (int i = 0; i + 1 < VEC; i += 2) {
+    const float2 t = __fadd2_rn(make_float2(a[i], a[i + 1]), make_float2(b[i], b[i + 1]));
+    o[i] = t.x, o[i + 1] = t.y;
+  }
+}
+template <int VEC>
+__device__ __forceinline__ void mul(const float* a, const float* b, float* o) {  // o = a b
+  if (VEC == 1) o[0] = a[0] * b[0];
+#pragma unroll
+  for (int i = 0; i + 1 < VEC; i += 2) {
+    const float2 t = __fmul2_rn(make_float2(a[i], a[i + 1]), make_float2(b[i], b[i + 1]));
+    o[i] = t.x, o[i + 1] = t.y;
+  }
+}
+template <int VEC>
+__device__ __forceinline__ void fma(const float* a, const float* b, const float* c,
+                                    float* o) {  // o = a b + c
+  if (VEC == 1) o[0] = fmaf(a[0], b[0], c[0]);
+#pragma unroll
+  for (int i = 0; i + 1 < VEC; i += 2) {
+    const float2 t = __ffma2_rn(make_float2(a[i], a[i + 1]), make_float2(b[i], b[i + 1]),
+                                make_float2(c[i], c[i + 1]));
+    o[i] = t.x, o[i + 1] = t.y;
+  }
+}
+template <int VEC>
+__device__ __forceinline__ void fill(float x, float* o) {
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) o[i] = x;
+}
+
 // The barrier of one group of W warps among the block's groups.
 template <int W, int GROUPS>
 __device__ __forceinline__ void group_sync(int group) {
@@ -159,9 +208,9 @@ struct NormBwdArgs {
 
 constexpr int kRowWarps = 8;  // rows side by side in a block when a warp holds a row
 
-// A group of W warps holds a row of up to 32 W VEC CH values; groups stride
-// over the rows, loading the next row while the current one is worked on.
-template <typename T, int VEC, int CH, int W, bool RES>
+// A group of W warps holds ROWS rows of up to 32 W VEC CH values; groups stride
+// over the rows, loading the next ones while the current ones are worked on.
+template <typename T, int VEC, int CH, int W, bool RES, int ROWS>
 __global__ void __launch_bounds__(W == 1 ? 32 * kRowWarps : 32 * W)
     norm_fwd_kernel(NormFwdArgs p) {
   using R = Raw<T, VEC>;
@@ -172,73 +221,105 @@ __global__ void __launch_bounds__(W == 1 ? 32 * kRowWarps : 32 * W)
   const int64_t step = (int64_t)gridDim.x * per_block;
   int64_t row = (int64_t)blockIdx.x * per_block + (W == 1 ? threadIdx.x >> 5 : 0);
   const int N = p.N;
-  R rx[CH], rr[CH];
+  R rx[ROWS][CH], rr[ROWS][CH];
   pdl_wait();
   pdl_trigger();
-  auto fetch = [&](int64_t r) {
+  auto fetch = [&](int k, int64_t r) {
     const T* x = static_cast<const T*>(p.x) + r * N;
     const T* s = static_cast<const T*>(p.res) + r * N;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int j = (c * G + tid) * VEC;
       if (j < N) {
-        rx[c] = *reinterpret_cast<const R*>(x + j);
-        if (RES) rr[c] = *reinterpret_cast<const R*>(s + j);
+        rx[k][c] = *reinterpret_cast<const R*>(x + j);
+        if (RES) rr[k][c] = *reinterpret_cast<const R*>(s + j);
       }
     }
   };
-  if (row < p.T) fetch(row);
-  for (; row < p.T; row += step) {
-    float v[CH * VEC];
-    float part = 0.f;
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const int j = (c * G + tid) * VEC;
-      if (j < N) {
-        rx[c].get(v + c * VEC);
-        if (RES) {
-          float a[VEC];
-          rr[c].get(a);
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) v[c * VEC + i] += a[i];
-        }
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) part += v[c * VEC + i];
-      }
+  // the sum of every row's share over the group
+  auto sums = [&](float (&part)[ROWS], int slot) {
+    if (ROWS == 2) {
+      const float2 t = group_sum2<W, 1>(part[0], part[ROWS - 1], red, slot, 0);
+      part[0] = t.x;
+      part[ROWS - 1] = t.y;
+    } else {
+      part[0] = group_sum<W>(part[0], red, slot);
     }
-    if (row + step < p.T) fetch(row + step);
-    const float mean = group_sum<W>(part, red, 0) / p.n;
-    part = 0.f;
+  };
 #pragma unroll
-    for (int c = 0; c < CH; ++c)
-      if ((c * G + tid) * VEC < N) {
+  for (int k = 0; k < ROWS; ++k)
+    if (row + k * step < p.T) fetch(k, row + k * step);
+  for (; row < p.T; row += ROWS * step) {
+    float v[ROWS][CH * VEC], part[ROWS], mean[ROWS], rstd[ROWS];
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          const float d = v[c * VEC + i] - mean;
-          part = fmaf(d, d, part);
+    for (int k = 0; k < ROWS; ++k) {
+      float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const int j = (c * G + tid) * VEC;
+        if (j < N) {
+          float* u = v[k] + c * VEC;
+          rx[k][c].get(u);
+          if (RES) {
+            float a[VEC];
+            rr[k][c].get(a);
+            add<VEC>(u, a, u);
+          }
+          add_up<VEC>(sum, u);
         }
       }
-    const float var = group_sum<W>(part, red, 1) / p.n;
-    const float rstd = 1.f / sqrtf(var + p.eps);
-    if (tid == 0 && p.stats) p.stats[row] = make_float2(mean, rstd);
-    T* y = static_cast<T*>(p.y) + row * N;
-    T* so = static_cast<T*>(p.sum) + row * N;
+      part[k] = sum.x + sum.y;
+      const int64_t next = row + (ROWS + k) * step;
+      if (next < p.T) fetch(k, next);
+    }
+    sums(part, 0);
+#pragma unroll
+    for (int k = 0; k < ROWS; ++k) {
+      mean[k] = part[k] / p.n;
+      float2 sum = make_float2(0.f, 0.f);
+      float shift[VEC], d[VEC];
+      fill<VEC>(-mean[k], shift);
+#pragma unroll
+      for (int c = 0; c < CH; ++c)
+        if ((c * G + tid) * VEC < N) {
+          add<VEC>(v[k] + c * VEC, shift, d);
+          mul_up<VEC>(sum, d, d);
+        }
+      part[k] = sum.x + sum.y;
+    }
+    sums(part, 1);
+#pragma unroll
+    for (int k = 0; k < ROWS; ++k) {
+      rstd[k] = 1.f / sqrtf(part[k] / p.n + p.eps);
+      if (tid == 0 && p.stats && row + k * step < p.T)
+        p.stats[row + k * step] = make_float2(mean[k], rstd[k]);
+    }
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int j = (c * G + tid) * VEC;
       if (j < N) {
-        R o;
-        if (p.sum) {
-          o.set(v + c * VEC);
-          *reinterpret_cast<R*>(so + j) = o;
-        }
-        float f[VEC], g[VEC], b[VEC];
+        float g[VEC], b[VEC];
         weights_at<VEC>(p.gamma, j, 1.f, p.gamma16, g);
         weights_at<VEC>(p.beta, j, 0.f, p.beta16, b);
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) f[i] = fmaf((v[c * VEC + i] - mean) * rstd, g[i], b[i]);
-        o.set(f);
-        *reinterpret_cast<R*>(y + j) = o;
+        for (int k = 0; k < ROWS; ++k) {
+          if (k > 0 && row + k * step >= p.T) break;
+          const int64_t at = (row + k * step) * N + j;
+          const float* u = v[k] + c * VEC;
+          R o;
+          if (p.sum) {
+            o.set(u);
+            *reinterpret_cast<R*>(static_cast<T*>(p.sum) + at) = o;
+          }
+          float f[VEC], shift[VEC], by[VEC];
+          fill<VEC>(-mean[k], shift);
+          fill<VEC>(rstd[k], by);
+          add<VEC>(u, shift, f);
+          mul<VEC>(f, by, f);
+          fma<VEC>(f, g, b, f);
+          o.set(f);
+          *reinterpret_cast<R*>(static_cast<T*>(p.y) + at) = o;
+        }
       }
     }
   }
@@ -290,8 +371,11 @@ __global__ void __launch_bounds__(32 * W * bwd_groups(W), W <= 8 ? 2 : 1)
   for (; row < p.T; row += step, flip ^= 1) {
     float h[E], g[E];  // normalised values; dy gamma
     R us[CH];
-    float sg = 0.f, sgh = 0.f;
+    float2 sg = make_float2(0.f, 0.f), sgh = sg;
     const float2 ms = st;
+    float shift[VEC], by[VEC];
+    fill<VEC>(-ms.x, shift);
+    fill<VEC>(ms.y, by);
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int j = (c * G + tid) * VEC;
@@ -299,34 +383,37 @@ __global__ void __launch_bounds__(32 * W * bwd_groups(W), W <= 8 ? 2 : 1)
       if (j < N) {
         float w[VEC];
         weights_at<VEC>(p.gamma, j, 1.f, p.gamma16, w);
-        rs[c].get(h + c * VEC);
-        rd[c].get(g + c * VEC);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          const int e = c * VEC + i;
-          h[e] = (h[e] - ms.x) * ms.y;
-          dg[e] = fmaf(g[e], h[e], dg[e]);
-          db[e] += g[e];
-          g[e] *= w[i];
-          sg += g[e];
-          sgh = fmaf(g[e], h[e], sgh);
-        }
+        float *hc = h + c * VEC, *gc = g + c * VEC;
+        rs[c].get(hc);
+        rd[c].get(gc);
+        add<VEC>(hc, shift, hc);
+        mul<VEC>(hc, by, hc);
+        fma<VEC>(gc, hc, dg + c * VEC, dg + c * VEC);
+        add<VEC>(gc, db + c * VEC, db + c * VEC);
+        mul<VEC>(gc, w, gc);
+        add_up<VEC>(sg, gc);
+        mul_up<VEC>(sgh, gc, hc);
       }
     }
     if (row + step < p.T) fetch(row + step);
-    const float2 t = group_sum2<W, GROUPS>(sg, sgh, red, flip, group);
-    const float a = t.x / p.n, b = t.y / p.n;
+    const float2 t = group_sum2<W, GROUPS>(sg.x + sg.y, sgh.x + sgh.y, red, flip, group);
+    float a[VEC], b[VEC];
+    fill<VEC>(-(t.x / p.n), a);
+    fill<VEC>(-(t.y / p.n), b);
     T* dx = static_cast<T*>(p.dx) + row * N;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int j = (c * G + tid) * VEC;
       if (j < N) {
-        float f[VEC], u[VEC];
-        if (p.dsum) us[c].get(u);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          const int e = c * VEC + i;
-          f[i] = ms.y * (g[e] - a - h[e] * b) + (p.dsum ? u[i] : 0.f);
+        float f[VEC];
+        add<VEC>(g + c * VEC, a, f);
+        fma<VEC>(h + c * VEC, b, f, f);
+        if (p.dsum) {
+          float u[VEC];
+          us[c].get(u);
+          fma<VEC>(f, by, u, f);
+        } else {
+          mul<VEC>(f, by, f);
         }
         R o;
         o.set(f);
@@ -518,10 +605,10 @@ int64_t bwd_blocks(int64_t N, int64_t T) {
 
 bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
 
-template <typename T, int VEC, int CH, int W, bool RES>
+template <typename T, int VEC, int CH, int W, bool RES, int ROWS>
 cudaError_t fwd_launch(const NormFwdArgs& a, cudaStream_t st) {
   constexpr int rows = W == 1 ? kRowWarps : 1, threads = W == 1 ? 32 * kRowWarps : 32 * W;
-  auto kernel = norm_fwd_kernel<T, VEC, CH, W, RES>;
+  auto kernel = norm_fwd_kernel<T, VEC, CH, W, RES, ROWS>;
   // as many blocks as stay on the SMs, each taking rows in turn
   static PerDevice once;
   static int fit[kMaxDevices] = {};
@@ -541,7 +628,18 @@ cudaError_t fwd_launch(const NormFwdArgs& a, cudaStream_t st) {
 }
 template <typename T, int VEC, int CH, int W>
 cudaError_t fwd_go(const NormFwdArgs& a, cudaStream_t st) {
-  return a.res ? fwd_launch<T, VEC, CH, W, true>(a, st) : fwd_launch<T, VEC, CH, W, false>(a, st);
+  // Without a residual, and with rows enough for every block, two rows at a time:
+  // the weights are read from L1 once for both (their 8 bytes a value, against 2
+  // from memory, took 78 % of the L1's rate) and each barrier serves both.  bf16,
+  // one -> two rows: 32768 x 4096 119 -> 108 us, 65536 x 2048 115 -> 95, 16384 x
+  // 8192 126 -> 116; one warp a row (65536 x 1024) 58 -> 62, 32 warps (8192 x
+  // 16384) 134 -> 150, with a residual (16384 x 4096) 89 -> 98: registers.
+  if constexpr (VEC > 1 && W >= 4 && W <= 16) {
+    if (!a.res && a.T >= 16 * (int64_t)device_sms())
+      return fwd_launch<T, VEC, CH, W, false, 2>(a, st);
+  }
+  return a.res ? fwd_launch<T, VEC, CH, W, true, 1>(a, st)
+               : fwd_launch<T, VEC, CH, W, false, 1>(a, st);
 }
 
 template <typename T, int V>
