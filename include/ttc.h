@@ -382,7 +382,11 @@ tt_status tt_norm_backward(const tt_plan_t* plan, int64_t T, const void* s, cons
  *   o_i = sum_j p_j v_j.
  * A row that sees no key gets o = 0 and lse = -infinity, and zero gradients.
  * Keys that no query of their sequence sees are not used: what they hold (a
- * cache's unwritten rows, NaN) reaches no output.
+ * cache's unwritten rows, NaN) reaches no output.  A key that some query sees
+ * must hold finite values: the products are taken over tiles, where a weight of
+ * zero times a value that is not finite is NaN, so such a value may reach every
+ * query within 128 rows of one that sees it (in a backward, a query's q, o or
+ * dout likewise every key within 128 of one that it sees).
  * Scores, softmax statistics and all sums are fp32.  With bf16 activations
  * the weights p (and in the backward z's gradient) are rounded to bf16 for
  * the tensor-core products. */

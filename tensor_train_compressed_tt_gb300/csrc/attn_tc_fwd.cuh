@@ -14,9 +14,19 @@
 // scores rise by more than 60 powers of two over those first keys shows in l,
 // and is computed again by itself with a running maximum (exact_row).
 //
-// Roles: warps 0-3 softmax and output, warp 4 finds the work and loads it,
-// warp 5 issues S, warp 6 O += P V.  S has two buffers, so that the next S is
-// computed during a softmax, and two CTAs on an SM fill each other's waits.
+// Roles: warps 0-3 softmax, warp 4 finds the work and loads it, warp 5 issues S,
+// warp 6 O += P V, warps 7-10 write the output.  S has two buffers, so that the
+// next S is computed during a softmax, and two CTAs on an SM fill each other's
+// waits.
+//
+// 128 sequences of 128, window +-64, 12 heads of 64: 24.8 us (101 MB: 4.1 TB/s);
+// 64 sequences of 257 to 512, window +-128, 16 heads of 64: 59.5 us (203 MB), the
+// tensor pipe 25 % and the issue slots 51 % busy: bound by the chain of a tile,
+// whose 96 columns take a softmax warp 1700 cycles, half of them waiting for
+// tensor memory, exponentials and the other warps of its scheduler.  Measured and
+// not kept (the second case, 59.5): columns in 16s 63 us; in 16s with the next
+// ones loaded ahead 82 us (twice the code); one buffer of S and four CTAs an SM 76
+// us, three 73 us; the softmax warps writing the output themselves 62 us.
 //
 // What held the kernel back was not a pipe.  The loops are not unrolled more
 // than the softmax needs: with the code at twice its size the kernel waited
