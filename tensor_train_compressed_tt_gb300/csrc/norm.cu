@@ -3,7 +3,7 @@
 //
 // Both passes are bound by HBM: a row is read once, kept in registers (up to
 // 16384 values across 1 to 32 warps), and written once.  Measured in bf16 (of the
-// 6.8 TB/s that a copy reaches): forward with a residual 16384 x 768 21.6 us, 4.7
+// 6.8 TB/s that a copy reaches): forward with a residual 16384 x 768 19.8 us, 5.1
 // TB/s; forward 32768 x 4096 105.5 us, 5.1 TB/s; f32 16384 x 4096 84 us, 6.4 TB/s
 // (bf16 has twice the values a byte: 57 % of the issue slots, barriers in the
 // rest); backward 16384 x 768 26 us, 3.9 TB/s, of which the sum of the partials 4;
@@ -58,6 +58,22 @@ struct Raw<__nv_bfloat16, 4> {
   }
 };
 template <>
+struct Raw<__nv_bfloat16, 8> {
+  uint4 v;
+  __device__ void get(float* f) const {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  }
+  __device__ void set(const float* f) {
+    v = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
+                   pack_bf16(f[6], f[7]));
+  }
+};
+template <>
 struct Raw<__nv_bfloat16, 1> {
   __nv_bfloat16 v;
   __device__ void get(float* f) const { f[0] = __bfloat162float(v); }
@@ -73,12 +89,12 @@ __device__ __forceinline__ void weights_at(const float* w, int j, float other, b
   if (!w) {
 #pragma unroll
     for (int i = 0; i < VEC; ++i) f[i] = other;
-  } else if (VEC == 4 && aligned) {
-    const float4 v = __ldg(reinterpret_cast<const float4*>(w + j));
-    f[0] = v.x;
-    f[VEC > 1 ? 1 : 0] = v.y;
-    f[VEC > 2 ? 2 : 0] = v.z;
-    f[VEC > 3 ? 3 : 0] = v.w;
+  } else if (VEC >= 4 && aligned) {
+#pragma unroll
+    for (int i = 0; i + 3 < VEC; i += 4) {
+      const float4 v = __ldg(reinterpret_cast<const float4*>(w + j + i));
+      f[i] = v.x, f[i + 1] = v.y, f[i + 2] = v.z, f[i + 3] = v.w;
+    }
   } else {
 #pragma unroll
     for (int i = 0; i < VEC; ++i) f[i] = __ldg(w + j + i);
@@ -643,12 +659,14 @@ cudaError_t fwd_go(const NormFwdArgs& a, cudaStream_t st) {
   // one -> two rows: 32768 x 4096 119 -> 108 us, 65536 x 2048 115 -> 95, 16384 x
   // 8192 126 -> 116; one warp a row (65536 x 1024) 58 -> 62, 32 warps (8192 x
   // 16384) 134 -> 150, with a residual (16384 x 4096) 89 -> 98: registers.
-  if constexpr (VEC > 1 && W >= 4 && W <= 16) {
-    if (!a.res && a.T >= 16 * (int64_t)device_sms())
-      return fwd_launch<T, VEC, CH, W, false, 2>(a, st);
+  if constexpr (VEC < 8) {
+    if constexpr (VEC > 1 && W >= 4 && W <= 16) {
+      if (!a.res && a.T >= 16 * (int64_t)device_sms())
+        return fwd_launch<T, VEC, CH, W, false, 2>(a, st);
+    }
+    if (!a.res) return fwd_launch<T, VEC, CH, W, false, 1>(a, st);
   }
-  return a.res ? fwd_launch<T, VEC, CH, W, true, 1>(a, st)
-               : fwd_launch<T, VEC, CH, W, false, 1>(a, st);
+  return fwd_launch<T, VEC, CH, W, true, 1>(a, st);
 }
 
 template <typename T, int V>
@@ -764,11 +782,17 @@ tt_status tt_norm_forward(const tt_plan_t* plan, int64_t T, const void* x, const
   a.gamma16 = aligned_to(gamma, 16);
   a.beta16 = aligned_to(beta, 16);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  // rows start aligned to four values only when four divide the width
+  // Rows start aligned to four or eight values only when those divide the width.
+  // Eight (16 bytes) only with a residual, whose four tensors are most of the loads
+  // and stores: 16384 x 768 21.6 -> 19.8 us, 32768 x 2048 88 -> 82; without one the
+  // weights are (32 bytes a lane, half of each line of the L1 a load): 32768 x 4096
+  // 105 -> 142, 65536 x 1024 57 -> 60.
   prof_begin(kPhElem, st);
   const cudaError_t e =
       P.act == TT_DT_BF16
-          ? (P.N % 4 == 0 ? fwd_pick<__nv_bfloat16, 4>(a, st) : fwd_pick<__nv_bfloat16, 1>(a, st))
+          ? (res && P.N % 8 == 0 ? fwd_pick<__nv_bfloat16, 8>(a, st)
+             : P.N % 4 == 0      ? fwd_pick<__nv_bfloat16, 4>(a, st)
+                                 : fwd_pick<__nv_bfloat16, 1>(a, st))
           : (P.N % 4 == 0 ? fwd_pick<float, 4>(a, st) : fwd_pick<float, 1>(a, st));
   prof_end(kPhElem, st);
   count_launches(1);
