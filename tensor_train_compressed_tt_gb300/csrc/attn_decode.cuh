@@ -36,16 +36,10 @@ struct DecodeCut {
 };
 
 // 16 bytes as floats
-template <typename T>
-struct Pack16;
-template <>
-struct Pack16<float> {
-  static constexpr int N = 4;
-  static __device__ void get(const uint4& v, float (&f)[4]) {
-    f[0] = __uint_as_float(v.x), f[1] = __uint_as_float(v.y);
-    f[2] = __uint_as_float(v.z), f[3] = __uint_as_float(v.w);
-  }
-};
+__device__ __forceinline__ void four(const uint4& v, float (&f)[4]) {
+  f[0] = __uint_as_float(v.x), f[1] = __uint_as_float(v.y);
+  f[2] = __uint_as_float(v.z), f[3] = __uint_as_float(v.w);
+}
 // The joint softmax state of two shares of a row: the weights of each.
 __device__ __forceinline__ float2 join(float ma, float mb, float* m) {
   *m = fmaxf(ma, mb);
@@ -367,10 +361,9 @@ __global__ void __launch_bounds__(32 * kDecWarps, N == 1 ? 3 : 2)
 }
 
 // R: rows in registers (at least the call's); L lanes a key.
-template <typename T, int R, int L>
+template <int R, int L>
 __global__ void __launch_bounds__(32 * kDecWarps) attn_decode_kernel(AttnArgs p, DecodeCut cut) {
-  using P = Pack16<T>;
-  constexpr int N = P::N, KEYS = 32 / L, U = kDecUnroll;
+  constexpr int N = 4, KEYS = 32 / L, U = kDecUnroll;
   __shared__ float so[kDecWarps][R][L * N + 4];
   pdl_wait();
   pdl_trigger();
@@ -392,8 +385,8 @@ __global__ void __launch_bounds__(32 * kDecWarps) attn_decode_kernel(AttnArgs p,
     for (int e = 0; e < N; ++e) q[r][e] = o[r][e] = 0.f;
     if (r < rows && on) {
       const int g = r / s.lq;
-      P::get(reinterpret_cast<const uint4*>(
-                 p.q.at<const T>(s.q0 + r - g * s.lq, hk * p.group + g))[u],
+      four(reinterpret_cast<const uint4*>(
+                 p.q.at<const float>(s.q0 + r - g * s.lq, hk * p.group + g))[u],
              q[r]);
 #pragma unroll
       for (int e = 0; e < N; ++e) q[r][e] *= p.scale * 1.4426950408889634f;
@@ -413,15 +406,15 @@ __global__ void __launch_bounds__(32 * kDecWarps) attn_decode_kernel(AttnArgs p,
       kk[i] = vv[i] = make_uint4(0u, 0u, 0u, 0u);
       if (y < x1 && on) {
         const int j = y < ks.a1 ? y : ks.b0 + y - ks.a1;
-        kk[i] = reinterpret_cast<const uint4*>(p.k.at<const T>(s.k0 + j, hk))[u];
-        vv[i] = reinterpret_cast<const uint4*>(p.v.at<const T>(s.k0 + j, hk))[u];
+        kk[i] = reinterpret_cast<const uint4*>(p.k.at<const float>(s.k0 + j, hk))[u];
+        vv[i] = reinterpret_cast<const uint4*>(p.v.at<const float>(s.k0 + j, hk))[u];
       }
     }
     float sc[U][R];
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       float k[N];
-      P::get(kk[i], k);
+      four(kk[i], k);
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         sc[i][r] = 0.f;
@@ -465,7 +458,7 @@ __global__ void __launch_bounds__(32 * kDecWarps) attn_decode_kernel(AttnArgs p,
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       float v[N];
-      P::get(vv[i], v);
+      four(vv[i], v);
 #pragma unroll
       for (int r = 0; r < R; ++r)
 #pragma unroll
@@ -491,7 +484,7 @@ __global__ void __launch_bounds__(32 * kDecWarps) attn_decode_kernel(AttnArgs p,
       if (u == 0) so[warp][r][L * N] = m[r], so[warp][r][L * N + 1] = l[r];
     }
   }
-  decode_out<T, L * N>(p, cut, s, hk, split, rows, &so[0][0][0], R * (L * N + 4));
+  decode_out<float, L * N>(p, cut, s, hk, split, rows, &so[0][0][0], R * (L * N + 4));
 }
 
 // The parts of a row (at most 32) joined, in their order: a warp a row.
@@ -590,24 +583,27 @@ cudaError_t decode_f32(const AttnArgs& p, const DecodeCut& cut, dim3 grid, cudaS
   auto go = [&](auto kernel) {
     return launch_cluster(kernel, grid, block, 0, st, cut.cluster, p, cut);
   };
-  if (p.dim <= 32) return go(attn_decode_kernel<float, R, 8>);
-  if (p.dim <= 64) return go(attn_decode_kernel<float, R, 16>);
-  return go(attn_decode_kernel<float, R, 32>);
+  if (p.dim <= 32) return go(attn_decode_kernel<R, 8>);
+  if (p.dim <= 64) return go(attn_decode_kernel<R, 16>);
+  return go(attn_decode_kernel<R, 32>);
+}
+template <int DB, int N>
+cudaError_t decode_go(const AttnArgs& p, const DecodeCut& cut, dim3 grid, cudaStream_t st) {
+  constexpr int kSmem = kDecRing<DB> * kDecWarps;
+  static PerDevice once;
+  const cudaError_t e = once.get([] {
+    return cudaFuncSetAttribute(attn_decode_mma_kernel<DB, N>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  });
+  if (e != cudaSuccess) return e;
+  return launch_cluster(attn_decode_mma_kernel<DB, N>, grid, dim3(32 * kDecWarps), kSmem, st,
+                        cut.cluster, p, cut);
 }
 cudaError_t decode_bf16(const AttnArgs& p, const DecodeCut& cut, dim3 grid, cudaStream_t st) {
-  const dim3 block(32 * kDecWarps);
-  auto go = [&](auto kernel, int ring) {
-    const size_t smem = (size_t)ring * kDecWarps;
-    const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    return e != cudaSuccess ? e : launch_cluster(kernel, grid, block, smem, st, cut.cluster, p, cut);
-  };
   const bool one = p.group * p.max_q <= 8;
   if (p.dim <= 64)
-    return one ? go(attn_decode_mma_kernel<2, 1>, kDecRing<2>)
-               : go(attn_decode_mma_kernel<2, 2>, kDecRing<2>);
-  return one ? go(attn_decode_mma_kernel<4, 1>, kDecRing<4>)
-             : go(attn_decode_mma_kernel<4, 2>, kDecRing<4>);
+    return one ? decode_go<2, 1>(p, cut, grid, st) : decode_go<2, 2>(p, cut, grid, st);
+  return one ? decode_go<4, 1>(p, cut, grid, st) : decode_go<4, 2>(p, cut, grid, st);
 }
 cudaError_t decode(const AttnPlan& P, const tt_attn_seqs* s, const AttnArgs& p, void* ws,
                    cudaStream_t st) {

@@ -399,3 +399,12 @@ def test_scores_that_rise_far(act, dim):
         assert_near(_np(lse), rl, 1e-5, "lse")
         got = op.backward(q, k, v, o, lse, do, seqs)
         assert all(bool(torch.isfinite(t.float()).all()) for t in got)
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("heads,kv,dim,lq", [(8, 1, 64, 1), (8, 1, 128, 2), (2, 2, 32, 3)])
+@pytest.mark.parametrize("left,sinks", [(-1, 0), (9000, 5), (70, 33)])
+def test_few_rows_of_a_long_cache(heads, kv, dim, lq, left, sinks, act):
+    """One sequence's keys in as many shares as a call makes, joined in two steps
+    (every share's sums are fp32, so the tolerances are those of short caches)."""
+    _check(cached([lq], [20000]), heads, kv, dim, left, 0, sinks, act, backward=False)
