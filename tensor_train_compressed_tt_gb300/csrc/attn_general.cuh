@@ -3,11 +3,11 @@
 // arithmetic (no tensor-core product holds fp32's error), tiles of 16 MT rows
 // in shared memory, 256 threads with MT x MT scores each.
 //
-// f32, 8 heads, causal: 8 sequences of 2048, heads of 32: forward 772 us, backward
-// 2218 us, 22 and 27 TFLOP/s of the fp32 pipes' 80, bound by the reads of shared
+// f32, 8 heads, causal: 8 sequences of 2048, heads of 32: forward 662 us, backward
+// 1928 us, 26 and 31 TFLOP/s of the fp32 pipes' 80, bound by the reads of shared
 // memory that feed them (8 of 16 bytes for 64 multiply-adds); 32 sequences of
-// 33 to 97: backward 54 us, 40% of the issue slots, the rest the latency of loads
-// and barriers of blocks that have two or three tiles each.
+// 33 to 97: backward 45 us, the latency of loads and barriers of blocks that have
+// two or three tiles each.
 #pragma once
 
 #include "attn_seq.cuh"
@@ -185,16 +185,19 @@ __device__ __forceinline__ float half_warp_max(float v) {
   return v;
 }
 
-// Block -> (sequence, head, tile)
+// Block -> (sequence, head, tile).  The tiles that see most under a causal mask come
+// first for all sequences and heads, so that the last blocks to run are short ones (8
+// sequences of 512, heads of 64, backward: 389 us with a sequence's tiles one after
+// another, 275 us so; 32 of 33 to 97: 54 and 45 us).
 struct GenWork {
   int b, h, tile;
 };
-__device__ __forceinline__ GenWork gen_work(int nheads, int ntiles) {
+__device__ __forceinline__ GenWork gen_work(const AttnArgs& p, int nheads, bool keys, int ntiles) {
   GenWork w;
-  w.tile = blockIdx.x % ntiles;
-  const int r = blockIdx.x / ntiles;
-  w.h = r % nheads;
+  const uint32_t per = (uint32_t)p.B * nheads, t = blockIdx.x / per, r = blockIdx.x - t * per;
+  w.tile = keys ? (int)t : ntiles - 1 - (int)t;
   w.b = r / nheads;
+  w.h = r - w.b * nheads;
   return w;
 }
 
@@ -210,7 +213,7 @@ __global__ void __launch_bounds__(kGenThreads)
   float* P = KV + S::TILE;
   pdl_wait();
   pdl_trigger();
-  const GenWork w = gen_work(p.heads, (p.max_q + S::BT - 1) / S::BT);
+  const GenWork w = gen_work(p, p.heads, false, (p.max_q + S::BT - 1) / S::BT);
   Seq s;
   if (!load_seq(p, w.b, &s, threadIdx.x == 0)) return;
   const int t0 = w.tile * S::BT;
@@ -300,7 +303,7 @@ __global__ void __launch_bounds__(kGenThreads)
   float* DS = V + S::TILE;
   pdl_wait();
   pdl_trigger();
-  const GenWork w = gen_work(p.heads, (p.max_q + S::BT - 1) / S::BT);
+  const GenWork w = gen_work(p, p.heads, false, (p.max_q + S::BT - 1) / S::BT);
   Seq s;
   if (!load_seq(p, w.b, &s, threadIdx.x == 0)) return;
   const int t0 = w.tile * S::BT;
@@ -398,7 +401,7 @@ __global__ void __launch_bounds__(kGenThreads)
   float* DS = P + S::BT * S::LP;
   pdl_wait();
   pdl_trigger();
-  const GenWork w = gen_work(p.kv, (p.max_k + S::BT - 1) / S::BT);
+  const GenWork w = gen_work(p, p.kv, true, (p.max_k + S::BT - 1) / S::BT);
   Seq s;
   if (!load_seq(p, w.b, &s, threadIdx.x == 0)) return;
   const int j0 = w.tile * S::BT;
@@ -486,9 +489,10 @@ cudaError_t general_go(const AttnArgs& p, int pass, cudaStream_t st) {
 template <typename T>
 cudaError_t general_pass(const AttnArgs& p, int pass, cudaStream_t st) {
   // Tiles of 32 rows for short sequences, whose last tile of 64 would be mostly
-  // padding.  Sequences of 65, 8 heads of 32, f32: forward 22 -> 18 us, backward
-  // 60 -> 47 us; of 128, heads of 64: 19 -> 21 and 61 -> 58 us; of 512, heads of
-  // 32, 72 -> 83 and 214 -> 236 us (tiles of 64 read shared memory half as often).
+  // padding.  f32, 64 -> 32 rows: sequences of 65, 8 heads of 32: forward 19.6 ->
+  // 15.3 us, backward 51 -> 40 us; of 128, 12 heads of 64: 17.4 -> 17.7 and 55 -> 49
+  // us; of 512, heads of 32, 49 -> 63 and 150 -> 183 us (tiles of 64 read shared
+  // memory half as often).
   const int longest = p.max_q > p.max_k ? p.max_q : p.max_k;
   const bool small = longest <= (pass ? 128 : 96);
   if (p.dim <= 32) return small ? general_go<T, 32, 2>(p, pass, st) : general_go<T, 32, 4>(p, pass, st);
