@@ -408,3 +408,11 @@ def test_few_rows_of_a_long_cache(heads, kv, dim, lq, left, sinks, act):
     """One sequence's keys in as many shares as a call makes, joined in two steps
     (every share's sums are fp32, so the tolerances are those of short caches)."""
     _check(cached([lq], [20000]), heads, kv, dim, left, 0, sinks, act, backward=False)
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("heads,kv,dim", [(4, 2, 64), (2, 1, 128)])
+def test_long_causal_sequences_beside_short_ones(heads, kv, dim, act):
+    """Tiles taken in order of their length over all sequences and heads."""
+    _check(packed([1100, 0, 300, 1, 897]), heads, kv, dim, -1, 0, 0, act)
+    _check(cached([900, 5], [1000, 1030]), heads, kv, dim, -1, 7, 0, act)
