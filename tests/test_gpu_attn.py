@@ -416,3 +416,14 @@ def test_long_causal_sequences_beside_short_ones(heads, kv, dim, act):
     """Tiles taken in order of their length over all sequences and heads."""
     _check(packed([1100, 0, 300, 1, 897]), heads, kv, dim, -1, 0, 0, act)
     _check(cached([900, 5], [1000, 1030]), heads, kv, dim, -1, 7, 0, act)
+
+
+@pytest.mark.parametrize("heads,kv", [(1, 1), (2, 2), (4, 2)])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("sinks", [4, 130])
+def test_first_tokens_of_long_windowed_sequences(heads, kv, dim, sinks):
+    """Gradients of first tokens that every later query sees: their key tiles are
+    cut into pieces, the other tiles are not."""
+    lens = [700, 1, 650]
+    _check(packed(lens), heads, kv, dim, 64, 0, sinks, "bf16")
+    _check(packed(lens * 4), heads, kv, dim, 64, 0, sinks, "bf16")

@@ -220,3 +220,11 @@ def test_wrapper_refuses():
         op.forward(x, gamma=torch.ones(64, dtype=torch.bfloat16, device="cuda"))
     with pytest.raises(ValueError):
         op.forward(x, res=x[:2])
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("N", [1028, 2048, 4096, 8192])
+@pytest.mark.parametrize("T", [2432, 2433, 5001])
+def test_many_rows_without_a_residual(T, N, act):
+    """Two rows at a time, and the last row of a block alone (from 16 rows an SM)."""
+    _case(T, N, act, res=False, seed=T + N)
