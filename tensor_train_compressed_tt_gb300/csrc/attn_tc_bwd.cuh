@@ -584,7 +584,7 @@ __global__ void __launch_bounds__(TcBwd<KV, NB>::THREADS, 1)
     // ---------------- the gradients
     const int quad = warp & 3, row = 32 * quad + lane;
     const uint32_t acc = tmem + ((uint32_t)(32 * quad) << 16) + C::ACC;
-    int nload = 0;
+    int nload = 0, turn = 0;  // turn: buffer of the item's first tile
 #pragma unroll 1
     for (int n = 0;; ++n) {
       if (!wait_all(&S.item_full[n % C::ITEMS], (n / C::ITEMS) & 1, abort_flag, 141)) break;
@@ -598,8 +598,14 @@ __global__ void __launch_bounds__(TcBwd<KV, NB>::THREADS, 1)
       if (!KV && some) {
         const int half = nload & 1;
         if (!wait_all(&S.half_full[half], (nload >> 1) & 1, abort_flag, 135)) break;
+        // In the order of the tiles: which buffer an item begins with depends on the
+        // items that the CTA has taken before.
 #pragma unroll
-        for (int i = 0; i < BUF; ++i) err += S.half[half][KV ? 0 : i][row];
+        for (int i = 0; i < BUF; ++i) {
+          err += S.half[half][KV ? 0 : turn][row];
+          if (++turn == BUF) turn = 0;
+        }
+        turn = (turn + w.nt) % BUF;
         delta = S.half[half][KV ? 0 : BUF][row] + err;
         __syncwarp();
         if (lane == 0) mbar_arrive(&S.half_free[half]);
