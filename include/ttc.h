@@ -432,7 +432,8 @@ typedef struct tt_heads {
 } tt_heads;
 
 /* Bytes of workspace (256-byte aligned) for a forward or a backward of seqs
- * (its device arrays are not read). */
+ * (its device arrays are not read).  Either can be the larger: one buffer for
+ * both passes takes the maximum of the two sizes. */
 tt_status tt_attn_workspace_size(const tt_plan_t* plan, const tt_attn_seqs* seqs, int backward,
                                  size_t* bytes);
 /* q and o: (Tq, heads, dim), k and v: (Tk, kv_heads, dim); lse: (heads, Tq)

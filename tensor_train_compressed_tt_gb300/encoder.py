@@ -130,7 +130,8 @@ class TTTransformerBlock(TTEncoderBlock):
         self.attn = TTAttention(heads, self.N // heads, left=left, right=right, sinks=sinks)
 
     def buffers(self, T: int, seqs: TTSeqs, device="cuda") -> Dict[str, torch.Tensor]:
-        """Everything a step of T tokens writes (allocated once)."""
+        """Everything a step of T tokens of seqs writes (allocated once): a training
+        step, or decode's."""
         b = super().buffers(T, device)
         for nm in ("s1", "h1", "s2", "h2", "att", "datt", "dq", "dk", "dv", "ds1", "ds2"):
             b[nm] = torch.empty((T, self.N), dtype=torch.bfloat16, device=device)

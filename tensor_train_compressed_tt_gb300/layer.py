@@ -361,8 +361,13 @@ class TTAttention:
                                      _DT[dtype])
 
     def workspace(self, seqs: TTSeqs, backward: bool = True, device="cuda") -> torch.Tensor:
-        return torch.empty(ttc.tt_attn_workspace_size(self.plan, seqs.c, backward),
-                           dtype=torch.uint8, device=device)
+        """Enough for a forward of seqs and, unless backward is False, for a backward
+        (either can be the larger: a few tokens against a long cache need theirs for
+        the forward)."""
+        n = ttc.tt_attn_workspace_size(self.plan, seqs.c, False)
+        if backward:
+            n = max(n, ttc.tt_attn_workspace_size(self.plan, seqs.c, True))
+        return torch.empty(n, dtype=torch.uint8, device=device)
 
     def _heads(self, t: torch.Tensor, rows: int, heads: int, name: str) -> ttc.tt_heads:
         """(rows, heads, dim) of any row and head stride, or (rows, heads * dim)."""

@@ -205,3 +205,48 @@ def test_decode_continues_a_forward(window):
                           [(i, i + 1, f, r + 1) for i, (f, r) in enumerate(zip(first, rows))],
                           **window)
     assert_near(_heads(_f64(bd["att"])), o, ATTN_TOL["bf16"], "attention against the cache")
+
+
+@pytest.mark.parametrize("n", [1, 2, 4, 5])
+@pytest.mark.parametrize("window", [dict(right=0), dict(left=1500, right=0, sinks=4)])
+def test_decode_against_a_long_cache(n, window):
+    """Few sequences and long caches: the keys of a head are split over several
+    clusters, whose shares meet in the workspace of the block's buffers."""
+    from tensor_train_compressed_tt_gb300.layer import TTSeqs
+    room = 2500
+    blk, _, _, params, _, _, x, res, _, _ = _setup((1,) * n, 54, **window)
+    lk = [room - 3 * i for i in range(n)]
+    i32 = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    first = [i * room for i in range(n)]
+    one = TTSeqs(i32(list(range(n))), i32(list(range(1, n + 1))), i32(first),
+                 i32([f + m for f, m in zip(first, lk)]), n, n * room, 1, room)
+    b = blk.buffers(n, one)
+    r = np.random.default_rng(55)
+    keys, values = (torch.from_numpy(r.standard_normal((n * room, HEADS, DIM)).astype(np.float32))
+                    .cuda().bfloat16() for _ in range(2))
+    rows = torch.tensor([f + m - 1 for f, m in zip(first, lk)], device="cuda")
+    blk.decode(x, res, keys, values, rows, one, params, b)
+    assert torch.equal(keys[rows].view(n, N), b["y_k"])
+    assert torch.equal(values[rows].view(n, N), b["y_v"])
+    o, _ = B.attn_forward(_heads(_f64(b["y_q"])), _f64(keys), _f64(values),
+                          [(i, i + 1, f, f + m) for i, (f, m) in enumerate(zip(first, lk))],
+                          **window)
+    assert_near(_heads(_f64(b["att"])), o, ATTN_TOL["bf16"], "attention against the cache")
+
+
+def test_one_workspace_for_both_passes():
+    """TTAttention.workspace's default serves the forward and the backward of its sequences."""
+    from tensor_train_compressed_tt_gb300.layer import TTAttention, TTSeqs
+    i32 = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    op = TTAttention(4, DIM)
+    seqs = TTSeqs(i32([0]), i32([1]), i32([0]), i32([4000]), 1, 4000, 1, 4000)
+    q = torch.randn(1, 4, DIM, device="cuda").bfloat16()
+    k = torch.randn(4000, 4, DIM, device="cuda").bfloat16()
+    ws = op.workspace(seqs)
+    assert ws.numel() >= op.workspace(seqs, False).numel()
+    o, lse = op.forward(q, k, k, seqs, ws=ws)
+    o2, lse2 = op.forward(q, k, k, seqs)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    for a, b in zip(op.backward(q, k, k, o, lse, q, seqs, ws=ws),
+                    op.backward(q, k, k, o, lse, q, seqs)):
+        assert torch.equal(a, b)
