@@ -6,6 +6,7 @@ pointers into one libttc call.  No arithmetic happens here.
 
 from __future__ import annotations
 
+import contextlib
 from typing import Optional, Sequence
 
 import torch
@@ -27,6 +28,11 @@ def _stream(stream: Optional[torch.cuda.Stream]) -> int:
     if stream is not None:
         return int(stream.cuda_stream)
     return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+
+
+def _on(stream: Optional[torch.cuda.Stream]):
+    """Makes the call's stream current for what the wrapper makes itself."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
 def _ptr(t: Optional[torch.Tensor]) -> int:
@@ -278,6 +284,7 @@ class TTNorm:
                  accumulate: bool = False):
         self.N = int(N)
         self.dtype = dtype
+        self.accumulate = bool(accumulate)
         self.plan = ttc.tt_norm_plan(N, eps, _DT[dtype], ttc.TT_ACCUMULATE if accumulate else 0)
 
     def workspace(self, T: int, device="cuda") -> torch.Tensor:
@@ -309,10 +316,12 @@ class TTNorm:
         T, N = s.shape[0], self.N
         if dx is None:
             dx = torch.empty((T, N), dtype=self.dtype, device=s.device)
-        if dgamma is None:
-            dgamma = torch.zeros(N, dtype=torch.float32, device=s.device)
-        if dbeta is None:
-            dbeta = torch.zeros(N, dtype=torch.float32, device=s.device)
+        make = torch.zeros if self.accumulate else torch.empty  # added to, or overwritten
+        with _on(stream):
+            if dgamma is None:
+                dgamma = make(N, dtype=torch.float32, device=s.device)
+            if dbeta is None:
+                dbeta = make(N, dtype=torch.float32, device=s.device)
         if ws is None:
             ws = self.workspace(T, s.device)
         f32, sh = torch.float32, (T, N)

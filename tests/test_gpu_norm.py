@@ -228,3 +228,23 @@ def test_wrapper_refuses():
 def test_many_rows_without_a_residual(T, N, act):
     """Two rows at a time, and the last row of a block alone (from 16 rows an SM)."""
     _case(T, N, act, res=False, seed=T + N)
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_default_gradients_on_a_given_stream(accumulate):
+    """stream= another one than the current, which is busy: the weight gradients
+    that the call makes are the kernel's."""
+    from tensor_train_compressed_tt_gb300.layer import TTNorm
+    r = np.random.default_rng(8)
+    op = TTNorm(768, accumulate=accumulate)
+    x, dy = _rand(r, (300, 768), "bf16"), _rand(r, (300, 768), "bf16")
+    _, _, st = op.forward(x)
+    dx, dg, db = op.backward(x, dy, None, st)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        torch.cuda._sleep(20_000_000)   # some 10 ms
+        got = op.backward(x, dy, None, st, stream=side)
+        torch.cuda.synchronize()
+        for a, b in zip((dx, dg, db), got):
+            assert torch.equal(a, b)
