@@ -6,7 +6,6 @@ pointers into one libttc call.  No arithmetic happens here.
 
 from __future__ import annotations
 
-import contextlib
 from typing import Optional, Sequence
 
 import torch
@@ -30,9 +29,26 @@ def _stream(stream: Optional[torch.cuda.Stream]) -> int:
     return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
-def _on(stream: Optional[torch.cuda.Stream]):
-    """Makes the call's stream current for what the wrapper makes itself."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+def _new(shape, dtype: torch.dtype, device, stream: Optional[torch.cuda.Stream],
+         zero: bool = False) -> torch.Tensor:
+    """An output that the caller did not give: of the memory of the stream that the
+    kernels run on, so that nothing else still uses it there, and held for the
+    caller's stream, which reads it afterwards."""
+    if stream is None:
+        return (torch.zeros if zero else torch.empty)(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = (torch.zeros if zero else torch.empty)(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(t.device))
+    return t
+
+
+def _scratch(stream: Optional[torch.cuda.Stream], workspace, *args) -> torch.Tensor:
+    """A workspace that is dropped at the call's end: of the memory of the call's
+    stream, where it is next used after the call's kernels."""
+    if stream is None:
+        return workspace(*args)
+    with torch.cuda.stream(stream):
+        return workspace(*args)
 
 
 def _ptr(t: Optional[torch.Tensor]) -> int:
@@ -75,9 +91,9 @@ class TTLinear:
                 ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         T = x.shape[0]
         if y is None:
-            y = torch.empty((T, self.M), dtype=self.out_dtype, device=x.device)
+            y = _new((T, self.M), self.out_dtype, x.device, stream)
         if ws is None:
-            ws = self.workspace(T, x.device)
+            ws = _scratch(stream, self.workspace, T, x.device)
         ttc.check(ttc.tt_forward(self.plan, T, _ptr(x), _ptr(params), _ptr(y), _ptr(ws),
                                  ws.numel(), _stream(stream)), "tt_forward")
         return y
@@ -87,11 +103,11 @@ class TTLinear:
                  ws: Optional[torch.Tensor] = None, stream=None):
         T = x.shape[0]
         if dx is None:
-            dx = torch.empty((T, self.N), dtype=self.out_dtype, device=x.device)
+            dx = _new((T, self.N), self.out_dtype, x.device, stream)
         if dparams is None:
-            dparams = torch.empty(self.n_params, dtype=torch.float32, device=x.device)
+            dparams = _new(self.n_params, torch.float32, x.device, stream)
         if ws is None:
-            ws = self.workspace(T, x.device)
+            ws = _scratch(stream, self.workspace, T, x.device)
         ttc.check(ttc.tt_backward(self.plan, T, _ptr(x), _ptr(dy), _ptr(params), _ptr(dx),
                                   _ptr(dparams), _ptr(ws), ws.numel(), _stream(stream)),
                   "tt_backward")
@@ -134,9 +150,9 @@ class TTFFN:
     def forward(self, x, p_up, p_down, y=None, ws=None, stream=None):
         T = x.shape[0]
         if y is None:
-            y = torch.empty((T, self.M), dtype=self.dtype, device=x.device)
+            y = _new((T, self.M), self.dtype, x.device, stream)
         if ws is None:
-            ws = self.workspace(T, x.device)
+            ws = _scratch(stream, self.workspace, T, x.device)
         ttc.check(ttc.tt_ffn_forward(self.plan, T, _ptr(x), _ptr(p_up), _ptr(p_down), _ptr(y),
                                      _ptr(ws), ws.numel(), _stream(stream)), "tt_ffn_forward")
         return y
@@ -145,13 +161,13 @@ class TTFFN:
                  stream=None):
         T = x.shape[0]
         if dx is None:
-            dx = torch.empty((T, self.N), dtype=self.dtype, device=x.device)
+            dx = _new((T, self.N), self.dtype, x.device, stream)
         if dp_up is None:
-            dp_up = torch.empty(self.layout[0][2], dtype=torch.float32, device=x.device)
+            dp_up = _new(self.layout[0][2], torch.float32, x.device, stream)
         if dp_down is None:
-            dp_down = torch.empty(self.layout[1][2], dtype=torch.float32, device=x.device)
+            dp_down = _new(self.layout[1][2], torch.float32, x.device, stream)
         if ws is None:
-            ws = self.workspace(T, x.device)
+            ws = _scratch(stream, self.workspace, T, x.device)
         ttc.check(ttc.tt_ffn_backward(self.plan, T, _ptr(x), _ptr(dy), _ptr(p_up),
                                       _ptr(p_down), _ptr(dx), _ptr(dp_up), _ptr(dp_down),
                                       _ptr(ws), ws.numel(), _stream(stream)),
@@ -193,9 +209,9 @@ class TTMulti:
     def forward(self, x, params, y=None, ws=None, stream=None):
         T = x.shape[0]
         if y is None:
-            y = [torch.empty((T, m), dtype=self.out_dtype, device=x.device) for m in self.M]
+            y = [_new((T, m), self.out_dtype, x.device, stream) for m in self.M]
         if ws is None:
-            ws = self.workspace(T, x.device)
+            ws = _scratch(stream, self.workspace, T, x.device)
         ttc.check(ttc.tt_multi_forward(self.plan, T, _ptr(x), [_ptr(p) for p in params],
                                        [_ptr(t) for t in y], _ptr(ws), ws.numel(),
                                        _stream(stream)), "tt_multi_forward")
@@ -204,12 +220,12 @@ class TTMulti:
     def backward(self, x, dy, params, dx=None, dparams=None, ws=None, stream=None):
         T = x.shape[0]
         if dx is None:
-            dx = torch.empty((T, self.N), dtype=self.out_dtype, device=x.device)
+            dx = _new((T, self.N), self.out_dtype, x.device, stream)
         if dparams is None:
-            dparams = [torch.empty(lay[2], dtype=torch.float32, device=x.device)
+            dparams = [_new(lay[2], torch.float32, x.device, stream)
                        for lay in self.layout]
         if ws is None:
-            ws = self.workspace(T, x.device)
+            ws = _scratch(stream, self.workspace, T, x.device)
         ttc.check(ttc.tt_multi_backward(self.plan, T, _ptr(x), [_ptr(t) for t in dy],
                                         [_ptr(p) for p in params], _ptr(dx),
                                         [_ptr(t) for t in dparams], _ptr(ws), ws.numel(),
@@ -242,9 +258,9 @@ class TTMEmbedding:
     def lookup(self, idx: torch.Tensor, params: torch.Tensor, out=None, ws=None, stream=None):
         B = idx.shape[0]
         if out is None:
-            out = torch.empty((B, self.Dm), dtype=torch.float32, device=idx.device)
+            out = _new((B, self.Dm), torch.float32, idx.device, stream)
         if ws is None:
-            ws = self.workspace(B, idx.device)
+            ws = _scratch(stream, self.workspace, B, idx.device)
         ttc.check(ttc.tt_ttm_lookup(self.plan, B, _ptr(idx), _ptr(params), _ptr(out), _ptr(ws),
                                     ws.numel(), _stream(stream)), "tt_ttm_lookup")
         return out
@@ -253,9 +269,9 @@ class TTMEmbedding:
                  dparams=None, ws=None, stream=None):
         B = idx.shape[0]
         if dparams is None:
-            dparams = torch.empty(self.n_params, dtype=torch.float32, device=idx.device)
+            dparams = _new(self.n_params, torch.float32, idx.device, stream)
         if ws is None:
-            ws = self.workspace(B, idx.device)
+            ws = _scratch(stream, self.workspace, B, idx.device)
         ttc.check(ttc.tt_ttm_lookup_backward(self.plan, B, _ptr(idx), _ptr(dout), _ptr(params),
                                              _ptr(dparams), _ptr(ws), ws.numel(),
                                              _stream(stream)), "tt_ttm_lookup_backward")
@@ -296,11 +312,11 @@ class TTNorm:
         holds each row's mean and 1 / sqrt(var + eps) for the backward."""
         T, N = x.shape[0], self.N
         if y is None:
-            y = torch.empty((T, N), dtype=self.dtype, device=x.device)
+            y = _new((T, N), self.dtype, x.device, stream)
         if res is not None and sum is None:
-            sum = torch.empty((T, N), dtype=self.dtype, device=x.device)
+            sum = _new((T, N), self.dtype, x.device, stream)
         if stats is None:
-            stats = torch.empty((T, 2), dtype=torch.float32, device=x.device)
+            stats = _new((T, 2), torch.float32, x.device, stream)
         f32, sh = torch.float32, (T, N)
         ttc.check(ttc.tt_norm_forward(
             self.plan, T, _dense(x, sh, self.dtype, "x"), _dense(res, sh, self.dtype, "res"),
@@ -315,15 +331,13 @@ class TTNorm:
         the gradient that reaches s along the residual path."""
         T, N = s.shape[0], self.N
         if dx is None:
-            dx = torch.empty((T, N), dtype=self.dtype, device=s.device)
-        make = torch.zeros if self.accumulate else torch.empty  # added to, or overwritten
-        with _on(stream):
-            if dgamma is None:
-                dgamma = make(N, dtype=torch.float32, device=s.device)
-            if dbeta is None:
-                dbeta = make(N, dtype=torch.float32, device=s.device)
+            dx = _new((T, N), self.dtype, s.device, stream)
+        if dgamma is None:  # added to, or overwritten
+            dgamma = _new(N, torch.float32, s.device, stream, zero=self.accumulate)
+        if dbeta is None:
+            dbeta = _new(N, torch.float32, s.device, stream, zero=self.accumulate)
         if ws is None:
-            ws = self.workspace(T, s.device)
+            ws = _scratch(stream, self.workspace, T, s.device)
         f32, sh = torch.float32, (T, N)
         ttc.check(ttc.tt_norm_backward(
             self.plan, T, _dense(s, sh, self.dtype, "s"), _dense(dy, sh, self.dtype, "dy"),
@@ -395,11 +409,11 @@ class TTAttention:
     def forward(self, q, k, v, seqs: TTSeqs, o=None, lse=None, ws=None, stream=None):
         """(o, lse); o like q but dense, lse (heads, Tq) fp32."""
         if o is None:
-            o = torch.empty(q.shape, dtype=self.dtype, device=q.device)
+            o = _new(q.shape, self.dtype, q.device, stream)
         if lse is None:
-            lse = torch.empty((self.heads, seqs.Tq), dtype=torch.float32, device=q.device)
+            lse = _new((self.heads, seqs.Tq), torch.float32, q.device, stream)
         if ws is None:
-            ws = self.workspace(seqs, False, q.device)
+            ws = _scratch(stream, self.workspace, seqs, False, q.device)
         H, G = self.heads, self.kv_heads
         ttc.check(ttc.tt_attn_forward(
             self.plan, seqs.c, self._heads(q, seqs.Tq, H, "q"), self._heads(k, seqs.Tk, G, "k"),
@@ -412,13 +426,13 @@ class TTAttention:
                  stream=None):
         """(dq, dk, dv) for the gradient do of o."""
         if dq is None:
-            dq = torch.empty(q.shape, dtype=self.dtype, device=q.device)
+            dq = _new(q.shape, self.dtype, q.device, stream)
         if dk is None:
-            dk = torch.empty(k.shape, dtype=self.dtype, device=q.device)
+            dk = _new(k.shape, self.dtype, q.device, stream)
         if dv is None:
-            dv = torch.empty(v.shape, dtype=self.dtype, device=q.device)
+            dv = _new(v.shape, self.dtype, q.device, stream)
         if ws is None:
-            ws = self.workspace(seqs, True, q.device)
+            ws = _scratch(stream, self.workspace, seqs, True, q.device)
         H, G = self.heads, self.kv_heads
         ttc.check(ttc.tt_attn_backward(
             self.plan, seqs.c, self._heads(q, seqs.Tq, H, "q"), self._heads(k, seqs.Tk, G, "k"),

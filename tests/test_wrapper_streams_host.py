@@ -72,3 +72,71 @@ def test_norm_weight_gradients_are_filled_on_the_calls_stream(made, accumulate):
     assert fills == ([s, s] if accumulate else [])   # overwritten unless added to
     if accumulate:
         assert float(dg.abs().max()) == 0 and float(db.abs().max()) == 0
+
+
+def _attn():
+    op = layer.TTAttention(2, 32, dtype=torch.float32)
+    off = torch.tensor([0, 4], dtype=torch.int32)
+    return op, torch.ones(4, 2, 32), layer.TTSeqs.packed(off, 4, 4)
+
+
+def _run_norm(s):
+    op, x, st = _norm()
+    op.forward(x, res=x, stream=s)
+    op.backward(x, x, None, st, stream=s)
+
+
+def _run_attn(s):
+    op, q, seqs = _attn()
+    o, lse = op.forward(q, q, q, seqs, stream=s)
+    op.backward(q, q, q, o, lse, q, seqs, stream=s)
+
+
+def _run_linear(s):
+    op = layer.TTLinear((4, 4), (4, 4), (1, 4, 4, 4, 1), torch.float32)
+    x, p = torch.ones(3, 16), torch.ones(op.n_params)
+    op.forward(x, p, stream=s)
+    op.backward(x, x, p, stream=s)
+
+
+def _run_ffn(s):
+    m = ((4, 4), (4, 4), (1, 4, 4, 4, 1))
+    op = layer.TTFFN(m, m, torch.float32)
+    x, p = torch.ones(3, 16), torch.ones(200)
+    op.forward(x, p, p, stream=s)
+    op.backward(x, x, p, p, stream=s)
+
+
+def _run_multi(s):
+    m = ((4, 4), (4, 4), (1, 4, 4, 4, 1))
+    op = layer.TTMulti([m, m], torch.float32)
+    x, p = torch.ones(3, 16), torch.ones(200)
+    op.forward(x, [p, p], stream=s)
+    op.backward(x, [x, x], [p, p], stream=s)
+
+
+def _run_ttm(s):
+    op = layer.TTMEmbedding((4, 4), (4, 4), (1, 4, 1))
+    idx, p = torch.ones(3, dtype=torch.int32), torch.ones(op.n_params)
+    out = op.lookup(idx, p, stream=s)
+    op.backward(idx, out, p, stream=s)
+
+
+RUNS = [_run_norm, _run_attn, _run_linear, _run_ffn, _run_multi, _run_ttm]
+
+
+@pytest.mark.parametrize("run", RUNS)
+def test_memory_is_the_calls_streams(made, monkeypatch, run):
+    """Outputs and workspaces that the caller does not give: from the memory of the
+    stream that the kernels run on, where a workspace that is dropped at the call's
+    end is next used after them; outputs are held for the caller's stream too."""
+    log, held = made
+    monkeypatch.setattr(layer.TTAttention, "_heads", lambda *a: None)
+    inside = FakeStream()
+    run(inside)
+    mine = [at for _, at in log]
+    assert mine and all(at is inside for at in mine)
+    assert held and all(s == "current" for _, s in held)
+    del log[:], held[:]
+    run(None)
+    assert log and all(at is None for _, at in log) and not held
