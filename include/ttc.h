@@ -455,7 +455,9 @@ tt_status tt_attn_backward(const tt_plan_t* plan, const tt_attn_seqs* seqs, cons
  * of the CTA, on a grid barrier) is bounded: after the limit it records
  * TT_ERR_TIMEOUT in the device status word, tells the CTA's other warps to
  * stop, waits (bounded) for its own copies and MMAs, frees its tensor memory
- * and returns, leaving the context usable.  Not part of the CoMERA method. */
+ * and returns, leaving the context usable.  Not part of the CoMERA method.
+ * In the attention kernels a wait's limit counts from the last tile that its CTA
+ * worked on: one piece of their work may be as long as the sequences are. */
 
 /* The limit of those waits on the current device, in nanoseconds of the
  * global timer (default 2e9, at least 1000).  Applies to kernels launched

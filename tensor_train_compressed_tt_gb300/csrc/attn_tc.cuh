@@ -75,25 +75,48 @@ __device__ __forceinline__ TileList key_list(const KeySpan& ks, int h) {
 // The wait for a load of one's own on the way out.
 __device__ __noinline__ void drain_one(uint64_t* b, uint32_t parity) { drain_bar(b, parity); }
 
+// What a CTA's waits look at: set when one has run out, and the number of the tile whose
+// product was issued last.
+struct WaitFlags {
+  int abort, tile;
+};
+
 // Waits of these kernels: one try in line, everything else out of line.  The
 // roles of all CTAs of an SM share its instruction cache, and a hand-over
 // between two roles is short, so the out-of-line part polls for a while
-// before it looks at the timer, whose limit is a load from global memory.
-__device__ __noinline__ bool wait_long(uint64_t* b, uint32_t parity, volatile int* abort_flag,
+// before it looks at the timer, whose limit is a load from global memory.  The
+// limit counts from the last tile that was worked on: the warps that write wait for all
+// of an item, and its list of tiles may be as long as the sequences are.
+__device__ __noinline__ bool wait_long(uint64_t* b, uint32_t parity, volatile WaitFlags* flags,
                                        unsigned where) {
 #pragma unroll 1
   for (int i = 0; i < 256; ++i)
     if (mbar_try_wait(b, parity)) return true;
-  return wait_bar(b, parity, abort_flag, where);
+  const uint64_t limit = *(volatile unsigned long long*)&g_wait_limit_ns;
+  uint64_t since = gtimer();
+  int tile = flags->tile;
+  while (!mbar_try_wait(b, parity)) {
+    if (flags->abort) return false;
+    const int now = flags->tile;
+    if (now != tile) {
+      tile = now;
+      since = gtimer();
+    } else if (gtimer() - since > limit) {
+      flags->abort = 1;
+      record_error(TT_ERR_TIMEOUT, where);
+      return false;
+    }
+  }
+  return true;
 }
-__device__ __forceinline__ bool wait_one(uint64_t* b, uint32_t parity, volatile int* abort_flag,
+__device__ __forceinline__ bool wait_one(uint64_t* b, uint32_t parity, volatile WaitFlags* flags,
                                          unsigned where) {
-  return mbar_try_wait(b, parity) || wait_long(b, parity, abort_flag, where);
+  return mbar_try_wait(b, parity) || wait_long(b, parity, flags, where);
 }
 // Every lane of a converged warp waits; the warp is converged after it.
-__device__ __forceinline__ bool wait_all(uint64_t* b, uint32_t parity, volatile int* abort_flag,
+__device__ __forceinline__ bool wait_all(uint64_t* b, uint32_t parity, volatile WaitFlags* flags,
                                          unsigned where) {
-  return __all_sync(0xffffffffu, wait_one(b, parity, abort_flag, where));
+  return __all_sync(0xffffffffu, wait_one(b, parity, flags, where));
 }
 // One lane of a converged warp.
 __device__ __forceinline__ bool elect_lane() {

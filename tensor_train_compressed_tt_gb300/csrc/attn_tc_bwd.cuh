@@ -92,7 +92,7 @@ struct TcBwd {
     alignas(16) float col[KV ? BUF : 1][2][2][KV ? YT : 4];  // lse and delta of a tile's queries
     float half[2][KV ? 1 : BUF + 1][KV ? 1 : AT];  // each buffer's sums of ds, then delta
     uint32_t tmem;
-    int abort_flag, never;
+    WaitFlags flags, never;
   };
   static constexpr size_t kSmem = XS * XSET + 2 * KP * UNIT + sizeof(Shared) + 1024;
   static_assert(ACC + 2 * 64 * NB <= COLS, "tensor memory");
@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(TcBwd<KV, NB>::THREADS, 1)
     mbar_init(&S.clc, 1);
     mbar_init(&S.fin, 1);
     mbar_init(&S.fin2, 1);
-    S.abort_flag = S.never = 0;
+    S.flags = S.never = WaitFlags{0, 0};
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == WARPS + 5) tmem_take(&S.tmem, C::COLS);
@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(TcBwd<KV, NB>::THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = S.tmem;
-  volatile int* abort_flag = &S.abort_flag;
+  volatile WaitFlags* flags = &S.flags;
 
   if (warp == WARPS + 4) {
     // ---------------- work and loads
@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(TcBwd<KV, NB>::THREADS, 1)
             continue;
           }
           const int slot = n % C::ITEMS;
-          ok = wait_one(&S.item_empty[slot], ((n / C::ITEMS) & 1) ^ 1, abort_flag, 120);
+          ok = wait_one(&S.item_empty[slot], ((n / C::ITEMS) & 1) ^ 1, flags, 120);
           if (!ok) {
             w.nt = -1;
             continue;
@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(TcBwd<KV, NB>::THREADS, 1)
         }
         if (ok && cur.nt > 0) {
           const int xs = nload % XS;
-          ok = wait_one(&S.x_empty[xs], ((nload / XS) & 1) ^ 1, abort_flag, 121);
+          ok = wait_one(&S.x_empty[xs], ((nload / XS) & 1) ^ 1, flags, 121);
           if (ok) {
             const int row = (int)cur.x0 + cur.r0;
             uint8_t* dst = xbuf + xs * C::XSET;
@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(TcBwd<KV, NB>::THREADS, 1)
           TileList l = cur.list;
 #pragma unroll 1
           for (int t = 0; ok && t < cur.nt; ++t) {
-            ok = wait_one(&S.y_empty[s], ph, abort_flag, 122);
+            ok = wait_one(&S.y_empty[s], ph, flags, 122);
             if (!ok) break;
             S.rows[s] = l.rows(YT);
             mbar_expect_tx(&S.y_full[s], 2 * C::UNIT);
@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(TcBwd<KV, NB>::THREADS, 1)
         if (w.nt < 0) break;
         cur = w;
       }
-      if (ok && wait_one(&S.item_empty[n % C::ITEMS], ((n / C::ITEMS) & 1) ^ 1, abort_flag, 124)) {
+      if (ok && wait_one(&S.item_empty[n % C::ITEMS], ((n / C::ITEMS) & 1) ^ 1, flags, 124)) {
         S.item[n % C::ITEMS].nt = -1;
         mbar_arrive(&S.item_full[n % C::ITEMS]);
       }
@@ -336,20 +336,20 @@ __global__ void __launch_bounds__(TcBwd<KV, NB>::THREADS, 1)
     bool ok = true;
 #pragma unroll 1
     for (int n = 0; ok; ++n) {
-      if (!wait_all(&S.item_full[n % C::ITEMS], (n / C::ITEMS) & 1, abort_flag, 125)) break;
+      if (!wait_all(&S.item_full[n % C::ITEMS], (n / C::ITEMS) & 1, flags, 125)) break;
       const int nt = S.item[n % C::ITEMS].nt;
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.item_empty[n % C::ITEMS]);
       if (nt < 0) break;
       if (nt == 0) continue;
       const int xs = nload % XS;
-      ok = wait_all(&S.x_full[xs], (nload / XS) & 1, abort_flag, 126);
+      ok = wait_all(&S.x_full[xs], (nload / XS) & 1, flags, 126);
       const uint64_t x = kdesc(su32(xbuf + xs * C::XSET));
 #pragma unroll 1
       for (int t = 0; ok && t < nt; ++t) {
         // the p and ds that lie over the buffer have been summed
-        ok = wait_all(&S.y_full[s], ph, abort_flag, 128) &&
-             wait_all(&S.done[b], pb, abort_flag, 127);
+        ok = wait_all(&S.y_full[s], ph, flags, 128) &&
+             wait_all(&S.done[b], pb, flags, 127);
         if (!ok) break;
         tc_fence_after();
         const int ny = S.rows[s];
@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(TcBwd<KV, NB>::THREADS, 1)
     bool ok = true;
 #pragma unroll 1
     for (int n = 0; ok; ++n) {
-      if (!wait_all(&S.item_full[n % C::ITEMS], (n / C::ITEMS) & 1, abort_flag, 139)) break;
+      if (!wait_all(&S.item_full[n % C::ITEMS], (n / C::ITEMS) & 1, flags, 139)) break;
       const int nt = S.item[n % C::ITEMS].nt;
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.item_empty[n % C::ITEMS]);
@@ -388,15 +388,15 @@ __global__ void __launch_bounds__(TcBwd<KV, NB>::THREADS, 1)
       if (nt == 0) continue;
 #pragma unroll 1
       for (int t = 0; ok && t < nt; ++t) {
-        ok = wait_all(&S.y_full[s], ph, abort_flag, 140);
+        ok = wait_all(&S.y_full[s], ph, flags, 140);
         if (!ok) break;
         const int ny = S.rows[s];
         uint8_t* y = ybuf + 2 * s * C::UNIT;
         zero_tail<NB>(y, C::YBOX, ny, lane);
         if (KV) zero_tail<NB>(y + C::UNIT, C::YBOX, ny, lane);
         // (the first: the item before has read its accumulators)
-        ok = (t > 0 || wait_all(&S.acc_free, (nload & 1) ^ 1, abort_flag, 129)) &&
-             wait_all(&S.p_full[b], pb, abort_flag, 130);
+        ok = (t > 0 || wait_all(&S.acc_free, (nload & 1) ^ 1, flags, 129)) &&
+             wait_all(&S.p_full[b], pb, flags, 130);
         if (!ok) break;
         tc_fence_after();
         if (elect_lane()) {
@@ -408,6 +408,7 @@ __global__ void __launch_bounds__(TcBwd<KV, NB>::THREADS, 1)
           mma_commit(&S.done[b]);
           mma_commit(&S.y_empty[s]);
           if (t == nt - 1) mma_commit(&S.acc_full);
+          flags->tile = t;
         }
         __syncwarp();
         if (++s == KP) s = 0, ph ^= 1;
@@ -433,7 +434,7 @@ __global__ void __launch_bounds__(TcBwd<KV, NB>::THREADS, 1)
     bool ok = true;
 #pragma unroll 1
     for (int n = 0; ok; ++n) {
-      if (!wait_all(&S.item_full[n % C::ITEMS], (n / C::ITEMS) & 1, abort_flag, 131)) break;
+      if (!wait_all(&S.item_full[n % C::ITEMS], (n / C::ITEMS) & 1, flags, 131)) break;
       const BwdItem w = S.item[n % C::ITEMS];
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.item_empty[n % C::ITEMS]);
@@ -448,7 +449,7 @@ __global__ void __launch_bounds__(TcBwd<KV, NB>::THREADS, 1)
       }
       if (!KV && w.nt > 0) {
         const int xs = nload % XS;
-        if (!wait_all(&S.x_full[xs], (nload / XS) & 1, abort_flag, 138)) break;
+        if (!wait_all(&S.x_full[xs], (nload / XS) & 1, flags, 138)) break;
         const uint8_t* x = xbuf + xs * C::XSET;
         if (in) rl.y = -row_delta<NB>(x + 2 * NB * ABOX, x + NB * ABOX, row, p.dim);
         __syncwarp();
@@ -492,7 +493,7 @@ __global__ void __launch_bounds__(TcBwd<KV, NB>::THREADS, 1)
           low = wl - 31;
         }
         const int end = 32 * quad < w.nx ? min(ny, up + 1) : 0;
-        if (!wait_all(&S.s_full[buf], ps, abort_flag, 132)) { ok = false; break; }
+        if (!wait_all(&S.s_full[buf], ps, flags, 132)) { ok = false; break; }
         ps ^= 1;
         tc_fence_after();
         const float* col = nullptr;
@@ -503,7 +504,7 @@ __global__ void __launch_bounds__(TcBwd<KV, NB>::THREADS, 1)
           col = dst;
           __syncwarp();
           if (lane == 0) mbar_arrive(&S.col_full[buf]);
-          if (!wait_all(&S.col_full[buf], flip, abort_flag, 134)) { ok = false; break; }
+          if (!wait_all(&S.col_full[buf], flip, flags, 134)) { ok = false; break; }
           flip ^= 1;
         }
         // 16 columns at a time: more would not fit the registers of as many warps
@@ -571,7 +572,7 @@ __global__ void __launch_bounds__(TcBwd<KV, NB>::THREADS, 1)
       if (w.nt > 0) {
         if (!KV) {  // for the warps that write
           const int half = nload & 1;
-          if (!wait_all(&S.half_free[half], ((nload >> 1) & 1) ^ 1, abort_flag, 134)) break;
+          if (!wait_all(&S.half_free[half], ((nload >> 1) & 1) ^ 1, flags, 134)) break;
           S.half[half][buf][row] = ds2.x + ds2.y;
           if (buf == 0) S.half[half][KV ? 0 : BUF][row] = -rl.y;
           __syncwarp();
@@ -587,7 +588,7 @@ __global__ void __launch_bounds__(TcBwd<KV, NB>::THREADS, 1)
     int nload = 0, turn = 0;  // turn: buffer of the item's first tile
 #pragma unroll 1
     for (int n = 0;; ++n) {
-      if (!wait_all(&S.item_full[n % C::ITEMS], (n / C::ITEMS) & 1, abort_flag, 141)) break;
+      if (!wait_all(&S.item_full[n % C::ITEMS], (n / C::ITEMS) & 1, flags, 141)) break;
       const BwdItem w = S.item[n % C::ITEMS];
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.item_empty[n % C::ITEMS]);
@@ -597,7 +598,7 @@ __global__ void __launch_bounds__(TcBwd<KV, NB>::THREADS, 1)
       float err = 0.f, delta = 0.f;  // sum of the row's ds
       if (!KV && some) {
         const int half = nload & 1;
-        if (!wait_all(&S.half_full[half], (nload >> 1) & 1, abort_flag, 135)) break;
+        if (!wait_all(&S.half_full[half], (nload >> 1) & 1, flags, 135)) break;
         // In the order of the tiles: which buffer an item begins with depends on the
         // items that the CTA has taken before.
 #pragma unroll
@@ -612,7 +613,7 @@ __global__ void __launch_bounds__(TcBwd<KV, NB>::THREADS, 1)
       }
       if (!KV && in) p.delta[(int64_t)w.hx * p.Tq + xr] = delta;
       if (some) {
-        if (!wait_all(&S.acc_full, nload & 1, abort_flag, 133)) break;
+        if (!wait_all(&S.acc_full, nload & 1, flags, 133)) break;
         tc_fence_after();
         ++nload;
       }

@@ -73,7 +73,7 @@ struct TcFwd {
     int rows[2 * KP];  // keys of a tile, by its number (a key tile's place is free before
                        // the product of its values has read this)
     uint32_t tmem;
-    int abort_flag, never;
+    WaitFlags flags, never;
   };
   static constexpr size_t kSmem = QS * NB * ABOX + 2 * KP * UNIT + sizeof(Shared) + 1024;
 };
@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(kTcThreads, TcFwd<NB>::CTAS)
     mbar_init(&S.clc, 1);
     mbar_init(&S.fin, 1);
     mbar_init(&S.fin2, 1);
-    S.abort_flag = S.never = 0;
+    S.flags = S.never = WaitFlags{0, 0};
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 5) tmem_take(&S.tmem, C::COLS);
@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(kTcThreads, TcFwd<NB>::CTAS)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = S.tmem;
-  volatile int* abort_flag = &S.abort_flag;
+  volatile WaitFlags* flags = &S.flags;
 
   if (warp == 4) {
     // ---------------- work and loads
@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(kTcThreads, TcFwd<NB>::CTAS)
             continue;
           }
           const int slot = n % C::ITEMS;
-          ok = wait_one(&S.item_empty[slot], ((n / C::ITEMS) & 1) ^ 1, abort_flag, 96);
+          ok = wait_one(&S.item_empty[slot], ((n / C::ITEMS) & 1) ^ 1, flags, 96);
           if (!ok) {
             w.nt = -1;
             continue;
@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(kTcThreads, TcFwd<NB>::CTAS)
         }
         if (ok && cur.nt > 0) {
           const int qs = nload % QS;
-          ok = wait_one(&S.q_empty[qs], ((nload / QS) & 1) ^ 1, abort_flag, 97);
+          ok = wait_one(&S.q_empty[qs], ((nload / QS) & 1) ^ 1, flags, 97);
           if (ok) {
             mbar_expect_tx(&S.q_full[qs], NB * ABOX);
             load_tile<NB>(qbuf + qs * NB * ABOX, ABOX, &tm_q, &S.q_full[qs], cur.h,
@@ -262,13 +262,13 @@ __global__ void __launch_bounds__(kTcThreads, TcFwd<NB>::CTAS)
           TileList l = cur.keys;
 #pragma unroll 1
           for (int t = 0; ok && t < cur.nt; ++t) {
-            ok = wait_one(&S.k_empty[s], ph, abort_flag, 98);
+            ok = wait_one(&S.k_empty[s], ph, flags, 98);
             if (!ok) break;
             S.rows[loads % (2 * KP)] = l.rows(KT);
             uint8_t* dst = kvbuf + 2 * s * C::UNIT;
             mbar_expect_tx(&S.k_full[s], C::UNIT);
             load_tile<NB>(dst, C::KBOX, &tm_k, &S.k_full[s], l.h, (int)cur.k0 + l.r);
-            ok = wait_one(&S.v_empty[s], ph, abort_flag, 94);
+            ok = wait_one(&S.v_empty[s], ph, flags, 94);
             if (!ok) {
               drain_one(&S.k_full[s], ph ^ 1);
               break;
@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(kTcThreads, TcFwd<NB>::CTAS)
         if (w.nt < 0) break;
         cur = w;
       }
-      if (ok && wait_one(&S.item_empty[n % C::ITEMS], ((n / C::ITEMS) & 1) ^ 1, abort_flag, 99)) {
+      if (ok && wait_one(&S.item_empty[n % C::ITEMS], ((n / C::ITEMS) & 1) ^ 1, flags, 99)) {
         S.item[n % C::ITEMS].nt = -1;
         mbar_arrive(&S.item_full[n % C::ITEMS]);
       }
@@ -306,20 +306,20 @@ __global__ void __launch_bounds__(kTcThreads, TcFwd<NB>::CTAS)
     bool ok = true;
 #pragma unroll 1
     for (int n = 0; ok; ++n) {
-      if (!wait_all(&S.item_full[n % C::ITEMS], (n / C::ITEMS) & 1, abort_flag, 100)) break;
+      if (!wait_all(&S.item_full[n % C::ITEMS], (n / C::ITEMS) & 1, flags, 100)) break;
       const int nt = S.item[n % C::ITEMS].nt;
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.item_empty[n % C::ITEMS]);
       if (nt < 0) break;
       if (nt == 0) continue;
       const int qs = nload % QS;
-      ok = wait_all(&S.q_full[qs], (nload / QS) & 1, abort_flag, 101);
+      ok = wait_all(&S.q_full[qs], (nload / QS) & 1, flags, 101);
       const uint64_t q = kdesc(su32(qbuf + qs * NB * ABOX));
 #pragma unroll 1
       for (int t = 0; ok && t < nt; ++t, ++g) {
         // S of tile g goes where P of tile g - 2 was
-        ok = wait_all(&S.k_full[s], ph, abort_flag, 102) &&
-             (g < 2 || wait_all(&S.pv_done[g & 1], ((g >> 1) - 1) & 1, abort_flag, 103));
+        ok = wait_all(&S.k_full[s], ph, flags, 102) &&
+             (g < 2 || wait_all(&S.pv_done[g & 1], ((g >> 1) - 1) & 1, flags, 103));
         if (!ok) break;
         tc_fence_after();
         const int nk = S.rows[g % (2 * KP)];
@@ -348,7 +348,7 @@ __global__ void __launch_bounds__(kTcThreads, TcFwd<NB>::CTAS)
     bool ok = true;
 #pragma unroll 1
     for (int n = 0; ok; ++n) {
-      if (!wait_all(&S.item_full[n % C::ITEMS], (n / C::ITEMS) & 1, abort_flag, 104)) break;
+      if (!wait_all(&S.item_full[n % C::ITEMS], (n / C::ITEMS) & 1, flags, 104)) break;
       const int nt = S.item[n % C::ITEMS].nt;
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.item_empty[n % C::ITEMS]);
@@ -356,14 +356,14 @@ __global__ void __launch_bounds__(kTcThreads, TcFwd<NB>::CTAS)
       if (nt == 0) continue;
 #pragma unroll 1
       for (int t = 0; ok && t < nt; ++t, ++g) {
-        ok = wait_all(&S.v_full[s], ph, abort_flag, 105);
+        ok = wait_all(&S.v_full[s], ph, flags, 105);
         if (!ok) break;
         const int nk = S.rows[g % (2 * KP)];
         uint8_t* vt = kvbuf + (2 * s + 1) * C::UNIT;
         zero_tail<NB>(vt, C::KBOX, nk, lane);
         // (the first: the item before has read its O)
-        ok = (t > 0 || wait_all(&S.o_free, (nload & 1) ^ 1, abort_flag, 106)) &&
-             wait_all(&S.p_full[g & 1], (g >> 1) & 1, abort_flag, 107);
+        ok = (t > 0 || wait_all(&S.o_free, (nload & 1) ^ 1, flags, 106)) &&
+             wait_all(&S.p_full[g & 1], (g >> 1) & 1, flags, 107);
         if (!ok) break;
         tc_fence_after();
         if (elect_lane()) {
@@ -371,6 +371,7 @@ __global__ void __launch_bounds__(kTcThreads, TcFwd<NB>::CTAS)
                  (nk + 15) >> 4, t > 0);
           mma_commit(&S.pv_done[g & 1]);
           mma_commit(&S.v_empty[s]);
+          flags->tile = g;
         }
         __syncwarp();
         if (++s == KP) s = 0, ph ^= 1;
@@ -392,7 +393,7 @@ __global__ void __launch_bounds__(kTcThreads, TcFwd<NB>::CTAS)
     bool ok = true;
 #pragma unroll 1
     for (int n = 0; ok; ++n) {
-      if (!wait_all(&S.item_full[n % C::ITEMS], (n / C::ITEMS) & 1, abort_flag, 108)) break;
+      if (!wait_all(&S.item_full[n % C::ITEMS], (n / C::ITEMS) & 1, flags, 108)) break;
       const FwdItem w = S.item[n % C::ITEMS];
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.item_empty[n % C::ITEMS]);
@@ -413,7 +414,7 @@ __global__ void __launch_bounds__(kTcThreads, TcFwd<NB>::CTAS)
         const int sk = p.sinks - j0;
         const int end = 32 * warp < w.nq ? min(nk, wh + 32) : 0;  // past the keys of any row
         float2 s2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        if (!wait_all(&S.s_full[g & 1], (g >> 1) & 1, abort_flag, 109)) { ok = false; break; }
+        if (!wait_all(&S.s_full[g & 1], (g >> 1) & 1, flags, 109)) { ok = false; break; }
         tc_fence_after();
 #pragma unroll 1
         for (int q = 0; q < nk; q += 32) {
@@ -460,7 +461,7 @@ __global__ void __launch_bounds__(kTcThreads, TcFwd<NB>::CTAS)
         __syncwarp();
         if (lane == 0) mbar_arrive(&S.p_full[g & 1]);
       }
-      ok = ok && wait_all(&S.stat_free, (n & 1) ^ 1, abort_flag, 110);
+      ok = ok && wait_all(&S.stat_free, (n & 1) ^ 1, flags, 110);
       S.m[row] = m;
       S.l[row] = l;
       __syncwarp();
@@ -474,13 +475,13 @@ __global__ void __launch_bounds__(kTcThreads, TcFwd<NB>::CTAS)
     int g = 0;
 #pragma unroll 1
     for (int n = 0;; ++n) {
-      if (!wait_all(&S.item_full[n % C::ITEMS], (n / C::ITEMS) & 1, abort_flag, 112)) break;
+      if (!wait_all(&S.item_full[n % C::ITEMS], (n / C::ITEMS) & 1, flags, 112)) break;
       const FwdItem w = S.item[n % C::ITEMS];
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.item_empty[n % C::ITEMS]);
       if (w.nt < 0) break;
       g += w.nt;
-      if (!wait_all(&S.stat_full, n & 1, abort_flag, 113)) break;
+      if (!wait_all(&S.stat_full, n & 1, flags, 113)) break;
       const float m = S.m[row], l = S.l[row];
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.stat_free);
@@ -498,7 +499,7 @@ __global__ void __launch_bounds__(kTcThreads, TcFwd<NB>::CTAS)
       // One barrier for even and one for odd tiles: the product of tile g - 3 was
       // done before S of tile g - 1 came, and that before the statistics, so the
       // parity is not taken for another's.
-      if (!wait_all(&S.pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, abort_flag, 111)) break;
+      if (!wait_all(&S.pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, flags, 111)) break;
       tc_fence_after();
       const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
 #pragma unroll 1

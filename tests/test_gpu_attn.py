@@ -453,3 +453,45 @@ def test_gradients_repeat_whatever_block_takes_the_work(dim):
         other = torch.randn(int(r.integers(1, 4000)), 1024, device="cuda").sum()  # noqa: F841
         for a, b in zip(first, run()):
             assert torch.equal(a, b)
+
+
+@pytest.fixture
+def wait_limit():
+    """Sets the limit of the kernels' waits (for kernels that have run once before)."""
+    from tensor_train_compressed_tt_gb300 import ttc
+
+    def to(ns):
+        torch.cuda.synchronize()
+        ttc.check(ttc.tt_set_wait_limit_ns(ns), "tt_set_wait_limit_ns")
+    yield to
+    to(2_000_000_000)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("heads,kv,lq,lk", [(1, 1, 128, 200000), (128, 1, 4096, 4096)])
+def test_no_wait_counts_a_whole_list_of_tiles(wait_limit, heads, kv, lq, lk, dim):
+    """One tile of queries against 200,000 keys, and keys that 128 heads of 4096
+    queries share: pieces of work of milliseconds under a limit of 0.3 ms, which
+    holds for what a wait is for (some microseconds), not for a piece."""
+    from tensor_train_compressed_tt_gb300 import ttc
+    from tensor_train_compressed_tt_gb300.layer import TTAttention, TTSeqs
+    g = torch.Generator(device="cuda")
+    g.manual_seed(22)
+    q, do = (torch.randn(lq, heads, dim, generator=g, device="cuda").bfloat16() for _ in range(2))
+    k, v = (torch.randn(lk, kv, dim, generator=g, device="cuda").bfloat16() for _ in range(2))
+    i32 = lambda *a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    seqs = TTSeqs(i32(0), i32(lq), i32(0), i32(lk), lq, lk, lq, lk)
+    op = TTAttention(heads, dim, kv_heads=kv)
+
+    def run():
+        o, lse = op.forward(q, k, v, seqs)
+        return [o, lse] + list(op.backward(q, k, v, o, lse, do, seqs))
+
+    st = torch.cuda.current_stream().cuda_stream
+    want = run()
+    assert ttc.tt_get_device_status(st) == 0
+    wait_limit(300_000)
+    got = run()
+    assert ttc.tt_get_device_status(st) == 0
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
