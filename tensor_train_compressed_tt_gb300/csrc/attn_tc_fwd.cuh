@@ -10,17 +10,24 @@
 // The reference m of a row need not be its maximum, only near enough that
 // nothing overflows: bf16 and fp32 share their exponents, and the division by
 // l takes m out again.  So m is the maximum of the first 32 keys that the row
-// sees, and stays: no pass for the maximum, no rescaling of O.  A row whose
-// scores rise by more than 60 powers of two over those first keys shows in l,
-// and is computed again by itself with a running maximum (exact_row).
+// sees, and stays while the scores keep within 60 powers of two of it: no pass for
+// the maximum, no rescaling of O.  Scores that rise further show in a tile's sum of
+// weights, before the tile's product is taken, and the row's m, l, weights of the
+// tile and O are brought to a higher reference there (far_tile; by the writing warps,
+// which wait at that time).  Nothing of it is in the softmax loop but a comparison a tile:
+// the check before each 32 keys' weights are written 69 us where this takes 59 (its
+// latency is in the chain), the raise called from the loop itself 200 us (registers).
+// 128 queries and 12000 causal keys, two heads of 64: 0.17 ms with level scores, 0.39 ms
+// with scores that rise by 0.7 powers of two a key (a raise a tile), 5.3 ms with two (192
+// powers a tile: its scores computed again, 42 us a tile).
 //
 // Roles: warps 0-3 softmax, warp 4 finds the work and loads it, warp 5 issues S,
 // warp 6 O += P V, warps 7-10 write the output.  S has two buffers, so that the
 // next S is computed during a softmax, and two CTAs on an SM fill each other's
 // waits.
 //
-// 128 sequences of 128, window +-64, 12 heads of 64: 24.8 us (101 MB: 4.1 TB/s);
-// 64 sequences of 257 to 512, window +-128, 16 heads of 64: 59.5 us (203 MB), the
+// 128 sequences of 128, window +-64, 12 heads of 64: 24.2 us (101 MB: 4.2 TB/s);
+// 64 sequences of 257 to 512, window +-128, 16 heads of 64: 59.1 us (203 MB), the
 // tensor pipe 25 % and the issue slots 51 % busy: bound by the chain of a tile,
 // whose 96 columns take a softmax warp 1700 cycles, half of them waiting for
 // tensor memory, exponentials and the other warps of its scheduler.  Measured and
@@ -46,7 +53,6 @@ namespace {
 struct FwdItem {
   int64_t q0, k0;      // the sequence's first rows
   int h, t0, nq, i0;   // head, first row, rows, position of the first row
-  int lk;              // keys of the sequence
   TileList keys;
   int nt;              // key tiles; < 0: no more work
 };
@@ -65,11 +71,14 @@ struct TcFwd {
   struct Shared {
     uint64_t q_full[QS], q_empty[QS], k_full[KP], k_empty[KP], v_full[KP], v_empty[KP];
     uint64_t s_full[2], p_full[2], pv_done[2], o_free, fin, fin2;  // [tile & 1]
-    uint64_t stat_full, stat_free;
+    uint64_t stat_full[4], stat_free[4];  // a message of a softmax warp to its writing warp
     uint64_t item_full[ITEMS], item_empty[ITEMS], clc;
     FwdItem item[ITEMS];
     uint4 answer;
-    float m[AT], l[AT];  // of an item's rows, for the writing warps
+    // the messages: an item's m and l (far = -1), or m and the tile's sum of a tile with
+    // far rows (its number), answered by m, sum and the scale of l
+    float m[AT], l[AT], f[AT];
+    int far[4];
     int rows[2 * KP];  // keys of a tile, by its number (a key tile's place is free before
                        // the product of its values has read this)
     uint32_t tmem;
@@ -85,7 +94,7 @@ constexpr int kTcThreads = 352;
 // most keys under a causal mask, first.  Under a causal mask without a window,
 // where a long sequence's tiles differ most, they come in that order over all
 // sequences and heads, so that the last to run are short: 8 sequences of 2048, 16
-// heads of 64, 105 -> 89 us, 16 of 1000, 8 heads of 128, 56 -> 50 us; but 64 of 512,
+// heads of 64, 105 -> 91 us, 16 of 1000, 8 heads of 128, 56 -> 50 us; but 64 of 512,
 // 12 heads of 64, 56 -> 63 us, and the windowed 64 of 257 to 512 59 -> 70 us.
 // False: nothing to do.
 __device__ __forceinline__ bool long_first(const AttnArgs& p, uint32_t ntiles) {
@@ -104,7 +113,6 @@ __device__ __forceinline__ bool fwd_item(const AttnArgs& p, uint32_t item, uint3
   if (!load_seq(p, (int)b, &s, true)) return false;
   w->q0 = s.q0;
   w->k0 = s.k0;
-  w->lk = s.lk;
   w->t0 = tile * AT;
   if (w->t0 >= s.lq) return false;
   w->nq = min(AT, s.lq - w->t0);
@@ -115,45 +123,181 @@ __device__ __forceinline__ bool fwd_item(const AttnArgs& p, uint32_t item, uint3
   return true;
 }
 
-// Row `t` of the item by one warp, over its visible keys with a running
-// maximum: a lane holds every 32nd channel.
-__device__ __noinline__ void exact_row(const AttnArgs& p, const FwdItem& w, int t, int lk) {
-  const int lane = threadIdx.x & 31, i = w.i0 + t, hk = w.h / p.group;
-  const int64_t r = w.q0 + w.t0 + t;
-  const __nv_bfloat16* q = p.q.at<const __nv_bfloat16>(r, w.h);
-  float x[4], o[4] = {0.f, 0.f, 0.f, 0.f}, m = -INFINITY, l = 0.f;
-  for (int c = 0; c < 4; ++c) {
-    const int d = lane + 32 * c;
-    x[c] = d < p.dim ? __bfloat162float(q[d]) * p.scale : 0.f;
+// The sum of weights over a tile from which a row's reference is raised: weights of up to
+// 2^60 times bf16 values of up to 2^68 stay finite in O.
+constexpr float kFar = 1152921504606846976.f;  // 2^60
+// The sum from which a weight may have overflowed (bf16 rounds up to infinity a little below
+// fp32's largest number): 2^127.
+constexpr float kOver = 1.7014118346046923e38f;
+
+// In keys from a tile's first, j0, on: the last one that the first of a warp's rows sees,
+// the first one that its last row sees, the end of the first tokens.  A later row sees
+// one key more on the right and one less on the left.  iw: position of the first row.
+struct TileView {
+  int nk, wh, wl, sk;
+  __device__ __forceinline__ TileView(const AttnArgs& p, int iw, int j0, int n) {
+    nk = n;
+    wh = p.right < 0 ? kAttnMaxLen : iw + p.right - j0;
+    wl = p.left < 0 ? -kAttnMaxLen : iw + 31 - p.left - j0;
+    sk = p.sinks - j0;
   }
-  const KeySpan ks = key_span(p, lk, i, i);
-  for (int part = 0; part < 2; ++part) {
-    const int hi = part ? ks.b1 : ks.a1;
-    for (int j = part ? ks.b0 : 0; j < hi; ++j) {
-      const __nv_bfloat16* k = p.k.at<const __nv_bfloat16>(w.k0 + j, hk);
-      const __nv_bfloat16* v = p.v.at<const __nv_bfloat16>(w.k0 + j, hk);
-      float s = 0.f;
-      for (int c = 0; c < 4; ++c) {
-        const int d = lane + 32 * c;
-        if (d < p.dim) s = fmaf(x[c], __bfloat162float(k[d]), s);
-      }
-      for (int e = 16; e; e >>= 1) s += __shfl_xor_sync(0xffffffffu, s, e);
-      const float mn = fmaxf(m, s), f = expf(m - mn), pr = expf(s - mn);
-      m = mn;
-      l = l * f + pr;
-      for (int c = 0; c < 4; ++c) {
-        const int d = lane + 32 * c;
-        o[c] *= f;
-        if (d < p.dim) o[c] = fmaf(pr, __bfloat162float(v[d]), o[c]);
+  // bit e: this lane's row sees key q + e of the tile
+  __device__ __forceinline__ uint32_t sees(int q, int lane) const {
+    return bit_span(0, min(nk - 1, wh + lane) - q) &
+           (bit_span(wl - 31 + lane - q, 31) | bit_span(0, sk - 1 - q));
+  }
+};
+
+// A tile in which some rows of a warp are far above their reference m (their sums ts of
+// weights are kFar or more): those rows get a reference higher by a whole number of powers
+// of two, so that the tile's weights and O, scaled to it, keep their bits.  Where a weight
+// may have overflowed (kOver), the row's scores are computed again from q and the tile's
+// keys (the weights lie over them), rounded before the reference is taken from them (a
+// score beyond 2^24 is rounded by whole powers of two), and the reference becomes their
+// maximum.  Returns the reference, the tile's sum, and the scale of l.
+__device__ __forceinline__ float3 far_tile(const AttnArgs& p, const FwdItem& w, int t, int KT,
+                                           uint32_t sp, uint32_t o_at, float m, float ts) {
+  const int lane = threadIdx.x & 31, row = 32 * ((threadIdx.x >> 5) & 3) + lane;
+  const int first = (w.keys.lim - w.keys.r + KT - 1) / KT;  // tiles before the list's second part
+  const int j0 = t < first ? w.keys.r + t * KT : w.keys.r2 + (t - first) * KT;
+  const int nk = min(KT, (t < first ? w.keys.lim : w.keys.lim2) - j0);
+  const int o_cols = t == 0 ? 0 : (p.dim + 15) & ~15;
+  const TileView view(p, w.i0 + row - lane, j0, nk);
+  const float c = p.scale * kLog2e;
+  const bool far = ts >= kFar && row < w.nq, over = far && ts >= kOver;
+  const bool any_over = __any_sync(0xffffffffu, over);
+  const __nv_bfloat16* q = p.q.at<const __nv_bfloat16>(w.q0 + w.t0 + row, w.h);
+  const __nv_bfloat16* k = p.k.at<const __nv_bfloat16>(w.k0 + j0, w.h / p.group);
+  float top = -INFINITY;
+#pragma unroll 1
+  for (int x = 0; any_over && x < nk; x += 4) {  // the scores of 4 keys, over S
+    float s[4], old[4];
+    uint32_t u[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[e] = 0.f;
+#pragma unroll 1
+    for (int d = 0; over && d < p.dim; d += 8) {
+      const uint4 a = *reinterpret_cast<const uint4*>(q + d);
+      const uint32_t qa[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint4 b = *reinterpret_cast<const uint4*>(k + min(x + e, nk - 1) * p.k.row + d);
+        const uint32_t kb[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          s[e] = fmaf(__uint_as_float(qa[i] << 16), __uint_as_float(kb[i] << 16), s[e]);
+          s[e] = fmaf(__uint_as_float(qa[i] & 0xFFFF0000u), __uint_as_float(kb[i] & 0xFFFF0000u),
+                      s[e]);
+        }
       }
     }
+    __syncwarp();
+    const uint32_t see = view.sees(x, lane);
+    tmem_ld4_async(sp + x, old);
+    tmem_wait_ld();
+    tmem_landed(old);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      s[e] = see & (1u << e) ? __fmul_rn(s[e], c) : -INFINITY;
+      top = fmaxf(top, s[e]);
+      u[e] = __float_as_uint(over ? s[e] : old[e]);  // the other rows' weights stay
+    }
+    tmem_st4(sp + x, u);
   }
-  __nv_bfloat16* out = p.o.at<__nv_bfloat16>(r, w.h);
-  for (int c = 0; c < 4; ++c) {
-    const int d = lane + 32 * c;
-    if (d < p.dim) out[d] = __float2bfloat16_rn(o[c] / l);
+  tmem_wait_st();
+  const float up = over ? ceilf(top - m) : ceilf(log2f(ts));
+  const float to = !far ? m : over && !(up < 8388608.f) ? top : m + up;
+  const float f = far ? exp2f(m - to) : 1.f;
+  float sum = 0.f;
+  // 8 weights lie in 4 columns; the scores they come from are read before, and weights
+  // are never written over scores that are still to come.  The product takes 16 keys a
+  // step: the weights of those past the tile's end, where scores may lie, become zero.
+#pragma unroll 1
+  for (int x = 0; x < nk || x % 16; x += 8) {
+    float old[4], z[2][4];
+    uint32_t u[4];
+    tmem_ld4_async(sp + (x >> 1), old);
+    tmem_ld4_async(sp + x, z[0]);
+    tmem_ld4_async(sp + x + 4, z[1]);
+    tmem_wait_ld();
+    tmem_landed(old);
+    tmem_landed(z[0]);
+    tmem_landed(z[1]);
+    const uint32_t see = view.sees(x, lane);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t b = __float_as_uint(old[e]);
+      float y0 = __uint_as_float(b << 16) * f, y1 = __uint_as_float(b & 0xFFFF0000u) * f;
+      if (over) {
+        y0 = see & (1u << (2 * e)) ? ex2(z[e >> 1][2 * (e & 1)] - to) : 0.f;
+        y1 = see & (2u << (2 * e)) ? ex2(z[e >> 1][2 * (e & 1) + 1] - to) : 0.f;
+        sum += y0 + y1;
+      }
+      u[e] = pack_bf16(y0, y1);
+    }
+    __syncwarp();
+    tmem_st4(sp + (x >> 1), u);
+    tmem_wait_st();
   }
-  if (p.lse && lane == 0) p.lse[(int64_t)w.h * p.Tq + r] = m + logf(l);
+#pragma unroll 1
+  for (int x = 0; x < o_cols; x += 4) {
+    float o[4];
+    uint32_t u[4];
+    tmem_ld4_async(o_at + x, o);
+    tmem_wait_ld();
+    tmem_landed(o);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) u[e] = __float_as_uint(o[e] * f);
+    tmem_st4(o_at + x, u);
+  }
+  tmem_wait_st();
+  return make_float3(to, over ? sum : ts * f, f);
+}
+
+// A writing warp's messages from the first one of a far tile on to the item's end.
+// Returns the number of messages taken, 0 after an abort.
+template <int NB>
+__device__ __forceinline__ uint32_t serve_far(const AttnArgs& p, typename TcFwd<NB>::Shared& S,
+                                              const FwdItem& w, int g0, uint32_t lanes,
+                                              uint32_t msgs) {
+  using C = TcFwd<NB>;
+  const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3, row = 32 * quad + lane;
+  while (true) {
+    const int g = S.far[quad];
+    // O holds the products up to the last tile's (of this item)
+    if (g > g0 && !wait_all(&S.pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, &S.flags, 114))
+      return 0;
+    tc_fence_after();
+    const float3 r = far_tile(p, w, g - g0, C::KT, lanes + (g & 1) * C::KT, lanes + C::O_COL,
+                              S.m[row], S.l[row]);
+    S.m[row] = r.x;
+    S.l[row] = r.y;
+    S.f[row] = r.z;
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&S.stat_free[quad]);
+    if (!wait_all(&S.stat_full[quad], msgs & 1, &S.flags, 113)) return 0;
+    ++msgs;
+    if (S.far[quad] < 0) return msgs;
+  }
+}
+
+// A softmax warp's side of it: m, the tile's sum, the scale of l, and 0 after an abort.
+template <int NB>
+__device__ __noinline__ float4 ask_far(typename TcFwd<NB>::Shared& S, int g, uint32_t msgs,
+                                       float m, float ts) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = threadIdx.x;
+  const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (!wait_all(&S.stat_free[warp], (msgs & 1) ^ 1, &S.flags, 110)) return none;
+  S.m[row] = m;
+  S.l[row] = ts;
+  if (lane == 0) S.far[warp] = g;
+  tc_fence_before();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(&S.stat_full[warp]);
+  if (!wait_all(&S.stat_free[warp], msgs & 1, &S.flags, 115)) return none;
+  tc_fence_after();
+  return make_float4(S.m[row], S.l[row], S.f[row], 1.f);
 }
 
 template <int NB>
@@ -186,8 +330,8 @@ __global__ void __launch_bounds__(kTcThreads, TcFwd<NB>::CTAS)
     for (int i = 0; i < C::ITEMS; ++i)
       mbar_init(&S.item_full[i], 1), mbar_init(&S.item_empty[i], 10);
     mbar_init(&S.o_free, 4);
-    mbar_init(&S.stat_full, 4);
-    mbar_init(&S.stat_free, 4);
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) mbar_init(&S.stat_full[i], 1), mbar_init(&S.stat_free[i], 1);
     mbar_init(&S.clc, 1);
     mbar_init(&S.fin, 1);
     mbar_init(&S.fin2, 1);
@@ -390,6 +534,7 @@ __global__ void __launch_bounds__(kTcThreads, TcFwd<NB>::CTAS)
     const float c = p.scale * kLog2e;
     const float2 c2 = make_float2(c, c);
     int g = 0;
+    uint32_t msgs = 0;
     bool ok = true;
 #pragma unroll 1
     for (int n = 0; ok; ++n) {
@@ -406,12 +551,8 @@ __global__ void __launch_bounds__(kTcThreads, TcFwd<NB>::CTAS)
       for (int t = 0; t < w.nt; ++t, ++g, keys.next(KT)) {
         const int j0 = keys.r, nk = keys.rows(KT);
         const uint32_t sp = tmem + lane_off + (g & 1) * KT;  // S, and P over it
-        // In keys from j0 on: the last one that the warp's first row sees, the first
-        // one that its last row sees, the end of the first tokens.  A later row sees
-        // one key more on the right and one less on the left.
-        const int wh = p.right < 0 ? kAttnMaxLen : iw + p.right - j0;
-        const int wl = p.left < 0 ? -kAttnMaxLen : iw + 31 - p.left - j0;
-        const int sk = p.sinks - j0;
+        const TileView view(p, iw, j0, nk);
+        const int wh = view.wh, wl = view.wl, sk = view.sk;
         const int end = 32 * warp < w.nq ? min(nk, wh + 32) : 0;  // past the keys of any row
         float2 s2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         if (!wait_all(&S.s_full[g & 1], (g >> 1) & 1, flags, 109)) { ok = false; break; }
@@ -428,8 +569,7 @@ __global__ void __launch_bounds__(kTcThreads, TcFwd<NB>::CTAS)
             tmem_wait_ld();
             tmem_landed(v);
             if (q + 32 > min(nk, wh + 1) || (q < wl && q + 32 > sk)) {  // not all see all of them
-              const uint32_t see = bit_span(0, min(nk - 1, wh + lane) - q) &
-                                   (bit_span(wl - 31 + lane - q, 31) | bit_span(0, sk - 1 - q));
+              const uint32_t see = view.sees(q, lane);
 #pragma unroll
               for (int e = 0; e < 32; ++e) v[e] = see & (1u << e) ? v[e] : -INFINITY;
             }
@@ -455,36 +595,58 @@ __global__ void __launch_bounds__(kTcThreads, TcFwd<NB>::CTAS)
           }
           tmem_st16(sp + (q >> 1), w16);  // the piece of S under it has been read
         }
-        l += (s2[0].x + s2[0].y) + (s2[1].x + s2[1].y);
+        const float ts = (s2[0].x + s2[0].y) + (s2[1].x + s2[1].y);
+        if (__any_sync(0xffffffffu, ts >= kFar && row < w.nq)) {
+          tmem_wait_st();
+          const float4 r = ask_far<NB>(S, g, msgs, m, ts);
+          ok = r.w != 0.f;
+          if (!ok) break;
+          ++msgs;
+          m = r.x;
+          l = fmaf(l, r.z, r.y);
+        } else {
+          l += ts;
+        }
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&S.p_full[g & 1]);
       }
-      ok = ok && wait_all(&S.stat_free, (n & 1) ^ 1, flags, 110);
+      ok = ok && wait_all(&S.stat_free[warp], (msgs & 1) ^ 1, flags, 110);
+      if (!ok) break;
+      ++msgs;
       S.m[row] = m;
       S.l[row] = l;
+      if (lane == 0) S.far[warp] = -1;
       __syncwarp();
-      if (ok && lane == 0) mbar_arrive(&S.stat_full);
+      if (lane == 0) mbar_arrive(&S.stat_full[warp]);
     }
   } else {
     // ---------------- output: thread = row of the warp's quarter of tensor memory
     const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
     const int row = 32 * (warp & 3) + lane;
     const bool wide = wide_rows(p.o);
+    const int quad = warp & 3;
     int g = 0;
+    uint32_t msgs = 0;
 #pragma unroll 1
     for (int n = 0;; ++n) {
       if (!wait_all(&S.item_full[n % C::ITEMS], (n / C::ITEMS) & 1, flags, 112)) break;
+      if (S.item[n % C::ITEMS].nt < 0) break;
+      if (!wait_all(&S.stat_full[quad], msgs & 1, flags, 113)) break;
+      ++msgs;
+      if (S.far[quad] >= 0) {
+        msgs = serve_far<NB>(p, S, S.item[n % C::ITEMS], g, tmem + lane_off, msgs);
+        if (msgs == 0) break;
+      }
       const FwdItem w = S.item[n % C::ITEMS];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&S.item_empty[n % C::ITEMS]);
-      if (w.nt < 0) break;
-      g += w.nt;
-      if (!wait_all(&S.stat_full, n & 1, flags, 113)) break;
       const float m = S.m[row], l = S.l[row];
       __syncwarp();
-      if (lane == 0) mbar_arrive(&S.stat_free);
+      if (lane == 0) {
+        mbar_arrive(&S.item_empty[n % C::ITEMS]);
+        mbar_arrive(&S.stat_free[quad]);
+      }
+      g += w.nt;
       const bool in = row < w.nq;
       if (p.lse && in)
         p.lse[(int64_t)w.h * p.Tq + w.q0 + w.t0 + row] =
@@ -517,11 +679,6 @@ __global__ void __launch_bounds__(kTcThreads, TcFwd<NB>::CTAS)
         for (int e = 0; e < 32; ++e) o[e] *= inv;
         if (in) st_row32(out + d, o, p.dim - d, wide);
       }
-      // rows whose reference was too low
-      uint32_t again = __ballot_sync(0xffffffffu, in && l >= 1.15e18f);
-#pragma unroll 1
-      for (; again; again &= again - 1)
-        exact_row(p, w, row - lane + __ffs(again) - 1, w.lk);
     }
   }
   tc_fence_before();

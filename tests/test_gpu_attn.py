@@ -495,3 +495,108 @@ def test_no_wait_counts_a_whole_list_of_tiles(wait_limit, heads, kv, lq, lk, dim
     assert ttc.tt_get_device_status(st) == 0
     for a, b in zip(want, got):
         assert torch.equal(a, b)
+
+
+def _by_hand(make_k, n, dim, act, q0, seed):
+    """q, k, v, do of two heads whose scores in powers of two are q0[t] make_k(j), at
+    scale ln 2 (channel 0 alone), the other channels of q zero."""
+    r = np.random.default_rng(seed)
+    q = np.zeros((n, 2, dim), np.float32)
+    q[:, :, 0] = q0
+    k = r.standard_normal((n, 2, dim)).astype(np.float32)
+    k[:, :, 0] = make_k(np.arange(n))[:, None]
+    v, do = (r.standard_normal((n, 2, dim)).astype(np.float32) for _ in range(2))
+    return [torch.from_numpy(a).to(DT[act]).cuda() for a in (q, k, v, do)]
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("dim", [40, 64, 128])
+@pytest.mark.parametrize("first,second", [(40, 70), (40, 63), (33, 95), (70, 130), (100, 200),
+                                          (190, 191), (60, 299)])
+def test_keys_that_share_a_row_at_both_sides_of_a_far_rise(first, second, dim, act):
+    """One key 59.5 powers of two above a row's first ones, a later one 60.25, another
+    300 above them for some rows: the first two share the softmax, wherever in a tile
+    of keys, or in which tiles, they lie."""
+    from tensor_train_compressed_tt_gb300.layer import TTAttention, TTSeqs
+    n, scale = 320, float(np.log(2.0))
+
+    def keys(j):
+        k = np.zeros(j.shape, np.float32)
+        k[first], k[second] = 59.5, 60.25
+        k[310] = -300.0
+        return k
+
+    q0 = np.where(np.arange(n) % 5 == 3, -1.0, np.where(np.arange(n) % 7 == 1, 0.0, 1.0))[:, None]
+    q, k, v, _ = _by_hand(keys, n, dim, act, q0, first + second)
+    off = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    seqs = TTSeqs.packed(off, n, n)
+    for left, right, sinks in ((-1, -1, 0), (-1, 0, 0), (150, 60, 45)):
+        op = TTAttention(2, dim, dtype=DT[act], left=left, right=right, sinks=sinks, scale=scale)
+        o, lse = op.forward(q, k, v, seqs)
+        ro, rl = B.attn_forward(_np(q), _np(k), _np(v), [(0, n, 0, n)], left, right, sinks, scale)
+        # fp32 scores of up to 300 powers of two are off by 300 2^-24 of them
+        assert_near(_np(o), ro, TOL[act] + 300 * 2.0 ** -23, "o")
+        assert_near(_np(lse), rl, 1e-5, "lse")
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_gradients_of_scores_that_rise_far(act, dim):
+    """q and k are whole quarters, so that every score is exact in fp32 in any order of
+    its terms (sixteenths of up to 1200), and what is lost is what the softmax loses.
+    The keys reach 150 in one channel and dq's terms cancel: each element is held to
+    the sum of its terms' sizes times the roundings that a term sees: three of bf16 (up
+    to 2^-8 each: eight bits), or
+    fp32's 1e-5, and eight of a number of 1200 (the lse's sum, its logarithm's base
+    changed forth and back, the scale's) in the exponent."""
+    from tensor_train_compressed_tt_gb300.layer import TTAttention, TTSeqs
+    r = np.random.default_rng(12)
+    n, ends = 300, (0, 120, 300)
+    q, k = (np.round(4 * r.standard_normal((n, 2, dim)).astype(np.float32)) / 4 for _ in range(2))
+    q[:, :, 0] = np.where(np.arange(n)[:, None] % 3 == 0, 8.0, 0.5)
+    k[:, :, 0] = np.arange(n)[:, None] * 0.5
+    q, k, v, do = (torch.from_numpy(a).to(DT[act]).cuda() for a in
+                   (q, k, r.standard_normal((n, 2, dim)).astype(np.float32),
+                    r.standard_normal((n, 2, dim)).astype(np.float32)))
+    spans = [(a, b, a, b) for a, b in zip(ends[:-1], ends[1:])]
+    seqs = TTSeqs.packed(torch.tensor(ends, dtype=torch.int32, device="cuda"), n, 180)
+    eps = {"bf16": 3 * 2.0 ** -8, "f32": 1e-5}[act] + 8 * 1200 * 2.0 ** -24
+    nq, nk, nv, nd = (_np(t) for t in (q, k, v, do))
+    for left, right, sinks in ((-1, -1, 0), (-1, 0, 0), (100, 0, 2)):
+        op = TTAttention(2, dim, dtype=DT[act], left=left, right=right, sinks=sinks, scale=1.0)
+        o, lse = op.forward(q, k, v, seqs)
+        got = op.backward(q, k, v, o, lse, do, seqs)
+        want = B.attn_backward(nq, nk, nv, nd, spans, left, right, sinks, 1.0)
+        size = [np.zeros_like(w) for w in want]
+        for a, b, _, _ in spans:
+            for h in range(2):
+                p, _ = B._one(nq[a:b, h], nk[a:b, h], B.attn_mask(b - a, b - a, left, right, sinks),
+                              1.0)
+                dp = np.abs(nd[a:b, h]) @ np.abs(nv[a:b, h]).T
+                ds = p * (dp + (p * dp).sum(1, keepdims=True))
+                size[0][a:b, h] = ds @ np.abs(nk[a:b, h])
+                size[1][a:b, h] = ds.T @ np.abs(nq[a:b, h])
+                size[2][a:b, h] = p.T @ np.abs(nd[a:b, h])
+        for g, w, z, name in zip(got, want, size, ("dq", "dk", "dv")):
+            assert (np.abs(_np(g) - w) <= eps * z + 1e-30).all(), name
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_scores_that_rise_without_end(wait_limit, dim):
+    """64 powers of two more with every 32 keys of a long sequence: no wait of a
+    kernel is as long as the rows of a tile are costly."""
+    from tensor_train_compressed_tt_gb300 import ttc
+    from tensor_train_compressed_tt_gb300.layer import TTAttention, TTSeqs
+    n, m, scale = 12000, 160, float(np.log(2.0))
+    q, k, v, _ = _by_hand(lambda j: 2.0 * j, n, dim, "bf16", 1.0, 5)
+    q = q[:m].contiguous()
+    i32 = lambda *a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    seqs = TTSeqs(i32(0), i32(m), i32(0), i32(n), m, n, m, n)
+    op = TTAttention(2, dim, right=0, scale=scale)
+    op.forward(q, k, v, TTSeqs(i32(0), i32(m), i32(0), i32(m), m, n, m, m))
+    wait_limit(5_000_000)
+    o, lse = op.forward(q, k, v, seqs)
+    assert ttc.tt_get_device_status(torch.cuda.current_stream().cuda_stream) == 0
+    ro, rl = B.attn_forward(_np(q), _np(k), _np(v), [(0, m, 0, n)], -1, 0, 0, scale)
+    assert_near(_np(o), ro, TOL["bf16"] + 24000 * 2.0 ** -23, "o")
+    assert_near(_np(lse), rl, 1e-5, "lse")
