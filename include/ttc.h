@@ -475,6 +475,10 @@ tt_status tt_set_wait_limit_ns(uint64_t ns);
 #define TT_DEBUG_FWD_TOKENS 1    /* forward token kernel: first stage never loaded */
 #define TT_DEBUG_BWD_TOKENS 2    /* backward token kernel: first stage never loaded */
 #define TT_DEBUG_MERGE_BARRIER 3 /* merge engine (programs of 2+ phases): one grid-barrier arrival */
+/* tensor-core attention kernels: the first tile of their lists never loaded */
+#define TT_DEBUG_ATTN_FWD 4
+#define TT_DEBUG_ATTN_BWD_QUERIES 5 /* the backward's pass over queries (dq) */
+#define TT_DEBUG_ATTN_BWD_KEYS 6    /* its pass over keys (dk, dv) */
 tt_status tt_debug_skip_arrival(int site);
 
 /* Synchronise stream, then read and clear the status word of the current

@@ -24,6 +24,10 @@ cudaError_t attn_set_wait_limit(unsigned long long ns) {
   return cudaMemcpyToSymbol(g_wait_limit_ns, &ns, sizeof(ns));
 }
 
+cudaError_t attn_set_debug_skip(int site) {
+  return cudaMemcpyToSymbol(g_debug_skip, &site, sizeof(site));
+}
+
 namespace {
 
 bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }

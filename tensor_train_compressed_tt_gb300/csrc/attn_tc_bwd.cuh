@@ -241,6 +241,9 @@ __global__ void __launch_bounds__(TcBwd<KV, NB>::THREADS, 1)
       int n = 0, nload = 0, s = 0, loads = 0;
       uint32_t ph = 1, clc = 0;  // parity of the ring's empty barriers; of the next answer
       bool ok = true, first = true;
+      // test hook: the first CTA leaves its first pair of tiles unloaded
+      const int from =
+          blockIdx.x == 0 && debug_take(KV ? TT_DEBUG_ATTN_BWD_KEYS : TT_DEBUG_ATTN_BWD_QUERIES);
       int cta = (int)blockIdx.x;
       BwdItem cur, w;
       cur.nt = -1;
@@ -302,10 +305,13 @@ __global__ void __launch_bounds__(TcBwd<KV, NB>::THREADS, 1)
             ok = wait_one(&S.y_empty[s], ph, flags, 122);
             if (!ok) break;
             S.rows[s] = l.rows(YT);
-            mbar_expect_tx(&S.y_full[s], 2 * C::UNIT);
             uint8_t* dst = ybuf + 2 * s * C::UNIT;
-            load_tile<NB>(dst, C::YBOX, &tm_y1, &S.y_full[s], l.h, (int)cur.y0 + l.r);
-            load_tile<NB>(dst + C::UNIT, C::YBOX, &tm_y2, &S.y_full[s], l.h, (int)cur.y0 + l.r);
+            if (loads >= from) {
+              mbar_expect_tx(&S.y_full[s], 2 * C::UNIT);
+              load_tile<NB>(dst, C::YBOX, &tm_y1, &S.y_full[s], l.h, (int)cur.y0 + l.r);
+              load_tile<NB>(dst + C::UNIT, C::YBOX, &tm_y2, &S.y_full[s], l.h,
+                            (int)cur.y0 + l.r);
+            }
             l.next(YT);
             ++loads;
             if (++s == KP) s = 0, ph ^= 1;

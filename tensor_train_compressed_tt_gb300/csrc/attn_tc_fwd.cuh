@@ -354,6 +354,8 @@ __global__ void __launch_bounds__(kTcThreads, TcFwd<NB>::CTAS)
       int n = 0, nload = 0, s = 0, loads = 0;
       uint32_t ph = 1, clc = 0;  // parity of the ring's empty barriers; of the next answer
       bool ok = true, first = true;
+      // test hook: the first CTA leaves its first tile of keys unloaded
+      const int from = blockIdx.x == 0 && debug_take(TT_DEBUG_ATTN_FWD);
       int cta = (int)blockIdx.x;
       FwdItem cur, w;
       cur.nt = -1;
@@ -410,8 +412,10 @@ __global__ void __launch_bounds__(kTcThreads, TcFwd<NB>::CTAS)
             if (!ok) break;
             S.rows[loads % (2 * KP)] = l.rows(KT);
             uint8_t* dst = kvbuf + 2 * s * C::UNIT;
-            mbar_expect_tx(&S.k_full[s], C::UNIT);
-            load_tile<NB>(dst, C::KBOX, &tm_k, &S.k_full[s], l.h, (int)cur.k0 + l.r);
+            if (loads >= from) {
+              mbar_expect_tx(&S.k_full[s], C::UNIT);
+              load_tile<NB>(dst, C::KBOX, &tm_k, &S.k_full[s], l.h, (int)cur.k0 + l.r);
+            }
             ok = wait_one(&S.v_empty[s], ph, flags, 94);
             if (!ok) {
               drain_one(&S.k_full[s], ph ^ 1);

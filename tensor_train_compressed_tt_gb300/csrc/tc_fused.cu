@@ -1334,9 +1334,11 @@ extern "C" tt_status tt_set_wait_limit_ns(uint64_t ns) {
 }
 
 extern "C" tt_status tt_debug_skip_arrival(int site) {
-  if (site < 0 || site > TT_DEBUG_MERGE_BARRIER) return TT_ERR_INVALID_ARG;
-  return cudaMemcpyToSymbol(ttc::g_debug_skip, &site, sizeof(site)) == cudaSuccess ? TT_OK
-                                                                                  : TT_ERR_CUDA;
+  if (site < 0 || site > TT_DEBUG_ATTN_BWD_KEYS) return TT_ERR_INVALID_ARG;
+  return cudaMemcpyToSymbol(ttc::g_debug_skip, &site, sizeof(site)) == cudaSuccess &&
+                 ttc::attn_set_debug_skip(site) == cudaSuccess
+             ? TT_OK
+             : TT_ERR_CUDA;
 }
 
 #include "merge_engine.cuh"

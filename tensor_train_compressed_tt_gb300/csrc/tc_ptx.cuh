@@ -1,7 +1,7 @@
 // Device helpers of the tensor-core kernels (mbarriers, TMA, tcgen05, the
 // swizzled tile layout) and their host-side launch helpers, shared by the
 // translation units that hold such kernels.  Each translation unit has its
-// own status word and wait limit; the C entry points read and set them all.
+// own status word, wait limit and test hook; the C entry points read and set them all.
 #pragma once
 
 #include <cuda.h>

@@ -116,9 +116,10 @@ struct DeviceStatus {
 cudaError_t read_and_clear_device_status(DeviceStatus* out);
 // The same for the embedding kernels' own word (ttm.cu).
 cudaError_t read_and_clear_ttm_status(DeviceStatus* out);
-// The same for the attention kernels' own word, and their wait limit (attn.cu).
+// The same for the attention kernels' own word, their wait limit and test hook (attn.cu).
 cudaError_t read_and_clear_attn_status(DeviceStatus* out);
 cudaError_t attn_set_wait_limit(unsigned long long ns);
+cudaError_t attn_set_debug_skip(int site);
 
 // ---- rank-adaptive step (rank_update.cu) ------------------------------------
 // One elementwise launch of the step over a layer's packed params / dparams.

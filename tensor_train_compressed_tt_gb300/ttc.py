@@ -450,6 +450,9 @@ TT_DEBUG_NONE = 0
 TT_DEBUG_FWD_TOKENS = 1
 TT_DEBUG_BWD_TOKENS = 2
 TT_DEBUG_MERGE_BARRIER = 3
+TT_DEBUG_ATTN_FWD = 4
+TT_DEBUG_ATTN_BWD_QUERIES = 5
+TT_DEBUG_ATTN_BWD_KEYS = 6
 
 
 def tt_set_wait_limit_ns(ns: int) -> int:

@@ -133,3 +133,44 @@ def test_wait_limit_arguments():
     assert ttc.tt_set_wait_limit_ns(10) == 1
     assert ttc.tt_debug_skip_arrival(-1) == 1
     assert ttc.tt_debug_skip_arrival(99) == 1
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("lens", [[100], [300, 40] * 40])
+@pytest.mark.parametrize("site", ["ATTN_FWD", "ATTN_BWD_QUERIES", "ATTN_BWD_KEYS"])
+def test_attention_wait_runs_out(short_limit, site, lens, dim):
+    """The tensor-core attention kernels: one piece of work, and more than there are
+    CTAs (the CTA that stops takes over those that have not started, and drops them)."""
+    from oracle import block_oracle as B
+    from tensor_train_compressed_tt_gb300.layer import TTAttention, TTSeqs
+    ttc = short_limit
+    st = torch.cuda.current_stream().cuda_stream
+    g = torch.Generator(device="cuda")
+    g.manual_seed(24)
+    T, heads = sum(lens), 8 if len(lens) > 1 else 1
+    q, k, v, do = (torch.randn(T, heads, dim, generator=g, device="cuda").bfloat16()
+                   for _ in range(4))
+    off = torch.tensor(np.cumsum([0] + lens), dtype=torch.int32, device="cuda")
+    seqs = TTSeqs.packed(off, T, max(lens))
+    op = TTAttention(heads, dim, left=60, right=60, sinks=1)
+
+    def run():
+        o, lse = op.forward(q, k, v, seqs)
+        return [o, lse] + list(op.backward(q, k, v, o, lse, do, seqs))
+
+    want = run()
+    assert ttc.tt_get_device_status(st) == 0
+    ttc.check(ttc.tt_debug_skip_arrival(getattr(ttc, f"TT_DEBUG_{site}")), "hook")
+    if site == "ATTN_FWD":
+        op.forward(q, k, v, seqs)
+    else:
+        op.backward(q, k, v, want[0], want[1], do, seqs)
+    assert ttc.tt_get_device_status(st) == 5   # TT_ERR_TIMEOUT, read and cleared
+    assert ttc.tt_get_device_status(st) == 0
+    for a, b in zip(want, run()):
+        assert torch.equal(a, b)
+    assert ttc.tt_get_device_status(st) == 0
+    if len(lens) == 1:
+        n = lambda t: t.double().cpu().numpy()  # noqa: E731
+        ro, _ = B.attn_forward(n(q), n(k), n(v), [(0, T, 0, T)], 60, 60, 1)
+        assert O.rel_err(n(want[0]), ro) <= TOL["bf16"]
