@@ -189,6 +189,23 @@ class TTTransformerBlock(TTEncoderBlock):
                            ws=b["ws_norm"], stream=stream)
         return b["ds1"]
 
+    def step(self, x, res: Optional[torch.Tensor], dffn, ds2: Optional[torch.Tensor],
+             seqs: TTSeqs, params: Dict[str, torch.Tensor], b: Dict[str, torch.Tensor],
+             stream=None) -> None:
+        """A training step: forward, then backward for the gradients dffn and ds2 of its
+        outputs; everything in b (y_ffn and s2, ds1, dp_*, dg1, db1, dg2, db2)."""
+        self.forward(x, res, seqs, params, b, stream)
+        self.backward(x, res, dffn, ds2, seqs, params, b, stream)
+
+    def capture(self, x, res: Optional[torch.Tensor], dffn, ds2: Optional[torch.Tensor],
+                seqs: TTSeqs, params: Dict[str, torch.Tensor],
+                b: Dict[str, torch.Tensor]) -> torch.cuda.CUDAGraph:
+        """The training step as one CUDA graph (replay() runs the whole block)."""
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            self.step(x, res, dffn, ds2, seqs, params, b)  # on the capture stream
+        return g
+
     def decode(self, x, res: Optional[torch.Tensor], keys, values, rows, seqs: TTSeqs,
                params: Dict[str, torch.Tensor], b: Dict[str, torch.Tensor], stream=None):
         """forward for a few new tokens: their keys and values go to `rows` (int64)

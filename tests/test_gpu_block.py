@@ -250,3 +250,34 @@ def test_one_workspace_for_both_passes():
     for a, b in zip(op.backward(q, k, k, o, lse, q, seqs, ws=ws),
                     op.backward(q, k, k, o, lse, q, seqs)):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("first", [False, True])
+def test_step_and_its_graph_run_the_whole_block(first):
+    lens = (70, 31)
+    blk, seqs, _, params, _, _, x, res, dffn, ds2 = _setup(lens, 56, left=40, right=0, sinks=1)
+    if first:
+        res = ds2 = None
+    b = blk.buffers(sum(lens), seqs)
+    blk.forward(x, res, seqs, params, b)
+    blk.backward(x, res, dffn, ds2, seqs, params, b)
+    names = ["y_ffn", "s2", "ds1", "dg1", "db1", "dg2", "db2"]
+    want = {k: b[k].clone() for k in names}
+    params_of = [k for k in b if k.startswith("dp_")]
+
+    def clear():
+        for k in names + params_of:
+            b[k].zero_()
+
+    clear()
+    blk.step(x, res, dffn, ds2, seqs, params, b)
+    for k in names:
+        assert torch.equal(b[k], want[k]), k
+    torch.cuda.synchronize()
+    g = blk.capture(x, res, dffn, ds2, seqs, params, b)
+    clear()
+    g.replay()
+    torch.cuda.synchronize()
+    for k in names:
+        assert torch.equal(b[k], want[k]), k
+    assert all(float(b[k].abs().max()) > 0 for k in params_of)
