@@ -6,6 +6,7 @@ pointers into one libttc call.  No arithmetic happens here.
 
 from __future__ import annotations
 
+import math
 from typing import Optional, Sequence
 
 import torch
@@ -29,15 +30,22 @@ def _stream(stream: Optional[torch.cuda.Stream]) -> int:
     return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
+def _filled(shape, dtype: torch.dtype, device, fill: Optional[float]) -> torch.Tensor:
+    if fill is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    return torch.full(shape, fill, dtype=dtype, device=device)
+
+
 def _new(shape, dtype: torch.dtype, device, stream: Optional[torch.cuda.Stream],
-         zero: bool = False) -> torch.Tensor:
+         fill: Optional[float] = None) -> torch.Tensor:
     """An output that the caller did not give: of the memory of the stream that the
     kernels run on, so that nothing else still uses it there, and held for the
-    caller's stream, which reads it afterwards."""
+    caller's stream, which reads it afterwards.  fill: what it holds where the
+    kernels do not write it."""
     if stream is None:
-        return (torch.zeros if zero else torch.empty)(shape, dtype=dtype, device=device)
+        return _filled(shape, dtype, device, fill)
     with torch.cuda.stream(stream):
-        t = (torch.zeros if zero else torch.empty)(shape, dtype=dtype, device=device)
+        t = _filled(shape, dtype, device, fill)
     t.record_stream(torch.cuda.current_stream(t.device))
     return t
 
@@ -332,10 +340,11 @@ class TTNorm:
         T, N = s.shape[0], self.N
         if dx is None:
             dx = _new((T, N), self.dtype, s.device, stream)
-        if dgamma is None:  # added to, or overwritten
-            dgamma = _new(N, torch.float32, s.device, stream, zero=self.accumulate)
+        fill = 0.0 if self.accumulate else None  # added to, or overwritten
+        if dgamma is None:
+            dgamma = _new((N,), torch.float32, s.device, stream, fill)
         if dbeta is None:
-            dbeta = _new(N, torch.float32, s.device, stream, zero=self.accumulate)
+            dbeta = _new((N,), torch.float32, s.device, stream, fill)
         if ws is None:
             ws = _scratch(stream, self.workspace, T, s.device)
         f32, sh = torch.float32, (T, N)
@@ -351,22 +360,29 @@ class TTNorm:
 class TTSeqs:
     """The sequences of a batch: int32 device arrays of first and past-the-end
     rows of each one's queries and keys, the buffers' row counts and bounds on
-    a sequence's lengths.  Keeps the arrays alive."""
+    a sequence's lengths.  Keeps the arrays alive.  gaps: rows of the buffers may
+    belong to no sequence (a cache's unused ones).  The kernels leave those rows of
+    their outputs as they are; outputs that TTAttention makes hold zeros there (and
+    lse -infinity).  With gaps=False, for sequences that cover every row, it does not
+    fill them first."""
 
-    def __init__(self, q_begin, q_end, k_begin, k_end, Tq: int, Tk: int, max_q: int, max_k: int):
+    def __init__(self, q_begin, q_end, k_begin, k_end, Tq: int, Tk: int, max_q: int, max_k: int,
+                 gaps: bool = True):
         B = q_begin.shape[0]
         self.arrays = (q_begin, q_end, k_begin, k_end)
         for t in self.arrays:
             _dense(t, (B,), torch.int32, "sequence rows")
         self.Tq, self.Tk = int(Tq), int(Tk)
+        self.gaps = bool(gaps)
         self.c = ttc.tt_attn_seqs(B, int(max_q), int(max_k), self.Tq, self.Tk,
                                   *(t.data_ptr() for t in self.arrays))
 
     @classmethod
     def packed(cls, offsets: torch.Tensor, T: int, max_len: int) -> "TTSeqs":
         """Self-attention over sequences packed one after another: sequence b
-        is rows offsets[b] .. offsets[b + 1] of T."""
-        return cls(offsets[:-1], offsets[1:], offsets[:-1], offsets[1:], T, T, max_len, max_len)
+        is rows offsets[b] .. offsets[b + 1] of T, from row 0 to row T without a gap."""
+        return cls(offsets[:-1], offsets[1:], offsets[:-1], offsets[1:], T, T, max_len, max_len,
+                   gaps=False)
 
 
 class TTAttention:
@@ -407,11 +423,13 @@ class TTAttention:
                          f"on {t.device}, strides {tuple(st)}")
 
     def forward(self, q, k, v, seqs: TTSeqs, o=None, lse=None, ws=None, stream=None):
-        """(o, lse); o like q but dense, lse (heads, Tq) fp32."""
+        """(o, lse); o like q but dense, lse (heads, Tq) fp32.  Rows of no sequence stay
+        as they are in tensors that the caller gives."""
         if o is None:
-            o = _new(q.shape, self.dtype, q.device, stream)
+            o = _new(q.shape, self.dtype, q.device, stream, 0.0 if seqs.gaps else None)
         if lse is None:
-            lse = _new((self.heads, seqs.Tq), torch.float32, q.device, stream)
+            lse = _new((self.heads, seqs.Tq), torch.float32, q.device, stream,
+                       -math.inf if seqs.gaps else None)
         if ws is None:
             ws = _scratch(stream, self.workspace, seqs, False, q.device)
         H, G = self.heads, self.kv_heads
@@ -424,13 +442,15 @@ class TTAttention:
 
     def backward(self, q, k, v, o, lse, do, seqs: TTSeqs, dq=None, dk=None, dv=None, ws=None,
                  stream=None):
-        """(dq, dk, dv) for the gradient do of o."""
+        """(dq, dk, dv) for the gradient do of o.  Rows of no sequence stay as they are
+        in tensors that the caller gives."""
+        fill = 0.0 if seqs.gaps else None
         if dq is None:
-            dq = _new(q.shape, self.dtype, q.device, stream)
+            dq = _new(q.shape, self.dtype, q.device, stream, fill)
         if dk is None:
-            dk = _new(k.shape, self.dtype, q.device, stream)
+            dk = _new(k.shape, self.dtype, q.device, stream, fill)
         if dv is None:
-            dv = _new(v.shape, self.dtype, q.device, stream)
+            dv = _new(v.shape, self.dtype, q.device, stream, fill)
         if ws is None:
             ws = _scratch(stream, self.workspace, seqs, True, q.device)
         H, G = self.heads, self.kv_heads

@@ -600,3 +600,29 @@ def test_scores_that_rise_without_end(wait_limit, dim):
     ro, rl = B.attn_forward(_np(q), _np(k), _np(v), [(0, m, 0, n)], -1, 0, 0, scale)
     assert_near(_np(o), ro, TOL["bf16"] + 24000 * 2.0 ** -23, "o")
     assert_near(_np(lse), rl, 1e-5, "lse")
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+def test_made_outputs_hold_no_garbage(act):
+    """Outputs that the calls make: rows of no sequence are zero (lse -infinity)."""
+    from tensor_train_compressed_tt_gb300.layer import TTAttention, TTSeqs
+    g = torch.Generator(device="cuda")
+    g.manual_seed(25)
+    q, do = (torch.randn(90, 4, 64, generator=g, device="cuda").to(DT[act]) for _ in range(2))
+    k, v = (torch.randn(200, 2, 64, generator=g, device="cuda").to(DT[act]) for _ in range(2))
+    spans = [(3, 40, 10, 60), (50, 51, 100, 180)]
+    seqs = TTSeqs(*_rows(spans), Tq=90, Tk=200, max_q=40, max_k=80)
+    op = TTAttention(4, 64, kv_heads=2, dtype=DT[act], left=30, right=0, sinks=1)
+    free_q, free_k = torch.ones(90, dtype=bool), torch.ones(200, dtype=bool)
+    for a, b, c, d in spans:
+        free_q[a:b], free_k[c:d] = False, False
+    for _ in range(3):
+        junk = [torch.full((n, h, 64), float("nan"), dtype=DT[act], device="cuda")
+                for n, h in ((90, 4), (90, 4), (200, 2), (200, 2))]
+        del junk   # the memory that the next tensors are likely to get
+        o, lse = op.forward(q, k, v, seqs)
+        dq, dk, dv = op.backward(q, k, v, o, lse, do, seqs)
+        for t, free in ((o, free_q), (dq, free_q), (dk, free_k), (dv, free_k)):
+            assert float(t[free].float().abs().max()) == 0
+            assert bool(torch.isfinite(t.float()).all())
+        assert bool((lse[:, free_q] == -np.inf).all())
