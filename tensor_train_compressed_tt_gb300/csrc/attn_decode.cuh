@@ -173,11 +173,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
-__device__ __forceinline__ float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -314,11 +309,11 @@ __global__ void __launch_bounds__(32 * kDecWarps, N == 1 ? 3 : 2)
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
         const float mn = fmaxf(m[n][e], top);
         const float ref = mn == -INFINITY ? 0.f : mn;
-        f[n][e] = exp2_fast(m[n][e] - ref);
+        f[n][e] = ex2(m[n][e] - ref);
         turn |= mn != m[n][e];
         m[n][e] = mn;
-        sc[n][e] = exp2_fast(sc[n][e] - ref);
-        sc[n][e + 2] = exp2_fast(sc[n][e + 2] - ref);
+        sc[n][e] = ex2(sc[n][e] - ref);
+        sc[n][e + 2] = ex2(sc[n][e + 2] - ref);
         l[n][e] = fmaf(l[n][e], f[n][e], sc[n][e] + sc[n][e + 2]);
       }
 #pragma unroll

@@ -4,7 +4,8 @@
 // in shared memory, 256 threads with MT x MT scores each.
 //
 // f32, 8 heads, causal: 8 sequences of 2048, heads of 32: forward 662 us, backward
-// 1928 us, 26 and 31 TFLOP/s of the fp32 pipes' 80, bound by the reads of shared
+// 1928 us, 26 and 22 TFLOP/s (31 of the seven products done, where a gradient needs
+// five) of the fp32 pipes' 80, bound by the reads of shared
 // memory that feed them (8 of 16 bytes for 64 multiply-adds); 32 sequences of
 // 33 to 97: backward 45 us, the latency of loads and barriers of blocks that have
 // two or three tiles each.

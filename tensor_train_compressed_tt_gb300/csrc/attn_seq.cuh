@@ -7,6 +7,13 @@
 namespace ttc {
 namespace {
 
+// 2^x by the exponential unit alone (results below 2^-126 are 0).
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // One sequence: its first query and key row and their counts.
 struct Seq {
   int64_t q0, k0;

@@ -245,12 +245,6 @@ __device__ __forceinline__ void tmem_give(uint32_t base, uint32_t cols) {
                : "memory");
 }
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // Two f32 in one 64-bit register: x * m + a, and a + b.
 __device__ __forceinline__ float2 fma2(float2 x, float2 m, float2 a) {
   return __ffma2_rn(x, m, a);

@@ -38,7 +38,7 @@
 // pieces), 47 % of the tensor pipe.  The product P K costs the last 20 us, and
 // with it dq's error is that of the bf16 weights alone.  Causal without a window,
 // long tiles first over all sequences: 4 sequences of 4096, 8 heads of 128, 619 ->
-// 492 us (977 TFLOP/s of the five products that a gradient needs).
+// 492 us (698 TFLOP/s of the five products that a gradient needs; 977 of the seven done).
 //
 // The pass over keys: the first tokens are seen by every later query, so their
 // tile is cut into pieces of its list of query tiles, each the work of one
