@@ -387,7 +387,8 @@ tt_status tt_norm_backward(const tt_plan_t* plan, int64_t T, const void* s, cons
  * zero times a value that is not finite is NaN, so such a value may reach every
  * query within 128 rows of one that sees it (in a backward, a query's q, o or
  * dout likewise every key within 128 of one that it sees).
- * Scores, softmax statistics and all sums are fp32.  With bf16 activations
+ * Scores, softmax statistics and all sums are fp32: a weight's relative error grows
+ * with its score, some 2^-22 |z| (a thousandth at scores of 5000).  With bf16 activations
  * the weights p (and in the backward z's gradient) are rounded to bf16 for
  * the tensor-core products. */
 typedef struct tt_attn_desc {

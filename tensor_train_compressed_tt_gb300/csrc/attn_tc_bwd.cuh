@@ -31,7 +31,7 @@
 // own four softmax warps.  Four more warps write the gradients, so that the
 // softmax goes on with the next item meanwhile.
 //
-// 128 sequences of 128, window +-64, 12 heads of 64: 76 us (dq 41, dk and dv 40);
+// 128 sequences of 128, window +-64, 12 heads of 64: 75 us (dq 40, dk and dv 40);
 // 64 sequences of 257 to 512, window +-128, 16 heads of 64: 228 us (110 and 124),
 // 1.3 TB/s and 27 % of the tensor pipe: the chain above.  One sequence of 16384,
 // the last 1024 keys, 8 heads of 128 on 2: 335 us (150, 177, and 11 for the
