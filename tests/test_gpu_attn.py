@@ -626,3 +626,29 @@ def test_made_outputs_hold_no_garbage(act):
             assert float(t[free].float().abs().max()) == 0
             assert bool(torch.isfinite(t.float()).all())
         assert bool((lse[:, free_q] == -np.inf).all())
+
+
+@pytest.mark.parametrize("lq", [1, 100])
+def test_default_outputs_on_a_given_stream(lq):
+    """stream= another one than the current, which is busy: outputs and workspaces
+    that the calls make are the given stream's."""
+    from tensor_train_compressed_tt_gb300.layer import TTAttention, TTSeqs
+    g = torch.Generator(device="cuda")
+    g.manual_seed(26)
+    i32 = lambda a: torch.tensor([a], dtype=torch.int32, device="cuda")  # noqa: E731
+    seqs = TTSeqs(i32(0), i32(lq), i32(5), i32(3005), Tq=lq, Tk=3010, max_q=lq, max_k=3000)
+    q, do = (torch.randn(lq, 4, 64, generator=g, device="cuda").bfloat16() for _ in range(2))
+    k, v = (torch.randn(3010, 2, 64, generator=g, device="cuda").bfloat16() for _ in range(2))
+    op = TTAttention(4, 64, kv_heads=2, right=0)
+    o, lse = op.forward(q, k, v, seqs)
+    want = [o, lse] + list(op.backward(q, k, v, o, lse, do, seqs))
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        torch.cuda._sleep(20_000_000)   # some 10 ms
+        o, lse = op.forward(q, k, v, seqs, stream=side)
+        got = [o, lse] + list(op.backward(q, k, v, o, lse, do, seqs, stream=side))
+        junk = torch.full((1 << 20,), float("nan"), device="cuda")  # noqa: F841
+        torch.cuda.synchronize()
+        for a, b in zip(want, got):
+            assert torch.equal(a, b)
