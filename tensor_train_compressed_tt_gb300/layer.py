@@ -50,6 +50,11 @@ def _new(shape, dtype: torch.dtype, device, stream: Optional[torch.cuda.Stream],
     return t
 
 
+def _grad_fill(accumulate: bool) -> Optional[float]:
+    """What a gradient that the call makes starts from: it is added to, or overwritten."""
+    return 0.0 if accumulate else None
+
+
 def _scratch(stream: Optional[torch.cuda.Stream], workspace, *args) -> torch.Tensor:
     """A workspace that is dropped at the call's end: of the memory of the call's
     stream, where it is next used after the call's kernels."""
@@ -74,6 +79,7 @@ class TTLinear:
         self.out_modes = tuple(out_modes)
         self.ranks = tuple(ranks)
         self.dtype = dtype
+        self.fill = _grad_fill(accumulate)
         # dtype of y and dx
         self.out_dtype = torch.bfloat16 if _DT[dtype] == ttc.TT_DT_E4M3 else dtype
         flags = (ttc.TT_ACCUMULATE if accumulate else 0) | \
@@ -113,7 +119,7 @@ class TTLinear:
         if dx is None:
             dx = _new((T, self.N), self.out_dtype, x.device, stream)
         if dparams is None:
-            dparams = _new(self.n_params, torch.float32, x.device, stream)
+            dparams = _new((self.n_params,), torch.float32, x.device, stream, self.fill)
         if ws is None:
             ws = _scratch(stream, self.workspace, T, x.device)
         ttc.check(ttc.tt_backward(self.plan, T, _ptr(x), _ptr(dy), _ptr(params), _ptr(dx),
@@ -140,6 +146,7 @@ class TTFFN:
             (ttc.TT_REUSE_MERGE if reuse_merge else 0) | (ttc.TT_REUSE_Z if reuse_z else 0) | \
             (ttc.TT_DETERMINISTIC if deterministic else 0)
         self.dtype = dtype
+        self.fill = _grad_fill(accumulate)
         self.up_desc = ttc.make_desc(up[0], up[1], up[2], _DT[dtype], flags)
         self.down_desc = ttc.make_desc(down[0], down[1], down[2], _DT[dtype], flags)
         self.plan = ttc.tt_ffn_plan(self.up_desc, self.down_desc)
@@ -171,9 +178,9 @@ class TTFFN:
         if dx is None:
             dx = _new((T, self.N), self.dtype, x.device, stream)
         if dp_up is None:
-            dp_up = _new(self.layout[0][2], torch.float32, x.device, stream)
+            dp_up = _new((self.layout[0][2],), torch.float32, x.device, stream, self.fill)
         if dp_down is None:
-            dp_down = _new(self.layout[1][2], torch.float32, x.device, stream)
+            dp_down = _new((self.layout[1][2],), torch.float32, x.device, stream, self.fill)
         if ws is None:
             ws = _scratch(stream, self.workspace, T, x.device)
         ttc.check(ttc.tt_ffn_backward(self.plan, T, _ptr(x), _ptr(dy), _ptr(p_up),
@@ -195,6 +202,7 @@ class TTMulti:
             (ttc.TT_REUSE_MERGE if reuse_merge else 0) | (ttc.TT_REUSE_Z if reuse_z else 0) | \
             (ttc.TT_DETERMINISTIC if deterministic else 0)
         self.dtype = dtype
+        self.fill = _grad_fill(accumulate)
         self.out_dtype = torch.bfloat16 if _DT[dtype] == ttc.TT_DT_E4M3 else dtype
         self.descs = [ttc.make_desc(i, o, r, _DT[dtype], flags) for i, o, r in layers]
         self.plan = ttc.tt_multi_plan(self.descs)
@@ -230,7 +238,7 @@ class TTMulti:
         if dx is None:
             dx = _new((T, self.N), self.out_dtype, x.device, stream)
         if dparams is None:
-            dparams = [_new(lay[2], torch.float32, x.device, stream)
+            dparams = [_new((lay[2],), torch.float32, x.device, stream, self.fill)
                        for lay in self.layout]
         if ws is None:
             ws = _scratch(stream, self.workspace, T, x.device)
@@ -250,6 +258,7 @@ class TTMEmbedding:
         # reuse: backward() takes the batch's distinct rows from the lookup()
         # of the same indices on the same workspace (TT_REUSE_MERGE)
         flags = (ttc.TT_ACCUMULATE if accumulate else 0) | (ttc.TT_REUSE_MERGE if reuse else 0)
+        self.fill = _grad_fill(accumulate)
         self.desc = ttc.make_ttm_desc(row_modes, col_modes, ranks, flags)
         self.plan = ttc.tt_ttm_plan(self.desc)
         self.core_off, self.diag_off, self.n_params = ttc.tt_param_layout(self.plan)
@@ -277,7 +286,7 @@ class TTMEmbedding:
                  dparams=None, ws=None, stream=None):
         B = idx.shape[0]
         if dparams is None:
-            dparams = _new(self.n_params, torch.float32, idx.device, stream)
+            dparams = _new((self.n_params,), torch.float32, idx.device, stream, self.fill)
         if ws is None:
             ws = _scratch(stream, self.workspace, B, idx.device)
         ttc.check(ttc.tt_ttm_lookup_backward(self.plan, B, _ptr(idx), _ptr(dout), _ptr(params),
@@ -308,7 +317,7 @@ class TTNorm:
                  accumulate: bool = False):
         self.N = int(N)
         self.dtype = dtype
-        self.accumulate = bool(accumulate)
+        self.fill = _grad_fill(accumulate)
         self.plan = ttc.tt_norm_plan(N, eps, _DT[dtype], ttc.TT_ACCUMULATE if accumulate else 0)
 
     def workspace(self, T: int, device="cuda") -> torch.Tensor:
@@ -340,11 +349,10 @@ class TTNorm:
         T, N = s.shape[0], self.N
         if dx is None:
             dx = _new((T, N), self.dtype, s.device, stream)
-        fill = 0.0 if self.accumulate else None  # added to, or overwritten
         if dgamma is None:
-            dgamma = _new((N,), torch.float32, s.device, stream, fill)
+            dgamma = _new((N,), torch.float32, s.device, stream, self.fill)
         if dbeta is None:
-            dbeta = _new((N,), torch.float32, s.device, stream, fill)
+            dbeta = _new((N,), torch.float32, s.device, stream, self.fill)
         if ws is None:
             ws = _scratch(stream, self.workspace, T, s.device)
         f32, sh = torch.float32, (T, N)

@@ -140,3 +140,37 @@ def test_memory_is_the_calls_streams(made, monkeypatch, run):
     del log[:], held[:]
     run(None)
     assert log and all(at is None for _, at in log) and not held
+
+
+def _linear():
+    op = layer.TTLinear((4, 4), (4, 4), (1, 4, 4, 4, 1), torch.float32, accumulate=True)
+    x = torch.ones(3, 16)
+    return [op.backward(x, x, torch.ones(op.n_params))[1]]
+
+
+def _ffn():
+    m = ((4, 4), (4, 4), (1, 4, 4, 4, 1))
+    x, p = torch.ones(3, 16), torch.ones(200)
+    return list(layer.TTFFN(m, m, torch.float32, accumulate=True).backward(x, x, p, p)[1:])
+
+
+def _multi():
+    m = ((4, 4), (4, 4), (1, 4, 4, 4, 1))
+    x, p = torch.ones(3, 16), torch.ones(200)
+    return list(layer.TTMulti([m, m], torch.float32, accumulate=True).backward(
+        x, [x, x], [p, p])[1])
+
+
+def _ttm():
+    op = layer.TTMEmbedding((4, 4), (4, 4), (1, 4, 1), accumulate=True)
+    out = torch.ones(3, 16)
+    return [op.backward(torch.ones(3, dtype=torch.int32), out, torch.ones(op.n_params))]
+
+
+@pytest.mark.parametrize("run", [_linear, _ffn, _multi, _ttm])
+def test_gradients_that_are_added_to_start_at_zero(made, monkeypatch, run):
+    """accumulate=True and no gradient given: the kernel adds to what the call makes."""
+    real = torch.empty
+    monkeypatch.setattr(torch, "empty", lambda *a, **k: real(*a, **k).fill_(7))
+    for g in run():
+        assert float(g.abs().max()) == 0
