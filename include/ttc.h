@@ -451,6 +451,148 @@ tt_status tt_attn_backward(const tt_plan_t* plan, const tt_attn_seqs* seqs, cons
                            const tt_heads* dk, const tt_heads* dv, void* ws, size_t ws_bytes,
                            void* stream);
 
+/* ---- norm of queries and keys for each head, and their rotation by position ----
+ * Between the Q, K projections and the attention.  The CoMERA pages do not
+ * describe positions; the definitions are root mean square normalisation
+ * (Zhang and Sennrich) of each head and rotary position embedding (Su et al.).
+ * For a token at position pos and a head x of dim values, with a weight g of dim
+ * values for all query heads and one for all key heads:
+ *   u_c = x_c g_c / sqrt(sum_c x_c^2 / dim + eps)    (u = x when eps == 0)
+ *   (y_a, y_b) = (u_a cos - u_b sin, u_a sin + u_b cos) of the angle pos f_i
+ * for the pairs i < rot / 2, (a, b) = (i, i + rot / 2), or (2 i, 2 i + 1) when
+ * interleaved; y_c = u_c for c >= rot.  f_i = base^(-2 i / rot), or freqs[i].
+ * All arithmetic is fp32 and y is rounded once; angles are reduced to a turn
+ * without rounding (64-bit fractions of a turn), so far positions keep theirs. */
+typedef struct tt_rope_desc {
+  int heads;           /* query heads, 1 .. 1024 */
+  int kv_heads;        /* key / value heads, a divisor of heads */
+  int dim;             /* width of a head, 1 .. 256 */
+  int rot;             /* channels that are rotated: even, 0 .. dim */
+  double base;         /* > 0; not read when freqs is given or rot == 0 */
+  const double* freqs; /* host array of rot / 2 frequencies (radians a position) or NULL */
+  int interleaved;     /* 0: pairs half a rotation apart; else neighbours */
+  float eps;           /* >= 0, finite; 0: no norm (then rot > 0) */
+  int act;             /* tt_dtype of q, k, v and their gradients: F32 or BF16 */
+  unsigned flags;      /* TT_ACCUMULATE: the backward adds into dgq and dgk */
+} tt_rope_desc;
+/* Host only; freqs is copied.  TT_ERR_INVALID_ARG for a bad field,
+ * TT_ERR_UNSUPPORTED for E4M3 or dim above 256. */
+tt_status tt_rope_plan(const tt_rope_desc* desc, tt_plan_t** out);
+/* T tokens (below 2^31) at positions pos (T int32, device; NULL: 0, 1, ..).
+ * q, q_out: (T, heads, dim); k: (T, kv_heads, dim).  gq, gk: dim fp32 each, NULL for
+ * ones (and NULL without a norm).  rows == NULL: k_out is (T, kv_heads, dim).
+ * With rows (T int32, device): token t's keys go to row rows[t] of k_out,
+ * (cache_rows, kv_heads, dim), the other rows stay as they are; a negative row is
+ * skipped, one of cache_rows or more too and recorded in the device status word
+ * (TT_ERR_DEVICE).  Rows that are not negative must differ from one another.  v and v_out
+ * (both or neither): v's heads are copied to the rows of k_out's, unchanged.
+ * q_out may be q, and without rows k_out may be k (the same strides).  Any strides
+ * (tt_heads); pointers aligned to 16 bytes, with strides, rot / 2 and dim - rot that
+ * are multiples of 8 and 16 values (bf16; 4 and 8 in f32), are fastest.  Needs no
+ * workspace.  T == 0 is a no-op. */
+tt_status tt_rope_forward(const tt_plan_t* plan, int64_t T, const int32_t* pos,
+                          const tt_heads* q, const tt_heads* k, const float* gq,
+                          const float* gk, const tt_heads* q_out, const tt_heads* k_out,
+                          const tt_heads* v, const tt_heads* v_out, const int32_t* rows,
+                          int64_t cache_rows, void* stream);
+/* Gradients of L = <dq_out, q_out> + <dk_out, k_out> (of the form without rows): dq,
+ * dk, and dgq, dgk (dim fp32 each, overwritten or added to under TT_ACCUMULATE; either
+ * may be NULL, and both are without a norm).  q and k are the forward's inputs, not
+ * read without a norm.  dq may be dq_out or q, dk dk_out or k (the same strides).
+ * Sums over tokens and heads are taken in a fixed order: the same inputs give the
+ * same bits on a given GPU model.  Workspace: tt_workspace_size(plan, T) bytes, 256-byte
+ * aligned (none without a norm).  T == 0 writes zero dgq and dgk (or leaves them). */
+tt_status tt_rope_backward(const tt_plan_t* plan, int64_t T, const int32_t* pos,
+                           const tt_heads* q, const tt_heads* k, const float* gq,
+                           const float* gk, const tt_heads* dq_out, const tt_heads* dk_out,
+                           const tt_heads* dq, const tt_heads* dk, float* dgq, float* dgk,
+                           void* ws, size_t ws_bytes, void* stream);
+
+/* ---- dropout ---------------------------------------------------------------------
+ * [Srivastava et al.]  An element stays with probability 1 - p and is then scaled by
+ * 1 / (1 - p), else it becomes 0 (whatever it held).  Which ones stay is a function of
+ * the element's index i in its dense tensor, the seed, the offset and the site, computed
+ * where it is needed and never stored: Philox 4x32 with ten rounds (Salmon et al.,
+ * 2011), key = seed, counter words = (low 32 bits of i / 8, its high bits + site 2^16,
+ * low and high 32 bits of the offset); element i takes 16 bits, the lower half of word
+ * (i % 8) / 2 for even i, the upper for odd, and stays when they are at least
+ * cut = floor(65536 p + 1/2).  p is thus taken in steps of 2^-16, and the scale is
+ * 65536 / (65536 - cut).  rng is device memory, two int64: seed and offset; a program
+ * adds to the offset once a step (in a captured graph as well) and gives each place of
+ * its model a site of its own. */
+typedef struct tt_dropout_desc {
+  float p;  /* 0 .. 1 */
+  int site; /* 0 .. 65535 */
+  int act;  /* tt_dtype: F32 or BF16 */
+} tt_dropout_desc;
+/* Host only.  TT_ERR_INVALID_ARG for a bad field, TT_ERR_UNSUPPORTED for E4M3. */
+tt_status tt_dropout_plan(const tt_dropout_desc* desc, tt_plan_t** out);
+/* y = dropout(x) + res for n elements (n below 2^48), dense, 16-byte aligned; res may
+ * be NULL; y may be x or res itself.  Its own backward pass: dx is the dropout of dy
+ * with the same rng and site, the gradient of res is dy.  The sum is fp32, rounded
+ * once.  n == 0 is a no-op. */
+tt_status tt_dropout(const tt_plan_t* plan, int64_t n, const int64_t* rng, const void* x,
+                     const void* res, void* y, void* stream);
+/* tt_norm_forward and tt_norm_backward with dropout of x in front of the residual sum:
+ * s = dropout(x) + res.  `dropout` is a plan of tt_dropout_plan with the same activation type;
+ * i = t N + j.  The backward takes the same rng and gives dres, the gradient of s and of
+ * res, and dx = dropout(dres); dres may be NULL, and is not dx.  dx and dres may each be
+ * dy or dsum.  All else as there. */
+tt_status tt_norm_dropout_forward(const tt_plan_t* plan, const tt_plan_t* dropout, int64_t T,
+                                  const int64_t* rng, const void* x, const void* res,
+                                  const float* gamma, const float* beta, void* sum, void* y,
+                                  float* stats, void* stream);
+tt_status tt_norm_dropout_backward(const tt_plan_t* plan, const tt_plan_t* dropout, int64_t T,
+                                   const int64_t* rng, const void* s, const void* dy,
+                                   const void* dsum, const float* gamma, const float* stats,
+                                   void* dx, void* dres, float* dgamma, float* dbeta, void* ws,
+                                   size_t ws_bytes, void* stream);
+
+/* ---- log probabilities of given tokens, their entropy, top alternatives, gradient ----
+ * What follows a model's output layer: the loss of training, the scores of a text,
+ * the choice of a next token.  For a row of V logits x, z = scale x:
+ *   lse = log sum_v exp(z_v),  p_v = exp(z_v - lse),
+ *   logp = z_target - lse,     entropy = lse - sum_v p_v z_v,
+ *   top: the indices of the largest logits in order, of equal ones the lowest index
+ *   first, and their z - lse.
+ * A negative target stands for none: logp = 0 and no gradient of it.  A target of V
+ * or more is taken as none and recorded in the device status word (TT_ERR_DEVICE).
+ * A logit of -infinity has p = 0; a row of nothing else gives lse = -infinity,
+ * entropy 0, logp -infinity and zero gradients.  A NaN or +infinity makes the row's
+ * results NaN (its top indices are valid, their order is not given).  All sums are fp32.
+ * Row t of the logits starts at logits[t stride], at any multiple of the element;
+ * columns from V on are not read (nor written, in dlogits). */
+typedef struct tt_logp_desc {
+  int64_t V;    /* 1 .. 2^24 */
+  float scale;  /* 1e-6 .. 1e6: 1 / temperature */
+  int top;      /* top alternatives, 0 .. min(V, 64) */
+  int act;      /* tt_dtype of logits and their gradients: F32 or BF16 */
+} tt_logp_desc;
+/* Host only.  TT_ERR_INVALID_ARG for a bad field, TT_ERR_UNSUPPORTED for E4M3, V
+ * above 2^24 or top above 64. */
+tt_status tt_logp_plan(const tt_logp_desc* desc, tt_plan_t** out);
+/* T rows (below 2^31).  stride: elements from row to row, V .. 2^31.  targets: T int32 (NULL:
+ * no logp).  logp, lse, entropy: T fp32 each, any of them NULL where it is not wanted;
+ * top (T x top int32) and top_logp (T x top fp32): both or neither.  Needs no workspace.
+ * T == 0 is a no-op. */
+tt_status tt_logp_forward(const tt_plan_t* plan, int64_t T, const void* logits, int64_t stride,
+                          const int32_t* targets, float* logp, float* lse, float* entropy,
+                          int32_t* top, float* top_logp, void* stream);
+/* dlogits of L = sum_t dlogp logp + dentropy entropy, from the forward's lse (and entropy
+ * where dentropy is given; one of the two gradients may be NULL):
+ *   dlogits_v = scale (dlogp ([v = target] - p_v) - dentropy p_v (z_v - lse + entropy)).
+ * dlogits may be logits (the same strides). */
+tt_status tt_logp_backward(const tt_plan_t* plan, int64_t T, const void* logits, int64_t stride,
+                           const int32_t* targets, const float* lse, const float* dlogp,
+                           const float* entropy, const float* dentropy, void* dlogits,
+                           int64_t dstride, void* stream);
+/* Both in one pass, where the gradients are known beforehand (-1 / T for a mean loss):
+ * logp, lse and entropy (each may be NULL) and dlogits; reads the logits once. */
+tt_status tt_logp_loss(const tt_plan_t* plan, int64_t T, const void* logits, int64_t stride,
+                       const int32_t* targets, const float* dlogp, const float* dentropy,
+                       float* logp, float* lse, float* entropy, void* dlogits, int64_t dstride,
+                       void* stream);
+
 /* ---- the device-side error path ---------------------------------------------
  * Every wait inside the library's kernels (on a TMA transfer, on another warp
  * of the CTA, on a grid barrier) is bounded: after the limit it records

@@ -30,7 +30,6 @@ cudaError_t attn_set_debug_skip(int site) {
 
 namespace {
 
-bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
 size_t al256(size_t b) { return (b + 255) & ~size_t(255); }
 
 bool seqs_ok(const tt_attn_seqs* s) {
@@ -51,16 +50,6 @@ bool seqs_ok(const tt_attn_seqs* s) {
 // tensor cores: 8 sequences of 16: 14 and 17 us, 256 of 16: 149 and 100 us,
 // 256 of 32: 186 and 102 us, 256 of 48: 470 and 105 us.
 constexpr int kTcBwdRows = 32;
-
-// A tensor that the call reads or writes when it has rows.
-bool heads_ok(const tt_heads* h, int64_t rows, int act, Heads* out) {
-  if (!h || h->row < 0 || h->head < 0 || !aligned_to(h->p, act == TT_DT_F32 ? 4 : 2)) return false;
-  if (rows > 0 && !h->p) return false;
-  out->p = h->p;
-  out->row = h->row;
-  out->head = h->head;
-  return true;
-}
 
 AttnArgs make_args(const AttnPlan& P, const tt_attn_seqs* s) {
   AttnArgs a = {};

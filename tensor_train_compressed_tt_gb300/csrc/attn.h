@@ -1,4 +1,4 @@
-// Windowed attention: what its translation unit's kernels share.
+// Tensors of heads, and what the translation unit of windowed attention shares.
 #pragma once
 
 #include "ttc_internal.h"
@@ -14,6 +14,20 @@ struct Heads {
     return static_cast<T*>(p) + t * row + h * head;
   }
 };
+
+inline bool aligned_to(const void* p, size_t n) {
+  return (reinterpret_cast<uintptr_t>(p) % n) == 0;
+}
+
+// A tensor that the call reads or writes when it has rows.
+inline bool heads_ok(const tt_heads* h, int64_t rows, int act, Heads* out) {
+  if (!h || h->row < 0 || h->head < 0 || !aligned_to(h->p, act == TT_DT_F32 ? 4 : 2)) return false;
+  if (rows > 0 && !h->p) return false;
+  out->p = h->p;
+  out->row = h->row;
+  out->head = h->head;
+  return true;
+}
 
 struct AttnArgs {
   int B, heads, kv, group, dim;

@@ -1,0 +1,143 @@
+// Dropout of a dense tensor, with an optional residual sum: the same kernel is its
+// own backward pass (of the gradient, without the residual).
+//
+// Bound by HBM: two or three values of traffic an element against some ten
+// instructions of the generator.
+#include <cmath>
+#include <new>
+
+#include "dropout.cuh"
+#include "ttc.h"
+#include "ttc_internal.h"
+
+namespace ttc {
+namespace {
+
+constexpr int kThreads = 256;
+
+template <typename T>
+struct DropRow;  // eight elements in registers
+template <>
+struct DropRow<__nv_bfloat16> {
+  Raw<__nv_bfloat16, 8> v;
+  __device__ void load(const __nv_bfloat16* p) { v = *reinterpret_cast<const decltype(v)*>(p); }
+  __device__ void store(__nv_bfloat16* p) const { *reinterpret_cast<decltype(v)*>(p) = v; }
+  __device__ void get(float* f) const { v.get(f); }
+  __device__ void set(const float* f) { v.set(f); }
+};
+template <>
+struct DropRow<float> {
+  Raw<float, 4> a, b;
+  __device__ void load(const float* p) {
+    a = reinterpret_cast<const Raw<float, 4>*>(p)[0];
+    b = reinterpret_cast<const Raw<float, 4>*>(p)[1];
+  }
+  __device__ void store(float* p) const {
+    reinterpret_cast<Raw<float, 4>*>(p)[0] = a;
+    reinterpret_cast<Raw<float, 4>*>(p)[1] = b;
+  }
+  __device__ void get(float* f) const { a.get(f), b.get(f + 4); }
+  __device__ void set(const float* f) { a.set(f), b.set(f + 4); }
+};
+
+// A thread takes groups of eight elements, a grid apart; the next one is loaded
+// while the generator works on the current one.
+template <typename T, bool RES>
+__global__ void __launch_bounds__(kThreads) drop_kernel(int64_t n, const T* x, const T* res, T* y,
+                                                        DropArgs d) {
+  pdl_wait();
+  pdl_trigger();
+  DropKey key;
+  key.read(d);
+  const int64_t step = (int64_t)gridDim.x * kThreads, groups = n >> 3;
+  int64_t g = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  DropRow<T> rx, rr;
+  if (g < groups) {
+    rx.load(x + 8 * g);
+    if (RES) rr.load(res + 8 * g);
+  }
+  for (; g < groups; g += step) {
+    float f[8], r[8];
+    rx.get(f);
+    if (RES) rr.get(r);
+    if (g + step < groups) {
+      rx.load(x + 8 * (g + step));
+      if (RES) rr.load(res + 8 * (g + step));
+    }
+    drop<8>(key, d, 8 * g, f);
+    if (RES)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] += r[i];
+    DropRow<T> o;
+    o.set(f);
+    o.store(y + 8 * g);
+  }
+  // the last elements, fewer than eight
+  if (blockIdx.x == 0 && threadIdx.x < (n & 7)) {
+    const int64_t i = (groups << 3) + threadIdx.x;
+    float f, r = 0.f;
+    reinterpret_cast<const Raw<T, 1>*>(x)[i].get(&f);
+    if (RES) reinterpret_cast<const Raw<T, 1>*>(res)[i].get(&r);
+    drop<1>(key, d, i, &f);
+    f += r;
+    reinterpret_cast<Raw<T, 1>*>(y)[i].set(&f);
+  }
+}
+
+template <typename T>
+cudaError_t drop_go(int64_t n, const void* x, const void* res, void* y, const DropArgs& d,
+                    cudaStream_t st) {
+  const int64_t need = ((n >> 3) + kThreads - 1) / kThreads;
+  const int64_t most = (int64_t)device_sms() * 8;
+  const dim3 grid((unsigned)(need < 1 ? 1 : need < most ? need : most));
+  const T *tx = static_cast<const T*>(x), *tr = static_cast<const T*>(res);
+  return res ? launch_ex(drop_kernel<T, true>, grid, dim3(kThreads), 0, st, false, n, tx, tr,
+                         static_cast<T*>(y), d)
+             : launch_ex(drop_kernel<T, false>, grid, dim3(kThreads), 0, st, false, n, tx, tr,
+                         static_cast<T*>(y), d);
+}
+
+}  // namespace
+}  // namespace ttc
+
+using namespace ttc;
+
+extern "C" {
+
+tt_status tt_dropout_plan(const tt_dropout_desc* desc, tt_plan_t** out) {
+  if (!out) return TT_ERR_INVALID_ARG;
+  *out = nullptr;
+  if (!desc || !(desc->p >= 0.f) || !(desc->p <= 1.f) || desc->site < 0 || desc->site > 0xFFFF)
+    return TT_ERR_INVALID_ARG;
+  if (desc->act != TT_DT_F32 && desc->act != TT_DT_BF16 && desc->act != TT_DT_E4M3)
+    return TT_ERR_INVALID_ARG;
+  if (desc->act == TT_DT_E4M3) return TT_ERR_UNSUPPORTED;
+  tt_plan_s* p = new (std::nothrow) tt_plan_s();
+  if (!p) return TT_ERR_INVALID_ARG;
+  p->kind = 7;
+  p->drop.cut = (uint32_t)std::floor((double)desc->p * 65536. + 0.5);
+  p->drop.site = (uint32_t)desc->site;
+  p->drop.act = desc->act;
+  *out = p;
+  return TT_OK;
+}
+
+tt_status tt_dropout(const tt_plan_t* plan, int64_t n, const int64_t* rng, const void* x,
+                     const void* res, void* y, void* stream) {
+  if (!plan || plan->kind != 7 || n < 0 || n >= (int64_t)1 << 48) return TT_ERR_INVALID_ARG;
+  if (n == 0) return TT_OK;
+  DropArgs d;
+  if (!x || !y || !aligned_to(x, 16) || !aligned_to(res, 16) || !aligned_to(y, 16) ||
+      !drop_args(plan->drop, rng, &d))
+    return TT_ERR_INVALID_ARG;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  prof_begin(kPhElem, st);
+  const cudaError_t e = plan->drop.act == TT_DT_BF16
+                            ? drop_go<__nv_bfloat16>(n, x, res, y, d, st)
+                            : drop_go<float>(n, x, res, y, d, st);
+  prof_end(kPhElem, st);
+  count_launches(1);
+  return e == cudaSuccess ? TT_OK : TT_ERR_CUDA;
+}
+
+}  // extern "C"

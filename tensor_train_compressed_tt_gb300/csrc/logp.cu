@@ -1,0 +1,797 @@
+// Log probabilities of given tokens with the row's log-sum, entropy and top
+// alternatives; their gradient; and both in one pass over the logits.
+//
+// All are bound by HBM.  In units of log2, with c = scale log2(e) and M = c max:
+//   t = c x - M,  e = 2^t,  s = sum e,  w = sum e t
+//   lse = ln2 (M + log2 s),  log p = ln2 (t - log2 s),  H = ln2 (log2 s - w / s)
+//   d L / d x = scale (g ([target] - p) - h p (log p + H))
+//             = e (A + B t) + scale g [target]
+// One pass finds M, s and w: each thread keeps the maximum of what it has seen and
+// scales its sums when that rises (rarely, after the first values); the threads'
+// sums meet at the common maximum.  t is one fused multiply-add on a common M, so a
+// log probability is as exact at logits of a thousand as at logits of one.
+//
+// A row is taken by 1, 4 or 16 warps by its width; rows that are few or long are
+// split over a cluster's CTAs, which meet through shared memory.  Rows start
+// anywhere: the elements before the first and after the last 16-byte boundary are
+// taken one by one.  The pass that also writes the gradient keeps the row in shared
+// memory in between (each thread its own values), so it reads it from HBM once.
+//
+// Top alternatives: the maxima of 128 groups of threads give a bound (the k-th
+// largest of them: at least k values are not below it); the few groups that reach
+// it are read again, the values not below the bound are ranked by (value, lowest
+// index).  Where ties make them too many, k rounds over the row take them in order.
+#include <cmath>
+#include <new>
+#include <type_traits>
+
+#include "rows.cuh"
+#include "ttc.h"
+#include "ttc_internal.h"
+
+namespace ttc {
+
+cudaError_t read_and_clear_logp_status(DeviceStatus* out) {
+  cudaError_t e = cudaMemcpyFromSymbol(out, g_status, sizeof(DeviceStatus));
+  if (e != cudaSuccess) return e;
+  DeviceStatus z{0, 0};
+  return cudaMemcpyToSymbol(g_status, &z, sizeof(z));
+}
+
+namespace {
+
+constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kLog2e = 1.4426950408889634074f;
+constexpr int kRowsPerBlock = 8;  // of one warp each
+constexpr int kMaxCluster = 8;
+constexpr int kMaxTop = 64;
+constexpr int kGroups = 128;      // of threads, for the bound of the top values
+constexpr int kList = 512;        // candidates; a cluster's kMaxTop each fit too
+
+struct LogpArgs {
+  int64_t T;
+  int V, top, cluster;
+  int staged;  // vectors a thread keeps in shared memory (with a gradient)
+  float c, scale;
+  const void* x;
+  int64_t stride;
+  const int32_t* targets;
+  float *logp, *lse, *ent;
+  int32_t* ids;
+  float* tops;
+  const float *dlogp, *dent;
+  const float *lse_in, *ent_in;  // the gradient alone
+  void* dx;
+  int64_t dstride;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// A vector of 16 bytes, or one element where rows of x and dx lie differently.
+template <typename T, int VEC>
+__device__ __forceinline__ float raw_max(const Raw<T, VEC>& r, const float* f) {
+  float m = f[0];
+#pragma unroll
+  for (int i = 1; i < VEC; ++i) m = fmaxf(m, f[i]);
+  return m;
+}
+template <>
+__device__ __forceinline__ float raw_max<__nv_bfloat16, 8>(const Raw<__nv_bfloat16, 8>& r,
+                                                           const float*) {
+  const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&r.v);
+  const __nv_bfloat162 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+  return fmaxf(__low2float(m), __high2float(m));
+}
+
+// Where a row's elements lie: `head` before the first whole vector, `vecs` vectors,
+// then the rest.
+struct Cut {
+  int head = 0, vecs = 0, edges = 0;
+  template <typename T, int VEC>
+  __device__ void set(const T* x, int V) {
+    head = VEC == 1 ? 0 : (int)((0u - (unsigned)(reinterpret_cast<uintptr_t>(x) / sizeof(T))) %
+                                (unsigned)VEC);
+    if (head > V) head = V;
+    vecs = (V - head) / VEC;
+    edges = V - vecs * VEC;
+  }
+  // the i-th element outside the vectors
+  template <int VEC>
+  __device__ int edge(int i) const {
+    return i < head ? i : vecs * VEC + i;
+  }
+};
+
+// Running maximum and sums of a thread.
+template <bool ENT>
+struct Sums {
+  float m = -INFINITY, M = 0.f;  // maximum; c times it (0 while there is none)
+  float2 s = make_float2(0.f, 0.f), w = s;
+  __device__ void raise(float to, float c) {
+    const float N = to * c;
+    if (m > -INFINITY) scale(M - N);
+    m = to;
+    M = N;
+  }
+  // the sums at a maximum higher by -by
+  __device__ void scale(float by) {
+    const float a = ex2(by);
+    if (ENT) {
+      // a sum of zero has no terms to shift (by may be -infinity)
+      w.x = s.x > 0.f ? a * fmaf(s.x, by, w.x) : w.x * a;
+      w.y = s.y > 0.f ? a * fmaf(s.y, by, w.y) : w.y * a;
+      if (a == 0.f) w.x = w.y = 0.f;
+    }
+    s.x *= a;
+    s.y *= a;
+  }
+  template <int VEC>
+  __device__ void add(const float* f, float top, float c) {
+    if (top > m) raise(top, c);
+    if (VEC == 1) {
+      const float t = fmaf(f[0], c, -M), e = ex2(t);
+      s.x += e;
+      if (ENT) w.x = fmaf(e, fmaxf(t, -256.f), w.x);
+    }
+    const float2 cc = make_float2(c, c), mm = make_float2(-M, -M);
+#pragma unroll
+    for (int i = 0; i + 1 < VEC; i += 2) {
+      float2 t = __ffma2_rn(make_float2(f[i], f[i + 1]), cc, mm);
+      const float2 e = make_float2(ex2(t.x), ex2(t.y));
+      s = __fadd2_rn(s, e);
+      if (ENT) {
+        t.x = fmaxf(t.x, -256.f);  // 0 times -infinity
+        t.y = fmaxf(t.y, -256.f);
+        w = __ffma2_rn(e, t, w);
+      }
+    }
+  }
+};
+
+template <int W>
+__device__ __forceinline__ float team_max(float v, float2 (*red)[32]) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  if (W == 1) return v;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (lane == 0) red[0][warp].x = v;
+  __syncthreads();
+  v = red[0][lane & (W - 1)].x;
+#pragma unroll
+  for (int o = W / 2; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+template <int W>
+__device__ __forceinline__ float2 team_sum(float2 v, float2 (*red)[32]) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+    v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+  }
+  if (W == 1) return v;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (lane == 0) red[1][warp] = v;
+  __syncthreads();
+  v = red[1][lane & (W - 1)];
+#pragma unroll
+  for (int o = W / 2; o; o >>= 1) {
+    v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+    v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+  }
+  return v;
+}
+
+// ---- the CTAs of a cluster ----------------------------------------------------------
+__device__ __forceinline__ uint32_t peer_at(const void* p, int rank) {
+  uint32_t there;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(su32(p)), "r"(rank));
+  return there;
+}
+__device__ __forceinline__ float peer_float(const float* p, int rank) {
+  float x;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(peer_at(p, rank)) : "memory");
+  return x;
+}
+__device__ __forceinline__ uint64_t peer_u64(const uint64_t* p, int rank) {
+  uint64_t x;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(x) : "r"(peer_at(p, rank)) : "memory");
+  return x;
+}
+__device__ __forceinline__ void cluster_meet() {
+  asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+
+// ---- order of the top values ----------------------------------------------------------
+// Larger keys come first: by value (-0 as 0, NaN above all numbers).
+__device__ __forceinline__ uint32_t key_of(float x) {
+  if (x != x) return 0xFFFFFFFFu;
+  const uint32_t b = __float_as_uint(x + 0.f);
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float of_key(uint32_t k) {
+  return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
+}
+// and by index, the lowest first.  0 stands for none.
+__device__ __forceinline__ uint64_t entry(uint32_t key, int index) {
+  return (uint64_t)key << 32 | (uint32_t)~index;
+}
+
+struct TopShared {
+  uint32_t keys[kGroups];
+  int groups[kGroups];
+  uint64_t list[kList];
+  uint64_t best[kMaxTop];
+  uint64_t red[16];
+  uint32_t bound;
+  int found, chosen;
+};
+
+// The slice's k first entries in order into sh.best (0 where there are fewer).
+template <typename T, int VEC, int W>
+__device__ void top_of_slice(TopShared& sh, const T* x, const Cut& cut, int first, int last,
+                             int edges, float most, int k) {
+  using R = Raw<T, VEC>;
+  constexpr int G = 32 * W, SIDE = G / kGroups;  // threads of a group
+  static_assert(G % kGroups == 0 && 32 % SIDE == 0, "groups within a warp");
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const R* body = reinterpret_cast<const R*>(x + cut.head);
+  uint32_t key = key_of(most);
+#pragma unroll
+  for (int o = SIDE / 2; o; o >>= 1) key = max(key, __shfl_xor_sync(0xffffffffu, key, o));
+  if (tid % SIDE == 0) sh.keys[tid / SIDE] = key;
+  if (tid == 0) sh.found = sh.chosen = 0;
+  if (tid < k) sh.best[tid] = 0;
+  __syncthreads();
+  if (tid < kGroups) {
+    const uint32_t mine = sh.keys[tid];
+    int before = 0;
+    for (int j = 0; j < kGroups; ++j)
+      before += sh.keys[j] > mine || (sh.keys[j] == mine && j < tid);
+    if (before == k - 1) sh.bound = mine;  // one group's rank, k <= kGroups
+  }
+  __syncthreads();
+  const uint32_t bound = sh.bound;
+  if (tid < kGroups && sh.keys[tid] >= bound) sh.groups[atomicAdd(&sh.chosen, 1)] = tid;
+  __syncthreads();
+  auto offer = [&](float f, int i) {
+    const uint32_t at = key_of(f);
+    if (at < bound) return;
+    const int n = atomicAdd(&sh.found, 1);
+    if (n < kList) sh.list[n] = entry(at, i);
+  };
+  for (int i = warp; i < sh.chosen; i += W) {
+    const int g = sh.groups[i];
+    for (int v = first + g * SIDE + lane % SIDE + G * (lane / SIDE); v < last;
+         v += G * (32 / SIDE)) {
+      float f[VEC];
+      body[v].get(f);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) offer(f[j], cut.head + v * VEC + j);
+    }
+  }
+  if (tid < edges) {
+    const int i = cut.edge<VEC>(tid);
+    float f;
+    reinterpret_cast<const Raw<T, 1>*>(x)[i].get(&f);
+    offer(f, i);
+  }
+  __syncthreads();
+  const int n = sh.found;
+  if (n <= kList) {
+    for (int i = tid; i < n; i += G) {
+      const uint64_t e = sh.list[i];
+      int before = 0;
+      for (int j = 0; j < n; ++j) before += sh.list[j] > e;
+      if (before < k) sh.best[before] = e;
+    }
+    __syncthreads();
+    return;
+  }
+  uint64_t prev = ~0ull;
+  for (int r = 0; r < k; ++r) {
+    uint64_t e = 0;
+    auto next = [&](float f, int i) {
+      const uint64_t at = entry(key_of(f), i);
+      if (at < prev && at > e) e = at;
+    };
+    for (int v = first + tid; v < last; v += G) {
+      float f[VEC];
+      body[v].get(f);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) next(f[j], cut.head + v * VEC + j);
+    }
+    if (tid < edges) {
+      const int i = cut.edge<VEC>(tid);
+      float f;
+      reinterpret_cast<const Raw<T, 1>*>(x)[i].get(&f);
+      next(f, i);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      const uint64_t b = __shfl_xor_sync(0xffffffffu, e, o);
+      if (b > e) e = b;
+    }
+    if (lane == 0) sh.red[warp] = e;
+    __syncthreads();
+    e = sh.red[0];
+    for (int j = 1; j < W; ++j)
+      if (sh.red[j] > e) e = sh.red[j];
+    __syncthreads();
+    if (tid == 0) sh.best[r] = e;
+    prev = e;
+  }
+  __syncthreads();
+}
+
+constexpr int kAhead = 4;  // vectors that a thread loads at once
+
+// One row a team of W warps (a cluster of such blocks where p.cluster > 1).
+template <typename T, int VEC, int W, bool ENT, bool TOP, bool GRAD>
+__global__ void __launch_bounds__(W == 1 ? 32 * kRowsPerBlock : 32 * W) logp_kernel(LogpArgs p) {
+  using R = Raw<T, VEC>;
+  constexpr int G = 32 * W;
+  extern __shared__ uint4 stage_bytes[];
+  __shared__ float2 red[2][32];
+  __shared__ float meet[3];
+  __shared__ typename std::conditional<TOP, TopShared, int>::type top_shared;
+  const int tid = W == 1 ? threadIdx.x & 31 : threadIdx.x;
+  const int rank = W == 16 ? blockIdx.x % p.cluster : 0;
+  const int64_t row = W == 1 ? (int64_t)blockIdx.x * kRowsPerBlock + (threadIdx.x >> 5)
+                             : (int64_t)blockIdx.x / p.cluster;
+  pdl_wait();
+  pdl_trigger();
+  if (row >= p.T) return;  // whole warps, and only where no barrier is met (W == 1)
+  const T* x = static_cast<const T*>(p.x) + row * p.stride;
+  Cut cut;
+  cut.set<T, VEC>(x, p.V);
+  int first = 0, last = cut.vecs;
+  if (W == 16 && p.cluster > 1) {
+    const int per = (cut.vecs + p.cluster - 1) / p.cluster;
+    first = min(rank * per, cut.vecs);
+    last = min(first + per, cut.vecs);
+  }
+  const R* body = reinterpret_cast<const R*>(x + cut.head);
+  R* stage = reinterpret_cast<R*>(stage_bytes) + threadIdx.x;
+  constexpr int stage_step = W == 1 ? 32 * kRowsPerBlock : G;
+  int target = -1;
+  float picked = 0.f;
+  if (p.targets) {
+    target = p.targets[row];
+    if (target >= p.V) {
+      if (tid == 0 && rank == 0) record_error(TT_ERR_DEVICE, 2);
+      target = -1;
+    }
+    if (target >= 0) reinterpret_cast<const Raw<T, 1>*>(x)[target].get(&picked);
+  }
+
+  Sums<ENT> sum;
+  const int edges = rank == 0 ? cut.edges : 0;
+  float lone = 0.f;
+  if (tid < edges) {
+    reinterpret_cast<const Raw<T, 1>*>(x)[cut.edge<VEC>(tid)].get(&lone);
+    sum.template add<1>(&lone, lone, p.c);
+  }
+  int kept = 0;
+  for (int v = first + tid; v < last; v += kAhead * G) {
+    R r[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      if (v + k * G < last) r[k] = body[v + k * G];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      if (v + k * G >= last) break;
+      float f[VEC];
+      r[k].get(f);
+      sum.template add<VEC>(f, raw_max<T, VEC>(r[k], f), p.c);
+      if (GRAD) {
+        if (kept < p.staged) stage[kept * stage_step] = r[k];
+        ++kept;
+      }
+    }
+  }
+  // the team's, then the cluster's
+  float most = team_max<W>(sum.m, red);
+  float M = most > -INFINITY ? most * p.c : 0.f;
+  if (sum.m > -INFINITY && M != sum.M) sum.scale(sum.M - M);
+  float2 sw = team_sum<W>(make_float2(sum.s.x + sum.s.y, sum.w.x + sum.w.y), red);
+  if (W == 16 && p.cluster > 1) {
+    if (tid == 0) meet[0] = most, meet[1] = sw.x, meet[2] = sw.y;
+    cluster_meet();
+    const int lane = tid & 31;
+    Sums<ENT> one;
+    if (lane < p.cluster) {
+      one.m = peer_float(meet, lane);
+      one.s.x = peer_float(meet + 1, lane);
+      one.w.x = peer_float(meet + 2, lane);
+    }
+    one.M = one.m > -INFINITY ? one.m * p.c : 0.f;
+    most = one.m;
+#pragma unroll
+    for (int o = kMaxCluster / 2; o; o >>= 1)
+      most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+    most = __shfl_sync(0xffffffffu, most, 0);
+    M = most > -INFINITY ? most * p.c : 0.f;
+    if (one.m > -INFINITY && M != one.M) one.scale(one.M - M);
+#pragma unroll
+    for (int o = kMaxCluster / 2; o; o >>= 1) {
+      one.s.x += __shfl_xor_sync(0xffffffffu, one.s.x, o);
+      one.w.x += __shfl_xor_sync(0xffffffffu, one.w.x, o);
+    }
+    sw.x = __shfl_sync(0xffffffffu, one.s.x, 0);
+    sw.y = __shfl_sync(0xffffffffu, one.w.x, 0);
+  }
+  const float logs = log2f(sw.x);  // -infinity where no logit is above it
+  const float ent = sw.x == 0.f ? 0.f : kLn2 * (logs - sw.y / sw.x);
+  if (tid == 0 && rank == 0) {
+    if (p.lse) p.lse[row] = sw.x == 0.f ? -INFINITY : kLn2 * (M + logs);
+    if (p.logp)
+      p.logp[row] = target < 0                                 ? 0.f
+                    : sw.x == 0.f || picked == -INFINITY ? -INFINITY
+                                                         : kLn2 * (fmaf(picked, p.c, -M) - logs);
+    if (ENT && p.ent) p.ent[row] = ent;
+  }
+
+  if constexpr (TOP) {
+    top_of_slice<T, VEC, W>(top_shared, x, cut, first, last, edges, sum.m, p.top);
+    if (W == 16 && p.cluster > 1) {
+      cluster_meet();
+      if (rank == 0) {
+        const int n = p.cluster * p.top;
+        for (int i = tid; i < n; i += G)
+          top_shared.list[i] = peer_u64(top_shared.best + i % p.top, i / p.top);
+        __syncthreads();
+        for (int i = tid; i < n; i += G) {
+          const uint64_t e = top_shared.list[i];
+          int before = 0;
+          for (int j = 0; j < n; ++j) before += top_shared.list[j] > e;
+          if (before < p.top && e) top_shared.best[before] = e;
+        }
+        __syncthreads();
+      }
+    }
+    if (rank == 0 && tid < p.top) {
+      const uint64_t e = top_shared.best[tid];
+      const float f = of_key((uint32_t)(e >> 32));
+      p.ids[row * p.top + tid] = (int)~(uint32_t)e;
+      p.tops[row * p.top + tid] = f == -INFINITY ? f : kLn2 * (fmaf(f, p.c, -M) - logs);
+    }
+  }
+
+  if constexpr (GRAD) {
+    if (W == 1) __syncwarp();  // dx may be x: the target's logit is read by now
+    T* dx = static_cast<T*>(p.dx) + row * p.dstride;
+    R* out = reinterpret_cast<R*>(dx + cut.head);
+    const float g = target >= 0 && p.dlogp ? p.dlogp[row] : 0.f;
+    const float h = ENT && p.dent ? p.dent[row] : 0.f;
+    const bool none = (g == 0.f && h == 0.f) || sw.x == 0.f;
+    const float inv = 1.f / sw.x;
+    const float A = -p.scale * fmaf(h, ent - kLn2 * logs, g) * inv;
+    const float B = -p.scale * kLn2 * h * inv;
+    auto grad = [&](float f) {
+      const float t = fmaf(f, p.c, -M);
+      return none ? 0.f : ex2(t) * (ENT ? fmaf(B, fmaxf(t, -256.f), A) : A);
+    };
+    if (tid < edges) {
+      const int i = cut.edge<VEC>(tid);
+      float d = grad(lone);
+      if (i == target && !none) d = fmaf(p.scale, g, d);
+      reinterpret_cast<Raw<T, 1>*>(dx)[i].set(&d);
+    }
+    const int there = target >= cut.head ? (target - cut.head) / VEC : -1;
+    int i = 0;
+    for (int v = first + tid; v < last; v += G, ++i) {
+      const R r = i < p.staged ? stage[i * stage_step] : body[v];
+      float f[VEC];
+      r.get(f);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) f[j] = grad(f[j]);
+      if (v == there && !none) {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j)
+          if (cut.head + v * VEC + j == target) f[j] = fmaf(p.scale, g, f[j]);
+      }
+      R o;
+      o.set(f);
+      out[v] = o;
+    }
+  }
+  if (W == 16 && p.cluster > 1) cluster_meet();  // no CTA leaves while another reads its shares
+}
+
+// The gradient alone, from the row's log-sum and entropy: a block a piece of a row
+// (a warp a row where rows are short).
+constexpr int kGradThreads = 256;
+template <typename T, int VEC, bool SHORT, bool ENT>
+__global__ void __launch_bounds__(kGradThreads) logp_grad_kernel(LogpArgs p, int pieces) {
+  using R = Raw<T, VEC>;
+  constexpr int G = SHORT ? 32 : kGradThreads;
+  const int tid = SHORT ? threadIdx.x & 31 : threadIdx.x;
+  const int64_t row = SHORT ? (int64_t)blockIdx.x * kRowsPerBlock + (threadIdx.x >> 5)
+                            : (int64_t)blockIdx.x / pieces;
+  const int piece = SHORT ? 0 : blockIdx.x % pieces;
+  pdl_wait();
+  pdl_trigger();
+  if (row >= p.T) return;
+  const T* x = static_cast<const T*>(p.x) + row * p.stride;
+  T* dx = static_cast<T*>(p.dx) + row * p.dstride;
+  Cut cut;
+  cut.set<T, VEC>(x, p.V);
+  const R* body = reinterpret_cast<const R*>(x + cut.head);
+  R* out = reinterpret_cast<R*>(dx + cut.head);
+  int target = p.targets ? p.targets[row] : -1;
+  if (target >= p.V) {
+    if (tid == 0 && piece == 0) record_error(TT_ERR_DEVICE, 2);
+    target = -1;
+  }
+  const float lse = p.lse_in[row];
+  const float g = target >= 0 && p.dlogp ? p.dlogp[row] : 0.f;
+  const float h = ENT ? p.dent[row] : 0.f;
+  const bool none = (g == 0.f && h == 0.f) || lse == -INFINITY;
+  const float A = ENT ? -p.scale * fmaf(h, p.ent_in[row], g) : -p.scale * g, B = -p.scale * h;
+  auto grad = [&](float f) {
+    const float lp = fmaf(f, p.scale, -lse);
+    return none ? 0.f : ex2(lp * kLog2e) * (ENT ? fmaf(B, fmaxf(lp, -256.f), A) : A);
+  };
+  if (piece == 0 && tid < cut.edges) {
+    const int i = cut.edge<VEC>(tid);
+    float d;
+    reinterpret_cast<const Raw<T, 1>*>(x)[i].get(&d);
+    d = grad(d);
+    if (i == target && !none) d = fmaf(p.scale, g, d);
+    reinterpret_cast<Raw<T, 1>*>(dx)[i].set(&d);
+  }
+  const int there = target >= cut.head ? (target - cut.head) / VEC : -1;
+  const int first = SHORT ? 0 : piece * kAhead * G;
+  const int last = SHORT ? cut.vecs : min(cut.vecs, first + kAhead * G);
+  for (int v = first + tid; v < last; v += kAhead * G) {
+    R r[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      if (v + k * G < last) r[k] = body[v + k * G];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int at = v + k * G;
+      if (at >= last) break;
+      float f[VEC];
+      r[k].get(f);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) f[j] = grad(f[j]);
+      if (at == there && !none) {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j)
+          if (cut.head + at * VEC + j == target) f[j] = fmaf(p.scale, g, f[j]);
+      }
+      R o;
+      o.set(f);
+      out[at] = o;
+    }
+  }
+}
+
+// ---- dispatch --------------------------------------------------------------------
+
+// Whether row t of x and of dx start at the same distance from a 16-byte boundary.
+bool alike(const LogpArgs& a, size_t size) {
+  const uintptr_t gap = reinterpret_cast<uintptr_t>(a.x) - reinterpret_cast<uintptr_t>(a.dx);
+  return gap % 16 == 0 && (a.T == 1 || ((uint64_t)(a.stride - a.dstride) * size) % 16 == 0);
+}
+
+constexpr size_t kStageBytes = 216 << 10;  // most that a CTA keeps of a row
+
+template <typename T, int VEC, int W, bool ENT, bool TOP, bool GRAD>
+cudaError_t go(LogpArgs& a, cudaStream_t st) {
+  auto kernel = logp_kernel<T, VEC, W, ENT, TOP, GRAD>;
+  constexpr int threads = W == 1 ? 32 * kRowsPerBlock : 32 * W;
+  const int64_t rows = W == 1 ? (a.T + kRowsPerBlock - 1) / kRowsPerBlock : a.T;
+  a.cluster = 1;
+  const int64_t vecs = a.V / VEC + 1;  // of a row, at most
+  if (W == 16) {
+    // CTAs for every SM, but no less than four vectors a thread of each; with a
+    // gradient, as many as keep a slice to 64 KB, three CTAs an SM
+    while (a.cluster < kMaxCluster && vecs / (2 * a.cluster) >= 4 * threads &&
+           rows * a.cluster < 2 * (int64_t)device_sms())
+      a.cluster *= 2;
+    if (GRAD)
+      while (a.cluster < kMaxCluster &&
+             (vecs + a.cluster - 1) / a.cluster * sizeof(Raw<T, VEC>) > (64 << 10))
+        a.cluster *= 2;
+  }
+  size_t smem = 0;
+  a.staged = 0;
+  if (GRAD) {
+    const size_t each = sizeof(Raw<T, VEC>) * threads;
+    const int64_t need = ((vecs + a.cluster - 1) / a.cluster + 32 * W - 1) / (32 * W);
+    a.staged = (int)(need * each <= kStageBytes ? need : kStageBytes / each);
+    smem = a.staged * each;
+    static PerDevice once;
+    const cudaError_t e = once.get([&] {
+      return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  (int)kStageBytes);
+    });
+    if (e != cudaSuccess) return e;
+  }
+  if (rows * a.cluster > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+  const dim3 grid((unsigned)(rows * a.cluster));
+  return a.cluster > 1 ? launch_cluster(kernel, grid, dim3(threads), smem, st, a.cluster, a)
+                       : launch_ex(kernel, grid, dim3(threads), smem, st, false, a);
+}
+
+// Warps of a row by its vectors: few have less than two a thread.
+template <typename T, int VEC, bool ENT, bool TOP, bool GRAD>
+cudaError_t by_width(LogpArgs& a, cudaStream_t st) {
+  const int64_t vecs = a.V / VEC;
+  if constexpr (!TOP)
+    if (vecs <= 64) return go<T, VEC, 1, ENT, TOP, GRAD>(a, st);
+  return vecs <= 512 ? go<T, VEC, 4, ENT, TOP, GRAD>(a, st)
+                     : go<T, VEC, 16, ENT, TOP, GRAD>(a, st);
+}
+
+template <typename T>
+cudaError_t forward(LogpArgs& a, cudaStream_t st) {
+  constexpr int VEC = 16 / sizeof(T);
+  if (a.top)
+    return a.ent ? by_width<T, VEC, true, true, false>(a, st)
+                 : by_width<T, VEC, false, true, false>(a, st);
+  return a.ent ? by_width<T, VEC, true, false, false>(a, st)
+               : by_width<T, VEC, false, false, false>(a, st);
+}
+template <typename T>
+cudaError_t loss(LogpArgs& a, cudaStream_t st) {
+  constexpr int VEC = 16 / sizeof(T);
+  const bool ent = a.ent || a.dent;
+  if (!alike(a, sizeof(T)))
+    return ent ? by_width<T, 1, true, false, true>(a, st)
+               : by_width<T, 1, false, false, true>(a, st);
+  return ent ? by_width<T, VEC, true, false, true>(a, st)
+             : by_width<T, VEC, false, false, true>(a, st);
+}
+template <typename T, int VEC, bool ENT>
+cudaError_t grad_go(LogpArgs& a, cudaStream_t st) {
+  const int64_t vecs = a.V / VEC;
+  const int64_t pieces = (vecs + kAhead * kGradThreads - 1) / (kAhead * kGradThreads);
+  const bool brief = vecs <= 128;
+  const int64_t blocks = brief ? (a.T + kRowsPerBlock - 1) / kRowsPerBlock : a.T * pieces;
+  if (blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+  return launch_ex(brief ? logp_grad_kernel<T, VEC, true, ENT>
+                         : logp_grad_kernel<T, VEC, false, ENT>,
+                   dim3((unsigned)blocks), dim3(kGradThreads), 0, st, false, a, (int)pieces);
+}
+template <typename T>
+cudaError_t backward(LogpArgs& a, cudaStream_t st) {
+  constexpr int VEC = 16 / sizeof(T);
+  if (!alike(a, sizeof(T)))
+    return a.dent ? grad_go<T, 1, true>(a, st) : grad_go<T, 1, false>(a, st);
+  return a.dent ? grad_go<T, VEC, true>(a, st) : grad_go<T, VEC, false>(a, st);
+}
+
+// The arguments that every call has.
+bool common_ok(const tt_plan_t* plan, int64_t T, const void* logits, int64_t stride,
+               const int32_t* targets, LogpArgs* a) {
+  if (!plan || plan->kind != 8 || T < 0 || T > 0x7FFFFFFF) return false;
+  const LogpPlan& P = plan->logits;
+  if (stride < P.V || stride > (int64_t)1 << 31 || !aligned_to(targets, 4) ||
+      !aligned_to(logits, P.act == TT_DT_F32 ? 4 : 2) || (T > 0 && !logits))
+    return false;
+  *a = LogpArgs{};
+  a->T = T;
+  a->V = (int)P.V;
+  a->c = P.scale * kLog2e;
+  a->scale = P.scale;
+  a->x = logits;
+  a->stride = stride;
+  a->targets = targets;
+  return true;
+}
+
+tt_status done(cudaError_t e, cudaStream_t st) {
+  prof_end(kPhElem, st);
+  count_launches(1);
+  return e == cudaErrorInvalidConfiguration ? TT_ERR_UNSUPPORTED
+         : e == cudaSuccess                 ? TT_OK
+                                            : TT_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace ttc
+
+using namespace ttc;
+
+extern "C" {
+
+tt_status tt_logp_plan(const tt_logp_desc* desc, tt_plan_t** out) {
+  if (!out) return TT_ERR_INVALID_ARG;
+  *out = nullptr;
+  if (!desc || desc->V < 1 || !(desc->scale >= 1e-6f) || !(desc->scale <= 1e6f) ||
+      desc->top < 0 || desc->top > desc->V)
+    return TT_ERR_INVALID_ARG;
+  if (desc->act != TT_DT_F32 && desc->act != TT_DT_BF16 && desc->act != TT_DT_E4M3)
+    return TT_ERR_INVALID_ARG;
+  if (desc->act == TT_DT_E4M3 || desc->V > (1 << 24) || desc->top > kMaxTop)
+    return TT_ERR_UNSUPPORTED;
+  tt_plan_s* p = new (std::nothrow) tt_plan_s();
+  if (!p) return TT_ERR_INVALID_ARG;
+  p->kind = 8;
+  p->logits.V = desc->V;
+  p->logits.scale = desc->scale;
+  p->logits.top = desc->top;
+  p->logits.act = desc->act;
+  *out = p;
+  return TT_OK;
+}
+
+tt_status tt_logp_forward(const tt_plan_t* plan, int64_t T, const void* logits, int64_t stride,
+                          const int32_t* targets, float* logp, float* lse, float* entropy,
+                          int32_t* top, float* top_logp, void* stream) {
+  LogpArgs a;
+  if (!common_ok(plan, T, logits, stride, targets, &a) || (logp && !targets) ||
+      (!top) != (!top_logp) || (top && !plan->logits.top) || !aligned_to(logp, 4) ||
+      !aligned_to(lse, 4) || !aligned_to(entropy, 4) || !aligned_to(top, 4) ||
+      !aligned_to(top_logp, 4))
+    return TT_ERR_INVALID_ARG;
+  if (T == 0) return TT_OK;
+  a.logp = logp;
+  a.lse = lse;
+  a.ent = entropy;
+  a.top = top ? plan->logits.top : 0;
+  a.ids = top;
+  a.tops = top_logp;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  prof_begin(kPhElem, st);
+  return done(plan->logits.act == TT_DT_BF16 ? forward<__nv_bfloat16>(a, st)
+                                             : forward<float>(a, st), st);
+}
+
+tt_status tt_logp_backward(const tt_plan_t* plan, int64_t T, const void* logits, int64_t stride,
+                           const int32_t* targets, const float* lse, const float* dlogp,
+                           const float* entropy, const float* dentropy, void* dlogits,
+                           int64_t dstride, void* stream) {
+  LogpArgs a;
+  if (!common_ok(plan, T, logits, stride, targets, &a) || dstride < a.V ||
+      dstride > (int64_t)1 << 31 || (dlogp && !targets) || (!dlogp && !dentropy) ||
+      (dentropy && !entropy && T > 0) || (T > 0 && (!lse || !dlogits)) || !aligned_to(lse, 4) ||
+      !aligned_to(dlogp, 4) || !aligned_to(entropy, 4) || !aligned_to(dentropy, 4) ||
+      !aligned_to(dlogits, plan->logits.act == TT_DT_F32 ? 4 : 2))
+    return TT_ERR_INVALID_ARG;
+  if (T == 0) return TT_OK;
+  a.lse_in = lse;
+  a.dlogp = dlogp;
+  a.ent_in = entropy;
+  a.dent = dentropy;
+  a.dx = dlogits;
+  a.dstride = dstride;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  prof_begin(kPhElem, st);
+  return done(plan->logits.act == TT_DT_BF16 ? backward<__nv_bfloat16>(a, st)
+                                             : backward<float>(a, st), st);
+}
+
+tt_status tt_logp_loss(const tt_plan_t* plan, int64_t T, const void* logits, int64_t stride,
+                       const int32_t* targets, const float* dlogp, const float* dentropy,
+                       float* logp, float* lse, float* entropy, void* dlogits, int64_t dstride,
+                       void* stream) {
+  LogpArgs a;
+  if (!common_ok(plan, T, logits, stride, targets, &a) || dstride < a.V ||
+      dstride > (int64_t)1 << 31 || ((dlogp || logp) && !targets) || (!dlogp && !dentropy) ||
+      (T > 0 && !dlogits) || !aligned_to(logp, 4) || !aligned_to(lse, 4) ||
+      !aligned_to(entropy, 4) || !aligned_to(dlogp, 4) || !aligned_to(dentropy, 4) ||
+      !aligned_to(dlogits, plan->logits.act == TT_DT_F32 ? 4 : 2))
+    return TT_ERR_INVALID_ARG;
+  if (T == 0) return TT_OK;
+  a.logp = logp;
+  a.lse = lse;
+  a.ent = entropy;
+  a.dlogp = dlogp;
+  a.dent = dentropy;
+  a.dx = dlogits;
+  a.dstride = dstride;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  prof_begin(kPhElem, st);
+  return done(plan->logits.act == TT_DT_BF16 ? loss<__nv_bfloat16>(a, st) : loss<float>(a, st),
+              st);
+}
+
+}  // extern "C"

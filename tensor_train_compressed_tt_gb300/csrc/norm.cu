@@ -14,92 +14,15 @@
 // dbeta) accumulate in registers over the rows a group of warps owns, each
 // block leaves one partial row in the workspace, and a second kernel adds the
 // partials in block order: no atomics, the same bits every time.
-#include <cuda_bf16.h>
-
 #include <cmath>
 #include <new>
 
-#include "tc_ptx.cuh"
+#include "dropout.cuh"
 #include "ttc.h"
 #include "ttc_internal.h"
 
 namespace ttc {
 namespace {
-
-// ---- vector loads and stores -------------------------------------------------
-// VEC consecutive elements of type T as they lie in memory.
-template <typename T, int VEC>
-struct Raw;
-template <>
-struct Raw<float, 4> {
-  float4 v;
-  __device__ void get(float* f) const { f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w; }
-  __device__ void set(const float* f) { v = make_float4(f[0], f[1], f[2], f[3]); }
-};
-template <>
-struct Raw<float, 1> {
-  float v;
-  __device__ void get(float* f) const { f[0] = v; }
-  __device__ void set(const float* f) { v = f[0]; }
-};
-template <>
-struct Raw<__nv_bfloat16, 4> {
-  uint2 v;
-  __device__ void get(float* f) const {
-    const uint32_t w[2] = {v.x, v.y};
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {  // a bf16 is the upper half of its f32
-      f[2 * i] = __uint_as_float(w[i] << 16);
-      f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
-  }
-  __device__ void set(const float* f) {
-    v = make_uint2(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]));
-  }
-};
-template <>
-struct Raw<__nv_bfloat16, 8> {
-  uint4 v;
-  __device__ void get(float* f) const {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = __uint_as_float(w[i] << 16);
-      f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
-  }
-  __device__ void set(const float* f) {
-    v = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
-                   pack_bf16(f[6], f[7]));
-  }
-};
-template <>
-struct Raw<__nv_bfloat16, 1> {
-  __nv_bfloat16 v;
-  __device__ void get(float* f) const { f[0] = __bfloat162float(v); }
-  __device__ void set(const float* f) { v = __float2bfloat16_rn(f[0]); }
-};
-
-// VEC values of gamma or beta (`other` where there is none).  Four in one load
-// when the array is 16-byte aligned: a warp's loads then cover whole lines of
-// the L1, which holds the array for every row but the first.
-template <int VEC>
-__device__ __forceinline__ void weights_at(const float* w, int j, float other, bool aligned,
-                                           float* f) {
-  if (!w) {
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) f[i] = other;
-  } else if (VEC >= 4 && aligned) {
-#pragma unroll
-    for (int i = 0; i + 3 < VEC; i += 4) {
-      const float4 v = __ldg(reinterpret_cast<const float4*>(w + j + i));
-      f[i] = v.x, f[i + 1] = v.y, f[i + 2] = v.z, f[i + 3] = v.w;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) f[i] = __ldg(w + j + i);
-  }
-}
 
 // VEC values at once, two an instruction where they come in pairs.
 template <int VEC>
@@ -209,6 +132,7 @@ struct NormFwdArgs {
   void* y;
   float2* stats;
   int gamma16, beta16;  // 16-byte aligned
+  DropArgs drop;        // of x, in front of the sum (the kernels with DROP)
 };
 
 struct NormBwdArgs {
@@ -225,14 +149,17 @@ struct NormBwdArgs {
   float* dgamma;  // written directly when the grid is one block (parts unused)
   float* dbeta;
   int accumulate;
-  int gamma16;  // 16-byte aligned
+  int gamma16;    // 16-byte aligned
+  DropArgs drop;  // of x: dx is dropped, dres (may be null) is not (the kernels with DROP)
+  void* dres;
 };
 
 constexpr int kRowWarps = 8;  // rows side by side in a block when a warp holds a row
 
 // A group of W warps holds ROWS rows of up to 32 W VEC CH values; groups stride
 // over the rows, loading the next ones while the current ones are worked on.
-template <typename T, int VEC, int CH, int W, bool RES, int ROWS>
+// With DROP x is dropped first, and a residual is there when p.res is.
+template <typename T, int VEC, int CH, int W, bool RES, int ROWS, bool DROP>
 __global__ void __launch_bounds__(W == 1 ? 32 * kRowWarps : 32 * W)
     norm_fwd_kernel(NormFwdArgs p) {
   using R = Raw<T, VEC>;
@@ -244,8 +171,10 @@ __global__ void __launch_bounds__(W == 1 ? 32 * kRowWarps : 32 * W)
   int64_t row = (int64_t)blockIdx.x * per_block + (W == 1 ? threadIdx.x >> 5 : 0);
   const int N = p.N;
   R rx[ROWS][CH], rr[ROWS][CH];
+  DropKey key;
   pdl_wait();
   pdl_trigger();
+  if (DROP) key.read(p.drop);
   auto fetch = [&](int k, int64_t r) {
     const T* x = static_cast<const T*>(p.x) + r * N;
     const T* s = static_cast<const T*>(p.res) + r * N;
@@ -254,7 +183,7 @@ __global__ void __launch_bounds__(W == 1 ? 32 * kRowWarps : 32 * W)
       const int j = (c * G + tid) * VEC;
       if (j < N) {
         rx[k][c] = *reinterpret_cast<const R*>(x + j);
-        if (RES) rr[k][c] = *reinterpret_cast<const R*>(s + j);
+        if (RES && (!DROP || p.res)) rr[k][c] = *reinterpret_cast<const R*>(s + j);
       }
     }
   };
@@ -282,7 +211,8 @@ __global__ void __launch_bounds__(W == 1 ? 32 * kRowWarps : 32 * W)
         if (j < N) {
           float* u = v[k] + c * VEC;
           rx[k][c].get(u);
-          if (RES) {
+          if (DROP) drop<VEC>(key, p.drop, (row + k * step) * N + j, u);
+          if (RES && (!DROP || p.res)) {
             float a[VEC];
             rr[k][c].get(a);
             add<VEC>(u, a, u);
@@ -347,15 +277,10 @@ __global__ void __launch_bounds__(W == 1 ? 32 * kRowWarps : 32 * W)
   }
 }
 
-// dgamma[j] or dbeta[j] from its sum
-__device__ __forceinline__ void put_sum(float* out, int j, float v, int accumulate) {
-  if (out) out[j] = accumulate ? out[j] + v : v;
-}
-
 // Groups of W warps side by side in a block of the backward.
 __host__ __device__ constexpr int bwd_groups(int W) { return W < kRowWarps ? kRowWarps / W : 1; }
 
-template <typename T, int VEC, int CH, int W>
+template <typename T, int VEC, int CH, int W, bool DROP>
 __global__ void __launch_bounds__(32 * W * bwd_groups(W), W <= 8 ? 2 : 1)
     norm_bwd_kernel(NormBwdArgs p) {
   using R = Raw<T, VEC>;
@@ -371,8 +296,10 @@ __global__ void __launch_bounds__(32 * W * bwd_groups(W), W <= 8 ? 2 : 1)
   float dg[E], db[E];
 #pragma unroll
   for (int i = 0; i < E; ++i) dg[i] = db[i] = 0.f;
+  DropKey key;
   pdl_wait();
   pdl_trigger();
+  if (DROP) key.read(p.drop);
   auto fetch = [&](int64_t r) {
     const T* s = static_cast<const T*>(p.s) + r * N;
     const T* d = static_cast<const T*>(p.dy) + r * N;
@@ -438,6 +365,13 @@ __global__ void __launch_bounds__(32 * W * bwd_groups(W), W <= 8 ? 2 : 1)
           mul<VEC>(f, by, f);
         }
         R o;
+        if (DROP) {
+          if (p.dres) {
+            o.set(f);
+            *reinterpret_cast<R*>(static_cast<T*>(p.dres) + row * N + j) = o;
+          }
+          drop<VEC>(key, p.drop, row * N + j, f);
+        }
         o.set(f);
         *reinterpret_cast<R*>(dx + j) = o;
       }
@@ -478,32 +412,6 @@ __global__ void __launch_bounds__(32 * W * bwd_groups(W), W <= 8 ? 2 : 1)
   }
 }
 
-// Sums of the partial rows in row order: 32 columns a block, 32 row slices
-// side by side, then the slices in order.
-__global__ void __launch_bounds__(1024)
-    norm_reduce_kernel(const float* parts, int nparts, int N, float* dgamma, float* dbeta,
-                       int accumulate) {
-  __shared__ float acc[32][33];
-  const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
-  const int col = blockIdx.x * 32 + lane;
-  pdl_wait();
-  pdl_trigger();
-  float v = 0.f;
-  if (col < 2 * N)
-    for (int r = slice; r < nparts; r += 32) v += parts[(size_t)r * 2 * N + col];
-  acc[slice][lane] = v;
-  __syncthreads();
-  if (slice == 0 && col < 2 * N) {
-    float t = 0.f;
-#pragma unroll
-    for (int k = 0; k < 32; ++k) t += acc[k][lane];
-    if (col < N)
-      put_sum(dgamma, col, t, accumulate);
-    else
-      put_sum(dbeta, col - N, t, accumulate);
-  }
-}
-
 // ---- rows wider than the registers of a block ----------------------------------
 constexpr int kWideThreads = 1024;
 
@@ -519,15 +427,19 @@ __device__ __forceinline__ void wide_put(void* p, int64_t i, float f) {
 }
 
 // One block a row, the row read three times (from L2 after the first).
-template <typename T>
+template <typename T, bool DROP>
 __global__ void __launch_bounds__(kWideThreads) norm_fwd_wide_kernel(NormFwdArgs p) {
   __shared__ float2 red[2][32];
+  DropKey key;
   pdl_wait();
   pdl_trigger();
+  if (DROP) key.read(p.drop);
   for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x) {
     const int64_t o = row * p.N;
     auto value = [&](int j) {
-      return wide_at<T>(p.x, o + j) + (p.res ? wide_at<T>(p.res, o + j) : 0.f);
+      float f = wide_at<T>(p.x, o + j);
+      if (DROP) drop<1>(key, p.drop, o + j, &f);
+      return f + (p.res ? wide_at<T>(p.res, o + j) : 0.f);
     };
     float part = 0.f;
     for (int j = threadIdx.x; j < p.N; j += kWideThreads) part += value(j);
@@ -567,11 +479,13 @@ __global__ void __launch_bounds__(256) norm_cols_wide_kernel(NormBwdArgs p) {
   p.parts[(size_t)blockIdx.y * 2 * p.N + p.N + j] = b;
 }
 
-template <typename T>
+template <typename T, bool DROP>
 __global__ void __launch_bounds__(kWideThreads) norm_dx_wide_kernel(NormBwdArgs p) {
   __shared__ float2 red[2][32];
+  DropKey key;
   pdl_wait();
   pdl_trigger();
+  if (DROP) key.read(p.drop);
   for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x) {
     const int64_t o = row * p.N;
     const float2 st = p.stats[row];
@@ -589,7 +503,12 @@ __global__ void __launch_bounds__(kWideThreads) norm_dx_wide_kernel(NormBwdArgs 
     const float b = group_sum<32>(sgh, red, 1) / p.n;
     for (int j = threadIdx.x; j < p.N; j += kWideThreads) {
       const float u = p.dsum ? wide_at<T>(p.dsum, o + j) : 0.f;
-      wide_put<T>(p.dx, o + j, st.y * (g(j) - a - h(j) * b) + u);
+      float f = st.y * (g(j) - a - h(j) * b) + u;
+      if (DROP) {
+        if (p.dres) wide_put<T>(p.dres, o + j, f);
+        drop<1>(key, p.drop, o + j, &f);
+      }
+      wide_put<T>(p.dx, o + j, f);
     }
   }
 }
@@ -628,12 +547,10 @@ int64_t bwd_blocks(int64_t N, int64_t T) {
   return b < most ? b : most;
 }
 
-bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
-
-template <typename T, int VEC, int CH, int W, bool RES, int ROWS>
+template <typename T, int VEC, int CH, int W, bool RES, int ROWS, bool DROP = false>
 cudaError_t fwd_launch(const NormFwdArgs& a, cudaStream_t st) {
   constexpr int rows = W == 1 ? kRowWarps : 1, threads = W == 1 ? 32 * kRowWarps : 32 * W;
-  auto kernel = norm_fwd_kernel<T, VEC, CH, W, RES, ROWS>;
+  auto kernel = norm_fwd_kernel<T, VEC, CH, W, RES, ROWS, DROP>;
   // as many blocks as stay on the SMs, each taking rows in turn
   static PerDevice once;
   static int fit[kMaxDevices] = {};
@@ -653,6 +570,7 @@ cudaError_t fwd_launch(const NormFwdArgs& a, cudaStream_t st) {
 }
 template <typename T, int VEC, int CH, int W>
 cudaError_t fwd_go(const NormFwdArgs& a, cudaStream_t st) {
+  if (a.drop.rng) return fwd_launch<T, VEC, CH, W, true, 1, true>(a, st);
   // Without a residual, and with rows enough for every block, two rows at a time:
   // the weights are read from L1 once for both (their 8 bytes a value, against 2
   // from memory, took 78 % of the L1's rate) and each barrier serves both.  bf16,
@@ -674,8 +592,9 @@ cudaError_t fwd_pick(const NormFwdArgs& a, cudaStream_t st) {
   const int N = a.N;
   if (N > kMaxRegRow) {
     const int64_t most = 2 * (int64_t)device_sms();
-    return launch_ex(norm_fwd_wide_kernel<T>, dim3((unsigned)(a.T < most ? a.T : most)),
-                     dim3(kWideThreads), 0, st, false, a);
+    return launch_ex(a.drop.rng ? norm_fwd_wide_kernel<T, true> : norm_fwd_wide_kernel<T, false>,
+                     dim3((unsigned)(a.T < most ? a.T : most)), dim3(kWideThreads), 0, st, false,
+                     a);
   }
   const int w = fwd_warps(N);
   const int e = (N + 32 * w - 1) / (32 * w);  // values a thread
@@ -692,8 +611,9 @@ cudaError_t fwd_pick(const NormFwdArgs& a, cudaStream_t st) {
 
 template <typename T, int VEC, int CH, int W>
 cudaError_t bwd_go(const NormBwdArgs& a, int64_t blocks, cudaStream_t st) {
-  return launch_ex(norm_bwd_kernel<T, VEC, CH, W>, dim3((unsigned)blocks),
-                   dim3(32 * W * bwd_groups(W)), 0, st, false, a);
+  return launch_ex(a.drop.rng ? norm_bwd_kernel<T, VEC, CH, W, true>
+                              : norm_bwd_kernel<T, VEC, CH, W, false>,
+                   dim3((unsigned)blocks), dim3(32 * W * bwd_groups(W)), 0, st, false, a);
 }
 
 template <typename T, int V>
@@ -721,8 +641,8 @@ cudaError_t bwd_wide(const NormBwdArgs& a, int64_t slices, cudaStream_t st) {
                             st, false, a);
   if (e != cudaSuccess) return e;
   const int64_t most = 2 * (int64_t)device_sms();
-  return launch_ex(norm_dx_wide_kernel<T>, dim3((unsigned)(a.T < most ? a.T : most)),
-                   dim3(kWideThreads), 0, st, false, a);
+  return launch_ex(a.drop.rng ? norm_dx_wide_kernel<T, true> : norm_dx_wide_kernel<T, false>,
+                   dim3((unsigned)(a.T < most ? a.T : most)), dim3(kWideThreads), 0, st, false, a);
 }
 
 }  // namespace
@@ -757,9 +677,11 @@ tt_status tt_norm_plan(const tt_norm_desc* desc, tt_plan_t** out) {
   return TT_OK;
 }
 
-tt_status tt_norm_forward(const tt_plan_t* plan, int64_t T, const void* x, const void* res,
-                          const float* gamma, const float* beta, void* sum, void* y,
-                          float* stats, void* stream) {
+// Both forms of each pass: `drop` is null without dropout.
+static tt_status norm_forward(const tt_plan_t* plan, const tt_plan_t* drop, int64_t T,
+                              const int64_t* rng, const void* x, const void* res,
+                              const float* gamma, const float* beta, void* sum, void* y,
+                              float* stats, void* stream) {
   if (!plan || plan->kind != 4 || T < 0) return TT_ERR_INVALID_ARG;
   if (T == 0) return TT_OK;
   if (!x || !y || !aligned_to(x, 16) || !aligned_to(y, 16) || !aligned_to(res, 16) ||
@@ -768,6 +690,8 @@ tt_status tt_norm_forward(const tt_plan_t* plan, int64_t T, const void* x, const
     return TT_ERR_INVALID_ARG;
   const NormPlan& P = plan->norm;
   NormFwdArgs a;
+  a.drop.rng = nullptr;
+  if (drop && !drop_args(drop->drop, rng, &a.drop)) return TT_ERR_INVALID_ARG;
   a.T = T;
   a.N = (int)P.N;
   a.eps = P.eps;
@@ -790,19 +714,20 @@ tt_status tt_norm_forward(const tt_plan_t* plan, int64_t T, const void* x, const
   prof_begin(kPhElem, st);
   const cudaError_t e =
       P.act == TT_DT_BF16
-          ? (res && P.N % 8 == 0 ? fwd_pick<__nv_bfloat16, 8>(a, st)
-             : P.N % 4 == 0      ? fwd_pick<__nv_bfloat16, 4>(a, st)
-                                 : fwd_pick<__nv_bfloat16, 1>(a, st))
+          ? ((res || drop) && P.N % 8 == 0 ? fwd_pick<__nv_bfloat16, 8>(a, st)
+             : P.N % 4 == 0                ? fwd_pick<__nv_bfloat16, 4>(a, st)
+                                           : fwd_pick<__nv_bfloat16, 1>(a, st))
           : (P.N % 4 == 0 ? fwd_pick<float, 4>(a, st) : fwd_pick<float, 1>(a, st));
   prof_end(kPhElem, st);
   count_launches(1);
   return e == cudaSuccess ? TT_OK : TT_ERR_CUDA;
 }
 
-tt_status tt_norm_backward(const tt_plan_t* plan, int64_t T, const void* s, const void* dy,
-                           const void* dsum, const float* gamma, const float* stats, void* dx,
-                           float* dgamma, float* dbeta, void* ws, size_t ws_bytes,
-                           void* stream) {
+static tt_status norm_backward(const tt_plan_t* plan, const tt_plan_t* drop, int64_t T,
+                               const int64_t* rng, const void* s, const void* dy,
+                               const void* dsum, const float* gamma, const float* stats, void* dx,
+                               void* dres, float* dgamma, float* dbeta, void* ws,
+                               size_t ws_bytes, void* stream) {
   if (!plan || plan->kind != 4 || T < 0) return TT_ERR_INVALID_ARG;
   const NormPlan& P = plan->norm;
   const int acc = (P.flags & TT_ACCUMULATE) != 0;
@@ -816,7 +741,8 @@ tt_status tt_norm_backward(const tt_plan_t* plan, int64_t T, const void* s, cons
     return TT_OK;
   }
   if (!s || !dy || !stats || !dx || !aligned_to(s, 16) || !aligned_to(dy, 16) ||
-      !aligned_to(dsum, 16) || !aligned_to(dx, 16) || !aligned_to(gamma, 4) ||
+      !aligned_to(dsum, 16) || !aligned_to(dx, 16) || !aligned_to(dres, 16) ||
+      !aligned_to(gamma, 4) ||
       !aligned_to(stats, 8))
     return TT_ERR_INVALID_ARG;
   if (!ws || !aligned_to(ws, 256) || ws_bytes < norm_workspace_bytes(P, T))
@@ -824,6 +750,9 @@ tt_status tt_norm_backward(const tt_plan_t* plan, int64_t T, const void* s, cons
   const int64_t blocks = bwd_blocks(P.N, T);
   const bool wide = P.N > kMaxRegRow;
   NormBwdArgs a;
+  a.drop.rng = nullptr;
+  a.dres = dres;
+  if (drop && !drop_args(drop->drop, rng, &a.drop)) return TT_ERR_INVALID_ARG;
   a.T = T;
   a.N = (int)P.N;
   a.n = (float)P.N;
@@ -850,12 +779,49 @@ tt_status tt_norm_backward(const tt_plan_t* plan, int64_t T, const void* s, cons
                        : bwd_pick<float, 1>(a, blocks, st);
   count_launches(wide ? 2 : 1);
   if (e == cudaSuccess && (wide || blocks > 1) && (dgamma || dbeta)) {
-    e = launch_ex(norm_reduce_kernel, dim3((unsigned)((2 * P.N + 31) / 32)), dim3(1024), 0, st,
+    e = launch_ex(sum_parts_kernel, dim3((unsigned)((2 * P.N + 31) / 32)), dim3(1024), 0, st,
                   false, (const float*)a.parts, (int)blocks, a.N, dgamma, dbeta, acc);
     count_launches(1);
   }
   prof_end(kPhElem, st);
   return e == cudaSuccess ? TT_OK : TT_ERR_CUDA;
+}
+
+tt_status tt_norm_forward(const tt_plan_t* plan, int64_t T, const void* x, const void* res,
+                          const float* gamma, const float* beta, void* sum, void* y,
+                          float* stats, void* stream) {
+  return norm_forward(plan, nullptr, T, nullptr, x, res, gamma, beta, sum, y, stats, stream);
+}
+
+tt_status tt_norm_backward(const tt_plan_t* plan, int64_t T, const void* s, const void* dy,
+                           const void* dsum, const float* gamma, const float* stats, void* dx,
+                           float* dgamma, float* dbeta, void* ws, size_t ws_bytes,
+                           void* stream) {
+  return norm_backward(plan, nullptr, T, nullptr, s, dy, dsum, gamma, stats, dx, nullptr, dgamma,
+                       dbeta, ws, ws_bytes, stream);
+}
+
+// A dropout plan of the normalisation's activation type.
+static bool drops(const tt_plan_t* plan, const tt_plan_t* drop) {
+  return plan && plan->kind == 4 && drop && drop->kind == 7 && drop->drop.act == plan->norm.act;
+}
+
+tt_status tt_norm_dropout_forward(const tt_plan_t* plan, const tt_plan_t* dropout, int64_t T,
+                                  const int64_t* rng, const void* x, const void* res,
+                                  const float* gamma, const float* beta, void* sum, void* y,
+                                  float* stats, void* stream) {
+  if (!drops(plan, dropout)) return TT_ERR_INVALID_ARG;
+  return norm_forward(plan, dropout, T, rng, x, res, gamma, beta, sum, y, stats, stream);
+}
+
+tt_status tt_norm_dropout_backward(const tt_plan_t* plan, const tt_plan_t* dropout, int64_t T,
+                                   const int64_t* rng, const void* s, const void* dy,
+                                   const void* dsum, const float* gamma, const float* stats,
+                                   void* dx, void* dres, float* dgamma, float* dbeta, void* ws,
+                                   size_t ws_bytes, void* stream) {
+  if (!drops(plan, dropout) || (dres && dres == dx)) return TT_ERR_INVALID_ARG;
+  return norm_backward(plan, dropout, T, rng, s, dy, dsum, gamma, stats, dx, dres, dgamma, dbeta,
+                       ws, ws_bytes, stream);
 }
 
 }  // extern "C"

@@ -971,6 +971,10 @@ tt_status tt_workspace_size(const tt_plan_t* plan, int64_t T, size_t* bytes) {
     *bytes = norm_workspace_bytes(plan->norm, T);
   } else if (plan->kind == 5) {
     return TT_ERR_INVALID_ARG;  // tt_attn_workspace_size
+  } else if (plan->kind == 6) {
+    *bytes = rope_workspace_bytes(plan->rope, T);
+  } else if (plan->kind == 7 || plan->kind == 8) {
+    *bytes = 0;
   } else {
     FfnLayout f;
     *bytes = ffn_layout(plan, T, &f);
@@ -1372,12 +1376,14 @@ tt_status tt_multi_backward(const tt_plan_t* plan, int64_t T, const void* x,
 tt_status tt_get_device_status(void* stream) {
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (cudaStreamSynchronize(st) != cudaSuccess) return TT_ERR_CUDA;
-  DeviceStatus h{0, 0}, e{0, 0}, a{0, 0};
+  DeviceStatus h{0, 0}, e{0, 0}, a{0, 0}, r{0, 0}, l{0, 0};
   if (read_and_clear_device_status(&h) != cudaSuccess) return TT_ERR_CUDA;
   if (read_and_clear_ttm_status(&e) != cudaSuccess) return TT_ERR_CUDA;
   if (read_and_clear_attn_status(&a) != cudaSuccess) return TT_ERR_CUDA;
+  if (read_and_clear_rope_status(&r) != cudaSuccess) return TT_ERR_CUDA;
+  if (read_and_clear_logp_status(&l) != cudaSuccess) return TT_ERR_CUDA;
   if (h.code == TT_ERR_TIMEOUT || a.code == TT_ERR_TIMEOUT) return TT_ERR_TIMEOUT;
-  if (h.code != 0 || e.code != 0 || a.code != 0) return TT_ERR_DEVICE;
+  if (h.code != 0 || e.code != 0 || a.code != 0 || r.code != 0 || l.code != 0) return TT_ERR_DEVICE;
   return TT_OK;
 }
 

@@ -55,6 +55,30 @@ struct NormPlan {
 };
 size_t norm_workspace_bytes(const NormPlan& P, int64_t T);
 
+// Dropout (dropout.cu, norm.cu).
+struct DropPlan {
+  uint32_t cut = 0;  // 0 .. 65536, of 16 random bits
+  uint32_t site = 0;
+  int act = TT_DT_F32;
+};
+// Log probabilities (logp.cu).
+struct LogpPlan {
+  int64_t V = 0;
+  float scale = 1.f;
+  int top = 0;
+  int act = TT_DT_F32;
+};
+// Norm of heads and rotation by position (rope.cu).
+struct RopePlan {
+  int heads = 0, kv = 0, dim = 0, rot = 0;
+  bool inter = false;
+  float eps = 0.f;  // 0: no norm
+  int act = TT_DT_F32;
+  unsigned flags = 0;
+  uint64_t turn[128] = {};  // frequencies as 64-bit fractions of a turn
+};
+size_t rope_workspace_bytes(const RopePlan& R, int64_t T);
+
 // Windowed attention (attn.cu).
 struct AttnPlan {
   int heads = 0, kv = 0, dim = 0;
@@ -66,13 +90,17 @@ struct AttnPlan {
 
 struct tt_plan_s {
   // 0 = single layer, 1 = FFN pair, 2 = TT-matrix embedding, 3 = layers on one x,
-  // 4 = layer normalisation, 5 = attention
+  // 4 = layer normalisation, 5 = attention, 6 = rotation by position,
+  // 7 = dropout, 8 = log probabilities
   int kind = 0;
   int G = 1;     // layers of a kind-3 plan
   ttc::LayerPlan L[3];
   ttc::TtmPlan ttm;
   ttc::NormPlan norm;
   ttc::AttnPlan attn;
+  ttc::RopePlan rope;
+  ttc::DropPlan drop;
+  ttc::LogpPlan logits;
 };
 
 namespace ttc {
@@ -116,6 +144,9 @@ struct DeviceStatus {
 cudaError_t read_and_clear_device_status(DeviceStatus* out);
 // The same for the embedding kernels' own word (ttm.cu).
 cudaError_t read_and_clear_ttm_status(DeviceStatus* out);
+// The same for the rotation's rows of a cache (rope.cu), and for targets (logp.cu).
+cudaError_t read_and_clear_rope_status(DeviceStatus* out);
+cudaError_t read_and_clear_logp_status(DeviceStatus* out);
 // The same for the attention kernels' own word, their wait limit and test hook (attn.cu).
 cudaError_t read_and_clear_attn_status(DeviceStatus* out);
 cudaError_t attn_set_wait_limit(unsigned long long ns);

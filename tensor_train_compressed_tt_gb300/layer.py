@@ -309,6 +309,22 @@ def _dense(t: Optional[torch.Tensor], shape, dtype: torch.dtype, name: str) -> i
     return t.data_ptr()
 
 
+def _heads_of(t: torch.Tensor, rows: int, heads: int, dim: int, dtype: torch.dtype,
+              name: str) -> ttc.tt_heads:
+    """(rows, heads, dim) of any row and head stride, or (rows, heads * dim)."""
+    shape, st = t.shape, t.stride()
+    if t.dtype == dtype and t.is_cuda and shape[0] == rows:
+        if len(shape) == 3 and shape[1] == heads and shape[2] == dim and \
+                (st[2] == 1 or dim == 1):
+            return ttc.tt_heads(t.data_ptr(), st[0], st[1])
+        if len(shape) == 2 and shape[1] == heads * dim and \
+                (st[1] == 1 or shape[1] == 1):
+            return ttc.tt_heads(t.data_ptr(), st[0], dim)
+    raise ValueError(f"{name}: expected a CUDA tensor of ({rows}, {heads}, {dim}) "
+                     f"{dtype} with its last axis dense, got {tuple(shape)} {t.dtype} "
+                     f"on {t.device}, strides {tuple(st)}")
+
+
 class TTNorm:
     """Layer normalisation of (T, N) rows with an optional residual sum in
     front of it: s = x + res, y = (s - mean(s)) / sqrt(var(s) + eps) gamma + beta."""
@@ -418,17 +434,7 @@ class TTAttention:
 
     def _heads(self, t: torch.Tensor, rows: int, heads: int, name: str) -> ttc.tt_heads:
         """(rows, heads, dim) of any row and head stride, or (rows, heads * dim)."""
-        shape, st = t.shape, t.stride()
-        if t.dtype == self.dtype and t.is_cuda and shape[0] == rows:
-            if len(shape) == 3 and shape[1] == heads and shape[2] == self.dim and \
-                    (st[2] == 1 or self.dim == 1):
-                return ttc.tt_heads(t.data_ptr(), st[0], st[1])
-            if len(shape) == 2 and shape[1] == heads * self.dim and \
-                    (st[1] == 1 or shape[1] == 1):
-                return ttc.tt_heads(t.data_ptr(), st[0], self.dim)
-        raise ValueError(f"{name}: expected a CUDA tensor of ({rows}, {heads}, {self.dim}) "
-                         f"{self.dtype} with its last axis dense, got {tuple(shape)} {t.dtype} "
-                         f"on {t.device}, strides {tuple(st)}")
+        return _heads_of(t, rows, heads, self.dim, self.dtype, name)
 
     def forward(self, q, k, v, seqs: TTSeqs, o=None, lse=None, ws=None, stream=None):
         """(o, lse); o like q but dense, lse (heads, Tq) fp32.  Rows of no sequence stay
@@ -470,3 +476,324 @@ class TTAttention:
             self._heads(dk, seqs.Tk, G, "dk"), self._heads(dv, seqs.Tk, G, "dv"), _ptr(ws),
             ws.numel(), _stream(stream)), "tt_attn_backward")
         return dq, dk, dv
+
+
+def _same_device(*tensors: Optional[torch.Tensor]) -> None:
+    """The kernels run on the current device: tensors of another one are refused."""
+    here = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.is_cuda and t.device.index != here:
+            raise ValueError(f"a tensor on {t.device}, while cuda:{here} is current")
+
+
+class TTRotary:
+    """Between the Q, K projections and the attention: the norm of each head of q and
+    k (root mean square, with one weight of dim values for all query heads and one for
+    all key heads) and its rotation by position, in one pass.  rot: the channels that
+    are rotated (all by default, 0: the norm alone), in pairs half a rotation apart or,
+    interleaved, of neighbours.  freqs: rot / 2 radians a position, in place of those of
+    base.  norm=False: the rotation alone."""
+
+    def __init__(self, heads: int, dim: int, kv_heads: Optional[int] = None,
+                 dtype: torch.dtype = torch.bfloat16, rot: Optional[int] = None,
+                 base: float = 10000.0, freqs: Optional[Sequence[float]] = None,
+                 interleaved: bool = False, norm: bool = True, eps: float = 1e-5,
+                 accumulate: bool = False):
+        self.heads, self.dim = int(heads), int(dim)
+        self.kv_heads = self.heads if kv_heads is None else int(kv_heads)
+        self.dtype = dtype
+        self.norm = bool(norm)
+        if norm and not eps > 0:
+            raise ValueError(f"eps: expected more than 0, got {eps}")
+        self.fill = _grad_fill(accumulate)
+        self.plan = ttc.tt_rope_plan(heads, self.kv_heads, dim, dim if rot is None else rot, base,
+                                     freqs, interleaved, eps if norm else 0.0, _DT[dtype],
+                                     ttc.TT_ACCUMULATE if accumulate else 0)
+
+    def workspace(self, T: int, device="cuda") -> torch.Tensor:
+        """For a backward of T tokens."""
+        return torch.empty(ttc.tt_workspace_size(self.plan, T), dtype=torch.uint8, device=device)
+
+    def _of(self, t, rows, heads, name):
+        return _heads_of(t, rows, heads, self.dim, self.dtype, name)
+
+    def _weights(self, gq, gk):
+        if not self.norm and (gq is not None or gk is not None):
+            raise ValueError("gq, gk: weights of a norm that this plan does not have")
+        sh = (self.dim,)
+        return _dense(gq, sh, torch.float32, "gq"), _dense(gk, sh, torch.float32, "gk")
+
+    def forward(self, q, k, pos=None, gq=None, gk=None, q_out=None, k_out=None, stream=None):
+        """(q_out, k_out) for tokens at positions pos (int32; None: 0, 1, ..)."""
+        T = q.shape[0]
+        _same_device(q, k, pos, gq, gk, q_out, k_out)
+        wq, wk = self._weights(gq, gk)
+        at = _dense(pos, (T,), torch.int32, "pos")
+        hq, hk = self._of(q, T, self.heads, "q"), self._of(k, T, self.kv_heads, "k")
+        if q_out is None:
+            q_out = _new(q.shape, self.dtype, q.device, stream)
+        if k_out is None:
+            k_out = _new(k.shape, self.dtype, k.device, stream)
+        ttc.check(ttc.tt_rope_forward(
+            self.plan, T, at, hq, hk, wq, wk, self._of(q_out, T, self.heads, "q_out"),
+            self._of(k_out, T, self.kv_heads, "k_out"), None, None, 0, 0, _stream(stream)),
+            "tt_rope_forward")
+        return q_out, k_out
+
+    def to_cache(self, q, k, v, pos, rows, keys, values, gq=None, gk=None, q_out=None,
+                 stream=None):
+        """(q_out, keys, values): forward for new tokens whose keys, and values as they
+        are, go to `rows` (int32, each its own; a negative one: nowhere) of the caches
+        keys and values (rows, kv_heads, dim).  A row that the cache does not have is
+        skipped and recorded in the device status word."""
+        T, n, G = q.shape[0], keys.shape[0], self.kv_heads
+        _same_device(q, k, v, pos, rows, keys, values, gq, gk, q_out)
+        wq, wk = self._weights(gq, gk)
+        if rows is None:
+            raise ValueError("rows: expected an int32 tensor")
+        at, to = _dense(pos, (T,), torch.int32, "pos"), _dense(rows, (T,), torch.int32, "rows")
+        hq, hk = self._of(q, T, self.heads, "q"), self._of(k, T, G, "k")
+        if q_out is None:
+            q_out = _new(q.shape, self.dtype, q.device, stream)
+        ttc.check(ttc.tt_rope_forward(
+            self.plan, T, at, hq, hk, wq, wk, self._of(q_out, T, self.heads, "q_out"),
+            self._of(keys, n, G, "keys"), self._of(v, T, G, "v"),
+            self._of(values, n, G, "values"), to, n, _stream(stream)), "tt_rope_forward")
+        return q_out, keys, values
+
+    def backward(self, dq, dk, pos=None, q=None, k=None, gq=None, gk=None, dq_in=None, dk_in=None,
+                 dgq=None, dgk=None, ws=None, stream=None):
+        """(dq_in, dk_in, dgq, dgk): the gradients of forward's q, k (which the norm's
+        needs) and of the weights, for those of its outputs; without a norm dgq and dgk
+        are None.  dq_in may be dq, dk_in dk."""
+        T = dq.shape[0]
+        _same_device(dq, dk, pos, q, k, gq, gk, dq_in, dk_in, dgq, dgk, ws)
+        H, G, sh = self.heads, self.kv_heads, (self.dim,)
+        wq, wk = self._weights(gq, gk)
+        at = _dense(pos, (T,), torch.int32, "pos")
+        if self.norm and (q is None or k is None):
+            raise ValueError("q, k: the norm's gradient needs them")
+        if not self.norm and (dgq is not None or dgk is not None):
+            raise ValueError("dgq, dgk: gradients of a norm that this plan does not have")
+        hq = self._of(q, T, H, "q") if self.norm else None
+        hk = self._of(k, T, G, "k") if self.norm else None
+        if dq_in is None:
+            dq_in = _new(dq.shape, self.dtype, dq.device, stream)
+        if dk_in is None:
+            dk_in = _new(dk.shape, self.dtype, dk.device, stream)
+        if self.norm:
+            if dgq is None:
+                dgq = _new(sh, torch.float32, dq.device, stream, self.fill)
+            if dgk is None:
+                dgk = _new(sh, torch.float32, dq.device, stream, self.fill)
+        if ws is None:
+            ws = _scratch(stream, self.workspace, T, dq.device)
+        ttc.check(ttc.tt_rope_backward(
+            self.plan, T, at, hq, hk, wq, wk, self._of(dq, T, H, "dq"), self._of(dk, T, G, "dk"),
+            self._of(dq_in, T, H, "dq_in"), self._of(dk_in, T, G, "dk_in"),
+            _dense(dgq, sh, torch.float32, "dgq"), _dense(dgk, sh, torch.float32, "dgk"),
+            _ptr(ws), ws.numel(), _stream(stream)), "tt_rope_backward")
+        return dq_in, dk_in, dgq, dgk
+
+
+def _state(rng: torch.Tensor) -> int:
+    if rng is None:
+        raise ValueError("rng: expected an int64 CUDA tensor of (seed, offset)")
+    return _dense(rng, (2,), torch.int64, "rng")
+
+
+class TTDropout:
+    """Dropout by a counter-based generator: an element stays with probability 1 - p
+    (in steps of 2^-16) and is scaled by the inverse.  rng is a device tensor of two int64, a
+    seed and an offset: a program adds to the offset once a step (`rng[1] += 1`, in a
+    captured graph too) and gives each place of its model its own site.  The mask is a
+    function of these and of an element's index; it is not stored."""
+
+    def __init__(self, p: float, dtype: torch.dtype = torch.bfloat16, site: int = 0):
+        self.p, self.site, self.dtype = float(p), int(site), dtype
+        self.plan = ttc.tt_dropout_plan(p, site, _DT[dtype])
+
+    @staticmethod
+    def state(seed: int, offset: int = 0, device="cuda") -> torch.Tensor:
+        return torch.tensor([seed, offset], dtype=torch.int64, device=device)
+
+    def forward(self, x, rng, res=None, y=None, stream=None):
+        """y = dropout(x) + res; y may be x or res."""
+        _same_device(x, rng, res, y)
+        if y is None:
+            y = _new(x.shape, self.dtype, x.device, stream)
+        sh = x.shape
+        ttc.check(ttc.tt_dropout(self.plan, x.numel(), _state(rng), _dense(x, sh, self.dtype, "x"),
+                                 _dense(res, sh, self.dtype, "res"),
+                                 _dense(y, sh, self.dtype, "y"), _stream(stream)), "tt_dropout")
+        return y
+
+    def backward(self, dy, rng, dx=None, stream=None):
+        """The gradient of x (that of res is dy itself); dx may be dy."""
+        return self.forward(dy, rng, None, dx, stream)
+
+
+class TTDropNorm:
+    """TTNorm with dropout of x in front of the residual sum, in the same pass:
+    s = dropout(x) + res, y = norm(s).  rng as in TTDropout."""
+
+    def __init__(self, N: int, p: float, dtype: torch.dtype = torch.bfloat16, eps: float = 1e-5,
+                 site: int = 0, accumulate: bool = False):
+        self.norm = TTNorm(N, dtype, eps, accumulate)
+        self.drop = TTDropout(p, dtype, site)
+        self.N, self.dtype = self.norm.N, dtype
+
+    def workspace(self, T: int, device="cuda") -> torch.Tensor:
+        return self.norm.workspace(T, device)
+
+    def forward(self, x, rng, gamma=None, beta=None, res=None, y=None, sum=None, stats=None,
+                stream=None):
+        """(y, s, stats)."""
+        T, N = x.shape[0], self.N
+        _same_device(x, rng, gamma, beta, res, y, sum, stats)
+        if y is None:
+            y = _new((T, N), self.dtype, x.device, stream)
+        if sum is None:
+            sum = _new((T, N), self.dtype, x.device, stream)
+        if stats is None:
+            stats = _new((T, 2), torch.float32, x.device, stream)
+        f32, sh = torch.float32, (T, N)
+        ttc.check(ttc.tt_norm_dropout_forward(
+            self.norm.plan, self.drop.plan, T, _state(rng), _dense(x, sh, self.dtype, "x"),
+            _dense(res, sh, self.dtype, "res"), _dense(gamma, (N,), f32, "gamma"),
+            _dense(beta, (N,), f32, "beta"), _dense(sum, sh, self.dtype, "sum"),
+            _dense(y, sh, self.dtype, "y"), _dense(stats, (T, 2), f32, "stats"),
+            _stream(stream)), "tt_norm_dropout_forward")
+        return y, sum, stats
+
+    def backward(self, s, dy, rng, gamma, stats, dsum=None, dx=None, dres=None, residual=True,
+                 dgamma=None, dbeta=None, ws=None, stream=None):
+        """(dx, dres, dgamma, dbeta): the gradients of x and of res (that of s).
+        residual=False: dres is None, where forward had no res."""
+        T, N = s.shape[0], self.N
+        _same_device(s, dy, rng, gamma, stats, dsum, dx, dres, dgamma, dbeta, ws)
+        if dx is None:
+            dx = _new((T, N), self.dtype, s.device, stream)
+        if dres is None and residual:
+            dres = _new((T, N), self.dtype, s.device, stream)
+        if dgamma is None:
+            dgamma = _new((N,), torch.float32, s.device, stream, self.norm.fill)
+        if dbeta is None:
+            dbeta = _new((N,), torch.float32, s.device, stream, self.norm.fill)
+        if ws is None:
+            ws = _scratch(stream, self.workspace, T, s.device)
+        f32, sh = torch.float32, (T, N)
+        ttc.check(ttc.tt_norm_dropout_backward(
+            self.norm.plan, self.drop.plan, T, _state(rng), _dense(s, sh, self.dtype, "s"),
+            _dense(dy, sh, self.dtype, "dy"), _dense(dsum, sh, self.dtype, "dsum"),
+            _dense(gamma, (N,), f32, "gamma"), _dense(stats, (T, 2), f32, "stats"),
+            _dense(dx, sh, self.dtype, "dx"), _dense(dres, sh, self.dtype, "dres"),
+            _dense(dgamma, (N,), f32, "dgamma"), _dense(dbeta, (N,), f32, "dbeta"), _ptr(ws),
+            ws.numel(), _stream(stream)), "tt_norm_dropout_backward")
+        return dx, dres, dgamma, dbeta
+
+
+class TTLogProbs:
+    """What follows the output layer: for rows of V logits (of any row stride), z = scale
+    logits, the log-sum, the log probability of each row's target, the entropy and the
+    `top` most likely tokens; the gradient of any sum of log probabilities and
+    entropies.  targets are int32; a negative one stands for none (logp 0)."""
+
+    def __init__(self, V: int, dtype: torch.dtype = torch.bfloat16, scale: float = 1.0,
+                 top: int = 0):
+        self.V, self.top, self.dtype = int(V), int(top), dtype
+        self.plan = ttc.tt_logp_plan(V, scale, top, _DT[dtype])
+
+    def _rows(self, t: torch.Tensor, rows: int, name: str):
+        """Pointer and row stride of (rows, V) with its last axis dense."""
+        st = t.stride()
+        if t.dtype != self.dtype or t.shape != (rows, self.V) or not t.is_cuda or \
+                (self.V > 1 and st[1] != 1):
+            raise ValueError(f"{name}: expected a CUDA tensor of ({rows}, {self.V}) {self.dtype} "
+                             f"with its last axis dense, got {tuple(t.shape)} {t.dtype} on "
+                             f"{t.device}, strides {tuple(st)}")
+        return t.data_ptr(), st[0] if rows > 1 else max(st[0], self.V)
+
+    def forward(self, logits, targets=None, logp=None, lse=None, entropy=None, top=None,
+                top_logp=None, stream=None):
+        """(logp, lse, entropy, top, top_logp).  logp is made where there are targets, top
+        (int32) and top_logp where the plan has them; the entropy is computed where a
+        tensor for it is given, else it is None."""
+        T, f32 = logits.shape[0], torch.float32
+        _same_device(logits, targets, logp, lse, entropy, top, top_logp)
+        if logp is not None and targets is None:
+            raise ValueError("logp: needs targets")
+        if logp is None and targets is not None:
+            logp = _new((T,), f32, logits.device, stream)
+        if lse is None:
+            lse = _new((T,), f32, logits.device, stream)
+        if self.top:
+            if top is None:
+                top = _new((T, self.top), torch.int32, logits.device, stream)
+            if top_logp is None:
+                top_logp = _new((T, self.top), f32, logits.device, stream)
+        elif top is not None or top_logp is not None:
+            raise ValueError("top: this plan has none")
+        at, stride = self._rows(logits, T, "logits")
+        ttc.check(ttc.tt_logp_forward(
+            self.plan, T, at, stride, _dense(targets, (T,), torch.int32, "targets"),
+            _dense(logp, (T,), f32, "logp"), _dense(lse, (T,), f32, "lse"),
+            _dense(entropy, (T,), f32, "entropy"),
+            _dense(top, (T, self.top), torch.int32, "top"),
+            _dense(top_logp, (T, self.top), f32, "top_logp"), _stream(stream)),
+            "tt_logp_forward")
+        return logp, lse, entropy, top, top_logp
+
+    def _gradients(self, T, targets, dlogp, dentropy):
+        f32 = torch.float32
+        if dlogp is None and dentropy is None:
+            raise ValueError("dlogp, dentropy: expected one of them")
+        if dlogp is not None and targets is None:
+            raise ValueError("dlogp: needs targets")
+        return (_dense(targets, (T,), torch.int32, "targets"), _dense(dlogp, (T,), f32, "dlogp"),
+                _dense(dentropy, (T,), f32, "dentropy"))
+
+    def backward(self, logits, targets, lse, dlogp=None, entropy=None, dentropy=None,
+                 dlogits=None, stream=None):
+        """dlogits for the gradients of logp and of the entropy (which then has to be
+        given), from forward's lse.  dlogits may be logits."""
+        T, f32 = logits.shape[0], torch.float32
+        _same_device(logits, targets, lse, dlogp, entropy, dentropy, dlogits)
+        t, g, h = self._gradients(T, targets, dlogp, dentropy)
+        if dentropy is not None and entropy is None:
+            raise ValueError("entropy: dentropy needs it")
+        if lse is None:
+            raise ValueError("lse: expected forward's")
+        if dlogits is None:
+            dlogits = _new((T, self.V), self.dtype, logits.device, stream)
+        at, stride = self._rows(logits, T, "logits")
+        to, dstride = self._rows(dlogits, T, "dlogits")
+        ttc.check(ttc.tt_logp_backward(
+            self.plan, T, at, stride, t, _dense(lse, (T,), f32, "lse"), g,
+            _dense(entropy, (T,), f32, "entropy"), h, to, dstride, _stream(stream)),
+            "tt_logp_backward")
+        return dlogits
+
+    def loss(self, logits, targets, dlogp=None, dentropy=None, logp=None, lse=None, entropy=None,
+             dlogits=None, stream=None):
+        """(logp, lse, entropy, dlogits): forward and backward in one pass over the
+        logits, where the gradients are known beforehand (-1 / T for a mean loss).
+        dlogits may be logits."""
+        T, f32 = logits.shape[0], torch.float32
+        _same_device(logits, targets, dlogp, dentropy, logp, lse, entropy, dlogits)
+        t, g, h = self._gradients(T, targets, dlogp, dentropy)
+        if logp is not None and targets is None:
+            raise ValueError("logp: needs targets")
+        if logp is None and targets is not None:
+            logp = _new((T,), f32, logits.device, stream)
+        if lse is None:
+            lse = _new((T,), f32, logits.device, stream)
+        if dlogits is None:
+            dlogits = _new((T, self.V), self.dtype, logits.device, stream)
+        at, stride = self._rows(logits, T, "logits")
+        to, dstride = self._rows(dlogits, T, "dlogits")
+        ttc.check(ttc.tt_logp_loss(
+            self.plan, T, at, stride, t, g, h, _dense(logp, (T,), f32, "logp"),
+            _dense(lse, (T,), f32, "lse"), _dense(entropy, (T,), f32, "entropy"), to, dstride,
+            _stream(stream)), "tt_logp_loss")
+        return logp, lse, entropy, dlogits

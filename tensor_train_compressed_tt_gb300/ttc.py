@@ -12,7 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import List, Sequence, Tuple
+from typing import List, Optional, Sequence, Tuple
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libttc.so")
@@ -118,6 +118,38 @@ class tt_heads(ctypes.Structure):
     ]
 
 
+class tt_rope_desc(ctypes.Structure):
+    _fields_ = [
+        ("heads", ctypes.c_int),
+        ("kv_heads", ctypes.c_int),
+        ("dim", ctypes.c_int),
+        ("rot", ctypes.c_int),
+        ("base", ctypes.c_double),
+        ("freqs", ctypes.c_void_p),
+        ("interleaved", ctypes.c_int),
+        ("eps", ctypes.c_float),
+        ("act", ctypes.c_int),
+        ("flags", ctypes.c_uint),
+    ]
+
+
+class tt_dropout_desc(ctypes.Structure):
+    _fields_ = [
+        ("p", ctypes.c_float),
+        ("site", ctypes.c_int),
+        ("act", ctypes.c_int),
+    ]
+
+
+class tt_logp_desc(ctypes.Structure):
+    _fields_ = [
+        ("V", ctypes.c_int64),
+        ("scale", ctypes.c_float),
+        ("top", ctypes.c_int),
+        ("act", ctypes.c_int),
+    ]
+
+
 _lib = None
 _P = ctypes.c_void_p
 _SZ = ctypes.c_size_t
@@ -159,6 +191,18 @@ def lib() -> ctypes.CDLL:
             "tt_norm_plan": [_P, _P],
             "tt_norm_forward": [_P, _I64, _P, _P, _P, _P, _P, _P, _P, _P],
             "tt_norm_backward": [_P, _I64, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P],
+            "tt_norm_dropout_forward": [_P, _P, _I64, _P, _P, _P, _P, _P, _P, _P, _P, _P],
+            "tt_norm_dropout_backward": [_P, _P, _I64, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P,
+                                         _SZ, _P],
+            "tt_dropout_plan": [_P, _P],
+            "tt_dropout": [_P, _I64, _P, _P, _P, _P, _P],
+            "tt_rope_plan": [_P, _P],
+            "tt_rope_forward": [_P, _I64, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _P],
+            "tt_rope_backward": [_P, _I64, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P],
+            "tt_logp_plan": [_P, _P],
+            "tt_logp_forward": [_P, _I64, _P, _I64, _P, _P, _P, _P, _P, _P, _P],
+            "tt_logp_backward": [_P, _I64, _P, _I64, _P, _P, _P, _P, _P, _P, _I64, _P],
+            "tt_logp_loss": [_P, _I64, _P, _I64, _P, _P, _P, _P, _P, _P, _P, _I64, _P],
             "tt_attn_plan": [_P, _P],
             "tt_attn_workspace_size": [_P, _P, ctypes.c_int, _P],
             "tt_attn_forward": [_P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P],
@@ -440,6 +484,95 @@ def tt_attn_backward(plan: Plan, seqs: tt_attn_seqs, q: tt_heads, k: tt_heads, v
     ref = ctypes.byref
     return lib().tt_attn_backward(plan.handle, ref(seqs), ref(q), ref(k), ref(v), ref(o), lse,
                                   ref(dout), ref(dq), ref(dk), ref(dv), ws, ws_bytes, stream)
+
+
+def tt_norm_dropout_forward(plan: Plan, dropout: Plan, T: int, rng: int, x: int, res: int,
+                            gamma: int, beta: int, sum: int, y: int, stats: int,
+                            stream: int = 0) -> int:
+    return lib().tt_norm_dropout_forward(plan.handle, dropout.handle, T, rng, x, res, gamma, beta,
+                                         sum, y, stats, stream)
+
+
+def tt_norm_dropout_backward(plan: Plan, dropout: Plan, T: int, rng: int, s: int, dy: int,
+                             dsum: int, gamma: int, stats: int, dx: int, dres: int, dgamma: int,
+                             dbeta: int, ws: int, ws_bytes: int, stream: int = 0) -> int:
+    return lib().tt_norm_dropout_backward(plan.handle, dropout.handle, T, rng, s, dy, dsum, gamma,
+                                          stats, dx, dres, dgamma, dbeta, ws, ws_bytes, stream)
+
+
+def tt_dropout_plan(p: float, site: int, act: int) -> Plan:
+    desc = tt_dropout_desc(float(p), int(site), int(act))
+    h = ctypes.c_void_p()
+    _check(lib().tt_dropout_plan(ctypes.byref(desc), ctypes.byref(h)), "tt_dropout_plan")
+    return Plan(h.value, "dropout", ())
+
+
+def tt_dropout(plan: Plan, n: int, rng: int, x: int, res: int, y: int, stream: int = 0) -> int:
+    return lib().tt_dropout(plan.handle, n, rng, x, res, y, stream)
+
+
+def tt_rope_plan(heads: int, kv_heads: int, dim: int, rot: int, base: float,
+                 freqs: Optional[Sequence[float]], interleaved: bool, eps: float, act: int,
+                 flags: int = 0) -> Plan:
+    """freqs: rot / 2 frequencies in radians a position, or None for those of base."""
+    given = None
+    if freqs is not None:
+        given = (ctypes.c_double * max(1, len(freqs)))(*(float(f) for f in freqs))
+        if 2 * len(freqs) != int(rot):
+            raise ValueError(f"freqs: expected {int(rot) // 2} values, got {len(freqs)}")
+    desc = tt_rope_desc(int(heads), int(kv_heads), int(dim), int(rot), float(base),
+                        None if given is None else ctypes.addressof(given), int(interleaved),
+                        float(eps), int(act), int(flags))
+    h = ctypes.c_void_p()
+    _check(lib().tt_rope_plan(ctypes.byref(desc), ctypes.byref(h)), "tt_rope_plan")
+    return Plan(h.value, "rope", ())
+
+
+def tt_rope_forward(plan: Plan, T: int, pos: int, q: tt_heads, k: tt_heads, gq: int, gk: int,
+                    q_out: tt_heads, k_out: tt_heads, v: Optional[tt_heads],
+                    v_out: Optional[tt_heads], rows: int, cache_rows: int,
+                    stream: int = 0) -> int:
+    ref = ctypes.byref
+    return lib().tt_rope_forward(plan.handle, T, pos, ref(q), ref(k), gq, gk, ref(q_out),
+                                 ref(k_out), None if v is None else ref(v),
+                                 None if v_out is None else ref(v_out), rows, cache_rows, stream)
+
+
+def tt_rope_backward(plan: Plan, T: int, pos: int, q: Optional[tt_heads], k: Optional[tt_heads],
+                     gq: int, gk: int, dq_out: tt_heads, dk_out: tt_heads, dq: tt_heads,
+                     dk: tt_heads, dgq: int, dgk: int, ws: int, ws_bytes: int,
+                     stream: int = 0) -> int:
+    ref = ctypes.byref
+    return lib().tt_rope_backward(plan.handle, T, pos, None if q is None else ref(q),
+                                  None if k is None else ref(k), gq, gk, ref(dq_out), ref(dk_out),
+                                  ref(dq), ref(dk), dgq, dgk, ws, ws_bytes, stream)
+
+
+def tt_logp_plan(V: int, scale: float, top: int, act: int) -> Plan:
+    desc = tt_logp_desc(int(V), float(scale), int(top), int(act))
+    h = ctypes.c_void_p()
+    _check(lib().tt_logp_plan(ctypes.byref(desc), ctypes.byref(h)), "tt_logp_plan")
+    return Plan(h.value, "logp", ())
+
+
+def tt_logp_forward(plan: Plan, T: int, logits: int, stride: int, targets: int, logp: int,
+                    lse: int, entropy: int, top: int, top_logp: int, stream: int = 0) -> int:
+    return lib().tt_logp_forward(plan.handle, T, logits, stride, targets, logp, lse, entropy, top,
+                                 top_logp, stream)
+
+
+def tt_logp_backward(plan: Plan, T: int, logits: int, stride: int, targets: int, lse: int,
+                     dlogp: int, entropy: int, dentropy: int, dlogits: int, dstride: int,
+                     stream: int = 0) -> int:
+    return lib().tt_logp_backward(plan.handle, T, logits, stride, targets, lse, dlogp, entropy,
+                                  dentropy, dlogits, dstride, stream)
+
+
+def tt_logp_loss(plan: Plan, T: int, logits: int, stride: int, targets: int, dlogp: int,
+                 dentropy: int, logp: int, lse: int, entropy: int, dlogits: int, dstride: int,
+                 stream: int = 0) -> int:
+    return lib().tt_logp_loss(plan.handle, T, logits, stride, targets, dlogp, dentropy, logp, lse,
+                              entropy, dlogits, dstride, stream)
 
 
 def tt_get_device_status(stream: int = 0) -> int:
