@@ -1,15 +1,16 @@
 // Log probabilities of given tokens with the row's log-sum, entropy and top
 // alternatives; their gradient; and both in one pass over the logits.
 //
-// All are bound by HBM.  In units of log2, with c = scale log2(e) and M = c max:
-//   t = c x - M,  e = 2^t,  s = sum e,  w = sum e t
-//   lse = ln2 (M + log2 s),  log p = ln2 (t - log2 s),  H = ln2 (log2 s - w / s)
+// All are bound by HBM.  In units of log2, with c = scale log2(e) and the row's maximum m:
+//   t = c (x - m),  e = 2^t,  s = sum e,  w = sum e t
+//   lse = scale m + ln2 log2 s,  log p = ln2 (t - log2 s),  H = ln2 (log2 s - w / s)
 //   d L / d x = scale (g ([target] - p) - h p (log p + H))
 //             = e (A + B t) + scale g [target]
-// One pass finds M, s and w: each thread keeps the maximum of what it has seen and
+// One pass finds m, s and w: each thread keeps the maximum of what it has seen and
 // scales its sums when that rises (rarely, after the first values); the threads'
-// sums meet at the common maximum.  t is one fused multiply-add on a common M, so a
-// log probability is as exact at logits of a thousand as at logits of one.
+// sums meet at the common maximum.  The difference comes first (one more instruction
+// for two values than c x - c m), so a log probability is as exact at logits of a
+// thousand as at logits of one, and logits of the type's lowest value do not overflow.
 //
 // A row is taken by 1, 4 or 16 warps by its width; rows that are few or long are
 // split over a cluster's CTAs, which meet through shared memory.  Rows start
@@ -109,13 +110,11 @@ struct Cut {
 // Running maximum and sums of a thread.
 template <bool ENT>
 struct Sums {
-  float m = -INFINITY, M = 0.f;  // maximum; c times it (0 while there is none)
+  float m = -INFINITY, ref = 0.f;  // maximum; what is taken off (0 while there is none)
   float2 s = make_float2(0.f, 0.f), w = s;
   __device__ void raise(float to, float c) {
-    const float N = to * c;
-    if (m > -INFINITY) scale(M - N);
-    m = to;
-    M = N;
+    if (m > -INFINITY) scale((m - to) * c);
+    m = ref = to;
   }
   // the sums at a maximum higher by -by
   __device__ void scale(float by) {
@@ -133,14 +132,14 @@ struct Sums {
   __device__ void add(const float* f, float top, float c) {
     if (top > m) raise(top, c);
     if (VEC == 1) {
-      const float t = fmaf(f[0], c, -M), e = ex2(t);
+      const float t = (f[0] - ref) * c, e = ex2(t);
       s.x += e;
       if (ENT) w.x = fmaf(e, fmaxf(t, -256.f), w.x);
     }
-    const float2 cc = make_float2(c, c), mm = make_float2(-M, -M);
+    const float2 cc = make_float2(c, c), off = make_float2(-ref, -ref);
 #pragma unroll
     for (int i = 0; i + 1 < VEC; i += 2) {
-      float2 t = __ffma2_rn(make_float2(f[i], f[i + 1]), cc, mm);
+      float2 t = __fmul2_rn(__fadd2_rn(make_float2(f[i], f[i + 1]), off), cc);
       const float2 e = make_float2(ex2(t.x), ex2(t.y));
       s = __fadd2_rn(s, e);
       if (ENT) {
@@ -395,8 +394,7 @@ __global__ void __launch_bounds__(W == 1 ? 32 * kRowsPerBlock : 32 * W) logp_ker
   }
   // the team's, then the cluster's
   float most = team_max<W>(sum.m, red);
-  float M = most > -INFINITY ? most * p.c : 0.f;
-  if (sum.m > -INFINITY && M != sum.M) sum.scale(sum.M - M);
+  if (sum.m > -INFINITY && sum.m != most) sum.scale((sum.m - most) * p.c);
   float2 sw = team_sum<W>(make_float2(sum.s.x + sum.s.y, sum.w.x + sum.w.y), red);
   if (W == 16 && p.cluster > 1) {
     if (tid == 0) meet[0] = most, meet[1] = sw.x, meet[2] = sw.y;
@@ -408,14 +406,12 @@ __global__ void __launch_bounds__(W == 1 ? 32 * kRowsPerBlock : 32 * W) logp_ker
       one.s.x = peer_float(meet + 1, lane);
       one.w.x = peer_float(meet + 2, lane);
     }
-    one.M = one.m > -INFINITY ? one.m * p.c : 0.f;
     most = one.m;
 #pragma unroll
     for (int o = kMaxCluster / 2; o; o >>= 1)
       most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
     most = __shfl_sync(0xffffffffu, most, 0);
-    M = most > -INFINITY ? most * p.c : 0.f;
-    if (one.m > -INFINITY && M != one.M) one.scale(one.M - M);
+    if (one.m > -INFINITY && one.m != most) one.scale((one.m - most) * p.c);
 #pragma unroll
     for (int o = kMaxCluster / 2; o; o >>= 1) {
       one.s.x += __shfl_xor_sync(0xffffffffu, one.s.x, o);
@@ -424,14 +420,15 @@ __global__ void __launch_bounds__(W == 1 ? 32 * kRowsPerBlock : 32 * W) logp_ker
     sw.x = __shfl_sync(0xffffffffu, one.s.x, 0);
     sw.y = __shfl_sync(0xffffffffu, one.w.x, 0);
   }
+  const float ref = most > -INFINITY ? most : 0.f;
   const float logs = log2f(sw.x);  // -infinity where no logit is above it
   const float ent = sw.x == 0.f ? 0.f : kLn2 * (logs - sw.y / sw.x);
   if (tid == 0 && rank == 0) {
-    if (p.lse) p.lse[row] = sw.x == 0.f ? -INFINITY : kLn2 * (M + logs);
+    if (p.lse) p.lse[row] = sw.x == 0.f ? -INFINITY : fmaf(ref, p.scale, kLn2 * logs);
     if (p.logp)
       p.logp[row] = target < 0                                 ? 0.f
                     : sw.x == 0.f || picked == -INFINITY ? -INFINITY
-                                                         : kLn2 * (fmaf(picked, p.c, -M) - logs);
+                                                         : fmaf(picked - ref, p.scale, -kLn2 * logs);
     if (ENT && p.ent) p.ent[row] = ent;
   }
 
@@ -457,7 +454,7 @@ __global__ void __launch_bounds__(W == 1 ? 32 * kRowsPerBlock : 32 * W) logp_ker
       const uint64_t e = top_shared.best[tid];
       const float f = of_key((uint32_t)(e >> 32));
       p.ids[row * p.top + tid] = (int)~(uint32_t)e;
-      p.tops[row * p.top + tid] = f == -INFINITY ? f : kLn2 * (fmaf(f, p.c, -M) - logs);
+      p.tops[row * p.top + tid] = f == -INFINITY ? f : fmaf(f - ref, p.scale, -kLn2 * logs);
     }
   }
 
@@ -472,7 +469,7 @@ __global__ void __launch_bounds__(W == 1 ? 32 * kRowsPerBlock : 32 * W) logp_ker
     const float A = -p.scale * fmaf(h, ent - kLn2 * logs, g) * inv;
     const float B = -p.scale * kLn2 * h * inv;
     auto grad = [&](float f) {
-      const float t = fmaf(f, p.c, -M);
+      const float t = (f - ref) * p.c;
       return none ? 0.f : ex2(t) * (ENT ? fmaf(B, fmaxf(t, -256.f), A) : A);
     };
     if (tid < edges) {
@@ -751,8 +748,8 @@ tt_status tt_logp_backward(const tt_plan_t* plan, int64_t T, const void* logits,
                            int64_t dstride, void* stream) {
   LogpArgs a;
   if (!common_ok(plan, T, logits, stride, targets, &a) || dstride < a.V ||
-      dstride > (int64_t)1 << 31 || (dlogp && !targets) || (!dlogp && !dentropy) ||
-      (dentropy && !entropy && T > 0) || (T > 0 && (!lse || !dlogits)) || !aligned_to(lse, 4) ||
+      dstride > (int64_t)1 << 31 || (dlogp && !targets) || (dentropy && !entropy) ||
+      (T > 0 && ((!dlogp && !dentropy) || !lse || !dlogits)) || !aligned_to(lse, 4) ||
       !aligned_to(dlogp, 4) || !aligned_to(entropy, 4) || !aligned_to(dentropy, 4) ||
       !aligned_to(dlogits, plan->logits.act == TT_DT_F32 ? 4 : 2))
     return TT_ERR_INVALID_ARG;
@@ -775,8 +772,8 @@ tt_status tt_logp_loss(const tt_plan_t* plan, int64_t T, const void* logits, int
                        void* stream) {
   LogpArgs a;
   if (!common_ok(plan, T, logits, stride, targets, &a) || dstride < a.V ||
-      dstride > (int64_t)1 << 31 || ((dlogp || logp) && !targets) || (!dlogp && !dentropy) ||
-      (T > 0 && !dlogits) || !aligned_to(logp, 4) || !aligned_to(lse, 4) ||
+      dstride > (int64_t)1 << 31 || ((dlogp || logp) && !targets) ||
+      (T > 0 && ((!dlogp && !dentropy) || !dlogits)) || !aligned_to(logp, 4) || !aligned_to(lse, 4) ||
       !aligned_to(entropy, 4) || !aligned_to(dlogp, 4) || !aligned_to(dentropy, 4) ||
       !aligned_to(dlogits, plan->logits.act == TT_DT_F32 ? 4 : 2))
     return TT_ERR_INVALID_ARG;
