@@ -3,18 +3,22 @@
 // with the reduction of the weight gradients.
 //
 // Both are bound by HBM: a head's values are read once into registers and written
-// once.  A warp takes a token; its lanes are dealt so that a lane holds both
-// channels of each of its pairs (two chunks of P consecutive channels half a
-// rotation apart, or one run of 2 P where neighbours are pairs), so the rotation
-// needs no exchange and the norm's sums only those over a head's lanes.  The
-// angles of a token are common to its heads: the warp's lanes compute them once, a
-// pair each, and share them through shared memory.
+// once.  A warp holds 32 / group heads side by side, the same ones for every token it
+// takes: its pointers step from row to row, its weights stay in registers, and so do
+// the backward's sums.  A lane holds both channels of each of its pairs (two chunks of
+// P consecutive channels half a rotation apart, or one run of 2 P where neighbours are
+// pairs), so the rotation needs no exchange and the norm's sums only those over a
+// head's lanes.  The warp's lanes compute the angles of its token, a pair each, and
+// share them through shared memory: each warp of a token does so again, which takes
+// fewer instructions than a warp that goes through all of a token's heads spends on
+// finding them (16384 tokens of 24 heads of 64 in bf16: 36 us, backward 98).
 //
 // An angle is pos f modulo a turn.  The frequency is held as a 64-bit fraction of a
 // turn, so the product modulo 2^64 is that reduction itself, without rounding: the
 // error is the frequency's own (2^-52 of it, times the position), at any position
-// of 31 bits.  The nearest quarter turn is taken off, and what is left, at most an
-// eighth of a turn either way, is rounded to fp32 for sincospi.
+// of 31 bits.  The nearest quarter turn is taken off; sine and cosine of the rest, an
+// eighth of a turn at most, come from the hardware's approximation in bf16 (off by
+// 2^-20, where the output's half step is 2^-8), from sincospi in f32.
 #include <cmath>
 #include <new>
 
@@ -40,11 +44,11 @@ struct RopeArgs {
   int64_t T;
   int heads, kv, dim, rot;
   int group;       // lanes of a head: a power of two
-  int chunks;      // chunks of a head; the first rotated ones, then the rest
+  int chunks;      // chunks of a head: the rotated ones, then the rest
   int turned;      // rotated chunks
-  int parts;       // warps of a token
+  int passes;      // warps of a token
   int norm;        // 0: rotation alone
-  float n, eps;
+  float inv_n, eps;
   const int32_t* pos;
   const int32_t* rows;  // k and v go to these rows of ko and vo
   int64_t cache_rows;
@@ -52,7 +56,6 @@ struct RopeArgs {
   Heads dq, dk;
   int values;                 // v is copied too
   const float *gq, *gk;
-  int gq16, gk16;             // 16-byte aligned
   float* sums;                // backward: [gridDim.x][2 dim] shares of dgq, dgk
   float *dgq, *dgk;           // written directly by a grid of one block
   int accumulate;
@@ -60,299 +63,304 @@ struct RopeArgs {
 };
 
 // cos and sin of pos frequency
-__device__ __forceinline__ float2 angle(int64_t pos, uint64_t turn) {
+template <typename T>
+__device__ __forceinline__ void angle(int64_t pos, uint64_t turn, float* cosine, float* sine) {
   const uint64_t a = (uint64_t)pos * turn;
-  const uint64_t quarter = (a + (1ull << 61)) >> 62;
-  // in [-2^61, 2^61): 2^63 is half a turn
-  const int64_t rest = (int64_t)(a - (quarter << 62));
+  const uint32_t quarter = (uint32_t)((a + (1ull << 61)) >> 62);
+  // in [-2^61, 2^61), where 2^63 is half a turn; 2^-31 of it fits 31 bits
+  const int32_t rest = (int32_t)((int64_t)(a - ((uint64_t)quarter << 62)) >> 31);
   float s, c;
-  sincospif((float)(int32_t)(rest >> 31) * 0x1p-32f, &s, &c);
-  if (quarter & 1) {
-    const float t = c;
-    c = -s;
-    s = t;
+  if (sizeof(T) == 2) {
+    const float x = (float)rest * (float)(3.14159265358979323846 * 0x1p-32);
+    s = __sinf(x);
+    c = __cosf(x);
+  } else {
+    sincospif((float)rest * 0x1p-32f, &s, &c);
   }
-  return quarter & 2 ? make_float2(-c, -s) : make_float2(c, s);
+  const float u = quarter & 1 ? -s : c, v = quarter & 1 ? c : s;
+  *cosine = quarter & 2 ? -u : u;
+  *sine = quarter & 2 ? -v : v;
 }
 
-// What a lane holds of a head: CH chunks of P pairs.  PAIRS: neighbouring channels
-// are a pair.
-template <typename T, int P, int CH, bool PAIRS>
-struct Lane {
-  using R = Raw<T, P>;
-  int at[CH], at2[CH];       // channels of a chunk's two halves
-  bool has[CH], has2[CH];
-  float2 cs[CH][P];
+// A lane's share of a head: the first channels of its pairs and the second ones.
+template <int P>
+struct Pairs {
+  float a[P], b[P];
+};
 
-  __device__ void place(const RopeArgs& p, int lane) {
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const int i = c * 32 + (lane & (p.group - 1));
-      has[c] = i < p.chunks;
-      if (i < p.turned) {
-        at[c] = PAIRS ? 2 * P * i : P * i;
-        at2[c] = PAIRS ? at[c] + P : p.rot / 2 + P * i;
-      } else {
-        at[c] = p.rot + 2 * P * (i - p.turned);
-        at2[c] = at[c] + P;
-      }
-      has2[c] = has[c] && at2[c] < p.dim;
+// Where that lies: two runs of P channels as they are in memory.  PAIRS: neighbouring
+// channels are a pair.  The channels that are not rotated are dealt in the same runs.
+template <typename T, int P, bool PAIRS>
+struct Place {
+  using R = Raw<T, P>;
+  int at, at2;      // channels
+  bool has, has2;
+  __device__ void set(const RopeArgs& p, int i) {
+    has = i < p.chunks;
+    if (i < p.turned) {
+      at = PAIRS ? 2 * P * i : P * i;
+      at2 = PAIRS ? at + P : p.rot / 2 + P * i;
+    } else {
+      at = p.rot + 2 * P * (i - p.turned);
+      at2 = at + P;
     }
+    has2 = has && at2 < p.dim;
   }
-  // the table of the token's angles: a lane keeps those of its pairs
-  __device__ void angles(const RopeArgs& p, int64_t pos, const uint64_t* turn, float2* table,
-                         int lane) {
-    __syncwarp();
-    for (int i = lane; i < p.rot / 2; i += 32) table[i] = angle(pos, turn[i]);
-    __syncwarp();
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const int i = c * 32 + (lane & (p.group - 1));
-#pragma unroll
-      for (int j = 0; j < P; ++j)
-        cs[c][j] = i < p.turned ? table[i * P + j] : make_float2(1.f, 0.f);
-    }
+  __device__ void load(const T* x, R& u, R& v) const {
+    if (has) u = *reinterpret_cast<const R*>(x + at);
+    if (has2) v = *reinterpret_cast<const R*>(x + at2);
   }
-  __device__ void turn_by(int c, float (&u)[2 * P], bool back) const {
+  // runs to pairs and back
+  __device__ static void split(const float* u, const float* v, Pairs<P>& x) {
 #pragma unroll
     for (int j = 0; j < P; ++j) {
-      float& a = u[PAIRS ? 2 * j : j];
-      float& b = u[PAIRS ? 2 * j + 1 : P + j];
-      const float co = cs[c][j].x, si = back ? -cs[c][j].y : cs[c][j].y;
-      const float t = fmaf(a, co, -b * si);
-      b = fmaf(a, si, b * co);
-      a = t;
+      const int k = 2 * j;
+      x.a[j] = !PAIRS || P == 1 ? u[j] : k < P ? u[k] : v[k - P];
+      x.b[j] = !PAIRS || P == 1 ? v[j] : k < P ? u[k + 1] : v[k + 1 - P];
     }
   }
-  __device__ void load(const T* x, R (&a)[CH], R (&b)[CH]) const {
+  __device__ static void join(const Pairs<P>& x, float* u, float* v) {
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      if (has[c]) a[c] = *reinterpret_cast<const R*>(x + at[c]);
-      if (has2[c]) b[c] = *reinterpret_cast<const R*>(x + at2[c]);
+    for (int j = 0; j < P; ++j) {
+      u[j] = !PAIRS || P == 1 ? x.a[j] : j % 2 ? x.b[j / 2] : x.a[j / 2];
+      v[j] = !PAIRS || P == 1 ? x.b[j] : j % 2 ? x.b[(P + j) / 2] : x.a[(P + j) / 2];
     }
   }
-  __device__ void get(int c, const R (&a)[CH], const R (&b)[CH], float (&u)[2 * P]) const {
-#pragma unroll
-    for (int j = 0; j < 2 * P; ++j) u[j] = 0.f;
-    if (has[c]) a[c].get(u);
-    if (has2[c]) b[c].get(u + P);
+  __device__ void get(const R& ru, const R& rv, Pairs<P>& x) const {
+    float u[P], v[P];
+    ru.get(u);
+    rv.get(v);
+    split(u, v, x);
   }
-  __device__ void put(T* y, int c, const float (&u)[2 * P]) const {
+  __device__ void put(T* y, const Pairs<P>& x) const {
+    float u[P], v[P];
+    join(x, u, v);
     R o;
-    if (has[c]) {
-      o.set(u);
-      *reinterpret_cast<R*>(y + at[c]) = o;
-    }
-    if (has2[c]) {
-      o.set(u + P);
-      *reinterpret_cast<R*>(y + at2[c]) = o;
-    }
+    o.set(u);
+    if (has) *reinterpret_cast<R*>(y + at) = o;
+    o.set(v);
+    if (has2) *reinterpret_cast<R*>(y + at2) = o;
   }
-  __device__ void weights(const float* g, bool aligned, int c, float (&w)[2 * P]) const {
+  // values of channels; 0 where there are none
+  __device__ void weights(const float* g, Pairs<P>& x) const {
+    float u[P], v[P];
 #pragma unroll
-    for (int j = 0; j < 2 * P; ++j) w[j] = 0.f;
-    if (has[c]) weights_at<P>(g, at[c], 1.f, aligned, w);
-    if (has2[c]) weights_at<P>(g, at2[c], 1.f, aligned, w + P);
+    for (int j = 0; j < P; ++j) {
+      u[j] = !has ? 0.f : g ? __ldg(g + at + j) : 1.f;
+      v[j] = !has2 ? 0.f : g ? __ldg(g + at2 + j) : 1.f;
+    }
+    split(u, v, x);
   }
 };
 
-__device__ __forceinline__ float head_sum(float v, int group) {
-  for (int o = group >> 1; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+// x turned by the angle, or back.
+template <int P>
+__device__ __forceinline__ void turn_by(const float* cosine, const float* sine, bool back,
+                                        Pairs<P>& x) {
+  float c[P], s[P], m[P], u[P], v[P];
+  if (P >= 4) {
+#pragma unroll
+    for (int j = 0; j < P; j += 4) {
+      const float4 f = *reinterpret_cast<const float4*>(cosine + j);
+      const float4 g = *reinterpret_cast<const float4*>(sine + j);
+      c[j] = f.x, c[j + 1] = f.y, c[j + 2] = f.z, c[j + 3] = f.w;
+      s[j] = g.x, s[j + 1] = g.y, s[j + 2] = g.z, s[j + 3] = g.w;
+    }
+  } else {
+    c[0] = cosine[0];
+    s[0] = sine[0];
+  }
+#pragma unroll
+  for (int j = 0; j < P; ++j) {
+    m[j] = -s[j];
+  }
+  mul<P>(x.a, c, u);
+  mul<P>(x.b, c, v);
+  fma<P>(x.b, back ? s : m, u, u);
+  fma<P>(x.a, back ? m : s, v, x.b);
+#pragma unroll
+  for (int j = 0; j < P; ++j) x.a[j] = u[j];
 }
 
-// A warp's passes over a token: its lanes hold 32 / group heads at a time, first
-// those of q, then of k, then of v.  With `parts` warps a token each takes every
-// parts-th pass.  The next pass is loaded while one is worked on.
+// 1 / sqrt(x): the hardware's approximation and one step of Newton's iteration.
+__device__ __forceinline__ float inverse_root(float x) {
+  const float r = rsqrtf(x);
+  return fmaf(0.5f * r, fmaf(-x * r, r, 1.f), r);
+}
+
 template <typename T, int P, int CH, bool PAIRS, bool GRAD>
-__global__ void __launch_bounds__(32 * kWarps, GRAD ? 2 : 3) rope_kernel(RopeArgs p) {
-  using L = Lane<T, P, CH, PAIRS>;
-  using R = typename L::R;
+__global__ void __launch_bounds__(32 * kWarps, GRAD ? 2 : 3)
+    rope_kernel(const __grid_constant__ RopeArgs p) {
+  using R = Raw<T, P>;
   __shared__ uint64_t turn[kMaxPairs];
-  __shared__ float2 tables[kWarps][kMaxPairs];
+  __shared__ __align__(16) float cosines[kWarps][kMaxPairs], sines[kWarps][kMaxPairs];
   __shared__ float cross[GRAD ? kWarps : 1][GRAD ? 2 * 2 * kMaxPairs : 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int i = threadIdx.x; i < p.rot / 2; i += 32 * kWarps) turn[i] = p.turn[i];
+  for (int i = p.rot / 2 + lane; i < kMaxPairs; i += 32) {  // what is not rotated
+    cosines[warp][i] = 1.f;
+    sines[warp][i] = 0.f;
+  }
   __syncthreads();
   pdl_wait();
   pdl_trigger();
-  L at;
-  at.place(p, lane);
-  const int side = 32 / p.group, mine = lane / p.group;  // heads of a pass; this lane's
-  const int nq = (p.heads + side - 1) / side, nk = (p.kv + side - 1) / side;
-  const int passes = nq + nk + (p.values ? nk : 0);
+  // this lane's head and channels
   const int64_t w = (int64_t)blockIdx.x * kWarps + warp;
-  const int64_t step = (int64_t)gridDim.x * kWarps / p.parts;
-  const int part = (int)(w % p.parts);
-  int64_t t = w / p.parts;
+  const int64_t step = (int64_t)gridDim.x * kWarps / p.passes;
+  int h = (int)(w % p.passes) * (32 / p.group) + lane / p.group;
+  int64_t t = w / p.passes;
   if (t >= step) t = p.T;
-  int s = part;
-
-  R xa[CH], xb[CH], da[GRAD ? CH : 1], db[GRAD ? CH : 1];
-  int64_t pos = 0, row = 0;
-  auto fetch = [&](int64_t t, int s) {
-    const int which = s < nq ? 0 : s < nq + nk ? 1 : 2;
-    const int h = (s - (which == 0 ? 0 : which == 1 ? nq : nq + nk)) * side + mine;
-    if (h >= (which == 0 ? p.heads : p.kv)) return;
-    if (!GRAD || p.norm) {
-      const Heads& from = which == 0 ? p.q : which == 1 ? p.k : p.v;
-      at.load(from.at<T>(t, h), xa, xb);
-    }
-    if constexpr (GRAD) at.load((which == 0 ? p.dq : p.dk).at<T>(t, h), da, db);
-  };
-  auto fetch_token = [&](int64_t t) {
-    pos = p.pos ? p.pos[t] : t;
-    row = p.rows ? p.rows[t] : t;
-  };
-  float accq[CH][2 * P], acck[CH][2 * P];
+  const int which = h < p.heads ? 0 : h < p.heads + p.kv ? 1 : 2;
+  h -= which == 0 ? 0 : which == 1 ? p.heads : p.heads + p.kv;
+  const bool here = which < 2 ? which == 0 || h < p.kv : p.values && h < p.kv;
+  Place<T, P, PAIRS> at[CH];
+  Pairs<P> g[CH];
 #pragma unroll
-  for (int c = 0; c < CH; ++c)
-#pragma unroll
-    for (int j = 0; j < 2 * P; ++j) accq[c][j] = acck[c][j] = 0.f;
-
-  int64_t to = 0;  // the row that the token's keys go to
-  bool fresh = true;
-  if (t < p.T) {
-    fetch_token(t);
-    fetch(t, s);
+  for (int c = 0; c < CH; ++c) {
+    at[c].set(p, c * 32 + (lane & (p.group - 1)));
+    if (!here) at[c].has = at[c].has2 = false;
+    if (p.norm) at[c].weights(which == 0 ? p.gq : p.gk, g[c]);
   }
-  while (t < p.T) {
-    if (fresh) {
-      at.angles(p, pos, turn, tables[warp], lane);
-      to = row;
-      if (!GRAD && p.rows && to >= p.cache_rows) {
-        if (lane == 0) record_error(TT_ERR_DEVICE, 1);
-        to = -1;
-      }
-    }
-    const int which = s < nq ? 0 : s < nq + nk ? 1 : 2;
-    const int h = (s - (which == 0 ? 0 : which == 1 ? nq : nq + nk)) * side + mine;
-    const bool here = h < (which == 0 ? p.heads : p.kv);
-    float u[CH][2 * P], d[GRAD ? CH : 1][2 * P];
-    R va[CH], vb[CH];  // v goes as it is
+  const int share = (lane & (p.group - 1)) * P;  // its pairs in the table of angles
+  // where the head starts in the tensors' first row
+  const Heads from = which == 0 ? p.q : which == 1 ? p.k : p.v;
+  const Heads into = which == 0 ? p.qo : which == 1 ? p.ko : p.vo;
+  const Heads grad = which == 0 ? p.dq : p.dk;
+  const bool reads = !GRAD || p.norm;
+  const T* x = reads ? from.at<T>(t, here ? h : 0) : nullptr;
+  const T* d = GRAD ? grad.at<T>(t, here ? h : 0) : nullptr;
+  T* y = into.at<T>(0, here ? h : 0);
+
+  R xu[CH] = {}, xv[CH] = {}, du[GRAD ? CH : 1] = {}, dv[GRAD ? CH : 1] = {};
+  int64_t pos = 0, row = 0;
+  auto fetch = [&] {
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      at.get(c, xa, xb, u[c]);
-      if constexpr (GRAD)
-        at.get(c, da, db, d[c]);
-      else
-        va[c] = xa[c], vb[c] = xb[c];
+      if (reads) at[c].load(x, xu[c], xv[c]);
+      if constexpr (GRAD) at[c].load(d, du[c], dv[c]);
     }
-    const int64_t now = t;
-    s += p.parts;
-    fresh = s >= passes;
-    if (fresh) {
-      s = part;
-      t += step;
-      if (t < p.T) fetch_token(t);
-    }
-    if (t < p.T) fetch(t, s);
+    pos = p.pos ? p.pos[t] : t;
+    row = !GRAD && p.rows && which > 0 ? p.rows[t] : t;
+  };
+  Pairs<P> sum[CH];
+#pragma unroll
+  for (int c = 0; c < CH; ++c) fill<P>(0.f, sum[c].a), fill<P>(0.f, sum[c].b);
 
-    const float* g = which == 0 ? p.gq : p.gk;
-    const bool g16 = which == 0 ? p.gq16 : p.gk16;
+  if (t < p.T) fetch();
+  while (t < p.T) {
+    __syncwarp();
+    for (int i = lane; i < p.rot / 2; i += 32)
+      angle<T>(pos, turn[i], &cosines[warp][i], &sines[warp][i]);
+    __syncwarp();
+    bool kept = here;
+    if (!GRAD && p.rows && which > 0) {
+      if (row < 0 || row >= p.cache_rows) {
+        if (row >= 0) record_error(TT_ERR_DEVICE, 1);
+        kept = false;
+      }
+    }
+    T* out = y + (kept ? row : 0) * into.row;
+    Pairs<P> u[CH], e[GRAD ? CH : 1];
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      at[c].get(xu[c], xv[c], u[c]);
+      if constexpr (GRAD) {
+        at[c].get(du[c], dv[c], e[c]);
+      } else if (which == 2 && kept) {  // v goes as it is
+        if (at[c].has) *reinterpret_cast<R*>(out + at[c].at) = xu[c];
+        if (at[c].has2) *reinterpret_cast<R*>(out + at[c].at2) = xv[c];
+      }
+    }
+    t += step;
+    x += step * from.row;
+    if constexpr (GRAD) d += step * grad.row;
+    if (t < p.T) fetch();
+
     if constexpr (!GRAD) {
-      const bool kept = here && (which == 0 || to >= 0);
-      const int64_t out = which == 0 ? now : to;
-      if (which == 2) {
-        if (kept) {
-          T* y = p.vo.at<T>(out, h);
-#pragma unroll
-          for (int c = 0; c < CH; ++c) {
-            if (at.has[c]) *reinterpret_cast<R*>(y + at.at[c]) = va[c];
-            if (at.has2[c]) *reinterpret_cast<R*>(y + at.at2[c]) = vb[c];
-          }
-        }
-        continue;
-      }
       if (p.norm) {
-        float sum = 0.f;
+        float2 s2 = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int c = 0; c < CH; ++c)
-#pragma unroll
-          for (int j = 0; j < 2 * P; ++j) sum = fmaf(u[c][j], u[c][j], sum);
-        sum = head_sum(sum, p.group);
-        const float r = 1.f / sqrtf(sum / p.n + p.eps);
+        for (int c = 0; c < CH; ++c) mul_up<P>(s2, u[c].a, u[c].a), mul_up<P>(s2, u[c].b, u[c].b);
+        float s = s2.x + s2.y;
+        for (int o = p.group >> 1; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        float r[P];
+        fill<P>(inverse_root(fmaf(s, p.inv_n, p.eps)), r);
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-          float f[2 * P];
-          at.weights(g, g16, c, f);
-#pragma unroll
-          for (int j = 0; j < 2 * P; ++j) u[c][j] = u[c][j] * r * f[j];
+          mul<P>(u[c].a, r, u[c].a), mul<P>(u[c].a, g[c].a, u[c].a);
+          mul<P>(u[c].b, r, u[c].b), mul<P>(u[c].b, g[c].b, u[c].b);
         }
       }
-      if (kept) {
-        T* y = (which == 0 ? p.qo : p.ko).at<T>(out, h);
+      if (kept && which < 2) {
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-          at.turn_by(c, u[c], false);
-          at.put(y, c, u[c]);
+          turn_by<P>(&cosines[warp][32 * P * c + share], &sines[warp][32 * P * c + share], false,
+                     u[c]);
+          at[c].put(out, u[c]);
         }
       }
     } else {
-      // du = R^T dy; h = x r; g' = du g; dx = r (g' - h mean(g' h)); dg = sum du h.
-      // Lanes of a head that the token lacks hold zeros or what the pass before
-      // left: they join the exchanges of other lanes' groups, not their sums.
+      // du = R^T dy; h = x r; g' = du g; dx = r (g' - h mean(g' h)); dg = sum du h
 #pragma unroll
-      for (int c = 0; c < CH; ++c) at.turn_by(c, d[c], true);
+      for (int c = 0; c < CH; ++c)
+        turn_by<P>(&cosines[warp][32 * P * c + share], &sines[warp][32 * P * c + share], true,
+                   e[c]);
       if (p.norm) {
-        float sx = 0.f, sg = 0.f, f[CH][2 * P];
+        float2 s2 = make_float2(0.f, 0.f), m2 = s2;
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-          at.weights(g, g16, c, f[c]);
-#pragma unroll
-          for (int j = 0; j < 2 * P; ++j) {
-            sx = fmaf(u[c][j], u[c][j], sx);
-            f[c][j] *= d[c][j];
-            sg = fmaf(f[c][j], u[c][j], sg);
-          }
+          float gu[P];
+          mul_up<P>(s2, u[c].a, u[c].a), mul_up<P>(s2, u[c].b, u[c].b);
+          mul<P>(e[c].a, u[c].a, gu), mul_up<P>(m2, gu, g[c].a);
+          mul<P>(e[c].b, u[c].b, gu), mul_up<P>(m2, gu, g[c].b);
         }
+        float s = s2.x + s2.y, m = m2.x + m2.y;
         for (int o = p.group >> 1; o; o >>= 1) {
-          sx += __shfl_xor_sync(0xffffffffu, sx, o);
-          sg += __shfl_xor_sync(0xffffffffu, sg, o);
+          s += __shfl_xor_sync(0xffffffffu, s, o);
+          m += __shfl_xor_sync(0xffffffffu, m, o);
         }
-        const float r = 1.f / sqrtf(sx / p.n + p.eps);
-        const float m = r * sg / p.n;  // mean(g' h)
+        const float one = inverse_root(fmaf(s, p.inv_n, p.eps));
+        float r[P], less[P];
+        fill<P>(one, r);
+        fill<P>(-one * m * p.inv_n, less);  // less mean(g' h)
 #pragma unroll
-        for (int c = 0; c < CH; ++c)
-#pragma unroll
-          for (int j = 0; j < 2 * P; ++j) {
-            const float x = u[c][j] * r;
-            if (here) {
-              if (which == 0)
-                accq[c][j] = fmaf(d[c][j], x, accq[c][j]);
-              else
-                acck[c][j] = fmaf(d[c][j], x, acck[c][j]);
-            }
-            d[c][j] = r * fmaf(-x, m, f[c][j]);
-          }
+        for (int c = 0; c < CH; ++c) {
+          mul<P>(u[c].a, r, u[c].a), mul<P>(u[c].b, r, u[c].b);
+          fma<P>(e[c].a, u[c].a, sum[c].a, sum[c].a);
+          fma<P>(e[c].b, u[c].b, sum[c].b, sum[c].b);
+          mul<P>(e[c].a, g[c].a, e[c].a), mul<P>(e[c].b, g[c].b, e[c].b);
+          fma<P>(u[c].a, less, e[c].a, e[c].a), fma<P>(u[c].b, less, e[c].b, e[c].b);
+          mul<P>(e[c].a, r, e[c].a), mul<P>(e[c].b, r, e[c].b);
+        }
       }
-      if (here) {
-        T* y = (which == 0 ? p.qo : p.ko).at<T>(now, h);
 #pragma unroll
-        for (int c = 0; c < CH; ++c) at.put(y, c, d[c]);
-      }
+      for (int c = 0; c < CH; ++c) at[c].put(out, e[c]);
     }
   }
 
   if constexpr (GRAD) {
     if (!p.norm || !p.sums) return;
-    // the warp's heads, then the block's warps in order
+    // the warp's heads of q and of k, then the block's warps in order
 #pragma unroll
-    for (int c = 0; c < CH; ++c)
+    for (int c = 0; c < CH; ++c) {
+      float u[2 * P];
+      Place<T, P, PAIRS>::join(sum[c], u, u + P);
+      Place<T, P, PAIRS> own;  // the channels, whether or not this lane's head exists
+      own.set(p, c * 32 + (lane & (p.group - 1)));
 #pragma unroll
       for (int j = 0; j < 2 * P; ++j) {
-        float a = accq[c][j], b = acck[c][j];
+        float a = here && which == 0 ? u[j] : 0.f, b = here && which == 1 ? u[j] : 0.f;
         for (int o = p.group; o < 32; o <<= 1) {
           a += __shfl_xor_sync(0xffffffffu, a, o);
           b += __shfl_xor_sync(0xffffffffu, b, o);
         }
-        const bool real = j < P ? at.has[c] : at.has2[c];
-        const int i = j < P ? at.at[c] + j : at.at2[c] + j - P;
-        if (mine == 0 && real) {
+        if (lane < p.group && (j < P ? own.has : own.has2)) {
+          const int i = j < P ? own.at + j : own.at2 + j - P;
           cross[warp][i] = a;
           cross[warp][p.dim + i] = b;
         }
       }
+    }
     __syncthreads();
     for (int i = threadIdx.x; i < 2 * p.dim; i += 32 * kWarps) {
       float v = 0.f;
@@ -376,15 +384,32 @@ int pow2_above(int n) {
   return g;
 }
 
-// Warps that the card keeps busy; a token is split over several where there are
-// fewer tokens.
-int64_t most_warps() { return (int64_t)device_sms() * 2 * kWarps; }
+// Blocks of T tokens of `passes` warps each: the fewest that keep the most that fit on
+// the SMs for the same number of tokens a warp.
+int64_t blocks_of(int64_t T, int64_t passes, int per_sm) {
+  const int64_t most = (int64_t)device_sms() * per_sm * kWarps;  // warps
+  int64_t side = most / passes;                                  // tokens side by side
+  if (side < 1) side = 1;
+  const int64_t rounds = (T + side - 1) / side;
+  side = (T + rounds - 1) / rounds;
+  return (side * passes + kWarps - 1) / kWarps;
+}
 
-int64_t grad_blocks(int64_t T) {
-  const int64_t b = (T + kWarps - 1) / kWarps;
-  if (T <= 4 * kWarps) return 1;  // a second launch would cost more than the rows
-  const int64_t most = (int64_t)device_sms() * 2;
-  return b < most ? b : most;
+constexpr int kGradPerSm = 2, kPerSm = 3;
+
+// A backward of few heads in all runs as one block: a second launch for the partial
+// sums would cost more.
+int64_t grad_blocks(int64_t T, int64_t passes) {
+  return T * passes <= 4 * kWarps && passes <= kWarps ? 1 : blocks_of(T, passes, kGradPerSm);
+}
+// For any number of heads side by side in a warp: no fewer warps a token than this.
+int64_t most_grad_blocks(const RopePlan& R, int64_t T) {
+  int64_t most = 1;
+  for (int side = 1; side <= 32; side *= 2) {
+    const int64_t b = grad_blocks(T, (R.heads + R.kv + side - 1) / side);
+    if (b > most) most = b;
+  }
+  return most;
 }
 
 // Whether chunks of P channels fit the layout: whole chunks in each half of the
@@ -404,27 +429,16 @@ bool fits(const RopePlan& R, const RopeArgs& a, int P, bool grad) {
 }
 
 template <typename T, int P, int CH, bool PAIRS, bool GRAD>
-cudaError_t go(RopeArgs& a, cudaStream_t st) {
-  auto kernel = rope_kernel<T, P, CH, PAIRS, GRAD>;
+cudaError_t go(RopeArgs& a, int64_t* blocks, cudaStream_t st) {
   const int side = 32 / a.group;
-  const int nk = (a.kv + side - 1) / side;
-  const int passes = (a.heads + side - 1) / side + nk + (a.values ? nk : 0);
-  int64_t blocks;
-  if (GRAD) {
-    blocks = grad_blocks(a.T);
-    a.parts = 1;
-  } else {
-    int64_t parts = most_warps() / a.T;
-    a.parts = parts < 1 ? 1 : parts > passes ? passes : (int)parts;
-    const int64_t need = (a.T * a.parts + kWarps - 1) / kWarps;
-    const int64_t most = (int64_t)device_sms() * 3;
-    blocks = need < most ? need : most;
-  }
-  return launch_ex(kernel, dim3((unsigned)blocks), dim3(32 * kWarps), 0, st, false, a);
+  a.passes = (a.heads + a.kv + (a.values ? a.kv : 0) + side - 1) / side;
+  *blocks = GRAD ? grad_blocks(a.T, a.passes) : blocks_of(a.T, a.passes, kPerSm);
+  return launch_ex(rope_kernel<T, P, CH, PAIRS, GRAD>, dim3((unsigned)*blocks),
+                   dim3(32 * kWarps), 0, st, false, a);
 }
 
 template <typename T, bool GRAD>
-cudaError_t pick(const RopePlan& R, RopeArgs& a, cudaStream_t st) {
+cudaError_t pick(const RopePlan& R, RopeArgs& a, int64_t* blocks, cudaStream_t st) {
   auto shape = [&](int P) {
     a.turned = R.rot / 2 / P;
     a.chunks = a.turned + (R.dim - R.rot + 2 * P - 1) / (2 * P);
@@ -433,19 +447,19 @@ cudaError_t pick(const RopePlan& R, RopeArgs& a, cudaStream_t st) {
   if constexpr (sizeof(T) == 2) {
     if (fits(R, a, 8, GRAD)) {
       shape(8);
-      return R.inter ? go<T, 8, 1, true, GRAD>(a, st) : go<T, 8, 1, false, GRAD>(a, st);
+      return R.inter ? go<T, 8, 1, true, GRAD>(a, blocks, st) : go<T, 8, 1, false, GRAD>(a, blocks, st);
     }
   }
   if (fits(R, a, 4, GRAD)) {
     shape(4);
-    return R.inter ? go<T, 4, 1, true, GRAD>(a, st) : go<T, 4, 1, false, GRAD>(a, st);
+    return R.inter ? go<T, 4, 1, true, GRAD>(a, blocks, st) : go<T, 4, 1, false, GRAD>(a, blocks, st);
   }
   shape(1);
   if (R.inter)
-    return a.chunks <= 32 ? go<T, 1, 1, true, GRAD>(a, st)
-                          : go<T, 1, 4, true, GRAD>(a, st);
-  return a.chunks <= 32 ? go<T, 1, 1, false, GRAD>(a, st)
-                        : go<T, 1, 4, false, GRAD>(a, st);
+    return a.chunks <= 32 ? go<T, 1, 1, true, GRAD>(a, blocks, st)
+                          : go<T, 1, 4, true, GRAD>(a, blocks, st);
+  return a.chunks <= 32 ? go<T, 1, 1, false, GRAD>(a, blocks, st)
+                        : go<T, 1, 4, false, GRAD>(a, blocks, st);
 }
 
 void fill(const RopePlan& R, int64_t T, const int32_t* pos, RopeArgs* a) {
@@ -455,7 +469,7 @@ void fill(const RopePlan& R, int64_t T, const int32_t* pos, RopeArgs* a) {
   a->dim = R.dim;
   a->rot = R.rot;
   a->norm = R.eps > 0.f;
-  a->n = (float)R.dim;
+  a->inv_n = 1.f / (float)R.dim;
   a->eps = R.eps;
   a->pos = pos;
   for (int i = 0; i < R.rot / 2; ++i) a->turn[i] = R.turn[i];
@@ -464,7 +478,7 @@ void fill(const RopePlan& R, int64_t T, const int32_t* pos, RopeArgs* a) {
 }  // namespace
 
 size_t rope_workspace_bytes(const RopePlan& R, int64_t T) {
-  return R.eps > 0.f ? (size_t)grad_blocks(T) * 2 * (size_t)R.dim * sizeof(float) : 0;
+  return R.eps > 0.f ? (size_t)most_grad_blocks(R, T) * 2 * (size_t)R.dim * sizeof(float) : 0;
 }
 
 }  // namespace ttc
@@ -537,12 +551,11 @@ tt_status tt_rope_forward(const tt_plan_t* plan, int64_t T, const int32_t* pos,
   a.cache_rows = cache_rows;
   a.gq = gq;
   a.gk = gk;
-  a.gq16 = aligned_to(gq, 16);
-  a.gk16 = aligned_to(gk, 16);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   prof_begin(kPhElem, st);
-  const cudaError_t e = R.act == TT_DT_BF16 ? pick<__nv_bfloat16, false>(R, a, st)
-                                            : pick<float, false>(R, a, st);
+  int64_t blocks = 0;
+  const cudaError_t e = R.act == TT_DT_BF16 ? pick<__nv_bfloat16, false>(R, a, &blocks, st)
+                                            : pick<float, false>(R, a, &blocks, st);
   prof_end(kPhElem, st);
   count_launches(1);
   return e == cudaSuccess ? TT_OK : TT_ERR_CUDA;
@@ -577,17 +590,15 @@ tt_status tt_rope_backward(const tt_plan_t* plan, int64_t T, const int32_t* pos,
   if (need && (!ws || !aligned_to(ws, 256) || ws_bytes < need)) return TT_ERR_WORKSPACE;
   a.gq = gq;
   a.gk = gk;
-  a.gq16 = aligned_to(gq, 16);
-  a.gk16 = aligned_to(gk, 16);
   const bool sums = a.norm && (dgq || dgk);
   a.sums = sums ? static_cast<float*>(ws) : nullptr;
   a.dgq = dgq;
   a.dgk = dgk;
   prof_begin(kPhElem, st);
-  cudaError_t e = R.act == TT_DT_BF16 ? pick<__nv_bfloat16, true>(R, a, st)
-                                      : pick<float, true>(R, a, st);
+  int64_t blocks = 0;
+  cudaError_t e = R.act == TT_DT_BF16 ? pick<__nv_bfloat16, true>(R, a, &blocks, st)
+                                      : pick<float, true>(R, a, &blocks, st);
   count_launches(1);
-  const int64_t blocks = grad_blocks(T);
   if (e == cudaSuccess && sums && blocks > 1) {
     e = launch_ex(sum_parts_kernel, dim3((unsigned)((2 * R.dim + 31) / 32)), dim3(1024), 0, st,
                   false, (const float*)a.sums, (int)blocks, R.dim, dgq, dgk, a.accumulate);

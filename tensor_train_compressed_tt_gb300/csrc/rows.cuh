@@ -86,6 +86,55 @@ __device__ __forceinline__ void weights_at(const float* w, int j, float other, b
   }
 }
 
+// VEC values at once, two an instruction where they come in pairs.
+template <int VEC>
+__device__ __forceinline__ void add_up(float2& sum, const float* v) {  // sum += v
+  if (VEC == 1) sum.x += v[0];
+#pragma unroll
+  for (int i = 0; i + 1 < VEC; i += 2) sum = __fadd2_rn(sum, make_float2(v[i], v[i + 1]));
+}
+template <int VEC>
+__device__ __forceinline__ void mul_up(float2& sum, const float* a, const float* b) {  // += a b
+  if (VEC == 1) sum.x = fmaf(a[0], b[0], sum.x);
+#pragma unroll
+  for (int i = 0; i + 1 < VEC; i += 2)
+    sum = __ffma2_rn(make_float2(a[i], a[i + 1]), make_float2(b[i], b[i + 1]), sum);
+}
+template <int VEC>
+__device__ __forceinline__ void add(const float* a, const float* b, float* o) {  // o = a + b
+  if (VEC == 1) o[0] = a[0] + b[0];
+#pragma unroll
+  for (int i = 0; i + 1 < VEC; i += 2) {
+    const float2 t = __fadd2_rn(make_float2(a[i], a[i + 1]), make_float2(b[i], b[i + 1]));
+    o[i] = t.x, o[i + 1] = t.y;
+  }
+}
+template <int VEC>
+__device__ __forceinline__ void mul(const float* a, const float* b, float* o) {  // o = a b
+  if (VEC == 1) o[0] = a[0] * b[0];
+#pragma unroll
+  for (int i = 0; i + 1 < VEC; i += 2) {
+    const float2 t = __fmul2_rn(make_float2(a[i], a[i + 1]), make_float2(b[i], b[i + 1]));
+    o[i] = t.x, o[i + 1] = t.y;
+  }
+}
+template <int VEC>
+__device__ __forceinline__ void fma(const float* a, const float* b, const float* c,
+                                    float* o) {  // o = a b + c
+  if (VEC == 1) o[0] = fmaf(a[0], b[0], c[0]);
+#pragma unroll
+  for (int i = 0; i + 1 < VEC; i += 2) {
+    const float2 t = __ffma2_rn(make_float2(a[i], a[i + 1]), make_float2(b[i], b[i + 1]),
+                                make_float2(c[i], c[i + 1]));
+    o[i] = t.x, o[i + 1] = t.y;
+  }
+}
+template <int VEC>
+__device__ __forceinline__ void fill(float x, float* o) {
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) o[i] = x;
+}
+
 // dgamma[j] or dbeta[j] from its sum
 __device__ __forceinline__ void put_sum(float* out, int j, float v, int accumulate) {
   if (out) out[j] = accumulate ? out[j] + v : v;
