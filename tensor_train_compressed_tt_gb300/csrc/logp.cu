@@ -1,18 +1,21 @@
 // Log probabilities of given tokens with the row's log-sum, entropy and top
 // alternatives; their gradient; and both in one pass over the logits.
 //
-// All are bound by HBM.  In units of log2, with c = scale log2(e) and the row's maximum m:
-//   t = c (x - m),  e = 2^t,  s = sum e,  w = sum e t
-//   lse = scale m + ln2 log2 s,  log p = ln2 (t - log2 s),  H = ln2 (log2 s - w / s)
+// All are bound by HBM.  In units of log2, with c = scale log2(e) and a reference r near
+// the row's maximum:
+//   t = c (x - r),  e = 2^t,  s = sum e,  w = sum e t
+//   lse = scale r + ln2 log2 s,  log p = ln2 (t - log2 s),  H = ln2 (log2 s - w / s)
 //   d L / d x = scale (g ([target] - p) - h p (log p + H))
 //             = e (A + B t) + scale g [target]
-// One pass finds m, s and w: each thread keeps the maximum of what it has seen and
-// scales its sums when that rises (rarely, after the first values); the threads'
-// sums meet at the common maximum.  The difference comes first (one more instruction
-// for two values than c x - c m), so a log probability is as exact at logits of a
+// One pass finds r, s and w.  A thread's reference is the maximum of the first values
+// that it sees and stays until one exceeds it by more than 2^8 in e: raising it at every
+// new maximum costs a warp its 20 instructions at nearly every vector, since some lane
+// has one (4096 rows of 50001: 17.5 instructions a value).  The threads' sums meet at
+// their largest reference.  The difference comes first (one more instruction
+// for two values than c x - c r), so a log probability is as exact at logits of a
 // thousand as at logits of one, and logits of the type's lowest value do not overflow.
 //
-// A row is taken by 1, 4 or 16 warps by its width; rows that are few or long are
+// A row is taken by 1, 4 or 8 warps by its width; rows that are few or long are
 // split over a cluster's CTAs, which meet through shared memory.  Rows start
 // anywhere: the elements before the first and after the last 16-byte boundary are
 // taken one by one.  The pass that also writes the gradient keeps the row in shared
@@ -72,20 +75,26 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// A vector of 16 bytes, or one element where rows of x and dx lie differently.
-template <typename T, int VEC>
-__device__ __forceinline__ float raw_max(const Raw<T, VEC>& r, const float* f) {
-  float m = f[0];
+// The largest value of n vectors of 16 bytes (or of one element each).
+template <typename T, int VEC, int N>
+__device__ __forceinline__ float raw_max(const Raw<T, VEC>* r) {
+  float m = -INFINITY;
+  if constexpr (sizeof(T) == 2 && VEC == 8) {
+    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(r);
+    __nv_bfloat162 p = h[0];
 #pragma unroll
-  for (int i = 1; i < VEC; ++i) m = fmaxf(m, f[i]);
+    for (int i = 1; i < 4 * N; ++i) p = __hmax2(p, h[i]);
+    m = fmaxf(__low2float(p), __high2float(p));
+  } else {
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      float f[VEC];
+      r[k].get(f);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) m = fmaxf(m, f[i]);
+    }
+  }
   return m;
-}
-template <>
-__device__ __forceinline__ float raw_max<__nv_bfloat16, 8>(const Raw<__nv_bfloat16, 8>& r,
-                                                           const float*) {
-  const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&r.v);
-  const __nv_bfloat162 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
-  return fmaxf(__low2float(m), __high2float(m));
 }
 
 // Where a row's elements lie: `head` before the first whole vector, `vecs` vectors,
@@ -107,49 +116,90 @@ struct Cut {
   }
 };
 
-// Running maximum and sums of a thread.
+// Reference and sums of a thread (and its maximum, where the top values are wanted).
+constexpr float kRise = 8.f;
 template <bool ENT>
 struct Sums {
-  float m = -INFINITY, ref = 0.f;  // maximum; what is taken off (0 while there is none)
+  float ref = -INFINITY;  // none yet
+  float limit = -INFINITY, off = 0.f, most = -INFINITY;
   float2 s = make_float2(0.f, 0.f), w = s;
   __device__ void raise(float to, float c) {
-    if (m > -INFINITY) scale((m - to) * c);
-    m = ref = to;
+    if (ref > -INFINITY) scale((ref - to) * c);
+    ref = to;
+    limit = to + kRise / c;
+    off = -to;
   }
-  // the sums at a maximum higher by -by
+  // the sums at a reference higher by -by
   __device__ void scale(float by) {
     const float a = ex2(by);
     if (ENT) {
-      // a sum of zero has no terms to shift (by may be -infinity)
-      w.x = s.x > 0.f ? a * fmaf(s.x, by, w.x) : w.x * a;
-      w.y = s.y > 0.f ? a * fmaf(s.y, by, w.y) : w.y * a;
-      if (a == 0.f) w.x = w.y = 0.f;
+      w.x = a * fmaf(s.x, by, w.x);
+      w.y = a * fmaf(s.y, by, w.y);
+      if (a == 0.f) w.x = w.y = 0.f;  // by may be -infinity
     }
     s.x *= a;
     s.y *= a;
   }
-  template <int VEC>
-  __device__ void add(const float* f, float top, float c) {
-    if (top > m) raise(top, c);
-    if (VEC == 1) {
-      const float t = (f[0] - ref) * c, e = ex2(t);
-      s.x += e;
-      if (ENT) w.x = fmaf(e, fmaxf(t, -256.f), w.x);
-    }
-    const float2 cc = make_float2(c, c), off = make_float2(-ref, -ref);
+  __device__ void one(float f, float c) {
+    if (f > limit) raise(f, c);
+    most = fmaxf(most, f);
+    const float t = (f + off) * c, e = ex2(t);
+    s.x += e;
+    if (ENT) w.x = fmaf(e, fmaxf(t, -256.f), w.x);
+  }
+  template <typename T, int VEC, int N>
+  __device__ __forceinline__ void add(const Raw<T, VEC>* r, float c) {
+    const float top = raw_max<T, VEC, N>(r);
+    if (top > limit) raise(top, c);
+    most = fmaxf(most, top);
+    const float2 cc = make_float2(c, c), oo = make_float2(off, off);
 #pragma unroll
-    for (int i = 0; i + 1 < VEC; i += 2) {
-      float2 t = __fmul2_rn(__fadd2_rn(make_float2(f[i], f[i + 1]), off), cc);
-      const float2 e = make_float2(ex2(t.x), ex2(t.y));
-      s = __fadd2_rn(s, e);
-      if (ENT) {
-        t.x = fmaxf(t.x, -256.f);  // 0 times -infinity
-        t.y = fmaxf(t.y, -256.f);
-        w = __ffma2_rn(e, t, w);
+    for (int k = 0; k < N; ++k) {
+      float f[VEC];
+      r[k].get(f);
+      if (VEC == 1) {
+        const float t = (f[0] + off) * c, e = ex2(t);
+        s.x += e;
+        if (ENT) w.x = fmaf(e, fmaxf(t, -256.f), w.x);
+      }
+#pragma unroll
+      for (int i = 0; i + 1 < VEC; i += 2) {
+        float2 t = __fmul2_rn(__fadd2_rn(make_float2(f[i], f[i + 1]), oo), cc);
+        const float2 e = make_float2(ex2(t.x), ex2(t.y));
+        s = __fadd2_rn(s, e);
+        if (ENT) {
+          t.x = fmaxf(t.x, -256.f);  // 0 times -infinity
+          t.y = fmaxf(t.y, -256.f);
+          w = __ffma2_rn(e, t, w);
+        }
       }
     }
   }
 };
+
+// Elements of one vector of the gradient: e (A + B t).
+template <int VEC, bool ENT>
+__device__ __forceinline__ void grad_of(float* f, float off, float c, float A, float B) {
+  if (VEC == 1) {
+    const float t = (f[0] + off) * c;
+    f[0] = ex2(t) * (ENT ? fmaf(B, fmaxf(t, -256.f), A) : A);
+  }
+  const float2 cc = make_float2(c, c), oo = make_float2(off, off), aa = make_float2(A, A),
+               bb = make_float2(B, B);
+#pragma unroll
+  for (int i = 0; i + 1 < VEC; i += 2) {
+    float2 t = __fmul2_rn(__fadd2_rn(make_float2(f[i], f[i + 1]), oo), cc);
+    float2 e = make_float2(ex2(t.x), ex2(t.y));
+    if (ENT) {
+      t.x = fmaxf(t.x, -256.f);
+      t.y = fmaxf(t.y, -256.f);
+      e = __fmul2_rn(e, __ffma2_rn(bb, t, aa));
+    } else {
+      e = __fmul2_rn(e, aa);
+    }
+    f[i] = e.x, f[i + 1] = e.y;
+  }
+}
 
 template <int W>
 __device__ __forceinline__ float team_max(float v, float2 (*red)[32]) {
@@ -224,7 +274,7 @@ struct TopShared {
   int groups[kGroups];
   uint64_t list[kList];
   uint64_t best[kMaxTop];
-  uint64_t red[16];
+  uint64_t red[8];
   uint32_t bound;
   int found, chosen;
 };
@@ -338,7 +388,7 @@ __global__ void __launch_bounds__(W == 1 ? 32 * kRowsPerBlock : 32 * W) logp_ker
   __shared__ float meet[3];
   __shared__ typename std::conditional<TOP, TopShared, int>::type top_shared;
   const int tid = W == 1 ? threadIdx.x & 31 : threadIdx.x;
-  const int rank = W == 16 ? blockIdx.x % p.cluster : 0;
+  const int rank = W == 8 ? blockIdx.x % p.cluster : 0;
   const int64_t row = W == 1 ? (int64_t)blockIdx.x * kRowsPerBlock + (threadIdx.x >> 5)
                              : (int64_t)blockIdx.x / p.cluster;
   pdl_wait();
@@ -348,7 +398,7 @@ __global__ void __launch_bounds__(W == 1 ? 32 * kRowsPerBlock : 32 * W) logp_ker
   Cut cut;
   cut.set<T, VEC>(x, p.V);
   int first = 0, last = cut.vecs;
-  if (W == 16 && p.cluster > 1) {
+  if (W == 8 && p.cluster > 1) {
     const int per = (cut.vecs + p.cluster - 1) / p.cluster;
     first = min(rank * per, cut.vecs);
     last = min(first + per, cut.vecs);
@@ -366,52 +416,66 @@ __global__ void __launch_bounds__(W == 1 ? 32 * kRowsPerBlock : 32 * W) logp_ker
     }
     if (target >= 0) reinterpret_cast<const Raw<T, 1>*>(x)[target].get(&picked);
   }
+  const float c = p.c;
 
   Sums<ENT> sum;
   const int edges = rank == 0 ? cut.edges : 0;
   float lone = 0.f;
   if (tid < edges) {
     reinterpret_cast<const Raw<T, 1>*>(x)[cut.edge<VEC>(tid)].get(&lone);
-    sum.template add<1>(&lone, lone, p.c);
+    sum.one(lone, c);
   }
-  int kept = 0;
-  for (int v = first + tid; v < last; v += kAhead * G) {
+  const int staged = GRAD ? p.staged : 0;
+  int kept = 0, v = first + tid;
+  for (; v + (kAhead - 1) * G < last; v += kAhead * G) {
     R r[kAhead];
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k)
-      if (v + k * G < last) r[k] = body[v + k * G];
+    for (int k = 0; k < kAhead; ++k) r[k] = body[v + k * G];
+    sum.template add<T, VEC, kAhead>(r, c);
+    if (GRAD) {
+      if (kept + kAhead <= staged) {
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      if (v + k * G >= last) break;
-      float f[VEC];
-      r[k].get(f);
-      sum.template add<VEC>(f, raw_max<T, VEC>(r[k], f), p.c);
-      if (GRAD) {
-        if (kept < p.staged) stage[kept * stage_step] = r[k];
-        ++kept;
+        for (int k = 0; k < kAhead; ++k) stage[(kept + k) * stage_step] = r[k];
+      } else {
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+          if (kept + k < staged) stage[(kept + k) * stage_step] = r[k];
       }
+      kept += kAhead;
     }
   }
+  if (v < last) {
+    R r[kAhead - 1];
+#pragma unroll
+    for (int k = 0; k < kAhead - 1; ++k)
+      if (v + k * G < last) r[k] = body[v + k * G];
+#pragma unroll
+    for (int k = 0; k < kAhead - 1; ++k)
+      if (v + k * G < last) {
+        sum.template add<T, VEC, 1>(r + k, c);
+        if (GRAD && kept + k < staged) stage[(kept + k) * stage_step] = r[k];
+      }
+  }
   // the team's, then the cluster's
-  float most = team_max<W>(sum.m, red);
-  if (sum.m > -INFINITY && sum.m != most) sum.scale((sum.m - most) * p.c);
+  float most = team_max<W>(sum.ref, red);
+  if (sum.ref > -INFINITY && sum.ref != most) sum.scale((sum.ref - most) * c);
   float2 sw = team_sum<W>(make_float2(sum.s.x + sum.s.y, sum.w.x + sum.w.y), red);
-  if (W == 16 && p.cluster > 1) {
+  if (W == 8 && p.cluster > 1) {
     if (tid == 0) meet[0] = most, meet[1] = sw.x, meet[2] = sw.y;
     cluster_meet();
     const int lane = tid & 31;
     Sums<ENT> one;
     if (lane < p.cluster) {
-      one.m = peer_float(meet, lane);
+      one.ref = peer_float(meet, lane);
       one.s.x = peer_float(meet + 1, lane);
       one.w.x = peer_float(meet + 2, lane);
     }
-    most = one.m;
+    most = one.ref;
 #pragma unroll
     for (int o = kMaxCluster / 2; o; o >>= 1)
       most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
     most = __shfl_sync(0xffffffffu, most, 0);
-    if (one.m > -INFINITY && one.m != most) one.scale((one.m - most) * p.c);
+    if (one.ref > -INFINITY && one.ref != most) one.scale((one.ref - most) * c);
 #pragma unroll
     for (int o = kMaxCluster / 2; o; o >>= 1) {
       one.s.x += __shfl_xor_sync(0xffffffffu, one.s.x, o);
@@ -433,8 +497,8 @@ __global__ void __launch_bounds__(W == 1 ? 32 * kRowsPerBlock : 32 * W) logp_ker
   }
 
   if constexpr (TOP) {
-    top_of_slice<T, VEC, W>(top_shared, x, cut, first, last, edges, sum.m, p.top);
-    if (W == 16 && p.cluster > 1) {
+    top_of_slice<T, VEC, W>(top_shared, x, cut, first, last, edges, sum.most, p.top);
+    if (W == 8 && p.cluster > 1) {
       cluster_meet();
       if (rank == 0) {
         const int n = p.cluster * p.top;
@@ -468,35 +532,36 @@ __global__ void __launch_bounds__(W == 1 ? 32 * kRowsPerBlock : 32 * W) logp_ker
     const float inv = 1.f / sw.x;
     const float A = -p.scale * fmaf(h, ent - kLn2 * logs, g) * inv;
     const float B = -p.scale * kLn2 * h * inv;
-    auto grad = [&](float f) {
-      const float t = (f - ref) * p.c;
-      return none ? 0.f : ex2(t) * (ENT ? fmaf(B, fmaxf(t, -256.f), A) : A);
-    };
     if (tid < edges) {
       const int i = cut.edge<VEC>(tid);
-      float d = grad(lone);
-      if (i == target && !none) d = fmaf(p.scale, g, d);
+      float d = lone;
+      grad_of<1, ENT>(&d, -ref, c, A, B);
+      if (i == target) d = fmaf(p.scale, g, d);
+      if (none) d = 0.f;
       reinterpret_cast<Raw<T, 1>*>(dx)[i].set(&d);
     }
     const int there = target >= cut.head ? (target - cut.head) / VEC : -1;
     int i = 0;
-    for (int v = first + tid; v < last; v += G, ++i) {
-      const R r = i < p.staged ? stage[i * stage_step] : body[v];
-      float f[VEC];
-      r.get(f);
+    if (none) {
+      for (int v = first + tid; v < last; v += G) out[v] = R{};
+    } else {
+      for (int v = first + tid; v < last; v += G, ++i) {
+        const R r = i < staged ? stage[i * stage_step] : body[v];
+        float f[VEC];
+        r.get(f);
+        grad_of<VEC, ENT>(f, -ref, c, A, B);
+        if (v == there) {
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) f[j] = grad(f[j]);
-      if (v == there && !none) {
-#pragma unroll
-        for (int j = 0; j < VEC; ++j)
-          if (cut.head + v * VEC + j == target) f[j] = fmaf(p.scale, g, f[j]);
+          for (int j = 0; j < VEC; ++j)
+            if (cut.head + v * VEC + j == target) f[j] = fmaf(p.scale, g, f[j]);
+        }
+        R o;
+        o.set(f);
+        out[v] = o;
       }
-      R o;
-      o.set(f);
-      out[v] = o;
     }
   }
-  if (W == 16 && p.cluster > 1) cluster_meet();  // no CTA leaves while another reads its shares
+  if (W == 8 && p.cluster > 1) cluster_meet();  // no CTA leaves while another reads its shares
 }
 
 // The gradient alone, from the row's log-sum and entropy: a block a piece of a row
@@ -586,7 +651,7 @@ cudaError_t go(LogpArgs& a, cudaStream_t st) {
   const int64_t rows = W == 1 ? (a.T + kRowsPerBlock - 1) / kRowsPerBlock : a.T;
   a.cluster = 1;
   const int64_t vecs = a.V / VEC + 1;  // of a row, at most
-  if (W == 16) {
+  if (W == 8) {
     // CTAs for every SM, but no less than four vectors a thread of each; with a
     // gradient, as many as keep a slice to 64 KB, three CTAs an SM
     while (a.cluster < kMaxCluster && vecs / (2 * a.cluster) >= 4 * threads &&
@@ -624,7 +689,7 @@ cudaError_t by_width(LogpArgs& a, cudaStream_t st) {
   if constexpr (!TOP)
     if (vecs <= 64) return go<T, VEC, 1, ENT, TOP, GRAD>(a, st);
   return vecs <= 512 ? go<T, VEC, 4, ENT, TOP, GRAD>(a, st)
-                     : go<T, VEC, 16, ENT, TOP, GRAD>(a, st);
+                     : go<T, VEC, 8, ENT, TOP, GRAD>(a, st);
 }
 
 template <typename T>
