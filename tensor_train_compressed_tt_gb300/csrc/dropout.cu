@@ -40,8 +40,11 @@ struct DropRow<float> {
   __device__ void set(const float* f) { a.set(f), b.set(f + 4); }
 };
 
-// A thread takes groups of eight elements, a grid apart; the next one is loaded
-// while the generator works on the current one.
+// A thread takes kSide groups of eight elements a block's width apart, then the grid's
+// next ones, which are loaded while the generator works on the current ones.  One group
+// at a time had 16 KB of loads in flight an SM: 32768 x 4096 bf16 102 us.
+constexpr int kSide = 2;
+
 template <typename T, bool RES>
 __global__ void __launch_bounds__(kThreads) drop_kernel(int64_t n, const T* x, const T* res, T* y,
                                                         DropArgs d) {
@@ -49,28 +52,38 @@ __global__ void __launch_bounds__(kThreads) drop_kernel(int64_t n, const T* x, c
   pdl_trigger();
   DropKey key;
   key.read(d);
-  const int64_t step = (int64_t)gridDim.x * kThreads, groups = n >> 3;
-  int64_t g = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  DropRow<T> rx, rr;
-  if (g < groups) {
-    rx.load(x + 8 * g);
-    if (RES) rr.load(res + 8 * g);
-  }
-  for (; g < groups; g += step) {
-    float f[8], r[8];
-    rx.get(f);
-    if (RES) rr.get(r);
-    if (g + step < groups) {
-      rx.load(x + 8 * (g + step));
-      if (RES) rr.load(res + 8 * (g + step));
-    }
-    drop<8>(key, d, 8 * g, f);
-    if (RES)
+  const int64_t step = (int64_t)gridDim.x * kThreads * kSide, groups = n >> 3;
+  int64_t first = (int64_t)blockIdx.x * kThreads * kSide + threadIdx.x;
+  DropRow<T> rx[kSide], rr[RES ? kSide : 1];
+  auto fetch = [&](int64_t g) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] += r[i];
-    DropRow<T> o;
-    o.set(f);
-    o.store(y + 8 * g);
+    for (int k = 0; k < kSide; ++k)
+      if (g + k * kThreads < groups) {
+        rx[k].load(x + 8 * (g + k * kThreads));
+        if constexpr (RES) rr[k].load(res + 8 * (g + k * kThreads));
+      }
+  };
+  fetch(first);
+  for (; first < groups; first += step) {
+    float f[kSide][8], r[RES ? kSide : 1][8];
+    int64_t group[kSide];
+#pragma unroll
+    for (int k = 0; k < kSide; ++k) {
+      rx[k].get(f[k]);
+      if constexpr (RES) rr[k].get(r[k]);
+      group[k] = first + k * kThreads;
+    }
+    if (first + step < groups) fetch(first + step);
+    uint4 w[kSide];
+    key.words(group, d.site, w);
+#pragma unroll
+    for (int k = 0; k < kSide; ++k) {
+      drop<8>(w[k], d, 0, f[k]);
+      if constexpr (RES) add<8>(f[k], r[k], f[k]);
+      DropRow<T> o;
+      o.set(f[k]);
+      if (group[k] < groups) o.store(y + 8 * group[k]);
+    }
   }
   // the last elements, fewer than eight
   if (blockIdx.x == 0 && threadIdx.x < (n & 7)) {
@@ -87,7 +100,7 @@ __global__ void __launch_bounds__(kThreads) drop_kernel(int64_t n, const T* x, c
 template <typename T>
 cudaError_t drop_go(int64_t n, const void* x, const void* res, void* y, const DropArgs& d,
                     cudaStream_t st) {
-  const int64_t need = ((n >> 3) + kThreads - 1) / kThreads;
+  const int64_t need = ((n >> 3) + kThreads * kSide - 1) / (kThreads * kSide);
   const int64_t most = (int64_t)device_sms() * 8;
   const dim3 grid((unsigned)(need < 1 ? 1 : need < most ? need : most));
   const T *tx = static_cast<const T*>(x), *tr = static_cast<const T*>(res);

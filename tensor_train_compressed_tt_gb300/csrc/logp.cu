@@ -22,8 +22,8 @@
 // memory in between (each thread its own values), so it reads it from HBM once.
 //
 // Top alternatives: the maxima of 128 groups of threads give a bound (the k-th
-// largest of them: at least k values are not below it); the few groups that reach
-// it are read again, the values not below the bound are ranked by (value, lowest
+// largest of them, to 16 bits: at least k values are not below it); the few groups that
+// reach it are read again, the values not below the bound are ranked by (value, lowest
 // index).  Where ties make them too many, k rounds over the row take them in order.
 #include <cmath>
 #include <new>
@@ -292,20 +292,33 @@ __device__ void top_of_slice(TopShared& sh, const T* x, const Cut& cut, int firs
 #pragma unroll
   for (int o = SIDE / 2; o; o >>= 1) key = max(key, __shfl_xor_sync(0xffffffffu, key, o));
   if (tid % SIDE == 0) sh.keys[tid / SIDE] = key;
-  if (tid == 0) sh.found = sh.chosen = 0;
+  if (tid == 0) sh.found = 0;
   if (tid < k) sh.best[tid] = 0;
   __syncthreads();
-  if (tid < kGroups) {
-    const uint32_t mine = sh.keys[tid];
-    int before = 0;
-    for (int j = 0; j < kGroups; ++j)
-      before += sh.keys[j] > mine || (sh.keys[j] == mine && j < tid);
-    if (before == k - 1) sh.bound = mine;  // one group's rank, k <= kGroups
+  if (warp == 0) {
+    // the largest bound of 16 bits that k groups reach, bit by bit, and those groups
+    uint32_t mine[kGroups / 32], bound = 0;
+#pragma unroll
+    for (int j = 0; j < kGroups / 32; ++j) mine[j] = sh.keys[32 * j + lane];
+#pragma unroll
+    for (int bit = 31; bit >= 16; --bit) {
+      const uint32_t higher = bound | 1u << bit;
+      int n = 0;
+#pragma unroll
+      for (int j = 0; j < kGroups / 32; ++j) n += mine[j] >= higher;
+      if (__reduce_add_sync(0xffffffffu, n) >= k) bound = higher;
+    }
+    int n = 0;
+#pragma unroll
+    for (int j = 0; j < kGroups / 32; ++j) {
+      const unsigned reach = __ballot_sync(0xffffffffu, mine[j] >= bound);
+      if (mine[j] >= bound) sh.groups[n + __popc(reach & ((1u << lane) - 1))] = 32 * j + lane;
+      n += __popc(reach);
+    }
+    if (lane == 0) sh.bound = bound, sh.chosen = n;
   }
   __syncthreads();
   const uint32_t bound = sh.bound;
-  if (tid < kGroups && sh.keys[tid] >= bound) sh.groups[atomicAdd(&sh.chosen, 1)] = tid;
-  __syncthreads();
   auto offer = [&](float f, int i) {
     const uint32_t at = key_of(f);
     if (at < bound) return;

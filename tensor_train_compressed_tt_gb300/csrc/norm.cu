@@ -105,6 +105,42 @@ struct NormBwdArgs {
   void* dres;
 };
 
+// The generator's words for a thread's CH chunks of VEC elements, those at
+// (c G + tid) VEC of a row that starts at element `first`.
+template <int VEC, int CH, int G>
+__device__ __forceinline__ void keep_words(const DropKey& key, const DropArgs& d, int64_t first,
+                                           int tid, uint4 (&w)[CH]) {
+  int64_t group[CH];
+  if constexpr (VEC == 4) {
+    // Two lanes side by side hold the halves of a group (rows start at multiples of
+    // four elements: where at one of eight, the even lane holds the first half).
+    // Of two chunks each lane computes one and they exchange what the other needs.
+    if (first % 8 == 0) {
+      const bool odd = tid & 1;
+#pragma unroll
+      for (int c = 0; c < CH; c += 2) {
+        const int at = c + 1 < CH && odd ? c + 1 : c;
+        int64_t one[1] = {(first + (int64_t)(at * G + tid) * VEC) >> 3};
+        uint4 x[1];
+        key.words(one, d.site, x);
+        if (c + 1 < CH) {
+          // the even lane keeps the first half of its chunk's words and sends the rest
+          const uint32_t a = __shfl_xor_sync(0xffffffffu, odd ? x[0].x : x[0].z, 1);
+          const uint32_t b = __shfl_xor_sync(0xffffffffu, odd ? x[0].y : x[0].w, 1);
+          w[c] = odd ? make_uint4(0, 0, a, b) : x[0];
+          w[c + 1 < CH ? c + 1 : c] = odd ? x[0] : make_uint4(a, b, 0, 0);
+        } else {
+          w[c] = x[0];
+        }
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < CH; ++c) group[c] = (first + (int64_t)(c * G + tid) * VEC) >> 3;
+  key.words(group, d.site, w);
+}
+
 constexpr int kRowWarps = 8;  // rows side by side in a block when a warp holds a row
 
 // A group of W warps holds ROWS rows of up to 32 W VEC CH values; groups stride
@@ -155,6 +191,8 @@ __global__ void __launch_bounds__(W == 1 ? 32 * kRowWarps : 32 * W)
     float v[ROWS][CH * VEC], part[ROWS], mean[ROWS], rstd[ROWS];
 #pragma unroll
     for (int k = 0; k < ROWS; ++k) {
+      uint4 keep[DROP ? CH : 1];
+      if constexpr (DROP) keep_words<VEC, CH, G>(key, p.drop, (row + k * step) * N, tid, keep);
       float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
@@ -162,7 +200,7 @@ __global__ void __launch_bounds__(W == 1 ? 32 * kRowWarps : 32 * W)
         if (j < N) {
           float* u = v[k] + c * VEC;
           rx[k][c].get(u);
-          if (DROP) drop<VEC>(key, p.drop, (row + k * step) * N + j, u);
+          if (DROP) drop<VEC>(keep[DROP ? c : 0], p.drop, (row + k * step) * N + j, u);
           if (RES && (!DROP || p.res)) {
             float a[VEC];
             rr[k][c].get(a);
@@ -301,6 +339,8 @@ __global__ void __launch_bounds__(32 * W * bwd_groups(W), W <= 8 ? 2 : 1)
     fill<VEC>(-(t.x / p.n), a);
     fill<VEC>(-(t.y / p.n), b);
     T* dx = static_cast<T*>(p.dx) + row * N;
+    uint4 keep[DROP ? CH : 1];
+    if constexpr (DROP) keep_words<VEC, CH, G>(key, p.drop, row * N, tid, keep);
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int j = (c * G + tid) * VEC;
@@ -321,7 +361,7 @@ __global__ void __launch_bounds__(32 * W * bwd_groups(W), W <= 8 ? 2 : 1)
             o.set(f);
             *reinterpret_cast<R*>(static_cast<T*>(p.dres) + row * N + j) = o;
           }
-          drop<VEC>(key, p.drop, row * N + j, f);
+          drop<VEC>(keep[DROP ? c : 0], p.drop, row * N + j, f);
         }
         o.set(f);
         *reinterpret_cast<R*>(dx + j) = o;

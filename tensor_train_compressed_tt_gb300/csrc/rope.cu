@@ -43,7 +43,8 @@ constexpr int kWarps = 8;       // warps a block
 struct RopeArgs {
   int64_t T;
   int heads, kv, dim, rot;
-  int group;       // lanes of a head: a power of two
+  int group;       // lanes of a head
+  int side;        // heads side by side in a warp: 32 / group
   int chunks;      // chunks of a head: the rotated ones, then the rest
   int turned;      // rotated chunks
   int passes;      // warps of a token
@@ -188,6 +189,20 @@ __device__ __forceinline__ float inverse_root(float x) {
   return fmaf(0.5f * r, fmaf(-x * r, r, 1.f), r);
 }
 
+// The sum over the lanes of each head; lane i of it is `i`.  A power of two by
+// exchanges, else from the upper lanes to the lower, then from the first to all.
+__device__ __forceinline__ float head_sum(float v, int group, int i) {
+  if ((group & (group - 1)) == 0) {
+    for (int o = group >> 1; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+  }
+  for (int o = group > 16 ? 16 : group > 8 ? 8 : group > 4 ? 4 : 2; o; o >>= 1) {
+    const float u = __shfl_down_sync(0xffffffffu, v, o);
+    if (i + o < group && i < o) v += u;
+  }
+  return __shfl_sync(0xffffffffu, v, (threadIdx.x & 31) - i);
+}
+
 template <typename T, int P, int CH, bool PAIRS, bool GRAD>
 __global__ void __launch_bounds__(32 * kWarps, GRAD ? 2 : 3)
     rope_kernel(const __grid_constant__ RopeArgs p) {
@@ -207,40 +222,42 @@ __global__ void __launch_bounds__(32 * kWarps, GRAD ? 2 : 3)
   // this lane's head and channels
   const int64_t w = (int64_t)blockIdx.x * kWarps + warp;
   const int64_t step = (int64_t)gridDim.x * kWarps / p.passes;
-  int h = (int)(w % p.passes) * (32 / p.group) + lane / p.group;
+  const int beside = lane / p.group, li = lane - beside * p.group;
+  int h = (int)(w % p.passes) * p.side + beside;
   int64_t t = w / p.passes;
   if (t >= step) t = p.T;
   const int which = h < p.heads ? 0 : h < p.heads + p.kv ? 1 : 2;
   h -= which == 0 ? 0 : which == 1 ? p.heads : p.heads + p.kv;
-  const bool here = which < 2 ? which == 0 || h < p.kv : p.values && h < p.kv;
+  const bool here = beside < p.side && (which == 0 || (h < p.kv && (which == 1 || p.values)));
   Place<T, P, PAIRS> at[CH];
   Pairs<P> g[CH];
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
-    at[c].set(p, c * 32 + (lane & (p.group - 1)));
+    at[c].set(p, c * 32 + li);
     if (!here) at[c].has = at[c].has2 = false;
     if (p.norm) at[c].weights(which == 0 ? p.gq : p.gk, g[c]);
   }
-  const int share = (lane & (p.group - 1)) * P;  // its pairs in the table of angles
+  const int share = li * P;  // its pairs in the table of angles
   // where the head starts in the tensors' first row
-  const Heads from = which == 0 ? p.q : which == 1 ? p.k : p.v;
-  const Heads into = which == 0 ? p.qo : which == 1 ? p.ko : p.vo;
-  const Heads grad = which == 0 ? p.dq : p.dk;
   const bool reads = !GRAD || p.norm;
-  const T* x = reads ? from.at<T>(t, here ? h : 0) : nullptr;
-  const T* d = GRAD ? grad.at<T>(t, here ? h : 0) : nullptr;
-  T* y = into.at<T>(0, here ? h : 0);
+  if (!here) h = 0;
+  const T* x = which == 0 ? p.q.at<T>(t, h) : which == 1 ? p.k.at<T>(t, h) : p.v.at<T>(t, h);
+  const int64_t step_in = step * (which == 0 ? p.q.row : which == 1 ? p.k.row : p.v.row);
+  const T* d = which == 0 ? p.dq.at<T>(t, h) : p.dk.at<T>(t, h);
+  const int64_t step_grad = step * (which == 0 ? p.dq.row : p.dk.row);
+  T* y = which == 0 ? p.qo.at<T>(0, h) : which == 1 ? p.ko.at<T>(0, h) : p.vo.at<T>(0, h);
+  const int64_t row_out = which == 0 ? p.qo.row : which == 1 ? p.ko.row : p.vo.row;
 
   R xu[CH] = {}, xv[CH] = {}, du[GRAD ? CH : 1] = {}, dv[GRAD ? CH : 1] = {};
-  int64_t pos = 0, row = 0;
+  int pos = 0, row = 0;
   auto fetch = [&] {
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       if (reads) at[c].load(x, xu[c], xv[c]);
       if constexpr (GRAD) at[c].load(d, du[c], dv[c]);
     }
-    pos = p.pos ? p.pos[t] : t;
-    row = !GRAD && p.rows && which > 0 ? p.rows[t] : t;
+    pos = p.pos ? p.pos[t] : (int)t;
+    row = !GRAD && p.rows && which > 0 ? p.rows[t] : (int)t;
   };
   Pairs<P> sum[CH];
 #pragma unroll
@@ -259,7 +276,7 @@ __global__ void __launch_bounds__(32 * kWarps, GRAD ? 2 : 3)
         kept = false;
       }
     }
-    T* out = y + (kept ? row : 0) * into.row;
+    T* out = y + (int64_t)(kept ? row : 0) * row_out;
     Pairs<P> u[CH], e[GRAD ? CH : 1];
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
@@ -272,8 +289,8 @@ __global__ void __launch_bounds__(32 * kWarps, GRAD ? 2 : 3)
       }
     }
     t += step;
-    x += step * from.row;
-    if constexpr (GRAD) d += step * grad.row;
+    x += step_in;
+    if constexpr (GRAD) d += step_grad;
     if (t < p.T) fetch();
 
     if constexpr (!GRAD) {
@@ -282,7 +299,7 @@ __global__ void __launch_bounds__(32 * kWarps, GRAD ? 2 : 3)
 #pragma unroll
         for (int c = 0; c < CH; ++c) mul_up<P>(s2, u[c].a, u[c].a), mul_up<P>(s2, u[c].b, u[c].b);
         float s = s2.x + s2.y;
-        for (int o = p.group >> 1; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        s = head_sum(s, p.group, li);
         float r[P];
         fill<P>(inverse_root(fmaf(s, p.inv_n, p.eps)), r);
 #pragma unroll
@@ -315,10 +332,8 @@ __global__ void __launch_bounds__(32 * kWarps, GRAD ? 2 : 3)
           mul<P>(e[c].b, u[c].b, gu), mul_up<P>(m2, gu, g[c].b);
         }
         float s = s2.x + s2.y, m = m2.x + m2.y;
-        for (int o = p.group >> 1; o; o >>= 1) {
-          s += __shfl_xor_sync(0xffffffffu, s, o);
-          m += __shfl_xor_sync(0xffffffffu, m, o);
-        }
+        s = head_sum(s, p.group, li);
+        m = head_sum(m, p.group, li);
         const float one = inverse_root(fmaf(s, p.inv_n, p.eps));
         float r[P], less[P];
         fill<P>(one, r);
@@ -346,13 +361,14 @@ __global__ void __launch_bounds__(32 * kWarps, GRAD ? 2 : 3)
       float u[2 * P];
       Place<T, P, PAIRS>::join(sum[c], u, u + P);
       Place<T, P, PAIRS> own;  // the channels, whether or not this lane's head exists
-      own.set(p, c * 32 + (lane & (p.group - 1)));
+      own.set(p, c * 32 + li);
 #pragma unroll
       for (int j = 0; j < 2 * P; ++j) {
         float a = here && which == 0 ? u[j] : 0.f, b = here && which == 1 ? u[j] : 0.f;
-        for (int o = p.group; o < 32; o <<= 1) {
-          a += __shfl_xor_sync(0xffffffffu, a, o);
-          b += __shfl_xor_sync(0xffffffffu, b, o);
+        for (int o = p.group; o < 32; o <<= 1) {  // the first of each two, four, .. heads
+          const float x = __shfl_down_sync(0xffffffffu, a, o);
+          const float y = __shfl_down_sync(0xffffffffu, b, o);
+          if (lane + o < 32) a += x, b += y;
         }
         if (lane < p.group && (j < P ? own.has : own.has2)) {
           const int i = j < P ? own.at + j : own.at2 + j - P;
@@ -405,7 +421,7 @@ int64_t grad_blocks(int64_t T, int64_t passes) {
 // For any number of heads side by side in a warp: no fewer warps a token than this.
 int64_t most_grad_blocks(const RopePlan& R, int64_t T) {
   int64_t most = 1;
-  for (int side = 1; side <= 32; side *= 2) {
+  for (int side = 1; side <= 32; ++side) {
     const int64_t b = grad_blocks(T, (R.heads + R.kv + side - 1) / side);
     if (b > most) most = b;
   }
@@ -430,8 +446,7 @@ bool fits(const RopePlan& R, const RopeArgs& a, int P, bool grad) {
 
 template <typename T, int P, int CH, bool PAIRS, bool GRAD>
 cudaError_t go(RopeArgs& a, int64_t* blocks, cudaStream_t st) {
-  const int side = 32 / a.group;
-  a.passes = (a.heads + a.kv + (a.values ? a.kv : 0) + side - 1) / side;
+  a.passes = (a.heads + a.kv + (a.values ? a.kv : 0) + a.side - 1) / a.side;
   *blocks = GRAD ? grad_blocks(a.T, a.passes) : blocks_of(a.T, a.passes, kPerSm);
   return launch_ex(rope_kernel<T, P, CH, PAIRS, GRAD>, dim3((unsigned)*blocks),
                    dim3(32 * kWarps), 0, st, false, a);
@@ -442,7 +457,11 @@ cudaError_t pick(const RopePlan& R, RopeArgs& a, int64_t* blocks, cudaStream_t s
   auto shape = [&](int P) {
     a.turned = R.rot / 2 / P;
     a.chunks = a.turned + (R.dim - R.rot + 2 * P - 1) / (2 * P);
+    // a power of two, whose sums take fewer exchanges, unless more heads fit without
+    // it (4099 x 20 heads of 80 in f32, ten lanes a head: 29.3 us by sixteens)
     a.group = a.chunks > 32 ? 32 : pow2_above(a.chunks);
+    if (a.chunks <= 32 && 32 / a.chunks > 32 / a.group) a.group = a.chunks;
+    a.side = 32 / a.group;
   };
   if constexpr (sizeof(T) == 2) {
     if (fits(R, a, 8, GRAD)) {
