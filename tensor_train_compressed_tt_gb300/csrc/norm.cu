@@ -602,9 +602,11 @@ cudaError_t fwd_pick(const NormFwdArgs& a, cudaStream_t st) {
 
 template <typename T, int VEC, int CH, int W>
 cudaError_t bwd_go(const NormBwdArgs& a, int64_t blocks, cudaStream_t st) {
-  return launch_ex(a.drop.rng ? norm_bwd_kernel<T, VEC, CH, W, true>
-                              : norm_bwd_kernel<T, VEC, CH, W, false>,
-                   dim3((unsigned)blocks), dim3(32 * W * bwd_groups(W)), 0, st, false, a);
+  const dim3 grid((unsigned)blocks), block(32 * W * bwd_groups(W));
+  if constexpr (VEC < 8)
+    if (!a.drop.rng)
+      return launch_ex(norm_bwd_kernel<T, VEC, CH, W, false>, grid, block, 0, st, false, a);
+  return launch_ex(norm_bwd_kernel<T, VEC, CH, W, true>, grid, block, 0, st, false, a);
 }
 
 template <typename T, int V>
@@ -616,7 +618,7 @@ cudaError_t bwd_pick(const NormBwdArgs& a, int64_t blocks, cudaStream_t st) {
       if (V > 1 && N <= 256) return bwd_go<T, V, 8 / V, 1>(a, blocks, st);
       return bwd_go<T, V, E / V, 1>(a, blocks, st);
     case 2:
-      if (V > 1 && N <= 768) return bwd_go<T, V, 12 / V, 2>(a, blocks, st);
+      if (V > 1 && V < 8 && N <= 768) return bwd_go<T, V, V < 8 ? 12 / V : 1, 2>(a, blocks, st);
       return bwd_go<T, V, E / V, 2>(a, blocks, st);
     case 4: return bwd_go<T, V, E / V, 4>(a, blocks, st);
     case 8: return bwd_go<T, V, E / V, 8>(a, blocks, st);
@@ -762,6 +764,7 @@ static tt_status norm_backward(const tt_plan_t* plan, const tt_plan_t* drop, int
   cudaError_t e;
   if (P.act == TT_DT_BF16)
     e = wide           ? bwd_wide<__nv_bfloat16>(a, blocks, st)
+        : drop && P.N % 8 == 0 ? bwd_pick<__nv_bfloat16, 8>(a, blocks, st)
         : P.N % 4 == 0 ? bwd_pick<__nv_bfloat16, 4>(a, blocks, st)
                        : bwd_pick<__nv_bfloat16, 1>(a, blocks, st);
   else

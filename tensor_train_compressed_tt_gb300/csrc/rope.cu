@@ -191,7 +191,13 @@ __device__ __forceinline__ float inverse_root(float x) {
 
 // The sum over the lanes of each head; lane i of it is `i`.  A power of two by
 // exchanges, else from the upper lanes to the lower, then from the first to all.
+template <int GROUP>
 __device__ __forceinline__ float head_sum(float v, int group, int i) {
+  if (GROUP) {
+#pragma unroll
+    for (int o = GROUP / 2; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+  }
   if ((group & (group - 1)) == 0) {
     for (int o = group >> 1; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
@@ -203,8 +209,13 @@ __device__ __forceinline__ float head_sum(float v, int group, int i) {
   return __shfl_sync(0xffffffffu, v, (threadIdx.x & 31) - i);
 }
 
-template <typename T, int P, int CH, bool PAIRS, bool GRAD>
-__global__ void __launch_bounds__(32 * kWarps, GRAD ? 2 : 3)
+// Blocks of 256 threads that an SM holds, by the registers of a lane's chunk.
+constexpr int kGradPerSm = 2, kPerSm = 3;
+
+// GROUP: the lanes of a head where they are known (16 and 32 bytes a lane of heads of 64
+// and 128), else 0.
+template <typename T, int P, int CH, bool PAIRS, bool GRAD, int GROUP>
+__global__ void __launch_bounds__(32 * kWarps, GRAD ? kGradPerSm : kPerSm)
     rope_kernel(const __grid_constant__ RopeArgs p) {
   using R = Raw<T, P>;
   __shared__ uint64_t turn[kMaxPairs];
@@ -222,13 +233,14 @@ __global__ void __launch_bounds__(32 * kWarps, GRAD ? 2 : 3)
   // this lane's head and channels
   const int64_t w = (int64_t)blockIdx.x * kWarps + warp;
   const int64_t step = (int64_t)gridDim.x * kWarps / p.passes;
-  const int beside = lane / p.group, li = lane - beside * p.group;
-  int h = (int)(w % p.passes) * p.side + beside;
+  const int group = GROUP ? GROUP : p.group, side = GROUP ? 32 / GROUP : p.side;
+  const int beside = lane / group, li = lane - beside * group;
+  int h = (int)(w % p.passes) * side + beside;
   int64_t t = w / p.passes;
   if (t >= step) t = p.T;
   const int which = h < p.heads ? 0 : h < p.heads + p.kv ? 1 : 2;
   h -= which == 0 ? 0 : which == 1 ? p.heads : p.heads + p.kv;
-  const bool here = beside < p.side && (which == 0 || (h < p.kv && (which == 1 || p.values)));
+  const bool here = beside < side && (which == 0 || (h < p.kv && (which == 1 || p.values)));
   Place<T, P, PAIRS> at[CH];
   Pairs<P> g[CH];
 #pragma unroll
@@ -299,7 +311,7 @@ __global__ void __launch_bounds__(32 * kWarps, GRAD ? 2 : 3)
 #pragma unroll
         for (int c = 0; c < CH; ++c) mul_up<P>(s2, u[c].a, u[c].a), mul_up<P>(s2, u[c].b, u[c].b);
         float s = s2.x + s2.y;
-        s = head_sum(s, p.group, li);
+        s = head_sum<GROUP>(s, group, li);
         float r[P];
         fill<P>(inverse_root(fmaf(s, p.inv_n, p.eps)), r);
 #pragma unroll
@@ -332,8 +344,8 @@ __global__ void __launch_bounds__(32 * kWarps, GRAD ? 2 : 3)
           mul<P>(e[c].b, u[c].b, gu), mul_up<P>(m2, gu, g[c].b);
         }
         float s = s2.x + s2.y, m = m2.x + m2.y;
-        s = head_sum(s, p.group, li);
-        m = head_sum(m, p.group, li);
+        s = head_sum<GROUP>(s, group, li);
+        m = head_sum<GROUP>(m, group, li);
         const float one = inverse_root(fmaf(s, p.inv_n, p.eps));
         float r[P], less[P];
         fill<P>(one, r);
@@ -365,12 +377,12 @@ __global__ void __launch_bounds__(32 * kWarps, GRAD ? 2 : 3)
 #pragma unroll
       for (int j = 0; j < 2 * P; ++j) {
         float a = here && which == 0 ? u[j] : 0.f, b = here && which == 1 ? u[j] : 0.f;
-        for (int o = p.group; o < 32; o <<= 1) {  // the first of each two, four, .. heads
+        for (int o = group; o < 32; o <<= 1) {  // the first of each two, four, .. heads
           const float x = __shfl_down_sync(0xffffffffu, a, o);
           const float y = __shfl_down_sync(0xffffffffu, b, o);
           if (lane + o < 32) a += x, b += y;
         }
-        if (lane < p.group && (j < P ? own.has : own.has2)) {
+        if (lane < group && (j < P ? own.has : own.has2)) {
           const int i = j < P ? own.at + j : own.at2 + j - P;
           cross[warp][i] = a;
           cross[warp][p.dim + i] = b;
@@ -411,8 +423,6 @@ int64_t blocks_of(int64_t T, int64_t passes, int per_sm) {
   return (side * passes + kWarps - 1) / kWarps;
 }
 
-constexpr int kGradPerSm = 2, kPerSm = 3;
-
 // A backward of few heads in all runs as one block: a second launch for the partial
 // sums would cost more.
 int64_t grad_blocks(int64_t T, int64_t passes) {
@@ -444,12 +454,20 @@ bool fits(const RopePlan& R, const RopeArgs& a, int P, bool grad) {
   return true;
 }
 
-template <typename T, int P, int CH, bool PAIRS, bool GRAD>
+template <typename T, int P, int CH, bool PAIRS, bool GRAD, int GROUP>
 cudaError_t go(RopeArgs& a, int64_t* blocks, cudaStream_t st) {
   a.passes = (a.heads + a.kv + (a.values ? a.kv : 0) + a.side - 1) / a.side;
   *blocks = GRAD ? grad_blocks(a.T, a.passes) : blocks_of(a.T, a.passes, kPerSm);
-  return launch_ex(rope_kernel<T, P, CH, PAIRS, GRAD>, dim3((unsigned)*blocks),
+  return launch_ex(rope_kernel<T, P, CH, PAIRS, GRAD, GROUP>, dim3((unsigned)*blocks),
                    dim3(32 * kWarps), 0, st, false, a);
+}
+
+template <typename T, int P, bool PAIRS, bool GRAD>
+cudaError_t by_group(RopeArgs& a, int64_t* blocks, cudaStream_t st) {
+  constexpr int of64 = 32 / P, of128 = 64 / P;  // lanes of heads of 64 and of 128
+  if (a.group == of64) return go<T, P, 1, PAIRS, GRAD, of64>(a, blocks, st);
+  if (a.group == of128) return go<T, P, 1, PAIRS, GRAD, of128>(a, blocks, st);
+  return go<T, P, 1, PAIRS, GRAD, 0>(a, blocks, st);
 }
 
 template <typename T, bool GRAD>
@@ -466,19 +484,21 @@ cudaError_t pick(const RopePlan& R, RopeArgs& a, int64_t* blocks, cudaStream_t s
   if constexpr (sizeof(T) == 2) {
     if (fits(R, a, 8, GRAD)) {
       shape(8);
-      return R.inter ? go<T, 8, 1, true, GRAD>(a, blocks, st) : go<T, 8, 1, false, GRAD>(a, blocks, st);
+      return R.inter ? by_group<T, 8, true, GRAD>(a, blocks, st)
+                     : by_group<T, 8, false, GRAD>(a, blocks, st);
     }
   }
   if (fits(R, a, 4, GRAD)) {
     shape(4);
-    return R.inter ? go<T, 4, 1, true, GRAD>(a, blocks, st) : go<T, 4, 1, false, GRAD>(a, blocks, st);
+    return R.inter ? by_group<T, 4, true, GRAD>(a, blocks, st)
+                   : by_group<T, 4, false, GRAD>(a, blocks, st);
   }
   shape(1);
   if (R.inter)
-    return a.chunks <= 32 ? go<T, 1, 1, true, GRAD>(a, blocks, st)
-                          : go<T, 1, 4, true, GRAD>(a, blocks, st);
-  return a.chunks <= 32 ? go<T, 1, 1, false, GRAD>(a, blocks, st)
-                        : go<T, 1, 4, false, GRAD>(a, blocks, st);
+    return a.chunks <= 32 ? go<T, 1, 1, true, GRAD, 0>(a, blocks, st)
+                          : go<T, 1, 4, true, GRAD, 0>(a, blocks, st);
+  return a.chunks <= 32 ? go<T, 1, 1, false, GRAD, 0>(a, blocks, st)
+                        : go<T, 1, 4, false, GRAD, 0>(a, blocks, st);
 }
 
 void fill(const RopePlan& R, int64_t T, const int32_t* pos, RopeArgs* a) {
