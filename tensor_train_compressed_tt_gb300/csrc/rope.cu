@@ -142,35 +142,32 @@ struct Place {
     o.set(v);
     if (has2) *reinterpret_cast<R*>(y + at2) = o;
   }
-  // values of channels; 0 where there are none
-  __device__ void weights(const float* g, Pairs<P>& x) const {
-    float u[P], v[P];
-#pragma unroll
-    for (int j = 0; j < P; ++j) {
-      u[j] = !has ? 0.f : g ? __ldg(g + at + j) : 1.f;
-      v[j] = !has2 ? 0.f : g ? __ldg(g + at2 + j) : 1.f;
-    }
-    split(u, v, x);
+  // the channels of pair n of a head
+  __device__ static void pair(const RopeArgs& p, int n, int& a, int& b) {
+    Place q;
+    q.set(p, n / P);
+    a = q.at + (PAIRS ? 2 * (n % P) : n % P);
+    b = PAIRS ? a + 1 : q.at2 + n % P;
   }
 };
+
+template <int P>
+__device__ __forceinline__ void from_shared(const float* p, float* f) {
+  if (P == 1) f[0] = p[0];
+#pragma unroll
+  for (int j = 0; j + 3 < P; j += 4) {
+    const float4 v = *reinterpret_cast<const float4*>(p + j);
+    f[j] = v.x, f[j + 1] = v.y, f[j + 2] = v.z, f[j + 3] = v.w;
+  }
+}
 
 // x turned by the angle, or back.
 template <int P>
 __device__ __forceinline__ void turn_by(const float* cosine, const float* sine, bool back,
                                         Pairs<P>& x) {
   float c[P], s[P], m[P], u[P], v[P];
-  if (P >= 4) {
-#pragma unroll
-    for (int j = 0; j < P; j += 4) {
-      const float4 f = *reinterpret_cast<const float4*>(cosine + j);
-      const float4 g = *reinterpret_cast<const float4*>(sine + j);
-      c[j] = f.x, c[j + 1] = f.y, c[j + 2] = f.z, c[j + 3] = f.w;
-      s[j] = g.x, s[j + 1] = g.y, s[j + 2] = g.z, s[j + 3] = g.w;
-    }
-  } else {
-    c[0] = cosine[0];
-    s[0] = sine[0];
-  }
+  from_shared<P>(cosine, c);
+  from_shared<P>(sine, s);
 #pragma unroll
   for (int j = 0; j < P; ++j) {
     m[j] = -s[j];
@@ -209,8 +206,30 @@ __device__ __forceinline__ float head_sum(float v, int group, int i) {
   return __shfl_sync(0xffffffffu, v, (threadIdx.x & 31) - i);
 }
 
-// Blocks of 256 threads that an SM holds, by the registers of a lane's chunk.
+// A lane's loads on their way: copied asynchronously to slots of its own in shared
+// memory, two tokens ahead.  (In registers one token ahead, a warp waited for memory
+// in four of ten cycles: backward of 16384 tokens of 24 heads of 64 38.4 us.)  Single
+// elements, which the asynchronous copy does not take, go one token ahead in registers.
+constexpr int kDepth = 3;
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* to, const void* from) {
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(su32(to)), "l"(from)
+                 : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(su32(to)), "l"(from),
+                 "n"(BYTES)
+                 : "memory");
+}
+
+// Blocks of 256 threads that an SM holds.
 constexpr int kGradPerSm = 2, kPerSm = 3;
+
+// Shared memory of a block's copies: two runs a lane of x, and of dy.
+template <typename T, int P, bool GRAD>
+constexpr size_t ring_bytes() {
+  return P > 1 ? (size_t)kDepth * kWarps * 32 * P * sizeof(T) * (GRAD ? 4 : 2) : 0;
+}
 
 // GROUP: the lanes of a head where they are known (16 and 32 bytes a lane of heads of 64
 // and 128), else 0.
@@ -220,6 +239,7 @@ __global__ void __launch_bounds__(32 * kWarps, GRAD ? kGradPerSm : kPerSm)
   using R = Raw<T, P>;
   __shared__ uint64_t turn[kMaxPairs];
   __shared__ __align__(16) float cosines[kWarps][kMaxPairs], sines[kWarps][kMaxPairs];
+  __shared__ __align__(16) float weights[2][2][kMaxPairs];  // of q and k, by pairs
   __shared__ float cross[GRAD ? kWarps : 1][GRAD ? 2 * 2 * kMaxPairs : 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int i = threadIdx.x; i < p.rot / 2; i += 32 * kWarps) turn[i] = p.turn[i];
@@ -227,9 +247,17 @@ __global__ void __launch_bounds__(32 * kWarps, GRAD ? kGradPerSm : kPerSm)
     cosines[warp][i] = 1.f;
     sines[warp][i] = 0.f;
   }
-  __syncthreads();
   pdl_wait();
   pdl_trigger();
+  if (p.norm)
+    for (int i = threadIdx.x; i < 2 * kMaxPairs; i += 32 * kWarps) {
+      const float* g = i < kMaxPairs ? p.gq : p.gk;
+      int a, b;
+      Place<T, P, PAIRS>::pair(p, i % kMaxPairs, a, b);
+      weights[i / kMaxPairs][0][i % kMaxPairs] = a < p.dim ? g ? __ldg(g + a) : 1.f : 0.f;
+      weights[i / kMaxPairs][1][i % kMaxPairs] = b < p.dim ? g ? __ldg(g + b) : 1.f : 0.f;
+    }
+  __syncthreads();
   // this lane's head and channels
   const int64_t w = (int64_t)blockIdx.x * kWarps + warp;
   const int64_t step = (int64_t)gridDim.x * kWarps / p.passes;
@@ -242,14 +270,17 @@ __global__ void __launch_bounds__(32 * kWarps, GRAD ? kGradPerSm : kPerSm)
   h -= which == 0 ? 0 : which == 1 ? p.heads : p.heads + p.kv;
   const bool here = beside < side && (which == 0 || (h < p.kv && (which == 1 || p.values)));
   Place<T, P, PAIRS> at[CH];
-  Pairs<P> g[CH];
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
     at[c].set(p, c * 32 + li);
     if (!here) at[c].has = at[c].has2 = false;
-    if (p.norm) at[c].weights(which == 0 ? p.gq : p.gk, g[c]);
   }
   const int share = li * P;  // its pairs in the table of angles
+  const float* mine = &weights[which == 0 ? 0 : 1][0][share];
+  auto weight = [&](int c, Pairs<P>& g) {
+    from_shared<P>(mine + 32 * P * c, g.a);
+    from_shared<P>(mine + kMaxPairs + 32 * P * c, g.b);
+  };
   // where the head starts in the tensors' first row
   const bool reads = !GRAD || p.norm;
   if (!here) h = 0;
@@ -262,22 +293,64 @@ __global__ void __launch_bounds__(32 * kWarps, GRAD ? kGradPerSm : kPerSm)
 
   R xu[CH] = {}, xv[CH] = {}, du[GRAD ? CH : 1] = {}, dv[GRAD ? CH : 1] = {};
   int pos = 0, row = 0;
-  auto fetch = [&] {
+  // One token's loads; with copies into slot k of the lane, and of the warp for the position.
+  extern __shared__ uint4 ring[];
+  __shared__ int at_pos[kWarps][kDepth], at_row[kWarps][kDepth];
+  constexpr bool copies = P > 1;
+  constexpr int runs = GRAD ? 4 : 2;
+  R* slots = reinterpret_cast<R*>(ring) + warp * kDepth * runs * 32 + lane;
+  auto fetch = [&](int64_t t, int k) {
+    if constexpr (copies) {
+      constexpr int bytes = sizeof(R);
+      R* to = slots + k * runs * 32;
+      if (t < p.T) {
+        if (reads && at[0].has) copy_async<bytes>(to, x + at[0].at);
+        if (reads && at[0].has2) copy_async<bytes>(to + 32, x + at[0].at2);
+        if constexpr (GRAD) {
+          if (at[0].has) copy_async<bytes>(to + 64, d + at[0].at);
+          if (at[0].has2) copy_async<bytes>(to + 96, d + at[0].at2);
+        }
+        if (lane == 0 && p.pos) copy_async<4>(&at_pos[warp][k], p.pos + t);
+        if (lane == 0 && !GRAD && p.rows) copy_async<4>(&at_row[warp][k], p.rows + t);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    } else if (t < p.T) {
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      if (reads) at[c].load(x, xu[c], xv[c]);
-      if constexpr (GRAD) at[c].load(d, du[c], dv[c]);
+      for (int c = 0; c < CH; ++c) {
+        if (reads) at[c].load(x, xu[c], xv[c]);
+        if constexpr (GRAD) at[c].load(d, du[c], dv[c]);
+      }
+      pos = p.pos ? p.pos[t] : (int)t;
+      row = !GRAD && p.rows && which > 0 ? p.rows[t] : (int)t;
     }
-    pos = p.pos ? p.pos[t] : (int)t;
-    row = !GRAD && p.rows && which > 0 ? p.rows[t] : (int)t;
+    x += step_in;
+    if constexpr (GRAD) d += step_grad;
   };
   Pairs<P> sum[CH];
 #pragma unroll
   for (int c = 0; c < CH; ++c) fill<P>(0.f, sum[c].a), fill<P>(0.f, sum[c].b);
 
-  if (t < p.T) fetch();
-  while (t < p.T) {
-    __syncwarp();
+  if constexpr (copies) {
+    // channels and heads that are not there stay zeros
+    for (int i = 0; i < kDepth * runs; ++i) slots[i * 32] = R{};
+#pragma unroll
+    for (int k = 0; k < kDepth - 1; ++k) fetch(t + k * step, k);
+  } else {
+    fetch(t, 0);
+  }
+  int slot = 0;
+  for (; t < p.T; t += step) {
+    if constexpr (copies) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 2) : "memory");
+      __syncwarp();
+      pos = p.pos ? at_pos[warp][slot] : (int)t;
+      row = !GRAD && p.rows && which > 0 ? at_row[warp][slot] : (int)t;
+      const R* have = slots + slot * runs * 32;
+      xu[0] = have[0], xv[0] = have[32];
+      if constexpr (GRAD) du[0] = have[64], dv[0] = have[96];
+    } else {
+      __syncwarp();
+    }
     for (int i = lane; i < p.rot / 2; i += 32)
       angle<T>(pos, turn[i], &cosines[warp][i], &sines[warp][i]);
     __syncwarp();
@@ -300,10 +373,9 @@ __global__ void __launch_bounds__(32 * kWarps, GRAD ? kGradPerSm : kPerSm)
         if (at[c].has2) *reinterpret_cast<R*>(out + at[c].at2) = xv[c];
       }
     }
-    t += step;
-    x += step_in;
-    if constexpr (GRAD) d += step_grad;
-    if (t < p.T) fetch();
+    // the slot that the token before this one was in
+    fetch(t + (copies ? kDepth - 1 : 1) * step, slot == 0 ? kDepth - 1 : slot - 1);
+    slot = slot == kDepth - 1 ? 0 : slot + 1;
 
     if constexpr (!GRAD) {
       if (p.norm) {
@@ -316,8 +388,10 @@ __global__ void __launch_bounds__(32 * kWarps, GRAD ? kGradPerSm : kPerSm)
         fill<P>(inverse_root(fmaf(s, p.inv_n, p.eps)), r);
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-          mul<P>(u[c].a, r, u[c].a), mul<P>(u[c].a, g[c].a, u[c].a);
-          mul<P>(u[c].b, r, u[c].b), mul<P>(u[c].b, g[c].b, u[c].b);
+          Pairs<P> g;
+          weight(c, g);
+          mul<P>(u[c].a, r, u[c].a), mul<P>(u[c].a, g.a, u[c].a);
+          mul<P>(u[c].b, r, u[c].b), mul<P>(u[c].b, g.b, u[c].b);
         }
       }
       if (kept && which < 2) {
@@ -339,9 +413,11 @@ __global__ void __launch_bounds__(32 * kWarps, GRAD ? kGradPerSm : kPerSm)
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
           float gu[P];
+          Pairs<P> g;
+          weight(c, g);
           mul_up<P>(s2, u[c].a, u[c].a), mul_up<P>(s2, u[c].b, u[c].b);
-          mul<P>(e[c].a, u[c].a, gu), mul_up<P>(m2, gu, g[c].a);
-          mul<P>(e[c].b, u[c].b, gu), mul_up<P>(m2, gu, g[c].b);
+          mul<P>(e[c].a, u[c].a, gu), mul_up<P>(m2, gu, g.a);
+          mul<P>(e[c].b, u[c].b, gu), mul_up<P>(m2, gu, g.b);
         }
         float s = s2.x + s2.y, m = m2.x + m2.y;
         s = head_sum<GROUP>(s, group, li);
@@ -352,10 +428,12 @@ __global__ void __launch_bounds__(32 * kWarps, GRAD ? kGradPerSm : kPerSm)
         fill<P>(-one * m * p.inv_n, less);  // less mean(g' h)
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
+          Pairs<P> g;
+          weight(c, g);
           mul<P>(u[c].a, r, u[c].a), mul<P>(u[c].b, r, u[c].b);
           fma<P>(e[c].a, u[c].a, sum[c].a, sum[c].a);
           fma<P>(e[c].b, u[c].b, sum[c].b, sum[c].b);
-          mul<P>(e[c].a, g[c].a, e[c].a), mul<P>(e[c].b, g[c].b, e[c].b);
+          mul<P>(e[c].a, g.a, e[c].a), mul<P>(e[c].b, g.b, e[c].b);
           fma<P>(u[c].a, less, e[c].a, e[c].a), fma<P>(u[c].b, less, e[c].b, e[c].b);
           mul<P>(e[c].a, r, e[c].a), mul<P>(e[c].b, r, e[c].b);
         }
@@ -458,8 +536,14 @@ template <typename T, int P, int CH, bool PAIRS, bool GRAD, int GROUP>
 cudaError_t go(RopeArgs& a, int64_t* blocks, cudaStream_t st) {
   a.passes = (a.heads + a.kv + (a.values ? a.kv : 0) + a.side - 1) / a.side;
   *blocks = GRAD ? grad_blocks(a.T, a.passes) : blocks_of(a.T, a.passes, kPerSm);
-  return launch_ex(rope_kernel<T, P, CH, PAIRS, GRAD, GROUP>, dim3((unsigned)*blocks),
-                   dim3(32 * kWarps), 0, st, false, a);
+  auto kernel = rope_kernel<T, P, CH, PAIRS, GRAD, GROUP>;
+  constexpr size_t smem = ring_bytes<T, P, GRAD>();
+  static PerDevice once;
+  const cudaError_t e = once.get([&] {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  });
+  if (e != cudaSuccess) return e;
+  return launch_ex(kernel, dim3((unsigned)*blocks), dim3(32 * kWarps), smem, st, false, a);
 }
 
 template <typename T, int P, bool PAIRS, bool GRAD>
@@ -481,6 +565,8 @@ cudaError_t pick(const RopePlan& R, RopeArgs& a, int64_t* blocks, cudaStream_t s
     if (a.chunks <= 32 && 32 / a.chunks > 32 / a.group) a.group = a.chunks;
     a.side = 32 / a.group;
   };
+  // 16 bytes a run (f32 with eight pairs a lane, 32 bytes: 4099 x 20 heads of 80 26.3 ->
+  // 28.6 us)
   if constexpr (sizeof(T) == 2) {
     if (fits(R, a, 8, GRAD)) {
       shape(8);

@@ -22,6 +22,18 @@ struct Raw<float, 4> {
   __device__ void set(const float* f) { v = make_float4(f[0], f[1], f[2], f[3]); }
 };
 template <>
+struct Raw<float, 8> {
+  float4 v[2];
+  __device__ void get(float* f) const {
+    f[0] = v[0].x, f[1] = v[0].y, f[2] = v[0].z, f[3] = v[0].w;
+    f[4] = v[1].x, f[5] = v[1].y, f[6] = v[1].z, f[7] = v[1].w;
+  }
+  __device__ void set(const float* f) {
+    v[0] = make_float4(f[0], f[1], f[2], f[3]);
+    v[1] = make_float4(f[4], f[5], f[6], f[7]);
+  }
+};
+template <>
 struct Raw<float, 1> {
   float v;
   __device__ void get(float* f) const { f[0] = v; }

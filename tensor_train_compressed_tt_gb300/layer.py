@@ -21,13 +21,14 @@ if hasattr(torch, "float8_e4m3fn"):
 _DT[torch.uint8] = ttc.TT_DT_E4M3
 
 
-def _stream(stream: Optional[torch.cuda.Stream]) -> int:
+def _stream(stream: Optional[torch.cuda.Stream], here: Optional[int] = None) -> int:
     """The stream's handle, by default the current one's: asked for without the
     torch.cuda.Stream object around it, which takes 2.9 us, a quarter of a small
     call on the host."""
     if stream is not None:
         return int(stream.cuda_stream)
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return torch._C._cuda_getCurrentRawStream(
+        torch.cuda.current_device() if here is None else here)
 
 
 def _filled(shape, dtype: torch.dtype, device, fill: Optional[float]) -> torch.Tensor:
@@ -478,12 +479,13 @@ class TTAttention:
         return dq, dk, dv
 
 
-def _same_device(*tensors: Optional[torch.Tensor]) -> None:
-    """The kernels run on the current device: tensors of another one are refused."""
+def _same_device(*tensors: Optional[torch.Tensor]) -> int:
+    """The current device, on which the kernels run: tensors of another one are refused."""
     here = torch.cuda.current_device()
     for t in tensors:
-        if t is not None and t.is_cuda and t.device.index != here:
+        if t is not None and t.get_device() not in (here, -1):
             raise ValueError(f"a tensor on {t.device}, while cuda:{here} is current")
+    return here
 
 
 class TTRotary:
@@ -526,7 +528,7 @@ class TTRotary:
     def forward(self, q, k, pos=None, gq=None, gk=None, q_out=None, k_out=None, stream=None):
         """(q_out, k_out) for tokens at positions pos (int32; None: 0, 1, ..)."""
         T = q.shape[0]
-        _same_device(q, k, pos, gq, gk, q_out, k_out)
+        here = _same_device(q, k, pos, gq, gk, q_out, k_out)
         wq, wk = self._weights(gq, gk)
         at = _dense(pos, (T,), torch.int32, "pos")
         hq, hk = self._of(q, T, self.heads, "q"), self._of(k, T, self.kv_heads, "k")
@@ -536,7 +538,7 @@ class TTRotary:
             k_out = _new(k.shape, self.dtype, k.device, stream)
         ttc.check(ttc.tt_rope_forward(
             self.plan, T, at, hq, hk, wq, wk, self._of(q_out, T, self.heads, "q_out"),
-            self._of(k_out, T, self.kv_heads, "k_out"), None, None, 0, 0, _stream(stream)),
+            self._of(k_out, T, self.kv_heads, "k_out"), None, None, 0, 0, _stream(stream, here)),
             "tt_rope_forward")
         return q_out, k_out
 
@@ -547,7 +549,7 @@ class TTRotary:
         keys and values (rows, kv_heads, dim).  A row that the cache does not have is
         skipped and recorded in the device status word."""
         T, n, G = q.shape[0], keys.shape[0], self.kv_heads
-        _same_device(q, k, v, pos, rows, keys, values, gq, gk, q_out)
+        here = _same_device(q, k, v, pos, rows, keys, values, gq, gk, q_out)
         wq, wk = self._weights(gq, gk)
         if rows is None:
             raise ValueError("rows: expected an int32 tensor")
@@ -558,7 +560,7 @@ class TTRotary:
         ttc.check(ttc.tt_rope_forward(
             self.plan, T, at, hq, hk, wq, wk, self._of(q_out, T, self.heads, "q_out"),
             self._of(keys, n, G, "keys"), self._of(v, T, G, "v"),
-            self._of(values, n, G, "values"), to, n, _stream(stream)), "tt_rope_forward")
+            self._of(values, n, G, "values"), to, n, _stream(stream, here)), "tt_rope_forward")
         return q_out, keys, values
 
     def backward(self, dq, dk, pos=None, q=None, k=None, gq=None, gk=None, dq_in=None, dk_in=None,
@@ -567,7 +569,7 @@ class TTRotary:
         needs) and of the weights, for those of its outputs; without a norm dgq and dgk
         are None.  dq_in may be dq, dk_in dk."""
         T = dq.shape[0]
-        _same_device(dq, dk, pos, q, k, gq, gk, dq_in, dk_in, dgq, dgk, ws)
+        here = _same_device(dq, dk, pos, q, k, gq, gk, dq_in, dk_in, dgq, dgk, ws)
         H, G, sh = self.heads, self.kv_heads, (self.dim,)
         wq, wk = self._weights(gq, gk)
         at = _dense(pos, (T,), torch.int32, "pos")
@@ -592,7 +594,7 @@ class TTRotary:
             self.plan, T, at, hq, hk, wq, wk, self._of(dq, T, H, "dq"), self._of(dk, T, G, "dk"),
             self._of(dq_in, T, H, "dq_in"), self._of(dk_in, T, G, "dk_in"),
             _dense(dgq, sh, torch.float32, "dgq"), _dense(dgk, sh, torch.float32, "dgk"),
-            _ptr(ws), ws.numel(), _stream(stream)), "tt_rope_backward")
+            _ptr(ws), ws.numel(), _stream(stream, here)), "tt_rope_backward")
         return dq_in, dk_in, dgq, dgk
 
 
@@ -619,13 +621,13 @@ class TTDropout:
 
     def forward(self, x, rng, res=None, y=None, stream=None):
         """y = dropout(x) + res; y may be x or res."""
-        _same_device(x, rng, res, y)
+        here = _same_device(x, rng, res, y)
         if y is None:
             y = _new(x.shape, self.dtype, x.device, stream)
         sh = x.shape
         ttc.check(ttc.tt_dropout(self.plan, x.numel(), _state(rng), _dense(x, sh, self.dtype, "x"),
                                  _dense(res, sh, self.dtype, "res"),
-                                 _dense(y, sh, self.dtype, "y"), _stream(stream)), "tt_dropout")
+                                 _dense(y, sh, self.dtype, "y"), _stream(stream, here)), "tt_dropout")
         return y
 
     def backward(self, dy, rng, dx=None, stream=None):
@@ -650,7 +652,7 @@ class TTDropNorm:
                 stream=None):
         """(y, s, stats)."""
         T, N = x.shape[0], self.N
-        _same_device(x, rng, gamma, beta, res, y, sum, stats)
+        here = _same_device(x, rng, gamma, beta, res, y, sum, stats)
         if y is None:
             y = _new((T, N), self.dtype, x.device, stream)
         if sum is None:
@@ -663,7 +665,7 @@ class TTDropNorm:
             _dense(res, sh, self.dtype, "res"), _dense(gamma, (N,), f32, "gamma"),
             _dense(beta, (N,), f32, "beta"), _dense(sum, sh, self.dtype, "sum"),
             _dense(y, sh, self.dtype, "y"), _dense(stats, (T, 2), f32, "stats"),
-            _stream(stream)), "tt_norm_dropout_forward")
+            _stream(stream, here)), "tt_norm_dropout_forward")
         return y, sum, stats
 
     def backward(self, s, dy, rng, gamma, stats, dsum=None, dx=None, dres=None, residual=True,
@@ -671,7 +673,7 @@ class TTDropNorm:
         """(dx, dres, dgamma, dbeta): the gradients of x and of res (that of s).
         residual=False: dres is None, where forward had no res."""
         T, N = s.shape[0], self.N
-        _same_device(s, dy, rng, gamma, stats, dsum, dx, dres, dgamma, dbeta, ws)
+        here = _same_device(s, dy, rng, gamma, stats, dsum, dx, dres, dgamma, dbeta, ws)
         if dx is None:
             dx = _new((T, N), self.dtype, s.device, stream)
         if dres is None and residual:
@@ -689,7 +691,7 @@ class TTDropNorm:
             _dense(gamma, (N,), f32, "gamma"), _dense(stats, (T, 2), f32, "stats"),
             _dense(dx, sh, self.dtype, "dx"), _dense(dres, sh, self.dtype, "dres"),
             _dense(dgamma, (N,), f32, "dgamma"), _dense(dbeta, (N,), f32, "dbeta"), _ptr(ws),
-            ws.numel(), _stream(stream)), "tt_norm_dropout_backward")
+            ws.numel(), _stream(stream, here)), "tt_norm_dropout_backward")
         return dx, dres, dgamma, dbeta
 
 
@@ -720,7 +722,7 @@ class TTLogProbs:
         (int32) and top_logp where the plan has them; the entropy is computed where a
         tensor for it is given, else it is None."""
         T, f32 = logits.shape[0], torch.float32
-        _same_device(logits, targets, logp, lse, entropy, top, top_logp)
+        here = _same_device(logits, targets, logp, lse, entropy, top, top_logp)
         if logp is not None and targets is None:
             raise ValueError("logp: needs targets")
         if logp is None and targets is not None:
@@ -740,7 +742,7 @@ class TTLogProbs:
             _dense(logp, (T,), f32, "logp"), _dense(lse, (T,), f32, "lse"),
             _dense(entropy, (T,), f32, "entropy"),
             _dense(top, (T, self.top), torch.int32, "top"),
-            _dense(top_logp, (T, self.top), f32, "top_logp"), _stream(stream)),
+            _dense(top_logp, (T, self.top), f32, "top_logp"), _stream(stream, here)),
             "tt_logp_forward")
         return logp, lse, entropy, top, top_logp
 
@@ -758,7 +760,7 @@ class TTLogProbs:
         """dlogits for the gradients of logp and of the entropy (which then has to be
         given), from forward's lse.  dlogits may be logits."""
         T, f32 = logits.shape[0], torch.float32
-        _same_device(logits, targets, lse, dlogp, entropy, dentropy, dlogits)
+        here = _same_device(logits, targets, lse, dlogp, entropy, dentropy, dlogits)
         t, g, h = self._gradients(T, targets, dlogp, dentropy)
         if dentropy is not None and entropy is None:
             raise ValueError("entropy: dentropy needs it")
@@ -770,7 +772,7 @@ class TTLogProbs:
         to, dstride = self._rows(dlogits, T, "dlogits")
         ttc.check(ttc.tt_logp_backward(
             self.plan, T, at, stride, t, _dense(lse, (T,), f32, "lse"), g,
-            _dense(entropy, (T,), f32, "entropy"), h, to, dstride, _stream(stream)),
+            _dense(entropy, (T,), f32, "entropy"), h, to, dstride, _stream(stream, here)),
             "tt_logp_backward")
         return dlogits
 
@@ -780,7 +782,7 @@ class TTLogProbs:
         logits, where the gradients are known beforehand (-1 / T for a mean loss).
         dlogits may be logits."""
         T, f32 = logits.shape[0], torch.float32
-        _same_device(logits, targets, dlogp, dentropy, logp, lse, entropy, dlogits)
+        here = _same_device(logits, targets, dlogp, dentropy, logp, lse, entropy, dlogits)
         t, g, h = self._gradients(T, targets, dlogp, dentropy)
         if logp is not None and targets is None:
             raise ValueError("logp: needs targets")
@@ -795,5 +797,5 @@ class TTLogProbs:
         ttc.check(ttc.tt_logp_loss(
             self.plan, T, at, stride, t, g, h, _dense(logp, (T,), f32, "logp"),
             _dense(lse, (T,), f32, "lse"), _dense(entropy, (T,), f32, "entropy"), to, dstride,
-            _stream(stream)), "tt_logp_loss")
+            _stream(stream, here)), "tt_logp_loss")
         return logp, lse, entropy, dlogits

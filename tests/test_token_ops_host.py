@@ -260,7 +260,10 @@ def test_weight_gradients_that_are_added_to_start_at_zero(fake, monkeypatch):
 
 def test_a_tensor_of_another_device_is_refused(monkeypatch):
     class Elsewhere:
-        is_cuda, device = True, torch.device("cuda:1")
+        device = torch.device("cuda:1")
+
+        def get_device(self):
+            return 1
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     with pytest.raises(ValueError):
         layer._same_device(None, Elsewhere())
