@@ -18,7 +18,8 @@
 // error is the frequency's own (2^-52 of it, times the position), at any position
 // of 31 bits.  The nearest quarter turn is taken off; sine and cosine of the rest, an
 // eighth of a turn at most, come from the hardware's approximation in bf16 (off by
-// 2^-20, where the output's half step is 2^-8), from sincospi in f32.
+// 2^-20, where the output's half step is 2^-8), in f32 from their Taylor series to the
+// ninth and tenth power, whose next terms are below 2^-28 at an eighth of a turn.
 #include <cmath>
 #include <new>
 
@@ -70,13 +71,22 @@ __device__ __forceinline__ void angle(int64_t pos, uint64_t turn, float* cosine,
   const uint32_t quarter = (uint32_t)((a + (1ull << 61)) >> 62);
   // in [-2^61, 2^61), where 2^63 is half a turn; 2^-31 of it fits 31 bits
   const int32_t rest = (int32_t)((int64_t)(a - ((uint64_t)quarter << 62)) >> 31);
+  const float x = (float)rest * (float)(3.14159265358979323846 * 0x1p-32);
   float s, c;
   if (sizeof(T) == 2) {
-    const float x = (float)rest * (float)(3.14159265358979323846 * 0x1p-32);
     s = __sinf(x);
     c = __cosf(x);
   } else {
-    sincospif((float)rest * 0x1p-32f, &s, &c);
+    const float y = x * x;
+    s = fmaf(y, 1.f / 362880, -1.f / 5040);
+    s = fmaf(y, s, 1.f / 120);
+    s = fmaf(y, s, -1.f / 6);
+    s = fmaf(x * y, s, x);
+    c = fmaf(y, -1.f / 3628800, 1.f / 40320);
+    c = fmaf(y, c, -1.f / 720);
+    c = fmaf(y, c, 1.f / 24);
+    c = fmaf(y, c, -0.5f);
+    c = fmaf(y, c, 1.f);
   }
   const float u = quarter & 1 ? -s : c, v = quarter & 1 ? c : s;
   *cosine = quarter & 2 ? -u : u;
