@@ -196,24 +196,29 @@ __device__ __forceinline__ float inverse_root(float x) {
   return fmaf(0.5f * r, fmaf(-x * r, r, 1.f), r);
 }
 
-// The sum over the lanes of each head; lane i of it is `i`.  A power of two by
-// exchanges, else from the upper lanes to the lower, then from the first to all.
+// The sum over the lanes of each head, lane i of which this one is.  Known powers of two by
+// exchanges; else from the upper lanes to the lower, in the same steps for every number
+// (a loop's branches cost heads of ten lanes a sixth of their instructions), then from the
+// first lane to all.  `takes`: bit k where step k adds a lane's value to this one.
+__device__ __forceinline__ uint32_t sum_steps(int group, int i) {
+  uint32_t takes = 0;
+#pragma unroll
+  for (int k = 0; k < 5; ++k) takes |= (uint32_t)(i < 1 << k && i + (1 << k) < group) << k;
+  return takes;
+}
 template <int GROUP>
-__device__ __forceinline__ float head_sum(float v, int group, int i) {
+__device__ __forceinline__ float head_sum(float v, uint32_t takes, int first) {
   if (GROUP) {
 #pragma unroll
     for (int o = GROUP / 2; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
   }
-  if ((group & (group - 1)) == 0) {
-    for (int o = group >> 1; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
+#pragma unroll
+  for (int k = 4; k >= 0; --k) {
+    const float u = __shfl_down_sync(0xffffffffu, v, 1 << k);
+    v += takes >> k & 1 ? u : 0.f;
   }
-  for (int o = group > 16 ? 16 : group > 8 ? 8 : group > 4 ? 4 : 2; o; o >>= 1) {
-    const float u = __shfl_down_sync(0xffffffffu, v, o);
-    if (i + o < group && i < o) v += u;
-  }
-  return __shfl_sync(0xffffffffu, v, (threadIdx.x & 31) - i);
+  return __shfl_sync(0xffffffffu, v, first);
 }
 
 // A lane's loads on their way: copied asynchronously to slots of its own in shared
@@ -273,6 +278,7 @@ __global__ void __launch_bounds__(32 * kWarps, GRAD ? kGradPerSm : kPerSm)
   const int64_t step = (int64_t)gridDim.x * kWarps / p.passes;
   const int group = GROUP ? GROUP : p.group, side = GROUP ? 32 / GROUP : p.side;
   const int beside = lane / group, li = lane - beside * group;
+  const uint32_t takes = GROUP ? 0 : sum_steps(group, li);
   int h = (int)(w % p.passes) * side + beside;
   int64_t t = w / p.passes;
   if (t >= step) t = p.T;
@@ -393,7 +399,7 @@ __global__ void __launch_bounds__(32 * kWarps, GRAD ? kGradPerSm : kPerSm)
 #pragma unroll
         for (int c = 0; c < CH; ++c) mul_up<P>(s2, u[c].a, u[c].a), mul_up<P>(s2, u[c].b, u[c].b);
         float s = s2.x + s2.y;
-        s = head_sum<GROUP>(s, group, li);
+        s = head_sum<GROUP>(s, takes, lane - li);
         float r[P];
         fill<P>(inverse_root(fmaf(s, p.inv_n, p.eps)), r);
 #pragma unroll
@@ -430,8 +436,8 @@ __global__ void __launch_bounds__(32 * kWarps, GRAD ? kGradPerSm : kPerSm)
           mul<P>(e[c].b, u[c].b, gu), mul_up<P>(m2, gu, g.b);
         }
         float s = s2.x + s2.y, m = m2.x + m2.y;
-        s = head_sum<GROUP>(s, group, li);
-        m = head_sum<GROUP>(m, group, li);
+        s = head_sum<GROUP>(s, takes, lane - li);
+        m = head_sum<GROUP>(m, takes, lane - li);
         const float one = inverse_root(fmaf(s, p.inv_n, p.eps));
         float r[P], less[P];
         fill<P>(one, r);
