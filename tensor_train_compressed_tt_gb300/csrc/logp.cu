@@ -15,7 +15,7 @@
 // for two values than c x - c r), so a log probability is as exact at logits of a
 // thousand as at logits of one, and logits of the type's lowest value do not overflow.
 //
-// A row is taken by 1, 4, 8 or 16 warps by its width; rows that are few or long are
+// A row is taken by 1 to 32 warps by its width; rows that are few or long are
 // split over a cluster's CTAs, which meet through shared memory.  Rows start
 // anywhere: the elements before the first and after the last 16-byte boundary are
 // taken one by one.  The pass that also writes the gradient keeps the row in shared
@@ -269,14 +269,19 @@ __device__ __forceinline__ uint64_t entry(uint32_t key, int index) {
   return (uint64_t)key << 32 | (uint32_t)~index;
 }
 
+constexpr int kAhead = 4;  // vectors that a thread loads at once
+constexpr int kHits = 256;
+
 struct TopShared {
   uint32_t keys[kGroups];
   int groups[kGroups];
   uint64_t list[kList];
   uint64_t best[kMaxTop];
   uint64_t red[8];
+  uint4 hits[kHits];   // vectors with a value not below the bound, and where they are
+  int hit_at[kHits];
   uint32_t bound;
-  int found, chosen;
+  int found, chosen, hit;
 };
 
 // The slice's k first entries in order into sh.best (0 where there are fewer).
@@ -292,7 +297,7 @@ __device__ void top_of_slice(TopShared& sh, const T* x, const Cut& cut, int firs
 #pragma unroll
   for (int o = SIDE / 2; o; o >>= 1) key = max(key, __shfl_xor_sync(0xffffffffu, key, o));
   if (tid % SIDE == 0) sh.keys[tid / SIDE] = key;
-  if (tid == 0) sh.found = 0;
+  if (tid == 0) sh.found = sh.hit = 0;
   if (tid < k) sh.best[tid] = 0;
   __syncthreads();
   if (warp == 0) {
@@ -325,15 +330,33 @@ __device__ void top_of_slice(TopShared& sh, const T* x, const Cut& cut, int firs
     const int n = atomicAdd(&sh.found, 1);
     if (n < kList) sh.list[n] = entry(at, i);
   };
-  for (int i = warp; i < sh.chosen; i += W) {
-    const int g = sh.groups[i];
-    for (int v = first + g * SIDE + lane % SIDE + G * (lane / SIDE); v < last;
-         v += G * (32 / SIDE)) {
-      float f[VEC];
-      body[v].get(f);
+  // half a warp a group, several vectors a lane at once: one or two waits for memory
+  constexpr int HALF = 16, ROWS = HALF / SIDE;  // of the group's vectors at a time
+  for (int i = tid / HALF; i < sh.chosen; i += G / HALF) {
+    const int l = lane % HALF;
+    for (int v = first + sh.groups[i] * SIDE + l % SIDE + G * (l / SIDE); v < last;
+         v += kAhead * ROWS * G) {
+      R r[kAhead];
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) offer(f[j], cut.head + v * VEC + j);
+      for (int k = 0; k < kAhead; ++k)
+        if (v + k * ROWS * G < last) r[k] = body[v + k * ROWS * G];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        if (v + k * ROWS * G >= last || key_of(raw_max<T, VEC, 1>(r + k)) < bound) continue;
+        const int n = atomicAdd(&sh.hit, 1);
+        if (n < kHits) {
+          *reinterpret_cast<R*>(sh.hits + n) = r[k];
+          sh.hit_at[n] = cut.head + (v + k * ROWS * G) * VEC;
+        }
+      }
     }
+  }
+  __syncthreads();
+  const int hits = sh.hit;
+  for (int i = tid; i < min(hits, kHits) * VEC; i += G) {
+    float f;
+    (reinterpret_cast<const Raw<T, 1>*>(sh.hits + i / VEC) + i % VEC)->get(&f);
+    offer(f, sh.hit_at[i / VEC] + i % VEC);
   }
   if (tid < edges) {
     const int i = cut.edge<VEC>(tid);
@@ -343,7 +366,7 @@ __device__ void top_of_slice(TopShared& sh, const T* x, const Cut& cut, int firs
   }
   __syncthreads();
   const int n = sh.found;
-  if (n <= kList) {
+  if (n <= kList && hits <= kHits) {
     for (int i = tid; i < n; i += G) {
       const uint64_t e = sh.list[i];
       int before = 0;
@@ -389,11 +412,16 @@ __device__ void top_of_slice(TopShared& sh, const T* x, const Cut& cut, int firs
   __syncthreads();
 }
 
-constexpr int kAhead = 4;  // vectors that a thread loads at once
+// Blocks that an SM keeps, by registers: 1536 threads of 40 (1280 of 48 where entropy and
+// gradient would spill), or one of a row that fills it.
+__host__ __device__ constexpr int kept_blocks(int W, bool ent, bool more) {
+  return W == 32 ? 1 : W == 16 ? 3 : (ent && more ? 40 : 48) / (W == 1 ? 8 : W);
+}
 
 // One row a team of W warps (a cluster of such blocks where p.cluster > 1).
 template <typename T, int VEC, int W, bool ENT, bool TOP, bool GRAD>
-__global__ void __launch_bounds__(W == 1 ? 32 * kRowsPerBlock : 32 * W) logp_kernel(LogpArgs p) {
+__global__ void __launch_bounds__(W == 1 ? 32 * kRowsPerBlock : 32 * W, kept_blocks(W, ENT, GRAD))
+    logp_kernel(LogpArgs p) {
   using R = Raw<T, VEC>;
   constexpr int G = 32 * W;
   extern __shared__ uint4 stage_bytes[];
@@ -419,16 +447,6 @@ __global__ void __launch_bounds__(W == 1 ? 32 * kRowsPerBlock : 32 * W) logp_ker
   const R* body = reinterpret_cast<const R*>(x + cut.head);
   R* stage = reinterpret_cast<R*>(stage_bytes) + threadIdx.x;
   constexpr int stage_step = W == 1 ? 32 * kRowsPerBlock : G;
-  int target = -1;
-  float picked = 0.f;
-  if (p.targets) {
-    target = p.targets[row];
-    if (target >= p.V) {
-      if (tid == 0 && rank == 0) record_error(TT_ERR_DEVICE, 2);
-      target = -1;
-    }
-    if (target >= 0) reinterpret_cast<const Raw<T, 1>*>(x)[target].get(&picked);
-  }
   const float c = p.c;
 
   Sums<ENT> sum;
@@ -468,6 +486,19 @@ __global__ void __launch_bounds__(W == 1 ? 32 * kRowsPerBlock : 32 * W) logp_ker
         sum.template add<T, VEC, 1>(r + k, c);
         if (GRAD && kept + k < staged) stage[(kept + k) * stage_step] = r[k];
       }
+  }
+  // the target and its logit, which come while the sums meet (asked for at the start
+  // they would hold registers through the loop)
+  int target = -1;
+  float picked = 0.f;
+  if (p.targets && (GRAD || (tid == 0 && rank == 0))) {
+    target = p.targets[row];
+    if (target >= p.V) {
+      if (tid == 0 && rank == 0) record_error(TT_ERR_DEVICE, 2);
+      target = -1;
+    }
+    if (target >= 0 && tid == 0 && rank == 0)
+      reinterpret_cast<const Raw<T, 1>*>(x)[target].get(&picked);
   }
   // the team's, then the cluster's
   float most = team_max<W>(sum.ref, red);
@@ -657,24 +688,23 @@ bool alike(const LogpArgs& a, size_t size) {
 
 constexpr size_t kStageBytes = 216 << 10;  // most that a CTA keeps of a row
 
+// Clusters for few rows: CTAs for every SM, but no fewer than four vectors a thread of each.
+template <int W>
+int cluster_of(int64_t rows, int64_t vecs) {
+  int n = 1;
+  while (n < kMaxCluster && vecs / (2 * n) >= 4 * 32 * W &&
+         rows * n < 2 * (int64_t)device_sms())
+    n *= 2;
+  return n;
+}
+
 template <typename T, int VEC, int W, bool ENT, bool TOP, bool GRAD>
 cudaError_t go(LogpArgs& a, cudaStream_t st) {
   auto kernel = logp_kernel<T, VEC, W, ENT, TOP, GRAD>;
   constexpr int threads = W == 1 ? 32 * kRowsPerBlock : 32 * W;
   const int64_t rows = W == 1 ? (a.T + kRowsPerBlock - 1) / kRowsPerBlock : a.T;
-  a.cluster = 1;
   const int64_t vecs = a.V / VEC + 1;  // of a row, at most
-  if (W >= 8) {
-    // CTAs for every SM, but no less than four vectors a thread of each; with a
-    // gradient, as many as keep a slice to 64 KB, three CTAs an SM
-    while (a.cluster < kMaxCluster && vecs / (2 * a.cluster) >= 4 * threads &&
-           rows * a.cluster < 2 * (int64_t)device_sms())
-      a.cluster *= 2;
-    if (GRAD)
-      while (a.cluster < kMaxCluster &&
-             (vecs + a.cluster - 1) / a.cluster * sizeof(Raw<T, VEC>) > (64 << 10))
-        a.cluster *= 2;
-  }
+  a.cluster = W >= 8 ? cluster_of<W>(rows, vecs) : 1;
   size_t smem = 0;
   a.staged = 0;
   if (GRAD) {
@@ -695,16 +725,24 @@ cudaError_t go(LogpArgs& a, cudaStream_t st) {
                        : launch_ex(kernel, grid, dim3(threads), smem, st, false, a);
 }
 
-// Warps of a row by its vectors: few have less than two a thread.  A row that stays in
-// shared memory for its gradient leaves room for two others on the SM: 16 warps each keep
-// it busy where eight do not (8192 x 32000 203.5 -> 196.7 us).
+// Warps of a row by its vectors: a warp alone to eight a lane, then four warps, whose
+// barrier costs little.  A long row that stays in shared memory for its gradient leaves
+// room for two others on the SM, and 16 warps each keep it busy where eight do not (8192
+// x 32000 203.5 -> 196.7 us); above 108 KB it has the SM to itself, with 32 warps, and
+// what exceeds the shared memory is read again from L2.
 template <typename T, int VEC, bool ENT, bool TOP, bool GRAD>
 cudaError_t by_width(LogpArgs& a, cudaStream_t st) {
   const int64_t vecs = a.V / VEC;
   if constexpr (!TOP)
-    if (vecs <= 64) return go<T, VEC, 1, ENT, TOP, GRAD>(a, st);
-  return vecs <= 512 ? go<T, VEC, 4, ENT, TOP, GRAD>(a, st)
-                     : go<T, VEC, GRAD ? 16 : 8, ENT, TOP, GRAD>(a, st);
+    if (vecs <= 512) return go<T, VEC, 1, ENT, TOP, GRAD>(a, st);
+  if (vecs <= 1536) return go<T, VEC, 4, ENT, TOP, GRAD>(a, st);
+  if constexpr (GRAD) {
+    if (a.V * (int64_t)sizeof(T) > (108 << 10) && cluster_of<16>(a.T, vecs) == 1)
+      return go<T, VEC, 32, ENT, TOP, GRAD>(a, st);
+    return go<T, VEC, 16, ENT, TOP, GRAD>(a, st);
+  } else {
+    return go<T, VEC, 8, ENT, TOP, GRAD>(a, st);
+  }
 }
 
 template <typename T>
