@@ -229,8 +229,7 @@ constexpr int kDepth = 3;
 template <int BYTES>
 __device__ __forceinline__ void copy_async(void* to, const void* from) {
   if constexpr (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(su32(to)), "l"(from)
-                 : "memory");
+    copy_async16(to, from);
   else
     asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(su32(to)), "l"(from),
                  "n"(BYTES)

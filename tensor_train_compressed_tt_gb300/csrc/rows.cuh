@@ -147,6 +147,11 @@ __device__ __forceinline__ void fill(float x, float* o) {
   for (int i = 0; i < VEC; ++i) o[i] = x;
 }
 
+// 16 bytes to shared memory, awaited with cp.async.wait_group.
+__device__ __forceinline__ void copy_async16(void* to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(su32(to)), "l"(from) : "memory");
+}
+
 // dgamma[j] or dbeta[j] from its sum
 __device__ __forceinline__ void put_sum(float* out, int j, float v, int accumulate) {
   if (out) out[j] = accumulate ? out[j] + v : v;
