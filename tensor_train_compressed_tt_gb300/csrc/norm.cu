@@ -105,41 +105,81 @@ struct NormBwdArgs {
   void* dres;
 };
 
-// The generator's words for a thread's CH chunks of VEC elements, those at
-// (c G + tid) VEC of a row that starts at element `first`.
+// Which of a thread's CH chunks of VEC elements, those at (c G + tid) VEC of a row that starts
+// at element `first`, stay.  With VEC > 1 the generator's words for each chunk; one by one
+// 32 lanes hold 32 elements in a row, from anywhere in a group, so the warp computes the five
+// groups of every chunk together, a lane a group, and shares their bits through shared memory
+// (each lane its own words: 20000 x 1023 f32 forward 448 us).
 template <int VEC, int CH, int G>
-__device__ __forceinline__ void keep_words(const DropKey& key, const DropArgs& d, int64_t first,
-                                           int tid, uint4 (&w)[CH]) {
-  int64_t group[CH];
-  if constexpr (VEC == 4) {
-    // Two lanes side by side hold the halves of a group (rows start at multiples of
-    // four elements: where at one of eight, the even lane holds the first half).
-    // Of two chunks each lane computes one and they exchange what the other needs.
-    if (first % 8 == 0) {
-      const bool odd = tid & 1;
+struct Keep {
+  uint4 w[CH];
+  __device__ __forceinline__ void get(const DropKey& key, const DropArgs& d, int64_t first,
+                                      int, int tid, uint2*) {
+    if constexpr (VEC == 4) {
+      // Two lanes side by side hold the halves of a group (rows start at multiples of
+      // four elements: where at one of eight, the even lane holds the first half).
+      // Of two chunks each lane computes one and they exchange what the other needs.
+      if (first % 8 == 0) {
+        const bool odd = tid & 1;
 #pragma unroll
-      for (int c = 0; c < CH; c += 2) {
-        const int at = c + 1 < CH && odd ? c + 1 : c;
-        int64_t one[1] = {(first + (int64_t)(at * G + tid) * VEC) >> 3};
-        uint4 x[1];
-        key.words(one, d.site, x);
-        if (c + 1 < CH) {
-          // the even lane keeps the first half of its chunk's words and sends the rest
-          const uint32_t a = __shfl_xor_sync(0xffffffffu, odd ? x[0].x : x[0].z, 1);
-          const uint32_t b = __shfl_xor_sync(0xffffffffu, odd ? x[0].y : x[0].w, 1);
-          w[c] = odd ? make_uint4(0, 0, a, b) : x[0];
-          w[c + 1 < CH ? c + 1 : c] = odd ? x[0] : make_uint4(a, b, 0, 0);
-        } else {
-          w[c] = x[0];
+        for (int c = 0; c < CH; c += 2) {
+          const int at = c + 1 < CH && odd ? c + 1 : c;
+          int64_t one[1] = {(first + (int64_t)(at * G + tid) * VEC) >> 3};
+          uint4 x[1];
+          key.words(one, d.site, x);
+          if (c + 1 < CH) {
+            // the even lane keeps the first half of its chunk's words and sends the rest
+            const uint32_t a = __shfl_xor_sync(0xffffffffu, odd ? x[0].x : x[0].z, 1);
+            const uint32_t b = __shfl_xor_sync(0xffffffffu, odd ? x[0].y : x[0].w, 1);
+            w[c] = odd ? make_uint4(0, 0, a, b) : x[0];
+            w[c + 1 < CH ? c + 1 : c] = odd ? x[0] : make_uint4(a, b, 0, 0);
+          } else {
+            w[c] = x[0];
+          }
         }
+        return;
       }
-      return;
     }
-  }
+    int64_t group[CH];
 #pragma unroll
-  for (int c = 0; c < CH; ++c) group[c] = (first + (int64_t)(c * G + tid) * VEC) >> 3;
-  key.words(group, d.site, w);
-}
+    for (int c = 0; c < CH; ++c) group[c] = (first + (int64_t)(c * G + tid) * VEC) >> 3;
+    key.words(group, d.site, w);
+  }
+  __device__ __forceinline__ void apply(const DropArgs& d, int c, int64_t first, int tid,
+                                        const uint2*, float* f) const {
+    drop<VEC>(w[c], d, first + (int64_t)(c * G + tid) * VEC, f);
+  }
+};
+template <int CH, int G>
+struct Keep<1, CH, G> {
+  // bits: this warp's, of every chunk the 40 elements of its groups
+  __device__ __forceinline__ void get(const DropKey& key, const DropArgs& d, int64_t first,
+                                      int N, int tid, uint2* bits) {
+    const int lane = tid & 31;
+    uint8_t* bytes = reinterpret_cast<uint8_t*>(bits);
+    __syncwarp();
+    const int all = 5 * ((N + G - 1) / G);
+    for (int i = lane; i < all; i += 32) {
+      const int c = i / 5, k = i - 5 * c;
+      const int64_t group[1] = {((first + c * G + (tid - lane)) >> 3) + k};
+      uint4 x[1];
+      key.words(group, d.site, x);
+      const uint32_t v[4] = {x[0].x, x[0].y, x[0].z, x[0].w};
+      uint32_t stay = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        stay |= (uint32_t)(v[j] << 16 >= d.cut) << (2 * j) | (uint32_t)(v[j] >= d.cut) << (2 * j + 1);
+      bytes[8 * c + k] = d.all ? 0 : (uint8_t)stay;
+    }
+    __syncwarp();
+  }
+  __device__ __forceinline__ void apply(const DropArgs& d, int c, int64_t first, int tid,
+                                        const uint2* bits, float* f) const {
+    const int at = (int)((first + c * G + (tid - (tid & 31))) & 7) + (tid & 31);
+    const uint2 b = bits[c];
+    f[0] = (at < 32 ? b.x >> at : b.y >> (at - 32)) & 1 ? f[0] * d.scale : 0.f;
+  }
+};
 
 constexpr int kRowWarps = 8;  // rows side by side in a block when a warp holds a row
 
@@ -159,6 +199,8 @@ __global__ void __launch_bounds__(W == 1 ? 32 * kRowWarps : 32 * W)
   const int N = p.N;
   R rx[ROWS][CH], rr[ROWS][CH];
   DropKey key;
+  __shared__ uint2 kept[DROP && VEC == 1 ? (W == 1 ? kRowWarps : W) * CH : 1];
+  uint2* bits = kept + (DROP && VEC == 1 ? (threadIdx.x >> 5) * CH : 0);
   pdl_wait();
   pdl_trigger();
   if (DROP) key.read(p.drop);
@@ -191,8 +233,8 @@ __global__ void __launch_bounds__(W == 1 ? 32 * kRowWarps : 32 * W)
     float v[ROWS][CH * VEC], part[ROWS], mean[ROWS], rstd[ROWS];
 #pragma unroll
     for (int k = 0; k < ROWS; ++k) {
-      uint4 keep[DROP ? CH : 1];
-      if constexpr (DROP) keep_words<VEC, CH, G>(key, p.drop, (row + k * step) * N, tid, keep);
+      Keep<VEC, DROP ? CH : 1, G> keep;
+      if constexpr (DROP) keep.get(key, p.drop, (row + k * step) * N, N, tid, bits);
       float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
@@ -200,7 +242,7 @@ __global__ void __launch_bounds__(W == 1 ? 32 * kRowWarps : 32 * W)
         if (j < N) {
           float* u = v[k] + c * VEC;
           rx[k][c].get(u);
-          if (DROP) drop<VEC>(keep[DROP ? c : 0], p.drop, (row + k * step) * N + j, u);
+          if (DROP) keep.apply(p.drop, DROP ? c : 0, (row + k * step) * N, tid, bits, u);
           if (RES && (!DROP || p.res)) {
             float a[VEC];
             rr[k][c].get(a);
@@ -286,6 +328,8 @@ __global__ void __launch_bounds__(32 * W * bwd_groups(W), W <= 8 ? 2 : 1)
 #pragma unroll
   for (int i = 0; i < E; ++i) dg[i] = db[i] = 0.f;
   DropKey key;
+  __shared__ uint2 kept[DROP && VEC == 1 ? W * GROUPS * CH : 1];
+  uint2* bits = kept + (DROP && VEC == 1 ? (threadIdx.x >> 5) * CH : 0);
   pdl_wait();
   pdl_trigger();
   if (DROP) key.read(p.drop);
@@ -339,8 +383,8 @@ __global__ void __launch_bounds__(32 * W * bwd_groups(W), W <= 8 ? 2 : 1)
     fill<VEC>(-(t.x / p.n), a);
     fill<VEC>(-(t.y / p.n), b);
     T* dx = static_cast<T*>(p.dx) + row * N;
-    uint4 keep[DROP ? CH : 1];
-    if constexpr (DROP) keep_words<VEC, CH, G>(key, p.drop, row * N, tid, keep);
+    Keep<VEC, DROP ? CH : 1, G> keep;
+    if constexpr (DROP) keep.get(key, p.drop, row * N, N, tid, bits);
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int j = (c * G + tid) * VEC;
@@ -361,7 +405,7 @@ __global__ void __launch_bounds__(32 * W * bwd_groups(W), W <= 8 ? 2 : 1)
             o.set(f);
             *reinterpret_cast<R*>(static_cast<T*>(p.dres) + row * N + j) = o;
           }
-          drop<VEC>(keep[DROP ? c : 0], p.drop, row * N + j, f);
+          keep.apply(p.drop, DROP ? c : 0, row * N, tid, bits, f);
         }
         o.set(f);
         *reinterpret_cast<R*>(dx + j) = o;
@@ -587,7 +631,10 @@ cudaError_t fwd_pick(const NormFwdArgs& a, cudaStream_t st) {
                      dim3((unsigned)(a.T < most ? a.T : most)), dim3(kWideThreads), 0, st, false,
                      a);
   }
-  const int w = fwd_warps(N);
+  int w = fwd_warps(N);
+  // one by one with dropout 32 values a lane leave no registers: four warps from 513 on
+  // (20000 x 1023 bf16 124 -> 77 us, f32 141 -> 76)
+  if (V == 1 && a.drop.rng && N > 512 && w == 1) w = 4;
   const int e = (N + 32 * w - 1) / (32 * w);  // values a thread
   if (w == 1) {
     if (e <= 8) return fwd_go<T, V, 8 / V, 1>(a, st);
@@ -595,6 +642,8 @@ cudaError_t fwd_pick(const NormFwdArgs& a, cudaStream_t st) {
     if (e <= 24) return fwd_go<T, V, 24 / V, 1>(a, st);
     return fwd_go<T, V, 32 / V, 1>(a, st);
   }
+  if constexpr (V == 1)
+    if (w == 4 && e <= 8) return fwd_go<T, 1, 8, 4>(a, st);
   if (w == 4) return fwd_go<T, V, 16 / V, 4>(a, st);
   if (w == 8) return fwd_go<T, V, 16 / V, 8>(a, st);
   return w == 16 ? fwd_go<T, V, 16 / V, 16>(a, st) : fwd_go<T, V, 16 / V, 32>(a, st);

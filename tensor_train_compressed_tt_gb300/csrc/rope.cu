@@ -163,11 +163,15 @@ struct Place {
 
 template <int P>
 __device__ __forceinline__ void from_shared(const float* p, float* f) {
-  if (P == 1) f[0] = p[0];
+  if constexpr (P < 4) {
 #pragma unroll
-  for (int j = 0; j + 3 < P; j += 4) {
-    const float4 v = *reinterpret_cast<const float4*>(p + j);
-    f[j] = v.x, f[j + 1] = v.y, f[j + 2] = v.z, f[j + 3] = v.w;
+    for (int j = 0; j < P; ++j) f[j] = p[j];
+  } else {
+#pragma unroll
+    for (int j = 0; j < P; j += 4) {
+      const float4 v = *reinterpret_cast<const float4*>(p + j);
+      f[j] = v.x, f[j + 1] = v.y, f[j + 2] = v.z, f[j + 3] = v.w;
+    }
   }
 }
 
@@ -208,7 +212,7 @@ __device__ __forceinline__ uint32_t sum_steps(int group, int i) {
 }
 template <int GROUP>
 __device__ __forceinline__ float head_sum(float v, uint32_t takes, int first) {
-  if (GROUP) {
+  if constexpr (GROUP > 0) {
 #pragma unroll
     for (int o = GROUP / 2; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
@@ -223,8 +227,8 @@ __device__ __forceinline__ float head_sum(float v, uint32_t takes, int first) {
 
 // A lane's loads on their way: copied asynchronously to slots of its own in shared
 // memory, two tokens ahead.  (In registers one token ahead, a warp waited for memory
-// in four of ten cycles: backward of 16384 tokens of 24 heads of 64 38.4 us.)  Single
-// elements, which the asynchronous copy does not take, go one token ahead in registers.
+// in four of ten cycles: backward of 16384 tokens of 24 heads of 64 38.4 us.)  Single bf16
+// values, which the asynchronous copy does not take, go one token ahead in registers.
 constexpr int kDepth = 3;
 template <int BYTES>
 __device__ __forceinline__ void copy_async(void* to, const void* from) {
@@ -240,9 +244,10 @@ __device__ __forceinline__ void copy_async(void* to, const void* from) {
 constexpr int kGradPerSm = 2, kPerSm = 3;
 
 // Shared memory of a block's copies: two runs a lane of x, and of dy.
-template <typename T, int P, bool GRAD>
+template <typename T, int P, int CH, bool GRAD>
 constexpr size_t ring_bytes() {
-  return P > 1 ? (size_t)kDepth * kWarps * 32 * P * sizeof(T) * (GRAD ? 4 : 2) : 0;
+  return P * sizeof(T) >= 4 ? (size_t)kDepth * kWarps * 32 * CH * P * sizeof(T) * (GRAD ? 4 : 2)
+                            : 0;
 }
 
 // GROUP: the lanes of a head where they are known (16 and 32 bytes a lane of heads of 64
@@ -287,14 +292,14 @@ __global__ void __launch_bounds__(32 * kWarps, GRAD ? kGradPerSm : kPerSm)
   Place<T, P, PAIRS> at[CH];
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
-    at[c].set(p, c * 32 + li);
+    at[c].set(p, c * group + li);
     if (!here) at[c].has = at[c].has2 = false;
   }
   const int share = li * P;  // its pairs in the table of angles
   const float* mine = &weights[which == 0 ? 0 : 1][0][share];
   auto weight = [&](int c, Pairs<P>& g) {
-    from_shared<P>(mine + 32 * P * c, g.a);
-    from_shared<P>(mine + kMaxPairs + 32 * P * c, g.b);
+    from_shared<P>(mine + group * P * c, g.a);
+    from_shared<P>(mine + kMaxPairs + group * P * c, g.b);
   };
   // where the head starts in the tensors' first row
   const bool reads = !GRAD || p.norm;
@@ -311,19 +316,23 @@ __global__ void __launch_bounds__(32 * kWarps, GRAD ? kGradPerSm : kPerSm)
   // One token's loads; with copies into slot k of the lane, and of the warp for the position.
   extern __shared__ uint4 ring[];
   __shared__ int at_pos[kWarps][kDepth], at_row[kWarps][kDepth];
-  constexpr bool copies = P > 1;
-  constexpr int runs = GRAD ? 4 : 2;
+  constexpr bool copies = sizeof(R) >= 4;
+  constexpr int runs = (GRAD ? 4 : 2) * CH;
   R* slots = reinterpret_cast<R*>(ring) + warp * kDepth * runs * 32 + lane;
   auto fetch = [&](int64_t t, int k) {
     if constexpr (copies) {
       constexpr int bytes = sizeof(R);
       R* to = slots + k * runs * 32;
       if (t < p.T) {
-        if (reads && at[0].has) copy_async<bytes>(to, x + at[0].at);
-        if (reads && at[0].has2) copy_async<bytes>(to + 32, x + at[0].at2);
-        if constexpr (GRAD) {
-          if (at[0].has) copy_async<bytes>(to + 64, d + at[0].at);
-          if (at[0].has2) copy_async<bytes>(to + 96, d + at[0].at2);
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+          R* mine = to + c * (GRAD ? 128 : 64);
+          if (reads && at[c].has) copy_async<bytes>(mine, x + at[c].at);
+          if (reads && at[c].has2) copy_async<bytes>(mine + 32, x + at[c].at2);
+          if constexpr (GRAD) {
+            if (at[c].has) copy_async<bytes>(mine + 64, d + at[c].at);
+            if (at[c].has2) copy_async<bytes>(mine + 96, d + at[c].at2);
+          }
         }
         if (lane == 0 && p.pos) copy_async<4>(&at_pos[warp][k], p.pos + t);
         if (lane == 0 && !GRAD && p.rows) copy_async<4>(&at_row[warp][k], p.rows + t);
@@ -361,8 +370,11 @@ __global__ void __launch_bounds__(32 * kWarps, GRAD ? kGradPerSm : kPerSm)
       pos = p.pos ? at_pos[warp][slot] : (int)t;
       row = !GRAD && p.rows && which > 0 ? at_row[warp][slot] : (int)t;
       const R* have = slots + slot * runs * 32;
-      xu[0] = have[0], xv[0] = have[32];
-      if constexpr (GRAD) du[0] = have[64], dv[0] = have[96];
+#pragma unroll
+      for (int c = 0; c < CH; ++c, have += GRAD ? 128 : 64) {
+        xu[c] = have[0], xv[c] = have[32];
+        if constexpr (GRAD) du[c] = have[64], dv[c] = have[96];
+      }
     } else {
       __syncwarp();
     }
@@ -412,7 +424,7 @@ __global__ void __launch_bounds__(32 * kWarps, GRAD ? kGradPerSm : kPerSm)
       if (kept && which < 2) {
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-          turn_by<P>(&cosines[warp][32 * P * c + share], &sines[warp][32 * P * c + share], false,
+          turn_by<P>(&cosines[warp][group * P * c + share], &sines[warp][group * P * c + share], false,
                      u[c]);
           at[c].put(out, u[c]);
         }
@@ -421,7 +433,7 @@ __global__ void __launch_bounds__(32 * kWarps, GRAD ? kGradPerSm : kPerSm)
       // du = R^T dy; h = x r; g' = du g; dx = r (g' - h mean(g' h)); dg = sum du h
 #pragma unroll
       for (int c = 0; c < CH; ++c)
-        turn_by<P>(&cosines[warp][32 * P * c + share], &sines[warp][32 * P * c + share], true,
+        turn_by<P>(&cosines[warp][group * P * c + share], &sines[warp][group * P * c + share], true,
                    e[c]);
       if (p.norm) {
         float2 s2 = make_float2(0.f, 0.f), m2 = s2;
@@ -466,7 +478,7 @@ __global__ void __launch_bounds__(32 * kWarps, GRAD ? kGradPerSm : kPerSm)
       float u[2 * P];
       Place<T, P, PAIRS>::join(sum[c], u, u + P);
       Place<T, P, PAIRS> own;  // the channels, whether or not this lane's head exists
-      own.set(p, c * 32 + li);
+      own.set(p, c * group + li);
 #pragma unroll
       for (int j = 0; j < 2 * P; ++j) {
         float a = here && which == 0 ? u[j] : 0.f, b = here && which == 1 ? u[j] : 0.f;
@@ -552,7 +564,7 @@ cudaError_t go(RopeArgs& a, int64_t* blocks, cudaStream_t st) {
   a.passes = (a.heads + a.kv + (a.values ? a.kv : 0) + a.side - 1) / a.side;
   *blocks = GRAD ? grad_blocks(a.T, a.passes) : blocks_of(a.T, a.passes, kPerSm);
   auto kernel = rope_kernel<T, P, CH, PAIRS, GRAD, GROUP>;
-  constexpr size_t smem = ring_bytes<T, P, GRAD>();
+  constexpr size_t smem = ring_bytes<T, P, CH, GRAD>();
   static PerDevice once;
   const cudaError_t e = once.get([&] {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -571,35 +583,42 @@ cudaError_t by_group(RopeArgs& a, int64_t* blocks, cudaStream_t st) {
 
 template <typename T, bool GRAD>
 cudaError_t pick(const RopePlan& R, RopeArgs& a, int64_t* blocks, cudaStream_t st) {
-  auto shape = [&](int P) {
+  auto shape = [&](int P, int CH) {
     a.turned = R.rot / 2 / P;
     a.chunks = a.turned + (R.dim - R.rot + 2 * P - 1) / (2 * P);
     // a power of two, whose sums take fewer exchanges, unless more heads fit without
     // it (4099 x 20 heads of 80 in f32, ten lanes a head: 29.3 us by sixteens)
-    a.group = a.chunks > 32 ? 32 : pow2_above(a.chunks);
-    if (a.chunks <= 32 && 32 / a.chunks > 32 / a.group) a.group = a.chunks;
+    const int lanes = (a.chunks + CH - 1) / CH;
+    a.group = pow2_above(lanes);
+    if (32 / lanes > 32 / a.group) a.group = lanes;
     a.side = 32 / a.group;
   };
   // 16 bytes a run (f32 with eight pairs a lane, 32 bytes: 4099 x 20 heads of 80 26.3 ->
   // 28.6 us)
   if constexpr (sizeof(T) == 2) {
     if (fits(R, a, 8, GRAD)) {
-      shape(8);
+      shape(8, 1);
       return R.inter ? by_group<T, 8, true, GRAD>(a, blocks, st)
                      : by_group<T, 8, false, GRAD>(a, blocks, st);
     }
   }
   if (fits(R, a, 4, GRAD)) {
-    shape(4);
+    shape(4, 1);
     return R.inter ? by_group<T, 4, true, GRAD>(a, blocks, st)
                    : by_group<T, 4, false, GRAD>(a, blocks, st);
   }
-  shape(1);
-  if (R.inter)
-    return a.chunks <= 32 ? go<T, 1, 1, true, GRAD, 0>(a, blocks, st)
-                          : go<T, 1, 4, true, GRAD, 0>(a, blocks, st);
-  return a.chunks <= 32 ? go<T, 1, 1, false, GRAD, 0>(a, blocks, st)
-                        : go<T, 1, 4, false, GRAD, 0>(a, blocks, st);
+  // Halves of a rotation, or rests, that four do not divide: runs of two or one, with eight
+  // values a lane all the same, so that a warp holds as many heads (backward of 20000 x 24
+  // heads of 40 in bf16: 20 channels rotated 71 us with one run a lane, 41 with two; ten
+  // channels 212 with one, 55 with four)
+  if (fits(R, a, 2, GRAD)) {
+    shape(2, 2);
+    return R.inter ? go<T, 2, 2, true, GRAD, 0>(a, blocks, st)
+                   : go<T, 2, 2, false, GRAD, 0>(a, blocks, st);
+  }
+  shape(1, 4);
+  return R.inter ? go<T, 1, 4, true, GRAD, 0>(a, blocks, st)
+                 : go<T, 1, 4, false, GRAD, 0>(a, blocks, st);
 }
 
 void fill(const RopePlan& R, int64_t T, const int32_t* pos, RopeArgs* a) {

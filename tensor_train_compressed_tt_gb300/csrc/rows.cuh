@@ -34,6 +34,12 @@ struct Raw<float, 8> {
   }
 };
 template <>
+struct Raw<float, 2> {
+  float2 v;
+  __device__ void get(float* f) const { f[0] = v.x, f[1] = v.y; }
+  __device__ void set(const float* f) { v = make_float2(f[0], f[1]); }
+};
+template <>
 struct Raw<float, 1> {
   float v;
   __device__ void get(float* f) const { f[0] = v; }
@@ -69,6 +75,15 @@ struct Raw<__nv_bfloat16, 8> {
     v = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
                    pack_bf16(f[6], f[7]));
   }
+};
+template <>
+struct Raw<__nv_bfloat16, 2> {
+  uint32_t v;
+  __device__ void get(float* f) const {
+    f[0] = __uint_as_float(v << 16);
+    f[1] = __uint_as_float(v & 0xFFFF0000u);
+  }
+  __device__ void set(const float* f) { v = pack_bf16(f[0], f[1]); }
 };
 template <>
 struct Raw<__nv_bfloat16, 1> {
