@@ -631,10 +631,11 @@ cudaError_t fwd_pick(const NormFwdArgs& a, cudaStream_t st) {
                      dim3((unsigned)(a.T < most ? a.T : most)), dim3(kWideThreads), 0, st, false,
                      a);
   }
-  int w = fwd_warps(N);
+  const int w = fwd_warps(N);
   // one by one with dropout 32 values a lane leave no registers: four warps from 513 on
   // (20000 x 1023 bf16 124 -> 77 us, f32 141 -> 76)
-  if (V == 1 && a.drop.rng && N > 512 && w == 1) w = 4;
+  if constexpr (V == 1)
+    if (a.drop.rng && N > 512 && w == 1) return fwd_launch<T, 1, 8, 4, true, 1, true>(a, st);
   const int e = (N + 32 * w - 1) / (32 * w);  // values a thread
   if (w == 1) {
     if (e <= 8) return fwd_go<T, V, 8 / V, 1>(a, st);
@@ -642,8 +643,6 @@ cudaError_t fwd_pick(const NormFwdArgs& a, cudaStream_t st) {
     if (e <= 24) return fwd_go<T, V, 24 / V, 1>(a, st);
     return fwd_go<T, V, 32 / V, 1>(a, st);
   }
-  if constexpr (V == 1)
-    if (w == 4 && e <= 8) return fwd_go<T, 1, 8, 4>(a, st);
   if (w == 4) return fwd_go<T, V, 16 / V, 4>(a, st);
   if (w == 8) return fwd_go<T, V, 16 / V, 8>(a, st);
   return w == 16 ? fwd_go<T, V, 16 / V, 16>(a, st) : fwd_go<T, V, 16 / V, 32>(a, st);

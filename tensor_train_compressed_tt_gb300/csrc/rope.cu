@@ -517,10 +517,10 @@ int pow2_above(int n) {
   return g;
 }
 
-// Blocks of T tokens of `passes` warps each: the fewest that keep the most that fit on
-// the SMs for the same number of tokens a warp.
-int64_t blocks_of(int64_t T, int64_t passes, int per_sm) {
-  const int64_t most = (int64_t)device_sms() * per_sm * kWarps;  // warps
+// Blocks for T tokens of `passes` warps each, `fit` of which stay on the SMs: as few as
+// give every warp no more tokens than that many would.
+int64_t blocks_of(int64_t T, int64_t passes, int64_t fit) {
+  const int64_t most = fit * kWarps;                             // warps
   int64_t side = most / passes;                                  // tokens side by side
   if (side < 1) side = 1;
   const int64_t rounds = (T + side - 1) / side;
@@ -530,14 +530,15 @@ int64_t blocks_of(int64_t T, int64_t passes, int per_sm) {
 
 // A backward of few heads in all runs as one block: a second launch for the partial
 // sums would cost more.
-int64_t grad_blocks(int64_t T, int64_t passes) {
-  return T * passes <= 4 * kWarps && passes <= kWarps ? 1 : blocks_of(T, passes, kGradPerSm);
+int64_t grad_blocks(int64_t T, int64_t passes, int64_t fit) {
+  return T * passes <= 4 * kWarps && passes <= kWarps ? 1 : blocks_of(T, passes, fit);
 }
 // For any number of heads side by side in a warp: no fewer warps a token than this.
 int64_t most_grad_blocks(const RopePlan& R, int64_t T) {
+  const int64_t fit = (int64_t)device_sms() * kGradPerSm;
   int64_t most = 1;
   for (int side = 1; side <= 32; ++side) {
-    const int64_t b = grad_blocks(T, (R.heads + R.kv + side - 1) / side);
+    const int64_t b = grad_blocks(T, (R.heads + R.kv + side - 1) / side, fit);
     if (b > most) most = b;
   }
   return most;
@@ -562,7 +563,9 @@ bool fits(const RopePlan& R, const RopeArgs& a, int P, bool grad) {
 template <typename T, int P, int CH, bool PAIRS, bool GRAD, int GROUP>
 cudaError_t go(RopeArgs& a, int64_t* blocks, cudaStream_t st) {
   a.passes = (a.heads + a.kv + (a.values ? a.kv : 0) + a.side - 1) / a.side;
-  *blocks = GRAD ? grad_blocks(a.T, a.passes) : blocks_of(a.T, a.passes, kPerSm);
+  const int64_t sms = device_sms();
+  *blocks = GRAD ? grad_blocks(a.T, a.passes, sms * kGradPerSm)
+                 : blocks_of(a.T, a.passes, sms * kPerSm);
   auto kernel = rope_kernel<T, P, CH, PAIRS, GRAD, GROUP>;
   constexpr size_t smem = ring_bytes<T, P, CH, GRAD>();
   static PerDevice once;
