@@ -622,6 +622,7 @@ tt_status tt_set_wait_limit_ns(uint64_t ns);
 #define TT_DEBUG_ATTN_FWD 4
 #define TT_DEBUG_ATTN_BWD_QUERIES 5 /* the backward's pass over queries (dq) */
 #define TT_DEBUG_ATTN_BWD_KEYS 6    /* its pass over keys (dk, dv) */
+#define TT_DEBUG_LOGP_LOSS 7 /* tt_logp_loss of many rows of 24 to 108 KB: the first never loaded */
 tt_status tt_debug_skip_arrival(int site);
 
 /* Synchronise stream, then read and clear the status word of the current

@@ -15,11 +15,17 @@
 // for two values than c x - c r), so a log probability is as exact at logits of a
 // thousand as at logits of one, and logits of the type's lowest value do not overflow.
 //
-// A row is taken by 1 to 32 warps by its width; rows that are few or long are
-// split over a cluster's CTAs, which meet through shared memory.  Rows start
-// anywhere: the elements before the first and after the last 16-byte boundary are
-// taken one by one.  The pass that also writes the gradient keeps the row in shared
-// memory in between (each thread its own values), so it reads it from HBM once.
+// A row is taken by 1 to 32 warps by its width; rows that are few are split over a
+// cluster's CTAs, which meet through shared memory.  Rows start anywhere: the elements
+// before the first and after the last 16-byte boundary are taken one by one.  The pass
+// that also writes the gradient keeps the row in shared memory in between, so it reads it
+// from HBM once; of many rows of 24 to 108 KB a block keeps a ring that asynchronous copies
+// fill.
+//
+// Measured in bf16 (of the 6.7 TB/s that a copy reaches): forward 4096 x 50001 67 us, 6.1
+// TB/s, with the entropy 69, with four top alternatives as well 87; loss and gradient 8192
+// x 32000 163 us, 6.4 TB/s (in one pass a block a row 191); 4096 x 50001 139; 2048 x 131072,
+// a row an SM, 225 us, 4.8 TB/s; gradient alone 2048 x 131072 171 us, 6.3 TB/s.
 //
 // Top alternatives: the maxima of 128 groups of threads give a bound (the k-th
 // largest of them, to 16 bits: at least k values are not below it); the few groups that
@@ -42,12 +48,21 @@ cudaError_t read_and_clear_logp_status(DeviceStatus* out) {
   return cudaMemcpyToSymbol(g_status, &z, sizeof(z));
 }
 
+cudaError_t logp_set_wait_limit(unsigned long long ns) {
+  return cudaMemcpyToSymbol(g_wait_limit_ns, &ns, sizeof(ns));
+}
+
+cudaError_t logp_set_debug_skip(int site) {
+  return cudaMemcpyToSymbol(g_debug_skip, &site, sizeof(site));
+}
+
 namespace {
 
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kLog2e = 1.4426950408889634074f;
 constexpr int kRowsPerBlock = 8;  // of one warp each
 constexpr int kMaxCluster = 8;
+constexpr int kMaxSlots = 8;  // of the ring of rows
 constexpr int kMaxTop = 64;
 constexpr int kGroups = 128;      // of threads, for the bound of the top values
 constexpr int kList = 512;        // candidates; a cluster's kMaxTop each fit too
@@ -199,6 +214,13 @@ __device__ __forceinline__ void grad_of(float* f, float off, float c, float A, f
     }
     f[i] = e.x, f[i + 1] = e.y;
   }
+}
+
+// The target's log probability: 0 without one, -infinity where its logit is (or every one).
+__device__ __forceinline__ float log_p(bool there, float x, float s, float ref, float scale,
+                                       float logs) {
+  if (!there) return 0.f;
+  return s == 0.f || x == -INFINITY ? -INFINITY : fmaf(x - ref, scale, -kLn2 * logs);
 }
 
 template <int W>
@@ -534,9 +556,7 @@ __global__ void __launch_bounds__(W == 1 ? 32 * kRowsPerBlock : 32 * W, kept_blo
   if (tid == 0 && rank == 0) {
     if (p.lse) p.lse[row] = sw.x == 0.f ? -INFINITY : fmaf(ref, p.scale, kLn2 * logs);
     if (p.logp)
-      p.logp[row] = target < 0                                 ? 0.f
-                    : sw.x == 0.f || picked == -INFINITY ? -INFINITY
-                                                         : fmaf(picked - ref, p.scale, -kLn2 * logs);
+      p.logp[row] = log_p(target >= 0, picked, sw.x, ref, p.scale, logs);
     if (ENT && p.ent) p.ent[row] = ent;
   }
 
@@ -606,6 +626,216 @@ __global__ void __launch_bounds__(W == 1 ? 32 * kRowsPerBlock : 32 * W, kept_blo
     }
   }
   if (W >= 8 && p.cluster > 1) cluster_meet();  // no CTA leaves while another reads its shares
+}
+
+// Both of many rows that fit on an SM at least twice: a block an SM with a ring of rows in
+// shared memory.  A row comes by one asynchronous copy of its whole vectors while the rows
+// before it are worked on, so the block reads memory all the time (8192 x 32000: blocks that
+// each load, sum and write in turn, three an SM, 191 us).  TEAMS teams of W warps take the
+// block's rows in turn, so that one sums while another waits for its warps to meet (one team
+// of 16 warps 201 us, two 163).
+template <typename T, bool ENT, int TEAMS, int W>
+__global__ void __launch_bounds__(32 * W * TEAMS, 1)
+    logp_ring_kernel(LogpArgs p, int slots, int slot_bytes) {
+  constexpr int VEC = 16 / sizeof(T), G = 32 * W;
+  using R = Raw<T, VEC>;
+  extern __shared__ __align__(128) uint8_t rows[];
+  __shared__ uint64_t full[kMaxSlots];
+  // each warp's reference and sums, and whether its team stops, of every other row
+  __shared__ float4 share[TEAMS][2][W];
+  __shared__ int abort_flag, sent[kMaxSlots];  // the last of the block's rows sent to a slot
+  const int team = threadIdx.x / G, tid = threadIdx.x % G, warp = tid >> 5, lane = tid & 31;
+  auto team_sync = [&] {
+    if (TEAMS == 1)
+      __syncthreads();
+    else
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(G) : "memory");
+  };
+  if (threadIdx.x == 0) {
+    for (int k = 0; k < slots; ++k) mbar_init(&full[k], 1), sent[k] = -1;
+    abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncthreads();
+  pdl_wait();
+  pdl_trigger();
+  auto row_at = [&](int64_t row, Cut& cut) {
+    const T* x = static_cast<const T*>(p.x) + row * p.stride;
+    cut.set<T, VEC>(x, p.V);
+    return x;
+  };
+  // the block's row n to its slot
+  auto send = [&](int n, int slot) {
+    const int64_t row = blockIdx.x + (int64_t)n * gridDim.x;
+    if (row >= p.T) return;
+    __threadfence_block();
+    *(volatile int*)&sent[slot] = n;
+    if (n == 0 && blockIdx.x == 0 && debug_take(TT_DEBUG_LOGP_LOSS)) return;
+    Cut cut;
+    const T* x = row_at(row, cut);
+    const uint32_t bytes = (uint32_t)(cut.vecs * sizeof(R));
+    mbar_expect_tx(&full[slot], bytes);
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+            "r"(su32(rows + slot * slot_bytes)),
+        "l"(x + cut.head), "r"(bytes), "r"(su32(&full[slot]))
+        : "memory");
+  };
+  // Row n is in its slot (false: the wait ran out, or another one did).  The row before it in
+  // that slot may be another team's and not even have come: until n is sent the barrier is
+  // a phase behind, whose parity is that of the phase after n's.
+  auto arrived = [&](int n, int slot, uint32_t parity) {
+    int ok = 0;
+    if (lane == 0) {
+      const uint64_t t0 = gtimer();
+      const uint64_t limit = *(volatile unsigned long long*)&g_wait_limit_ns;
+      while (!(ok = *(volatile int*)&sent[slot] == n)) {
+        if (*(volatile int*)&abort_flag) break;
+        if (gtimer() - t0 > limit) {
+          *(volatile int*)&abort_flag = 1;
+          record_error(TT_ERR_TIMEOUT, 0x701);
+          break;
+        }
+      }
+      __threadfence_block();
+      ok = ok && wait_bar(&full[slot], parity, &abort_flag, 0x700);
+    }
+    return __shfl_sync(0xffffffffu, ok, 0) != 0;
+  };
+  if (threadIdx.x == 0)
+    for (int k = 0; k < slots; ++k) send(k, k);
+  int n = team;
+  int64_t row = blockIdx.x + (int64_t)n * gridDim.x;
+  const int64_t step = (int64_t)TEAMS * gridDim.x;
+  // what of a row does not come by the copy: asked for a row ahead
+  Cut cut;
+  float lone = 0.f, g = 0.f, h = 0.f;
+  int target = -1;
+  auto ahead = [&](int64_t r) {
+    if (r >= p.T) return;
+    const T* x = row_at(r, cut);
+    if (tid < cut.edges) reinterpret_cast<const Raw<T, 1>*>(x)[cut.edge<VEC>(tid)].get(&lone);
+    target = p.targets ? p.targets[r] : -1;
+    g = p.dlogp ? p.dlogp[r] : 0.f;
+    h = ENT && p.dent ? p.dent[r] : 0.f;
+  };
+  ahead(row);
+  const float c = p.c;
+  int slot = team, flip = 0;
+  uint32_t parity = 0;
+  for (; row < p.T; row += step, n += TEAMS, flip ^= 1) {
+    const Cut at = cut;
+    const float mine = lone, h1 = h;
+    int goal = target;
+    if (goal >= p.V) {
+      if (tid == 0) record_error(TT_ERR_DEVICE, 2);
+      goal = -1;
+    }
+    const float g1 = goal >= 0 ? g : 0.f;
+    ahead(row + step);
+    const R* have = reinterpret_cast<const R*>(rows + slot * slot_bytes);
+    Sums<ENT> sum;
+    if (tid < at.edges) sum.one(mine, c);
+    if (arrived(n, slot, parity)) {
+      int v = tid;
+      for (; v + (kAhead - 1) * G < at.vecs; v += kAhead * G) {
+        R r[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) r[k] = have[v + k * G];
+        sum.template add<T, VEC, kAhead>(r, c);
+      }
+#pragma unroll
+      for (int k = 0; k < kAhead - 1; ++k)
+        if (v + k * G < at.vecs) {
+          const R r = have[v + k * G];
+          sum.template add<T, VEC, 1>(&r, c);
+        }
+    }
+    // the warp's sums, then the block's
+    auto meet = [&](Sums<ENT>& a, int most) {
+      float top = a.ref;
+      for (int o = most / 2; o; o >>= 1)
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      if (a.ref > -INFINITY && a.ref != top) a.scale((a.ref - top) * c);
+      a.ref = top;
+      a.s.x += a.s.y;
+      a.w.x += a.w.y;
+      for (int o = most / 2; o; o >>= 1) {
+        a.s.x += __shfl_xor_sync(0xffffffffu, a.s.x, o);
+        if (ENT) a.w.x += __shfl_xor_sync(0xffffffffu, a.w.x, o);
+      }
+    };
+    meet(sum, 32);
+    if (lane == 0)
+      share[team][flip][warp] =
+          make_float4(sum.ref, sum.s.x, sum.w.x, *(volatile int*)&abort_flag ? 1.f : 0.f);
+    // the target's logit: from the copy, or from beside it before dx (which may be x) is written
+    const int in_copy = goal - at.head;
+    const bool copied = goal >= 0 && in_copy >= 0 && in_copy < at.vecs * VEC;
+    float picked = 0.f;
+    if (tid == 0 && goal >= 0 && !copied)
+      (static_cast<const Raw<T, 1>*>(p.x) + row * p.stride + goal)->get(&picked);
+    team_sync();
+    const float4 all = share[team][flip][lane & (W - 1)];
+    // the other team may give up at any time: what this one's warps saw decides for all of it
+    if (__any_sync(0xffffffffu, all.w != 0.f)) break;
+    Sums<ENT> one;
+    one.ref = all.x;
+    one.s.x = all.y;
+    one.w.x = all.z;
+    meet(one, W);
+    const float ref = one.ref > -INFINITY ? one.ref : 0.f, s = one.s.x;
+    const float logs = log2f(s);
+    const float ent = s == 0.f ? 0.f : kLn2 * (logs - one.w.x / s);
+    if (tid == 0) {
+      if (copied) (reinterpret_cast<const Raw<T, 1>*>(have) + in_copy)->get(&picked);
+      if (p.lse) p.lse[row] = s == 0.f ? -INFINITY : fmaf(ref, p.scale, kLn2 * logs);
+      if (p.logp)
+        p.logp[row] = log_p(goal >= 0, picked, s, ref, p.scale, logs);
+      if (ENT && p.ent) p.ent[row] = ent;
+    }
+    T* dx = static_cast<T*>(p.dx) + row * p.dstride;
+    R* out = reinterpret_cast<R*>(dx + at.head);
+    const bool none = (g1 == 0.f && h1 == 0.f) || s == 0.f;
+    const float inv = 1.f / s;
+    const float A = -p.scale * fmaf(h1, ent - kLn2 * logs, g1) * inv;
+    const float B = -p.scale * kLn2 * h1 * inv;
+    if (tid < at.edges) {
+      const int i = at.edge<VEC>(tid);
+      float d = mine;
+      grad_of<1, ENT>(&d, -ref, c, A, B);
+      if (i == goal) d = fmaf(p.scale, g1, d);
+      if (none) d = 0.f;
+      reinterpret_cast<Raw<T, 1>*>(dx)[i].set(&d);
+    }
+    const int there = goal >= at.head ? (goal - at.head) / VEC : -1;
+    if (none) {
+      for (int v = tid; v < at.vecs; v += G) out[v] = R{};
+    } else {
+#pragma unroll 2
+      for (int v = tid; v < at.vecs; v += G) {
+        float f[VEC];
+        have[v].get(f);
+        grad_of<VEC, ENT>(f, -ref, c, A, B);
+        if (v == there) {
+#pragma unroll
+          for (int j = 0; j < VEC; ++j)
+            if (at.head + v * VEC + j == goal) f[j] = fmaf(p.scale, g1, f[j]);
+        }
+        R o;
+        o.set(f);
+        out[v] = o;
+      }
+    }
+    team_sync();  // the slot is read
+    if (tid == 0) send(n + slots, slot);
+    slot += TEAMS;
+    if (slot >= slots) slot -= slots, parity ^= 1;
+  }
+  __syncthreads();
+  if (abort_flag && threadIdx.x == 0)  // the copies on their way end before the block does
+    for (int k = 0; k < slots; ++k)
+      if (sent[k] >= 0) drain_bar(&full[k], sent[k] / slots & 1);
 }
 
 // The gradient alone, from the row's log-sum and entropy: a block a piece of a row
@@ -725,11 +955,26 @@ cudaError_t go(LogpArgs& a, cudaStream_t st) {
                        : launch_ex(kernel, grid, dim3(threads), smem, st, false, a);
 }
 
-// Warps of a row by its vectors: a warp alone to eight a lane, then four warps, whose
-// barrier costs little.  A long row that stays in shared memory for its gradient leaves
-// room for two others on the SM, and 16 warps each keep it busy where eight do not (8192
-// x 32000 203.5 -> 196.7 us); above 108 KB it has the SM to itself, with 32 warps, and
-// what exceeds the shared memory is read again from L2.
+template <typename T, bool ENT, int TEAMS, int W>
+cudaError_t ring_go(const LogpArgs& a, int slots, size_t bytes, cudaStream_t st) {
+  auto kernel = logp_ring_kernel<T, ENT, TEAMS, W>;
+  static PerDevice once;
+  const cudaError_t e = once.get([&] {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)kStageBytes);
+  });
+  if (e != cudaSuccess) return e;
+  return launch_ex(kernel, dim3((unsigned)device_sms()), dim3(32 * W * TEAMS),
+                   slots * bytes, st, false, a, slots, (int)bytes);
+}
+
+// Warps of a row by its vectors: a warp alone to sixteen a lane (16384 x 1000 bf16 with
+// four warps 24.0 us, with one 10.7), then four warps, whose barrier costs little.  With a
+// gradient, rows above 24 KB that are many go by the ring: in two slots by one team, three
+// or four by two, more by four (16384 x 13000 a block a row 212 us, by the ring 140; 8192 x
+// 32000 191 and 163; 16384 x 8000, 16 KB a row, 99 and 112).  Others stay in shared memory
+// with 16 warps each, above 108 KB with 32 on an SM of its own, and what exceeds the shared
+// memory is read again from L2 (2048 x 131072 in clusters of four 371 us, so 225).
 template <typename T, int VEC, bool ENT, bool TOP, bool GRAD>
 cudaError_t by_width(LogpArgs& a, cudaStream_t st) {
   const int64_t vecs = a.V / VEC;
@@ -737,6 +982,15 @@ cudaError_t by_width(LogpArgs& a, cudaStream_t st) {
     if (vecs <= 512) return go<T, VEC, 1, ENT, TOP, GRAD>(a, st);
   if (vecs <= 1536) return go<T, VEC, 4, ENT, TOP, GRAD>(a, st);
   if constexpr (GRAD) {
+    const size_t bytes = ((size_t)vecs * sizeof(Raw<T, VEC>) + 127) / 128 * 128;
+    if constexpr (VEC > 1)
+      if (2 * bytes <= kStageBytes && a.T >= 4 * (int64_t)device_sms()) {
+        const int slots = (int)(kStageBytes / bytes);
+        return slots >= 5   ? ring_go<T, ENT, 4, 8>(a, slots < kMaxSlots ? slots : kMaxSlots,
+                                                  bytes, st)
+               : slots >= 3 ? ring_go<T, ENT, 2, 16>(a, slots, bytes, st)
+                            : ring_go<T, ENT, 1, 16>(a, slots, bytes, st);
+      }
     if (a.V * (int64_t)sizeof(T) > (108 << 10) && cluster_of<16>(a.T, vecs) == 1)
       return go<T, VEC, 32, ENT, TOP, GRAD>(a, st);
     return go<T, VEC, 16, ENT, TOP, GRAD>(a, st);
@@ -891,7 +1145,8 @@ tt_status tt_logp_loss(const tt_plan_t* plan, int64_t T, const void* logits, int
   LogpArgs a;
   if (!common_ok(plan, T, logits, stride, targets, &a) || dstride < a.V ||
       dstride > (int64_t)1 << 31 || ((dlogp || logp) && !targets) ||
-      (T > 0 && ((!dlogp && !dentropy) || !dlogits)) || !aligned_to(logp, 4) || !aligned_to(lse, 4) ||
+      (T > 0 && ((!dlogp && !dentropy) || !dlogits)) || !aligned_to(logp, 4) ||
+      !aligned_to(lse, 4) ||
       !aligned_to(entropy, 4) || !aligned_to(dlogp, 4) || !aligned_to(dentropy, 4) ||
       !aligned_to(dlogits, plan->logits.act == TT_DT_F32 ? 4 : 2))
     return TT_ERR_INVALID_ARG;

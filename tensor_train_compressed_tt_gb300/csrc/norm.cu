@@ -168,7 +168,8 @@ struct Keep<1, CH, G> {
       uint32_t stay = 0;
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        stay |= (uint32_t)(v[j] << 16 >= d.cut) << (2 * j) | (uint32_t)(v[j] >= d.cut) << (2 * j + 1);
+        stay |= (uint32_t)(v[j] << 16 >= d.cut) << (2 * j) |
+                (uint32_t)(v[j] >= d.cut) << (2 * j + 1);
       bytes[8 * c + k] = d.all ? 0 : (uint8_t)stay;
     }
     __syncwarp();

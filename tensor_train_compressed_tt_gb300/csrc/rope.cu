@@ -424,17 +424,18 @@ __global__ void __launch_bounds__(32 * kWarps, GRAD ? kGradPerSm : kPerSm)
       if (kept && which < 2) {
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-          turn_by<P>(&cosines[warp][group * P * c + share], &sines[warp][group * P * c + share], false,
-                     u[c]);
+          const int i = group * P * c + share;
+          turn_by<P>(&cosines[warp][i], &sines[warp][i], false, u[c]);
           at[c].put(out, u[c]);
         }
       }
     } else {
       // du = R^T dy; h = x r; g' = du g; dx = r (g' - h mean(g' h)); dg = sum du h
 #pragma unroll
-      for (int c = 0; c < CH; ++c)
-        turn_by<P>(&cosines[warp][group * P * c + share], &sines[warp][group * P * c + share], true,
-                   e[c]);
+      for (int c = 0; c < CH; ++c) {
+        const int i = group * P * c + share;
+        turn_by<P>(&cosines[warp][i], &sines[warp][i], true, e[c]);
+      }
       if (p.norm) {
         float2 s2 = make_float2(0.f, 0.f), m2 = s2;
 #pragma unroll

@@ -1328,15 +1328,17 @@ extern "C" tt_status tt_set_wait_limit_ns(uint64_t ns) {
   if (ns < 1000) return TT_ERR_INVALID_ARG;
   const unsigned long long v = ns;
   return cudaMemcpyToSymbol(ttc::g_wait_limit_ns, &v, sizeof(v)) == cudaSuccess &&
-                 ttc::attn_set_wait_limit(v) == cudaSuccess
+                 ttc::attn_set_wait_limit(v) == cudaSuccess &&
+                 ttc::logp_set_wait_limit(v) == cudaSuccess
              ? TT_OK
              : TT_ERR_CUDA;
 }
 
 extern "C" tt_status tt_debug_skip_arrival(int site) {
-  if (site < 0 || site > TT_DEBUG_ATTN_BWD_KEYS) return TT_ERR_INVALID_ARG;
+  if (site < 0 || site > TT_DEBUG_LOGP_LOSS) return TT_ERR_INVALID_ARG;
   return cudaMemcpyToSymbol(ttc::g_debug_skip, &site, sizeof(site)) == cudaSuccess &&
-                 ttc::attn_set_debug_skip(site) == cudaSuccess
+                 ttc::attn_set_debug_skip(site) == cudaSuccess &&
+                 ttc::logp_set_debug_skip(site) == cudaSuccess
              ? TT_OK
              : TT_ERR_CUDA;
 }

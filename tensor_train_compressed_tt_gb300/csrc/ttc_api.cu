@@ -1382,7 +1382,8 @@ tt_status tt_get_device_status(void* stream) {
   if (read_and_clear_attn_status(&a) != cudaSuccess) return TT_ERR_CUDA;
   if (read_and_clear_rope_status(&r) != cudaSuccess) return TT_ERR_CUDA;
   if (read_and_clear_logp_status(&l) != cudaSuccess) return TT_ERR_CUDA;
-  if (h.code == TT_ERR_TIMEOUT || a.code == TT_ERR_TIMEOUT) return TT_ERR_TIMEOUT;
+  if (h.code == TT_ERR_TIMEOUT || a.code == TT_ERR_TIMEOUT || l.code == TT_ERR_TIMEOUT)
+    return TT_ERR_TIMEOUT;
   if (h.code != 0 || e.code != 0 || a.code != 0 || r.code != 0 || l.code != 0) return TT_ERR_DEVICE;
   return TT_OK;
 }

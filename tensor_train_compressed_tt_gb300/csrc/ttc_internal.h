@@ -151,6 +151,9 @@ cudaError_t read_and_clear_logp_status(DeviceStatus* out);
 cudaError_t read_and_clear_attn_status(DeviceStatus* out);
 cudaError_t attn_set_wait_limit(unsigned long long ns);
 cudaError_t attn_set_debug_skip(int site);
+// Those of the ring of rows (logp.cu).
+cudaError_t logp_set_wait_limit(unsigned long long ns);
+cudaError_t logp_set_debug_skip(int site);
 
 // ---- rank-adaptive step (rank_update.cu) ------------------------------------
 // One elementwise launch of the step over a layer's packed params / dparams.

@@ -586,6 +586,7 @@ TT_DEBUG_MERGE_BARRIER = 3
 TT_DEBUG_ATTN_FWD = 4
 TT_DEBUG_ATTN_BWD_QUERIES = 5
 TT_DEBUG_ATTN_BWD_KEYS = 6
+TT_DEBUG_LOGP_LOSS = 7
 
 
 def tt_set_wait_limit_ns(ns: int) -> int:

@@ -343,11 +343,83 @@ def test_results_repeat_on_streams_and_in_a_graph():
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("row_bytes,pad", [(24800, 0), (30000, 1), (50002, 0), (70000, 3),
+                                           (100000, 1)])
+def test_loss_of_many_rows(row_bytes, pad, act):
+    """Rows that a block keeps a ring of, in two, three or more slots and by one, two or four
+    teams; from rows without a target, masked and special ones, and in place."""
+    from tensor_train_compressed_tt_gb300.layer import TTLogProbs
+    size = {"f32": 4, "bf16": 2}[act]
+    T, V = 700, row_bytes // size
+    r = np.random.default_rng(row_bytes)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(row_bytes)
+    x = torch.randn(T, V + pad, generator=g, device="cuda").mul_(3).to(DT[act])
+    x[3], x[4, V // 2:], x[5], x[699] = -np.inf, -np.inf, 0, 7
+    whole, x = x, x[:, :V]  # a gradient laid out otherwise would not go by the ring
+    t = r.integers(0, V, T)
+    t[::5] = -1
+    t[6], t[7], t[4] = 0, V - 1, 1
+    d, h = r.standard_normal(T).astype(np.float32), r.standard_normal(T).astype(np.float32)
+    d[8], h[8] = 0, 0
+    op = TTLogProbs(V, DT[act], scale=0.9)
+    rows = np.r_[0:12, 150:156, 303:308, 600:606, 694:700]
+    for dent in (None, h):
+        e = None if dent is None else nan((T,), torch.float32)
+        out = torch.full_like(whole, float("nan"))[:, :V]
+        logp, lse, e, got = op.loss(x, _i32(t), _f32(d), None if dent is None else _f32(h),
+                                    entropy=e, dlogits=out)
+        some = lambda a: None if a is None else a[torch.from_numpy(rows).cuda()]  # noqa: E731
+        _check_fwd(some(x), t[rows], 0.9, 0, (some(logp), some(lse), some(e)))
+        _check_grad(some(x), t[rows], d[rows], None if dent is None else h[rows], 0.9, act,
+                    some(got), "dlogits")
+        # every row against the pass of its own, and in place
+        other = op.backward(x, _i32(t), lse, _f32(d), e, None if dent is None else _f32(h))
+        near = 2.0 ** -6 if act == "bf16" else 2.0 ** -14
+        keep = torch.isfinite(lse)
+        a, b = got[keep].double(), other[keep].double()
+        bound = near * b.abs() + 2.0 ** -14 * (torch.tensor(d).cuda()[keep].abs()
+                                              + torch.tensor(h).cuda()[keep].abs())[:, None]
+        assert ((a - b).abs() <= bound).all()
+        y = whole.clone()[:, :V]
+        logp2, lse2, _, _ = op.loss(y, _i32(t), _f32(d), None if dent is None else _f32(h),
+                                    dlogits=y)
+        assert torch.equal(y, got) and torch.equal(logp, logp2) and torch.equal(lse, lse2)
+    assert _status() == 0
+
+
+@pytest.mark.parametrize("V", [13000, 32000, 50000])
+def test_loss_wait_runs_out(V):
+    """A row that never comes: the block's teams leave, the status says so, and the next call
+    is right."""
+    from tensor_train_compressed_tt_gb300 import ttc
+    from tensor_train_compressed_tt_gb300.layer import TTLogProbs
+    T = 700
+    x = torch.randn(T, V, device="cuda").bfloat16()
+    t, g = torch.zeros(T, dtype=torch.int32, device="cuda"), torch.ones(T, device="cuda")
+    op = TTLogProbs(V)
+    want = op.loss(x, t, g)
+    torch.cuda.synchronize()
+    ttc.check(ttc.tt_set_wait_limit_ns(20_000_000), "limit")
+    try:
+        ttc.check(ttc.tt_debug_skip_arrival(ttc.TT_DEBUG_LOGP_LOSS), "hook")
+        op.loss(x, t, g)
+        assert _status() == 5 and _status() == 0
+        for a, b in zip(want, op.loss(x, t, g)):
+            assert a is None or torch.equal(a, b)
+        assert _status() == 0
+    finally:
+        torch.cuda.synchronize()
+        ttc.check(ttc.tt_set_wait_limit_ns(2_000_000_000), "limit")
+
+
 def test_wrapper_refuses():
     from tensor_train_compressed_tt_gb300.layer import TTLogProbs
     op = TTLogProbs(64, torch.float32)
     x, t, g = torch.zeros(4, 64, device="cuda"), _i32([0] * 4), _f32([0] * 4)
-    for bad in (x.bfloat16(), x[:, :32], x.t(), x.cpu(), torch.zeros(4, 128, device="cuda")[:, ::2]):
+    for bad in (x.bfloat16(), x[:, :32], x.t(), x.cpu(),
+                torch.zeros(4, 128, device="cuda")[:, ::2]):
         with pytest.raises(ValueError):
             op.forward(bad, t)
     for bad in (t.long(), t[:3], t.cpu()):

@@ -74,7 +74,8 @@ def test_dropout_plan_refuses(args, code):
 
 
 def test_plans_of_another_kind_are_refused():
-    rope, logp, drop = _rope(), ttc.tt_logp_plan(64, 1.0, 0, BF16), ttc.tt_dropout_plan(0.5, 0, BF16)
+    rope, logp = _rope(), ttc.tt_logp_plan(64, 1.0, 0, BF16)
+    drop = ttc.tt_dropout_plan(0.5, 0, BF16)
     norm = ttc.tt_norm_plan(64, 1e-5, BF16)
     h = ttc.tt_heads(OK, 64, 64)
     for p in (logp, drop, norm):
@@ -105,8 +106,10 @@ def test_plans_of_another_kind_are_refused():
 def test_rope_arguments():
     p, flat = _rope(), _rope(eps=0.0)
     h = ttc.tt_heads(OK, 256, 64)
-    fwd = lambda pl=p, T=4, pos=0, hs=(h,) * 4, gq=0, gk=0, v=None, vo=None, rows=0, n=0: \
-        ttc.tt_rope_forward(pl, T, pos, hs[0], hs[1], gq, gk, hs[2], hs[3], v, vo, rows, n)  # noqa: E731
+
+    def fwd(pl=p, T=4, pos=0, hs=(h,) * 4, gq=0, gk=0, v=None, vo=None, rows=0, n=0):
+        return ttc.tt_rope_forward(pl, T, pos, hs[0], hs[1], gq, gk, hs[2], hs[3], v, vo, rows, n)
+
     bads = (ttc.tt_heads(0, 256, 64), ttc.tt_heads(OK + 1, 256, 64), ttc.tt_heads(OK, -1, 64),
             ttc.tt_heads(OK, 256, -1))
     for kw in (dict(T=-1), dict(T=1 << 31), dict(pos=OK + 2), dict(gq=OK + 2), dict(gk=OK + 1),
@@ -122,8 +125,11 @@ def test_rope_arguments():
     none = ttc.tt_heads(0, 256, 64)
     assert fwd(T=0, hs=(none,) * 4) == 0
     ws = ttc.tt_workspace_size(p, 4)
-    bwd = lambda pl=p, T=4, hs=(h,) * 6, g=(0,) * 4, at=OK, n=ws: ttc.tt_rope_backward(  # noqa: E731
-        pl, T, 0, hs[0], hs[1], g[0], g[1], hs[2], hs[3], hs[4], hs[5], g[2], g[3], at, n)
+
+    def bwd(pl=p, T=4, hs=(h,) * 6, g=(0,) * 4, at=OK, n=ws):
+        return ttc.tt_rope_backward(pl, T, 0, hs[0], hs[1], g[0], g[1], hs[2], hs[3], hs[4], hs[5],
+                                    g[2], g[3], at, n)
+
     for bad in bads:
         for i in range(6):
             hs = [h] * 6
