@@ -25,7 +25,7 @@
 // Measured in bf16 (of the 6.7 TB/s that a copy reaches): forward 4096 x 50001 67 us, 6.1
 // TB/s, with the entropy 69, with four top alternatives as well 87; loss and gradient 8192
 // x 32000 163 us, 6.4 TB/s (in one pass a block a row 191); 4096 x 50001 139; 2048 x 131072,
-// a row an SM, 225 us, 4.8 TB/s; gradient alone 2048 x 131072 171 us, 6.3 TB/s.
+// a row an SM, 210 us, 5.1 TB/s; gradient alone 2048 x 131072 171 us, 6.3 TB/s.
 //
 // Top alternatives: the maxima of 128 groups of threads give a bound (the k-th
 // largest of them, to 16 bits: at least k values are not below it); the few groups that
@@ -63,6 +63,7 @@ constexpr float kLog2e = 1.4426950408889634074f;
 constexpr int kRowsPerBlock = 8;  // of one warp each
 constexpr int kMaxCluster = 8;
 constexpr int kMaxSlots = 8;  // of the ring of rows
+constexpr int kSentAhead = 256 << 10;  // bytes of a long row; those of all SMs stay in L2
 constexpr int kMaxTop = 64;
 constexpr int kGroups = 128;      // of threads, for the bound of the top values
 constexpr int kList = 512;        // candidates; a cluster's kMaxTop each fit too
@@ -440,23 +441,17 @@ __host__ __device__ constexpr int kept_blocks(int W, bool ent, bool more) {
   return W == 32 ? 1 : W == 16 ? 3 : (ent && more ? 40 : 48) / (W == 1 ? 8 : W);
 }
 
-// One row a team of W warps (a cluster of such blocks where p.cluster > 1).
+// One row by a team of W warps (or a cluster of such blocks where p.cluster > 1); `then` is
+// the team's next one.
 template <typename T, int VEC, int W, bool ENT, bool TOP, bool GRAD>
-__global__ void __launch_bounds__(W == 1 ? 32 * kRowsPerBlock : 32 * W, kept_blocks(W, ENT, GRAD))
-    logp_kernel(LogpArgs p) {
+__device__ __forceinline__ void logp_row(const LogpArgs& p, int64_t row, int64_t then, int rank,
+                                         int tid) {
   using R = Raw<T, VEC>;
   constexpr int G = 32 * W;
   extern __shared__ uint4 stage_bytes[];
   __shared__ float2 red[2][32];
   __shared__ float meet[3];
   __shared__ typename std::conditional<TOP, TopShared, int>::type top_shared;
-  const int tid = W == 1 ? threadIdx.x & 31 : threadIdx.x;
-  const int rank = W >= 8 ? blockIdx.x % p.cluster : 0;
-  const int64_t row = W == 1 ? (int64_t)blockIdx.x * kRowsPerBlock + (threadIdx.x >> 5)
-                             : (int64_t)blockIdx.x / p.cluster;
-  pdl_wait();
-  pdl_trigger();
-  if (row >= p.T) return;  // whole warps, and only where no barrier is met (W == 1)
   const T* x = static_cast<const T*>(p.x) + row * p.stride;
   Cut cut;
   cut.set<T, VEC>(x, p.V);
@@ -587,6 +582,16 @@ __global__ void __launch_bounds__(W == 1 ? 32 * kRowsPerBlock : 32 * W, kept_blo
   }
 
   if constexpr (GRAD) {
+    if (W == 32 && VEC > 1 && tid == 0 && then < p.T) {
+      // the row after this one comes to L2 while this one's gradient is written
+      const T* next = static_cast<const T*>(p.x) + then * p.stride;
+      Cut there;
+      there.set<T, VEC>(next, p.V);
+      const int bytes = min(there.vecs, kSentAhead / (int)sizeof(R)) * (int)sizeof(R);
+      asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(next + there.head),
+                   "r"(bytes)
+                   : "memory");
+    }
     if (W == 1) __syncwarp();  // dx may be x: the target's logit is read by now
     T* dx = static_cast<T*>(p.dx) + row * p.dstride;
     R* out = reinterpret_cast<R*>(dx + cut.head);
@@ -626,6 +631,23 @@ __global__ void __launch_bounds__(W == 1 ? 32 * kRowsPerBlock : 32 * W, kept_blo
     }
   }
   if (W >= 8 && p.cluster > 1) cluster_meet();  // no CTA leaves while another reads its shares
+}
+
+template <typename T, int VEC, int W, bool ENT, bool TOP, bool GRAD>
+__global__ void __launch_bounds__(W == 1 ? 32 * kRowsPerBlock : 32 * W, kept_blocks(W, ENT, GRAD))
+    logp_kernel(LogpArgs p) {
+  const int tid = W == 1 ? threadIdx.x & 31 : threadIdx.x;
+  pdl_wait();
+  pdl_trigger();
+  if constexpr (W == 32) {  // an SM's rows one after another
+    for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x)
+      logp_row<T, VEC, W, ENT, TOP, GRAD>(p, row, row + gridDim.x, 0, tid);
+  } else {
+    const int64_t row = W == 1 ? (int64_t)blockIdx.x * kRowsPerBlock + (threadIdx.x >> 5)
+                               : (int64_t)blockIdx.x / p.cluster;
+    if (row >= p.T) return;  // whole warps, and only where no barrier is met (W == 1)
+    logp_row<T, VEC, W, ENT, TOP, GRAD>(p, row, p.T, W >= 8 ? blockIdx.x % p.cluster : 0, tid);
+  }
 }
 
 // Both of many rows that fit on an SM at least twice: a block an SM with a ring of rows in
@@ -934,7 +956,7 @@ cudaError_t go(LogpArgs& a, cudaStream_t st) {
   constexpr int threads = W == 1 ? 32 * kRowsPerBlock : 32 * W;
   const int64_t rows = W == 1 ? (a.T + kRowsPerBlock - 1) / kRowsPerBlock : a.T;
   const int64_t vecs = a.V / VEC + 1;  // of a row, at most
-  a.cluster = W >= 8 ? cluster_of<W>(rows, vecs) : 1;
+  a.cluster = W == 8 || W == 16 ? cluster_of<W>(rows, vecs) : 1;
   size_t smem = 0;
   a.staged = 0;
   if (GRAD) {
@@ -949,8 +971,9 @@ cudaError_t go(LogpArgs& a, cudaStream_t st) {
     });
     if (e != cudaSuccess) return e;
   }
-  if (rows * a.cluster > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-  const dim3 grid((unsigned)(rows * a.cluster));
+  const int64_t blocks = W == 32 && rows > device_sms() ? device_sms() : rows * a.cluster;
+  if (blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+  const dim3 grid((unsigned)blocks);
   return a.cluster > 1 ? launch_cluster(kernel, grid, dim3(threads), smem, st, a.cluster, a)
                        : launch_ex(kernel, grid, dim3(threads), smem, st, false, a);
 }
@@ -974,7 +997,8 @@ cudaError_t ring_go(const LogpArgs& a, int slots, size_t bytes, cudaStream_t st)
 // or four by two, more by four (16384 x 13000 a block a row 212 us, by the ring 140; 8192 x
 // 32000 191 and 163; 16384 x 8000, 16 KB a row, 99 and 112).  Others stay in shared memory
 // with 16 warps each, above 108 KB with 32 on an SM of its own, and what exceeds the shared
-// memory is read again from L2 (2048 x 131072 in clusters of four 371 us, so 225).
+// memory is read again from L2 (2048 x 131072 in clusters of four 371 us, so 225, and 210 with
+// the next row sent for while a gradient is written; f32 4096 x 50001 361, 387 and 312).
 template <typename T, int VEC, bool ENT, bool TOP, bool GRAD>
 cudaError_t by_width(LogpArgs& a, cudaStream_t st) {
   const int64_t vecs = a.V / VEC;
