@@ -104,6 +104,18 @@ def test_in_place(act):
     assert torch.equal(a, y) and torch.equal(b, y)
 
 
+def test_elements_beyond_32_bits():
+    """2^32 + 77 elements: the groups' index keeps its high bits, first, middle and last."""
+    from tensor_train_compressed_tt_gb300.layer import TTDropout
+    n = (1 << 32) + 77
+    op = TTDropout(0.5, site=3)
+    x = torch.ones(n, dtype=torch.bfloat16, device="cuda")
+    op.forward(x, op.state(21), y=x)
+    for first in (0, (1 << 31) - 40, (1 << 32) - 40, n - 60):
+        keep = K.drop_bits(60, 21, 0, 3, first=first) >= 32768
+        assert np.array_equal(f64(x[first:first + 60]), 2.0 * keep)
+
+
 def test_a_graph_takes_the_offset_of_each_replay():
     from tensor_train_compressed_tt_gb300.layer import TTDropNorm, TTDropout
     r = np.random.default_rng(6)

@@ -414,6 +414,27 @@ def test_loss_wait_runs_out(V):
         ttc.check(ttc.tt_set_wait_limit_ns(2_000_000_000), "limit")
 
 
+@pytest.mark.parametrize("V", [100, 3001, 20001])
+def test_rows_beyond_32_bits(V):
+    """Rows 2^30 elements apart: the third begins behind 2^31."""
+    from tensor_train_compressed_tt_gb300.layer import TTLogProbs
+    stride = 1 << 30
+    flat = torch.empty(2 * stride + V, dtype=torch.bfloat16, device="cuda")
+    x = flat.as_strided((3, V), (stride, 1))
+    r = np.random.default_rng(V)
+    x.copy_(torch.from_numpy(r.standard_normal((3, V)).astype(np.float32)))
+    t, g = r.integers(0, V, 3), r.standard_normal(3).astype(np.float32)
+    op = TTLogProbs(V, top=5)
+    got = op.forward(x, _i32(t), entropy=nan((3,), torch.float32))
+    _check_fwd(x, t, 1.0, 5, got)
+    want = x.clone()
+    op.loss(x, _i32(t), _f32(g), dlogits=x)
+    _check_grad(want, t, g, None, 1.0, "bf16", x, "loss: dlogits")
+    x.copy_(want)
+    op.backward(x, _i32(t), got[1], _f32(g), dlogits=x)
+    _check_grad(want, t, g, None, 1.0, "bf16", x, "dlogits", given=True)
+
+
 def test_wrapper_refuses():
     from tensor_train_compressed_tt_gb300.layer import TTLogProbs
     op = TTLogProbs(64, torch.float32)

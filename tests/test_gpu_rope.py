@@ -223,6 +223,23 @@ def test_into_a_cache(T, heads, kv, dim, eps, act):
     assert int(torch.isnan(keys[:, 0, 0].float()).sum()) == n - (T - 3)
 
 
+@pytest.mark.parametrize("dim", [64, 33])
+def test_a_cache_beyond_32_bits(dim):
+    """Rows of the cache 2^26 + 8 elements apart: the last begins behind 2^31."""
+    r = np.random.default_rng(dim)
+    op = _plan(2, 2, dim, "bf16", rot=dim // 2 * 2)
+    n, step = 34, (1 << 26) + 8
+    flat = torch.empty(n * step, dtype=torch.bfloat16, device="cuda")
+    keys = flat.as_strided((n, 2, dim), (step, dim, 1))
+    values = flat.as_strided((n, 2, dim), (step, dim, 1), storage_offset=1 << 20)
+    q, k, v = (rand(r, (3, 2, dim), "bf16") for _ in range(3))
+    pos = torch.tensor([0, 9, 4], dtype=torch.int32, device="cuda")
+    rows = torch.tensor([33, 0, 32], dtype=torch.int32, device="cuda")
+    op.to_cache(q, k, v, pos, rows, keys, values)
+    want = op.forward(q, k, pos)[1]
+    assert torch.equal(keys[rows.long()], want) and torch.equal(values[rows.long()], v)
+
+
 @pytest.mark.parametrize("act", ["f32", "bf16"])
 @pytest.mark.parametrize("dim", [64, 33])
 def test_in_place(dim, act):
