@@ -196,6 +196,31 @@ def test_norm_token_counts(T, N, act):
 
 
 @pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("N", [8, 512, 768, 1024, 1028, 4096, 16384, 17000])
+def test_norm_weights_off_a_16_byte_boundary(N, act):
+    from tensor_train_compressed_tt_gb300.layer import TTDropNorm
+    r = np.random.default_rng(7)
+    T, op = 37, TTDropNorm(N, 0.25, DT[act], site=2)
+    rng = op.drop.state(4, 3)
+    f = K.drop_factor((T, N), 0.25, 4, 3, 2)
+    x, rs, dy = (rand(r, (T, N), act) for _ in range(3))
+    gamma, beta = rand(r, N + 1, "f32", 0.3, 1.0)[1:], rand(r, N + 1, "f32", 0.3)[1:]
+    assert gamma.data_ptr() % 16 and beta.data_ptr() % 16
+    y, s, st = op.forward(x, rng, gamma, beta, res=rs, y=nan((T, N), DT[act]),
+                          sum=nan((T, N), DT[act]), stats=nan((T, 2), torch.float32))
+    ry, rsum, rst = B.norm_forward(f64(x) * f, f64(gamma), f64(beta), f64(rs))
+    assert_near(f64(y), ry, NORM_TOL[act], "y")
+    assert_near(f64(s), rsum, NORM_TOL[act], "sum")
+    assert_near(f64(st), rst, 1e-5, "stats")
+    _, _, st = op.norm.forward(s)  # the statistics of the rounded sum
+    dx, _, dg, db = op.backward(s, dy, rng, gamma, st, dx=nan((T, N), DT[act]))
+    rx, rg, rb = B.norm_backward(f64(s), f64(dy), f64(gamma))
+    assert_near(f64(dx), rx * f, NORM_TOL[act], "dx")
+    assert_near(f64(dg), rg, 1e-5, "dgamma")
+    assert_near(f64(db), rb, 1e-5, "dbeta")
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
 @pytest.mark.parametrize("N", [768, 1023, 17000])
 def test_norm_without_residual_and_weights(N, act):
     _norm_case(20, N, act, res=False, affine=False)
