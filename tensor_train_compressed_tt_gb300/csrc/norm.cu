@@ -651,11 +651,18 @@ cudaError_t fwd_pick(const NormFwdArgs& a, cudaStream_t st) {
 
 template <typename T, int VEC, int CH, int W>
 cudaError_t bwd_go(const NormBwdArgs& a, int64_t blocks, cudaStream_t st) {
-  const dim3 grid((unsigned)blocks), block(32 * W * bwd_groups(W));
+  const dim3 grid((unsigned)blocks);
   if constexpr (VEC < 8)
     if (!a.drop.rng)
-      return launch_ex(norm_bwd_kernel<T, VEC, CH, W, false>, grid, block, 0, st, false, a);
-  return launch_ex(norm_bwd_kernel<T, VEC, CH, W, true>, grid, block, 0, st, false, a);
+      return launch_ex(norm_bwd_kernel<T, VEC, CH, W, false>, grid, dim3(32 * W * bwd_groups(W)),
+                       0, st, false, a);
+  // fp32 with dropout: sixteen values a thread, the next row's and the draws' words spill;
+  // eight a thread in twice the warps do not (20000 rows of 512 64 -> 40 us, of 1024 121 ->
+  // 71, of 2048 248 -> 141; twelve a thread as they are: of 768 57 us, split 61)
+  constexpr bool kSplit = sizeof(T) == 4 && VEC == 4 && CH == 4 && W <= 4;
+  constexpr int W2 = kSplit ? 2 * W : W;
+  return launch_ex(norm_bwd_kernel<T, VEC, kSplit ? 2 : CH, W2, true>, grid,
+                   dim3(32 * W2 * bwd_groups(W2)), 0, st, false, a);
 }
 
 template <typename T, int V>
