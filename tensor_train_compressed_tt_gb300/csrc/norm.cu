@@ -606,7 +606,8 @@ cudaError_t fwd_launch(const NormFwdArgs& a, cudaStream_t st) {
 }
 template <typename T, int VEC, int CH, int W>
 cudaError_t fwd_go(const NormFwdArgs& a, cudaStream_t st) {
-  if (a.drop.rng) return fwd_launch<T, VEC, CH, W, true, 1, true>(a, st);
+  if constexpr (VEC > 1 || W > 1 || CH <= 16)  // fwd_pick takes four warps for the others
+    if (a.drop.rng) return fwd_launch<T, VEC, CH, W, true, 1, true>(a, st);
   // Without a residual, and with rows enough for every block, two rows at a time:
   // the weights are read from L1 once for both (their 8 bytes a value, against 2
   // from memory, took 78 % of the L1's rate) and each barrier serves both.  bf16,
@@ -656,10 +657,11 @@ cudaError_t bwd_go(const NormBwdArgs& a, int64_t blocks, cudaStream_t st) {
     if (!a.drop.rng)
       return launch_ex(norm_bwd_kernel<T, VEC, CH, W, false>, grid, dim3(32 * W * bwd_groups(W)),
                        0, st, false, a);
-  // fp32 with dropout: sixteen values a thread, the next row's and the draws' words spill;
-  // eight a thread in twice the warps do not (20000 rows of 512 64 -> 40 us, of 1024 121 ->
-  // 71, of 2048 248 -> 141; twelve a thread as they are: of 768 57 us, split 61)
-  constexpr bool kSplit = sizeof(T) == 4 && VEC == 4 && CH == 4 && W <= 4;
+  // With dropout sixteen values a thread, the next row's and the draws' words spill in
+  // fp32; eight a thread in twice the warps do not (20000 rows of 512 64 -> 40 us, of 1024
+  // 121 -> 71, of 2048 248 -> 141; twelve a thread as they are: of 768 57 us, split 61).
+  // bf16 by fours is quicker so too (of 1004 65 -> 58), by eights not (of 1024 46 -> 49).
+  constexpr bool kSplit = VEC == 4 && CH == 4 && W <= 4;
   constexpr int W2 = kSplit ? 2 * W : W;
   return launch_ex(norm_bwd_kernel<T, VEC, kSplit ? 2 : CH, W2, true>, grid,
                    dim3(32 * W2 * bwd_groups(W2)), 0, st, false, a);
@@ -674,7 +676,8 @@ cudaError_t bwd_pick(const NormBwdArgs& a, int64_t blocks, cudaStream_t st) {
       if (V > 1 && N <= 256) return bwd_go<T, V, 8 / V, 1>(a, blocks, st);
       return bwd_go<T, V, E / V, 1>(a, blocks, st);
     case 2:
-      if (V > 1 && V < 8 && N <= 768) return bwd_go<T, V, V < 8 ? 12 / V : 1, 2>(a, blocks, st);
+      if constexpr (V > 1 && V < 8)
+        if (N <= 768) return bwd_go<T, V, 12 / V, 2>(a, blocks, st);
       return bwd_go<T, V, E / V, 2>(a, blocks, st);
     case 4: return bwd_go<T, V, E / V, 4>(a, blocks, st);
     case 8: return bwd_go<T, V, E / V, 8>(a, blocks, st);
