@@ -532,6 +532,7 @@ int64_t blocks_of(int64_t T, int64_t passes, int64_t fit) {
 // A backward of few heads in all runs as one block: a second launch for the partial
 // sums would cost more.
 int64_t grad_blocks(int64_t T, int64_t passes, int64_t fit) {
+  if (T < 1) return 1;
   return T * passes <= 4 * kWarps && passes <= kWarps ? 1 : blocks_of(T, passes, fit);
 }
 // For any number of heads side by side in a warp: no fewer warps a token than this.
