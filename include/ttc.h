@@ -500,8 +500,9 @@ tt_status tt_rope_forward(const tt_plan_t* plan, int64_t T, const int32_t* pos,
  * may be NULL, and both are without a norm).  q and k are the forward's inputs, not
  * read without a norm.  dq may be dq_out or q, dk dk_out or k (the same strides).
  * Sums over tokens and heads are taken in a fixed order: the same inputs give the
- * same bits on a given GPU model.  Workspace: tt_workspace_size(plan, T) bytes, 256-byte
- * aligned (none without a norm).  T == 0 writes zero dgq and dgk (or leaves them). */
+ * same bits on a given GPU model.  Workspace: tt_workspace_size(plan, T) bytes or more (it
+ * never falls as T grows), 256-byte aligned (none without a norm).  T == 0 writes zero dgq
+ * and dgk (or leaves them). */
 tt_status tt_rope_backward(const tt_plan_t* plan, int64_t T, const int32_t* pos,
                            const tt_heads* q, const tt_heads* k, const float* gq,
                            const float* gk, const tt_heads* dq_out, const tt_heads* dk_out,

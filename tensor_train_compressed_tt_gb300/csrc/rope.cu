@@ -532,15 +532,19 @@ int64_t blocks_of(int64_t T, int64_t passes, int64_t fit) {
 // A backward of few heads in all runs as one block: a second launch for the partial
 // sums would cost more.
 int64_t grad_blocks(int64_t T, int64_t passes, int64_t fit) {
-  if (T < 1) return 1;
   return T * passes <= 4 * kWarps && passes <= kWarps ? 1 : blocks_of(T, passes, fit);
 }
-// For any number of heads side by side in a warp: no fewer warps a token than this.
+// No launch of T tokens or fewer has more blocks, with any number of heads side by side in a
+// warp.  blocks_of evens out the tokens of its warps, so that one token more can halve its
+// blocks (24 heads of 64: 303 for 101 tokens, 153 for 102): this bound leaves the evening out
+// and never falls, and a workspace serves every batch up to the one that it was made for.
 int64_t most_grad_blocks(const RopePlan& R, int64_t T) {
-  const int64_t fit = (int64_t)device_sms() * kGradPerSm;
+  const int64_t warps = (int64_t)device_sms() * kGradPerSm * kWarps;
   int64_t most = 1;
   for (int side = 1; side <= 32; ++side) {
-    const int64_t b = grad_blocks(T, (R.heads + R.kv + side - 1) / side, fit);
+    const int64_t passes = (R.heads + R.kv + side - 1) / side;
+    const int64_t beside = warps / passes < 1 ? 1 : warps / passes;  // tokens side by side
+    const int64_t b = ((T < beside ? T : beside) * passes + kWarps - 1) / kWarps;
     if (b > most) most = b;
   }
   return most;
