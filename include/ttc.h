@@ -559,8 +559,10 @@ tt_status tt_norm_dropout_backward(const tt_plan_t* plan, const tt_plan_t* dropo
  * A negative target stands for none: logp = 0 and no gradient of it.  A target of V
  * or more is taken as none and recorded in the device status word (TT_ERR_DEVICE).
  * A logit of -infinity has p = 0; a row of nothing else gives lse = -infinity,
- * entropy 0, logp -infinity and zero gradients.  A NaN or +infinity makes the row's
- * results NaN (its top indices are valid, their order is not given).  All sums are fp32.
+ * entropy 0, logp -infinity and zero gradients.  An lse beyond fp32's range is the infinity
+ * of its sign; the row's other results are those of its logits.  A NaN or +infinity makes
+ * the row's results NaN (its top indices are valid, their order is not given).  All sums are
+ * fp32.
  * Row t of the logits starts at logits[t stride], at any multiple of the element;
  * columns from V on are not read (nor written, in dlogits). */
 typedef struct tt_logp_desc {
@@ -582,6 +584,9 @@ tt_status tt_logp_forward(const tt_plan_t* plan, int64_t T, const void* logits, 
 /* dlogits of L = sum_t dlogp logp + dentropy entropy, from the forward's lse (and entropy
  * where dentropy is given; one of the two gradients may be NULL):
  *   dlogits_v = scale (dlogp ([v = target] - p_v) - dentropy p_v (z_v - lse + entropy)).
+ * lse is rounded to fp32, which a weight p_v feels by 2^-24 |lse| of itself.  A row of
+ * |lse| above 256 (f32) or 4096 (bf16), infinities among them, has its sum taken again from
+ * the logits, so rows of large finite masks have the gradient of tt_logp_loss.
  * dlogits may be logits (the same strides). */
 tt_status tt_logp_backward(const tt_plan_t* plan, int64_t T, const void* logits, int64_t stride,
                            const int32_t* targets, const float* lse, const float* dlogp,

@@ -860,11 +860,89 @@ __global__ void __launch_bounds__(32 * W * TEAMS, 1)
       if (sent[k] >= 0) drain_bar(&full[k], sent[k] / slots & 1);
 }
 
+// The largest |lse| that the gradient alone takes its weights from.  Rounded to fp32 an lse is
+// off by 2^-24 of itself, and the weight by as much in proportion: 2^-16 here in f32, in bf16
+// 2^-12, an eighth of the gradient's own half step.  Beyond it (rows whose every logit is a
+// mask of -1e9: lse comes in steps of 64 and has lost log V; log-sums beyond the type's range)
+// the row's sum is taken again, as the pass that makes both has it.
+template <typename T>
+constexpr float kFarLse = sizeof(T) == 2 ? 4096.f : 256.f;
+constexpr int kGradThreads = 256;
+
+// Such a row by one warp or one block (dx may be x, whose values the sum is of), a vector a
+// thread at a time, which leaves the other rows their registers (2048 x 131072 bf16 163 us,
+// one row in sixteen far 213, all of them 340).
+template <typename T, int VEC, bool SHORT, bool ENT>
+__device__ __forceinline__ void logp_far_row(const LogpArgs& p, int64_t row) {
+  using R = Raw<T, VEC>;
+  constexpr int G = SHORT ? 32 : kGradThreads, W = G / 32;
+  __shared__ float2 red[2][32];
+  const int tid = threadIdx.x % G;
+  const float c = p.c, scale = p.scale;
+  const T* x = static_cast<const T*>(p.x) + row * p.stride;
+  T* dx = static_cast<T*>(p.dx) + row * p.dstride;
+  int target = p.targets ? p.targets[row] : -1;
+  if (target >= p.V) {
+    if (tid == 0) record_error(TT_ERR_DEVICE, 2);
+    target = -1;
+  }
+  const float g = target >= 0 && p.dlogp ? p.dlogp[row] : 0.f;
+  const float h = ENT ? p.dent[row] : 0.f;
+  const float A = ENT ? -scale * fmaf(h, p.ent_in[row], g) : -scale * g, B = -scale * h;
+  Cut cut;
+  cut.set<T, VEC>(x, p.V);
+  const R* body = reinterpret_cast<const R*>(x + cut.head);
+  R* out = reinterpret_cast<R*>(dx + cut.head);
+  Sums<false> sum;
+  float lone = 0.f;
+  if (tid < cut.edges) {
+    reinterpret_cast<const Raw<T, 1>*>(x)[cut.edge<VEC>(tid)].get(&lone);
+    sum.one(lone, c);
+  }
+#pragma unroll 1
+  for (int v = tid; v < cut.vecs; v += G) {
+    const R r = body[v];
+    sum.template add<T, VEC, 1>(&r, c);
+  }
+  const float most = team_max<W>(sum.ref, red);
+  if (sum.ref > -INFINITY && sum.ref != most) sum.scale((sum.ref - most) * c);
+  const float s = team_sum<W>(make_float2(sum.s.x + sum.s.y, 0.f), red).x;
+  const float ref = most > -INFINITY ? most : 0.f, less = -kLn2 * log2f(s);
+  auto grad = [&](float f, int i) {
+    const float lp = fmaf(f - ref, scale, less);
+    const float d = ex2(lp * kLog2e) * (ENT ? fmaf(B, fmaxf(lp, -256.f), A) : A);
+    return s == 0.f ? 0.f : i == target ? fmaf(scale, g, d) : d;  // 0: no logit above -infinity
+  };
+  // each thread the elements that it read before
+  if (tid < cut.edges) {
+    const int i = cut.edge<VEC>(tid);
+    lone = grad(lone, i);
+    reinterpret_cast<Raw<T, 1>*>(dx)[i].set(&lone);
+  }
+#pragma unroll 1
+  for (int v = tid; v < cut.vecs; v += G) {
+    float f[VEC];
+    body[v].get(f);
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) f[j] = grad(f[j], cut.head + v * VEC + j);
+    R o;
+    o.set(f);
+    out[v] = o;
+  }
+}
+
+// Blocks that an SM keeps, by registers; only far rows spill.  Without a limit their code takes
+// the other rows' registers: with the entropy bf16 2048 x 131072 171 -> 179 us, 16384 x 2500 55
+// -> 66; f32 2048 x 65536 without it 154 -> 159 (five blocks: 173, 58, 164).
+__host__ __device__ constexpr int grad_blocks(int vec, bool brief, bool ent) {
+  return vec == 1 ? 8 : brief ? 4 : vec == 4 && !ent ? 7 : 6;
+}
+
 // The gradient alone, from the row's log-sum and entropy: a block a piece of a row
 // (a warp a row where rows are short).
-constexpr int kGradThreads = 256;
 template <typename T, int VEC, bool SHORT, bool ENT>
-__global__ void __launch_bounds__(kGradThreads) logp_grad_kernel(LogpArgs p, int pieces) {
+__global__ void __launch_bounds__(kGradThreads, grad_blocks(VEC, SHORT, ENT))
+    logp_grad_kernel(const __grid_constant__ LogpArgs p, int pieces) {
   using R = Raw<T, VEC>;
   constexpr int G = SHORT ? 32 : kGradThreads;
   const int tid = SHORT ? threadIdx.x & 31 : threadIdx.x;
@@ -888,28 +966,25 @@ __global__ void __launch_bounds__(kGradThreads) logp_grad_kernel(LogpArgs p, int
   const float lse = p.lse_in[row];
   const float g = target >= 0 && p.dlogp ? p.dlogp[row] : 0.f;
   const float h = ENT ? p.dent[row] : 0.f;
-  const bool none = (g == 0.f && h == 0.f) || lse == -INFINITY;
+  const bool none = g == 0.f && h == 0.f;
   const float A = ENT ? -p.scale * fmaf(h, p.ent_in[row], g) : -p.scale * g, B = -p.scale * h;
   auto grad = [&](float f) {
     const float lp = fmaf(f, p.scale, -lse);
-    return none ? 0.f : ex2(lp * kLog2e) * (ENT ? fmaf(B, fmaxf(lp, -256.f), A) : A);
+    return ex2(lp * kLog2e) * (ENT ? fmaf(B, fmaxf(lp, -256.f), A) : A);
   };
-  if (piece == 0 && tid < cut.edges) {
-    const int i = cut.edge<VEC>(tid);
-    float d;
-    reinterpret_cast<const Raw<T, 1>*>(x)[i].get(&d);
-    d = grad(d);
-    if (i == target && !none) d = fmaf(p.scale, g, d);
-    reinterpret_cast<Raw<T, 1>*>(dx)[i].set(&d);
-  }
   const int there = target >= cut.head ? (target - cut.head) / VEC : -1;
   const int first = SHORT ? 0 : piece * kAhead * G;
   const int last = SHORT ? cut.vecs : min(cut.vecs, first + kAhead * G);
+  float lone = 0.f;
+  const bool edge = piece == 0 && tid < cut.edges;
+  if (edge) reinterpret_cast<const Raw<T, 1>*>(x)[cut.edge<VEC>(tid)].get(&lone);
+  const bool far = !none && fabsf(lse) > kFarLse<T>;
   for (int v = first + tid; v < last; v += kAhead * G) {
     R r[kAhead];
 #pragma unroll
     for (int k = 0; k < kAhead; ++k)
       if (v + k * G < last) r[k] = body[v + k * G];
+    if (none || far) break;  // asked behind the loads, which do not wait for lse
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
       const int at = v + k * G;
@@ -918,7 +993,7 @@ __global__ void __launch_bounds__(kGradThreads) logp_grad_kernel(LogpArgs p, int
       r[k].get(f);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) f[j] = grad(f[j]);
-      if (at == there && !none) {
+      if (at == there) {
 #pragma unroll
         for (int j = 0; j < VEC; ++j)
           if (cut.head + at * VEC + j == target) f[j] = fmaf(p.scale, g, f[j]);
@@ -927,6 +1002,19 @@ __global__ void __launch_bounds__(kGradThreads) logp_grad_kernel(LogpArgs p, int
       o.set(f);
       out[at] = o;
     }
+  }
+  if (far) {
+    if (piece == 0) logp_far_row<T, VEC, SHORT, ENT>(p, row);
+    return;
+  }
+  if (none)
+    for (int v = first + tid; v < last; v += G) out[v] = R{};
+  if (edge) {
+    const int i = cut.edge<VEC>(tid);
+    float d = grad(lone);
+    if (i == target) d = fmaf(p.scale, g, d);
+    if (none) d = 0.f;
+    reinterpret_cast<Raw<T, 1>*>(dx)[i].set(&d);
   }
 }
 

@@ -1,4 +1,5 @@
-"""Ends of the ranges of rotary positions, log probabilities and dropout on the GPU."""
+"""Ends of the ranges of rotary positions, log probabilities and dropout on the GPU against the
+fp64 oracle, at the bounds of their other tests (test_gpu_rope, test_gpu_logp)."""
 
 import numpy as np
 import pytest
@@ -7,7 +8,9 @@ pytestmark = pytest.mark.gpu
 
 torch = pytest.importorskip("torch")
 
-from token_util import rand  # noqa: E402
+from tensor_train_compressed_tt_gb300.layer import TTLogProbs  # noqa: E402
+from test_gpu_logp import _check_grad, _f32, _i32, _rows, _status  # noqa: E402
+from token_util import DT, nan, rand  # noqa: E402
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -35,3 +38,52 @@ def test_rope_workspace_of_the_most_tokens_serves_fewer(heads, kv):
         want = op.backward(dq, dk, None, q, k)
         for a, b in zip(op.backward(dq, dk, None, q, k, ws=ws), want):
             assert torch.equal(a, b)
+
+
+def _far_rows(V, act, r):
+    """Rows whose log-sum is so large that its rounding to fp32 loses some or all of the
+    logarithm of the sum, between ordinary ones."""
+    x = r.standard_normal((12, V))
+    x[1] = -1e9                          # a finite mask on everything
+    x[2], x[2, V // 2] = -1e9, 3.0       # and on all but one
+    x[3] = -3e38
+    x[4] = 3e38
+    x[5] += 7000.0
+    x[6] -= 300.0
+    x[7] = 1e9 + 128.0 * r.integers(0, 2, V)
+    x[8] = -np.inf
+    x[9], x[9, ::2] = -20000.0, -np.inf  # half of it masked, the rest equal
+    x[10], x[10, V - 1] = -3e38, 3e38
+    return x
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("scale", [1.0, 2.5])
+@pytest.mark.parametrize("V,pad,shift,dpad", [
+    (2, 0, 0, 0), (13, 1, 0, 1), (700, 0, 0, 0), (3001, 1, 3, 1), (3000, 0, 0, 1), (40001, 7, 1, 7),
+    (100, 0, 1, 3)])
+def test_gradient_where_the_log_sum_is_large(V, pad, shift, dpad, scale, act):
+    """From the forward's lse, which at 1e9 is rounded to 64: the weights are the row's own all
+    the same, as tt_logp_loss has them, and sum to one.  With scale 2.5 the log-sums of the
+    type's ends are infinite.  The bounds are those of the pass that rounds nothing between."""
+    r = np.random.default_rng(V)
+    x = _rows(_far_rows(V, act, r), act, pad, shift)
+    T = x.shape[0]
+    t = r.integers(0, V, T)
+    t[4], t[6], t[9] = -1, 0, V - 1
+    g, h = r.standard_normal(T).astype(np.float32), r.standard_normal(T).astype(np.float32)
+    op = TTLogProbs(V, DT[act], scale=scale)
+    ent = nan((T,), torch.float32)
+    _, lse, _, _, _ = op.forward(x, _i32(t), entropy=ent)
+    for dent in (None, h):
+        d = _rows(np.full((T, V), np.nan), act, dpad, shift)
+        args = (_f32(g), ent if dent is not None else None, None if dent is None else _f32(dent))
+        op.backward(x, _i32(t), lse, *args, dlogits=d)
+        _check_grad(x, t, g, dent, scale, act, d, "dlogits")
+        if dpad == pad:  # in place
+            whole = x.as_strided((T, V + pad), (V + pad, 1), x.storage_offset())
+            y = torch.empty(T * (V + pad) + shift, dtype=DT[act], device="cuda")[shift:]
+            y = y.view(T, V + pad).copy_(whole)[:, :V]
+            op.backward(y, _i32(t), lse, *args, dlogits=y)
+            assert torch.equal(y, d)
+    assert _status() == 0
