@@ -217,11 +217,13 @@ __device__ __forceinline__ void grad_of(float* f, float off, float c, float A, f
   }
 }
 
-// The target's log probability: 0 without one, -infinity where its logit is (or every one).
+// The target's log probability: 0 without one, -infinity where its logit is (or every one) in
+// a row whose sum is a number.
 __device__ __forceinline__ float log_p(bool there, float x, float s, float ref, float scale,
                                        float logs) {
   if (!there) return 0.f;
-  return s == 0.f || x == -INFINITY ? -INFINITY : fmaf(x - ref, scale, -kLn2 * logs);
+  return s == 0.f || (x == -INFINITY && s == s) ? -INFINITY
+                                                : fmaf(x - ref, scale, -kLn2 * logs);
 }
 
 template <int W>
@@ -577,7 +579,7 @@ __device__ __forceinline__ void logp_row(const LogpArgs& p, int64_t row, int64_t
       const uint64_t e = top_shared.best[tid];
       const float f = of_key((uint32_t)(e >> 32));
       p.ids[row * p.top + tid] = (int)~(uint32_t)e;
-      p.tops[row * p.top + tid] = f == -INFINITY ? f : fmaf(f - ref, p.scale, -kLn2 * logs);
+      p.tops[row * p.top + tid] = log_p(true, f, sw.x, ref, p.scale, logs);
     }
   }
 

@@ -87,3 +87,25 @@ def test_gradient_where_the_log_sum_is_large(V, pad, shift, dpad, scale, act):
             op.backward(y, _i32(t), lse, *args, dlogits=y)
             assert torch.equal(y, d)
     assert _status() == 0
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("T,V", [(6, 40), (6, 3000), (6, 40000), (6, 131072), (700, 14000),
+                                 (310, 60001)])
+def test_masked_targets_of_rows_that_are_not_finite(T, V, act):
+    """A NaN or +infinity makes the whole row's results NaN, also of a target or an alternative
+    whose logit is -infinity; without one those are -infinity."""
+    x = torch.randn(T, V, device="cuda").to(DT[act])
+    x[:, 8:] = -float("inf")
+    x[1, 3], x[2, 4] = float("nan"), float("inf")
+    t = torch.full((T,), V - 1, dtype=torch.int32, device="cuda")
+    op = TTLogProbs(V, DT[act], top=20)
+    logp, lse, _, ids, tops = op.forward(x, t)
+    logp2 = op.loss(x, t, torch.ones(T, device="cuda"))[0]
+    bad = torch.zeros(T, dtype=torch.bool, device="cuda")
+    bad[1:3] = True
+    for a in (logp, logp2):
+        assert torch.isnan(a[bad]).all() and (a[~bad] == -float("inf")).all()
+    assert torch.isnan(lse[bad]).all() and torch.isnan(tops[bad]).all()
+    assert torch.isfinite(tops[~bad][:, :8]).all() and (tops[~bad][:, 8:] == -float("inf")).all()
+    assert int(ids.min()) >= 0 and int(ids.max()) < V
