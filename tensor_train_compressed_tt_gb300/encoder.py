@@ -29,7 +29,7 @@ import torch
 
 from . import synth, ttc
 from .layer import (TTAttention, TTDropNorm, TTFFN, TTLinear, TTLogProbs, TTMulti, TTNorm,
-                    TTRotary, TTSeqs)
+                    TTRotary, TTSeqs, _filled)
 
 PROJ = ("q", "k", "v", "o")
 QKV = ("q", "k", "v")
@@ -128,7 +128,8 @@ class TTTransformerBlock(TTEncoderBlock):
     rotary: Q h1 and K h1 pass through it in front of the attention, at the tokens'
     positions pos (int32; None: their rows, which serves packed sequences as well, where
     the distances alone count).  With a norm, params may hold its weights gq, gk, whose
-    gradients are b["dgq"], b["dgk"].
+    gradients are b["dgq"], b["dgk"] (of a rotary with accumulate the sums over the steps,
+    from zeros on).
     dropout: of x and of a in front of their sums, in a pass that is given the state rng
     (TTDropout.state; None: nothing is dropped).  The block takes the sites `site` and
     `site` + 1."""
@@ -162,8 +163,8 @@ class TTTransformerBlock(TTEncoderBlock):
             for nm in ("rq", "rk"):
                 b[nm] = torch.empty((T, self.N), dtype=torch.bfloat16, device=device)
             if self.rotary.norm:
-                for nm in ("dgq", "dgk"):
-                    b[nm] = torch.empty(self.attn.dim, dtype=torch.float32, device=device)
+                for nm in ("dgq", "dgk"):  # zeros where the rotary adds to them
+                    b[nm] = _filled((self.attn.dim,), torch.float32, device, self.rotary.fill)
             b["ws_rope"] = self.rotary.workspace(T, device)
         if self.drops is not None:
             for nm in ("dx", "da"):

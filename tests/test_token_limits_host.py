@@ -5,7 +5,9 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from tensor_train_compressed_tt_gb300 import ttc  # noqa: E402
+from tensor_train_compressed_tt_gb300 import layer, ttc  # noqa: E402
+from tensor_train_compressed_tt_gb300.encoder import TTTransformerBlock  # noqa: E402
+from tensor_train_compressed_tt_gb300.layer import TTRotary, TTSeqs  # noqa: E402
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -24,3 +26,16 @@ def test_rope_workspace_of_no_tokens(heads, kv):
     """An empty batch has a workspace of a size, whatever the number of heads."""
     assert 0 < ttc.tt_workspace_size(_rope(heads, kv), 0) <= \
         ttc.tt_workspace_size(_rope(heads, kv), 1)
+
+
+def test_a_block_with_an_accumulating_rotary_starts_at_zero(monkeypatch):
+    """The block's buffers of gradients that are added to hold zeros, the others' nothing."""
+    real = torch.empty
+    monkeypatch.setattr(layer, "_dense", lambda t, *a: t.data_ptr())
+    monkeypatch.setattr(torch, "empty", lambda *a, **k: real(*a, **k).fill_(7))
+    seqs = TTSeqs.packed(torch.tensor([0, 4], dtype=torch.int32), 4, 4)
+    for accumulate in (True, False):
+        block = TTTransformerBlock(12, rotary=TTRotary(12, 64, accumulate=accumulate))
+        b = block.buffers(4, seqs, device="cpu")
+        for nm in ("dgq", "dgk"):
+            assert b[nm].shape == (64,) and (b[nm] == (0 if accumulate else 7)).all()
