@@ -35,6 +35,15 @@ PROJ = ("q", "k", "v", "o")
 QKV = ("q", "k", "v")
 
 
+def _drop_norms(N: int, p: float, eps: float, site: int, places: int):
+    """The dropouts of a part of a model, at sites from `site` on; None for p = 0."""
+    if not 0 <= p <= 1:
+        raise ValueError(f"dropout: expected 0 to 1, got {p}")
+    if p == 0:
+        return None
+    return [TTDropNorm(N, p, torch.bfloat16, eps, site + i) for i in range(places)]
+
+
 class TTEncoderBlock:
     """Q, K, V, O (768 x 768) and the GELU FFN pair (768 -> 3072 -> 768), each
     a rank-30 TT layer, bf16 activations; the backward of every layer reuses
@@ -136,7 +145,8 @@ class TTTransformerBlock(TTEncoderBlock):
 
     def __init__(self, heads: int = 12, left: int = -1, right: int = -1, sinks: int = 0,
                  eps: float = 1e-5, reuse_z: bool = True, deterministic: bool = False,
-                 rotary: Optional[TTRotary] = None, dropout: float = 0.0, site: int = 0):
+                 rotary: Optional[TTRotary] = None, dropout: float = 0.0,
+                 site: int = 0):
         super().__init__(reuse_z, deterministic)
         self.N = self.qkv.N
         self.norm = TTNorm(self.N, torch.bfloat16, eps)
@@ -146,8 +156,7 @@ class TTTransformerBlock(TTEncoderBlock):
             raise ValueError(f"rotary: expected {heads} heads of {self.attn.dim} for q and k in "
                              f"bfloat16")
         self.rotary = rotary
-        self.drops = [TTDropNorm(self.N, dropout, torch.bfloat16, eps, site + i)
-                      for i in (0, 1)] if dropout > 0 else None
+        self.drops = _drop_norms(self.N, dropout, eps, site, 2)
 
     def buffers(self, T: int, seqs: TTSeqs, device="cuda") -> Dict[str, torch.Tensor]:
         """Everything a step of T tokens of seqs writes (allocated once): a training
@@ -324,8 +333,8 @@ class TTTokenHead:
 
     def __init__(self, in_modes: Sequence[int], out_modes: Sequence[int], ranks: Sequence[int],
                  vocab: Optional[int] = None, eps: float = 1e-5, scale: float = 1.0,
-                 top: int = 0, dropout: float = 0.0, site: int = 0, reuse_z: bool = True,
-                 deterministic: bool = False):
+                 top: int = 0, dropout: float = 0.0, site: int = 0,
+                 reuse_z: bool = True, deterministic: bool = False):
         self.linear = TTLinear(in_modes, out_modes, ranks, torch.bfloat16, reuse_z=reuse_z,
                                deterministic=deterministic)
         self.N, self.M = self.linear.N, self.linear.M
@@ -333,7 +342,8 @@ class TTTokenHead:
         if not 1 <= self.vocab <= self.M:
             raise ValueError(f"vocab: expected 1 to {self.M}, got {vocab}")
         self.norm = TTNorm(self.N, torch.bfloat16, eps)
-        self.drop = TTDropNorm(self.N, dropout, torch.bfloat16, eps, site) if dropout > 0 else None
+        drops = _drop_norms(self.N, dropout, eps, site, 1)
+        self.drop = drops[0] if drops else None
         self.probs = TTLogProbs(self.vocab, torch.bfloat16, scale, top)
 
     def buffers(self, T: int, device="cuda") -> Dict[str, torch.Tensor]:

@@ -6,7 +6,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 from tensor_train_compressed_tt_gb300 import layer, ttc  # noqa: E402
-from tensor_train_compressed_tt_gb300.encoder import TTTransformerBlock  # noqa: E402
+from tensor_train_compressed_tt_gb300.encoder import TTTokenHead, TTTransformerBlock  # noqa: E402
 from tensor_train_compressed_tt_gb300.layer import TTRotary, TTSeqs  # noqa: E402
 
 
@@ -39,3 +39,22 @@ def test_a_block_with_an_accumulating_rotary_starts_at_zero(monkeypatch):
         b = block.buffers(4, seqs, device="cpu")
         for nm in ("dgq", "dgk"):
             assert b[nm].shape == (64,) and (b[nm] == (0 if accumulate else 7)).all()
+
+
+def _block(**kw):
+    return TTTransformerBlock(12, **kw)
+
+
+def _head(**kw):
+    return TTTokenHead((12, 8, 8), (16, 16, 20), ttc.tt_default_ranks((12, 8, 8), (16, 16, 20), 30),
+                       **kw)
+
+
+@pytest.mark.parametrize("make", [_block, _head])
+def test_a_share_that_is_none_is_refused(make):
+    """Not taken as no dropout."""
+    for p in (-0.1, 1.1, float("nan")):
+        with pytest.raises(ValueError, match="dropout"):
+            make(dropout=p, site=0)
+    for p in (0.0, 0.1, 1.0):
+        make(dropout=p, site=0)
