@@ -35,12 +35,15 @@ PROJ = ("q", "k", "v", "o")
 QKV = ("q", "k", "v")
 
 
-def _drop_norms(N: int, p: float, eps: float, site: int, places: int):
+def _drop_norms(N: int, p: float, eps: float, site: Optional[int], places: int):
     """The dropouts of a part of a model, at sites from `site` on; None for p = 0."""
     if not 0 <= p <= 1:
         raise ValueError(f"dropout: expected 0 to 1, got {p}")
     if p == 0:
         return None
+    if site is None:
+        raise ValueError("site: parts with dropout need sites of their own (two at the same one "
+                         "drop the same elements)")
     return [TTDropNorm(N, p, torch.bfloat16, eps, site + i) for i in range(places)]
 
 
@@ -141,12 +144,13 @@ class TTTransformerBlock(TTEncoderBlock):
     from zeros on).
     dropout: of x and of a in front of their sums, in a pass that is given the state rng
     (TTDropout.state; None: nothing is dropped).  The block takes the sites `site` and
-    `site` + 1."""
+    `site` + 1, which nothing else in the model may have: with dropout, site has to be
+    given."""
 
     def __init__(self, heads: int = 12, left: int = -1, right: int = -1, sinks: int = 0,
                  eps: float = 1e-5, reuse_z: bool = True, deterministic: bool = False,
                  rotary: Optional[TTRotary] = None, dropout: float = 0.0,
-                 site: int = 0):
+                 site: Optional[int] = None):
         super().__init__(reuse_z, deterministic)
         self.N = self.qkv.N
         self.norm = TTNorm(self.N, torch.bfloat16, eps)
@@ -333,7 +337,7 @@ class TTTokenHead:
 
     def __init__(self, in_modes: Sequence[int], out_modes: Sequence[int], ranks: Sequence[int],
                  vocab: Optional[int] = None, eps: float = 1e-5, scale: float = 1.0,
-                 top: int = 0, dropout: float = 0.0, site: int = 0,
+                 top: int = 0, dropout: float = 0.0, site: Optional[int] = None,
                  reuse_z: bool = True, deterministic: bool = False):
         self.linear = TTLinear(in_modes, out_modes, ranks, torch.bfloat16, reuse_z=reuse_z,
                                deterministic=deterministic)

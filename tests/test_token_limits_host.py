@@ -58,3 +58,17 @@ def test_a_share_that_is_none_is_refused(make):
             make(dropout=p, site=0)
     for p in (0.0, 0.1, 1.0):
         make(dropout=p, site=0)
+
+
+@pytest.mark.parametrize("make", [_block, _head])
+def test_dropout_in_a_model_has_places_of_its_own(make):
+    """Blocks and a head that all took the same site would drop the same elements."""
+    for p in (0.1, 1.0):
+        with pytest.raises(ValueError, match="site"):
+            make(dropout=p)
+        make(dropout=p, site=7)
+    make(dropout=0.0)
+    make()
+    for site in (-1, 65536):
+        with pytest.raises(ttc.TTError):
+            make(dropout=0.1, site=site)
