@@ -724,7 +724,10 @@ __global__ void __launch_bounds__(32 * W * TEAMS, 1)
       __threadfence_block();
       ok = ok && wait_bar(&full[slot], parity, &abort_flag, 0x700);
     }
-    return __shfl_sync(0xffffffffu, ok, 0) != 0;
+    ok = __shfl_sync(0xffffffffu, ok, 0);
+    // a shuffle orders no memory: the copy that lane 0 saw, in front of every lane's reads
+    __syncwarp();
+    return ok != 0;
   };
   if (threadIdx.x == 0)
     for (int k = 0; k < slots; ++k) send(k, k);
