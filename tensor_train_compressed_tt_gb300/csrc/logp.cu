@@ -579,7 +579,8 @@ __device__ __forceinline__ void logp_row(const LogpArgs& p, int64_t row, int64_t
       const uint64_t e = top_shared.best[tid];
       const float f = of_key((uint32_t)(e >> 32));
       p.ids[row * p.top + tid] = (int)~(uint32_t)e;
-      p.tops[row * p.top + tid] = log_p(true, f, sw.x, ref, p.scale, logs);
+      p.tops[row * p.top + tid] =
+          f == -INFINITY && logs == logs ? f : fmaf(f - ref, p.scale, -kLn2 * logs);
     }
   }
 
