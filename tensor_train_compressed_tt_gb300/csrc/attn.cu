@@ -15,7 +15,7 @@ namespace ttc {
 
 cudaError_t read_and_clear_attn_status(DeviceStatus* out) {
   cudaError_t e = cudaMemcpyFromSymbol(out, g_status, sizeof(DeviceStatus));
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || out->code == 0) return e;
   DeviceStatus z{0, 0};
   return cudaMemcpyToSymbol(g_status, &z, sizeof(z));
 }

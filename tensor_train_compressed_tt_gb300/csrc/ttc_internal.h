@@ -140,7 +140,7 @@ struct DeviceStatus {
   unsigned code;    // 0 = ok, else a tt_status value
   unsigned detail;  // where it happened (kernel-specific)
 };
-// Copies the current device's status word to *out and zeroes it.
+// Copies the current device's status word to *out and zeroes one that holds something.
 cudaError_t read_and_clear_device_status(DeviceStatus* out);
 // The same for the embedding kernels' own word (ttm.cu).
 cudaError_t read_and_clear_ttm_status(DeviceStatus* out);

@@ -996,7 +996,7 @@ size_t ttm_workspace_bytes(const TtmPlan& P, int64_t B) { return ttm_layout(P, B
 
 cudaError_t read_and_clear_ttm_status(DeviceStatus* out) {
   cudaError_t e = cudaMemcpyFromSymbol(out, g_ttm_status, sizeof(DeviceStatus));
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || out->code == 0) return e;
   DeviceStatus z{0, 0};
   return cudaMemcpyToSymbol(g_ttm_status, &z, sizeof(z));
 }
