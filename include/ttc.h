@@ -461,8 +461,9 @@ tt_status tt_attn_backward(const tt_plan_t* plan, const tt_attn_seqs* seqs, cons
  *   (y_a, y_b) = (u_a cos - u_b sin, u_a sin + u_b cos) of the angle pos f_i
  * for the pairs i < rot / 2, (a, b) = (i, i + rot / 2), or (2 i, 2 i + 1) when
  * interleaved; y_c = u_c for c >= rot.  f_i = base^(-2 i / rot), or freqs[i].
- * All arithmetic is fp32 and y is rounded once; angles are reduced to a turn
- * without rounding (64-bit fractions of a turn), so far positions keep theirs. */
+ * All arithmetic is fp32 and y is rounded once (finite values whose squares' sum is beyond
+ * fp32 give zeros); angles are reduced to a turn without rounding (64-bit fractions of a
+ * turn), so far positions keep theirs. */
 typedef struct tt_rope_desc {
   int heads;           /* query heads, 1 .. 1024 */
   int kv_heads;        /* key / value heads, a divisor of heads */

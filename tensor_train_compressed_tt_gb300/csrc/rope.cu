@@ -194,10 +194,11 @@ __device__ __forceinline__ void turn_by(const float* cosine, const float* sine, 
   for (int j = 0; j < P; ++j) x.a[j] = u[j];
 }
 
-// 1 / sqrt(x): the hardware's approximation and one step of Newton's iteration.
+// 1 / sqrt(x): the hardware's approximation and one step of Newton's iteration, which has no
+// meaning for an infinity (a sum of squares beyond fp32): 0, as the quotient is.
 __device__ __forceinline__ float inverse_root(float x) {
   const float r = rsqrtf(x);
-  return fmaf(0.5f * r, fmaf(-x * r, r, 1.f), r);
+  return x < INFINITY ? fmaf(0.5f * r, fmaf(-x * r, r, 1.f), r) : r;
 }
 
 // The sum over the lanes of each head, lane i of which this one is.  Known powers of two by
@@ -453,7 +454,8 @@ __global__ void __launch_bounds__(32 * kWarps, GRAD ? kGradPerSm : kPerSm)
         const float one = inverse_root(fmaf(s, p.inv_n, p.eps));
         float r[P], less[P];
         fill<P>(one, r);
-        fill<P>(-one * m * p.inv_n, less);  // less mean(g' h)
+        // less mean(g' h): 0 where h is, although the sum of g' x may be an infinity there
+        fill<P>(one == 0.f ? 0.f : -one * m * p.inv_n, less);
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
           Pairs<P> g;

@@ -296,3 +296,28 @@ def test_a_block_without_tokens():
     for nm in ("dgq", "dgk", "dg1", "db2"):
         assert float(b[nm].abs().max()) == 0
     assert _status() == 0
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("dim", [64, 33])
+def test_rope_heads_whose_squares_exceed_fp32(dim, act):
+    """Finite values over the root of an infinite sum are zeros, gradients too, as in the formula
+    in fp32; an infinity or a NaN spoils its own head alone."""
+    op = _plan(3, 1, dim, act, rot=dim // 2 * 2)
+    r = np.random.default_rng(dim)
+    q, k, dq, dk = (rand(r, (9, h, dim), act) for h in (3, 1, 3, 1))
+    clean = op.forward(q, k)[0], op.backward(dq, dk, None, q, k)[0]
+    q[2, 1] = 1e20
+    q[3, 0, 5] = -3e38
+    got = op.forward(q, k)[0], op.backward(dq, dk, None, q, k)
+    for a, b in zip((got[0], got[1][0]), clean):
+        for t, h in ((2, 1), (3, 0)):
+            assert float(a[t, h].float().abs().max()) == 0
+            a[t, h] = b[t, h]
+        assert torch.equal(a, b)
+    assert all(torch.isfinite(g).all() for g in got[1][2:])
+    q[2, 1, 7], q[3, 0, 5] = float("nan"), float("inf")
+    y = op.forward(q, k)[0]
+    assert torch.isnan(y[2, 1].float()).any() and torch.isnan(y[3, 0].float()).any()
+    y[2, 1], y[3, 0] = clean[0][2, 1], clean[0][3, 0]
+    assert torch.equal(y, clean[0])
