@@ -303,7 +303,8 @@ class TTTransformerBlock(TTEncoderBlock):
         """forward for a few new tokens: their keys and values go to `rows` (int64, or
         int32 with a rotary) of the caches keys and values (rows, heads, dim), which seqs
         names as the sequences' keys; (FFN output, s2).  With a rotary pos (int32) is
-        the tokens' positions, as the cached keys had them."""
+        the tokens' positions, as the cached keys had them, and rows of int64 are converted
+        in each call."""
         s1 = self._project(x, res, params, b, stream)
         shape = (-1, self.attn.kv_heads, self.attn.dim)
         here = stream if stream is not None else torch.cuda.current_stream()

@@ -699,7 +699,10 @@ class TTLogProbs:
     """What follows the output layer: for rows of V logits (of any row stride), z = scale
     logits, the log-sum, the log probability of each row's target, the entropy and the
     `top` most likely tokens; the gradient of any sum of log probabilities and
-    entropies.  targets are int32; a negative one stands for none (logp 0)."""
+    entropies.  targets are int32; a negative one stands for none (logp 0).  A dlogits whose
+    rows start like the logits' modulo 16 bytes is fastest: for a slice of wider logits that
+    is a slice of the same row stride, not the dense one that is made where none is given
+    (4096 x 50257 of 50304 columns in bf16: the loss 142 us against 373)."""
 
     def __init__(self, V: int, dtype: torch.dtype = torch.bfloat16, scale: float = 1.0,
                  top: int = 0):
@@ -758,7 +761,8 @@ class TTLogProbs:
     def backward(self, logits, targets, lse, dlogp=None, entropy=None, dentropy=None,
                  dlogits=None, stream=None):
         """dlogits for the gradients of logp and of the entropy (which then has to be
-        given), from forward's lse.  dlogits may be logits."""
+        given), from forward's lse; rows whose lse fp32 rounds too far for the weights (above
+        256 in f32, 4096 in bf16) take their sum again.  dlogits may be logits."""
         T, f32 = logits.shape[0], torch.float32
         here = _same_device(logits, targets, lse, dlogp, entropy, dentropy, dlogits)
         t, g, h = self._gradients(T, targets, dlogp, dentropy)
