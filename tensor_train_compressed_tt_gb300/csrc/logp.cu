@@ -868,7 +868,7 @@ __global__ void __launch_bounds__(32 * W * TEAMS, 1)
 
 // The largest |lse| that the gradient alone takes its weights from.  Rounded to fp32 an lse is
 // off by 2^-24 of itself, and the weight by as much in proportion: 2^-16 here in f32, in bf16
-// 2^-12, an eighth of the gradient's own half step.  Beyond it (rows whose every logit is a
+// 2^-12, a sixteenth of the gradient's own half step.  Beyond it (rows whose every logit is a
 // mask of -1e9: lse comes in steps of 64 and has lost log V; log-sums beyond the type's range)
 // the row's sum is taken again, as the pass that makes both has it.
 template <typename T>
